@@ -20,7 +20,8 @@ from ._build import LIB as _LIB_PATH, build as _build_lib
 
 __all__ = ["attn_fwd", "attn_fwd_out", "attn_fwd_host", "attn_fwd_trace", "attn_fwd_splitkv",
            "splitkv_default_splits", "attn_bwd", "attn_bwd_host", "bwd_workspace_bytes",
-           "chunk_scan", "chunk_scan_host", "selftest_qk", "selftest_pv", "device_status", "status_string",
+           "chunk_scan", "chunk_scan_host", "kv_cache_empty", "kv_append", "kv_read",
+           "attn_fwd_paged", "paged_workspace_bytes", "selftest_qk", "selftest_pv", "device_status", "status_string",
            "lib_path", "build", "AttnError", "STATUS"]
 
 STATUS = {
@@ -30,9 +31,10 @@ STATUS = {
     3: "ATTN_ERR_MISALIGNED",
     4: "ATTN_ERR_CUDA",
     5: "ATTN_ERR_TIMEOUT",
+    6: "ATTN_ERR_BAD_INDEX",
 }
 
-# every entry point of include/attn.h and include/attn_selftest.h
+# every entry point of the headers in include/
 EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_status_string", "attn_device_status",
            "attn_version", "attn_selftest_qk", "attn_selftest_pv", "attn_fwd_trace",
            "attn_fwd_timeout_test", "attn_fwd_tail_timeout_test", "attn_fwd_tail_pairs",
@@ -40,7 +42,8 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_status_string", "attn_device_statu
            "attn_splitkv_default_splits", "attn_fwd_splitkv_noalloc",
            "attn_splitkv_noalloc_capacity", "attn_bwd", "attn_bwd_deterministic",
            "attn_bwd_workspace_bytes", "attn_bwd_timeout_test",
-           "attn_bwd_host", "chunk_scan_fwd", "chunk_scan_fwd_host"]
+           "attn_bwd_host", "chunk_scan_fwd", "chunk_scan_fwd_host",
+           "attn_kv_append", "attn_kv_read", "attn_fwd_paged", "attn_paged_workspace_bytes"]
 
 
 class AttnError(RuntimeError):
@@ -117,6 +120,14 @@ def _load():
     lib.chunk_scan_fwd.restype = ci
     lib.chunk_scan_fwd_host.argtypes = [vp] * 10 + [ci] * 6 + [vp]
     lib.chunk_scan_fwd_host.restype = ci
+    lib.attn_kv_append.argtypes = [vp] * 9 + [ci] * 5 + [vp]
+    lib.attn_kv_append.restype = ci
+    lib.attn_kv_read.argtypes = [vp] * 5 + [ci, vp]
+    lib.attn_kv_read.restype = ci
+    lib.attn_fwd_paged.argtypes = [vp] * 7 + [ctypes.c_size_t] + [ci] * 3 + [cf, vp]
+    lib.attn_fwd_paged.restype = ci
+    lib.attn_paged_workspace_bytes.argtypes = [ci] * 5
+    lib.attn_paged_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -422,7 +433,12 @@ def selftest_pv(p, v):
 
 
 def device_status(reset: bool = True) -> int:
-    """The device-side status word (0, or 5 = a kernel wait timed out)."""
+    """The device-side status word (0, 5 = a kernel wait timed out, or 6 = a paged-cache kernel met
+    an index out of range)."""
     st = ctypes.c_int(0)
     _check(_load().attn_device_status(ctypes.byref(st), int(bool(reset))), "attn_device_status")
     return st.value
+
+
+from .paged import (attn_fwd_paged, kv_append, kv_cache_empty, kv_read,  # noqa: E402
+                    paged_workspace_bytes)

@@ -36,6 +36,10 @@ EncodeTiledFn get_encode_fn() {
 int g_arch_ok[64] = {};
 std::mutex g_arch_mu;
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
 attn_status_t check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
@@ -53,10 +57,6 @@ attn_status_t check_device() {
   }
   return ATTN_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-}  // namespace
 
 bool encode_bf16_map_3d(CUtensorMap* map, const void* base, uint64_t D, uint64_t rows,
                         uint64_t outer, uint32_t box_rows) {
@@ -900,6 +900,7 @@ const char* attn_status_string(attn_status_t status) {
     case ATTN_ERR_MISALIGNED: return "pointer not 16-byte aligned";
     case ATTN_ERR_CUDA: return "CUDA runtime or driver call failed";
     case ATTN_ERR_TIMEOUT: return "a wait inside the kernel ran out of time";
+    case ATTN_ERR_BAD_INDEX: return "a page number, length or position on the device is out of range";
   }
   return "unknown status";
 }
@@ -909,15 +910,20 @@ attn_status_t attn_device_status(int* status_out, int reset) {
   attn_status_t st = check_device();
   if (st != ATTN_OK) return st;
   int main_status = 0, selftest_status = 0, bwd_status = 0, cs_status = 0;
+  int kv_status = 0, paged_status = 0;
   if (read_device_status(&main_status, reset != 0) != cudaSuccess ||
       read_selftest_status(&selftest_status, reset != 0) != cudaSuccess ||
       read_bwd_status(&bwd_status, reset != 0) != cudaSuccess ||
-      read_chunk_scan_status(&cs_status, reset != 0) != cudaSuccess)
+      read_chunk_scan_status(&cs_status, reset != 0) != cudaSuccess ||
+      read_kv_status(&kv_status, reset != 0) != cudaSuccess ||
+      read_paged_status(&paged_status, reset != 0) != cudaSuccess)
     return ATTN_ERR_CUDA;
   *status_out = main_status != 0 ? main_status
                 : bwd_status != 0 ? bwd_status
                 : cs_status != 0  ? cs_status
-                                  : selftest_status;
+                : kv_status != 0  ? kv_status
+                : paged_status != 0 ? paged_status
+                                    : selftest_status;
   return ATTN_OK;
 }
 

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "attn_paged.h"
 
 namespace attnpipe {
 
@@ -133,6 +134,71 @@ cudaError_t launch_chunk_scan(const ChunkScanParams& p, cudaStream_t stream);
 // Reads (and optionally clears) the chunk-scan kernel's status word.
 cudaError_t read_chunk_scan_status(int* status, bool reset);
 
+// The paged key/value cache as the kernels read it (include/attn_paged.h).
+struct KvCache {
+  const uint8_t* k;
+  const uint8_t* v;
+  const int* table;      // [B, max_blocks] page numbers
+  int num_pages, page_size, blocks_per_page, max_blocks;  // 16-token blocks
+  int B, H_kv;
+  int capacity;          // max_blocks * page_size: positions a sequence may hold
+};
+
+// A strided bf16 [B, H, S, D] tensor (strides in elements).
+struct KvTensor {
+  const uint16_t* data;
+  long long sb, sh, ss;
+};
+
+struct KvAppendParams {
+  KvCache cache;
+  KvTensor q, k, v;
+  uint16_t* q_out;       // [B, H_q, S, D] contiguous
+  const int* start;      // [B]
+  const int* new_lens;   // [B] or nullptr
+  const float* cos;      // [rope_rows, rot_dim / 2]
+  const float* sin;
+  int rope_rows, rot_dim, interleaved;
+  int H_q, S;
+  int rounds;            // rows of a token per row slot (set at launch)
+};
+
+struct KvReadParams {
+  KvCache cache;
+  uint16_t* k_out;       // [B, H_kv, S, D] contiguous
+  uint16_t* v_out;
+  const int* lens;       // [B]
+  const int* start;      // [B] or nullptr
+  int S;
+};
+
+struct PagedParams {
+  KvCache cache;
+  KvTensor q;
+  uint16_t* o;           // [B, H_q, S_q, D]
+  float* lse;            // [B, H_q, S_q]
+  const int* lens;       // [B]
+  const int* q_lens;     // [B] or nullptr
+  float* part_o;         // workspace: [2 kPagedMaxCtas, rows, D]
+  float* part_lse;       // workspace: [2 kPagedMaxCtas, rows], base 2
+  int H_q, S_q, group;   // group = H_q / H_kv
+  int row_tiles;         // ceil(group * S_q / rows)
+  int causal;
+  float scale_log2;
+};
+
+// CTAs of the paged attention, at most (the workspace holds two parts of each).
+constexpr int kPagedMaxCtas = 1024;
+
+cudaError_t launch_kv_append(const KvAppendParams& p, int D, bool int4, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvReadParams& p, int D, bool int4, cudaStream_t stream);
+// Queues the paged attention with `rows` (8, 16 or 32) query rows to a tile.
+cudaError_t launch_attn_paged(const PagedParams& p, int D, bool int4, int rows,
+                              cudaStream_t stream);
+// Read (and optionally clear) the cache's and the paged attention's status words.
+cudaError_t read_kv_status(int* status, bool reset);
+cudaError_t read_paged_status(int* status, bool reset);
+
 // Events stamped by the trace instantiation, one slot per KV block j.
 enum TraceEvent : int {
   kEvSm0Wake = 0,   // softmax 0: S_0(j) ready (wait returned)
@@ -190,6 +256,8 @@ cudaError_t launch_selftest_pv(const uint16_t* p, const CUtensorMap& tv, float* 
                                cudaStream_t stream);
 
 // Host-side pieces of the C ABI (attn_api.cu) used by more than one file.
+// ATTN_OK when the current device is an sm_103 part (cached per device).
+attn_status_t check_device();
 attn_status_t validate(const void* q, const void* k, const void* v, const void* o, const void* lse,
                        int B, int H_q, int H_kv, int S_q, int S_kv, int D, int causal,
                        float scale);

@@ -51,7 +51,9 @@ typedef enum {
   ATTN_ERR_UNSUPPORTED = 2, /* D not 64 or 128, size beyond the kernel's limits, not sm_103 */
   ATTN_ERR_MISALIGNED = 3,  /* a device pointer not 16-byte aligned */
   ATTN_ERR_CUDA = 4,        /* a CUDA runtime or driver call failed */
-  ATTN_ERR_TIMEOUT = 5      /* a kernel wait ran out of time (see attn_device_status) */
+  ATTN_ERR_TIMEOUT = 5,     /* a kernel wait ran out of time (see attn_device_status) */
+  ATTN_ERR_BAD_INDEX = 6    /* a kernel met a page number, length or position out of range
+                               (attn_paged.h; see attn_device_status) */
 } attn_status_t;
 
 /*
@@ -276,9 +278,10 @@ const char *attn_status_string(attn_status_t status);
 
 /*
  * Reads the device-side status words of the current device (forward,
- * backward and self-test kernels): ATTN_OK, or ATTN_ERR_TIMEOUT if a launch
- * since the last reset gave up on a wait (that launch's outputs are then
- * unspecified).  Synchronises the device.  With
+ * backward, self-test and paged-cache kernels): ATTN_OK, ATTN_ERR_TIMEOUT if a
+ * launch since the last reset gave up on a wait (that launch's outputs are then
+ * unspecified), or ATTN_ERR_BAD_INDEX if a paged-cache kernel met an index out
+ * of range (attn_paged.h says what it did with it).  Synchronises the device.  With
  * reset != 0 the word is cleared afterwards.
  */
 attn_status_t attn_device_status(int *status_out, int reset);

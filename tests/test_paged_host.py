@@ -1,0 +1,181 @@
+"""The paged cache's entry points refuse bad arguments on the host, before any CUDA
+call (CPU only; fake, never-dereferenced device addresses)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import attention_pipelining_gb300 as ap
+from attention_pipelining_gb300 import paged
+from tests import paged_ref as ref
+
+A = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ap.build()
+    return ap._load()
+
+
+def cache(**kw):
+    d = dict(k=A, v=A, block_table=A, format=0, num_pages=10, page_size=64, max_blocks=8, B=2,
+             H_kv=2, D=128)
+    d.update(kw)
+    return paged._Cache(*[d[n] for n, _ in paged._Cache._fields_])
+
+
+def tensor(data=A, sb=8 * 128, sh=128, ss=2 * 128):
+    return paged._Bhsd(data, sb, sh, ss)
+
+
+def ref_(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def append(lib, c=None, q=None, q_out=None, k=None, v=None, start=A, new=None, cos=A, sin=A,
+           rows=512, rot=128, inter=0, H_q=0, S=4):
+    c = cache() if c is None else c
+    k, v = k or tensor(), v or tensor()
+    return lib.attn_kv_append(ctypes.byref(c), ref_(q), q_out, ctypes.byref(k), ctypes.byref(v),
+                              start, new, cos, sin, rows, rot, inter, H_q, S, None)
+
+
+def read(lib, c=None, k=A, v=A, lens=A, start=None, S=4):
+    c = cache() if c is None else c
+    return lib.attn_kv_read(ctypes.byref(c), k, v, lens, start, S, None)
+
+
+def attend(lib, c=None, q=None, o=A, lse=A, lens=A, q_lens=None, ws=A, nbytes=1 << 30, H_q=4,
+           S_q=1, causal=1, scale=0.1):
+    c = cache() if c is None else c
+    q = q or tensor()
+    return lib.attn_fwd_paged(ctypes.byref(c), ctypes.byref(q), o, lse, lens, q_lens, ws, nbytes,
+                              H_q, S_q, causal, ctypes.c_float(scale), None)
+
+
+BAD_CACHE = [(dict(k=None), 1), (dict(v=None), 1), (dict(block_table=None), 1), (dict(B=0), 1),
+             (dict(H_kv=-1), 1), (dict(D=0), 1), (dict(num_pages=0), 1), (dict(page_size=0), 1),
+             (dict(max_blocks=0), 1), (dict(format=2), 1), (dict(page_size=24), 1),
+             (dict(D=96), 2), (dict(B=70000), 2), (dict(H_kv=40000), 2),
+             (dict(max_blocks=1 << 24), 2), (dict(num_pages=2**31 - 1, H_kv=32767, page_size=4096), 2),
+             (dict(k=A + 8), 3), (dict(v=A + 4), 3), (dict(block_table=A + 2), 3)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHE, ids=[str(k) for k, _ in BAD_CACHE])
+def test_every_entry_checks_the_cache(lib, kw, code):
+    c = cache(**kw)
+    assert append(lib, c) == code
+    assert read(lib, c) == code
+    assert attend(lib, c) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(start=None), 1), (dict(S=0), 1), (dict(H_q=-1), 1), (dict(H_q=2), 1),
+    (dict(H_q=2, q=tensor()), 1), (dict(q=tensor(), q_out=A), 1), (dict(inter=2), 1),
+    (dict(rot=-16), 1), (dict(rot=144), 1), (dict(rot=24), 1), (dict(cos=None), 1),
+    (dict(sin=None), 1), (dict(rows=0), 1), (dict(S=1 << 30), 2), (dict(start=A + 2), 3),
+    (dict(cos=A + 8), 3), (dict(k=tensor(data=None)), 1), (dict(k=tensor(A + 8)), 3),
+    (dict(v=tensor(sb=12)), 3), (dict(k=tensor(sh=4)), 3), (dict(v=tensor(ss=129)), 3),
+    (dict(H_q=2, q=tensor(A + 2), q_out=A), 3), (dict(H_q=2, q=tensor(), q_out=A + 8), 3),
+    (dict(H_q=70000, q=tensor(), q_out=A), 2),
+])
+def test_append_refuses(lib, kw, code):
+    assert append(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(lens=None), 1), (dict(S=0), 1), (dict(S=-2), 1),
+    (dict(S=1 << 30), 2), (dict(k=A + 8), 3), (dict(v=A + 2), 3), (dict(lens=A + 1), 3),
+    (dict(start=A + 2), 3),
+])
+def test_read_refuses(lib, kw, code):
+    assert read(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(o=None), 1), (dict(lse=None), 1), (dict(lens=None), 1), (dict(ws=None), 1),
+    (dict(causal=2), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(H_q=3), 1), (dict(H_q=0), 1), (dict(S_q=0), 1), (dict(S_q=1 << 30), 2),
+    (dict(q=tensor(data=None)), 1), (dict(q=tensor(sh=20)), 3), (dict(o=A + 8), 3),
+    (dict(lse=A + 2), 3), (dict(ws=A + 16), 3), (dict(nbytes=1000), 1), (dict(q_lens=A + 1), 3),
+])
+def test_attention_refuses(lib, kw, code):
+    assert attend(lib, **kw) == code
+
+
+def test_strides_of_single_dimensions_are_not_looked_at(lib):
+    """[B, 1, 1, D] views may carry any stride there: the call stops at a later rule."""
+    c = cache(H_kv=1)
+    odd = tensor(sh=3, ss=5)
+    assert append(lib, c, k=odd, v=tensor(A + 2, sh=3, ss=5), S=1) == 3   # v's address, not k's strides
+    assert append(lib, c, k=odd, v=tensor(A, sh=3, ss=5), S=1, rows=0) == 1
+
+
+def test_workspace_bytes(lib):
+    """Two parts of each of at most 1024 thread blocks, D + 1 floats a row of the tile."""
+    f = lib.attn_paged_workspace_bytes
+    for H_q, H_kv, S_q, rows in ((8, 1, 1, 8), (9, 1, 1, 16), (32, 8, 1, 8), (32, 8, 4, 16),
+                                 (32, 8, 5, 32), (32, 8, 500, 32)):
+        for D in (64, 128):
+            assert f(3, H_q, H_kv, S_q, D) == 2 * 1024 * rows * (D + 1) * 4
+    for bad in ((0, 8, 1, 1, 64), (1, 8, 3, 1, 64), (1, 8, 1, 0, 64), (1, 8, 1, 1, 96)):
+        assert f(*bad) == 0
+
+
+def test_binding_refuses_on_the_host():
+    t = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    pool = torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16)
+    bt = torch.zeros(1, 4, dtype=torch.int32)
+    n = torch.ones(1, dtype=torch.int32)
+    for f in (lambda: ap.kv_append(t, t, pool, pool, bt, n),
+              lambda: ap.kv_read(pool, pool, bt, n, 4),
+              lambda: ap.attn_fwd_paged(t, pool, pool, bt, n, True, 0.1)):
+        with pytest.raises(TypeError):   # not on a GPU
+            f()
+    for bad in (dict(fmt="fp8"), dict(D=80), dict(page_size=20), dict(page_size=0)):
+        with pytest.raises(ValueError):
+            ap.kv_cache_empty(**{**dict(num_pages=2, H_kv=1, page_size=16, D=64, device="cpu"), **bad})
+    k, v = ap.kv_cache_empty(3, 2, 48, 128, "int4", device="cpu")
+    assert k.shape == v.shape == (3, 2, 3, 9 * 128) and k.dtype == torch.uint8
+    k, v = ap.kv_cache_empty(3, 2, 48, 64, device="cpu")
+    assert k.shape == (3, 2, 48, 64) and k.dtype == torch.bfloat16
+
+
+# ---------------------------------------------------------------- the reference itself
+
+
+@pytest.mark.parametrize("kind", ["k", "v"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_reference_format(kind, D):
+    """Every nibble of a block belongs to one element, no byte to two tokens; packed
+    values come back within half a step of their group, or as NaN."""
+    idx = ref.nibble_index(kind, D)
+    assert sorted(idx.ravel()) == list(range(16 * D))
+    owner = np.zeros(16 * D, int)
+    owner[idx] = np.arange(16)[:, None]
+    assert (owner[0::2] == owner[1::2]).all()
+    x = ref.bf16(np.random.default_rng(3).normal(size=(48, D)))
+    x[5, :32] = 0.0
+    x[7, 33] = np.inf
+    y, s = ref.unpack(ref.pack(x, kind), kind)
+    assert np.isnan(y[7, 32:64]).all() and (y[5, :32] == 0).all()
+    e = np.abs(y - x).reshape(48, D // 32, 32)
+    ok = np.isfinite(s)
+    assert (e[ok] <= 0.5 * s[ok][:, None] * (1 + 2.0 ** -5)).all()
+
+
+def test_reference_attention_matches_torch():
+    """The reference on one sequence against torch's float64 softmax."""
+    g = np.random.default_rng(4)
+    vals = g.normal(size=(3, 2, 16, 64)), g.normal(size=(3, 2, 16, 64))
+    q = g.normal(size=(1, 4, 2, 64))
+    table = np.array([[2, 0]])
+    o, lse, _, _ = ref.attention(q, *vals, None, None, table, [21], 16, True, 0.2)
+    k, v = (torch.from_numpy(np.concatenate([x[2], x[0]], 1)[:, :21]) for x in vals)
+    for h in range(4):
+        for i in range(2):
+            s = 0.2 * k[h // 2][:20 + i] @ torch.from_numpy(q[0, h, i])
+            assert np.allclose(torch.softmax(s, 0) @ v[h // 2][:20 + i], o[0, h, i], atol=1e-12)
+            assert np.allclose(torch.logsumexp(s, 0), lse[0, h, i], atol=1e-12)
