@@ -173,6 +173,8 @@ struct KvReadParams {
 };
 
 struct PagedParams {
+  CUtensorMap tm_k, tm_v;  // bf16 pools as [num_pages * H_kv, page_size, D], box {64, 16, 1},
+                           // 128-byte swizzle (a 4-bit pool is copied by address)
   KvCache cache;
   KvTensor q;
   uint16_t* o;           // [B, H_q, S_q, D]
@@ -185,6 +187,7 @@ struct PagedParams {
   int row_tiles;         // ceil(group * S_q / rows)
   int causal;
   float scale_log2;
+  unsigned long long timeout_ns;  // budget of any single wait inside the kernel
 };
 
 // CTAs of the paged attention, at most (the workspace holds two parts of each).

@@ -23,6 +23,8 @@ attn_status_t take_cache(const attn_kv_cache_t* c, KvCache* out) {
   if (c->D != 64 && c->D != 128) return ATTN_ERR_UNSUPPORTED;
   if (c->B > 65535 || c->H_kv > 32767) return ATTN_ERR_UNSUPPORTED;
   if ((int64_t)c->max_blocks * c->page_size >= (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
+  // pages times heads index the pool's tensor map
+  if ((int64_t)c->num_pages * c->H_kv >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
   // byte offsets are 64-bit; the pool must fit them
   if ((int64_t)c->num_pages * c->H_kv >= (1ll << 46) / ((int64_t)c->page_size * 256))
     return ATTN_ERR_UNSUPPORTED;
@@ -180,6 +182,13 @@ attn_status_t attn_fwd_paged(const attn_kv_cache_t* cache, const attn_bhsd_t* q,
   p.row_tiles = (int)(((int64_t)p.group * S_q + rows - 1) / rows);
   p.causal = causal;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.timeout_ns = kDefaultTimeoutNs;
+  if (cache->format == ATTN_KV_BF16) {
+    const uint64_t heads = (uint64_t)cache->num_pages * cache->H_kv;
+    if (!encode_bf16_map_3d(&p.tm_k, cache->k, cache->D, cache->page_size, heads, 16) ||
+        !encode_bf16_map_3d(&p.tm_v, cache->v, cache->D, cache->page_size, heads, 16))
+      return ATTN_ERR_CUDA;
+  }
   return launch_attn_paged(p, cache->D, cache->format == ATTN_KV_INT4, rows,
                            static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? ATTN_OK

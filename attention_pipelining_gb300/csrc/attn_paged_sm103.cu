@@ -294,7 +294,9 @@ struct Warp {
         for (int c = 0; c < 4; ++c) o[d][n][c] = 0.f;
   }
 
-  // The 16 keys key0 .. key0 + 15, whose K and V blocks lie at kb and vb.
+  // The 16 keys key0 .. key0 + 15, whose K and V blocks lie at kb and vb in
+  // shared memory; kMasked where some row may not see all of them.
+  template <bool kMasked>
   __device__ __forceinline__ void step(const uint8_t* kb, const uint8_t* vb, int key0) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float s[MT][2][4];   // [query tile][keys 0-7, 8-15]
@@ -337,7 +339,7 @@ struct Warp {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t w[4];
-          load_words<4>(kb + key * (D * 2) + 128 * (c >> 1) + 16 * (2 * t + (c & 1)), w);
+          load_words<4>(kb + 2048 * (c >> 1) + key * 128 + 16 * ((2 * t + (c & 1)) ^ g), w);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             mma_bf16(s[mt][kt], q[mt][2 * c], w[0], w[1]);
@@ -346,20 +348,27 @@ struct Warp {
         }
       }
     }
-    // base-2 exponents, masked
-    const bool whole = key0 + 16 <= min_lim;
+    // base-2 exponents where some are masked
+    if constexpr (kMasked) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const int mt = r / HALVES, hf = r % HALVES;
+      for (int r = 0; r < NR; ++r) {
+        const int mt = r / HALVES, hf = r % HALVES;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float& x = s[mt][kt][2 * hf + c];
+        for (int c = 0; c < 4; ++c) {
+          float& x = s[mt][c >> 1][2 * hf + (c & 1)];
           x *= fac[r];
-          if (!whole && key0 + kt * 8 + 2 * t + c >= lim[r]) x = -INFINITY;
+          if (key0 + (c >> 1) * 8 + 2 * t + (c & 1) >= lim[r]) x = -INFINITY;
         }
+      }
     }
+    const auto exponent = [&](int r, int c) {   // of row r, key 8 (c / 2) + 2t + c % 2
+      const float x = s[r / HALVES][c >> 1][2 * (r % HALVES) + (c & 1)];
+      return kMasked ? x : x * fac[r];
+    };
+    const auto probability = [&](int r, int c) {
+      const float x = s[r / HALVES][c >> 1][2 * (r % HALVES) + (c & 1)];
+      return ex2_approx(kMasked ? x - m[r] : fmaf(x, fac[r], -m[r]));
+    };
     // the values' scales of this lane's keys (pairs 2t, 2t + 1 of each eight)
     uint32_t sv[2][kInt4 ? G : 1];
     float smax = 1.f;
@@ -368,7 +377,7 @@ struct Warp {
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         load_words<G>(vb + 8 * D + (kt * 8 + 2 * t) * 2 * G, sv[kt]);
-        if (!whole) {   // behind the last visible key there may be anything
+        if (kMasked) {   // behind the last visible key there may be anything
           const int left = max_lim - key0 - kt * 8 - 2 * t;
 #pragma unroll
           for (int j = 0; j < G; ++j)
@@ -384,11 +393,10 @@ struct Warp {
     bool over = false;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int mt = r / HALVES, hf = r % HALVES;
       float pm = 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        pr[r][c] = ex2_approx(s[mt][c >> 1][2 * hf + (c & 1)] - m[r]);
+        pr[r][c] = probability(r, c);
         pm = fmaxf(pm, pr[r][c]);
       }
       over |= pm * smax > kMaxProb || pm > kMaxSum;
@@ -402,10 +410,9 @@ struct Warp {
       float alpha[NR];
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const int mt = r / HALVES, hf = r % HALVES;
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) mx = fmaxf(mx, s[mt][c >> 1][2 * hf + (c & 1)]);
+        for (int c = 0; c < 4; ++c) mx = fmaxf(mx, exponent(r, c));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
         const float next = fmaxf(m[r], mx + up);
@@ -413,8 +420,7 @@ struct Warp {
         m[r] = next;
         l[r] *= alpha[r];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          pr[r][c] = ex2_approx(s[mt][c >> 1][2 * hf + (c & 1)] - next);
+        for (int c = 0; c < 4; ++c) pr[r][c] = probability(r, c);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {   // column tile n: rows 8 n + 2t, 8 n + 2t + 1
@@ -454,7 +460,7 @@ struct Warp {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float x0 = pr[n][0] * s0, x1 = pr[n][1] * s1, x2 = pr[n][2] * s2, x3 = pr[n][3] * s3;
-          if (!whole) {   // a masked key's scale may be anything
+          if (kMasked) {   // a masked key's scale may be anything
             const int k0 = key0 + 2 * t;
             if (k0 >= lim[n]) x0 = 0.f;
             if (k0 + 1 >= lim[n]) x1 = 0.f;
@@ -478,7 +484,7 @@ struct Warp {
       // values of keys that no row sees may be anything: keep key pairs
       // by their last visible key
       uint32_t keep0 = kFull, keep1 = kFull;
-      if (!whole) {
+      if (kMasked) {
         const int left = max_lim - key0 - 2 * t;
         keep0 = left <= 0 ? 0u : left == 1 ? 0xffffu : kFull;
         keep1 = left <= 8 ? 0u : left == 9 ? 0xffffu : kFull;
@@ -488,7 +494,8 @@ struct Warp {
         uint32_t w[4][4];   // keys 2t, 2t + 1, 8 + 2t, 9 + 2t: elements 64 sl + 8 g ..
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          load_words<4>(vb + ((c >> 1) * 8 + 2 * t + (c & 1)) * (D * 2) + 128 * sl + 16 * g, w[c]);
+          load_words<4>(vb + 2048 * sl + ((c >> 1) * 8 + 2 * t + (c & 1)) * 128 +
+                            16 * (g ^ (2 * t + (c & 1))), w[c]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t a[4] = {__byte_perm(w[0][e], w[1][e], 0x5410u) & keep0,
@@ -511,19 +518,120 @@ __device__ __forceinline__ int element_of(int d, int g) {
   return kInt4 ? 32 * (d >> 1) + 4 * g + 2 * (d & 1) : 64 * (d >> 2) + 8 * g + 2 * (d & 3);
 }
 
+// Shared memory of a thread block: each warp's ring of kStages stages of 16
+// keys (K block, then V block), reused for the merge of the warps' results.
+template <int D, bool kInt4, int ROWS>
+struct Smem {
+  static constexpr int kBlock = kKvBlockBytes<D, kInt4>;
+  static constexpr int kStage = 2 * kBlock;
+  static constexpr int kStages = kInt4 ? (D == 128 ? 4 : 6) : (D == 128 ? 3 : 4);
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kMerge = kPgWarps * ROWS * (D + 4) * 4;
+  static constexpr int kBytes = (kPgWarps * kRing > kMerge ? kPgWarps * kRing : kMerge) + 1024;
+};
+
+// One warp's stream of 16-key blocks w, w + kPgWarps, .. of a segment through
+// its ring: blocks are requested kStages ahead by asynchronous bulk copies
+// (4-bit: K's and V's blocks are contiguous, one copy each) or tensor copies
+// with the 128-byte swizzle (bf16), and their page numbers one block further.
+template <int D, bool kInt4, int ROWS>
+struct Stream {
+  using S = Smem<D, kInt4, ROWS>;
+  uint8_t* ring;
+  uint64_t* full;        // [kStages]
+  uint32_t issued = 0, taken = 0;   // blocks since the kernel began (all lanes alike)
+  uint32_t present = 0;  // bit per stage: the block's page exists
+  // the next block to request
+  const int* table;
+  int left = 0, pg, blk, page;
+  long long head;        // 4-bit: byte offset of the head in a page; bf16: the head
+
+  __device__ __forceinline__ void look_up() { page = left > 0 ? table[pg] : -1; }
+
+  __device__ __forceinline__ void begin(const PagedParams& p, int b, int h, int first_block,
+                                        int blocks) {
+    const KvCache& kc = p.cache;
+    table = kc.table + (long long)b * kc.max_blocks;
+    left = blocks;
+    pg = first_block / kc.blocks_per_page;
+    blk = first_block % kc.blocks_per_page;
+    head = kInt4 ? (long long)h * kc.blocks_per_page * S::kBlock : h;
+    look_up();
+  }
+
+  // Requests the next block, if there is one; returns false if its page does
+  // not exist.
+  __device__ __forceinline__ bool request(const PagedParams& p) {
+    if (left <= 0) return true;
+    const KvCache& kc = p.cache;
+    const uint32_t st = issued % S::kStages;
+    const bool ok = (unsigned)page < (unsigned)kc.num_pages;
+    if ((threadIdx.x & 31) == 0) {
+      uint8_t* dst = ring + st * S::kStage;
+      if (ok) {
+        mbar_arrive_expect_tx(&full[st], S::kStage);
+        if constexpr (kInt4) {
+          const long long off = (long long)page * kc.H_kv * kc.blocks_per_page * S::kBlock + head +
+                                blk * S::kBlock;
+          bulk_load(dst, kc.k + off, S::kBlock, &full[st]);
+          bulk_load(dst + S::kBlock, kc.v + off, S::kBlock, &full[st]);
+        } else {
+          // read once, or once by every row tile
+          const uint64_t once = p.row_tiles == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+          const int z = page * kc.H_kv + (int)head;
+#pragma unroll
+          for (int sl = 0; sl < D / 64; ++sl) {
+            tma_load_3d(dst + sl * 2048, &p.tm_k, &full[st], 64 * sl, 16 * blk, z, once);
+            tma_load_3d(dst + S::kBlock + sl * 2048, &p.tm_v, &full[st], 64 * sl, 16 * blk, z, once);
+          }
+        }
+      } else {
+        mbar_arrive(&full[st]);
+      }
+    }
+    present = (present & ~(1u << st)) | ((uint32_t)ok << st);
+    ++issued;
+    --left;
+    blk += kPgWarps;
+    while (blk >= kc.blocks_per_page) {
+      blk -= kc.blocks_per_page;
+      ++pg;
+    }
+    look_up();
+    return ok;
+  }
+
+  // Waits for the oldest requested block; false if the wait ran out of time.
+  __device__ __forceinline__ bool take(volatile int* abort_flag, uint64_t budget) {
+    const uint32_t st = taken % S::kStages;
+    const bool ok = mbar_wait(&full[st], (taken / S::kStages) & 1, abort_flag, budget);
+    ++taken;
+    return __all_sync(kFull, ok);
+  }
+};
+
 template <int D, bool kInt4, int ROWS>
 __global__ void __launch_bounds__(kPgThreads)
     attn_paged_kernel(const __grid_constant__ PagedParams p) {
   using W = Warp<D, kInt4, ROWS>;
-  extern __shared__ __align__(16) float sm_o[];   // [kPgWarps][ROWS][D + 4]
+  using S = Smem<D, kInt4, ROWS>;
+  extern __shared__ uint8_t smem_raw_pg[];
+  uint8_t* smem = align_smem_1024(smem_raw_pg);
+  float* sm_o = reinterpret_cast<float*>(smem);   // [kPgWarps][ROWS][D + 4], over the rings
   __shared__ Plan plan;
   __shared__ float sm_m[kPgWarps][ROWS], sm_l[kPgWarps][ROWS];
+  __shared__ uint64_t sm_full[kPgWarps][S::kStages];
+  __shared__ int sm_abort;
+  volatile int* abort_flag = &sm_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const KvCache& kc = p.cache;
   const int HR = kc.H_kv * p.row_tiles;
 
-  const long long U = make_plan(p, plan) * HR;
+  if (threadIdx.x < kPgWarps * S::kStages) mbar_init(&sm_full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x == 0) sm_abort = 0;
+  fence_mbar_init();
+  const long long U = make_plan(p, plan) * HR;   // (synchronises the thread block)
   const int G = active_ctas(U, gridDim.x);
   if (blockIdx.x >= G) return;
   const long long u0 = U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
@@ -535,6 +643,9 @@ __global__ void __launch_bounds__(kPgThreads)
   int unit = (int)((u0 - before * HR) % units);
   bool first = true;
   bool bad = p.lens[b] != len;
+  Stream<D, kInt4, ROWS> stream;
+  stream.ring = smem + warp * S::kRing;
+  stream.full = sm_full[warp];
 
   for (long long u = u0; u < u1;) {
     const int n_units = (int)min((long long)(units - unit), u1 - u);
@@ -550,19 +661,25 @@ __global__ void __launch_bounds__(kPgThreads)
       for (int d = 4; d < 32; d <<= 1) x = max(x, __shfl_xor_sync(kFull, x, d));
       w.max_lim = x;
     }
-    const int end = min((unit + n_units) * kUnit, w.max_lim);
-    for (int key0 = unit * kUnit + warp * 32; key0 < end; key0 += kPgWarps * 32) {
+    const int begin = unit * kUnit, end = min((unit + n_units) * kUnit, w.max_lim);
+    const int blocks = end > begin ? (end - begin + 15) / 16 : 0;
+    const int mine = (blocks - warp + kPgWarps - 1) / kPgWarps;
+    stream.begin(p, b, h, begin / 16 + warp, mine);
 #pragma unroll 1
-      for (int k = key0; k < min(key0 + 32, end); k += 16) {
-        const int blk = k >> 4;
-        const int page = kc.table[(long long)b * kc.max_blocks + blk / kc.blocks_per_page];
-        if (page < 0 || page >= kc.num_pages) {
-          bad = true;
-          continue;
-        }
-        const long long off = kv_block_offset<D, kInt4>(kc, page, h, blk % kc.blocks_per_page);
-        w.step(kc.k + off, kc.v + off, k);
+    for (int i = 0; i < S::kStages; ++i) bad |= !stream.request(p);
+#pragma unroll 1
+    for (int i = 0, key0 = begin + 16 * warp; i < mine; ++i, key0 += 16 * kPgWarps) {
+      const uint32_t st = stream.taken % S::kStages;
+      if (!stream.take(abort_flag, p.timeout_ns)) break;
+      if ((stream.present >> st) & 1u) {
+        const uint8_t* kb = stream.ring + st * S::kStage;
+        if (key0 + 16 <= w.min_lim)
+          w.template step<false>(kb, kb + S::kBlock, key0);
+        else
+          w.template step<true>(kb, kb + S::kBlock, key0);
       }
+      __syncwarp();
+      bad |= !stream.request(p);
     }
     // merge the warps: reference and sum of every row, then O
 #pragma unroll
@@ -576,6 +693,7 @@ __global__ void __launch_bounds__(kPgThreads)
       }
     }
     __syncthreads();
+    if (*abort_flag) break;   // (nothing sets it between this barrier and the next take)
 #pragma unroll
     for (int n = 0; n < W::NT; ++n) {
       float f[2];
@@ -629,6 +747,7 @@ __global__ void __launch_bounds__(kPgThreads)
         if (d == 0) p.part_lse[out] = lse2;
       }
     }
+    fence_proxy_async_smem();   // the merge's accesses before the next segment's copies
     __syncthreads();
     u += n_units;
     first = false;
@@ -640,6 +759,17 @@ __global__ void __launch_bounds__(kPgThreads)
       bad = bad || p.lens[b] != len;
       units = units_of(len);
     }
+  }
+  if (*abort_flag) {
+    // a wait ran out: this warp's copies in flight are waited for, once each
+    volatile int never = 0;
+    while (stream.taken < stream.issued) {
+      const uint32_t st = stream.taken % S::kStages;
+      mbar_wait(&stream.full[st], (stream.taken / S::kStages) & 1, &never, p.timeout_ns);
+      ++stream.taken;
+    }
+    g_paged_status = ATTN_ERR_TIMEOUT;
+    return;
   }
   if (bad) g_paged_status = ATTN_ERR_BAD_INDEX;
 }
@@ -694,7 +824,7 @@ __global__ void __launch_bounds__(kPgThreads)
 
 template <int D, bool kInt4, int ROWS>
 cudaError_t launch(const PagedParams& p, cudaStream_t stream) {
-  const size_t smem = (size_t)kPgWarps * ROWS * (D + 4) * sizeof(float);
+  const size_t smem = Smem<D, kInt4, ROWS>::kBytes;
   // per device: the shared-memory attribute set, and the resident CTAs
   static std::atomic<int> resident[64] = {};
   cudaError_t e;
