@@ -126,7 +126,7 @@ def _load():
     lib.attn_kv_read.restype = ci
     lib.attn_fwd_paged.argtypes = [vp] * 7 + [ctypes.c_size_t] + [ci] * 3 + [cf, vp]
     lib.attn_fwd_paged.restype = ci
-    lib.attn_paged_workspace_bytes.argtypes = [ci] * 5
+    lib.attn_paged_workspace_bytes.argtypes = [ci] * 6
     lib.attn_paged_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib
     return lib

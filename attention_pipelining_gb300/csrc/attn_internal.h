@@ -160,7 +160,7 @@ struct KvAppendParams {
   const float* sin;
   int rope_rows, rot_dim, interleaved;
   int H_q, S;
-  int rounds;            // rows of a token per row slot (set at launch)
+  int tokens;            // tokens of a thread block (set at launch)
 };
 
 struct KvReadParams {
@@ -181,21 +181,30 @@ struct PagedParams {
   float* lse;            // [B, H_q, S_q]
   const int* lens;       // [B]
   const int* q_lens;     // [B] or nullptr
-  float* part_o;         // workspace: [2 kPagedMaxCtas, rows, D]
-  float* part_lse;       // workspace: [2 kPagedMaxCtas, rows], base 2
+  // workspace, of the n CTAs there may be where items are split:
+  float* part_o;         // [2 n, rows, D]
+  float* part_lse;       // [2 n, rows], base 2
+  int4* shared;          // [n], the item that CTA c began and did not finish: {sequence (-1:
+                         // none), head and row tile, slot of its first part, last CTA that has
+                         // a part}
   int H_q, S_q, group;   // group = H_q / H_kv
-  int row_tiles;         // ceil(group * S_q / rows)
+  int row_tiles;         // ceil(group * S_q / rows) (set at launch)
+  int unit, split;       // keys per unit of work, and whether items are split (set at launch)
   int causal;
   float scale_log2;
+  uint32_t code_base_low, code_base_high;  // fp16 pairs of 1024 and 64 (see the kernel)
   unsigned long long timeout_ns;  // budget of any single wait inside the kernel
 };
 
-// CTAs of the paged attention, at most (the workspace holds two parts of each).
-constexpr int kPagedMaxCtas = 1024;
+// Keys per unit of the paged attention's work, and up to how many keys (of the
+// block tables' span) an item is kept whole; and its CTAs, at most.
+constexpr int kPagedUnit = 128;
+constexpr int kPagedWholeKeys = 1024;
+constexpr int kPagedMaxCtas = 512;
 
 cudaError_t launch_kv_append(const KvAppendParams& p, int D, bool int4, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadParams& p, int D, bool int4, cudaStream_t stream);
-// Queues the paged attention with `rows` (8, 16 or 32) query rows to a tile.
+// Queues the paged attention with `rows` (8, 16, 32 or 64) query rows to a tile.
 cudaError_t launch_attn_paged(const PagedParams& p, int D, bool int4, int rows,
                               cudaStream_t stream);
 // Read (and optionally clear) the cache's and the paged attention's status words.

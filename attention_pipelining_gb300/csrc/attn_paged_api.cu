@@ -55,14 +55,23 @@ attn_status_t take_tensor(const attn_bhsd_t* t, int B, int H, int S, KvTensor* o
   return ATTN_OK;
 }
 
-// Query rows to a tile: the smallest that holds a KV head's rows, at most 32.
+// Query rows to a tile: the smallest that holds a KV head's rows, at most 64.
 int tile_rows(int group, int S_q) {
   const int64_t rows = (int64_t)group * S_q;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-size_t paged_bytes(int rows, int D) {
-  return (size_t)2 * kPagedMaxCtas * rows * (D + 1) * sizeof(float);
+constexpr size_t kLeastWorkspace = 256;   // reported where none is used: 0 says invalid
+
+// CTAs that may write parts to the workspace: none where an item is kept whole.
+int64_t part_ctas(int64_t B, int64_t H_kv, int64_t rows, int tile, int64_t max_keys) {
+  if (max_keys <= kPagedWholeKeys) return 0;
+  const int64_t units = B * H_kv * ((rows + tile - 1) / tile) * ((max_keys + kPagedUnit - 1) / kPagedUnit);
+  return units < kPagedMaxCtas ? units : kPagedMaxCtas;
+}
+
+size_t part_bytes(int64_t ctas, int tile, int D) {
+  return (size_t)ctas * (2 * tile * (D + 1) * sizeof(float) + sizeof(int4));
 }
 
 // The sizes of a paged attention: ATTN_OK where its rows and tiles can be
@@ -71,8 +80,8 @@ attn_status_t check_rows(int B, int H_q, int H_kv, int S_q) {
   if (B <= 0 || H_q <= 0 || H_kv <= 0 || S_q <= 0 || H_q % H_kv != 0) return ATTN_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)(H_q / H_kv) * S_q;
   if (rows >= (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
-  // one thread block an item merges the parts
-  if (((rows + 31) / 32) * B * H_kv >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+  // heads times row tiles are counted in an int
+  if (((rows + 63) / 64) * H_kv >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -146,9 +155,11 @@ attn_status_t attn_kv_read(const attn_kv_cache_t* cache, void* k_out, void* v_ou
              : ATTN_ERR_CUDA;
 }
 
-size_t attn_paged_workspace_bytes(int B, int H_q, int H_kv, int S_q, int D) {
-  if (check_rows(B, H_q, H_kv, S_q) != ATTN_OK || (D != 64 && D != 128)) return 0;
-  return paged_bytes(tile_rows(H_q / H_kv, S_q), D);
+size_t attn_paged_workspace_bytes(int B, int H_q, int H_kv, int S_q, int D, int max_keys) {
+  if (check_rows(B, H_q, H_kv, S_q) != ATTN_OK || (D != 64 && D != 128) || max_keys <= 0) return 0;
+  const int group = H_q / H_kv, tile = tile_rows(group, S_q);
+  const size_t n = part_bytes(part_ctas(B, H_kv, (int64_t)group * S_q, tile, max_keys), tile, D);
+  return n < kLeastWorkspace ? kLeastWorkspace : n;
 }
 
 attn_status_t attn_fwd_paged(const attn_kv_cache_t* cache, const attn_bhsd_t* q, void* o,
@@ -159,7 +170,7 @@ attn_status_t attn_fwd_paged(const attn_kv_cache_t* cache, const attn_bhsd_t* q,
   std::memset(&p, 0, sizeof(p));
   attn_status_t st = take_cache(cache, &p.cache);
   if (st != ATTN_OK) return st;
-  if (!o || !lse || !lens || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!o || !lse || !lens) return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if ((st = check_rows(cache->B, H_q, cache->H_kv, S_q)) != ATTN_OK) return st;
@@ -169,19 +180,24 @@ attn_status_t attn_fwd_paged(const attn_kv_cache_t* cache, const attn_bhsd_t* q,
     return ATTN_ERR_MISALIGNED;
   p.group = H_q / cache->H_kv;
   const int rows = tile_rows(p.group, S_q);
-  if (workspace_bytes < paged_bytes(rows, cache->D)) return ATTN_ERR_INVALID_ARG;
+  const int64_t parts = part_ctas(cache->B, cache->H_kv, (int64_t)p.group * S_q, rows,
+                                  p.cache.capacity);
+  if (parts > 0 && (!workspace || workspace_bytes < part_bytes(parts, rows, cache->D)))
+    return ATTN_ERR_INVALID_ARG;
   if ((st = check_device()) != ATTN_OK) return st;
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
   p.lens = lens;
   p.q_lens = q_lens;
   p.part_o = static_cast<float*>(workspace);
-  p.part_lse = p.part_o + (size_t)2 * kPagedMaxCtas * rows * cache->D;
+  p.part_lse = p.part_o + (size_t)2 * parts * rows * cache->D;
+  p.shared = reinterpret_cast<int4*>(p.part_lse + (size_t)2 * parts * rows);
   p.H_q = H_q;
   p.S_q = S_q;
-  p.row_tiles = (int)(((int64_t)p.group * S_q + rows - 1) / rows);
   p.causal = causal;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.code_base_low = 0x64006400u;
+  p.code_base_high = 0x54005400u;
   p.timeout_ns = kDefaultTimeoutNs;
   if (cache->format == ATTN_KV_BF16) {
     const uint64_t heads = (uint64_t)cache->num_pages * cache->H_kv;

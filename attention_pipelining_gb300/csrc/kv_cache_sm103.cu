@@ -1,11 +1,12 @@
 // kv_cache_sm103.cu -- new tokens into the paged key/value cache (rotation,
 // 4-bit quantisation) and cached tokens back into contiguous tensors.
 //
-// Both kernels stream: a token's vector of one head is a "row" of D elements
-// that D / 8 neighbouring lanes hold, 16 bytes (8 elements) each, so that one
-// lane's 8 elements of a 4-bit row are one 32-bit word of codes and a scale's
-// group of 32 elements is four neighbouring lanes.
+// Both kernels stream, and are bound by HBM as long as the rotation's and the
+// quantisation's instructions stay below about ten an element: 6.8 TB/s of 4
+// bytes an element (bf16 read and written) leave each SM 22 thread-instructions
+// an element, of 2.6 bytes (a 4-bit write) 14.
 #include <cstdint>
+#include <cstring>
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
@@ -18,19 +19,19 @@ __device__ int g_kv_status = 0;
 
 namespace {
 
-constexpr int kKvThreads = 256;
+constexpr int kKvThreads = 256;         // of the read kernel
+constexpr int kAppendThreads = 128;
+constexpr int kAppendBlocks = 1216;     // eight blocks on each of 152 SMs
 
 // ---------------------------------------------------------------- rotation
 
-// x a - y b rounded once to bf16 (returned as a float): the products' and the
-// sum's rounding errors are recovered (fma, two-sum) and added back, and the
-// fp32 result, when it falls on a tie of the bf16 rounding that the remainder
-// breaks, is moved one step to the remainder's side.  x and y are bf16 values
-// and a and b fp32, so the exact value has at most 32 significant bits a
-// product: without this, about one element in 2^15 would round the other way
-// than the exact value, and in a 4-bit cache change its code.  Non-finite
+// x a - y b rounded once to bf16 (returned as a float).  x and y are bf16
+// values and a and b fp32, so the exact value may have more bits than a float:
+// the products' and the sum's rounding errors are recovered (fma, two-sum) and
+// added back, and the fp32 result, when it falls on a tie of the bf16 rounding
+// that the remainder breaks, is moved one step to the remainder's side.  Non-finite
 // values take the plain formula's result.
-__device__ __forceinline__ float rotate_bf16(float x, float a, float y, float b) {
+__device__ __noinline__ float rotate_bf16(float x, float a, float y, float b) {
   const float h = __fmul_rn(x, a), h2 = __fmul_rn(-y, b);
   const float e = __fmaf_rn(x, a, -h), e2 = __fmaf_rn(-y, b, -h2);
   const float s = __fadd_rn(h, h2);
@@ -45,70 +46,142 @@ __device__ __forceinline__ float rotate_bf16(float x, float a, float y, float b)
   return __uint_as_float(u);
 }
 
+// The same for eight elements in pairs, r = x c + y s (y negated by the caller
+// where the formula subtracts): first with four operations an element,
+// fma(x, c, h) + e with h + e = y s exactly, which is off by at most two units of
+// fp32's last place; only where that leaves the bf16 rounding open (four units
+// around a tie: one element in 2^13) or a value is not finite, by rotate_bf16.
+// Rounding the plain fp32 formula instead would round about one element in 2^15
+// the other way than the exact value, and in a 4-bit cache change its code.
+__device__ __forceinline__ void rotate8(const uint64_t (&x)[4], const uint64_t (&y)[4],
+                                        const uint64_t (&c)[4], const uint64_t (&s)[4],
+                                        uint32_t (&out)[4]) {
+  const uint64_t minus = f2_pack(-1.f, -1.f), zero = f2_pack(0.f, 0.f);
+  uint32_t nearest = 0xffffffffu;   // of the even elements, of the odd ones
+  uint64_t finite = zero;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t h = f2_mul(y[i], s[i]);
+    const uint64_t e = f2_fma(y[i], s[i], f2_mul(h, minus));
+    const uint64_t r = f2_add(f2_fma(x[i], c[i], h), e);
+    finite = f2_fma(r, zero, finite);
+    float r0, r1;
+    f2_unpack(r, r0, r1);
+    nearest = __viaddmin_u16x2(
+        __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x5410u), 0x80048004u, nearest);
+    out[i] = pack_bf16x2(r0, r1);
+  }
+  float f0, f1;
+  f2_unpack(finite, f0, f1);
+  if ((nearest & 0xffffu) <= 8u || (nearest >> 16) <= 8u || f0 + f1 != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x0, x1, y0, y1, c0, c1, s0, s1;
+      f2_unpack(x[i], x0, x1);
+      f2_unpack(y[i], y0, y1);
+      f2_unpack(c[i], c0, c1);
+      f2_unpack(s[i], s0, s1);
+      out[i] = pack_bf16x2(rotate_bf16(x0, c0, -y0, s0), rotate_bf16(x1, c1, -y1, s1));
+    }
+  }
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // The rotation of this lane's 8 elements (chunk c of its row), in place;
 // every lane of the row takes part.  With pairs (d, d + rot / 2) the partner
-// chunk is another lane's; with adjacent pairs it is the lane's own.
+// chunk is another lane's, and cs, sn belong to the elements; with adjacent pairs
+// it is the lane's own, and they belong to its four pairs.
 template <int kLanes>
-__device__ __forceinline__ void rotate_chunk(uint4& w, int c, int rot_chunks, bool interleaved,
-                                             const float (&cs)[8], const float (&sn)[8]) {
-  uint32_t x[4] = {w.x, w.y, w.z, w.w};
-  if (interleaved) {
-    if (c < rot_chunks) {
+__device__ __forceinline__ void rotate_chunk(uint4& w, uint32_t row_mask, int c, int rot_chunks,
+                                             bool interleaved,
+                                             const uint64_t (&cs)[4], const uint64_t (&sn)[4]) {
+  const uint32_t own[4] = {w.x, w.y, w.z, w.w};
+  uint64_t x[4], y[4];
+  uint32_t out[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = bf16_lo(x[i]), b = bf16_hi(x[i]);
-        x[i] = pack_bf16x2(rotate_bf16(a, cs[i], b, sn[i]), rotate_bf16(b, cs[i], -a, sn[i]));
-      }
+  for (int i = 0; i < 4; ++i) x[i] = f2_pack(bf16_lo(own[i]), bf16_hi(own[i]));
+  if (interleaved) {   // (a cos - b sin, b cos + a sin)
+    uint64_t ci[4], si[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = f2_pack(-bf16_hi(own[i]), bf16_lo(own[i]));
+      float c0, c1, s0, s1;
+      f2_unpack(cs[i >> 1], c0, c1);
+      f2_unpack(sn[i >> 1], s0, s1);
+      ci[i] = (i & 1) ? f2_pack(c1, c1) : f2_pack(c0, c0);
+      si[i] = (i & 1) ? f2_pack(s1, s1) : f2_pack(s0, s0);
     }
+    rotate8(x, y, ci, si, out);
   } else {
     const int half = rot_chunks >> 1;
     const bool first = c < half;
     const int partner = first ? c + half : c < rot_chunks ? c - half : c;
-    uint32_t y[4];
+    const uint32_t flip = first ? 0x80008000u : 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner, kLanes);
-    if (c < rot_chunks) {
-      const float sg = first ? 1.f : -1.f;   // (a cos - b sin), (b cos + a sin)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = pack_bf16x2(
-            rotate_bf16(bf16_lo(x[i]), cs[2 * i], sg * bf16_lo(y[i]), sn[2 * i]),
-            rotate_bf16(bf16_hi(x[i]), cs[2 * i + 1], sg * bf16_hi(y[i]), sn[2 * i + 1]));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t o = __shfl_sync(row_mask, own[i], partner, kLanes) ^ flip;
+      y[i] = f2_pack(bf16_lo(o), bf16_hi(o));
     }
+    rotate8(x, y, cs, sn, out);
   }
-  w = make_uint4(x[0], x[1], x[2], x[3]);
+  if (c < rot_chunks) w = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 // ---------------------------------------------------------------- 4 bits
 
 // The codes (one word, element n in nibble n) and the scale of this lane's 8
-// elements; its group is the four lanes c / 4 * 4 .. + 3.  The division is
-// the IEEE one: a code on a tie goes to the even one, as the definition says.
-__device__ __forceinline__ uint32_t quantise8(const uint4& w, uint32_t& scale_bits) {
+// elements; its group is the four lanes c / 4 * 4 .. + 3.  rint(x / s) without a
+// division an element: x and s are bf16 numbers, so x / s either lies on a tie
+// k + 1/2 exactly or at least 2^-10 from one; x (1 / s), off by 2^-21 at most,
+// rounded to a multiple of 2^-11 is then on the tie in the first case and on
+// the right side of it in the second.
+__device__ __forceinline__ uint32_t quantise8(const uint4& w, uint32_t row_mask,
+                                              uint32_t& scale_bits) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
   // the largest magnitude by the bits' order, where a NaN is above infinity
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t m2 = __vimax3_u16x2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu,
+                                     __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu));
+  uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+  m = max(m, __shfl_xor_sync(row_mask, m, 1));
+  m = max(m, __shfl_xor_sync(row_mask, m, 2));
   if (m >= 0x7f80u) {   // an infinity or a NaN in the group
     scale_bits = 0x7fffu;
     return 0x88888888u;
   }
-  scale_bits = pack_bf16x2(__fdiv_rn(__uint_as_float(m << 16), 7.f), 0.f) & 0xffffu;
+  // (m / 7 is never nearer than 2^-13 to a tie of its rounding to bf16)
+  scale_bits = pack_bf16x2(__uint_as_float(m << 16) * (1.f / 7.f), 0.f) & 0xffffu;
   const float s = __uint_as_float(scale_bits << 16);
-  uint32_t codes = 0;
+  uint32_t u[8];
+  if (s >= 1.0e-30f) {
+    const float inv = __frcp_rn(s);
+    const uint64_t inv2 = f2_pack(inv, inv), grid = f2_pack(6144.f, 6144.f);
+    const uint64_t back = f2_pack(-6144.f, -6144.f);
+    // 1.5 * 2^23 + 8: the sum's last bits are rint(q) + 8, ties to even
+    const uint64_t whole = f2_pack(12582920.f, 12582920.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = (i & 1) ? bf16_hi(x[i >> 1]) : bf16_lo(x[i >> 1]);
-    const float q = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(v, s)), -7.f), 7.f) : 0.f;
-    codes |= (uint32_t)((int)q + 8) << (4 * i);
+    for (int i = 0; i < 4; ++i) {
+      uint64_t q = f2_mul(f2_pack(bf16_lo(x[i]), bf16_hi(x[i])), inv2);
+      q = f2_add(f2_add(f2_add(q, grid), back), whole);   // by way of a multiple of 2^-11
+      float q0, q1;
+      f2_unpack(q, q0, q1);
+      u[2 * i] = __float_as_uint(q0);
+      u[2 * i + 1] = __float_as_uint(q1);
+    }
+  } else {   // few or no significant bits left in s: divide, and clamp
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = (i & 1) ? bf16_hi(x[i >> 1]) : bf16_lo(x[i >> 1]);
+      const float q = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(v, s)), -7.f), 7.f) : 0.f;
+      u[i] = (uint32_t)((int)q + 8);
+    }
   }
-  return codes;
+  const uint32_t even = __byte_perm(__byte_perm(u[0], u[2], 0x0040u), __byte_perm(u[4], u[6], 0x0040u),
+                                    0x5410u);
+  const uint32_t odd = __byte_perm(__byte_perm(u[1], u[3], 0x0040u), __byte_perm(u[5], u[7], 0x0040u),
+                                   0x5410u);
+  return (even & 0x0f0f0f0fu) | (odd & 0x0f0f0f0fu) << 4;
 }
 
 // Stores a lane's codes and its group's scale into the block of its token.
@@ -129,164 +202,215 @@ __device__ __forceinline__ void store4(uint8_t* block, int r, int c, bool value,
     *reinterpret_cast<uint16_t*>(block + 8 * D + (r * G + j) * 2) = (uint16_t)scale_bits;
 }
 
-template <int D>
-__device__ __forceinline__ void load4(const uint8_t* block, int r, int c, bool value,
-                                      uint32_t& codes, float& scale) {
-  constexpr int G = D / 32;
-  const int j = c >> 2, t = c & 3;
-  if (value) {
-    const uint8_t* p = block + (((r >> 1) * 8 + 2 * t) * 2 + (r & 1)) * 2 * G + 2 * j;
-    codes = (uint32_t)*reinterpret_cast<const uint16_t*>(p) |
-            (uint32_t)*reinterpret_cast<const uint16_t*>(p + 4 * G) << 16;
-  } else {
-    codes = *reinterpret_cast<const uint32_t*>(block + r * (D / 2) + (t * G + j) * 4);
-  }
-  scale = __uint_as_float(
-      (uint32_t)*reinterpret_cast<const uint16_t*>(block + 8 * D + (r * G + j) * 2) << 16);
-}
-
 // ---------------------------------------------------------------- append
 
-// One thread block handles heads blockIdx.y * kSlots * p.rounds .. of one
-// token (its rows: H_q queries, H_kv keys, H_kv values), kSlots at a time: the
-// token's rotation, 8 cosines and sines a lane, is read once for all of them.
+// A token's vector of one head is a row that D / 8 neighbouring lanes hold, 8
+// elements each: one word of codes, a quarter of a scale's group.  A thread
+// block has kSlots places for rows and takes one token, whose H_q queries, then
+// H_kv keys and H_kv values its places take in turn (with gridDim.y blocks to a
+// token, all their places), so that a lane reads its part of the token's rotation,
+// 8 cosines and sines, once; or, where a token has few rows, p.tokens tokens.  Rows
+// side by side in a warp may be of different kinds: they diverge, and only a row's
+// own lanes exchange values.
 template <int D, bool kInt4>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvAppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const KvAppendParams p) {
   constexpr int kLanes = D / 8;
-  constexpr int kSlots = kKvThreads / kLanes;
-  const int b = blockIdx.x / p.S, i = blockIdx.x % p.S;
-  if (p.new_lens && i >= p.new_lens[b]) return;
-  const int c = threadIdx.x % kLanes, slot_row = threadIdx.x / kLanes;
-  const long long pos = (long long)p.start[b] + i;
+  constexpr int kSlots = kAppendThreads / kLanes;
   const KvCache& kc = p.cache;
-  const bool in_range = pos >= 0 && pos < kc.capacity && (p.rot_dim == 0 || pos < p.rope_rows);
-  int page = -1;
-  if (in_range) page = kc.table[(long long)b * kc.max_blocks + pos / kc.page_size];
-  if (page < 0 || page >= kc.num_pages) {
-    if (threadIdx.x == 0) g_kv_status = ATTN_ERR_BAD_INDEX;
+  const int rows = p.H_q + 2 * kc.H_kv;
+  const int c = threadIdx.x % kLanes, place = threadIdx.x / kLanes;
+  const uint32_t row_mask = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
+  const int sub = p.tokens > 1 ? place / rows : 0;   // which of the block's tokens
+  const int first = p.tokens > 1 ? place % rows : blockIdx.y * kSlots + place;
+  const int step = p.tokens > 1 ? rows : kSlots * gridDim.y;
+  const uint32_t token = blockIdx.x * p.tokens + sub;
+  if (sub >= p.tokens || token >= (uint32_t)(kc.B * p.S)) return;
+  const int b = (int)(token / (uint32_t)p.S), i = (int)(token % (uint32_t)p.S);
+  if (p.new_lens && i >= p.new_lens[b]) return;
+  const auto row_of = [&](const KvTensor& t, int h) {
+    return t.data + b * t.sb + h * t.sh + i * t.ss + 8 * c;
+  };
+  const auto load = [](const uint16_t* src) { return *reinterpret_cast<const uint4*>(src); };
+  // the first loads need neither the position nor the page
+  int row = first;
+  const uint16_t* q_src = row_of(p.q, row);
+  uint4 q_next = row < p.H_q ? load(q_src) : make_uint4(0, 0, 0, 0);
+  const auto kv_source = [&](int r) {
+    const bool v = r >= p.H_q + kc.H_kv;
+    return row_of(v ? p.v : p.k, v ? r - p.H_q - kc.H_kv : r - p.H_q);
+  };
+  int kv_row = row;   // this place's first key or value
+  if (kv_row < p.H_q) kv_row += (p.H_q - kv_row + step - 1) / step * step;
+  uint4 kv_next = kv_row < rows ? load(kv_source(kv_row)) : make_uint4(0, 0, 0, 0);
+  const long long pos = (long long)p.start[b] + i;
+  const int rot_chunks = p.rot_dim / 8;
+  const bool good = pos >= 0 && pos < kc.capacity && (p.rot_dim == 0 || pos < p.rope_rows);
+  const int page =
+      good ? kc.table[(long long)b * kc.max_blocks + (int)pos / kc.page_size] : -1;
+  uint64_t cs[4] = {}, sn[4] = {};   // pairs of cosines and of sines
+  if (good && c < rot_chunks) {
+    const long long at = pos * (p.rot_dim / 2) +
+                         (p.interleaved ? 4 * c : 8 * (c < rot_chunks / 2 ? c : c - rot_chunks / 2));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && p.interleaved) break;
+      const float4 a = *reinterpret_cast<const float4*>(p.cos + at + 4 * h);
+      const float4 d = *reinterpret_cast<const float4*>(p.sin + at + 4 * h);
+      cs[2 * h] = f2_pack(a.x, a.y), cs[2 * h + 1] = f2_pack(a.z, a.w);
+      sn[2 * h] = f2_pack(d.x, d.y), sn[2 * h + 1] = f2_pack(d.z, d.w);
+    }
+  }
+  if ((unsigned)page >= (unsigned)kc.num_pages) {
+    g_kv_status = ATTN_ERR_BAD_INDEX;
     return;
   }
-  const int slot = (int)(pos % kc.page_size);
-  const int rot_chunks = p.rot_dim / 8;
-  float cs[8], sn[8];
-  if (c < rot_chunks) {
-    const long long row = pos * (p.rot_dim / 2);
-    if (p.interleaved) {
-      const float4 a = *reinterpret_cast<const float4*>(p.cos + row + 4 * c);
-      const float4 d = *reinterpret_cast<const float4*>(p.sin + row + 4 * c);
-      cs[0] = a.x, cs[1] = a.y, cs[2] = a.z, cs[3] = a.w;
-      sn[0] = d.x, sn[1] = d.y, sn[2] = d.z, sn[3] = d.w;
-    } else {
-      const int at = 8 * (c < rot_chunks / 2 ? c : c - rot_chunks / 2);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 a = *reinterpret_cast<const float4*>(p.cos + row + at + 4 * h);
-        const float4 d = *reinterpret_cast<const float4*>(p.sin + row + at + 4 * h);
-        cs[4 * h] = a.x, cs[4 * h + 1] = a.y, cs[4 * h + 2] = a.z, cs[4 * h + 3] = a.w;
-        sn[4 * h] = d.x, sn[4 * h + 1] = d.y, sn[4 * h + 2] = d.z, sn[4 * h + 3] = d.w;
-      }
-    }
+  uint16_t* q_dst = p.q_out + (((long long)b * p.H_q + row) * p.S + i) * D + 8 * c;
+  for (; row < p.H_q; row += step) {
+    uint4 w = q_next;
+    q_src += step * p.q.sh;
+    if (row + step < p.H_q) q_next = load(q_src);
+    if (rot_chunks) rotate_chunk<kLanes>(w, row_mask, c, rot_chunks, p.interleaved, cs, sn);
+    *reinterpret_cast<uint4*>(q_dst) = w;
+    q_dst += (long long)step * p.S * D;
   }
-  const int rows = p.H_q + 2 * kc.H_kv;
-  for (int n = 0; n < p.rounds; ++n) {
-    const int row = (blockIdx.y * p.rounds + n) * kSlots + slot_row;
-    const bool live = row < rows;
-    const bool is_q = row < p.H_q;
-    const bool is_v = row >= p.H_q + kc.H_kv;
-    const int h = is_q ? row : is_v ? row - p.H_q - kc.H_kv : row - p.H_q;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live) {
-      const KvTensor& t = is_q ? p.q : is_v ? p.v : p.k;
-      w = *reinterpret_cast<const uint4*>(t.data + b * t.sb + h * t.sh + i * t.ss + 8 * c);
-    }
-    // a row's lanes agree on is_v, but a warp's rows may not: all take part
-    uint4 turned = w;
-    if (rot_chunks) rotate_chunk<kLanes>(turned, c, rot_chunks, p.interleaved, cs, sn);
-    if (!is_v) w = turned;
-    uint32_t codes = 0, scale = 0;
-    if (kInt4) codes = quantise8(w, scale);
-    if (!live) continue;
-    if (is_q) {
-      *reinterpret_cast<uint4*>(p.q_out + (((long long)b * p.H_q + h) * p.S + i) * D + 8 * c) = w;
+  const int slot = (int)pos % kc.page_size;
+  for (row = kv_row; row < rows; row += step) {
+    const bool v = row >= p.H_q + kc.H_kv;
+    const int h = v ? row - p.H_q - kc.H_kv : row - p.H_q;
+    uint4 w = kv_next;
+    if (row + step < rows) kv_next = load(kv_source(row + step));
+    if (rot_chunks && !v)
+      rotate_chunk<kLanes>(w, row_mask, c, rot_chunks, p.interleaved, cs, sn);
+    uint8_t* block = const_cast<uint8_t*>(v ? kc.v : kc.k) +
+                     kv_block_offset<D, kInt4>(kc, page, h, slot >> 4);
+    if (kInt4) {
+      uint32_t scale;
+      const uint32_t codes = quantise8(w, row_mask, scale);
+      store4<D>(block, slot & 15, c, v, codes, scale);
     } else {
-      uint8_t* block = const_cast<uint8_t*>(is_v ? kc.v : kc.k) +
-                       kv_block_offset<D, kInt4>(kc, page, h, slot >> 4);
-      if (kInt4)
-        store4<D>(block, slot & 15, c, is_v, codes, scale);
-      else
-        *reinterpret_cast<uint4*>(block + (slot & 15) * D * 2 + 16 * c) = w;
+      *reinterpret_cast<uint4*>(block + (slot & 15) * D * 2 + 16 * c) = w;
     }
   }
 }
 
 // ---------------------------------------------------------------- read
 
-// One row slot handles rows of k_out (blockIdx.y even: keys, odd: values).
+// One warp copies one 16-token block of one head's keys or values (blockIdx.y
+// even or odd): it reads the block's codes 16 bytes a lane, 8 or 4 consecutive
+// elements of which go out together (bf16: 16 bytes of a token's vector).
 template <int D, bool kInt4>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadParams p) {
-  constexpr int kLanes = D / 8;
-  constexpr int kSlots = kKvThreads / kLanes;
   const KvCache& kc = p.cache;
-  const int c = threadIdx.x % kLanes;
+  const int lane = threadIdx.x & 31;
   const bool value = blockIdx.y & 1;
-  const long long row = (long long)blockIdx.x * kSlots + threadIdx.x / kLanes;
   const int h = blockIdx.y >> 1;
-  const long long per_head = (long long)kc.B * p.S;
-  if (row >= per_head) return;
-  const int b = (int)(row / p.S), i = (int)(row % p.S);
-  const long long pos = (p.start ? (long long)p.start[b] : 0) + i;
+  // blocks of a sequence that its S positions may touch
+  const int per_seq = (p.S + 15) / 16 + (p.start ? 1 : 0);
+  const long long unit = (long long)blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= (long long)kc.B * per_seq) return;
+  const int b = (int)(unit / per_seq);
+  const long long first = p.start ? p.start[b] : 0;
   const int len = p.lens[b];
-  if (len < 0 || len > kc.capacity || pos < 0) {
-    if (c == 0) g_kv_status = ATTN_ERR_BAD_INDEX;
-    if (pos < 0) return;
-  }
-  if (pos >= len || pos >= kc.capacity) return;
-  const int page = kc.table[(long long)b * kc.max_blocks + pos / kc.page_size];
-  if (page < 0 || page >= kc.num_pages) {
-    if (c == 0) g_kv_status = ATTN_ERR_BAD_INDEX;
+  if ((len < 0 || len > kc.capacity || first < 0) && lane == 0) g_kv_status = ATTN_ERR_BAD_INDEX;
+  const long long lo = first < 0 ? 0 : first;                     // positions [lo, hi)
+  long long hi = first + p.S;
+  hi = hi < len ? hi : len;
+  hi = hi < kc.capacity ? hi : kc.capacity;
+  const long long pos0 = (lo / 16 + unit % per_seq) * 16;         // of the block
+  if (pos0 >= hi) return;
+  const int blk = (int)(pos0 >> 4);
+  const int page = kc.table[(long long)b * kc.max_blocks + blk / kc.blocks_per_page];
+  if ((unsigned)page >= (unsigned)kc.num_pages) {
+    if (lane == 0) g_kv_status = ATTN_ERR_BAD_INDEX;
     return;
   }
-  const int slot = (int)(pos % kc.page_size);
-  const uint8_t* block = (value ? kc.v : kc.k) + kv_block_offset<D, kInt4>(kc, page, h, slot >> 4);
-  uint4 w;
-  if (kInt4) {
-    uint32_t codes, x[4];
-    float s;
-    load4<D>(block, slot & 15, c, value, codes, s);
+  const uint8_t* block = (value ? kc.v : kc.k) +
+                         kv_block_offset<D, kInt4>(kc, page, h, blk % kc.blocks_per_page);
+  uint16_t* out = (value ? p.v_out : p.k_out) +
+                  (((long long)b * kc.H_kv + h) * p.S + (pos0 - first)) * D;   // of token 0
+  const auto wanted = [&](int r) { return pos0 + r >= lo && pos0 + r < hi; };
+  if constexpr (!kInt4) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int c = lane % kLanes;
+    uint4 w[16 / kRows];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const float a = (float)((int)((codes >> (8 * n)) & 15u) - 8) * s;
-      const float d = (float)((int)((codes >> (8 * n + 4)) & 15u) - 8) * s;
-      x[n] = pack_bf16x2(a, d);
+    for (int n = 0; n < 16 / kRows; ++n)
+      w[n] = *reinterpret_cast<const uint4*>(block + (n * kRows + lane / kLanes) * D * 2 + 16 * c);
+#pragma unroll
+    for (int n = 0; n < 16 / kRows; ++n) {
+      const int r = n * kRows + lane / kLanes;
+      if (wanted(r)) *reinterpret_cast<uint4*>(out + r * D + 8 * c) = w[n];
     }
-    w = make_uint4(x[0], x[1], x[2], x[3]);
   } else {
-    w = *reinterpret_cast<const uint4*>(block + (slot & 15) * D * 2 + 16 * c);
+    constexpr int G = D / 32;
+    const auto two = [](uint32_t codes, int n, float s) {   // elements n, n + 1
+      return pack_bf16x2((float)((int)((codes >> (4 * n)) & 15u) - 8) * s,
+                         (float)((int)((codes >> (4 * n + 4)) & 15u) - 8) * s);
+    };
+    if (!value) {   // 4 G bytes: key r's words (t, j)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int r = n * 8 + (lane >> 2), t = lane & 3;
+        uint32_t w[G];
+        uint16_t sc[G];
+        memcpy(w, __builtin_assume_aligned(block + r * (D / 2) + t * 4 * G, 4 * G), 4 * G);
+        memcpy(sc, __builtin_assume_aligned(block + 8 * D + r * 2 * G, 2 * G), 2 * G);
+        if (!wanted(r)) continue;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          const float s = __uint_as_float((uint32_t)sc[j] << 16);
+          *reinterpret_cast<uint4*>(out + r * D + 32 * j + 8 * t) =
+              make_uint4(two(w[j], 0, s), two(w[j], 2, s), two(w[j], 4, s), two(w[j], 6, s));
+        }
+      }
+    } else {        // 4 G bytes: elements 32 j + 4 g .. of both tokens of a pair
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int pair = n * 4 + (lane >> 3), g = lane & 7;
+        uint16_t w[2][G], sc[2][G];
+        memcpy(w, __builtin_assume_aligned(block + (pair * 8 + g) * 4 * G, 4 * G), 4 * G);
+        memcpy(sc, __builtin_assume_aligned(block + 8 * D + pair * 4 * G, 4 * G), 4 * G);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = 2 * pair + k;
+          if (!wanted(r)) continue;
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            const float s = __uint_as_float((uint32_t)sc[k][j] << 16);
+            *reinterpret_cast<uint2*>(out + r * D + 32 * j + 4 * g) =
+                make_uint2(two(w[k][j], 0, s), two(w[k][j], 2, s));
+          }
+        }
+      }
+    }
   }
-  uint16_t* out = value ? p.v_out : p.k_out;
-  *reinterpret_cast<uint4*>(out + (((long long)b * kc.H_kv + h) * p.S + i) * D + 8 * c) = w;
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendParams& p0, int D, bool int4, cudaStream_t stream) {
   KvAppendParams p = p0;
-  const int slots = kKvThreads / (D / 8);
+  const int slots = kAppendThreads / (D / 8);
   const int rows = p.H_q + 2 * p.cache.H_kv;
-  p.rounds = 1;
-  const int ny = (rows + slots * p.rounds - 1) / (slots * p.rounds);
-  const dim3 grid((unsigned)((long long)p.cache.B * p.S), (unsigned)ny);
-  if (D == 128 && int4) kv_append_kernel<128, true><<<grid, kKvThreads, 0, stream>>>(p);
-  else if (D == 128) kv_append_kernel<128, false><<<grid, kKvThreads, 0, stream>>>(p);
-  else if (int4) kv_append_kernel<64, true><<<grid, kKvThreads, 0, stream>>>(p);
-  else kv_append_kernel<64, false><<<grid, kKvThreads, 0, stream>>>(p);
+  const long long tokens = (long long)p.cache.B * p.S;
+  // Tokens of few rows share a block; a token of many rows is one block's, or,
+  // when there are few tokens, is spread over several.
+  p.tokens = rows < slots ? slots / rows : 1;
+  const long long blocks = (tokens + p.tokens - 1) / p.tokens;
+  const int most = (rows + slots - 1) / slots;
+  const long long spread = kAppendBlocks / blocks;
+  const dim3 grid((unsigned)blocks, (unsigned)(spread < 1 ? 1 : spread < most ? spread : most));
+  if (D == 128 && int4) kv_append_kernel<128, true><<<grid, kAppendThreads, 0, stream>>>(p);
+  else if (D == 128) kv_append_kernel<128, false><<<grid, kAppendThreads, 0, stream>>>(p);
+  else if (int4) kv_append_kernel<64, true><<<grid, kAppendThreads, 0, stream>>>(p);
+  else kv_append_kernel<64, false><<<grid, kAppendThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, int D, bool int4, cudaStream_t stream) {
-  const int slots = kKvThreads / (D / 8);
-  const long long rows = (long long)p.cache.B * p.S;
-  const dim3 grid((unsigned)((rows + slots - 1) / slots), (unsigned)(2 * p.cache.H_kv));
+  const long long blocks = (long long)p.cache.B * ((p.S + 15) / 16 + (p.start ? 1 : 0));
+  const int per = kKvThreads / 32;
+  const dim3 grid((unsigned)((blocks + per - 1) / per), (unsigned)(2 * p.cache.H_kv));
   if (D == 128 && int4) kv_read_kernel<128, true><<<grid, kKvThreads, 0, stream>>>(p);
   else if (D == 128) kv_read_kernel<128, false><<<grid, kKvThreads, 0, stream>>>(p);
   else if (int4) kv_read_kernel<64, true><<<grid, kKvThreads, 0, stream>>>(p);

@@ -133,8 +133,8 @@ attn_status_t attn_kv_read(const attn_kv_cache_t *cache, void *k_out, void *v_ou
  * The work (16-key blocks of all sequences) is dealt out evenly to a grid that
  * fills the GPU, whatever the lengths; a sequence that ends up on more than
  * one thread block is merged by a second kernel.  Meant for decoding, where
- * S_q is one or a few tokens: each (H_q / H_kv) * S_q <= 32 query rows of a KV
- * head read the cache once, and more rows read it once for every 32.  A whole
+ * S_q is one or a few tokens: each (H_q / H_kv) * S_q <= 64 query rows of a KV
+ * head read the cache once, and more rows read it once for every 64.  A whole
  * prompt is faster through attn_fwd, with attn_kv_read for what it shares
  * with the cache.  The results are deterministic for given lengths.
  *
@@ -149,9 +149,12 @@ attn_status_t attn_fwd_paged(const attn_kv_cache_t *cache, const attn_bhsd_t *q,
                              size_t workspace_bytes, int H_q, int S_q, int causal, float scale,
                              attn_stream_t stream);
 
-/* Workspace bytes attn_fwd_paged needs (0 if the arguments are invalid); it
- * does not depend on the lengths. */
-size_t attn_paged_workspace_bytes(int B, int H_q, int H_kv, int S_q, int D);
+/* Workspace bytes attn_fwd_paged needs (0 if the arguments are invalid);
+ * max_keys = max_blocks * page_size, what the block table spans.  It does not
+ * depend on the lengths, and stops growing at 512 thread blocks' parts (4.2 MB at
+ * up to 8 rows and D = 128).  256 means that none is used (max_keys <= 1024):
+ * attn_fwd_paged then takes a NULL workspace too. */
+size_t attn_paged_workspace_bytes(int B, int H_q, int H_kv, int S_q, int D, int max_keys);
 
 #ifdef __cplusplus
 }

@@ -20,38 +20,35 @@ def lib():
 
 
 def cache(**kw):
-    d = dict(k=A, v=A, block_table=A, format=0, num_pages=10, page_size=64, max_blocks=8, B=2,
-             H_kv=2, D=128)
+    d = dict(k=A, v=A, block_table=A, format=0, num_pages=10, page_size=64, max_blocks=8, B=2, H_kv=2,
+             D=128)
     d.update(kw)
-    return paged._Cache(*[d[n] for n, _ in paged._Cache._fields_])
+    return paged._CACHE.pack(*[d[n] or 0 for n in (
+        "k", "v", "block_table", "format", "num_pages", "page_size", "max_blocks", "B", "H_kv", "D")])
 
 
 def tensor(data=A, sb=8 * 128, sh=128, ss=2 * 128):
-    return paged._Bhsd(data, sb, sh, ss)
-
-
-def ref_(x):
-    return None if x is None else ctypes.byref(x)
+    return paged._BHSD.pack(data or 0, sb, sh, ss)
 
 
 def append(lib, c=None, q=None, q_out=None, k=None, v=None, start=A, new=None, cos=A, sin=A,
            rows=512, rot=128, inter=0, H_q=0, S=4):
     c = cache() if c is None else c
     k, v = k or tensor(), v or tensor()
-    return lib.attn_kv_append(ctypes.byref(c), ref_(q), q_out, ctypes.byref(k), ctypes.byref(v),
+    return lib.attn_kv_append(c, q, q_out, k, v,
                               start, new, cos, sin, rows, rot, inter, H_q, S, None)
 
 
 def read(lib, c=None, k=A, v=A, lens=A, start=None, S=4):
     c = cache() if c is None else c
-    return lib.attn_kv_read(ctypes.byref(c), k, v, lens, start, S, None)
+    return lib.attn_kv_read(c, k, v, lens, start, S, None)
 
 
 def attend(lib, c=None, q=None, o=A, lse=A, lens=A, q_lens=None, ws=A, nbytes=1 << 30, H_q=4,
            S_q=1, causal=1, scale=0.1):
     c = cache() if c is None else c
     q = q or tensor()
-    return lib.attn_fwd_paged(ctypes.byref(c), ctypes.byref(q), o, lse, lens, q_lens, ws, nbytes,
+    return lib.attn_fwd_paged(c, q, o, lse, lens, q_lens, ws, nbytes,
                               H_q, S_q, causal, ctypes.c_float(scale), None)
 
 
@@ -95,14 +92,22 @@ def test_read_refuses(lib, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(o=None), 1), (dict(lse=None), 1), (dict(lens=None), 1), (dict(ws=None), 1),
+    (dict(o=None), 1), (dict(lse=None), 1), (dict(lens=None), 1),
     (dict(causal=2), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(H_q=3), 1), (dict(H_q=0), 1), (dict(S_q=0), 1), (dict(S_q=1 << 30), 2),
     (dict(q=tensor(data=None)), 1), (dict(q=tensor(sh=20)), 3), (dict(o=A + 8), 3),
-    (dict(lse=A + 2), 3), (dict(ws=A + 16), 3), (dict(nbytes=1000), 1), (dict(q_lens=A + 1), 3),
+    (dict(lse=A + 2), 3), (dict(ws=A + 16), 3), (dict(q_lens=A + 1), 3),
 ])
 def test_attention_refuses(lib, kw, code):
     assert attend(lib, **kw) == code
+
+
+def test_attention_checks_the_workspace_of_split_items(lib):
+    need = lib.attn_paged_workspace_bytes(2, 4, 2, 1, 128, 64 * 40)
+    assert attend(lib, cache(max_blocks=40), nbytes=need - 1) == 1
+    assert attend(lib, cache(max_blocks=40), ws=None) == 1
+    assert attend(lib, cache(max_blocks=16), ws=None, nbytes=0, o=A + 8) == 3   # needs none
+    assert attend(lib, cache(max_blocks=40), nbytes=need, o=A + 8) == 3   # stops at another rule
 
 
 def test_strides_of_single_dimensions_are_not_looked_at(lib):
@@ -114,13 +119,18 @@ def test_strides_of_single_dimensions_are_not_looked_at(lib):
 
 
 def test_workspace_bytes(lib):
-    """Two parts of each of at most 1024 thread blocks, D + 1 floats a row of the tile."""
+    """Two parts of each of at most 512 thread blocks, D + 1 floats a row of the tile, and 16
+    bytes a thread block; one block a unit of 128 keys where there are fewer units; next to
+    nothing where the block tables span no more keys than an item is kept whole for."""
     f = lib.attn_paged_workspace_bytes
     for H_q, H_kv, S_q, rows in ((8, 1, 1, 8), (9, 1, 1, 16), (32, 8, 1, 8), (32, 8, 4, 16),
-                                 (32, 8, 5, 32), (32, 8, 500, 32)):
+                                 (32, 8, 5, 32), (32, 8, 9, 64), (32, 8, 500, 64)):
         for D in (64, 128):
-            assert f(3, H_q, H_kv, S_q, D) == 2 * 1024 * rows * (D + 1) * 4
-    for bad in ((0, 8, 1, 1, 64), (1, 8, 3, 1, 64), (1, 8, 1, 0, 64), (1, 8, 1, 1, 96)):
+            assert f(300, H_q, H_kv, S_q, D, 4096) == 512 * (2 * rows * (D + 1) * 4 + 16)
+            assert f(300, H_q, H_kv, S_q, D, 1024) == 256
+    assert f(2, 8, 2, 1, 64, 1025) == 2 * 2 * 9 * (2 * 8 * 65 * 4 + 16)
+    for bad in ((0, 8, 1, 1, 64, 9), (1, 8, 3, 1, 64, 9), (1, 8, 1, 0, 64, 9), (1, 8, 1, 1, 96, 9),
+                (1, 8, 1, 1, 64, 0)):
         assert f(*bad) == 0
 
 
