@@ -199,6 +199,7 @@ struct PagedParams {
 // Keys per unit of the paged attention's work, and up to how many keys (of the
 // block tables' span) an item is kept whole; and its CTAs, at most.
 constexpr int kPagedUnit = 128;
+constexpr int kPagedItemCost = 2;  // units that an item's beginning and end count for
 constexpr int kPagedWholeKeys = 1024;
 constexpr int kPagedMaxCtas = 512;
 

@@ -80,8 +80,10 @@ attn_status_t check_rows(int B, int H_q, int H_kv, int S_q) {
   if (B <= 0 || H_q <= 0 || H_kv <= 0 || S_q <= 0 || H_q % H_kv != 0) return ATTN_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)(H_q / H_kv) * S_q;
   if (rows >= (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
-  // heads times row tiles are counted in an int
-  if (((rows + 63) / 64) * H_kv >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+  // items, with what each counts for apart from its keys, are counted in an int
+  const int tile = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  if (((rows + tile - 1) / tile) * H_kv * B * (kPagedItemCost + 1) >= (1ll << 31))
+    return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 

@@ -32,10 +32,9 @@
 // block of K and of V, each requested by its own lane.
 //
 // Work is dealt out in units of kUnit keys of one (sequence, KV head, tile of
-// query rows): CTA c of G takes units [U c / G, U (c + 1) / G) of all U.
-// An item (the units of one sequence, head and row tile) that lies within one
-// CTA's range is finished there; otherwise each CTA writes its part to the
-// workspace and paged_merge_kernel merges them.
+// query rows) evenly to the CTAs (see Deal).  An item (the units of one sequence, head
+// and row tile) that lies within one CTA's range is finished there; otherwise
+// each CTA writes its part to the workspace and paged_merge_kernel merges them.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -54,7 +53,9 @@ namespace {
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = kPgWarps * 32;
 constexpr int kMergeThreads = 512;
+constexpr int kMergeRows = 4;              // rows of a block of the merge kernel
 constexpr int kUnit = kPagedUnit;
+constexpr int kItemCost = kPagedItemCost;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kPgBar = 1;             // named barrier of the consumer warps
 // The reference of a row's exponentials starts below every finite score, and
@@ -72,21 +73,9 @@ constexpr float kTargetLog2 = 6.f;
 constexpr float kMinScale = 5.42101086e-20f;  // 2^-64
 constexpr float kMaxSum = 1.0e30f;
 
-// sequences' units: thread i sums those of sequences [i per, (i + 1) per)
-struct Plan {
-  long long prefix[kPgThreads + 1];
-};
-
 __device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
   const int L = p.lens[b];
   return L < 0 ? 0 : L > p.cache.capacity ? p.cache.capacity : L;
-}
-
-// Units of sequence b per (head, row tile): at least one, so that a sequence
-// without keys has its rows written too.
-__device__ __forceinline__ int units_of(const PagedParams& p, int b) {
-  const int len = clamp_len(p, b);
-  return len <= p.unit ? 1 : (len + p.unit - 1) / p.unit;
 }
 
 // Queries of sequence b.
@@ -95,63 +84,87 @@ __device__ __forceinline__ int query_count(const PagedParams& p, int b) {
   return n < 0 ? 0 : n > p.S_q ? p.S_q : n;
 }
 
-// Fills the plan; returns the total of the sequences' units.  All threads of
-// the block call it, the first kPgThreads fill it.
-__device__ __forceinline__ long long make_plan(const PagedParams& p, Plan& plan) {
-  __shared__ long long warp_sum[kPgWarps];
-  const int per = (p.cache.B + kPgThreads - 1) / kPgThreads;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long incl = 0;
-  if (warp < kPgWarps) {
-    const int b0 = threadIdx.x * per;
-    for (int i = 0; i < per; ++i)
-      if (b0 + i < p.cache.B) incl += units_of(p, b0 + i);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(kFull, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-  }
-  __syncthreads();
-  if (warp < kPgWarps) {
-    for (int w = 0; w < warp; ++w) incl += warp_sum[w];
-    plan.prefix[threadIdx.x + 1] = incl;
-  }
-  if (threadIdx.x == 0) plan.prefix[0] = 0;
-  __syncthreads();
-  return plan.prefix[kPgThreads];
+// Units of keys of an item of a sequence of that length: at least one, so
+// that a sequence without keys has its rows written too.
+__device__ __forceinline__ int units_of(const PagedParams& p, int len) {
+  return len <= p.unit ? 1 : (len + p.unit - 1) / p.unit;
 }
 
-// The sequence whose units hold unit v (of the sequences' units, one head and
-// row tile), and the number of units before that sequence.
-__device__ __forceinline__ int find_sequence(const PagedParams& p, const Plan& plan, long long v,
-                                             long long& before) {
-  int lo = 0, hi = kPgThreads;   // prefix[lo] <= v < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (plan.prefix[mid] <= v) lo = mid; else hi = mid;
+// An item weighs its units and kItemCost more, about what the beginning and
+// the end of an item take: the positions 0 .. U - 1 of all items' weights, sequence by
+// sequence and within it item by item, are dealt out to G CTAs in even
+// consecutive ranges.  The first kItemCost positions of an item do nothing: its
+// unit k is position kItemCost + k.
+struct Deal {
+  int U, G, q, r;   // CTA c has q positions, or q + 1 where c < r
+  __device__ __forceinline__ Deal(int U_, int launched) : U(U_) {
+    G = U < launched ? U : launched;
+    q = U / G;
+    r = U - q * G;
   }
+  __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int owner(int u) const {   // the CTA that has position u
+    const int big = r * (q + 1);
+    return u < big ? u / (q + 1) : r + (u - big) / q;
+  }
+};
+
+// The sequences' weights (of one item each), summed: thread i of the first kPgThreads
+// has those of sequences [i per, (i + 1) per).
+struct Plan {
+  int before[kPgThreads];     // of the sequences before thread i's, within its warp
+  int warp_sum[kPgWarps];
+};
+
+// All threads of the block call it.  Returns the sum over all sequences.
+__device__ __forceinline__ int make_plan(const PagedParams& p, Plan& plan) {
   const int per = (p.cache.B + kPgThreads - 1) / kPgThreads;
-  int b = lo * per;
-  before = plan.prefix[lo];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp < kPgWarps) {
+    const int b0 = threadIdx.x * per;
+    int sum = 0;
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < p.cache.B) sum += kItemCost + units_of(p, clamp_len(p, b0 + i));
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += o;
+    }
+    plan.before[threadIdx.x] = incl - sum;
+    if (lane == 31) plan.warp_sum[warp] = incl;
+  }
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kPgWarps; ++w) total += plan.warp_sum[w];
+  return total;
+}
+
+// The sequence whose weight covers position v of the sequences' weights, and
+// the weight before it.  Whole warps.
+__device__ __forceinline__ int find_sequence(const PagedParams& p, const Plan& plan, int v,
+                                             int& before) {
+  int w = 0, base = 0;
+#pragma unroll
+  for (int i = 0; i < kPgWarps - 1; ++i) {
+    const int next = base + plan.warp_sum[w];
+    if (w == i && v >= next) base = next, ++w;
+  }
+  // the last thread of that warp whose sequences begin at or before v (threads
+  // without sequences begin at the end)
+  const int mine = base + plan.before[w * 32 + (threadIdx.x & 31)];
+  const uint32_t at = __ballot_sync(kFull, mine <= v);
+  const int lane = 31 - __clz(at);
+  before = __shfl_sync(kFull, mine, lane);
+  const int per = (p.cache.B + kPgThreads - 1) / kPgThreads;
+  int b = (w * 32 + lane) * per;
   while (true) {
-    const int n = units_of(p, b);
+    const int n = kItemCost + units_of(p, clamp_len(p, b));
     if (before + n > v) return b;
     before += n;
     ++b;
   }
-}
-
-// CTAs that take part: no more than there are units, so that none has an
-// empty range (the merge reads a part of every CTA between the first and last).
-__device__ __forceinline__ int active_ctas(long long U, int ctas) {
-  return U < ctas ? (int)U : ctas;
-}
-
-// The CTA whose range [U c / G, U (c + 1) / G) holds unit u.
-__device__ __forceinline__ int cta_of(long long u, long long U, int G) {
-  return (int)(((u + 1) * G - 1) / U);
 }
 
 // Programmatic launch: the dependent kernel's blocks may be made ready before
@@ -591,40 +604,48 @@ struct Shape {
 // A thread block's share of the work, segment by segment (consecutive units
 // of one item).  Producer and consumers walk it alike.
 struct Segments {
-  long long u, u1;
-  int b, len, units, hr, unit;   // of the current segment's item; its first unit
-  int n;                         // its units
-  bool first = true, bad;
+  int x, x1;            // positions left
+  int b, len, units, hr;
+  int unit, n;          // of the current segment: its first unit and their number
+  bool bad;
 
-  __device__ __forceinline__ void begin(const PagedParams& p, const Plan& plan, long long U, int G,
+  // The first segment; false if there is none.  Whole warps.
+  __device__ __forceinline__ bool begin(const PagedParams& p, const Plan& plan, const Deal& deal,
                                         int HR) {
-    u = U * blockIdx.x / G;
-    u1 = U * (blockIdx.x + 1) / G;
-    long long before;
-    b = find_sequence(p, plan, u / HR, before);
+    x = deal.start(blockIdx.x);
+    x1 = deal.start(blockIdx.x + 1);
+    int before;
+    b = find_sequence(p, plan, x / HR, before);
     take_sequence(p);
-    hr = (int)((u - before * HR) / units);
-    unit = (int)((u - before * HR) % units);
-    n = (int)min((long long)(units - unit), u1 - u);
+    const int local = x - before * HR, weight = units + kItemCost;
+    hr = local / weight;
+    x = before * HR + hr * weight;   // of the item
+    unit = max(0, local - hr * weight - kItemCost);
+    return fit(p, HR);
   }
   __device__ __forceinline__ void take_sequence(const PagedParams& p) {
     len = clamp_len(p, b);
-    units = units_of(p, b);
+    units = units_of(p, len);
     bad = p.lens[b] != len || (p.q_lens && (unsigned)p.q_lens[b] > (unsigned)p.S_q);
   }
+  // How much of the item from `unit` on is this CTA's
+  __device__ __forceinline__ bool fit(const PagedParams& p, int HR) {
+    n = min(units, x1 - x - kItemCost) - unit;
+    return n > 0;
+  }
   __device__ __forceinline__ bool next(const PagedParams& p, int HR) {
-    u += n;
-    if (u >= u1) return false;
-    first = false;
+    x += units + kItemCost;
+    if (x >= x1) return false;
     unit = 0;
     if (++hr == HR) {
       hr = 0;
       ++b;
       take_sequence(p);
     }
-    n = (int)min((long long)units, u1 - u);
-    return true;
+    return fit(p, HR);
   }
+  // The position of the item's first unit
+  __device__ __forceinline__ int first_position() const { return x + kItemCost; }
 };
 
 // Keys that some query row of a tile may see: all of the sequence's, but in
@@ -740,11 +761,10 @@ __global__ void __launch_bounds__(kPgThreads + 32, Shape<D, kInt4, WR, RS>::kCta
     if (p.split) p.shared[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   fence_mbar_init();
-  const long long U = make_plan(p, plan) * HR;   // (synchronises the thread block)
-  const int G = active_ctas(U, gridDim.x);
-  if (blockIdx.x >= G) return;
+  const Deal deal(make_plan(p, plan) * HR, gridDim.x);   // (synchronises the thread block)
+  if (blockIdx.x >= deal.G) return;
   Segments seg;
-  seg.begin(p, plan, U, G, HR);
+  if (!seg.begin(p, plan, deal, HR)) return;
 
   if (warp == kPgWarps) {
     const uint32_t requested =
@@ -845,9 +865,12 @@ __global__ void __launch_bounds__(kPgThreads + 32, Shape<D, kInt4, WR, RS>::kCta
       named_barrier_sync(kPgBar, kPgThreads);
     }
     const bool whole = seg.n == seg.units;
-    const int slot = 2 * blockIdx.x + (seg.first ? 0 : 1);
-    if (seg.unit == 0 && !whole && threadIdx.x == 0)   // the item goes on in the next CTAs
-      p.shared[blockIdx.x] = make_int4(b, seg.hr, slot, cta_of(seg.u + seg.units - 1, U, G));
+    // a CTA has at most one item that it goes on with and one that goes on
+    // after it
+    const int slot = 2 * blockIdx.x + (seg.unit == 0 ? 1 : 0);
+    if (seg.unit == 0 && !whole && threadIdx.x == 0)
+      p.shared[blockIdx.x] =
+          make_int4(b, seg.hr, slot, deal.owner(seg.first_position() + seg.units - 1));
     const int n_q = query_count(p, b);
     for (int x = threadIdx.x; x < ROWS * (D / 4); x += kPgThreads) {
       const int row = x / (D / 4), d = 4 * (x % (D / 4));
@@ -885,15 +908,14 @@ __global__ void __launch_bounds__(kPgThreads + 32, Shape<D, kInt4, WR, RS>::kCta
 }
 
 // Merges the parts of items that several CTAs share: O = sum_c w_c O_c with
-// w_c = 2^(lse_c - lse), lse = log2 sum_c 2^lse_c.  Thread block c merges the
-// item that CTA c began and did not finish, if there is one (p.shared[c]):
-// 16 rows at a time, its warps dealt out to the rows, and where a row has
-// several warps they take turns at its parts.
+// w_c = 2^(lse_c - lse), lse = log2 sum_c 2^lse_c.  Thread blocks (c, y)
+// merge the item that CTA c began and did not finish, if there is one
+// (p.shared[c]), kMergeRows rows each; a row's warps take turns at its parts.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads)
     paged_merge_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kWarps = kMergeThreads / 32;
-  constexpr int kRows = ROWS < kWarps ? ROWS : kWarps;   // rows at a time
+  constexpr int kRows = kMergeRows;                      // of a block
   constexpr int kPer = kWarps / kRows;                   // warps a row
   constexpr int E = D / 32;                              // elements a lane
   __shared__ float sm_acc[kWarps][D], sm_sum[kWarps];
@@ -904,8 +926,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int h = hr / p.row_tiles, rt = hr % p.row_tiles;
   const int n_q = p.q_lens ? p.q_lens[b] : p.S_q;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r0 = 0; r0 < ROWS; r0 += kRows) {
-    const int row = r0 + warp / kPer, share = warp % kPer;
+  {
+    const int row = blockIdx.y * kRows + warp / kPer, share = warp % kPer;
     const int rho = rt * ROWS + row;
     const bool live = rho < p.group * p.S_q && rho % p.S_q < n_q;
     const auto at = [&](int c) {   // part c's place in the workspace
@@ -959,7 +981,6 @@ __global__ void __launch_bounds__(kMergeThreads)
       if (lane == 0)
         p.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
     }
-    if constexpr (kPer > 1) __syncthreads();
   }
 }
 
@@ -995,6 +1016,8 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
   p.split = split;
   p.unit = split ? kUnit : (p.cache.capacity + kUnit - 1) / kUnit * kUnit;
   const long long items = (long long)p.cache.B * p.cache.H_kv * p.row_tiles;
+  // positions are counted in an int: larger units where there could be too many
+  while (items * ((p.cache.capacity + p.unit - 1) / p.unit + kItemCost) >= (1ll << 31)) p.unit *= 2;
   const long long most = items * ((p.cache.capacity + p.unit - 1) / p.unit);
   if (ctas > most) ctas = most;
   kernel<<<(unsigned)ctas, kPgThreads + 32, S::kBytes, stream>>>(p);
@@ -1003,7 +1026,7 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = dim3((unsigned)ctas, S::kRows / kMergeRows);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
