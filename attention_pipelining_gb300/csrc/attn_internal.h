@@ -160,7 +160,7 @@ struct KvAppendParams {
   const float* sin;
   int rope_rows, rot_dim, interleaved;
   int H_q, S;
-  int tokens;            // tokens of a thread block (set at launch)
+  int rows;              // of a token's H_q + 2 H_kv, a thread block's (set at launch)
 };
 
 struct KvReadParams {

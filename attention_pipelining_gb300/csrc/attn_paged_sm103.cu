@@ -61,11 +61,11 @@ constexpr uint32_t kPgBar = 1;             // named barrier of the consumer warp
 // The reference of a row's exponentials starts below every finite score, and
 // far enough above minus infinity that a masked score (-inf) minus it is -inf.
 constexpr float kNoMax = -3.0e38f;
-// The reference follows the running maximum lazily: it moves only when a
-// probability times the largest value scale would pass 2^15 (fp16 holds up
-// to 65504), and is then set so that the largest one is 2^6 at most: 2^9 of
-// growth before the next move, and values down to 2^-14 (2^-20 of the largest)
-// keep all their bits.
+// The reference follows the running maximum lazily: it moves only when a sum
+// of a lane's probabilities times the largest value scale would pass 2^15 (fp16
+// holds up to 65504), and is then set so that the largest one is 2^6 at most: 2^7
+// or more of growth before the next move, and values down to 2^-14 (2^-20 of the
+// largest) keep all their bits.
 constexpr float kMaxProb = 32768.f;
 constexpr float kTargetLog2 = 6.f;
 // value scales are taken as at least this when the reference is set, so that
@@ -411,7 +411,7 @@ struct Warp {
         }
       }
     }
-    // base-2 exponents where some keys are masked; element c of s belongs to key
+    // base-2 exponents where some are masked; element c of s belongs to key
     // 16 i + g + 8 (c / 2) and row 8 n + 2t + c % 2
     const auto seen = [&](int i, int n, int c) {
       return key0 + 16 * i + 8 * (c >> 1) + g < lim[n][c & 1] && ((have >> (2 * i)) & 1u);
@@ -428,9 +428,25 @@ struct Warp {
     const auto exponent = [&](int i, int n, int c) {
       return kMasked ? s[i][n][c] : s[i][n][c] * fac[n][c & 1];
     };
-    const auto probability = [&](int i, int n, int c) {
-      return ex2_approx(kMasked ? s[i][n][c] - m[n][c & 1]
-                                : fmaf(s[i][n][c], fac[n][c & 1], -m[n][c & 1]));
+    // the probabilities of rows 8 n + 2t, 8 n + 2t + 1, and their sums, in pairs
+    float pr[NB][NT][4], sum[NT][2];
+    const auto probabilities = [&](int n) {
+      const uint64_t f2 = kMasked ? f2_pack(1.f, 1.f) : f2_pack(fac[n][0], fac[n][1]);
+      const uint64_t m2 = f2_pack(-m[n][0], -m[n][1]);
+      uint64_t total = 0;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          const uint64_t x = f2_pack(s[i][n][c], s[i][n][c + 1]);
+          float x0, x1;
+          f2_unpack(kMasked ? f2_add(x, m2) : f2_fma(x, f2, m2), x0, x1);
+          pr[i][n][c] = ex2_approx(x0);
+          pr[i][n][c + 1] = ex2_approx(x1);
+          const uint64_t pair = f2_pack(pr[i][n][c], pr[i][n][c + 1]);
+          total = i + c == 0 ? pair : f2_add(total, pair);
+        }
+      f2_unpack(total, sum[n][0], sum[n][1]);
     };
     // the values' scales of this lane's keys, and the largest
     uint32_t sv[NB][2][kInt4 ? G / 2 : 1];
@@ -452,18 +468,14 @@ struct Warp {
         }
       smax = fmaxf(lo_f(top), hi_f(top));   // (a NaN scale is left out of the maximum)
     }
-    // probabilities against the lazy reference
-    float pr[NB][NT][4], pm = 0.f;
+    // against the lazy reference
+    float most = 0.f;
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          pr[i][n][c] = probability(i, n, c);
-          pm = fmaxf(pm, pr[i][n][c]);
-        }
-    if (__any_sync(kFull, pm * smax > kMaxProb || pm > kMaxSum)) {
+    for (int n = 0; n < NT; ++n) {
+      probabilities(n);
+      most = fmaxf(most, fmaxf(sum[n][0], sum[n][1]));
+    }
+    if (__any_sync(kFull, most * smax > kMaxProb || most > kMaxSum)) {
       float big = fmaxf(smax, kMinScale);
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, d));
@@ -488,18 +500,11 @@ struct Warp {
         for (int d = 0; d < KS; ++d)
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[d][n][c] *= alpha[c & 1];
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) pr[i][n][c] = probability(i, n, c);
+        probabilities(n);
       }
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) l[n][c & 1] += pr[i][n][c];
+    for (int n = 0; n < NT; ++n) l[n][0] += sum[n][0], l[n][1] += sum[n][1];
     // O^T += V^T P^T
 #pragma unroll
     for (int i = 0; i < NB; ++i) {

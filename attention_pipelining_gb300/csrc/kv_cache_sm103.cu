@@ -21,7 +21,22 @@ namespace {
 
 constexpr int kKvThreads = 256;         // of the read kernel
 constexpr int kAppendThreads = 128;
-constexpr int kAppendBlocks = 1216;     // eight blocks on each of 152 SMs
+constexpr int kAhead = 4;               // rows of a thread under way in the append kernel
+constexpr int kAppendBlocks = 2432;     // sixteen blocks on each of 152 SMs
+
+// 16 bytes to shared memory, asynchronously, in the thread's open group.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most the newest N groups of the thread are under way.
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // ---------------------------------------------------------------- rotation
 
@@ -31,7 +46,7 @@ constexpr int kAppendBlocks = 1216;     // eight blocks on each of 152 SMs
 // added back, and the fp32 result, when it falls on a tie of the bf16 rounding
 // that the remainder breaks, is moved one step to the remainder's side.  Non-finite
 // values take the plain formula's result.
-__device__ __noinline__ float rotate_bf16(float x, float a, float y, float b) {
+__device__ __forceinline__ float rotate_bf16(float x, float a, float y, float b) {
   const float h = __fmul_rn(x, a), h2 = __fmul_rn(-y, b);
   const float e = __fmaf_rn(x, a, -h), e2 = __fmaf_rn(-y, b, -h2);
   const float s = __fadd_rn(h, h2);
@@ -46,11 +61,22 @@ __device__ __noinline__ float rotate_bf16(float x, float a, float y, float b) {
   return __uint_as_float(u);
 }
 
+// Eight elements x c + y s, for v = {x, y, c, s}.
+__device__ __noinline__ void rotate8_exactly(const float (&v)[4][8], uint32_t (&out)[4]) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i)
+    out[i] = pack_bf16x2(rotate_bf16(v[0][2 * i], v[2][2 * i], -v[1][2 * i], v[3][2 * i]),
+                         rotate_bf16(v[0][2 * i + 1], v[2][2 * i + 1], -v[1][2 * i + 1],
+                                     v[3][2 * i + 1]));
+}
+
 // The same for eight elements in pairs, r = x c + y s (y negated by the caller
 // where the formula subtracts): first with four operations an element,
 // fma(x, c, h) + e with h + e = y s exactly, which is off by at most two units of
-// fp32's last place; only where that leaves the bf16 rounding open (four units
-// around a tie: one element in 2^13) or a value is not finite, by rotate_bf16.
+// fp32's last place (half a unit in each of the two sums, of which the first may
+// be twice as large as the second's; the sum of products that cancel is exact);
+// only where that leaves the bf16 rounding open (two units around a tie: one
+// element in 13000) or a value is not finite, by rotate_bf16.
 // Rounding the plain fp32 formula instead would round about one element in 2^15
 // the other way than the exact value, and in a 4-bit cache change its code.
 __device__ __forceinline__ void rotate8(const uint64_t (&x)[4], const uint64_t (&y)[4],
@@ -68,21 +94,24 @@ __device__ __forceinline__ void rotate8(const uint64_t (&x)[4], const uint64_t (
     float r0, r1;
     f2_unpack(r, r0, r1);
     nearest = __viaddmin_u16x2(
-        __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x5410u), 0x80048004u, nearest);
+        __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x5410u), 0x80028002u, nearest);
     out[i] = pack_bf16x2(r0, r1);
   }
   float f0, f1;
   f2_unpack(finite, f0, f1);
-  if ((nearest & 0xffffu) <= 8u || (nearest >> 16) <= 8u || f0 + f1 != 0.f) {
+  if ((nearest & 0xffffu) <= 4u || (nearest >> 16) <= 4u || f0 + f1 != 0.f) {
+    float v[4][8];   // copies: the arrays themselves stay in registers
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x0, x1, y0, y1, c0, c1, s0, s1;
-      f2_unpack(x[i], x0, x1);
-      f2_unpack(y[i], y0, y1);
-      f2_unpack(c[i], c0, c1);
-      f2_unpack(s[i], s0, s1);
-      out[i] = pack_bf16x2(rotate_bf16(x0, c0, -y0, s0), rotate_bf16(x1, c1, -y1, s1));
+      f2_unpack(x[i], v[0][2 * i], v[0][2 * i + 1]);
+      f2_unpack(y[i], v[1][2 * i], v[1][2 * i + 1]);
+      f2_unpack(c[i], v[2][2 * i], v[2][2 * i + 1]);
+      f2_unpack(s[i], v[3][2 * i], v[3][2 * i + 1]);
     }
+    rotate8_exactly(v, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = w[i];
   }
 }
 
@@ -93,16 +122,15 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // every lane of the row takes part.  With pairs (d, d + rot / 2) the partner
 // chunk is another lane's, and cs, sn belong to the elements; with adjacent pairs
 // it is the lane's own, and they belong to its four pairs.
-template <int kLanes>
+template <int kLanes, bool kInterleaved>
 __device__ __forceinline__ void rotate_chunk(uint4& w, uint32_t row_mask, int c, int rot_chunks,
-                                             bool interleaved,
                                              const uint64_t (&cs)[4], const uint64_t (&sn)[4]) {
   const uint32_t own[4] = {w.x, w.y, w.z, w.w};
   uint64_t x[4], y[4];
   uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = f2_pack(bf16_lo(own[i]), bf16_hi(own[i]));
-  if (interleaved) {   // (a cos - b sin, b cos + a sin)
+  if constexpr (kInterleaved) {   // (a cos - b sin, b cos + a sin)
     uint64_t ci[4], si[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -206,42 +234,66 @@ __device__ __forceinline__ void store4(uint8_t* block, int r, int c, bool value,
 
 // A token's vector of one head is a row that D / 8 neighbouring lanes hold, 8
 // elements each: one word of codes, a quarter of a scale's group.  A thread
-// block has kSlots places for rows and takes one token, whose H_q queries, then
-// H_kv keys and H_kv values its places take in turn (with gridDim.y blocks to a
-// token, all their places), so that a lane reads its part of the token's rotation,
-// 8 cosines and sines, once; or, where a token has few rows, p.tokens tokens.  Rows
-// side by side in a warp may be of different kinds: they diverge, and only a row's
-// own lanes exchange values.
-template <int D, bool kInt4>
-__global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const KvAppendParams p) {
+// block takes kSlots consecutive tokens, one to a row of lanes, and goes with all
+// of them through p.rows of their H_q queries, H_kv keys and H_kv values: what
+// belongs to the token (its page, its rotation's 8 cosines and sines a lane) is
+// read once, and neighbouring tokens, which lie side by side in q_out and in the
+// cache, are written together.  The next rows are on their way while one is
+// worked on: bytes under way are what the kernel needs most (8192 tokens of 32 +
+// 8 heads of 128 into 4 bits, 177 MB: 54 us with one token to a block or two rows
+// ahead in registers, 44 us, 4.0 TB/s, with four ahead in shared memory).
+template <int D, bool kInt4, bool kInterleaved>
+__global__ void __launch_bounds__(kAppendThreads, 8)
+    kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kSlots = kAppendThreads / kLanes;
   const KvCache& kc = p.cache;
-  const int rows = p.H_q + 2 * kc.H_kv;
-  const int c = threadIdx.x % kLanes, place = threadIdx.x / kLanes;
+  const int c = threadIdx.x % kLanes;
   const uint32_t row_mask = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
-  const int sub = p.tokens > 1 ? place / rows : 0;   // which of the block's tokens
-  const int first = p.tokens > 1 ? place % rows : blockIdx.y * kSlots + place;
-  const int step = p.tokens > 1 ? rows : kSlots * gridDim.y;
-  const uint32_t token = blockIdx.x * p.tokens + sub;
-  if (sub >= p.tokens || token >= (uint32_t)(kc.B * p.S)) return;
+  const uint32_t token = blockIdx.x * kSlots + threadIdx.x / kLanes;
+  if (token >= (uint32_t)(kc.B * p.S)) return;
   const int b = (int)(token / (uint32_t)p.S), i = (int)(token % (uint32_t)p.S);
   if (p.new_lens && i >= p.new_lens[b]) return;
-  const auto row_of = [&](const KvTensor& t, int h) {
-    return t.data + b * t.sb + h * t.sh + i * t.ss + 8 * c;
+  // this block's rows: heads [q0, q1) of the queries, [k0, k1) of the keys and
+  // [v0, v1) of the values
+  const int r0 = blockIdx.y * p.rows, r1 = r0 + p.rows;
+  const int q0 = min(r0, p.H_q), q1 = min(r1, p.H_q);
+  const int k0 = min(max(r0 - p.H_q, 0), kc.H_kv), k1 = min(max(r1 - p.H_q, 0), kc.H_kv);
+  const int v0 = min(max(r0 - p.H_q - kc.H_kv, 0), kc.H_kv);
+  const int v1 = min(max(r1 - p.H_q - kc.H_kv, 0), kc.H_kv);
+  const auto source = [&](const KvTensor& t, int h) {
+    return t.data + b * t.sb + i * t.ss + h * t.sh + 8 * c;
   };
-  const auto load = [](const uint16_t* src) { return *reinterpret_cast<const uint4*>(src); };
-  // the first loads need neither the position nor the page
-  int row = first;
-  const uint16_t* q_src = row_of(p.q, row);
-  uint4 q_next = row < p.H_q ? load(q_src) : make_uint4(0, 0, 0, 0);
-  const auto kv_source = [&](int r) {
-    const bool v = r >= p.H_q + kc.H_kv;
-    return row_of(v ? p.v : p.k, v ? r - p.H_q - kc.H_kv : r - p.H_q);
+  // The rows in turn come by way of shared memory, kAhead of them requested in
+  // advance; a lane takes what it requested itself.
+  __shared__ uint4 ring[kAhead][kAppendThreads];
+  int left = (q1 - q0) + (k1 - k0) + (v1 - v0), at = q1 - q0, kind = 0, put_in = 0, take_from = 0;
+  const uint16_t* src = source(p.q, q0);
+  long long step = p.q.sh;
+  const auto request = [&]() {
+    if (left > 0) {
+      while (at == 0) {   // on to the keys, then to the values
+        src = ++kind == 1 ? source(p.k, k0) : source(p.v, v0);
+        step = kind == 1 ? p.k.sh : p.v.sh;
+        at = kind == 1 ? k1 - k0 : v1 - v0;
+      }
+      copy_async16(&ring[put_in][threadIdx.x], src);
+      src += step;
+      --at;
+      --left;
+      put_in = put_in + 1 == kAhead ? 0 : put_in + 1;
+    }
+    copy_async_commit();
   };
-  int kv_row = row;   // this place's first key or value
-  if (kv_row < p.H_q) kv_row += (p.H_q - kv_row + step - 1) / step * step;
-  uint4 kv_next = kv_row < rows ? load(kv_source(kv_row)) : make_uint4(0, 0, 0, 0);
+  const auto take = [&]() {   // the oldest row, and a request for another
+    copy_async_wait<kAhead - 1>();
+    const uint4 w = ring[take_from][threadIdx.x];
+    take_from = take_from + 1 == kAhead ? 0 : take_from + 1;
+    request();
+    return w;
+  };
+#pragma unroll 1
+  for (int n = 0; n < kAhead; ++n) request();   // (needs neither position nor page)
   const long long pos = (long long)p.start[b] + i;
   const int rot_chunks = p.rot_dim / 8;
   const bool good = pos >= 0 && pos < kc.capacity && (p.rot_dim == 0 || pos < p.rope_rows);
@@ -250,10 +302,10 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const KvAp
   uint64_t cs[4] = {}, sn[4] = {};   // pairs of cosines and of sines
   if (good && c < rot_chunks) {
     const long long at = pos * (p.rot_dim / 2) +
-                         (p.interleaved ? 4 * c : 8 * (c < rot_chunks / 2 ? c : c - rot_chunks / 2));
+                         (kInterleaved ? 4 * c : 8 * (c < rot_chunks / 2 ? c : c - rot_chunks / 2));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (h == 1 && p.interleaved) break;
+      if (h == 1 && kInterleaved) break;
       const float4 a = *reinterpret_cast<const float4*>(p.cos + at + 4 * h);
       const float4 d = *reinterpret_cast<const float4*>(p.sin + at + 4 * h);
       cs[2 * h] = f2_pack(a.x, a.y), cs[2 * h + 1] = f2_pack(a.z, a.w);
@@ -264,32 +316,39 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const KvAp
     g_kv_status = ATTN_ERR_BAD_INDEX;
     return;
   }
-  uint16_t* q_dst = p.q_out + (((long long)b * p.H_q + row) * p.S + i) * D + 8 * c;
-  for (; row < p.H_q; row += step) {
-    uint4 w = q_next;
-    q_src += step * p.q.sh;
-    if (row + step < p.H_q) q_next = load(q_src);
-    if (rot_chunks) rotate_chunk<kLanes>(w, row_mask, c, rot_chunks, p.interleaved, cs, sn);
-    *reinterpret_cast<uint4*>(q_dst) = w;
-    q_dst += (long long)step * p.S * D;
-  }
   const int slot = (int)pos % kc.page_size;
-  for (row = kv_row; row < rows; row += step) {
-    const bool v = row >= p.H_q + kc.H_kv;
-    const int h = v ? row - p.H_q - kc.H_kv : row - p.H_q;
-    uint4 w = kv_next;
-    if (row + step < rows) kv_next = load(kv_source(row + step));
-    if (rot_chunks && !v)
-      rotate_chunk<kLanes>(w, row_mask, c, rot_chunks, p.interleaved, cs, sn);
-    uint8_t* block = const_cast<uint8_t*>(v ? kc.v : kc.k) +
-                     kv_block_offset<D, kInt4>(kc, page, h, slot >> 4);
-    if (kInt4) {
+  uint16_t* q_dst = p.q_out + (((long long)b * p.H_q + q0) * p.S + i) * D + 8 * c;
+  const long long q_dst_step = (long long)p.S * D;
+#pragma unroll 1
+  for (int h = q0; h < q1; ++h) {
+    uint4 w = take();
+    if (rot_chunks) rotate_chunk<kLanes, kInterleaved>(w, row_mask, c, rot_chunks, cs, sn);
+    *reinterpret_cast<uint4*>(q_dst) = w;
+    q_dst += q_dst_step;
+  }
+  const long long head_bytes = (long long)kc.blocks_per_page * kKvBlockBytes<D, kInt4>;
+  const auto put = [&](uint8_t* block, const uint4& w, bool value) {
+    if constexpr (kInt4) {
       uint32_t scale;
       const uint32_t codes = quantise8(w, row_mask, scale);
-      store4<D>(block, slot & 15, c, v, codes, scale);
+      store4<D>(block, slot & 15, c, value, codes, scale);
     } else {
       *reinterpret_cast<uint4*>(block + (slot & 15) * D * 2 + 16 * c) = w;
     }
+  };
+  uint8_t* dst = const_cast<uint8_t*>(kc.k) + kv_block_offset<D, kInt4>(kc, page, k0, slot >> 4);
+#pragma unroll 1
+  for (int h = k0; h < k1; ++h) {
+    uint4 w = take();
+    if (rot_chunks) rotate_chunk<kLanes, kInterleaved>(w, row_mask, c, rot_chunks, cs, sn);
+    put(dst, w, false);
+    dst += head_bytes;
+  }
+  dst = const_cast<uint8_t*>(kc.v) + kv_block_offset<D, kInt4>(kc, page, v0, slot >> 4);
+#pragma unroll 1
+  for (int h = v0; h < v1; ++h) {
+    put(dst, take(), true);
+    dst += head_bytes;
   }
 }
 
@@ -392,18 +451,21 @@ cudaError_t launch_kv_append(const KvAppendParams& p0, int D, bool int4, cudaStr
   KvAppendParams p = p0;
   const int slots = kAppendThreads / (D / 8);
   const int rows = p.H_q + 2 * p.cache.H_kv;
-  const long long tokens = (long long)p.cache.B * p.S;
-  // Tokens of few rows share a block; a token of many rows is one block's, or,
-  // when there are few tokens, is spread over several.
-  p.tokens = rows < slots ? slots / rows : 1;
-  const long long blocks = (tokens + p.tokens - 1) / p.tokens;
-  const int most = (rows + slots - 1) / slots;
-  const long long spread = kAppendBlocks / blocks;
-  const dim3 grid((unsigned)blocks, (unsigned)(spread < 1 ? 1 : spread < most ? spread : most));
-  if (D == 128 && int4) kv_append_kernel<128, true><<<grid, kAppendThreads, 0, stream>>>(p);
-  else if (D == 128) kv_append_kernel<128, false><<<grid, kAppendThreads, 0, stream>>>(p);
-  else if (int4) kv_append_kernel<64, true><<<grid, kAppendThreads, 0, stream>>>(p);
-  else kv_append_kernel<64, false><<<grid, kAppendThreads, 0, stream>>>(p);
+  const long long blocks = ((long long)p.cache.B * p.S + slots - 1) / slots;
+  // where there are few tokens, their rows are spread over several blocks
+  const long long spread = (kAppendBlocks + blocks - 1) / blocks;
+  p.rows = spread >= rows ? 1 : (int)((rows + spread - 1) / spread);
+  const dim3 grid((unsigned)blocks, (unsigned)((rows + p.rows - 1) / p.rows));
+  const auto kernel =
+      D == 128 ? int4 ? p.interleaved ? kv_append_kernel<128, true, true>
+                                      : kv_append_kernel<128, true, false>
+                      : p.interleaved ? kv_append_kernel<128, false, true>
+                                      : kv_append_kernel<128, false, false>
+               : int4 ? p.interleaved ? kv_append_kernel<64, true, true>
+                                      : kv_append_kernel<64, true, false>
+                      : p.interleaved ? kv_append_kernel<64, false, true>
+                                      : kv_append_kernel<64, false, false>;
+  kernel<<<grid, kAppendThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
