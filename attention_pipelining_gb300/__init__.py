@@ -43,7 +43,8 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_status_string", "attn_device_statu
            "attn_splitkv_noalloc_capacity", "attn_bwd", "attn_bwd_deterministic",
            "attn_bwd_workspace_bytes", "attn_bwd_timeout_test",
            "attn_bwd_host", "chunk_scan_fwd", "chunk_scan_fwd_host",
-           "attn_kv_append", "attn_kv_read", "attn_fwd_paged", "attn_paged_workspace_bytes"]
+           "attn_kv_append", "attn_kv_read", "attn_fwd_paged", "attn_paged_workspace_bytes",
+           "attn_fwd_paged_timeout_test"]
 
 
 class AttnError(RuntimeError):
@@ -126,6 +127,9 @@ def _load():
     lib.attn_kv_read.restype = ci
     lib.attn_fwd_paged.argtypes = [vp] * 7 + [ctypes.c_size_t] + [ci] * 3 + [cf, vp]
     lib.attn_fwd_paged.restype = ci
+    lib.attn_fwd_paged_timeout_test.argtypes = [vp] * 7 + [ctypes.c_size_t] + [ci] * 3 + [
+        cf, ci, ctypes.c_ulonglong, vp]
+    lib.attn_fwd_paged_timeout_test.restype = ci
     lib.attn_paged_workspace_bytes.argtypes = [ci] * 6
     lib.attn_paged_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib

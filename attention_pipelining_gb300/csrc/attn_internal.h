@@ -194,6 +194,9 @@ struct PagedParams {
   float scale_log2;
   uint32_t code_base_low, code_base_high;  // fp16 pairs of 1024 and 64 (see the kernel)
   unsigned long long timeout_ns;  // budget of any single wait inside the kernel
+  // Test of the timeout path: when >= 0, the producer warp of every CTA leaves this
+  // stage unrequested, so the consumers' bounded wait for it runs out.
+  int fault_drop_stage;
 };
 
 // Keys per unit of the paged attention's work, and up to how many keys (of the

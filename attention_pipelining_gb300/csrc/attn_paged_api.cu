@@ -1,11 +1,13 @@
 // attn_paged_api.cu -- the C ABI of include/attn_paged.h: argument checks and
 // launches.  Every check runs before anything is queued; nothing here
 // allocates memory.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 
 #include "attn_internal.h"
+#include "attn_testing.h"
 
 namespace attnpipe {
 namespace {
@@ -85,6 +87,59 @@ attn_status_t check_rows(int B, int H_q, int H_kv, int S_q) {
   if (((rows + tile - 1) / tile) * H_kv * B * (kPagedItemCost + 1) >= (1ll << 31))
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
+}
+
+attn_status_t paged_impl(const attn_kv_cache_t* cache, const attn_bhsd_t* q, void* o, float* lse,
+                         const int* lens, const int* q_lens, void* workspace,
+                         size_t workspace_bytes, int H_q, int S_q, int causal, float scale,
+                         attn_stream_t stream, int drop_stage = -1,
+                         unsigned long long timeout_ns = kDefaultTimeoutNs) {
+  PagedParams p;
+  std::memset(&p, 0, sizeof(p));
+  attn_status_t st = take_cache(cache, &p.cache);
+  if (st != ATTN_OK) return st;
+  if (!o || !lse || !lens) return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if ((st = check_rows(cache->B, H_q, cache->H_kv, S_q)) != ATTN_OK) return st;
+  if ((st = take_tensor(q, cache->B, H_q, S_q, &p.q)) != ATTN_OK) return st;
+  if (!aligned16(o) || !aligned4(lse) || !aligned4(lens) || !aligned4(q_lens) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return ATTN_ERR_MISALIGNED;
+  p.group = H_q / cache->H_kv;
+  const int rows = tile_rows(p.group, S_q);
+  const int64_t parts = part_ctas(cache->B, cache->H_kv, (int64_t)p.group * S_q, rows,
+                                  p.cache.capacity);
+  if (parts > 0 && (!workspace || workspace_bytes < part_bytes(parts, rows, cache->D)))
+    return ATTN_ERR_INVALID_ARG;
+  if ((st = check_device()) != ATTN_OK) return st;
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.lens = lens;
+  p.q_lens = q_lens;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + (size_t)2 * parts * rows * cache->D;
+  p.shared = reinterpret_cast<int4*>(p.part_lse + (size_t)2 * parts * rows);
+  p.H_q = H_q;
+  p.S_q = S_q;
+  p.causal = causal;
+  // (kept finite)
+  const double scale_log2 = (double)scale * 1.4426950408889634;
+  p.scale_log2 = (float)std::fmin(std::fmax(scale_log2, -(double)FLT_MAX), (double)FLT_MAX);
+  p.code_base_low = 0x64006400u;
+  p.code_base_high = 0x54005400u;
+  p.timeout_ns = timeout_ns;
+  p.fault_drop_stage = drop_stage;
+  if (cache->format == ATTN_KV_BF16) {
+    const uint64_t heads = (uint64_t)cache->num_pages * cache->H_kv;
+    if (!encode_bf16_map_3d(&p.tm_k, cache->k, cache->D, cache->page_size, heads, 16) ||
+        !encode_bf16_map_3d(&p.tm_v, cache->v, cache->D, cache->page_size, heads, 16))
+      return ATTN_ERR_CUDA;
+  }
+  return launch_attn_paged(p, cache->D, cache->format == ATTN_KV_INT4, rows,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -168,49 +223,22 @@ attn_status_t attn_fwd_paged(const attn_kv_cache_t* cache, const attn_bhsd_t* q,
                              float* lse, const int* lens, const int* q_lens, void* workspace,
                              size_t workspace_bytes, int H_q, int S_q, int causal, float scale,
                              attn_stream_t stream) {
-  PagedParams p;
-  std::memset(&p, 0, sizeof(p));
-  attn_status_t st = take_cache(cache, &p.cache);
-  if (st != ATTN_OK) return st;
-  if (!o || !lse || !lens) return ATTN_ERR_INVALID_ARG;
-  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
-  if ((st = check_rows(cache->B, H_q, cache->H_kv, S_q)) != ATTN_OK) return st;
-  if ((st = take_tensor(q, cache->B, H_q, S_q, &p.q)) != ATTN_OK) return st;
-  if (!aligned16(o) || !aligned4(lse) || !aligned4(lens) || !aligned4(q_lens) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-    return ATTN_ERR_MISALIGNED;
-  p.group = H_q / cache->H_kv;
-  const int rows = tile_rows(p.group, S_q);
-  const int64_t parts = part_ctas(cache->B, cache->H_kv, (int64_t)p.group * S_q, rows,
-                                  p.cache.capacity);
-  if (parts > 0 && (!workspace || workspace_bytes < part_bytes(parts, rows, cache->D)))
+  return paged_impl(cache, q, o, lse, lens, q_lens, workspace, workspace_bytes, H_q, S_q, causal,
+                    scale, stream);
+}
+
+attn_status_t attn_fwd_paged_timeout_test(const attn_kv_cache_t* cache, const attn_bhsd_t* q,
+                                          void* o, float* lse, const int* lens,
+                                          const int* q_lens, void* workspace,
+                                          size_t workspace_bytes, int H_q, int S_q, int causal,
+                                          float scale, int drop_stage,
+                                          unsigned long long wait_budget_ns,
+                                          attn_stream_t stream) {
+  if (drop_stage < 0) return ATTN_ERR_INVALID_ARG;
+  if (wait_budget_ns < 1000000ull || wait_budget_ns > kDefaultTimeoutNs)
     return ATTN_ERR_INVALID_ARG;
-  if ((st = check_device()) != ATTN_OK) return st;
-  p.o = static_cast<uint16_t*>(o);
-  p.lse = lse;
-  p.lens = lens;
-  p.q_lens = q_lens;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_lse = p.part_o + (size_t)2 * parts * rows * cache->D;
-  p.shared = reinterpret_cast<int4*>(p.part_lse + (size_t)2 * parts * rows);
-  p.H_q = H_q;
-  p.S_q = S_q;
-  p.causal = causal;
-  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-  p.code_base_low = 0x64006400u;
-  p.code_base_high = 0x54005400u;
-  p.timeout_ns = kDefaultTimeoutNs;
-  if (cache->format == ATTN_KV_BF16) {
-    const uint64_t heads = (uint64_t)cache->num_pages * cache->H_kv;
-    if (!encode_bf16_map_3d(&p.tm_k, cache->k, cache->D, cache->page_size, heads, 16) ||
-        !encode_bf16_map_3d(&p.tm_v, cache->v, cache->D, cache->page_size, heads, 16))
-      return ATTN_ERR_CUDA;
-  }
-  return launch_attn_paged(p, cache->D, cache->format == ATTN_KV_INT4, rows,
-                           static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ERR_CUDA;
+  return paged_impl(cache, q, o, lse, lens, q_lens, workspace, workspace_bytes, H_q, S_q, causal,
+                    scale, stream, drop_stage, wait_budget_ns);
 }
 
 }  // extern "C"

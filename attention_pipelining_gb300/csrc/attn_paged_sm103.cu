@@ -52,8 +52,8 @@ namespace {
 
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = kPgWarps * 32;
-constexpr int kMergeThreads = 512;
-constexpr int kMergeRows = 4;              // rows of a block of the merge kernel
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 2;              // rows of a block of the merge kernel
 constexpr int kUnit = kPagedUnit;
 constexpr int kItemCost = kPagedItemCost;
 constexpr uint32_t kFull = 0xffffffffu;
@@ -167,15 +167,6 @@ __device__ __forceinline__ int find_sequence(const PagedParams& p, const Plan& p
   }
 }
 
-// Programmatic launch: the dependent kernel's blocks may be made ready before
-// this one ends; there, everything this kernel wrote is visible after the wait.
-__device__ __forceinline__ void allow_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_prerequisites() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // ---------------------------------------------------------------- fragments
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -284,13 +275,13 @@ struct Warp {
   // The tile's queries; those of a 4-bit cache scaled by a power of two to
   // [1, 2) at their row's largest element, for fp16.
   __device__ __forceinline__ void start(const PagedParams& p, int b, int h, int row0, int len,
-                                        int tile_end) {
+                                        int tile_common, int tile_end) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int R = p.group * p.S_q;
     const int n_q = query_count(p, b);
     code_base.low = p.code_base_low;
     code_base.high = p.code_base_high;
-    min_lim = p.causal ? max(0, len - n_q + 1) : len;
+    min_lim = tile_common;
     max_lim = tile_end;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -544,11 +535,12 @@ struct Warp {
           b0[n] = transpose8(pack_bf16x2(pr[i][n][0], pr[i][n][1]));
           b1[n] = transpose8(pack_bf16x2(pr[i][n][2], pr[i][n][3]));
         }
-        // values of keys that no row sees may be anything: keep key pairs by
-        // their last visible key
+        // Values of keys that some row does not see may be anything, and 0 times NaN
+        // is NaN: the products take the keys that every row sees (a mask by pairs),
+        const int kb0 = key0 + 16 * i;
         uint32_t keep0 = kFull, keep1 = kFull;
         if constexpr (kMasked) {
-          const int left = ((have >> (2 * i)) & 1u) ? max_lim - key0 - 16 * i - 2 * t : 0;
+          const int left = ((have >> (2 * i)) & 1u) ? min_lim - kb0 - 2 * t : 0;
           keep0 = left <= 0 ? 0u : left == 1 ? 0xffffu : kFull;
           keep1 = left <= 8 ? 0u : left == 9 ? 0xffffu : kFull;
         }
@@ -568,6 +560,35 @@ struct Warp {
             if constexpr (kMasked) a[0] &= keep0, a[1] &= keep0, a[2] &= keep1, a[3] &= keep1;
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_bf16(o[4 * sl + e][n], a, b0[n], b1[n]);
+          }
+        }
+        // and the few others (a causal tile's newest) are added one by one.
+        if constexpr (kMasked) {
+          const int last = ((have >> (2 * i)) & 1u) ? min(max_lim, kb0 + 16) : 0;
+#pragma unroll 1
+          for (int k = max(min_lim, kb0); k < last; ++k) {
+            const int r = k - kb0;   // its probabilities are lane 4 (r % 8) + t's
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float p[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                p[c] = __shfl_sync(kFull, r < 8 ? pr[i][n][c] : pr[i][n][c + 2], (r & 7) * 4 + t);
+              }
+#pragma unroll
+              for (int sl = 0; sl < D / 64; ++sl) {
+                uint32_t w[4];
+                load_words<4>(vb + 2048 * sl + r * 128 + 16 * (g ^ (r & 7)), w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    if (k < lim[n][c]) {
+                      o[4 * sl + e][n][c] = fmaf(p[c], lo_f(w[e]), o[4 * sl + e][n][c]);
+                      o[4 * sl + e][n][c + 2] = fmaf(p[c], hi_f(w[e]), o[4 * sl + e][n][c + 2]);
+                    }
+              }
+            }
           }
         }
       }
@@ -664,6 +685,14 @@ __device__ __forceinline__ int tile_keys(const PagedParams& p, int b, int rt, in
   return p.causal ? max(0, min(len, len - n_q + min(i0 + ROWS, n_q))) : len;
 }
 
+// Keys that every query row of a tile sees.
+template <int ROWS>
+__device__ __forceinline__ int common_keys(const PagedParams& p, int b, int rt, int len) {
+  const int i0 = (int)((long long)rt * ROWS % p.S_q);
+  const int first = i0 + ROWS > p.S_q ? 0 : i0;
+  return p.causal ? max(0, min(len, len - query_count(p, b) + first + 1)) : len;
+}
+
 // The producer warp: requests every stage of the block's segments in turn, as
 // the consumers free them; lane 2 i + v requests block i of K (v = 0) or V, where
 // its page exists (bit 2 i of have[stage]).  Returns the stages requested.
@@ -709,16 +738,17 @@ __device__ __forceinline__ uint32_t produce(const PagedParams& p, Segments seg, 
       }
       page = number < blocks ? table[pg] : -1;   // of the next stage
       const uint32_t mask = __ballot_sync(kFull, ok);
+      const bool drop = requested == (uint32_t)p.fault_drop_stage;   // test of the wait
       // (the first round finds every stage free)
       if (!__all_sync(kFull, mbar_wait(&empty[st], phase, abort_flag, p.timeout_ns)))
         return requested;
-      if (lane == 0) {
+      if (lane == 0 && !drop) {
         have[st] = mask;
         if (mask) mbar_arrive_expect_tx(&full[st], __popc(mask) * S::kBlock);
         else mbar_arrive(&full[st]);
       }
       __syncwarp();
-      if (ok) {
+      if (ok && !drop) {
         if constexpr (kInt4) {
           bulk_load(dst + st * S::kStage, head + now_page * page_bytes + now_blk * S::kBlock,
                     S::kBlock, &full[st]);
@@ -734,6 +764,12 @@ __device__ __forceinline__ uint32_t produce(const PagedParams& p, Segments seg, 
     }
   } while (seg.next(p, HR));
   if (bad) g_paged_status = ATTN_ERR_BAD_INDEX;
+  // stay until the consumers have had the last stages, and with them every copy
+  for (int n = 0; n < S::kStages; ++n) {
+    if (requested + n >= S::kStages)
+      if (!__all_sync(kFull, mbar_wait(&empty[st], phase, abort_flag, p.timeout_ns))) break;
+    if (++st == S::kStages) st = 0, phase ^= 1;
+  }
   return requested;
 }
 
@@ -756,16 +792,17 @@ __global__ void __launch_bounds__(kPgThreads + 32, Shape<D, kInt4, WR, RS>::kCta
   const int g = lane >> 2, t = lane & 3;
   const int HR = p.cache.H_kv * p.row_tiles;
 
-  allow_dependents();   // the merge kernel may be made ready
+  allow_later();   // the merge kernel may be made ready
   if (threadIdx.x < S::kStages) {
     mbar_init(&full[threadIdx.x], 1);
     mbar_init(&empty[threadIdx.x], kPgWarps);
   }
+  fence_mbar_init();
+  wait_for_earlier();
   if (threadIdx.x == 0) {
     sm_abort = 0;
     if (p.split) p.shared[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
-  fence_mbar_init();
   const Deal deal(make_plan(p, plan) * HR, gridDim.x);   // (synchronises the thread block)
   if (blockIdx.x >= deal.G) return;
   Segments seg;
@@ -792,7 +829,7 @@ __global__ void __launch_bounds__(kPgThreads + 32, Shape<D, kInt4, WR, RS>::kCta
     const int h = seg.hr / p.row_tiles, rt = seg.hr % p.row_tiles, b = seg.b;
     const int keys = tile_keys<ROWS>(p, b, rt, seg.len);
     W w;
-    w.start(p, b, h, rt * ROWS + rs * WR, seg.len, keys);
+    w.start(p, b, h, rt * ROWS + rs * WR, seg.len, common_keys<ROWS>(p, b, rt, seg.len), keys);
     const int end = min((seg.unit + seg.n) * p.unit, keys);
     bool ok = true;
 #pragma unroll 1
@@ -924,7 +961,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   constexpr int kPer = kWarps / kRows;                   // warps a row
   constexpr int E = D / 32;                              // elements a lane
   __shared__ float sm_acc[kWarps][D], sm_sum[kWarps];
-  wait_prerequisites();
+  allow_later();
+  wait_for_earlier();
   const int4 it = p.shared[blockIdx.x];
   if (it.x < 0) return;
   const int b = it.x, hr = it.y, c0 = blockIdx.x, parts = it.w - c0 + 1;
@@ -1025,18 +1063,10 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
   while (items * ((p.cache.capacity + p.unit - 1) / p.unit + kItemCost) >= (1ll << 31)) p.unit *= 2;
   const long long most = items * ((p.cache.capacity + p.unit - 1) / p.unit);
   if (ctas > most) ctas = most;
-  kernel<<<(unsigned)ctas, kPgThreads + 32, S::kBytes, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !split) return e;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, S::kRows / kMergeRows);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, S::kRows>, p);
+  e = launch_ahead(kernel, dim3((unsigned)ctas), kPgThreads + 32, S::kBytes, stream, p);
+  if (e != cudaSuccess || !split) return e;
+  return launch_ahead(paged_merge_kernel<D, S::kRows>,
+                      dim3((unsigned)ctas, S::kRows / kMergeRows), kMergeThreads, 0, stream, p);
 }
 
 template <int D, bool kInt4>

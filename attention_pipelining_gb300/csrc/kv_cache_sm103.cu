@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
   const KvCache& kc = p.cache;
   const int c = threadIdx.x % kLanes;
   const uint32_t row_mask = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
+  allow_later();
+  wait_for_earlier();
   const uint32_t token = blockIdx.x * kSlots + threadIdx.x / kLanes;
   if (token >= (uint32_t)(kc.B * p.S)) return;
   const int b = (int)(token / (uint32_t)p.S), i = (int)(token % (uint32_t)p.S);
@@ -358,8 +360,11 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
 // even or odd): it reads the block's codes 16 bytes a lane, 8 or 4 consecutive
 // elements of which go out together (bf16: 16 bytes of a token's vector).
 template <int D, bool kInt4>
-__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadParams p) {
+__global__ void __launch_bounds__(kKvThreads)
+    kv_read_kernel(const __grid_constant__ KvReadParams p) {
   const KvCache& kc = p.cache;
+  allow_later();
+  wait_for_earlier();
   const int lane = threadIdx.x & 31;
   const bool value = blockIdx.y & 1;
   const int h = blockIdx.y >> 1;
@@ -465,19 +470,16 @@ cudaError_t launch_kv_append(const KvAppendParams& p0, int D, bool int4, cudaStr
                                       : kv_append_kernel<64, true, false>
                       : p.interleaved ? kv_append_kernel<64, false, true>
                                       : kv_append_kernel<64, false, false>;
-  kernel<<<grid, kAppendThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_ahead(kernel, grid, kAppendThreads, 0, stream, p);
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, int D, bool int4, cudaStream_t stream) {
   const long long blocks = (long long)p.cache.B * ((p.S + 15) / 16 + (p.start ? 1 : 0));
   const int per = kKvThreads / 32;
   const dim3 grid((unsigned)((blocks + per - 1) / per), (unsigned)(2 * p.cache.H_kv));
-  if (D == 128 && int4) kv_read_kernel<128, true><<<grid, kKvThreads, 0, stream>>>(p);
-  else if (D == 128) kv_read_kernel<128, false><<<grid, kKvThreads, 0, stream>>>(p);
-  else if (int4) kv_read_kernel<64, true><<<grid, kKvThreads, 0, stream>>>(p);
-  else kv_read_kernel<64, false><<<grid, kKvThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const auto kernel = D == 128 ? int4 ? kv_read_kernel<128, true> : kv_read_kernel<128, false>
+                               : int4 ? kv_read_kernel<64, true> : kv_read_kernel<64, false>;
+  return launch_ahead(kernel, grid, kKvThreads, 0, stream, p);
 }
 
 cudaError_t read_kv_status(int* status, bool reset) {

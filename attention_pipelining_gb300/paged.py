@@ -216,7 +216,7 @@ def paged_workspace_bytes(B, H_q, H_kv, S_q, D, max_keys) -> int:
 
 
 def attn_fwd_paged(q, k_cache, v_cache, block_table, lens, causal: bool, scale: float, q_lens=None,
-                   workspace=None, out=None, stream=None):
+                   workspace=None, out=None, stream=None, _fault=None):
     """Attention of q [B, H_q, S_q, D] over the first lens[b] cached positions of each sequence;
     returns (o, lse).  With ``causal`` the queries are the newest tokens (the last q_lens[b], or
     S_q, of lens[b]).  ``workspace``: optional uint8 tensor of at least paged_workspace_bytes(...)
@@ -250,10 +250,22 @@ def attn_fwd_paged(q, k_cache, v_cache, block_table, lens, causal: bool, scale: 
             lse = make(shape[:3], dtype=f32, device=q.device)
         else:
             o, lse = out
-        _check(_load().attn_fwd_paged(c, qs, _out("out[0]", o, shape, bf16, dev),
-                                      _out("out[1]", lse, shape[:3], f32, dev), lens_p, ql_p,
-                                      ws_p, ws_n, H_q, S_q, 1 if causal else 0, scale, handle),
-               "attn_fwd_paged")
+        args = (c, qs, _out("out[0]", o, shape, bf16, dev), _out("out[1]", lse, shape[:3], f32, dev),
+                lens_p, ql_p, ws_p, ws_n, H_q, S_q, 1 if causal else 0, scale)
+        if _fault is None:
+            _check(_load().attn_fwd_paged(*args, handle), "attn_fwd_paged")
+        else:
+            _check(_load().attn_fwd_paged_timeout_test(*args, *_fault, handle),
+                   "attn_fwd_paged_timeout_test")
         return o, lse
 
     return _on(dev, stream, call)
+
+
+def fwd_paged_timeout_test(q, k_cache, v_cache, block_table, lens, causal: bool, scale: float,
+                           drop_stage: int, wait_budget_ns: int = 20_000_000, **kw):
+    """Test hook: attn_fwd_paged with one stage of keys and values never requested, so that the
+    kernel's bounded wait for it runs out (see attn_testing.h).  The device status word then reads
+    ATTN_ERR_TIMEOUT."""
+    return attn_fwd_paged(q, k_cache, v_cache, block_table, lens, causal, scale,
+                          _fault=(int(drop_stage), int(wait_budget_ns)), **kw)

@@ -39,6 +39,14 @@
  * unspecified.  `drop_item` must be >= 0 and `wait_budget_ns` in [1 ms,
  * 2 s] (else ATTN_ERR_INVALID_ARG).  For tests only.
  *
+ * attn_fwd_paged_timeout_test runs attn_fwd_paged (attn_paged.h; same arguments
+ * and buffers) with one difference: the producer warp of every thread block that
+ * gets as far as stage `drop_stage` of its keys and values (counted from 0)
+ * does not request it, so the consumers' wait for it runs out after
+ * `wait_budget_ns`; every warp stops, the producer once its copies under way
+ * are in.  Outputs are unspecified.  `drop_stage` must be >= 0 and `wait_budget_ns` in
+ * [1 ms, 2 s] (else ATTN_ERR_INVALID_ARG).  For tests only.
+ *
  * attn_fwd_tail_pairs returns how many tiles attn_fwd splits across CTA
  * pairs for these sizes on the current device (0 when the tail is not
  * split), or -1 for invalid sizes or a device that cannot be queried.
@@ -48,6 +56,7 @@
 #define ATTN_GB300_TESTING_H
 
 #include "attn.h"
+#include "attn_paged.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -69,6 +78,14 @@ attn_status_t attn_bwd_timeout_test(const void *q, const void *k, const void *v,
                                     int H_q, int H_kv, int S_q, int S_kv, int D, int causal,
                                     float scale, int drop_item, unsigned long long wait_budget_ns,
                                     attn_stream_t stream);
+
+attn_status_t attn_fwd_paged_timeout_test(const attn_kv_cache_t *cache, const attn_bhsd_t *q,
+                                          void *o, float *lse, const int *lens,
+                                          const int *q_lens, void *workspace,
+                                          size_t workspace_bytes, int H_q, int S_q, int causal,
+                                          float scale, int drop_stage,
+                                          unsigned long long wait_budget_ns,
+                                          attn_stream_t stream);
 
 int attn_fwd_tail_pairs(int B, int H_q, int H_kv, int S_q, int S_kv, int D, int causal);
 

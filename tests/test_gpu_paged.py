@@ -256,3 +256,530 @@ def test_long_and_ragged_batch(fmt):
     got = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(),
                             torch.tensor(lens, dtype=torch.int32).cuda(), True, 0.2)
     check_attention(q, kc, vc, bt, lens, True, 0.2, got, what=fmt)
+
+
+# ---------------------------------------------------------------- what must not matter
+
+
+def device_ints(*x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def spoil(pool, bt, lens, page, inside=None):
+    """A copy whose slots behind the sequences' ends, and pages of no sequence, hold NaN and
+    infinities (bf16) or bytes of ones (4 bits: codes 15 and NaN scales)."""
+    bad = torch.full_like(pool, 255) if pool.dtype == torch.uint8 else \
+        torch.where(torch.rand(pool.shape, generator=rng(99)) < 0.5, float("nan"), float("inf")).to(pool.dtype)
+    D = pool.shape[3] // 9 if pool.dtype == torch.uint8 else pool.shape[3]
+    for b, L in enumerate(lens):
+        for x in range(L):
+            pg, slot = int(bt[b, x // page]), x % page
+            if pool.dtype != torch.uint8:
+                bad[pg, :, slot] = pool[pg, :, slot]
+                continue
+            for kind in (inside,):
+                byte = np.unique(ref.nibble_index(kind, D)[slot % 16] // 2)
+                byte = np.concatenate([byte, 8 * D + slot % 16 * (D // 16) + np.arange(D // 16)])
+                bad[pg, :, slot // 16, byte] = pool[pg, :, slot // 16, byte]
+    return bad
+
+
+@pytest.mark.parametrize("Sq", [1, 5])
+@pytest.mark.parametrize("fmt,D", [("int4", 128), ("int4", 64), ("bf16", 128), ("bf16", 64)])
+def test_what_lies_behind_the_end_does_not_matter(fmt, D, Sq):
+    lens, page = [77, 16, 5, 33], 32
+    bt, pages = tables(lens, page, 31)
+    kc, vc = pools(fmt, pages, 2, page, D, 32)
+    q = randn(rng(33), 4, 6, Sq, D)
+    n = device_ints(*lens)
+    want = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), n, True, 0.1)
+    kb, vb = spoil(kc, bt, lens, page, "k"), spoil(vc, bt, lens, page, "v")
+    for wide in (bt, torch.cat([bt, torch.full((4, 64), 2 ** 30, dtype=torch.int32)], 1)):
+        got = ap.attn_fwd_paged(q.cuda(), kb.cuda(), vb.cuda(), wide.cuda(), n, True, 0.1)
+        if wide is bt:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        check_attention(q, kc, vc, bt, lens, True, 0.1, got)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("fmt,D,Hq", [("int4", 64, 4), ("bf16", 128, 2), ("bf16", 64, 12)])
+def test_a_value_that_a_row_does_not_see_does_not_matter(fmt, D, Hq, bad):
+    """The last token's key and value are not finite: of four causal queries only the last one
+    sees them."""
+    L, page = 45, 16
+    bt, pages = tables([L], page, 41)
+    g = rng(42)
+    k, v = randn(g, pages, 1, page, D), randn(g, pages, 1, page, D)
+    kc, vc = fill(k, fmt, "k"), fill(v, fmt, "v")
+    pg, slot = int(bt[0, (L - 1) // page]), (L - 1) % page
+    k[pg, 0, slot], v[pg, 0, slot, ::3] = bad, bad
+    kn, vn = fill(k, fmt, "k"), fill(v, fmt, "v")
+    q = randn(g, 1, Hq, 4, D)
+    o, lse = ap.attn_fwd_paged(q.cuda(), kn.cuda(), vn.cuda(), bt.cuda(), device_ints(L), True, 0.1)
+    head = (o[:, :, :3].contiguous(), lse[:, :, :3].contiguous())
+    check_attention(q[:, :, :3], kc, vc, bt, [L - 1], True, 0.1, head)
+    assert not torch.isfinite(o[0, :, 3]).all()
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_a_sequence_s_nan_stays_its_own(fmt):
+    """A NaN key in one sequence: its rows are NaN, the others' as without."""
+    lens, page, D = [100, 300, 40], 16, 64
+    bt, pages = tables(lens, page, 43)
+    g = rng(44)
+    k, v = randn(g, pages, 2, page, D), randn(g, pages, 2, page, D)
+    q = randn(g, 3, 4, 1, D)
+    bad = k.clone()
+    bad[int(bt[1, 7]), 1, 3, 9] = float("nan")
+    vc = fill(v, fmt, "v")
+    a, _ = ap.attn_fwd_paged(q.cuda(), fill(k, fmt, "k").cuda(), vc.cuda(), bt.cuda(),
+                             device_ints(*lens), True, 0.1)
+    b, _ = ap.attn_fwd_paged(q.cuda(), fill(bad, fmt, "k").cuda(), vc.cuda(), bt.cuda(),
+                             device_ints(*lens), True, 0.1)
+    assert torch.equal(a[[0, 2]], b[[0, 2]]) and torch.equal(a[1, :2], b[1, :2])
+    assert torch.isnan(b[1, 2:]).all()
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_page_numbers_out_of_range(fmt):
+    """Such pages are never followed: their keys are masked, their tokens neither written nor
+    read, and the status word says so."""
+    L, page, D, H = 200, 16, 64, 2
+    bt, pages = tables([L, L], page, 51)
+    kc, vc = pools(fmt, pages, H, page, D, 52)
+    bad = bt.clone()
+    bad[0, 2], bad[0, 7], bad[1, 12] = -1, pages, 2 ** 31 - 1
+    q = randn(rng(53), 2, 4, 1, D)
+    got = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bad.cuda(), device_ints(L, L), False, 0.1)
+    torch.cuda.synchronize()
+    assert ap.device_status(reset=True) == BAD_INDEX
+    for b, gone in ((0, (2, 7)), (1, (12,))):
+        keep = torch.tensor([[int(p) for i, p in enumerate(bt[b]) if i not in gone]], dtype=torch.int32)
+        n = L - sum(min(page, L - i * page) for i in gone)
+        check_attention(q[b:b + 1], kc, vc, keep, [n], False, 0.1, [t[b:b + 1] for t in got])
+    # read: the rows of missing pages stay as they were
+    out = tuple(torch.full((2, H, L, D), 3.0, dtype=torch.bfloat16).cuda() for _ in range(2))
+    ap.kv_read(kc.cuda(), vc.cuda(), bad.cuda(), device_ints(L, L), L, out=out)
+    torch.cuda.synchronize()
+    assert ap.device_status(reset=True) == BAD_INDEX
+    full = ap.kv_read(kc.cuda(), vc.cuda(), bt.cuda(), device_ints(L, L), L)
+    for got_t, want in zip(out, full):
+        want[0, :, 32:48], want[0, :, 112:128], want[1, :, 192:] = 3.0, 3.0, 3.0
+        assert torch.equal(got_t, want)
+    # append: tokens 190 .. 195 of sequence 1 reach into its missing page
+    k = randn(rng(54), 2, H, 6, D).cuda()
+    qo = torch.full((2, 3, 6, D), 4.0, dtype=torch.bfloat16).cuda()
+    k1, v1 = kc.cuda(), vc.cuda()
+    ap.kv_append(k, k, k1, v1, bad.cuda(), device_ints(50, 190), q=randn(rng(55), 2, 3, 6, D).cuda(), q_out=qo)
+    torch.cuda.synchronize()
+    assert ap.device_status(reset=True) == BAD_INDEX
+    k2, v2 = kc.cuda(), vc.cuda()
+    ap.kv_append(k, k, k2, v2, bt.cuda(), device_ints(50, 190), new_lens=device_ints(6, 2))
+    torch.cuda.synchronize()
+    assert torch.equal(k1, k2) and torch.equal(v1, v2)
+    assert (qo[1, :, 2:] == 4.0).all() and not (qo[:, :, :2] == 4.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_lengths_out_of_range_are_cut(fmt):
+    page, D = 16, 64
+    bt, pages = tables([64, 64, 64], page, 56)
+    kc, vc = (t.cuda() for t in pools(fmt, pages, 1, page, D, 57))
+    q = randn(rng(58), 3, 2, 2, D).cuda()
+    want = ap.attn_fwd_paged(q, kc, vc, bt.cuda(), device_ints(0, 64, 40), True, 0.1,
+                             q_lens=device_ints(2, 2, 0))
+    torch.cuda.synchronize()
+    assert ap.device_status(reset=True) == 0
+    for lens, ql in (((-7, 64, 40), (2, 2, 0)), ((0, 65, 40), (2, 2, 0)), ((0, 64, 40), (2, 3, -1))):
+        got = ap.attn_fwd_paged(q, kc, vc, bt.cuda(), device_ints(*lens), True, 0.1,
+                                q_lens=device_ints(*ql))
+        torch.cuda.synchronize()
+        assert ap.device_status(reset=True) == BAD_INDEX
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # positions before the cache or behind its end, or without a rotation, are skipped
+    cos, sin = (t.cuda() for t in rope(40, D))
+    k = randn(rng(59), 3, 1, 4, D).cuda()
+    before = kc.clone()
+    ap.kv_append(k, k, kc, vc, bt.cuda(), device_ints(-4, 64, 40), cos=cos, sin=sin)
+    torch.cuda.synchronize()
+    assert ap.device_status(reset=True) == BAD_INDEX
+    assert torch.equal(kc, before)
+
+
+def test_scores_of_any_size():
+    """Large, tiny, negative and zero softmax scales; keys and values whose scales differ by
+    many powers of two from token to token; a row of zeros and one of tiny queries."""
+    L, page, D = 300, 48, 128
+    bt, pages = tables([L], page, 61)
+    g = rng(62)
+    span = torch.exp2(torch.randint(-12, 9, (pages, 1, page, 1), generator=g).float())
+    k = (torch.randn((pages, 1, page, D), generator=g) * span).to(torch.bfloat16)
+    v = (torch.randn((pages, 1, page, D), generator=g) * span.flip(2)).to(torch.bfloat16)
+    q = randn(g, 1, 6, 1, D)
+    q[0, 1], q[0, 2], q[0, 3] = 0.0, q[0, 2] * 2.0 ** -100, q[0, 3] * 2.0 ** 20
+    for fmt in ("int4", "bf16"):
+        kc, vc = fill(k, fmt, "k"), fill(v, fmt, "v")
+        for scale in (0.001, -0.002, 0.0, 1e-30):
+            got = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(L), False, scale)
+            check_attention(q, kc, vc, bt, [L], False, scale, got, what=(fmt, scale))
+        # the largest scale that is finite: nothing breaks down
+        o, _ = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(L), False, 3.4e38)
+        assert torch.isfinite(o[0, 1]).all()
+
+
+# ---------------------------------------------------------------- rounding of the rotation
+
+
+def test_rotation_rounds_the_exact_value():
+    """Two million rotated elements, bit for bit, and sums next to a tie of the rounding that
+    only the products' lowest bits decide."""
+    S, H, D = 2048, 8, 128
+    x = randn(rng(71), 1, H, S, D, scale=2.0)
+    cos, sin = rope(S, D)
+    kc, vc = ap.kv_cache_empty(S // 64, H, 64, D)
+    bt = torch.arange(S // 64, dtype=torch.int32)[None].cuda()
+    xd = x.cuda()
+    ap.kv_append(xd, xd, kc, vc, bt, device_ints(0), cos=cos.cuda(), sin=sin.cuda())
+    got = ap.kv_read(kc, vc, bt, device_ints(S), S)[0]
+    want = ref.rotate(ref.f64(x), cos.double().numpy(), sin.double().numpy(), False)
+    assert np.array_equal(ref.f64(got), want)
+    # x cos is a tie of the rounding to 8 bits; y sin moves it by less than fp32 holds
+    t = np.array([1 + 2.0 ** -8, 1 + 3 * 2.0 ** -8, 129 * 2.0 ** -7 + 2.0 ** -8])
+    d = np.array([0.0, 2.0 ** -30, -2.0 ** -30, 2.0 ** -40, -2.0 ** -40])
+    cos2 = np.repeat(t, len(d))[:, None] * np.ones((1, 8))
+    sin2 = np.tile(d, len(t))[:, None] * np.ones((1, 8))
+    n = len(cos2)
+    one = torch.ones((1, 1, n, 64), dtype=torch.bfloat16)
+    kc, vc = ap.kv_cache_empty(1, 1, 16, 64)
+    for sign in (1.0, -1.0):
+        y = (one * sign).cuda()
+        ap.kv_append(y, y, kc, vc, bt[:, :1], device_ints(0), cos=torch.from_numpy(cos2).float().cuda(),
+                     sin=torch.from_numpy(sin2).float().cuda(), interleaved=True)
+        got = ref.f64(kc[0, 0, :n, :16])
+        a = sign * np.repeat(cos2, 2, 1)
+        b = sign * np.stack([-sin2, sin2], -1).reshape(n, 16)
+        want = ref.bf16(a)
+        tie = np.abs(a) * 256 % 2 == 1
+        up = np.sign(a) * (2.0 ** -8)
+        want = np.where(b == 0, want, np.where(np.sign(b) == np.sign(a), a + up, a - up))
+        assert tie.all() and np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_append_of_values_that_are_not_finite(fmt):
+    """A 4-bit group with an infinity or a NaN reads as NaN, the others as ever; bf16 keeps them;
+    a rotated infinity is the formula's."""
+    D, S = 64, 3
+    x = randn(rng(73), 1, 1, S, D)
+    x[0, 0, 0, 5], x[0, 0, 1, 40] = float("inf"), float("nan")
+    kc, vc = ap.kv_cache_empty(1, 1, 16, D, fmt)
+    bt = torch.zeros((1, 1), dtype=torch.int32).cuda()
+    cos, sin = torch.full((16, 8), 0.5).cuda(), torch.full((16, 8), 0.25).cuda()
+    q = ap.kv_append(x.cuda(), x.cuda(), kc, vc, bt, device_ints(0), cos=cos, sin=sin, q=x.cuda())
+    k, v = ap.kv_read(kc, vc, bt, device_ints(S), S)
+    q, k, v = q.cpu(), k.cpu(), v.cpu()
+    assert q[0, 0, 0, 5] == float("inf") and q[0, 0, 0, 13] == float("inf")   # x .5, x .25 of the pair
+    assert torch.isnan(q[0, 0, 1, 40]) and torch.isfinite(q[0, 0, 2]).all()
+    if fmt == "bf16":
+        assert torch.equal(v.isnan(), x.isnan()) and torch.equal(v.isinf(), x.isinf())
+        return
+    assert v[0, 0, 0, :32].isnan().all() and v[0, 0, 1, 32:].isnan().all()
+    assert v[0, 0, 0, 32:].isfinite().all() and v[0, 0, 1, :32].isfinite().all()
+    assert v[0, 0, 2].isfinite().all() and k[0, 0, 2].isfinite().all()
+
+
+def test_quantisation_of_every_ratio():
+    """Codes of all pairs (element, largest of the group) of 8-bit mantissas on both sides of a
+    power of two, ties among them; subnormal groups; bit for bit."""
+    D = 64
+    m = np.arange(128, 256) / 128.0
+    top = np.repeat(m, 128 * 4)
+    x = (m[None, :, None] * np.array([1.0, 0.5, 0.25, 0.125])[None, None]).repeat(128, 0).reshape(-1)
+    n = len(top)
+    rows = -(-n // 31)
+    vals = np.zeros((128 * -(-rows // 128) + 16, 2, 32))
+    # each group: its largest element and 31 others that are not larger
+    for i, t in enumerate(m):
+        mine = np.minimum(x[np.isclose(top, t)], t)
+        g = np.zeros((-(-len(mine) // 31), 31))
+        g.reshape(-1)[:len(mine)] = mine
+        at = i * len(g)
+        if at + len(g) > vals.shape[0] * 2:
+            break
+        flat = vals.reshape(-1, 32)
+        flat[at:at + len(g), 0], flat[at:at + len(g), 1:] = t, g * np.where(np.arange(31) % 2, 1, -1)
+    vals = vals.reshape(-1, D)
+    vals[-3:] *= 2.0 ** -126            # subnormal scales
+    vals[-6:-3] *= 2.0 ** -100
+    S = len(vals)
+    v = torch.from_numpy(vals).to(torch.bfloat16)[None, None]
+    kc, vc = ap.kv_cache_empty(-(-S // 64), 1, 64, D, "int4")
+    vc.zero_()
+    bt = torch.arange(kc.shape[0], dtype=torch.int32)[None].cuda()
+    ap.kv_append(v.cuda(), v.cuda(), kc, vc, bt, device_ints(0))
+    torch.cuda.synchronize()
+    f = ref.f64(v)[0, 0]
+    # float64 division and torch's rounding of the scale to bf16 (subnormals too)
+    g = f.reshape(-1, 2, 32)
+    s = torch.from_numpy(np.abs(g).max(-1) / 7).to(torch.bfloat16).double().numpy()
+    with np.errstate(divide="ignore", invalid="ignore"):
+        code = np.where(s[..., None] > 0, np.clip(np.round(g / s[..., None]), -7, 7), 0) + 8
+    code = code.astype(np.uint8).reshape(S, D)
+    got = vc.cpu().numpy().reshape(-1, 9 * D)
+    idx = ref.nibble_index("v", D)
+    for t in range(S):
+        blk = got[t // 16]
+        nib = (blk[idx[t % 16] // 2] >> (4 * (idx[t % 16] % 2))) & 15
+        assert np.array_equal(nib, code[t]), t
+
+
+# ---------------------------------------------------------------- together, as used
+
+
+@pytest.mark.parametrize("fmt,D,Hq,H", [("int4", 128, 8, 2), ("bf16", 64, 6, 3)])
+def test_prompts_then_decoding(fmt, D, Hq, H):
+    """Two prompts of different lengths go into the cache and get their attention from what the
+    cache holds; then both sequences grow token by token, a captured graph of one step replayed
+    while the lengths advance on the device.  Every step against the 64-bit attention over
+    everything appended so far, and bit for bit against uncaptured calls."""
+    page, steps, prompt = 16, 9, [37, 12]
+    cap = [n + steps for n in prompt]
+    bt, pages = tables(cap, page, 81)
+    bt = torch.cat([bt, torch.full((2, 70), -1, dtype=torch.int32)], 1)     # room that splits items
+    btd = bt.cuda()
+    g = rng(82)
+    cos, sin = (t.cuda() for t in rope(128, D))
+    scale = D ** -0.5
+    kc, vc = ap.kv_cache_empty(pages, H, page, D, fmt)
+    kc.fill_(255 if fmt == "int4" else float("nan"))
+    vc.fill_(255 if fmt == "int4" else float("nan"))
+    S = max(prompt)
+    x = randn(g, 2, S, Hq + 2 * H, D).transpose(1, 2).cuda()
+    lens = device_ints(*prompt)
+    q = ap.kv_append(x[:, Hq:Hq + H], x[:, Hq + H:], kc, vc, btd, device_ints(0, 0), cos=cos, sin=sin,
+                     q=x[:, :Hq], new_lens=lens)
+    o, lse = ap.attn_fwd_paged(q, kc, vc, btd, lens, True, scale, q_lens=lens)
+    check_attention(q.cpu(), kc, vc, bt, prompt, True, scale, (o, lse), prompt, "prompt")
+    # the same through the framework's prompt attention on what kv_read returns
+    k, v = ap.kv_read(kc, vc, btd, lens, S)
+    for b, n in enumerate(prompt):
+        ob, lb = ap.attn_fwd(q[b:b + 1, :, :n].contiguous(), k[b:b + 1, :, :n].contiguous(),
+                             v[b:b + 1, :, :n].contiguous(), True, scale)
+        assert (ob.float() - o[b:b + 1, :, :n].float()).abs().max() <= 0.03
+        assert (lb - lse[b:b + 1, :, :n]).abs().max() <= 0.02
+    # decoding
+    new = torch.empty((2, 1, Hq + 2 * H, D), dtype=torch.bfloat16).cuda().transpose(1, 2)
+    start, total = lens.clone(), lens + 1
+    ws = torch.empty(ap.paged_workspace_bytes(2, Hq, H, 1, D, bt.shape[1] * page), dtype=torch.uint8).cuda()
+    q1 = torch.empty((2, Hq, 1, D), dtype=torch.bfloat16).cuda()
+    out = (torch.empty_like(q1), torch.empty((2, Hq, 1)).cuda())
+
+    def step():
+        ap.kv_append(new[:, Hq:Hq + H], new[:, Hq + H:], kc, vc, btd, start, cos=cos, sin=sin,
+                     q=new[:, :Hq], q_out=q1)
+        ap.attn_fwd_paged(q1, kc, vc, btd, total, True, scale, workspace=ws, out=out)
+        start.add_(1)
+        total.add_(1)
+
+    tokens = [randn(g, 2, Hq + 2 * H, 1, D) for _ in range(steps)]
+    new.copy_(tokens[0].cuda())
+    saved = kc.clone(), vc.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    assert torch.equal(start, lens)                      # captured, not run
+    got = []
+    for i in range(steps):
+        new.copy_(tokens[i].cuda())
+        graph.replay()
+        torch.cuda.synchronize()
+        got.append((q1.clone(), out[0].clone(), out[1].clone()))
+        now = [n + i + 1 for n in prompt]
+        check_attention(q1.cpu(), kc, vc, bt, now, True, scale, out, what=i)
+    assert start.tolist() == [n + steps for n in prompt]
+    final = kc.clone(), vc.clone()
+    kc.copy_(saved[0]), vc.copy_(saved[1])
+    start.copy_(lens), total.copy_(lens + 1)
+    for i in range(steps):
+        new.copy_(tokens[i].cuda())
+        step()
+        assert torch.equal(q1, got[i][0]) and torch.equal(out[0], got[i][1]) and torch.equal(out[1], got[i][2])
+    torch.cuda.synchronize()
+    assert torch.equal(kc.view(torch.uint8), final[0].view(torch.uint8))
+    assert torch.equal(vc.view(torch.uint8), final[1].view(torch.uint8))
+
+
+def test_cross_attention_to_encoder_states():
+    """Two decoders' queries over encoder states of other lengths, kept in the cache unrotated,
+    and without a mask."""
+    D, H, enc, page = 64, 4, [93, 20], 32
+    bt, pages = tables(enc, page, 83)
+    kc, vc = ap.kv_cache_empty(pages, H, page, D)
+    kc.zero_(), vc.zero_()
+    k, v = (randn(rng(84 + i), 2, H, max(enc), D).cuda() for i in range(2))
+    n = device_ints(*enc)
+    assert ap.kv_append(k, v, kc, vc, bt.cuda(), device_ints(0, 0), new_lens=n) is None
+    q = randn(rng(86), 2, H, 7, D)
+    got = ap.attn_fwd_paged(q.cuda(), kc, vc, bt.cuda(), n, False, 0.125)
+    check_attention(q, kc, vc, bt, enc, False, 0.125, got)
+    for b, m in enumerate(enc):
+        assert torch.equal(ap.kv_read(kc, vc, bt.cuda(), n, m)[1][b], v[b, :, :m])
+
+
+def test_streams_shared_pages_and_two_calls_at_once():
+    """Sequences that share pages; calls on two streams at once, each with its own workspace,
+    and one without; the bits are those of a single call."""
+    D, H, page, L = 128, 2, 64, 3000
+    bt, pages = tables([L], page, 87)
+    bt = bt.repeat(6, 1)                       # six sequences, one set of pages
+    kc, vc = (t.cuda() for t in pools("int4", pages, H, page, D, 88))
+    lens = [L, 1, 700, 0, 2999, 64]
+    q = randn(rng(89), 6, 8, 1, D)
+    n = device_ints(*lens)
+    qd, btd = q.cuda(), bt.cuda()
+    want = ap.attn_fwd_paged(qd, kc, vc, btd, n, True, 0.1)
+    check_attention(q, kc, vc, bt, lens, True, 0.1, want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    ws = [torch.full((ap.paged_workspace_bytes(6, 8, H, 1, D, bt.shape[1] * page),), 255,
+                     dtype=torch.uint8).cuda() for _ in range(2)] + [None]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got += [ap.attn_fwd_paged(qd, kc, vc, btd, n, True, 0.1, workspace=w, stream=s)
+                for s, w in zip(streams, ws)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in got)
+
+
+def test_graphs_with_their_own_workspaces():
+    """Two captured graphs, replayed in turn and on two streams at once."""
+    D, H, page, L = 64, 1, 16, 4000
+    bt, pages = tables([L], page, 91)
+    kc, vc = (t.cuda() for t in pools("bf16", pages, H, page, D, 92))
+    btd, n = bt.cuda(), device_ints(L)
+    qs = [randn(rng(93 + i), 1, 4, 1, D).cuda() for i in range(2)]
+    want = [ap.attn_fwd_paged(q, kc, vc, btd, n, True, 0.1) for q in qs]
+    graphs, outs, keep = [], [], []
+    for q in qs:
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        out = (torch.empty_like(q), torch.empty((1, 4, 1)).cuda())
+        ws = torch.empty(ap.paged_workspace_bytes(1, 4, H, 1, D, bt.shape[1] * page), dtype=torch.uint8).cuda()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            ap.attn_fwd_paged(q, kc, vc, btd, n, True, 0.1, workspace=ws, out=out)
+        graphs.append(g), outs.append(out), keep.append((s, ws))
+    for _ in range(3):
+        for (s, _), g, out in zip(keep, graphs, outs):
+            with torch.cuda.stream(s):
+                out[0].zero_()
+                g.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out[0], w[0]) and torch.equal(out[1], w[1])
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_pools_larger_than_32_bit_offsets(fmt):
+    """The sequence's pages are the last of a pool of more than 2^32 bytes."""
+    H, page, D, L = 8, 64, 128, 300
+    per = H * page * (D * 2 if fmt == "bf16" else 72)
+    pages = (1 << 32) // per + 40
+    kc, vc = ap.kv_cache_empty(pages, H, page, D, fmt)
+    bt = torch.arange(pages - 1, pages - 6, -1, dtype=torch.int32)[None].cuda()
+    k, v = (randn(rng(95 + i), 1, H, L, D).cuda() for i in range(2))
+    ap.kv_append(k, v, kc, vc, bt, device_ints(0))
+    small = tuple(t[pages - 5:].clone() for t in (kc, vc))
+    q = randn(rng(97), 1, 8, 1, D)
+    near = torch.tensor([[4, 3, 2, 1, 0]], dtype=torch.int32)
+    got = ap.attn_fwd_paged(q.cuda(), kc, vc, bt, device_ints(L), True, 0.09)
+    check_attention(q, *small, near, [L], True, 0.09, got)
+    if fmt == "bf16":
+        back = ap.kv_read(kc, vc, bt, device_ints(L), L)
+        assert torch.equal(back[0], k) and torch.equal(back[1], v)
+
+
+def test_one_very_long_sequence():
+    """131072 4-bit keys of one head over many thread blocks."""
+    L, page, D = 131072, 256, 64
+    bt, pages = tables([L], page, 98, spare=0)
+    g = torch.Generator().manual_seed(99)
+    kc = torch.randint(0, 256, (pages, 1, page // 16, 9 * D), generator=g, dtype=torch.uint8)
+    vc = torch.randint(0, 256, (pages, 1, page // 16, 9 * D), generator=g, dtype=torch.uint8)
+    for t in (kc, vc):   # scales of about 1 / 8, positive
+        s = (torch.rand(t.shape[:3] + (D // 2,), generator=g) * 0.1 + 0.1).to(torch.bfloat16)
+        t[..., 8 * D:] = s.view(torch.uint8)
+    q = randn(rng(100), 1, 5, 1, D)
+    got = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(L), True, 0.125)
+    check_attention(q, kc, vc, bt, [L], True, 0.125, got)
+
+
+def test_refusals_on_the_device():
+    D = 64
+    kc, vc = ap.kv_cache_empty(4, 2, 16, D, "int4")
+    kb, vb = ap.kv_cache_empty(4, 2, 16, D)
+    bt = torch.zeros((2, 80), dtype=torch.int32).cuda()
+    n = device_ints(1, 1)
+    q = torch.zeros((2, 4, 1, D), dtype=torch.bfloat16).cuda()
+    k = torch.zeros((2, 2, 1, D), dtype=torch.bfloat16).cuda()
+    f = ap.attn_fwd_paged
+    with pytest.raises(TypeError):
+        f(q.half(), kb, vb, bt, n, True, 0.1)
+    with pytest.raises(ValueError):
+        f(q, kb, vc, bt, n, True, 0.1)
+    with pytest.raises(TypeError):
+        f(q, kb, vb, bt.long(), n, True, 0.1)
+    with pytest.raises(TypeError):
+        f(q, kb, vb, bt, n.long(), True, 0.1)
+    with pytest.raises(TypeError):
+        f(q, kb, vb, bt, n[:1], True, 0.1)
+    with pytest.raises(ValueError):
+        f(q[:1], kb, vb, bt, n, True, 0.1)
+    with pytest.raises(ap.AttnError):
+        f(q[:, :3], kb, vb, bt, n, True, 0.1)                    # three heads over two
+    with pytest.raises(ap.AttnError):
+        f(q, kb, vb, bt, n, True, float("nan"))
+    with pytest.raises(ap.AttnError):
+        f(q, kb, vb, bt, n, True, 0.1, workspace=torch.empty(64, dtype=torch.uint8).cuda())
+    with pytest.raises(TypeError):
+        f(q, kb, vb, bt, n, True, 0.1, out=(q, torch.empty(2, 4).cuda()))
+    odd = torch.zeros((2, 4, 1, D + 4), dtype=torch.bfloat16).cuda()[..., 4:]
+    with pytest.raises(ap.AttnError):
+        f(odd, kb, vb, bt, n, True, 0.1)                          # 8 bytes off, strides of 68
+    with pytest.raises(ValueError):
+        ap.kv_append(k.expand(2, 2, 1, D).transpose(2, 3), k, kc, vc, bt, n)
+    with pytest.raises(ValueError):
+        ap.kv_append(k, k, kc, vc, bt, n, cos=torch.zeros(9, 0).cuda(), sin=torch.zeros(9, 0).cuda())
+    with pytest.raises(ap.AttnError):
+        ap.kv_append(k, k, kc, vc, bt, n, cos=torch.zeros(9, 4).cuda(), sin=torch.zeros(9, 4).cuda())
+    with pytest.raises(TypeError):
+        ap.kv_append(k, k, kc, vc, bt, n, cos=torch.zeros(9, 8).cuda())
+    with pytest.raises(ValueError):
+        ap.kv_append(k, k, kc, vc, bt, n, q_out=q)
+    with pytest.raises(TypeError):
+        ap.kv_read(kc, vc, bt, n, 4, out=(k, k))
+    with pytest.raises(ap.AttnError):
+        ap.kv_read(kc, vc, bt, n, 0)
+
+
+# ---------------------------------------------------------------- failure detection
+
+
+@pytest.mark.parametrize("fmt,D,Hq", [("int4", 128, 4), ("int4", 64, 20), ("bf16", 128, 4), ("bf16", 64, 64)])
+def test_a_wait_that_runs_out(fmt, D, Hq):
+    """One stage of keys and values is never requested: every warp stops, the status word reads
+    ATTN_ERR_TIMEOUT, and the same call right after is right."""
+    L, page = 5000, 16
+    bt, pages = tables([L], page, 101)
+    kc, vc = pools(fmt, pages, 1, page, D, 102)
+    q = randn(rng(103), 1, Hq, 1, D)
+    args = (q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(L), True, 0.1)
+    ap.paged.fwd_paged_timeout_test(*args, drop_stage=0, wait_budget_ns=20_000_000)
+    torch.cuda.synchronize()
+    assert ap.device_status(reset=True) == 5
+    check_attention(q, kc, vc, bt, [L], True, 0.1, ap.attn_fwd_paged(*args))
+    # a stage that no thread block gets to: nothing is withheld
+    check_attention(q, kc, vc, bt, [L], True, 0.1,
+                    ap.paged.fwd_paged_timeout_test(*args, drop_stage=10 ** 6))
