@@ -33,20 +33,24 @@ KV_BF16, KV_INT4 = 0, 1
 # wrong is worked out only when something is.
 
 
-@functools.cache
-def _torch():
-    import torch
-    return (torch, torch.bfloat16, torch.uint8, torch.int32, torch.float32)
+torch = None   # imported with the first call, as in the package's other functions
+
+
+def _import():
+    global torch, _Tensor, _bf16, _u8, _i32, _f32, _current_device, _current_stream
+    import torch as t
+    _Tensor, _bf16, _u8, _i32, _f32 = t.Tensor, t.bfloat16, t.uint8, t.int32, t.float32
+    _current_device, _current_stream = t._C._cuda_getDevice, t._C._cuda_getCurrentRawStream
+    torch = t
 
 
 def _why_not_cache(k, v, bt):
-    torch, bf16, u8, i32, _ = _torch()
     for name, t in (("k_cache", k), ("v_cache", v), ("block_table", bt)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        if not isinstance(t, _Tensor) or not t.is_cuda or not t.is_contiguous():
             raise TypeError(f"{name} must be a contiguous CUDA tensor")
-    if k.dtype not in (bf16, u8):
+    if k.dtype not in (_bf16, _u8):
         raise TypeError("k_cache must be bfloat16 or, for a 4-bit cache, uint8")
-    if bt.dtype != i32 or bt.dim() != 2:
+    if bt.dtype != _i32 or bt.dim() != 2:
         raise TypeError("block_table must be an int32 [B, max_blocks] tensor")
     if v.device != k.device or bt.device != k.device:
         raise ValueError("k_cache, v_cache and block_table must be on one device")
@@ -57,18 +61,19 @@ def _why_not_cache(k, v, bt):
 
 def _cache(k, v, bt):
     """(attn_kv_cache_t, device index, B, H_kv, D, positions the block table spans)"""
-    _, bf16, u8, i32, _ = _torch()
+    if torch is None:
+        _import()
     try:
         dev, dtype, shape = k.get_device(), k.dtype, k.shape
         if dev < 0 or v.get_device() != dev or bt.get_device() != dev or v.dtype is not dtype \
-                or bt.dtype is not i32 or v.shape != shape or not k.is_contiguous() \
+                or bt.dtype is not _i32 or v.shape != shape or not k.is_contiguous() \
                 or not v.is_contiguous() or not bt.is_contiguous():
             raise ValueError
         pages, heads, page, D = shape
         B, blocks = bt.shape
-        if dtype is bf16:
+        if dtype is _bf16:
             fmt = KV_BF16
-        elif dtype is u8 and D % 9 == 0:
+        elif dtype is _u8 and D % 9 == 0:
             fmt, page, D = KV_INT4, 16 * page, D // 9
         else:
             raise ValueError
@@ -80,8 +85,7 @@ def _cache(k, v, bt):
 
 def _bhsd(name, t, shape, dev):
     """attn_bhsd_t of a bf16 tensor of that shape"""
-    torch, bf16, _, _, _ = _torch()
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not bf16:
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not _bf16:
         raise TypeError(f"{name} must be a bfloat16 tensor on the cache's device")
     sb, sh, ss, sd = t.stride() if t.shape == shape else (0, 0, 0, 0)
     if sd != 1:
@@ -93,15 +97,14 @@ def _bhsd(name, t, shape, dev):
 def _ints(name, t, B, dev, optional=False):
     if t is None and optional:
         return None
-    torch, _, _, i32, _ = _torch()
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not i32 \
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not _i32 \
             or t.shape != (B,) or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 [{B}] tensor on the cache's device")
     return t.data_ptr()
 
 
 def _out(name, t, shape, dtype, dev):
-    if not isinstance(t, _torch()[0].Tensor) or t.get_device() != dev or t.dtype is not dtype \
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not dtype \
             or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the cache's "
                         "device")
@@ -111,29 +114,29 @@ def _out(name, t, shape, dtype, dev):
 def _on(dev, stream, call):
     """call(stream handle) with device `dev` current, on `stream` or else on the device's current
     stream, to which what it allocates belongs."""
-    torch = _torch()[0]
     if stream is not None:
         if stream.device.index != dev:
             raise ValueError("stream belongs to another device than the cache")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if torch.cuda.current_device() == dev:
-        return call(torch._C._cuda_getCurrentRawStream(dev))
+    if _current_device() == dev:
+        return call(_current_stream(dev))
     with torch.cuda.device(dev):
-        return call(torch._C._cuda_getCurrentRawStream(dev))
+        return call(_current_stream(dev))
 
 
 def kv_cache_empty(num_pages: int, H_kv: int, page_size: int, D: int, fmt: str = "bf16",
                    device="cuda"):
     """A pair of uninitialised pools (k_cache, v_cache); fmt "bf16" or "int4"."""
-    torch, bf16, u8, _, _ = _torch()
+    if torch is None:
+        _import()
     if fmt not in ("bf16", "int4"):
         raise ValueError('fmt must be "bf16" or "int4"')
     if D not in (64, 128) or page_size <= 0 or page_size % 16:
         raise ValueError("D must be 64 or 128 and page_size a multiple of 16")
     shape = (num_pages, H_kv, page_size, D) if fmt == "bf16" else \
         (num_pages, H_kv, page_size // 16, 9 * D)
-    dtype = bf16 if fmt == "bf16" else u8
+    dtype = _bf16 if fmt == "bf16" else _u8
     return (torch.empty(shape, dtype=dtype, device=device),
             torch.empty(shape, dtype=dtype, device=device))
 
@@ -145,9 +148,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, start, cos=None, sin=None, q=
     [B, H_q, S, D] also rotates the queries and returns them (in ``q_out`` if given, which may be q
     itself where q is contiguous; where new_lens leaves padding its rows keep what they held, zeros
     in a q_out allocated here)."""
-    torch, bf16, _, _, f32 = _torch()
     c, dev, B, heads, D, _ = _cache(k_cache, v_cache, block_table)
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+    if not isinstance(k, _Tensor) or k.dim() != 4:
         raise TypeError("k must be a [B, H_kv, S, D] tensor")
     S = k.shape[2]
     ks, vs = _bhsd("k", k, (B, heads, S, D), dev), _bhsd("v", v, (B, heads, S, D), dev)
@@ -156,7 +158,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, start, cos=None, sin=None, q=
     cos_p = sin_p = None
     if cos is not None or sin is not None:
         for name, t in (("cos", cos), ("sin", sin)):
-            if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not f32 \
+            if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not _f32 \
                     or t.dim() != 2 or not t.is_contiguous():
                 raise TypeError(f"{name} must be a contiguous float32 [positions, rot_dim / 2] tensor "
                                 "on the cache's device")
@@ -170,7 +172,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, start, cos=None, sin=None, q=
             raise ValueError("q_out without q")
         H_q, qs = 0, None
     else:
-        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        if not isinstance(q, _Tensor) or q.dim() != 4:
             raise TypeError("q must be a [B, H_q, S, D] tensor")
         H_q = q.shape[1]
         qs = _bhsd("q", q, (B, H_q, S, D), dev)
@@ -180,8 +182,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, start, cos=None, sin=None, q=
         if q is not None:
             if out is None:
                 make = torch.zeros if new_lens is not None else torch.empty
-                out = make((B, H_q, S, D), dtype=bf16, device=q.device)
-            out_p = _out("q_out", out, (B, H_q, S, D), bf16, dev)
+                out = make((B, H_q, S, D), dtype=_bf16, device=q.device)
+            out_p = _out("q_out", out, (B, H_q, S, D), _bf16, dev)
         _check(_load().attn_kv_append(c, qs, out_p, ks, vs, start_p, new_p, cos_p, sin_p, rows, rot,
                                       1 if interleaved else 0, H_q, S, handle), "attn_kv_append")
         return out
@@ -193,16 +195,15 @@ def kv_read(k_cache, v_cache, block_table, lens, S: int, start=None, out=None, s
     """Positions start[b] .. start[b] + S - 1 (from 0 without ``start``) of every sequence as
     contiguous bf16 (k, v) [B, H_kv, S, D]; rows at or beyond lens[b] keep what ``out`` held, zeros
     where it is allocated here."""
-    torch, bf16, _, _, _ = _torch()
     c, dev, B, heads, D, _ = _cache(k_cache, v_cache, block_table)
     lens_p, start_p = _ints("lens", lens, B, dev), _ints("start", start, B, dev, True)
     shape = (B, heads, S, D)
 
     def call(handle):
         k, v = out if out is not None else (
-            torch.zeros(shape, dtype=bf16, device=k_cache.device) for _ in range(2))
-        _check(_load().attn_kv_read(c, _out("out[0]", k, shape, bf16, dev),
-                                    _out("out[1]", v, shape, bf16, dev), lens_p, start_p, S, handle),
+            torch.zeros(shape, dtype=_bf16, device=k_cache.device) for _ in range(2))
+        _check(_load().attn_kv_read(c, _out("out[0]", k, shape, _bf16, dev),
+                                    _out("out[1]", v, shape, _bf16, dev), lens_p, start_p, S, handle),
                "attn_kv_read")
         return k, v
 
@@ -223,9 +224,8 @@ def attn_fwd_paged(q, k_cache, v_cache, block_table, lens, causal: bool, scale: 
     bytes, not shared with calls that may run at the same time (allocated if None); ``out``: optional
     (o, lse) to write into (rows of queries at or beyond q_lens[b] keep what it held, zeros where it
     is allocated here)."""
-    torch, bf16, u8, _, f32 = _torch()
     c, dev, B, heads, D, span = _cache(k_cache, v_cache, block_table)
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+    if not isinstance(q, _Tensor) or q.dim() != 4:
         raise TypeError("q must be a [B, H_q, S_q, D] tensor")
     H_q, S_q = q.shape[1], q.shape[2]
     shape = (B, H_q, S_q, D)
@@ -234,23 +234,23 @@ def attn_fwd_paged(q, k_cache, v_cache, block_table, lens, causal: bool, scale: 
     nbytes = paged_workspace_bytes(B, H_q, heads, S_q, D, span)
     if nbytes == 0:
         raise AttnError(1, "attn_paged_workspace_bytes")
-    if workspace is not None and (not isinstance(workspace, torch.Tensor)
-                                  or workspace.get_device() != dev or workspace.dtype is not u8
+    if workspace is not None and (not isinstance(workspace, _Tensor)
+                                  or workspace.get_device() != dev or workspace.dtype is not _u8
                                   or not workspace.is_contiguous()):
         raise TypeError("workspace must be a contiguous uint8 tensor on the cache's device")
 
     def call(handle):
         ws = workspace
         if ws is None and nbytes > 256:   # 256: none is used
-            ws = torch.empty(nbytes, dtype=u8, device=q.device)
+            ws = torch.empty(nbytes, dtype=_u8, device=q.device)
         ws_p, ws_n = (ws.data_ptr(), ws.numel()) if ws is not None else (None, 0)
         if out is None:
             make = torch.zeros if q_lens is not None else torch.empty
-            o = make(shape, dtype=bf16, device=q.device)
-            lse = make(shape[:3], dtype=f32, device=q.device)
+            o = make(shape, dtype=_bf16, device=q.device)
+            lse = make(shape[:3], dtype=_f32, device=q.device)
         else:
             o, lse = out
-        args = (c, qs, _out("out[0]", o, shape, bf16, dev), _out("out[1]", lse, shape[:3], f32, dev),
+        args = (c, qs, _out("out[0]", o, shape, _bf16, dev), _out("out[1]", lse, shape[:3], _f32, dev),
                 lens_p, ql_p, ws_p, ws_n, H_q, S_q, 1 if causal else 0, scale)
         if _fault is None:
             _check(_load().attn_fwd_paged(*args, handle), "attn_fwd_paged")
