@@ -205,6 +205,7 @@ constexpr int kPagedUnit = 128;
 constexpr int kPagedItemCost = 2;  // units that an item's beginning and end count for
 constexpr int kPagedWholeKeys = 1024;
 constexpr int kPagedMaxCtas = 512;
+constexpr int kPagedFewItems = 152;   // items that have an SM each
 
 cudaError_t launch_kv_append(const KvAppendParams& p, int D, bool int4, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadParams& p, int D, bool int4, cudaStream_t stream);

@@ -68,7 +68,8 @@ constexpr size_t kLeastWorkspace = 256;   // reported where none is used: 0 says
 // CTAs that may write parts to the workspace: none where an item is kept whole.
 int64_t part_ctas(int64_t B, int64_t H_kv, int64_t rows, int tile, int64_t max_keys) {
   if (max_keys <= kPagedWholeKeys) return 0;
-  const int64_t units = B * H_kv * ((rows + tile - 1) / tile) * ((max_keys + kPagedUnit - 1) / kPagedUnit);
+  const int64_t units =
+      B * H_kv * ((rows + tile - 1) / tile) * ((max_keys + kPagedUnit - 1) / kPagedUnit);
   return units < kPagedMaxCtas ? units : kPagedMaxCtas;
 }
 
@@ -83,7 +84,7 @@ attn_status_t check_rows(int B, int H_q, int H_kv, int S_q) {
   const int64_t rows = (int64_t)(H_q / H_kv) * S_q;
   if (rows >= (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
   // items, with what each counts for apart from its keys, are counted in an int
-  const int tile = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int tile = tile_rows(H_q / H_kv, S_q);
   if (((rows + tile - 1) / tile) * H_kv * B * (kPagedItemCost + 1) >= (1ll << 31))
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
@@ -165,7 +166,8 @@ attn_status_t attn_kv_append(const attn_kv_cache_t* cache, const attn_bhsd_t* q,
   if (rot_dim > 0 && (!cos || !sin || rope_rows <= 0)) return ATTN_ERR_INVALID_ARG;
   // one grid column a token, one row of blocks per few heads
   if ((int64_t)cache->B * S >= (1ll << 31) || H_q > 65535) return ATTN_ERR_UNSUPPORTED;
-  if (!aligned4(start) || !aligned4(new_lens) || (rot_dim > 0 && (!aligned16(cos) || !aligned16(sin))))
+  if (!aligned4(start) || !aligned4(new_lens) ||
+      (rot_dim > 0 && (!aligned16(cos) || !aligned16(sin))))
     return ATTN_ERR_MISALIGNED;
   if (H_q > 0) {
     if ((st = take_tensor(q, cache->B, H_q, S, &p.q)) != ATTN_OK) return st;

@@ -205,10 +205,10 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& w, uint32_t row_mask,
       u[i] = (uint32_t)((int)q + 8);
     }
   }
-  const uint32_t even = __byte_perm(__byte_perm(u[0], u[2], 0x0040u), __byte_perm(u[4], u[6], 0x0040u),
-                                    0x5410u);
-  const uint32_t odd = __byte_perm(__byte_perm(u[1], u[3], 0x0040u), __byte_perm(u[5], u[7], 0x0040u),
-                                   0x5410u);
+  const auto low_bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040u), __byte_perm(c, d, 0x0040u), 0x5410u);
+  };
+  const uint32_t even = low_bytes(u[0], u[2], u[4], u[6]), odd = low_bytes(u[1], u[3], u[5], u[7]);
   return (even & 0x0f0f0f0fu) | (odd & 0x0f0f0f0fu) << 4;
 }
 

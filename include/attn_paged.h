@@ -92,9 +92,8 @@ typedef struct {
  *              1: element 2 d pairs with 2 d + 1
  *
  * A pair (a, b) at position x becomes (a cos - b sin, b cos + a sin), rounded
- * once to bf16 (products and sum exact to 48 bits before that), and a 4-bit
- * cache quantises that rounded key: the result depends on nothing but the
- * inputs' values.  Slots must be distinct: two tokens of one call in the same
+ * once to bf16 from the exact value, and a 4-bit cache quantises that rounded
+ * key: the result depends on nothing but the inputs' values.  Slots must be distinct: two tokens of one call in the same
  * slot (two sequences appending to a shared page) leave either, or a mixture.
  */
 attn_status_t attn_kv_append(const attn_kv_cache_t *cache, const attn_bhsd_t *q, void *q_out,
@@ -130,19 +129,22 @@ attn_status_t attn_kv_read(const attn_kv_cache_t *cache, void *k_out, void *v_ou
  *              attn_paged_workspace_bytes(...) bytes; need not be cleared; not
  *              shared with calls that may run at the same time
  *
- * The work (16-key blocks of all sequences) is dealt out evenly to a grid that
- * fills the GPU, whatever the lengths; a sequence that ends up on more than
- * one thread block is merged by a second kernel.  Meant for decoding, where
- * S_q is one or a few tokens: each (H_q / H_kv) * S_q <= 64 query rows of a KV
- * head read the cache once, and more rows read it once for every 64.  A whole
- * prompt is faster through attn_fwd, with attn_kv_read for what it shares
- * with the cache.  The results are deterministic for given lengths.
+ * Where the block table spans more than 1024 keys, the work (units of 128 keys of all
+ * sequences) is dealt out evenly to a grid that fills the GPU, whatever the
+ * lengths; a sequence that ends up on more than one thread block is merged by a
+ * second kernel.  Meant for decoding, where S_q is one or a few tokens: each
+ * (H_q / H_kv) * S_q <= 64 query rows of a KV head read the cache once, and more
+ * rows read it once for every 64.  A whole prompt is faster through attn_fwd,
+ * with attn_kv_read for what it shares with the cache.  The results are
+ * deterministic for given lengths.
  *
  * Arithmetic: fp32 accumulation and softmax statistics.  bf16 cache: the
  * probabilities are rounded to bf16 for the second product.  4-bit cache: the
- * codes are exact in the products, the queries keep bits down to 2^-22 of
- * their row's largest element, the probabilities times the values' scales are
- * rounded to fp16.
+ * codes are exact in the products, the queries are exact down to 2^-17 of their
+ * row's largest element (smaller elements are off by 2^-25 of it at most), and the
+ * probabilities times the values' scales are rounded to fp16 (an error of 2^-11
+ * of a key's share in O, or of 2^-30 of the largest value, or 2^-90, where that
+ * is more).
  */
 attn_status_t attn_fwd_paged(const attn_kv_cache_t *cache, const attn_bhsd_t *q, void *o,
                              float *lse, const int *lens, const int *q_lens, void *workspace,

@@ -11,11 +11,9 @@ Also the error bounds of the CUDA attention, from its rounding model:
 * The scores' error, which every probability takes as a relative error (twice in
   O: numerator and denominator): tensor-core sums in fp32, at most 2^-20 of the
   sum of the magnitudes per instruction chain (eight instructions of at most
-  four steps of 2^-23 each at D = 128 give 2^-18); for 4-bit keys those
-  magnitudes include the constants the codes are read with (264 q per code at
-  most, one chain of two instructions: 2^-20), and a query's fp16 rounding of at
-  most 2^-11 2^-14 of its row's largest element; then the exponent's three fp32
-  roundings (2^-22 of its magnitude) and ex2's 2^-22.
+  four steps of 2^-23 each at D = 128 give 2^-18); for 4-bit keys also a
+  query's fp16 rounding of at most 2^-11 2^-14 of its row's largest element; then
+  the exponent's three fp32 roundings (2^-22 of its magnitude) and ex2's 2^-22.
 """
 import numpy as np
 import torch
@@ -141,7 +139,7 @@ def attention(q, kvals, vvals, kscales, vscales, table, lens, page, causal, scal
             continue
         k, v = gather(kvals, table[b], L, page), gather(vvals, table[b], L, page)
         if four:
-            ks, vs = gather(kscales, table[b], L, page), gather(vscales, table[b], L, page)
+            vs = gather(vscales, table[b], L, page)
         for h in range(Hq):
             kh, vh = k[h // R], v[h // R]
             for i in range(nq):
@@ -158,8 +156,6 @@ def attention(q, kvals, vvals, kscales, vscales, table, lens, page, causal, scal
                 A = p @ np.abs(vh[:n]) / l
                 es = abs(scale) * (np.abs(kh[:n]) @ np.abs(x)) * 2.0 ** -18
                 if four:
-                    g = np.abs(x).reshape(-1, 32).sum(-1)
-                    es = es + abs(scale) * (ks[h // R][:n] @ g) * 264 * 2.0 ** -20
                     es = es + abs(scale) * np.abs(kh[:n]).sum(-1) * np.abs(x).max() * 2.0 ** -25
                 e = float(es.max()) + np.abs(s).max() * 1.5 * 2.0 ** -22 + 2.0 ** -22
                 share = 2.0 ** -11 if four else 2.0 ** -8

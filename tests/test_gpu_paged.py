@@ -490,27 +490,19 @@ def test_append_of_values_that_are_not_finite(fmt):
 
 def test_quantisation_of_every_ratio():
     """Codes of all pairs (element, largest of the group) of 8-bit mantissas on both sides of a
-    power of two, ties among them; subnormal groups; bit for bit."""
+    power of two, ties among them; groups whose scale is subnormal or 0; bit for bit."""
     D = 64
     m = np.arange(128, 256) / 128.0
-    top = np.repeat(m, 128 * 4)
-    x = (m[None, :, None] * np.array([1.0, 0.5, 0.25, 0.125])[None, None]).repeat(128, 0).reshape(-1)
-    n = len(top)
-    rows = -(-n // 31)
-    vals = np.zeros((128 * -(-rows // 128) + 16, 2, 32))
-    # each group: its largest element and 31 others that are not larger
-    for i, t in enumerate(m):
-        mine = np.minimum(x[np.isclose(top, t)], t)
-        g = np.zeros((-(-len(mine) // 31), 31))
-        g.reshape(-1)[:len(mine)] = mine
-        at = i * len(g)
-        if at + len(g) > vals.shape[0] * 2:
-            break
-        flat = vals.reshape(-1, 32)
-        flat[at:at + len(g), 0], flat[at:at + len(g), 1:] = t, g * np.where(np.arange(31) % 2, 1, -1)
+    x = np.concatenate([m, m / 2, m / 4, m / 8])
+    vals = np.zeros((len(m), 17, 32))   # each group: its largest element and 31 others
+    for i, top in enumerate(m):
+        others = np.zeros(17 * 31)
+        others[:len(x)] = np.minimum(x, top)
+        vals[i, :, 0] = top
+        vals[i, :, 1:] = others.reshape(17, 31) * np.where(np.arange(31) % 2, 1, -1)
     vals = vals.reshape(-1, D)
-    vals[-3:] *= 2.0 ** -126            # subnormal scales
-    vals[-6:-3] *= 2.0 ** -100
+    vals = np.concatenate([vals, vals[::7] * 2.0 ** -98, vals[::7] * 2.0 ** -120,
+                           vals[::7] * 2.0 ** -126, vals[::7] * 2.0 ** -131])
     S = len(vals)
     v = torch.from_numpy(vals).to(torch.bfloat16)[None, None]
     kc, vc = ap.kv_cache_empty(-(-S // 64), 1, 64, D, "int4")

@@ -102,6 +102,12 @@ def test_attention_refuses(lib, kw, code):
     assert attend(lib, **kw) == code
 
 
+@pytest.mark.parametrize("drop,budget,code", [(-1, 10**7, 1), (0, 999_999, 1), (0, 2**63, 1)])
+def test_timeout_hook_refuses(lib, drop, budget, code):
+    assert lib.attn_fwd_paged_timeout_test(cache(), tensor(), A, A, A, None, A, 1 << 30, 4, 1, 1,
+                                           ctypes.c_float(0.1), drop, budget, None) == code
+
+
 def test_attention_checks_the_workspace_of_split_items(lib):
     need = lib.attn_paged_workspace_bytes(2, 4, 2, 1, 128, 64 * 40)
     assert attend(lib, cache(max_blocks=40), nbytes=need - 1) == 1
