@@ -1,10 +1,9 @@
 // kv_cache_sm103.cu -- new tokens into the paged key/value cache (rotation,
 // 4-bit quantisation) and cached tokens back into contiguous tensors.
 //
-// Both kernels stream, and are bound by HBM as long as the rotation's and the
-// quantisation's instructions stay below about ten an element: 6.8 TB/s of 4
-// bytes an element (bf16 read and written) leave each SM 22 thread-instructions
-// an element, of 2.6 bytes (a 4-bit write) 14.
+// Both kernels stream.  6.8 TB/s of 4 bytes an element (bf16 read and written)
+// leave each SM 22 thread-instructions an element, of 2.6 bytes (a 4-bit write)
+// 14: the rotation takes about 12 and the quantisation 8, loads and stores included.
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
@@ -21,12 +20,16 @@ namespace {
 
 constexpr int kKvThreads = 256;         // of the read kernel
 constexpr int kAppendThreads = 128;
-constexpr int kAhead = 4;               // rows of a thread under way in the append kernel
-constexpr int kAppendBlocks = 2432;     // sixteen blocks on each of 152 SMs
+constexpr int kAhead = 3;               // rows of a thread under way in the append kernel
+constexpr int kAppendBlocks = 4864;     // 32 blocks on each of 152 SMs, in four rounds
 
-// 16 bytes to shared memory, asynchronously, in the thread's open group.
+// 16 and 8 bytes to shared memory, asynchronously, in the thread's open group.
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src)
                : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() {
@@ -61,100 +64,83 @@ __device__ __forceinline__ float rotate_bf16(float x, float a, float y, float b)
   return __uint_as_float(u);
 }
 
-// Eight elements x c + y s, for v = {x, y, c, s}.
-__device__ __noinline__ void rotate8_exactly(const float (&v)[4][8], uint32_t (&out)[4]) {
+// Four pairs, v = {x, y, c, s}: r = {x c - y s, y c + x s}.
+__device__ __noinline__ void rotate4_exactly(const float (&v)[4][4], float (&r)[2][4]) {
 #pragma unroll 1
-  for (int i = 0; i < 4; ++i)
-    out[i] = pack_bf16x2(rotate_bf16(v[0][2 * i], v[2][2 * i], -v[1][2 * i], v[3][2 * i]),
-                         rotate_bf16(v[0][2 * i + 1], v[2][2 * i + 1], -v[1][2 * i + 1],
-                                     v[3][2 * i + 1]));
+  for (int i = 0; i < 4; ++i) {
+    r[0][i] = rotate_bf16(v[0][i], v[2][i], v[1][i], v[3][i]);
+    r[1][i] = rotate_bf16(v[1][i], v[2][i], -v[0][i], v[3][i]);
+  }
 }
 
-// The same for eight elements in pairs, r = x c + y s (y negated by the caller
-// where the formula subtracts): first with four operations an element,
-// fma(x, c, h) + e with h + e = y s exactly, which is off by at most two units of
+// The same, two pairs at a time: first with five operations a result,
+// fma(x, c, h) + e with h + e = -y s exactly, which is off by at most two units of
 // fp32's last place (half a unit in each of the two sums, of which the first may
 // be twice as large as the second's; the sum of products that cancel is exact);
 // only where that leaves the bf16 rounding open (two units around a tie: one
 // element in 13000) or a value is not finite, by rotate_bf16.
 // Rounding the plain fp32 formula instead would round about one element in 2^15
 // the other way than the exact value, and in a 4-bit cache change its code.
-__device__ __forceinline__ void rotate8(const uint64_t (&x)[4], const uint64_t (&y)[4],
-                                        const uint64_t (&c)[4], const uint64_t (&s)[4],
-                                        uint32_t (&out)[4]) {
+__device__ __forceinline__ void rotate4(const uint64_t (&x)[2], const uint64_t (&y)[2],
+                                        const uint64_t (&c)[2], const uint64_t (&s)[2],
+                                        float (&r1)[4], float (&r2)[4]) {
   const uint64_t minus = f2_pack(-1.f, -1.f), zero = f2_pack(0.f, 0.f);
-  uint32_t nearest = 0xffffffffu;   // of the even elements, of the odd ones
+  uint32_t nearest = 0xffffffffu;   // of the first of each two, of the second
   uint64_t finite = zero;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t h = f2_mul(y[i], s[i]);
-    const uint64_t e = f2_fma(y[i], s[i], f2_mul(h, minus));
-    const uint64_t r = f2_add(f2_fma(x[i], c[i], h), e);
+  const auto one = [&](uint64_t u, uint64_t w, uint64_t cs, uint64_t sn, uint64_t minus_sn,
+                       float& f0, float& f1) {   // u cs + w sn
+    const uint64_t e = f2_fma(w, sn, f2_mul(w, minus_sn));
+    const uint64_t r = f2_add(f2_fma(u, cs, f2_mul(w, sn)), e);
     finite = f2_fma(r, zero, finite);
-    float r0, r1;
-    f2_unpack(r, r0, r1);
+    f2_unpack(r, f0, f1);
     nearest = __viaddmin_u16x2(
-        __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x5410u), 0x80028002u, nearest);
-    out[i] = pack_bf16x2(r0, r1);
+        __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x5410u), 0x80028002u, nearest);
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t ms = f2_mul(s[i], minus);
+    one(x[i], y[i], c[i], ms, s[i], r1[2 * i], r1[2 * i + 1]);
+    one(y[i], x[i], c[i], s[i], ms, r2[2 * i], r2[2 * i + 1]);
   }
   float f0, f1;
   f2_unpack(finite, f0, f1);
   if ((nearest & 0xffffu) <= 4u || (nearest >> 16) <= 4u || f0 + f1 != 0.f) {
-    float v[4][8];   // copies: the arrays themselves stay in registers
-    uint32_t w[4];
+    float v[4][4], r[2][4];   // copies: the arrays themselves stay in registers
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       f2_unpack(x[i], v[0][2 * i], v[0][2 * i + 1]);
       f2_unpack(y[i], v[1][2 * i], v[1][2 * i + 1]);
       f2_unpack(c[i], v[2][2 * i], v[2][2 * i + 1]);
       f2_unpack(s[i], v[3][2 * i], v[3][2 * i + 1]);
     }
-    rotate8_exactly(v, w);
+    rotate4_exactly(v, r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = w[i];
+    for (int i = 0; i < 4; ++i) r1[i] = r[0][i], r2[i] = r[1][i];
   }
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// The rotation of this lane's 8 elements (chunk c of its row), in place;
-// every lane of the row takes part.  With pairs (d, d + rot / 2) the partner
-// chunk is another lane's, and cs, sn belong to the elements; with adjacent pairs
-// it is the lane's own, and they belong to its four pairs.
-template <int kLanes, bool kInterleaved>
-__device__ __forceinline__ void rotate_chunk(uint4& w, uint32_t row_mask, int c, int rot_chunks,
-                                             const uint64_t (&cs)[4], const uint64_t (&sn)[4]) {
-  const uint32_t own[4] = {w.x, w.y, w.z, w.w};
-  uint64_t x[4], y[4];
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = f2_pack(bf16_lo(own[i]), bf16_hi(own[i]));
-  if constexpr (kInterleaved) {   // (a cos - b sin, b cos + a sin)
-    uint64_t ci[4], si[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = f2_pack(-bf16_hi(own[i]), bf16_lo(own[i]));
-      float c0, c1, s0, s1;
-      f2_unpack(cs[i >> 1], c0, c1);
-      f2_unpack(sn[i >> 1], s0, s1);
-      ci[i] = (i & 1) ? f2_pack(c1, c1) : f2_pack(c0, c0);
-      si[i] = (i & 1) ? f2_pack(s1, s1) : f2_pack(s0, s0);
-    }
-    rotate8(x, y, ci, si, out);
+// The rotation of a lane's eight elements, w.x, w.y and w.z, w.w: four first
+// and four second elements of its pairs, or (interleaved) four adjacent pairs.
+template <bool kInterleaved>
+__device__ __forceinline__ void rotate_lane(uint4& w, const uint64_t (&cs)[2],
+                                            const uint64_t (&sn)[2]) {
+  uint64_t x[2], y[2];
+  float r1[4], r2[4];
+  if constexpr (kInterleaved) {
+    x[0] = f2_pack(bf16_lo(w.x), bf16_lo(w.y)), x[1] = f2_pack(bf16_lo(w.z), bf16_lo(w.w));
+    y[0] = f2_pack(bf16_hi(w.x), bf16_hi(w.y)), y[1] = f2_pack(bf16_hi(w.z), bf16_hi(w.w));
   } else {
-    const int half = rot_chunks >> 1;
-    const bool first = c < half;
-    const int partner = first ? c + half : c < rot_chunks ? c - half : c;
-    const uint32_t flip = first ? 0x80008000u : 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t o = __shfl_sync(row_mask, own[i], partner, kLanes) ^ flip;
-      y[i] = f2_pack(bf16_lo(o), bf16_hi(o));
-    }
-    rotate8(x, y, cs, sn, out);
+    x[0] = f2_pack(bf16_lo(w.x), bf16_hi(w.x)), x[1] = f2_pack(bf16_lo(w.y), bf16_hi(w.y));
+    y[0] = f2_pack(bf16_lo(w.z), bf16_hi(w.z)), y[1] = f2_pack(bf16_lo(w.w), bf16_hi(w.w));
   }
-  if (c < rot_chunks) w = make_uint4(out[0], out[1], out[2], out[3]);
+  rotate4(x, y, cs, sn, r1, r2);
+  w = kInterleaved ? make_uint4(pack_bf16x2(r1[0], r2[0]), pack_bf16x2(r1[1], r2[1]),
+                                pack_bf16x2(r1[2], r2[2]), pack_bf16x2(r1[3], r2[3]))
+                   : make_uint4(pack_bf16x2(r1[0], r1[1]), pack_bf16x2(r1[2], r1[3]),
+                                pack_bf16x2(r2[0], r2[1]), pack_bf16x2(r2[2], r2[3]));
 }
 
 // ---------------------------------------------------------------- 4 bits
@@ -233,15 +219,23 @@ __device__ __forceinline__ void store4(uint8_t* block, int r, int c, bool value,
 // ---------------------------------------------------------------- append
 
 // A token's vector of one head is a row that D / 8 neighbouring lanes hold, 8
-// elements each: one word of codes, a quarter of a scale's group.  A thread
-// block takes kSlots consecutive tokens, one to a row of lanes, and goes with all
-// of them through p.rows of their H_q queries, H_kv keys and H_kv values: what
-// belongs to the token (its page, its rotation's 8 cosines and sines a lane) is
+// elements each: side by side, or, where the lane rotates pairs (d, d + rot_dim /
+// 2), four from either side of its pairs (which takes no exchange between lanes
+// and half the cosines; a 4-bit key's lanes change to 8 consecutive elements
+// afterwards, one word of codes and a quarter of a scale's group, by way of
+// shared memory).  A thread block takes kSlots consecutive tokens, one to a row
+// of lanes, and goes with all of them through p.rows of their H_q queries, H_kv
+// keys and H_kv values: what belongs to the token (its page, its rotation) is
 // read once, and neighbouring tokens, which lie side by side in q_out and in the
 // cache, are written together.  The next rows are on their way while one is
-// worked on: bytes under way are what the kernel needs most (8192 tokens of 32 +
-// 8 heads of 128 into 4 bits, 177 MB: 54 us with one token to a block or two rows
-// ahead in registers, 44 us, 4.0 TB/s, with four ahead in shared memory).
+// worked on.
+//
+// Measured, 8192 tokens of 32 + 8 heads of 128 (device time): 4 bits, 181 MB,
+// 39 us, 4.6 TB/s (68 % of the measured HBM copy rate; 36 us with adjacent pairs),
+// bf16, 206 MB, 36.5 us, 5.6 TB/s (83 %).  Bound by the instructions of
+// rotation and quantisation together with the rows' latencies.  It took 54 us
+// with one token to a block or two rows ahead in registers, 44 with eight
+// neighbouring elements a lane throughout.
 template <int D, bool kInt4, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, 8)
     kv_append_kernel(const __grid_constant__ KvAppendParams p) {
@@ -263,23 +257,46 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
   const int k0 = min(max(r0 - p.H_q, 0), kc.H_kv), k1 = min(max(r1 - p.H_q, 0), kc.H_kv);
   const int v0 = min(max(r0 - p.H_q - kc.H_kv, 0), kc.H_kv);
   const int v1 = min(max(r1 - p.H_q - kc.H_kv, 0), kc.H_kv);
+  const int rot_lanes = p.rot_dim / 8;
+  const bool rotates = c < rot_lanes;
+  // the lane's elements lo .. lo + 3, hi .. hi + 3 of a query or a key
+  const bool apart = !kInterleaved && p.rot_dim > 0;   // (not in every lane, perhaps)
+  const int lo = apart && rotates ? 4 * c : 8 * c;
+  const int hi = apart && rotates ? p.rot_dim / 2 + 4 * c : 8 * c + 4;
+  const auto store = [&](uint16_t* row, const uint4& w, bool in_halves) {
+    if (in_halves) {
+      *reinterpret_cast<uint2*>(row + lo) = make_uint2(w.x, w.y);
+      *reinterpret_cast<uint2*>(row + hi) = make_uint2(w.z, w.w);
+    } else {
+      *reinterpret_cast<uint4*>(row + 8 * c) = w;
+    }
+  };
   const auto source = [&](const KvTensor& t, int h) {
-    return t.data + b * t.sb + i * t.ss + h * t.sh + 8 * c;
+    return t.data + b * t.sb + i * t.ss + h * t.sh;
   };
   // The rows in turn come by way of shared memory, kAhead of them requested in
   // advance; a lane takes what it requested itself.
   __shared__ uint4 ring[kAhead][kAppendThreads];
+  __shared__ uint4 regroup[kInt4 && !kInterleaved ? kAppendThreads : 1];
   int left = (q1 - q0) + (k1 - k0) + (v1 - v0), at = q1 - q0, kind = 0, put_in = 0, take_from = 0;
-  const uint16_t* src = source(p.q, q0);
+  const uint16_t* src = source(p.q, q0) + lo;
   long long step = p.q.sh;
+  bool halves = apart;
   const auto request = [&]() {
     if (left > 0) {
       while (at == 0) {   // on to the keys, then to the values
-        src = ++kind == 1 ? source(p.k, k0) : source(p.v, v0);
+        src = ++kind == 1 ? source(p.k, k0) + lo : source(p.v, v0) + 8 * c;
         step = kind == 1 ? p.k.sh : p.v.sh;
         at = kind == 1 ? k1 - k0 : v1 - v0;
+        halves = apart && kind == 1;
       }
-      copy_async16(&ring[put_in][threadIdx.x], src);
+      uint2* const dst = reinterpret_cast<uint2*>(&ring[put_in][threadIdx.x]);
+      if (halves) {
+        copy_async8(dst, src);
+        copy_async8(dst + 1, src + (hi - lo));
+      } else {
+        copy_async16(dst, src);
+      }
       src += step;
       --at;
       --left;
@@ -297,52 +314,54 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
 #pragma unroll 1
   for (int n = 0; n < kAhead; ++n) request();   // (needs neither position nor page)
   const long long pos = (long long)p.start[b] + i;
-  const int rot_chunks = p.rot_dim / 8;
   const bool good = pos >= 0 && pos < kc.capacity && (p.rot_dim == 0 || pos < p.rope_rows);
   const int page =
       good ? kc.table[(long long)b * kc.max_blocks + (int)pos / kc.page_size] : -1;
-  uint64_t cs[4] = {}, sn[4] = {};   // pairs of cosines and of sines
-  if (good && c < rot_chunks) {
-    const long long at = pos * (p.rot_dim / 2) +
-                         (kInterleaved ? 4 * c : 8 * (c < rot_chunks / 2 ? c : c - rot_chunks / 2));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && kInterleaved) break;
-      const float4 a = *reinterpret_cast<const float4*>(p.cos + at + 4 * h);
-      const float4 d = *reinterpret_cast<const float4*>(p.sin + at + 4 * h);
-      cs[2 * h] = f2_pack(a.x, a.y), cs[2 * h + 1] = f2_pack(a.z, a.w);
-      sn[2 * h] = f2_pack(d.x, d.y), sn[2 * h + 1] = f2_pack(d.z, d.w);
-    }
+  uint64_t cs[2] = {}, sn[2] = {};   // cosines and sines of the lane's pairs
+  if (good && rotates) {
+    const long long at = pos * (p.rot_dim / 2) + 4 * c;
+    const float4 a = *reinterpret_cast<const float4*>(p.cos + at);
+    const float4 d = *reinterpret_cast<const float4*>(p.sin + at);
+    cs[0] = f2_pack(a.x, a.y), cs[1] = f2_pack(a.z, a.w);
+    sn[0] = f2_pack(d.x, d.y), sn[1] = f2_pack(d.z, d.w);
   }
   if ((unsigned)page >= (unsigned)kc.num_pages) {
     g_kv_status = ATTN_ERR_BAD_INDEX;
+    copy_async_wait<0>();
     return;
   }
   const int slot = (int)pos % kc.page_size;
-  uint16_t* q_dst = p.q_out + (((long long)b * p.H_q + q0) * p.S + i) * D + 8 * c;
+  uint16_t* q_dst = p.q_out + (((long long)b * p.H_q + q0) * p.S + i) * D;
   const long long q_dst_step = (long long)p.S * D;
 #pragma unroll 1
   for (int h = q0; h < q1; ++h) {
     uint4 w = take();
-    if (rot_chunks) rotate_chunk<kLanes, kInterleaved>(w, row_mask, c, rot_chunks, cs, sn);
-    *reinterpret_cast<uint4*>(q_dst) = w;
+    if (rotates) rotate_lane<kInterleaved>(w, cs, sn);
+    store(q_dst, w, apart);
     q_dst += q_dst_step;
   }
   const long long head_bytes = (long long)kc.blocks_per_page * kKvBlockBytes<D, kInt4>;
-  const auto put = [&](uint8_t* block, const uint4& w, bool value) {
+  const auto put = [&](uint8_t* block, uint4 w, bool value) {
     if constexpr (kInt4) {
+      if (apart && !value) {   // to 8 consecutive elements a lane
+        uint4* const row = regroup + (threadIdx.x - c);
+        store(reinterpret_cast<uint16_t*>(row), w, true);
+        __syncwarp(row_mask);
+        w = row[c];
+        __syncwarp(row_mask);
+      }
       uint32_t scale;
       const uint32_t codes = quantise8(w, row_mask, scale);
       store4<D>(block, slot & 15, c, value, codes, scale);
     } else {
-      *reinterpret_cast<uint4*>(block + (slot & 15) * D * 2 + 16 * c) = w;
+      store(reinterpret_cast<uint16_t*>(block) + (slot & 15) * D, w, apart && !value);
     }
   };
   uint8_t* dst = const_cast<uint8_t*>(kc.k) + kv_block_offset<D, kInt4>(kc, page, k0, slot >> 4);
 #pragma unroll 1
   for (int h = k0; h < k1; ++h) {
     uint4 w = take();
-    if (rot_chunks) rotate_chunk<kLanes, kInterleaved>(w, row_mask, c, rot_chunks, cs, sn);
+    if (rotates) rotate_lane<kInterleaved>(w, cs, sn);
     put(dst, w, false);
     dst += head_bytes;
   }
@@ -457,7 +476,8 @@ cudaError_t launch_kv_append(const KvAppendParams& p0, int D, bool int4, cudaStr
   const int slots = kAppendThreads / (D / 8);
   const int rows = p.H_q + 2 * p.cache.H_kv;
   const long long blocks = ((long long)p.cache.B * p.S + slots - 1) / slots;
-  // where there are few tokens, their rows are spread over several blocks
+  // Where there are few tokens, their rows are spread over several blocks (1024
+  // blocks of tokens, 48 rows: cut in five 39 us, in three 41, in ten 45)
   const long long spread = (kAppendBlocks + blocks - 1) / blocks;
   p.rows = spread >= rows ? 1 : (int)((rows + spread - 1) / spread);
   const dim3 grid((unsigned)blocks, (unsigned)((rows + p.rows - 1) / p.rows));
