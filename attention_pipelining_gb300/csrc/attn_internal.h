@@ -184,12 +184,13 @@ struct PagedParams {
   // workspace, of the n CTAs there may be where items are split:
   float* part_o;         // [2 n, rows, D]
   float* part_lse;       // [2 n, rows], base 2
-  int4* shared;          // [n], the item that CTA c began and did not finish: {sequence (-1:
-                         // none), head and row tile, slot of its first part, last CTA that has
-                         // a part}
+  int4* shared;          // [n], the item that CTA c began and did not finish, or by_item: item
+                         // c: {item (-1: none, or whole), the CTA that began it, slot of its
+                         // first part, last CTA that has a part}
   int H_q, S_q, group;   // group = H_q / H_kv
   int row_tiles;         // ceil(group * S_q / rows) (set at launch)
   int unit, split;       // keys per unit of work, and whether items are split (set at launch)
+  int ctas, by_item;     // CTAs, and whether `shared` goes by items (set at launch)
   int causal;
   float scale_log2;
   uint32_t code_base_low, code_base_high;  // fp16 pairs of 1024 and 64 (see the kernel)

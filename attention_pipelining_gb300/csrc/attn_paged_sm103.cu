@@ -40,8 +40,9 @@
 // of 8192 keys, bf16, 1.07 GB: 163 us, 6.6 TB/s, 97 % of the measured HBM copy
 // rate; 4 bits, 303 MB: 67 us, 4.5 TB/s (66 %), of which the instructions, 650
 // for 32 keys and a warp, about half of them masks, packed subtractions and scales,
-// keep the issue slots 75 % busy; 131072 keys of one sequence, 4 bits: 41 us
-// (55 %), of which 12 us are the two launches, the first loads and the merges.
+// keep the issue slots 75 % busy; 131072 keys of one sequence, 4 bits: 37.5 us
+// (60 %).  About 10 us of a call are the beginning (plan, page table and first keys, one
+// after the other: 5 us) and the end (the warps' merge, the CTAs' merge: 5 us).
 #include <atomic>
 #include <cfloat>
 #include <cmath>
@@ -60,8 +61,8 @@ namespace {
 
 constexpr int kPlanWarps = 4;              // warps that sum up the sequences' weights
 constexpr int kPlanThreads = kPlanWarps * 32;
-constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 2;              // rows of a block of the merge kernel
+constexpr int kMergeWarps = 8;
+constexpr int kManyParts = 8;              // of an item, on average: more warps for its rows
 constexpr int kItemCost = kPagedItemCost;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kPgBar = 1;             // named barrier of the consumer warps
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
   const int g = lane >> 2, t = lane & 3;
   const int HR = p.cache.H_kv * p.row_tiles;
 
-  allow_later();   // the merge kernel may be made ready
+  if (p.split) allow_later();   // the merge kernel may be made ready
   if (threadIdx.x < S::kStages) {
     mbar_init(&full[threadIdx.x], 1);
     mbar_init(&empty[threadIdx.x], CW);
@@ -817,9 +818,9 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
   wait_for_earlier();
   if (threadIdx.x == 0) {
     sm_abort = 0;
-    if (p.split) p.shared[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (p.split && !p.by_item) p.shared[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
-  const Deal deal(make_plan(p, plan) * HR, gridDim.x);   // (synchronises the thread block)
+  const Deal deal(make_plan(p, plan) * HR, gridDim.x);   // (a barrier within)
   if (blockIdx.x >= deal.G) return;
   Segments seg;
   if (!seg.begin(p, plan, deal, HR)) return;
@@ -926,9 +927,10 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
     // a CTA has at most one item that it goes on with and one that goes on
     // after it
     const int slot = 2 * blockIdx.x + (seg.unit == 0 ? 1 : 0);
-    if (seg.unit == 0 && !whole && threadIdx.x == 0)
-      p.shared[blockIdx.x] =
-          make_int4(b, seg.hr, slot, deal.owner(seg.first_position() + seg.units - 1));
+    if (seg.unit == 0 && threadIdx.x == 0 && (!whole || p.by_item))
+      p.shared[p.by_item ? b * HR + seg.hr : blockIdx.x] = make_int4(
+          whole ? -1 : b * HR + seg.hr, blockIdx.x, slot,
+          whole ? 0 : deal.owner(seg.first_position() + seg.units - 1));
     const int n_q = query_count(p, b);
     for (int x = threadIdx.x; x < ROWS * (D / 4); x += S::kThreads) {
       const int row = x / (D / 4), d = 4 * (x % (D / 4));
@@ -966,81 +968,103 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
 }
 
 // Merges the parts of items that several CTAs share: O = sum_c w_c O_c with
-// w_c = 2^(lse_c - lse), lse = log2 sum_c 2^lse_c.  Thread blocks (c, y)
-// merge the item that CTA c began and did not finish, if there is one
-// (p.shared[c]), kMergeRows rows each; a row's warps take turns at its parts.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kMergeThreads)
+// w_c = 2^(lse_c - lse), lse = log2 sum_c 2^lse_c.  Thread blocks (x, y) merge the
+// item that p.shared[x] tells of, if it does: kMergeWarps / kPer rows each, whose
+// kPer warps take turns at the parts.  A chain of waits (for the kernel before, the
+// entry, the parts, 2.5 to 4 us in all) that moves little data: a warp asks for
+// several parts at a time, and where there are many, as few blocks as possible
+// come and all of their warps share a row's (8 items of 57 parts: the call takes
+// 37.4 us, against 41.0 with blocks for all CTAs and four warps a row).
+template <int D, int ROWS, int kPer>
+__global__ void __launch_bounds__(32 * kMergeWarps)
     paged_merge_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int kWarps = kMergeThreads / 32;
-  constexpr int kRows = kMergeRows;                      // of a block
-  constexpr int kPer = kWarps / kRows;                   // warps a row
+  constexpr int kRows = kMergeWarps / kPer;
+  constexpr int kBatch = kPer > 1 ? 8 : 4;               // parts that a warp loads together
   constexpr int E = D / 32;                              // elements a lane
-  __shared__ float sm_acc[kWarps][D], sm_sum[kWarps];
-  allow_later();
+  __shared__ float sm_acc[kPer > 1 ? kMergeWarps : 1][D], sm_sum[kMergeWarps], sm_max[kMergeWarps];
   wait_for_earlier();
   const int4 it = p.shared[blockIdx.x];
-  if (it.x < 0) return;
-  const int b = it.x, hr = it.y, c0 = blockIdx.x, parts = it.w - c0 + 1;
+  const int HR = p.cache.H_kv * p.row_tiles, c0 = it.y, parts = it.w - c0 + 1;
+  // (an entry is never written where a wait ran out: anything may be there)
+  if ((unsigned)it.x >= (unsigned)(p.cache.B * HR) || (unsigned)c0 >= (unsigned)p.ctas ||
+      (unsigned)it.w >= (unsigned)p.ctas || (unsigned)(it.z - 2 * c0) > 1u)
+    return;
+  const int b = it.x / HR, hr = it.x % HR;
   const int h = hr / p.row_tiles, rt = hr % p.row_tiles;
-  const int n_q = p.q_lens ? p.q_lens[b] : p.S_q;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  {
-    const int row = blockIdx.y * kRows + warp / kPer, share = warp % kPer;
-    const int rho = rt * ROWS + row;
-    const bool live = rho < p.group * p.S_q && rho % p.S_q < n_q;
-    const auto at = [&](int c) {   // part c's place in the workspace
-      return (long long)(c == 0 ? it.z : 2 * (c0 + c)) * ROWS + row;
-    };
-    float mx = -INFINITY, sum = 0.f, acc[E];
+  const int row = blockIdx.y * kRows + warp / kPer, share = warp % kPer;
+  const int rho = rt * ROWS + row;
+  const bool live = rho < p.group * p.S_q && rho % p.S_q < query_count(p, b);
+  float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (live) {
-      for (int c = lane; c < parts; c += 32) mx = fmaxf(mx, p.part_lse[at(c)]);
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  // adds 2^(l - base) of (s, v) to the sums
+  const auto add = [&](float l, float base, float s, const float (&v)[E]) {
+    const float f = ex2_approx(l - base);
+    sum = fmaf(f, s, sum);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-      if (mx == -INFINITY) mx = 0.f;   // no part sees a key, or all are NaN
-#pragma unroll 8
-      for (int c = share; c < parts; c += kPer) {
-        const float f = ex2_approx(p.part_lse[at(c)] - mx);
-        float v[E];
-        const float* src = p.part_o + at(c) * D + lane * E;
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+  };
+  const auto finite = [](float m) { return m == -INFINITY ? 0.f : m; };   // (no part sees a key)
+  const auto rescale = [&](float next) {
+    const float f = ex2_approx(mx - finite(next));
+    sum *= f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+    mx = next;
+  };
+  if (live) {
+    for (int c = share; c < parts; c += kPer * kBatch) {
+      float l[kBatch], v[kBatch][E], next = mx;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int part = c + i * kPer;
+        const long long at =   // its place in the workspace
+            (long long)(part == 0 ? it.z : 2 * (c0 + part)) * ROWS + row;
+        const bool there = part < parts;
+        l[i] = there ? p.part_lse[at] : -INFINITY;
+        const float* src = p.part_o + at * D + lane * E;
         if constexpr (E == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+          const float4 x = there ? *reinterpret_cast<const float4*>(src) : make_float4(0, 0, 0, 0);
+          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
         } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          v[0] = x.x, v[1] = x.y;
-        }
-        sum += f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * v[e];
-      }
-    }
-    if constexpr (kPer > 1) {   // join the row's warps
-#pragma unroll
-      for (int e = 0; e < E; ++e) sm_acc[warp][lane * E + e] = acc[e];
-      if (lane == 0) sm_sum[warp] = sum;
-      __syncthreads();
-      if (share == 0) {
-#pragma unroll
-        for (int i = 1; i < kPer; ++i) {
-          sum += sm_sum[warp + i];
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += sm_acc[warp + i][lane * E + e];
+          const float2 x = there ? *reinterpret_cast<const float2*>(src) : make_float2(0, 0);
+          v[i][0] = x.x, v[i][1] = x.y;
         }
       }
-    }
-    if (live && share == 0) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const long long out = (long long)b * p.H_q * p.S_q + (long long)h * p.group * p.S_q + rho;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + out * D + lane * E);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-      if (lane == 0)
-        p.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+      for (int i = 0; i < kBatch; ++i) next = fmaxf(next, l[i]);
+      rescale(next);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) add(l[i], finite(mx), 1.f, v[i]);
     }
   }
+  if constexpr (kPer > 1) {   // join the row's warps
+#pragma unroll
+    for (int e = 0; e < E; ++e) sm_acc[warp][lane * E + e] = acc[e];
+    if (lane == 0) sm_sum[warp] = sum, sm_max[warp] = mx;
+    __syncthreads();
+    if (share > 0) return;
+    float next = mx;
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) next = fmaxf(next, sm_max[warp + i]);
+    rescale(next);
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) {
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = sm_acc[warp + i][lane * E + e];
+      add(sm_max[warp + i], finite(mx), sm_sum[warp + i], v);
+    }
+  }
+  if (!live) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const long long out = (long long)b * p.H_q * p.S_q + (long long)h * p.group * p.S_q + rho;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + out * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0)
+    p.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, bool kInt4, int WR, int RS, int CW>
@@ -1080,10 +1104,20 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
   while (items * ((p.cache.capacity + p.unit - 1) / p.unit + kItemCost) >= (1ll << 31)) p.unit *= 2;
   const long long most = items * ((p.cache.capacity + p.unit - 1) / p.unit);
   if (ctas > most) ctas = most;
+  p.ctas = (int)ctas;
+  p.by_item = split && items * kManyParts <= ctas;
   e = launch_ahead(kernel, dim3((unsigned)ctas), S::kThreads + 32, S::kBytes, stream, p);
   if (e != cudaSuccess || !split) return e;
-  return launch_ahead(paged_merge_kernel<D, S::kRows>,
-                      dim3((unsigned)ctas, S::kRows / kMergeRows), kMergeThreads, 0, stream, p);
+  const long long rows = (long long)p.group * p.S_q;
+  const unsigned live = (unsigned)(rows < S::kRows ? rows : S::kRows);   // of a tile
+  // Few items of many parts each: a block for every item and row, whose warps share the
+  // parts; else a block for every CTA's item and eight rows, a row to a warp
+  if (p.by_item)
+    return launch_ahead(paged_merge_kernel<D, S::kRows, kMergeWarps>, dim3((unsigned)items, live),
+                        32 * kMergeWarps, 0, stream, p);
+  return launch_ahead(paged_merge_kernel<D, S::kRows, 1>,
+                      dim3((unsigned)ctas, (live + kMergeWarps - 1) / kMergeWarps),
+                      32 * kMergeWarps, 0, stream, p);
 }
 
 template <int D, bool kInt4>

@@ -170,14 +170,14 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& w, uint32_t row_mask,
   uint32_t u[8];
   if (s >= 1.0e-30f) {
     const float inv = __frcp_rn(s);
+    // 6144 + q has steps of 2^-11; with 1.5 * 2^23 + 8 - 6144 more it has steps of
+    // 1, and its last bits are rint(q) + 8, ties to even
     const uint64_t inv2 = f2_pack(inv, inv), grid = f2_pack(6144.f, 6144.f);
-    const uint64_t back = f2_pack(-6144.f, -6144.f);
-    // 1.5 * 2^23 + 8: the sum's last bits are rint(q) + 8, ties to even
-    const uint64_t whole = f2_pack(12582920.f, 12582920.f);
+    const uint64_t whole = f2_pack(12576776.f, 12576776.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint64_t q = f2_mul(f2_pack(bf16_lo(x[i]), bf16_hi(x[i])), inv2);
-      q = f2_add(f2_add(f2_add(q, grid), back), whole);   // by way of a multiple of 2^-11
+      const uint64_t q =
+          f2_add(f2_fma(f2_pack(bf16_lo(x[i]), bf16_hi(x[i])), inv2, grid), whole);
       float q0, q1;
       f2_unpack(q, q0, q1);
       u[2 * i] = __float_as_uint(q0);
@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
   const KvCache& kc = p.cache;
   const int c = threadIdx.x % kLanes;
   const uint32_t row_mask = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
-  allow_later();
   wait_for_earlier();
   const uint32_t token = blockIdx.x * kSlots + threadIdx.x / kLanes;
   if (token >= (uint32_t)(kc.B * p.S)) return;
@@ -382,7 +381,6 @@ template <int D, bool kInt4>
 __global__ void __launch_bounds__(kKvThreads)
     kv_read_kernel(const __grid_constant__ KvReadParams p) {
   const KvCache& kc = p.cache;
-  allow_later();
   wait_for_earlier();
   const int lane = threadIdx.x & 31;
   const bool value = blockIdx.y & 1;
