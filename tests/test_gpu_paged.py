@@ -525,6 +525,46 @@ def test_quantisation_of_every_ratio():
         assert np.array_equal(nib, code[t]), t
 
 
+MERGE = [
+    # fmt, D, H_q, H_kv, S_q, lens, causal, q_lens: few items of many parts, down to one part
+    ("int4", 128, 4, 1, 1, [9000], True, None),
+    ("int4", 64, 8, 2, 5, [6000, 0, 130], True, [5, 5, 2]),
+    ("int4", 128, 2, 2, 1, [1, 7001], False, None),
+    ("bf16", 128, 6, 1, 9, [8000, 40], True, [9, 0]),
+    ("bf16", 64, 1, 1, 100, [5000], True, None),
+    ("bf16", 128, 3, 3, 1, [4097], False, None),
+    # many items, two or three parts each
+    ("int4", 128, 16, 16, 2, [1200, 900, 1, 1090, 0], True, [2, 1, 1, 2, 2]),
+    ("bf16", 64, 40, 20, 1, [1100, 1300, 1290, 7], False, None),
+]
+
+
+@pytest.mark.parametrize("case", MERGE, ids=[str(c) for c in MERGE])
+def test_parts_of_items(case):
+    """Items on one to hundreds of thread blocks; a workspace full of NaN and of every bit set;
+    rows of padding stay as they were."""
+    fmt, D, Hq, H, Sq, lens, causal, q_lens = case
+    B, page = len(lens), 64
+    bt, pages = tables([max(n, 1) for n in lens], page, 91)
+    kc, vc = pools(fmt, pages, H, page, D, 92)
+    q = randn(rng(93), B, Hq, Sq, D)
+    n = ap.paged_workspace_bytes(B, Hq, H, Sq, D, bt.shape[1] * page)
+    results = []
+    for fill_with in (0xff, 0x7f):
+        ws = torch.full((n,), fill_with, dtype=torch.uint8).cuda()
+        out = (torch.full((B, Hq, Sq, D), 3.0, dtype=torch.bfloat16).cuda(),
+               torch.full((B, Hq, Sq), 3.0).cuda())
+        got = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(*lens), causal,
+                                0.3, q_lens=device_ints(*q_lens) if q_lens else None, workspace=ws,
+                                out=out)
+        torch.cuda.synchronize()
+        results.append([x.cpu() for x in got])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    check_attention(q, kc, vc, bt, lens, causal, 0.3, results[0], q_lens, what=str(case))
+    for b in range(B if q_lens else 0):
+        assert (results[0][0][b, :, q_lens[b]:] == 3).all() and (results[0][1][b, :, q_lens[b]:] == 3).all()
+
+
 # ---------------------------------------------------------------- together, as used
 
 
