@@ -189,7 +189,8 @@ struct PagedParams {
                          // first part, last CTA that has a part}
   int H_q, S_q, group;   // group = H_q / H_kv
   int row_tiles;         // ceil(group * S_q / rows) (set at launch)
-  int unit, split;       // keys per unit of work, and whether items are split (set at launch)
+  int unit, item_cost;   // keys per unit of work, units an item counts for apart from its own,
+  int split;             // and whether items are split (set at launch)
   int ctas, by_item;     // CTAs, and whether `shared` goes by items (set at launch)
   int causal;
   float scale_log2;
@@ -200,10 +201,11 @@ struct PagedParams {
   int fault_drop_stage;
 };
 
-// Keys per unit of the paged attention's work, and up to how many keys (of the
-// block tables' span) an item is kept whole; and its CTAs, at most.
-constexpr int kPagedUnit = 128;
-constexpr int kPagedItemCost = 2;  // units that an item's beginning and end count for
+// Keys per unit of the paged attention's work, at least; keys that an item's beginning
+// and end count for; up to how many keys (of the block tables' span) an item is kept
+// whole; and its CTAs, at most.
+constexpr int kPagedUnit = 64;
+constexpr int kPagedItemKeys = 256;
 constexpr int kPagedWholeKeys = 1024;
 constexpr int kPagedMaxCtas = 512;
 constexpr int kPagedFewItems = 152;   // items that have an SM each

@@ -85,7 +85,8 @@ attn_status_t check_rows(int B, int H_q, int H_kv, int S_q) {
   if (rows >= (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
   // items, with what each counts for apart from its keys, are counted in an int
   const int tile = tile_rows(H_q / H_kv, S_q);
-  if (((rows + tile - 1) / tile) * H_kv * B * (kPagedItemCost + 1) >= (1ll << 31))
+  if (((rows + tile - 1) / tile) * H_kv * B * (kPagedItemKeys / kPagedUnit + 1) >=
+      (1ll << 31))
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }

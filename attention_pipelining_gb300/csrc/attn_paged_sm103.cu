@@ -31,8 +31,8 @@
 // ring of stages, with one asynchronous copy per 16-key block of K and of V, each
 // requested by its own lane.
 //
-// Work is dealt out evenly to the CTAs in units of kPagedUnit keys of one sequence,
-// KV head and tile of query rows (see Deal).  An item (the units of one sequence,
+// Work is dealt out evenly to the CTAs in units of 128 keys (64 of a bf16 cache) of one
+// sequence, KV head and tile of query rows (see Deal).  An item (the units of one sequence,
 // head and row tile) that lies within one CTA's range is finished there; otherwise
 // each CTA writes its part to the workspace and paged_merge_kernel merges them.
 //
@@ -63,7 +63,6 @@ constexpr int kPlanWarps = 4;              // warps that sum up the sequences' w
 constexpr int kPlanThreads = kPlanWarps * 32;
 constexpr int kMergeWarps = 8;
 constexpr int kManyParts = 8;              // of an item, on average: more warps for its rows
-constexpr int kItemCost = kPagedItemCost;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kPgBar = 1;             // named barrier of the consumer warps
 // The reference of a row's exponentials starts below every finite score, and
@@ -98,11 +97,12 @@ __device__ __forceinline__ int units_of(const PagedParams& p, int len) {
   return len <= p.unit ? 1 : (len + p.unit - 1) / p.unit;
 }
 
-// An item weighs its units and kItemCost more, about what the beginning and
-// the end of an item take: the positions 0 .. U - 1 of all items' weights, sequence by
+// An item weighs its units and p.item_cost more, about what the beginning and
+// the end of an item take (64 ragged sequences, 4 bits, with 1, 2 and 4 units of 128 keys:
+// 24.7, 22.1, 24.3 us): the positions 0 .. U - 1 of all items' weights, sequence by
 // sequence and within it item by item, are dealt out to G CTAs in even
-// consecutive ranges.  The first kItemCost positions of an item do nothing: its
-// unit k is position kItemCost + k.
+// consecutive ranges.  The first p.item_cost positions of an item do
+// nothing: its unit k is position p.item_cost + k.
 struct Deal {
   int U, G, q, r;   // CTA c has q positions, or q + 1 where c < r
   __device__ __forceinline__ Deal(int U_, int launched) : U(U_) {
@@ -132,7 +132,7 @@ __device__ __forceinline__ int make_plan(const PagedParams& p, Plan& plan) {
     const int b0 = threadIdx.x * per;
     int sum = 0;
     for (int i = 0; i < per; ++i)
-      if (b0 + i < p.cache.B) sum += kItemCost + units_of(p, clamp_len(p, b0 + i));
+      if (b0 + i < p.cache.B) sum += p.item_cost + units_of(p, clamp_len(p, b0 + i));
     int incl = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -168,7 +168,7 @@ __device__ __forceinline__ int find_sequence(const PagedParams& p, const Plan& p
   const int per = (p.cache.B + kPlanThreads - 1) / kPlanThreads;
   int b = min((w * 32 + lane) * per, p.cache.B - 1);
   for (; b + 1 < p.cache.B; ++b) {
-    const int n = kItemCost + units_of(p, clamp_len(p, b));
+    const int n = p.item_cost + units_of(p, clamp_len(p, b));
     if (before + n > v) break;
     before += n;
   }
@@ -631,14 +631,16 @@ struct Shape {
   static constexpr int kStage = kCopies * kBlock;
   static constexpr int kStages =
       CW == 8 ? 2 : kInt4 || (D == 128 && WR == 8) ? 3 : D == 128 ? 2 : 3;
-  static constexpr int kUnit = CW == 8 ? 2 * kPagedUnit : kPagedUnit;   // whole stages
+  // whole stages (bf16: 8 ragged sequences with 5 queries 23.3 us with units of 64 keys, 24.7
+  // with 128)
+  static constexpr int kUnit = 16 * kBlocks;
   static constexpr int kPitch = D + 4;                // floats a row, against bank conflicts
   static constexpr int kSlots = kGroups > 1 ? kGroups / 2 : 1;
   static constexpr int kMerge = kSlots * kRows * kPitch * 4;
   static constexpr int kBytes = kStages * kStage + kMerge + 1024;
   // thread blocks per SM
   static constexpr int kCtas = CW == 8 ? 1 : WR == 8 && (kInt4 || D == 64) ? 3 : 2;
-  static_assert(kCopies <= 32 && kMine % NB == 0 && kUnit % (16 * kBlocks) == 0, "stage");
+  static_assert(kCopies <= 32 && kMine % NB == 0 && kUnit >= kPagedUnit, "stage");
 };
 
 // A thread block's share of the work, segment by segment (consecutive units
@@ -650,20 +652,22 @@ struct Segments {
   int x, x1;            // positions left
   int b, len, units, hr;
   int unit, n;          // of the current segment: its first unit and their number
+  int cost;             // p.item_cost
   bool bad;
 
   // The first segment; false if there is none.  Whole warps.
   __device__ __forceinline__ bool begin(const PagedParams& p, const Plan& plan, const Deal& deal,
                                         int HR) {
+    cost = p.item_cost;
     x = deal.start(blockIdx.x);
     x1 = deal.start(blockIdx.x + 1);
     int before;
     b = find_sequence(p, plan, x / HR, before);
     take_sequence(p);
-    const int local = x - before * HR, weight = units + kItemCost;
+    const int local = x - before * HR, weight = units + cost;
     hr = min(local / weight, HR - 1);
     x = before * HR + hr * weight;   // of the item
-    unit = max(0, local - hr * weight - kItemCost);
+    unit = max(0, local - hr * weight - cost);
     return fit();
   }
   __device__ __forceinline__ void take_sequence(const PagedParams& p) {
@@ -673,11 +677,11 @@ struct Segments {
   }
   // How much of the item from `unit` on is this CTA's
   __device__ __forceinline__ bool fit() {
-    n = min(units, x1 - x - kItemCost) - unit;
+    n = min(units, x1 - x - cost) - unit;
     return n > 0;
   }
   __device__ __forceinline__ bool next(const PagedParams& p, int HR) {
-    x += units + kItemCost;
+    x += units + cost;
     if (x >= x1) return false;
     unit = 0;
     if (++hr == HR) {
@@ -688,7 +692,7 @@ struct Segments {
     return fit();
   }
   // The position of the item's first unit
-  __device__ __forceinline__ int first_position() const { return x + kItemCost; }
+  __device__ __forceinline__ int first_position() const { return x + cost; }
 };
 
 // Keys that some query row of a tile may see: all of the sequence's, but in
@@ -1098,10 +1102,12 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
   // and one launch instead of two)
   const bool split = p.cache.capacity > kPagedWholeKeys;
   p.split = split;
+  p.item_cost = kPagedItemKeys / S::kUnit;
   p.unit = split ? S::kUnit : (p.cache.capacity + S::kUnit - 1) / S::kUnit * S::kUnit;
   const long long items = (long long)p.cache.B * p.cache.H_kv * p.row_tiles;
   // positions are counted in an int: larger units where there could be too many
-  while (items * ((p.cache.capacity + p.unit - 1) / p.unit + kItemCost) >= (1ll << 31)) p.unit *= 2;
+  while (items * ((p.cache.capacity + p.unit - 1) / p.unit + p.item_cost) >= (1ll << 31))
+    p.unit *= 2;
   const long long most = items * ((p.cache.capacity + p.unit - 1) / p.unit);
   if (ctas > most) ctas = most;
   p.ctas = (int)ctas;

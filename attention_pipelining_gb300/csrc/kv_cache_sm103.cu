@@ -21,6 +21,7 @@ namespace {
 constexpr int kKvThreads = 256;         // of the read kernel
 constexpr int kAppendThreads = 128;
 constexpr int kAhead = 3;               // rows of a thread under way in the append kernel
+constexpr int kFewTokens = 8;           // of a sequence, in a decoding step
 constexpr int kAppendBlocks = 4864;     // 32 blocks on each of 152 SMs, in four rounds
 
 // 16 and 8 bytes to shared memory, asynchronously, in the thread's open group.
@@ -244,6 +245,9 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
   const KvCache& kc = p.cache;
   const int c = threadIdx.x % kLanes;
   const uint32_t row_mask = ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
+  // (prompts: 8 ragged ones of up to 1021 tokens 11.8 us, against 12.8; where few
+  // tokens are appended, the attention over them comes next: see allow_later)
+  if (p.S > kFewTokens) allow_later();
   wait_for_earlier();
   const uint32_t token = blockIdx.x * kSlots + threadIdx.x / kLanes;
   if (token >= (uint32_t)(kc.B * p.S)) return;

@@ -129,8 +129,8 @@ attn_status_t attn_kv_read(const attn_kv_cache_t *cache, void *k_out, void *v_ou
  *              attn_paged_workspace_bytes(...) bytes; need not be cleared; not
  *              shared with calls that may run at the same time
  *
- * Where the block table spans more than 1024 keys, the work (units of 128 keys of all
- * sequences) is dealt out evenly to a grid that fills the GPU, whatever the
+ * Where the block table spans more than 1024 keys, the work (units of 64 or 128 keys of
+ * all sequences) is dealt out evenly to a grid that fills the GPU, whatever the
  * lengths; a sequence that ends up on more than one thread block is merged by a
  * second kernel.  Meant for decoding, where S_q is one or a few tokens: each
  * (H_q / H_kv) * S_q <= 64 query rows of a KV head read the cache once, and more

@@ -126,7 +126,7 @@ def test_strides_of_single_dimensions_are_not_looked_at(lib):
 
 def test_workspace_bytes(lib):
     """Two parts of each of at most 512 thread blocks, D + 1 floats a row of the tile, and 16
-    bytes a thread block; one block a unit of 128 keys where there are fewer units; next to
+    bytes a thread block; one block a unit of 64 keys where there are fewer units; next to
     nothing where the block tables span no more keys than an item is kept whole for."""
     f = lib.attn_paged_workspace_bytes
     for H_q, H_kv, S_q, rows in ((8, 1, 1, 8), (9, 1, 1, 16), (32, 8, 1, 8), (32, 8, 4, 16),
@@ -134,7 +134,7 @@ def test_workspace_bytes(lib):
         for D in (64, 128):
             assert f(300, H_q, H_kv, S_q, D, 4096) == 512 * (2 * rows * (D + 1) * 4 + 16)
             assert f(300, H_q, H_kv, S_q, D, 1024) == 256
-    assert f(2, 8, 2, 1, 64, 1025) == 2 * 2 * 9 * (2 * 8 * 65 * 4 + 16)
+    assert f(2, 8, 2, 1, 64, 1025) == 2 * 2 * 17 * (2 * 8 * 65 * 4 + 16)
     for bad in ((0, 8, 1, 1, 64, 9), (1, 8, 3, 1, 64, 9), (1, 8, 1, 0, 64, 9), (1, 8, 1, 1, 96, 9),
                 (1, 8, 1, 1, 64, 0)):
         assert f(*bad) == 0
