@@ -38,9 +38,9 @@
 //
 // Measured (device time, D = 128, 32 query heads over 8 KV heads): 32 sequences
 // of 8192 keys, bf16, 1.07 GB: 163 us, 6.6 TB/s, 97 % of the measured HBM copy
-// rate; 4 bits, 303 MB: 67 us, 4.5 TB/s (66 %), of which the instructions, 650
-// for 32 keys and a warp, about half of them masks, packed subtractions and scales,
-// keep the issue slots 75 % busy; 131072 keys of one sequence, 4 bits: 37.5 us
+// rate; 4 bits, 303 MB: 67 us, 4.5 TB/s (66 %), with 340 warp-instructions for 16
+// keys, about half of them masks, packed subtractions and scales, that keep 60 % of the
+// issue slots busy; 131072 keys of one sequence, 4 bits: 37.5 us
 // (60 %).  About 10 us of a call are the beginning (plan, page table and first keys, one
 // after the other: 5 us) and the end (the warps' merge, the CTAs' merge: 5 us).
 #include <atomic>

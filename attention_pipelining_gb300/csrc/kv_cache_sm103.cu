@@ -3,7 +3,7 @@
 //
 // Both kernels stream.  6.8 TB/s of 4 bytes an element (bf16 read and written)
 // leave each SM 22 thread-instructions an element, of 2.6 bytes (a 4-bit write)
-// 14: the rotation takes about 12 and the quantisation 8, loads and stores included.
+// 14: an append into 4 bits runs 22 on average.
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
