@@ -38,9 +38,9 @@
 //
 // Measured (device time, D = 128, 32 query heads over 8 KV heads): 32 sequences
 // of 8192 keys, bf16, 1.07 GB: 163 us, 6.6 TB/s, 97 % of the measured HBM copy
-// rate; 4 bits, 303 MB: 67 us, 4.5 TB/s (66 %), with 340 warp-instructions for 16
+// rate; 4 bits, 303 MB: 67 us, 4.5 TB/s (67 %), with 340 warp-instructions for 16
 // keys, about half of them masks, packed subtractions and scales, that keep 60 % of the
-// issue slots busy; 131072 keys of one sequence, 4 bits: 37.5 us
+// issue slots busy; 131072 keys of one sequence, 4 bits: 37 us
 // (60 %).  About 10 us of a call are the beginning (plan, page table and first keys, one
 // after the other: 5 us) and the end (the warps' merge, the CTAs' merge: 5 us).
 #include <atomic>
@@ -634,9 +634,12 @@ struct Shape {
   // whole stages (bf16: 8 ragged sequences with 5 queries 23.3 us with units of 64 keys, 24.7
   // with 128)
   static constexpr int kUnit = 16 * kBlocks;
-  static constexpr int kPitch = D + 4;                // floats a row, against bank conflicts
-  static constexpr int kSlots = kGroups > 1 ? kGroups / 2 : 1;
-  static constexpr int kMerge = kSlots * kRows * kPitch * 4;
+  // of all O that the key groups put down for the merge, at a time: half where two blocks of
+  // an SM have no room for more
+  static constexpr int kTurns = CW == 4 && WR == 8 && D == 128 && !kInt4 ? 2 : 1;
+  static constexpr int kWidth = D / kTurns;
+  static constexpr int kPitch = kWidth + 4;           // floats a row, against bank conflicts
+  static constexpr int kMerge = kGroups * kRows * kPitch * 4;
   static constexpr int kBytes = kStages * kStage + kMerge + 1024;
   // thread blocks per SM
   static constexpr int kCtas = CW == 8 ? 1 : WR == 8 && (kInt4 || D == 64) ? 3 : 2;
@@ -802,7 +805,7 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
   constexpr int ROWS = S::kRows;
   extern __shared__ uint8_t smem_raw_pg[];
   uint8_t* ring = align_smem_1024(smem_raw_pg);
-  float* sm_o = reinterpret_cast<float*>(ring + S::kStages * S::kStage);   // [kSlots][ROWS][kPitch]
+  float* sm_o = reinterpret_cast<float*>(ring + S::kStages * S::kStage);   // [kGroups][ROWS][kPitch]
   __shared__ Plan plan;
   __shared__ float sm_m[S::kGroups][ROWS], sm_l[S::kGroups][ROWS];
   __shared__ uint64_t full[S::kStages], empty[S::kStages];
@@ -874,7 +877,10 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
       if (lane == 0) mbar_arrive(&empty[st]);
       if (++st == S::kStages) st = 0, phase ^= 1;
     }
-    // merge the key groups: reference and sum of every row, then O
+    // Merge the key groups: every one puts down its rows' references, sums and O, and all
+    // threads add them up.  (Two barriers; with O rescaled first and the groups added in
+    // halves, four barriers and less shared memory, one sequence of 500 keys took 8.2 us
+    // instead of 7.7, 16 x 16 heads x 2048 keys 21.4 instead of 20.7.)
 #pragma unroll
     for (int n = 0; n < W::NT; ++n)
 #pragma unroll
@@ -887,46 +893,22 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
           sm_l[kg][rs * WR + 8 * n + 2 * t + c] = x;
         }
       }
+    const auto put_down = [&](int turn) {
+      float* const mine_o = sm_o + (kg * ROWS + rs * WR) * S::kPitch;
+#pragma unroll
+      for (int n = 0; n < W::NT; ++n)
+#pragma unroll
+        for (int d = 0; d < W::KS; ++d)
+          if (d / (W::KS / S::kTurns) == turn)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<float2*>(mine_o + (8 * n + 2 * t + c) * S::kPitch +
+                                         element_of<kInt4>(d, g) - turn * S::kWidth) =
+                  make_float2(w.o[d][n][c], w.o[d][n][c + 2]);
+    };
+    put_down(0);
     // (also that every consumer sees whether one of them gave up)
     if (barrier_or(kPgBar, S::kThreads, !ok)) break;
-#pragma unroll
-    for (int n = 0; n < W::NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int row = rs * WR + 8 * n + 2 * t + c;
-        float mx = sm_m[0][row];
-#pragma unroll
-        for (int i = 1; i < S::kGroups; ++i) mx = fmaxf(mx, sm_m[i][row]);
-        const float f = ex2_approx(w.m[n][c] - mx);
-#pragma unroll
-        for (int d = 0; d < W::KS; ++d) {
-          w.o[d][n][c] *= f;
-          w.o[d][n][c + 2] *= f;
-        }
-      }
-    // the upper half of the groups put theirs down, the lower half add theirs
-#pragma unroll
-    for (int turn = S::kGroups > 1 ? 1 : 0; turn >= 0; --turn) {
-      if (kg / S::kSlots == turn) {
-        float* slot_o = sm_o + (kg % S::kSlots) * ROWS * S::kPitch;
-#pragma unroll
-        for (int n = 0; n < W::NT; ++n)
-#pragma unroll
-          for (int d = 0; d < W::KS; ++d)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float2* dst = reinterpret_cast<float2*>(
-                  slot_o + (rs * WR + 8 * n + 2 * t + c) * S::kPitch + element_of<kInt4>(d, g));
-              float2 v = make_float2(w.o[d][n][c], w.o[d][n][c + 2]);
-              if (S::kGroups > 1 && turn == 0) {
-                const float2 x = *dst;
-                v.x += x.x, v.y += x.y;
-              }
-              *dst = v;
-            }
-      }
-      named_barrier_sync(kPgBar, S::kThreads);
-    }
     const bool whole = seg.n == seg.units;
     // a CTA has at most one item that it goes on with and one that goes on
     // after it
@@ -936,35 +918,45 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
           whole ? -1 : b * HR + seg.hr, blockIdx.x, slot,
           whole ? 0 : deal.owner(seg.first_position() + seg.units - 1));
     const int n_q = query_count(p, b);
-    for (int x = threadIdx.x; x < ROWS * (D / 4); x += S::kThreads) {
-      const int row = x / (D / 4), d = 4 * (x % (D / 4));
-      const int rho = rt * ROWS + row;
-      if (rho >= p.group * p.S_q || rho % p.S_q >= n_q) continue;
-      float mx = sm_m[0][row];
 #pragma unroll
-      for (int k = 1; k < S::kGroups; ++k) mx = fmaxf(mx, sm_m[k][row]);
-      float sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < S::kGroups; ++k) sum += sm_l[k][row] * ex2_approx(sm_m[k][row] - mx);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < S::kSlots; ++k) {
-        const float4 v =
-            *reinterpret_cast<const float4*>(sm_o + (k * ROWS + row) * S::kPitch + d);
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    for (int turn = 0; turn < S::kTurns; ++turn) {
+      if (turn > 0) {
+        named_barrier_sync(kPgBar, S::kThreads);
+        put_down(turn);
+        named_barrier_sync(kPgBar, S::kThreads);
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
-      acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-      if (whole) {
-        const long long out = (long long)b * p.H_q * p.S_q + (long long)h * p.group * p.S_q + rho;
-        *reinterpret_cast<uint2*>(p.o + out * D + d) =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-        if (d == 0) p.lse[out] = lse2 * 0.6931471805599453f;
-      } else {
-        const long long out = (long long)slot * ROWS + row;
-        *reinterpret_cast<float4*>(p.part_o + out * D + d) = acc;
-        if (d == 0) p.part_lse[out] = lse2;
+      for (int x = threadIdx.x; x < ROWS * (S::kWidth / 4); x += S::kThreads) {
+        const int row = x / (S::kWidth / 4), e = 4 * (x % (S::kWidth / 4));
+        const int d = turn * S::kWidth + e, rho = rt * ROWS + row;
+        if (rho >= p.group * p.S_q || rho % p.S_q >= n_q) continue;
+        float mx = sm_m[0][row];
+#pragma unroll
+        for (int k = 1; k < S::kGroups; ++k) mx = fmaxf(mx, sm_m[k][row]);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < S::kGroups; ++k) {
+          const float f = ex2_approx(sm_m[k][row] - mx);
+          const float4 v =
+              *reinterpret_cast<const float4*>(sm_o + (k * ROWS + row) * S::kPitch + e);
+          sum = fmaf(sm_l[k][row], f, sum);
+          acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+        if (whole) {
+          const long long out =
+              (long long)b * p.H_q * p.S_q + (long long)h * p.group * p.S_q + rho;
+          *reinterpret_cast<uint2*>(p.o + out * D + d) =
+              make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+          if (d == 0)
+            p.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+        } else {
+          const long long out = (long long)slot * ROWS + row;
+          *reinterpret_cast<float4*>(p.part_o + out * D + d) = acc;
+          if (d == 0) p.part_lse[out] = sum == 0.f ? -INFINITY : mx + log2f(sum);
+        }
       }
     }
     named_barrier_sync(kPgBar, S::kThreads);   // before the scratch is written again
