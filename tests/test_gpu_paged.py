@@ -713,6 +713,49 @@ def test_graphs_with_their_own_workspaces():
         assert torch.equal(out[0], w[0]) and torch.equal(out[1], w[1])
 
 
+def test_workspace_that_the_call_allocates():
+    """It belongs to the call's stream, and in a captured call to the graph: memory that others get
+    meanwhile is other memory."""
+    D, H, page, L = 128, 2, 32, 30000
+    bt, pages = tables([L], page, 96)
+    kc, vc = (t.cuda() for t in pools("int4", pages, H, page, D, 97))
+    btd, n = bt.cuda(), device_ints(L)
+    q = randn(rng(98), 1, 8, 1, D).cuda()
+    size = ap.paged_workspace_bytes(1, 8, H, 1, D, bt.shape[1] * page)
+    want = ap.attn_fwd_paged(q, kc, vc, btd, n, True, 0.1)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    s = torch.cuda.Stream()
+    outs = [(torch.zeros_like(q), torch.zeros((1, 8, 1)).cuda()) for _ in range(8)]
+    torch.cuda.synchronize()
+    for out in outs:
+        ap.attn_fwd_paged(q, kc, vc, btd, n, True, 0.1, out=out, stream=s)
+        for _ in range(4):
+            torch.full((size,), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        for out in outs[:2]:
+            ap.attn_fwd_paged(q, kc, vc, btd, n, True, 0.1, out=out)
+    for _ in range(5):
+        outs[0][0].zero_(), outs[1][0].zero_()
+        g.replay()
+        held = [torch.full((size,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        for out in outs[:2]:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+        assert all((x == 0xff).all() for x in held)
+    del held, out, outs
+    # (a workspace still held would be `size` more; the graph itself holds two small blocks)
+    after = torch.cuda.memory_allocated()
+    assert after < before + size
+    with pytest.raises(ap.AttnError):   # refused after it was allocated: freed all the same
+        ap.attn_fwd_paged(q, kc, vc, btd, n, True, float("inf"))
+    assert torch.cuda.memory_allocated() == after
+
+
 @pytest.mark.parametrize("fmt", ["int4", "bf16"])
 def test_pools_larger_than_32_bit_offsets(fmt):
     """The sequence's pages are the last of a pool of more than 2^32 bytes."""
