@@ -128,6 +128,10 @@ struct Plan {
 __device__ __forceinline__ int make_plan(const PagedParams& p, Plan& plan) {
   const int per = (p.cache.B + kPlanThreads - 1) / kPlanThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!p.split) {   // every item is one unit: no need to read the lengths first (7.5 -> 7.2 us)
+    __syncthreads();
+    return p.cache.B * (p.item_cost + 1);
+  }
   if (warp < kPlanWarps) {
     const int b0 = threadIdx.x * per;
     int sum = 0;
@@ -153,6 +157,11 @@ __device__ __forceinline__ int make_plan(const PagedParams& p, Plan& plan) {
 // the weight before it.  Whole warps.
 __device__ __forceinline__ int find_sequence(const PagedParams& p, const Plan& plan, int v,
                                              int& before) {
+  if (!p.split) {
+    const int b = min(v / (p.item_cost + 1), p.cache.B - 1);
+    before = b * (p.item_cost + 1);
+    return b;
+  }
   int w = 0, base = 0;
 #pragma unroll
   for (int i = 0; i < kPlanWarps - 1; ++i) {
