@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(32 * CW + 32, Shape<D, kInt4, WR, RS, CW>::kCt
   constexpr int ROWS = S::kRows;
   extern __shared__ uint8_t smem_raw_pg[];
   uint8_t* ring = align_smem_1024(smem_raw_pg);
-  float* sm_o = reinterpret_cast<float*>(ring + S::kStages * S::kStage);   // [kGroups][ROWS][kPitch]
+  float* sm_o = reinterpret_cast<float*>(ring + S::kStages * S::kStage);  // [kGroups][ROWS][kPitch]
   __shared__ Plan plan;
   __shared__ float sm_m[S::kGroups][ROWS], sm_l[S::kGroups][ROWS];
   __shared__ uint64_t full[S::kStages], empty[S::kStages];
