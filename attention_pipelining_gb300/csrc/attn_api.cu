@@ -918,12 +918,10 @@ attn_status_t attn_device_status(int* status_out, int reset) {
       read_kv_status(&kv_status, reset != 0) != cudaSuccess ||
       read_paged_status(&paged_status, reset != 0) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  *status_out = main_status != 0 ? main_status
-                : bwd_status != 0 ? bwd_status
-                : cs_status != 0  ? cs_status
-                : kv_status != 0  ? kv_status
-                : paged_status != 0 ? paged_status
-                                    : selftest_status;
+  // A timeout says more than an index out of range: outputs are then unspecified.
+  *status_out = ATTN_OK;
+  for (int s : {main_status, bwd_status, cs_status, kv_status, paged_status, selftest_status})
+    if (s == ATTN_ERR_TIMEOUT || *status_out == ATTN_OK) *status_out = s;
   return ATTN_OK;
 }
 

@@ -796,7 +796,8 @@ __device__ __forceinline__ uint32_t produce(const PagedParams& p, Segments seg, 
       if (++st == S::kStages) st = 0, phase ^= 1;
     }
   } while (seg.next(p, HR));
-  if (bad) g_paged_status = ATTN_ERR_BAD_INDEX;
+  // (never in place of a timeout, which says more: the outputs are then unspecified)
+  if (bad) atomicCAS(&g_paged_status, 0, ATTN_ERR_BAD_INDEX);
   // stay until the consumers have had the last stages, and with them every copy
   for (int n = 0; n < S::kStages; ++n) {
     if (requested + n >= S::kStages)

@@ -281,8 +281,8 @@ const char *attn_status_string(attn_status_t status);
  * backward, self-test and paged-cache kernels): ATTN_OK, ATTN_ERR_TIMEOUT if a
  * launch since the last reset gave up on a wait (that launch's outputs are then
  * unspecified), or ATTN_ERR_BAD_INDEX if a paged-cache kernel met an index out
- * of range (attn_paged.h says what it did with it).  Synchronises the device.  With
- * reset != 0 the word is cleared afterwards.
+ * of range (attn_paged.h says what it did with it) and none gave up.  Synchronises
+ * the device.  With reset != 0 the words are cleared afterwards.
  */
 attn_status_t attn_device_status(int *status_out, int reset);
 

@@ -858,3 +858,43 @@ def test_a_wait_that_runs_out(fmt, D, Hq):
     # a stage that no thread block gets to: nothing is withheld
     check_attention(q, kc, vc, bt, [L], True, 0.1,
                     ap.paged.fwd_paged_timeout_test(*args, drop_stage=10 ** 6))
+
+
+# ---------------------------------------------------------------- what the status word says
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_a_timeout_is_not_hidden_by_a_bad_index(fmt):
+    """Outputs are unspecified after a timeout, but not after an index out of range: where both
+    happened, in whichever order and call, the status word says the first."""
+    L, page, D = 3000, 16, 64
+    bt, pages = tables([L], page, 111)
+    kc, vc = (t.cuda() for t in pools(fmt, pages, 1, page, D, 112))
+    q = randn(rng(113), 1, 4, 1, D).cuda()
+    bad = bt.clone()
+    bad[0, 0] = -1
+    btd, badd, n = bt.cuda(), bad.cuda(), device_ints(L)
+    k = randn(rng(114), 1, 1, 1, D).cuda()
+
+    def append():
+        ap.kv_append(k, k, kc, vc, badd, device_ints(0))
+
+    def attend():
+        ap.attn_fwd_paged(q, kc, vc, badd, n, True, 0.1)
+
+    def give_up():
+        ap.paged.fwd_paged_timeout_test(q, kc, vc, btd, n, True, 0.1, drop_stage=0,
+                                        wait_budget_ns=20_000_000)
+
+    for calls in ((append, give_up), (give_up, append), (attend, give_up), (give_up, attend),
+                  (append, attend, give_up, append, attend)):
+        for call in calls:
+            call()
+        torch.cuda.synchronize()
+        assert ap.device_status(reset=False) == 5, [c.__name__ for c in calls]
+        assert ap.device_status(reset=True) == 5
+        assert ap.device_status(reset=True) == 0
+    for call in (append, attend):
+        call()
+        torch.cuda.synchronize()
+        assert ap.device_status(reset=True) == BAD_INDEX
