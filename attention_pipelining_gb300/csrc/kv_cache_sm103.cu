@@ -252,7 +252,11 @@ __global__ void __launch_bounds__(kAppendThreads, 8)
   const uint32_t token = blockIdx.x * kSlots + threadIdx.x / kLanes;
   if (token >= (uint32_t)(kc.B * p.S)) return;
   const int b = (int)(token / (uint32_t)p.S), i = (int)(token % (uint32_t)p.S);
-  if (p.new_lens && i >= p.new_lens[b]) return;
+  if (p.new_lens) {
+    const int n = p.new_lens[b];
+    if ((unsigned)n > (unsigned)p.S) g_kv_status = ATTN_ERR_BAD_INDEX;
+    if (i >= n) return;
+  }
   // this block's rows: heads [q0, q1) of the queries, [k0, k1) of the keys and
   // [v0, v1) of the values
   const int r0 = blockIdx.y * p.rows, r1 = r0 + p.rows;
@@ -396,7 +400,8 @@ __global__ void __launch_bounds__(kKvThreads)
   const int b = (int)(unit / per_seq);
   const long long first = p.start ? p.start[b] : 0;
   const int len = p.lens[b];
-  if ((len < 0 || len > kc.capacity || first < 0) && lane == 0) g_kv_status = ATTN_ERR_BAD_INDEX;
+  if ((len < 0 || len > kc.capacity || first < 0 || first > kc.capacity) && lane == 0)
+    g_kv_status = ATTN_ERR_BAD_INDEX;
   const long long lo = first < 0 ? 0 : first;                     // positions [lo, hi)
   long long hi = first + p.S;
   hi = hi < len ? hi : len;

@@ -33,10 +33,12 @@
  * kernels check every page number, length and position they read.  A page
  * number outside [0, num_pages) is never followed: attn_kv_append skips that
  * token, attn_kv_read leaves its rows as they were, and attn_fwd_paged treats
- * the keys as masked.  A length, start or count below 0 or beyond what the
- * block table spans (or, for a rotated token, beyond the rotation table) is
- * cut to that range.  Either is recorded in the device's status word
- * (attn_device_status): ATTN_ERR_BAD_INDEX.
+ * the keys as masked.  A length or start below 0 or beyond what the block table
+ * spans, and a count of new or query tokens below 0 or above S or S_q, is cut to
+ * that range; tokens at positions before 0, behind the span or (where they are
+ * rotated) behind the rotation table are skipped.  All of these are recorded in
+ * the device's status word (attn_device_status): ATTN_ERR_BAD_INDEX.  The start
+ * of a sequence without new tokens is not looked at.
  *
  * All calls return once their kernels are queued on `stream`; nothing is
  * allocated.

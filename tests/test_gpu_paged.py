@@ -898,3 +898,44 @@ def test_a_timeout_is_not_hidden_by_a_bad_index(fmt):
         call()
         torch.cuda.synchronize()
         assert ap.device_status(reset=True) == BAD_INDEX
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_counts_and_starts_out_of_range_are_recorded(fmt):
+    """kv_append's new_lens below 0 or above S and kv_read's start beyond what the block table
+    spans are cut, and the status word says so; at the range's ends it stays clean."""
+    page, D, S, span = 16, 64, 3, 64
+    bt, pages = tables([span, span], page, 115)
+    kc, vc = (t.cuda() for t in pools(fmt, pages, 2, page, D, 116))
+    k = randn(rng(117), 2, 2, S, D).cuda()
+    start = device_ints(5, 30)
+
+    def appended(*new):
+        a, b = kc.clone(), vc.clone()
+        ap.kv_append(k, k, a, b, bt.cuda(), start, new_lens=device_ints(*new))
+        torch.cuda.synchronize()
+        return a, b, ap.device_status(reset=True)
+
+    for good, others in (((0, 3), ((-1, 3), (0, 4), (-2 ** 31, 2 ** 31 - 1))), ((3, 0), ((3, -5), (7, 0)))):
+        want = appended(*good)
+        assert want[2] == 0
+        for new in others:
+            got = appended(*new)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert got[2] == BAD_INDEX, new
+    lens = device_ints(span, span)
+
+    def read(*at):
+        out = tuple(torch.full((2, 2, S, D), 3.0, dtype=torch.bfloat16).cuda() for _ in range(2))
+        ap.kv_read(kc, vc, bt.cuda(), lens, S, start=device_ints(*at), out=out)
+        torch.cuda.synchronize()
+        return out, ap.device_status(reset=True)
+
+    want, status = read(span - 1, span)
+    assert status == 0 and (want[0][1] == 3.0).all() and (want[0][0, :, 1:] == 3.0).all()
+    for at in ((span - 1, span + 1), (span - 1, 2 ** 31 - 1)):
+        got, status = read(*at)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert status == BAD_INDEX, at
+    got, status = read(-2 ** 31, 0)
+    assert status == BAD_INDEX and (got[0][0] == 3.0).all() and not (got[0][1] == 3.0).any()
