@@ -194,6 +194,7 @@ struct PagedParams {
   int ctas, by_item;     // CTAs, and whether `shared` goes by items (set at launch)
   int causal;
   float scale_log2;
+  float max_prob, lead;  // of a bf16 cache's probabilities (see the kernel)
   uint32_t code_base_low, code_base_high;  // fp16 pairs of 1024 and 64 (see the kernel)
   unsigned long long timeout_ns;  // budget of any single wait inside the kernel
   // Test of the timeout path: when >= 0, the producer warp of every CTA leaves this

@@ -128,6 +128,10 @@ attn_status_t paged_impl(const attn_kv_cache_t* cache, const attn_bhsd_t* q, voi
   // (kept finite)
   const double scale_log2 = (double)scale * 1.4426950408889634;
   p.scale_log2 = (float)std::fmin(std::fmax(scale_log2, -(double)FLT_MAX), (double)FLT_MAX);
+  int bits = 0;   // 2^bits >= capacity
+  while ((1 << bits) < p.cache.capacity) ++bits;
+  p.max_prob = std::ldexp(1.f, -bits);
+  p.lead = (float)(bits + 8);
   p.code_base_low = 0x64006400u;
   p.code_base_high = 0x54005400u;
   p.timeout_ns = timeout_ns;

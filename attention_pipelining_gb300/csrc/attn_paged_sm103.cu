@@ -68,13 +68,17 @@ constexpr uint32_t kPgBar = 1;             // named barrier of the consumer warp
 // The reference of a row's exponentials starts below every finite score, and
 // far enough above minus infinity that a masked score (-inf) minus it is -inf.
 constexpr float kNoMax = -3.0e38f;
-// The reference follows the running maximum lazily: it moves only when a sum
-// of a lane's probabilities times the largest value scale would pass 2^15 (fp16
-// holds up to 65504), and is then set so that the largest one is 2^6 at most: 2^7
-// or more of growth before the next move, and values down to 2^-14 (2^-20 of the
-// largest) keep all their bits.
-constexpr float kMaxProb = 32768.f;
-constexpr float kTargetLog2 = 6.f;
+// The reference follows the running maximum lazily: it moves only when a sum of a
+// lane's probabilities in a step (times the largest value scale) would pass
+// p.max_prob, and then by enough for 7 bits or more of growth before the next move:
+// 4 bits: max_prob is 2^15 (fp16 holds up to 65504), and the largest product is set
+//   to 2^6 at most: values down to 2^-14 (2^-20 of the largest) keep all their bits;
+// bf16: max_prob is 2^-e with 2^e keys or more in the block table's span, and the
+//   largest probability is set to 2^-(e + 8) at most, so that all sums of
+//   probabilities stay below 1 and those of probabilities times values below the
+//   largest value: no finite value makes an infinite O.
+constexpr float kMaxProbFp16 = 32768.f;
+constexpr float kTargetLog2Fp16 = 6.f;
 // value scales are taken as at least this when the reference is set, so that
 // the sum of the probabilities stays finite
 constexpr float kMinScale = 5.42101086e-20f;  // 2^-64
@@ -283,6 +287,7 @@ struct Warp {
   // B fragments of Q (fp16 for a 4-bit cache): [n][32 elements]{two k16 steps}
   uint32_t q[NT][G][4];
   CodeBase code_base;
+  float max_prob, lead;      // see kMaxProbFp16; the reference above the maximum (bf16)
   float fac[NT][2];          // S to base-2 exponents
   int lim[NT][2];            // keys the row sees
   int min_lim, max_lim;      // keys every row of the tile sees, and any may see
@@ -298,6 +303,8 @@ struct Warp {
     const int n_q = query_count(p, b);
     code_base.low = p.code_base_low;
     code_base.high = p.code_base_high;
+    max_prob = kInt4 ? kMaxProbFp16 : p.max_prob;
+    lead = p.lead;
     min_lim = tile_common;
     max_lim = tile_end;
 #pragma unroll
@@ -485,12 +492,15 @@ struct Warp {
       probabilities(n);
       most = fmaxf(most, fmaxf(sum[n][0], sum[n][1]));
     }
-    if (__any_sync(kFull, most * smax > kMaxProb || most > kMaxSum)) {
-      float big = fmaxf(smax, kMinScale);
+    if (__any_sync(kFull, most * smax > max_prob || (kInt4 && most > kMaxSum))) {
+      float up = lead;
+      if constexpr (kInt4) {
+        float big = fmaxf(smax, kMinScale);
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, d));
-      // log2 of the next power of two
-      const float up = (float)((int)(__float_as_uint(big) >> 23) - 126) - kTargetLog2;
+        for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, d));
+        // log2 of the next power of two
+        up = (float)((int)(__float_as_uint(big) >> 23) - 126) - kTargetLog2Fp16;
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float alpha[2];
@@ -987,6 +997,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   constexpr int kRows = kMergeWarps / kPer;
   constexpr int kBatch = kPer > 1 ? 8 : 4;               // parts that a warp loads together
   constexpr int E = D / 32;                              // elements a lane
+  // of a part, in the sums: they stay below the largest value (parts are fewer)
+  constexpr float kPartShare = 1.f / kPagedMaxCtas;
   __shared__ float sm_acc[kPer > 1 ? kMergeWarps : 1][D], sm_sum[kMergeWarps], sm_max[kMergeWarps];
   wait_for_earlier();
   const int4 it = p.shared[blockIdx.x];
@@ -1004,9 +1016,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  // adds 2^(l - base) of (s, v) to the sums
-  const auto add = [&](float l, float base, float s, const float (&v)[E]) {
-    const float f = ex2_approx(l - base);
+  // adds `share` 2^(l - base) of (s, v) to the sums
+  const auto add = [&](float l, float base, float share, float s, const float (&v)[E]) {
+    const float f = share * ex2_approx(l - base);
     sum = fmaf(f, s, sum);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
@@ -1042,7 +1054,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       for (int i = 0; i < kBatch; ++i) next = fmaxf(next, l[i]);
       rescale(next);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) add(l[i], finite(mx), 1.f, v[i]);
+      for (int i = 0; i < kBatch; ++i) add(l[i], finite(mx), kPartShare, 1.f, v[i]);
     }
   }
   if constexpr (kPer > 1) {   // join the row's warps
@@ -1060,7 +1072,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       float v[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = sm_acc[warp + i][lane * E + e];
-      add(sm_max[warp + i], finite(mx), sm_sum[warp + i], v);
+      add(sm_max[warp + i], finite(mx), 1.f, sm_sum[warp + i], v);
     }
   }
   if (!live) return;
@@ -1070,7 +1082,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   if (lane == 0)
-    p.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+    p.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum / kPartShare)) * 0.6931471805599453f;
 }
 
 template <int D, bool kInt4, int WR, int RS, int CW>

@@ -939,3 +939,33 @@ def test_counts_and_starts_out_of_range_are_recorded(fmt):
         assert status == BAD_INDEX, at
     got, status = read(-2 ** 31, 0)
     assert status == BAD_INDEX and (got[0][0] == 3.0).all() and not (got[0][1] == 3.0).any()
+
+
+# ---------------------------------------------------------------- values of any size
+
+
+@pytest.mark.parametrize("D,Hq,lens,wide", [
+    (64, 1, [1, 2, 3, 17], False), (128, 4, [1, 300, 40], False), (128, 12, [5, 260], False),
+    (64, 20, [33, 2], False), (128, 2, [5000, 3], True), (64, 3, [7000], True), (128, 40, [1300], True)])
+@pytest.mark.parametrize("size", [3e38, 1e37, 2.0 ** 100, 2.0 ** -100, 2.0 ** -110])
+def test_values_of_any_size_in_bf16(D, Hq, lens, wide, size):
+    """Values next to the ends of bf16's range, of one sign and of both, under equal scores, scores
+    that rise key by key and scores of a normal distribution: finite values give a finite O."""
+    page, B = 16, len(lens)
+    bt, pages = tables(lens, page, 121)
+    if wide:
+        bt = torch.cat([bt, torch.full((B, 80), -1, dtype=torch.int32)], 1)
+    g = rng(122)
+    k = randn(g, pages, 1, page, D)
+    v = torch.full((pages, 1, page, D), size).to(torch.bfloat16)
+    v[..., 1::2] *= (torch.randint(0, 2, (pages, 1, page, D // 2), generator=g) * 2 - 1).to(torch.bfloat16)
+    q = randn(g, B, Hq, 1, D)
+    rising = torch.zeros_like(k)
+    for b, L in enumerate(lens):     # key x of the sequence: x / 16 in its first element
+        for i in range(-(-L // page)):
+            rising[int(bt[b, i]), 0, :, 0] = (torch.arange(page) + i * page) / 16.0
+    q1 = torch.zeros_like(q)
+    q1[..., 0] = 1.0
+    for what, qq, kk, scale in (("equal", q, k, 0.0), ("rising", q1, rising, 1.0), ("normal", q, k, 0.2)):
+        got = ap.attn_fwd_paged(qq.cuda(), kk.cuda(), v.cuda(), bt.cuda(), device_ints(*lens), True, scale)
+        check_attention(qq, kk, v, bt, lens, True, scale, got, what=(what, size))
