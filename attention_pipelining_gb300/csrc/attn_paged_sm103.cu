@@ -493,19 +493,32 @@ struct Warp {
       most = fmaxf(most, fmaxf(sum[n][0], sum[n][1]));
     }
     if (__any_sync(kFull, most * smax > max_prob || (kInt4 && most > kMaxSum))) {
-      float up = lead;
-      if constexpr (kInt4) {
-        float big = fmaxf(smax, kMinScale);
+      // how far above the maximum: log2 of the next power of two of the largest of the
+      // lanes' value scales, less the target
+      const auto above = [&](float big) {
+        big = fmaxf(big, kMinScale);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, d));
-        // log2 of the next power of two
-        up = (float)((int)(__float_as_uint(big) >> 23) - 126) - kTargetLog2Fp16;
-      }
+        return (float)((int)(__float_as_uint(big) >> 23) - 126) - kTargetLog2Fp16;
+      };
+      const float up_all = kInt4 ? above(smax) : lead;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float alpha[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          float up = up_all;
+          if constexpr (kInt4 && kMasked) {   // of the keys that this row sees
+            uint32_t top = 0u;
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < G / 2; ++j)
+                  top = max_bf16x2(top, seen(i, n, 2 * k + c) ? sv[i][k][j] : 0u);
+            up = above(fmaxf(lo_f(top), hi_f(top)));
+          }
           float mx = -INFINITY;
 #pragma unroll
           for (int i = 0; i < NB; ++i)

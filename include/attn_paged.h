@@ -146,8 +146,8 @@ attn_status_t attn_kv_read(const attn_kv_cache_t *cache, void *k_out, void *v_ou
  * codes are exact in the products, the queries are exact down to 2^-17 of their
  * row's largest element (smaller elements are off by 2^-25 of it at most), and the
  * probabilities times the values' scales are rounded to fp16 (an error of 2^-11
- * of a key's share in O, or of 2^-30 of the largest value, or 2^-90, where that
- * is more).
+ * of a key's share in O, or of 2^-30 of the largest value that the query sees, or
+ * 2^-90, where that is more).
  */
 attn_status_t attn_fwd_paged(const attn_kv_cache_t *cache, const attn_bhsd_t *q, void *o,
                              float *lse, const int *lens, const int *q_lens, void *workspace,

@@ -969,3 +969,26 @@ def test_values_of_any_size_in_bf16(D, Hq, lens, wide, size):
     for what, qq, kk, scale in (("equal", q, k, 0.0), ("rising", q1, rising, 1.0), ("normal", q, k, 0.2)):
         got = ap.attn_fwd_paged(qq.cuda(), kk.cuda(), v.cuda(), bt.cuda(), device_ints(*lens), True, scale)
         check_attention(qq, kk, v, bt, lens, True, scale, got, what=(what, size))
+
+
+@pytest.mark.parametrize("size", [2.0 ** 30, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("fmt,D,Hq", [("int4", 64, 4), ("int4", 128, 2), ("int4", 128, 12), ("bf16", 128, 2),
+                                      ("bf16", 64, 12)])
+def test_a_large_value_that_a_row_does_not_see_does_not_matter(fmt, D, Hq, size):
+    """The last token's value is finite and far larger than the others: of four causal queries only
+    the last one sees it, and the others' results are as exact as without it."""
+    for L in (4, 45, 1300):
+        page = 16
+        bt, pages = tables([L], page, 131)
+        bt = torch.cat([bt, torch.full((1, 2), -1, dtype=torch.int32)], 1)
+        g = rng(132)
+        k, v = randn(g, pages, 1, page, D), randn(g, pages, 1, page, D)
+        kc, small = fill(k, fmt, "k"), fill(v, fmt, "v")
+        pg, slot = int(bt[0, (L - 1) // page]), (L - 1) % page
+        v[pg, 0, slot] *= size
+        vc = fill(v, fmt, "v")
+        q = randn(g, 1, Hq, 4, D)
+        o, lse = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(L), True, 0.1)
+        head = (o[:, :, :3].contiguous(), lse[:, :, :3].contiguous())
+        check_attention(q[:, :, :3], kc, small, bt, [L - 1], True, 0.1, head, what=L)
+        check_attention(q, kc, vc, bt, [L], True, 0.1, (o, lse), what=L)
