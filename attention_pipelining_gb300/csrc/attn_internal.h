@@ -209,7 +209,6 @@ constexpr int kPagedUnit = 64;
 constexpr int kPagedItemKeys = 256;
 constexpr int kPagedWholeKeys = 1024;
 constexpr int kPagedMaxCtas = 512;
-constexpr int kPagedFewItems = 152;   // items that have an SM each
 
 cudaError_t launch_kv_append(const KvAppendParams& p, int D, bool int4, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadParams& p, int D, bool int4, cudaStream_t stream);

@@ -63,6 +63,7 @@ constexpr int kPlanWarps = 4;              // warps that sum up the sequences' w
 constexpr int kPlanThreads = kPlanWarps * 32;
 constexpr int kMergeWarps = 8;
 constexpr int kManyParts = 8;              // of an item, on average: more warps for its rows
+constexpr int kMaxDevices = 64;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kPgBar = 1;             // named barrier of the consumer warps
 // The reference of a row's exponentials starts below every finite score, and
@@ -1103,11 +1104,11 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
   using S = Shape<D, kInt4, WR, RS, CW>;
   const auto kernel = attn_paged_kernel<D, kInt4, WR, RS, CW>;
   // per device: the shared-memory attribute set, and the resident CTAs
-  static std::atomic<int> resident[64] = {};
+  static std::atomic<int> resident[kMaxDevices] = {};
   cudaError_t e;
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   long long ctas = resident[dev].load(std::memory_order_acquire);
   if (ctas == 0) {
     int sms = 0, per_sm = 0;
@@ -1153,14 +1154,31 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
                       32 * kMergeWarps, 0, stream, p);
 }
 
+// SMs of the current device (each device is asked once).
+cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  *sms = known[dev].load(std::memory_order_acquire);
+  if (*sms > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_release);
+  return e;
+}
+
 template <int D, bool kInt4>
 cudaError_t launch_rows(const PagedParams& p, int rows, cudaStream_t stream) {
-  // Few short items: blocks of eight consumer warps, one on an SM (128 items of
+  // No more short items than SMs: blocks of eight consumer warps, one on an SM (128 items of
   // 1000 keys, D = 128: 11.5 us, 16.4 in bf16, against 14.5 and 18.3 with blocks of
   // four; 8 items of 500 keys 7.7 and 9.9 against 8.0 and 10.4)
-  if (rows == 8 && p.cache.capacity <= kPagedWholeKeys &&
-      (long long)p.cache.B * p.cache.H_kv <= kPagedFewItems)
-    return launch<D, kInt4, 8, 1, 8>(p, stream);
+  if (rows == 8 && p.cache.capacity <= kPagedWholeKeys) {
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    if ((long long)p.cache.B * p.cache.H_kv <= sms) return launch<D, kInt4, 8, 1, 8>(p, stream);
+  }
   if (rows == 8) return launch<D, kInt4, 8, 1, 4>(p, stream);
   if (rows == 16) return launch<D, kInt4, 16, 1, 4>(p, stream);
   if (rows == 32) return launch<D, kInt4, 16, 2, 4>(p, stream);

@@ -992,3 +992,41 @@ def test_a_large_value_that_a_row_does_not_see_does_not_matter(fmt, D, Hq, size)
         head = (o[:, :, :3].contiguous(), lse[:, :, :3].contiguous())
         check_attention(q[:, :, :3], kc, small, bt, [L - 1], True, 0.1, head, what=L)
         check_attention(q, kc, vc, bt, [L], True, 0.1, (o, lse), what=L)
+
+
+# ---------------------------------------------------------------- many short items
+
+
+def short_lens(B, seed, most=1024):
+    """Mostly short, some empty, a few as long as the block table."""
+    g = np.random.default_rng(seed)
+    n = [int(x) for x in np.exp(g.uniform(0, np.log(130), B))]
+    n[0], n[B // 3], n[B // 2], n[-1] = 0, most, 1000, 0
+    return n
+
+
+@pytest.mark.parametrize("fmt,D,B,H,group,Sq,causal", [
+    ("int4", 128, 40, 4, 2, 1, True), ("bf16", 128, 40, 4, 2, 1, True),
+    ("int4", 64, 150, 4, 1, 2, True), ("bf16", 64, 150, 4, 1, 2, False),
+    ("int4", 128, 300, 3, 1, 1, False), ("bf16", 128, 300, 3, 2, 1, True),
+    ("int4", 64, 160, 1, 8, 1, True), ("bf16", 64, 1300, 1, 1, 1, True),
+    ("int4", 64, 140, 2, 5, 3, True), ("bf16", 128, 140, 2, 5, 3, True)])
+def test_many_short_items(fmt, D, B, H, group, Sq, causal):
+    """Block tables of at most 1024 keys (items kept whole) and more items than SMs, up to several
+    for every thread block, lengths from 0 on: each block walks its items in turn, with more
+    sequences than the plan has threads."""
+    page = 64
+    lens = short_lens(B, 141)
+    bt, pages = tables([max(n, 1) for n in lens], page, 142)
+    assert bt.shape[1] * page == 1024
+    kc, vc = pools(fmt, pages, H, page, D, 143)
+    q = randn(rng(144), B, H * group, Sq, D)
+    q_lens = [(3 * b) % (Sq + 1) for b in range(B)] if Sq > 1 else None
+    out = (torch.full((B, H * group, Sq, D), 5.0, dtype=torch.bfloat16).cuda(),
+           torch.full((B, H * group, Sq), 5.0).cuda())
+    ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(*lens), causal, 0.11,
+                      q_lens=device_ints(*q_lens) if q_lens else None, out=out)
+    torch.cuda.synchronize()
+    check_attention(q, kc, vc, bt, lens, causal, 0.11, out, q_lens)
+    for b in range(B if q_lens else 0):
+        assert (out[0][b, :, q_lens[b]:] == 5.0).all() and (out[1][b, :, q_lens[b]:] == 5.0).all()
