@@ -1030,3 +1030,73 @@ def test_many_short_items(fmt, D, B, H, group, Sq, causal):
     check_attention(q, kc, vc, bt, lens, causal, 0.11, out, q_lens)
     for b in range(B if q_lens else 0):
         assert (out[0][b, :, q_lens[b]:] == 5.0).all() and (out[1][b, :, q_lens[b]:] == 5.0).all()
+
+
+# ---------------------------------------------------------------- bytes that only a 4-bit cache has
+
+
+def packed_tokens(x, kind, page):
+    """Values [1, H, L, D] (bf16, L a multiple of 16) as the 4-bit blocks [L / page, H, page / 16, 9 D]
+    of pages in order."""
+    _, H, L, D = x.shape
+    b = ref.pack(ref.f64(x).reshape(-1, D), kind)
+    return torch.from_numpy(b).reshape(H, L // page, page // 16, 9 * D).transpose(0, 1)
+
+
+def test_a_4_bit_pool_larger_than_32_bit_offsets():
+    """The appended bytes lie in the last pages of a pool of more than 2^32 bytes, and nowhere else
+    in the pages that an offset cut to 32 bits would reach; they are read back from there."""
+    H, page, D, L = 8, 64, 128, 256
+    per = H * page * 72
+    pages = (1 << 32) // per + 40
+    kc, vc = ap.kv_cache_empty(pages, H, page, D, "int4")
+    kc.fill_(0x5a), vc.fill_(0x5a)
+    bt = torch.arange(pages - 1, pages - 5, -1, dtype=torch.int32)[None].cuda()
+    k, v = (randn(rng(151 + i), 1, H, L, D) for i in range(2))
+    ap.kv_append(k.cuda(), v.cuda(), kc, vc, bt, device_ints(0))
+    got = ap.kv_read(kc, vc, bt, device_ints(L), L)
+    torch.cuda.synchronize()
+    for pool, x, kind, back in ((kc, k, "k", got[0]), (vc, v, "v", got[1])):
+        want = packed_tokens(x, kind, page)
+        assert torch.equal(pool[pages - 4:].flip(0).cpu(), want)
+        assert (pool[:48] == 0x5a).all() and (pool[pages - 8:pages - 4] == 0x5a).all()
+        vals = ref.unpack(want.transpose(0, 1).reshape(-1, 9 * D).numpy(), kind)[0]
+        assert np.array_equal(ref.f64(back), ref.bf16(vals).reshape(1, H, L, D))
+
+
+def test_scales_and_keys_of_every_ratio():
+    """The groups of test_quantisation_of_every_ratio, and others down to bf16's smallest numbers:
+    the scales' bytes, and the codes of keys as well as of values."""
+    D = 64
+    m = np.arange(128, 256) / 128.0
+    tops = np.concatenate([m * 2.0 ** e for e in (0, 1, -1, 37, -98, -99, -120, -125, -126, -128, -131, -133, 127)])
+    tops = torch.from_numpy(tops).to(torch.bfloat16).double().numpy()
+    g = np.random.default_rng(153)
+    x = g.uniform(-1, 1, (len(tops), 32)) * tops[:, None]
+    x[np.arange(len(tops)), g.integers(0, 32, len(tops))] = tops * np.where(g.random(len(tops)) < 0.5, -1, 1)
+    x = torch.from_numpy(x.reshape(-1, D)).to(torch.bfloat16)
+    S = len(x)
+    kc, vc = ap.kv_cache_empty(-(-S // 64), 1, 64, D, "int4")
+    kc.zero_(), vc.zero_()
+    bt = torch.arange(kc.shape[0], dtype=torch.int32)[None].cuda()
+    xd = x[None, None].cuda()
+    ap.kv_append(xd, xd, kc, vc, bt, device_ints(0))
+    back = ap.kv_read(kc, vc, bt, device_ints(S), S)
+    torch.cuda.synchronize()
+    f = x.double().numpy().reshape(S, D // 32, 32)
+    scale = torch.from_numpy(np.abs(f).max(-1) / 7).to(torch.bfloat16)   # (subnormals too)
+    s = scale.double().numpy()[..., None]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        c = np.where(s > 0, np.clip(np.round(f / s), -7, 7), 0)
+    code = (c + 8).astype(np.uint8).reshape(S, D)
+    bytes_of = scale.view(torch.int16).numpy().view(np.uint8).reshape(S, D // 16)
+    want_back = torch.from_numpy((c * s).reshape(S, D)).to(torch.bfloat16)
+    for pool, kind, b in ((kc, "k", back[0]), (vc, "v", back[1])):
+        got = pool.cpu().numpy().reshape(-1, 9 * D)
+        idx = ref.nibble_index(kind, D)
+        for t in range(S):
+            blk, r = got[t // 16], t % 16
+            assert np.array_equal((blk[idx[r] // 2] >> (4 * (idx[r] % 2))) & 15, code[t]), (kind, t)
+            at = 8 * D + r * (D // 16)
+            assert np.array_equal(blk[at:at + D // 16], bytes_of[t]), (kind, t)
+        assert np.array_equal(ref.f64(b[0, 0]), want_back.double().numpy())
