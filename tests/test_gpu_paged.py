@@ -1100,3 +1100,30 @@ def test_scales_and_keys_of_every_ratio():
             at = 8 * D + r * (D // 16)
             assert np.array_equal(blk[at:at + D // 16], bytes_of[t]), (kind, t)
         assert np.array_equal(ref.f64(b[0, 0]), want_back.double().numpy())
+
+
+# ---------------------------------------------------------------- queries rotated in place
+
+
+@pytest.mark.parametrize("fmt,D,S,rot,inter", [
+    ("int4", 128, 1, 128, False), ("int4", 64, 33, 32, True), ("bf16", 128, 40, 64, False),
+    ("bf16", 64, 1, 64, True), ("int4", 128, 700, 128, False), ("bf16", 128, 9, 16, False)])
+def test_queries_rotated_in_place(fmt, D, S, rot, inter):
+    """q_out may be q itself: the same bits as into another tensor, padding untouched."""
+    B, Hq, H, page = 2, 12, 2, 32
+    new = [S, S // 2]
+    bt, pages = tables([S + 7] * B, page, 161)
+    cos, sin = (t.cuda() for t in rope(S + 7, rot))
+    g = rng(162)
+    q, k, v = (randn(g, B, h, S, D).cuda() for h in (Hq, H, H))
+    pool = [[t.cuda() for t in pools(fmt, pages, H, page, D, 163)] for _ in range(2)]
+    args = (bt.cuda(), device_ints(0, 7))
+    kw = dict(cos=cos, sin=sin, new_lens=device_ints(*new), interleaved=inter)
+    want = ap.kv_append(k, v, *pool[0], *args, q=q, q_out=q.clone(), **kw)
+    got = q.clone()
+    assert ap.kv_append(k, v, *pool[1], *args, q=got, q_out=got, **kw) is got
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got[1, :, new[1]:], q[1, :, new[1]:])
+    assert S == 1 or not torch.equal(got[0], q[0])       # (position 0 turns by nothing)
+    for a, b in zip(*pool):
+        assert torch.equal(a, b)
