@@ -27,6 +27,7 @@ _CACHE = struct.Struct("@PPPiiiiiii")
 # attn_bhsd_t: data and the strides of the batch, the heads and the tokens
 _BHSD = struct.Struct("@Pqqq")
 KV_BF16, KV_INT4 = 0, 1
+_INT_MAX = 2 ** 31 - 1   # the C entries' sizes are ints
 
 # The checks below cost more than a small call's kernel if each goes through
 # torch's slower accessors, so a call looks at each tensor once, and what is
@@ -155,6 +156,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, start, cos=None, sin=None, q=
     if not isinstance(k, _Tensor) or k.dim() != 4:
         raise TypeError("k must be a [B, H_kv, S, D] tensor")
     S = k.shape[2]
+    if S > _INT_MAX:   # (a view may claim any number of tokens)
+        raise ValueError("S must be below 2^31")
     ks, vs = _bhsd("k", k, (B, heads, S, D), dev), _bhsd("v", v, (B, heads, S, D), dev)
     start_p, new_p = _ints("start", start, B, dev), _ints("new_lens", new_lens, B, dev, True)
     rows = rot = 0

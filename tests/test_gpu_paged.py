@@ -1127,3 +1127,18 @@ def test_queries_rotated_in_place(fmt, D, S, rot, inter):
     assert S == 1 or not torch.equal(got[0], q[0])       # (position 0 turns by nothing)
     for a, b in zip(*pool):
         assert torch.equal(a, b)
+
+
+def test_more_tokens_than_an_int_are_refused():
+    """A view of one token that claims 2^32 + 1 of them: its length must not be cut to 32 bits."""
+    D = 64
+    kc, vc = ap.kv_cache_empty(1, 1, 16, D)
+    kc.zero_(), vc.zero_()
+    bt = torch.zeros((1, 1), dtype=torch.int32).cuda()
+    one = torch.ones((1, 1, 1, D), dtype=torch.bfloat16).cuda()
+    for n in (2 ** 32 + 1, 2 ** 31):
+        many = one.expand(1, 1, n, D)
+        with pytest.raises((ap.AttnError, ValueError)):
+            ap.kv_append(many, many, kc, vc, bt, device_ints(0), new_lens=device_ints(1))
+    torch.cuda.synchronize()
+    assert (kc == 0).all() and (vc == 0).all()
