@@ -1142,3 +1142,26 @@ def test_more_tokens_than_an_int_are_refused():
             ap.kv_append(many, many, kc, vc, bt, device_ints(0), new_lens=device_ints(1))
     torch.cuda.synchronize()
     assert (kc == 0).all() and (vc == 0).all()
+
+
+def test_without_torch_s_short_ways(monkeypatch):
+    """The same bits by way of torch.cuda's public functions, on the current and on another stream,
+    with the workspace that the call allocates freed again."""
+    D, H, page, L = 64, 2, 32, 4000
+    bt, pages = tables([L], page, 181)
+    kc, vc = (t.cuda() for t in pools("int4", pages, H, page, D, 182))
+    btd, n, q = bt.cuda(), device_ints(L), randn(rng(183), 1, 8, 1, D).cuda()
+    want = ap.attn_fwd_paged(q, kc, vc, btd, n, True, 0.1)
+    out = (torch.zeros_like(want[0]), torch.zeros_like(want[1]))
+    ways = ap.paged._short_ways(object())
+    for name, way in zip(("_current_device", "_current_stream", "_alloc", "_free"), ways):
+        monkeypatch.setattr(ap.paged, name, way)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for stream in (None, torch.cuda.Stream()):
+        out[0].zero_(), out[1].zero_()
+        torch.cuda.synchronize()
+        ap.attn_fwd_paged(q, kc, vc, btd, n, True, 0.1, out=out, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    assert torch.cuda.memory_allocated() == before

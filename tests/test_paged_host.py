@@ -195,3 +195,26 @@ def test_reference_attention_matches_torch():
             s = 0.2 * k[h // 2][:20 + i] @ torch.from_numpy(q[0, h, i])
             assert np.allclose(torch.softmax(s, 0) @ v[h // 2][:20 + i], o[0, h, i], atol=1e-12)
             assert np.allclose(torch.logsumexp(s, 0), lse[0, h, i], atol=1e-12)
+
+
+def test_a_torch_without_the_short_ways(monkeypatch):
+    """Where torch has no function of the names that the binding takes first, it takes
+    torch.cuda's own."""
+    class Stream:
+        cuda_stream = 77
+    calls = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: Stream)
+    monkeypatch.setattr(torch.cuda, "caching_allocator_alloc",
+                        lambda n, device=None, stream=None: calls.append((n, stream)) or 0x4000)
+    monkeypatch.setattr(torch.cuda, "caching_allocator_delete", calls.append)
+    device, stream, alloc, free = paged._short_ways(object())
+    assert device() == 3 and stream(3) == 77
+    assert alloc(512, 77) == 0x4000 and free(0x4000) is None
+    assert calls == [(512, 77), 0x4000]
+    # and the first ones where they are there
+    class Names:
+        _cuda_getDevice, _cuda_getCurrentRawStream = (lambda: 5), (lambda dev: dev + 1)
+        _cuda_cudaCachingAllocator_raw_alloc, _cuda_cudaCachingAllocator_raw_delete = max, min
+    got = paged._short_ways(Names)
+    assert got[0]() == 5 and got[1](8) == 9 and got[2:] == (max, min)
