@@ -284,6 +284,12 @@ struct Warp {
   static constexpr int G = D / 32;
   static constexpr int KS = D / 16;
   static constexpr int NB = kInt4 && WR == 8 ? 2 : 1;   // 16-key blocks a step
+  // bf16 numbers whose sum stands for a probability in the second product of a bf16
+  // cache: off by 2^-16 of it with two, by 2^-8 with one.  Two cost a second product, for
+  // which tiles of 8 rows have the time while they wait for memory (32 x 8192 keys
+  // 160.2 us with one, 160.3 with two), but not the larger ones (8 x 4096 keys, 16 rows
+  // 30.9 and 33.2 us, 64 rows 60.3 and 66.5; 8 ragged with 5 queries 23.2 and 25.4).
+  static constexpr int kTerms = WR == 8 ? 2 : 1;
 
   // B fragments of Q (fp16 for a 4-bit cache): [n][32 elements]{two k16 steps}
   uint32_t q[NT][G][4];
@@ -574,11 +580,17 @@ struct Warp {
           }
         }
       } else {
-        uint32_t b0[NT], b1[NT];
+        uint32_t b0[NT][kTerms], b1[NT][kTerms];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          b0[n] = transpose8(pack_bf16x2(pr[i][n][0], pr[i][n][1]));
-          b1[n] = transpose8(pack_bf16x2(pr[i][n][2], pr[i][n][3]));
+          const float (&x)[4] = pr[i][n];
+          const uint32_t p0 = pack_bf16x2(x[0], x[1]), p1 = pack_bf16x2(x[2], x[3]);
+          b0[n][0] = transpose8(p0);
+          b1[n][0] = transpose8(p1);
+          if constexpr (kTerms == 2) {   // and what that leaves (exact in fp32)
+            b0[n][1] = transpose8(pack_bf16x2(x[0] - lo_f(p0), x[1] - hi_f(p0)));
+            b1[n][1] = transpose8(pack_bf16x2(x[2] - lo_f(p1), x[3] - hi_f(p1)));
+          }
         }
         // Values of keys that some row does not see may be anything, and 0 times NaN
         // is NaN: the products take the keys that every row sees (a mask by pairs),
@@ -604,7 +616,9 @@ struct Warp {
                              __byte_perm(w[2][e], w[3][e], 0x7632u)};
             if constexpr (kMasked) a[0] &= keep0, a[1] &= keep0, a[2] &= keep1, a[3] &= keep1;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_bf16(o[4 * sl + e][n], a, b0[n], b1[n]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int x = 0; x < kTerms; ++x) mma_bf16(o[4 * sl + e][n], a, b0[n][x], b1[n][x]);
           }
         }
         // and the few others (a causal tile's newest) are added one by one.

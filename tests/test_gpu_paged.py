@@ -1165,3 +1165,37 @@ def test_without_torch_s_short_ways(monkeypatch):
         torch.cuda.synchronize()
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     assert torch.cuda.memory_allocated() == before
+
+
+# ---------------------------------------------------------------- how exact a bf16 cache's attention is
+
+
+@pytest.mark.parametrize("D,group,Sq,lens,wide", [
+    (128, 4, 1, [500, 37], False), (64, 1, 1, [1000], False), (128, 8, 1, [90, 400], False),
+    (64, 2, 3, [300, 6], False), (128, 4, 1, [6000], True), (64, 1, 8, [2000], True)])
+def test_probabilities_of_up_to_eight_rows_keep_sixteen_bits(D, group, Sq, lens, wide):
+    """With up to eight query rows a KV head the second product takes a probability as the sum of two
+    bf16 numbers: off by half a step of the second, 2^-16 of it.  The bound of O is that of the reference with this share in place of
+    one bf16 number's 2^-8, and exponents of up to 32, of which a subtraction's rounding is 2^-20."""
+    page, B, scale = 64, len(lens), 0.1
+    bt, pages = tables(lens, page, 171)
+    if wide:
+        bt = torch.cat([bt, torch.full((B, 20), -1, dtype=torch.int32)], 1)
+    kc, vc = pools("bf16", pages, 1, page, D, 172)
+    q = randn(rng(173), B, group, Sq, D)
+    o, _ = ap.attn_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), bt.cuda(), device_ints(*lens), True, scale)
+    o, kv, vv, qf = ref.f64(o), ref.f64(kc), ref.f64(vc), ref.f64(q)
+    for b, L in enumerate(lens):
+        k, v = ref.gather(kv, bt[b].numpy(), L, page)[0], ref.gather(vv, bt[b].numpy(), L, page)[0]
+        for h in range(group):
+            for i in range(Sq):
+                n = max(0, L - Sq + i + 1)
+                x = qf[b, h, i]
+                s = scale * (k[:n] @ x)
+                p = np.exp(s - s.max())
+                want, A = p @ v[:n] / p.sum(), p @ np.abs(v[:n]) / p.sum()
+                e = (scale * (np.abs(k[:n]) @ np.abs(x))).max() * 2.0 ** -18 + np.abs(s).max() * 1.5 * 2.0 ** -22 \
+                    + 2.0 ** -20 + 2.0 ** -22
+                tol = 1.01 * (2.0 ** -16 + 2 * e) * A
+                tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
+                assert (np.abs(o[b, h, i] - want) <= tol).all(), (b, h, i, (np.abs(o[b, h, i] - want) / tol).max())
