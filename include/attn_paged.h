@@ -136,9 +136,13 @@ attn_status_t attn_kv_read(const attn_kv_cache_t *cache, void *k_out, void *v_ou
  * lengths; a sequence that ends up on more than one thread block is merged by a
  * second kernel.  Meant for decoding, where S_q is one or a few tokens: each
  * (H_q / H_kv) * S_q <= 64 query rows of a KV head read the cache once, and more
- * rows read it once for every 64.  A whole prompt is faster through attn_fwd,
- * with attn_kv_read for what it shares with the cache.  The results are
- * deterministic for given lengths.
+ * rows read it once for every 64.  A whole prompt is faster through attn_fwd (2048
+ * tokens of 32 heads over 8 of 128: 36 us, here 377): from the first token on, a call
+ * over the new keys; behind a cached prefix two calls, one without mask over the
+ * prefix as attn_kv_read returns it and one causal over the new keys (attn_fwd's mask
+ * begins at its first key), joined by their LSE.  attn_fwd takes one S_q and S_kv a
+ * call, so sequences of different lengths are calls of their own.  The results are
+ * deterministic for given lengths and span of the block table.
  *
  * Arithmetic: fp32 accumulation and softmax statistics.  bf16 cache: for the
  * second product a probability is the sum of two bf16 numbers (off by 2^-16 of it)

@@ -1199,3 +1199,39 @@ def test_probabilities_of_up_to_eight_rows_keep_sixteen_bits(D, group, Sq, lens,
                 tol = 1.01 * (2.0 ** -16 + 2 * e) * A
                 tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
                 assert (np.abs(o[b, h, i] - want) <= tol).all(), (b, h, i, (np.abs(o[b, h, i] - want) / tol).max())
+
+
+@pytest.mark.parametrize("fmt", ["int4", "bf16"])
+def test_prompts_behind_cached_prefixes_in_two_parts(fmt):
+    """attn_fwd's causal mask begins at its first key, so a prompt behind a cached prefix is two of
+    its calls, joined by their log-sum-exps: the prefix as kv_read returns it without mask, the new
+    tokens' keys with.  Against attn_fwd_paged's 64-bit reference: each part's O is rounded to bf16
+    (2^-8) and has probabilities rounded to bf16 (2^-8 of A, the sum of |shares|), which the
+    reference's bound has once, and its scores are in fp32 as the reference's bound takes them;
+    kv_read rounds 4-bit values to bf16, 2^-8 of a value and, through the keys, of a score's terms."""
+    D, Hq, H, page, scale = 64, 4, 2, 32, 0.125
+    for prefix, new in ((37, 20), (300, 129), (64, 1)):
+        L = prefix + new
+        bt, pages = tables([L], page, 191)
+        kc, vc = pools(fmt, pages, H, page, D, 192)
+        q = randn(rng(193), 1, Hq, new, D)
+        n = device_ints(L)
+        kd, vd, bd, qd = kc.cuda(), vc.cuda(), bt.cuda(), q.cuda()
+        k, v = ap.kv_read(kd, vd, bd, n, prefix)
+        k2, v2 = ap.kv_read(kd, vd, bd, n, new, start=device_ints(prefix))
+        parts = [ap.attn_fwd(qd, k, v, False, scale), ap.attn_fwd(qd, k2, v2, True, scale)]
+        lse = torch.logaddexp(parts[0][1], parts[1][1])
+        o = sum(p[0].float() * torch.exp(p[1] - lse)[..., None] for p in parts)
+        kv, ks = ref.cache_values(kc, "k")
+        vv, vs = ref.cache_values(vc, "v")
+        args = bt.numpy(), [L], page, True, scale
+        ro, rl, _, _ = ref.attention(ref.f64(q), kv, vv, ks, vs, *args)
+        ra = ref.attention(ref.f64(q), kv, np.abs(vv), ks, vs, *args)[0]     # A
+        es = scale * max(np.abs(kv[:, h // 2]).reshape(-1, D).max(0) @ np.abs(ref.f64(q[0, h])).max(0)
+                         for h in range(Hq))
+        e = es * (2.0 ** -18 + (2.0 ** -8 if fmt == "int4" else 0)) + 2.0 ** -19
+        tol = (2.0 ** -8 * (2 if fmt == "bf16" else 3) + 2 * e) * 1.02 * ra
+        assert (np.abs(ref.f64(o) - ro) <= tol).all()
+        assert np.abs(ref.f64(lse) - rl).max() <= e + 2.0 ** -8
+        got = ap.attn_fwd_paged(qd, kd, vd, bd, n, True, scale)
+        check_attention(q, kc, vc, bt, [L], True, scale, got)
