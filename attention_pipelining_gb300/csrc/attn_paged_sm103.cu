@@ -37,12 +37,20 @@
 // each CTA writes its part to the workspace and paged_merge_kernel merges them.
 //
 // Measured (device time, D = 128, 32 query heads over 8 KV heads): 32 sequences
-// of 8192 keys, bf16, 1.07 GB: 163 us, 6.6 TB/s, 97 % of the measured HBM copy
-// rate; 4 bits, 303 MB: 67 us, 4.5 TB/s (67 %), with 340 warp-instructions for 16
-// keys, about half of them masks, packed subtractions and scales, that keep 60 % of the
-// issue slots busy; 131072 keys of one sequence, 4 bits: 37 us
-// (60 %).  About 10 us of a call are the beginning (plan, page table and first keys, one
-// after the other: 5 us) and the end (the warps' merge, the CTAs' merge: 5 us).
+// of 8192 keys, bf16, 1.07 GB: 162 us, 6.6 TB/s, 98 % of the measured HBM copy
+// rate; 4 bits, 303 MB: 67 us, 4.5 TB/s (67 %); 131072 keys of one sequence, 4 bits:
+// 37 us (60 %).  What bounds 4 bits is latency: 340 warp-instructions for 16 keys (about
+// half of them masks, packed subtractions and scales) would fill the issue slots for
+// 38 us and the bytes take 45, but with three consumer warps on a scheduler, each in
+// one dependent chain from K's products by the exponentials to V's, there is a ready
+// warp in 60 % of the cycles only.  About 10 us of a call are the beginning (plan, page
+// table and first keys, one after the other: 5 us) and the end (the warps' merge, the
+// CTAs' merge: 5 us).
+//
+// Tiles of 16 rows and more at D = 128 want more registers than the 168 that two
+// blocks of five warps leave a thread, and spill (bf16: 124 to 172 bytes stored, 152 to
+// 228 loaded; 4 bits: 124 to 156 and 152 to 192).  8 sequences of 4096 keys with 1, 5
+// and 16 queries: bf16 27.5, 34.5 and 60.4 us, 4 bits 17.9, 34.4 and 61.2.
 #include <atomic>
 #include <cfloat>
 #include <cmath>
@@ -103,8 +111,9 @@ __device__ __forceinline__ int units_of(const PagedParams& p, int len) {
 }
 
 // An item weighs its units and p.item_cost more, about what the beginning and
-// the end of an item take (64 ragged sequences, 4 bits, with 1, 2 and 4 units of 128 keys:
-// 24.7, 22.1, 24.3 us): the positions 0 .. U - 1 of all items' weights, sequence by
+// the end of an item take (64 ragged sequences, 4 bits, D = 64, with 1, 2 and 4 units of
+// 128 keys: 24.7, 22.1, 24.3 us; the same 256 keys hold for bf16 and for D = 128, where
+// others were not compared): the positions 0 .. U - 1 of all items' weights, sequence by
 // sequence and within it item by item, are dealt out to G CTAs in even
 // consecutive ranges.  The first p.item_cost positions of an item do
 // nothing: its unit k is position p.item_cost + k.
@@ -1140,8 +1149,12 @@ cudaError_t launch(const PagedParams& p0, cudaStream_t stream) {
   PagedParams p = p0;
   p.row_tiles = (int)(((long long)p.group * p.S_q + S::kRows - 1) / S::kRows);
   // Where the block tables span few keys, an item is one unit, which needs no
-  // merge kernel (8 items of 500 keys, 4 bits: 8.2 us, against 9.4 split four ways,
-  // and one launch instead of two)
+  // merge kernel and no workspace.  8 items of 250, 500, 1000 keys, 4 bits: 6.0, 7.5,
+  // 10.7 us whole, 7.9, 8.9, 9.0 split; bf16 6.9, 9.5, 14.7 and 8.4, 8.6, 8.8; 128 items,
+  // 4 bits: 6.5, 7.7, 10.7 and 8.7, 11.0, 12.3; bf16 7.1, 10.3, 15.5 and 10.9, 13.5, 17.3:
+  // whole is faster for many items up to the limit, and on the host for all (8.7 us a call
+  // against 11.5), but not on the device for a few items near it.  The span decides, since the
+  // lengths are on the device: short sequences under a wide table are split.
   const bool split = p.cache.capacity > kPagedWholeKeys;
   p.split = split;
   p.item_cost = kPagedItemKeys / S::kUnit;
@@ -1185,8 +1198,8 @@ cudaError_t sm_count(int* sms) {
 template <int D, bool kInt4>
 cudaError_t launch_rows(const PagedParams& p, int rows, cudaStream_t stream) {
   // No more short items than SMs: blocks of eight consumer warps, one on an SM (128 items of
-  // 1000 keys, D = 128: 11.5 us, 16.4 in bf16, against 14.5 and 18.3 with blocks of
-  // four; 8 items of 500 keys 7.7 and 9.9 against 8.0 and 10.4)
+  // 1000 keys, D = 128: 10.7 us, 15.5 in bf16, against 11.5 and 17.0 with blocks of
+  // four; 8 items of 500 keys 7.5 and 9.5 against 7.7 and 10.4)
   if (rows == 8 && p.cache.capacity <= kPagedWholeKeys) {
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
