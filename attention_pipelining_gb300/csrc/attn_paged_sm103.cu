@@ -85,7 +85,7 @@ constexpr float kNoMax = -3.0e38f;
 // bf16: max_prob is 2^-e with 2^e keys or more in the block table's span, and the
 //   largest probability is set to 2^-(e + 8) at most, so that all sums of
 //   probabilities stay below 1 and those of probabilities times values below the
-//   largest value: no finite value makes an infinite O.
+//   largest value, which fp32 holds.
 constexpr float kMaxProbFp16 = 32768.f;
 constexpr float kTargetLog2Fp16 = 6.f;
 // value scales are taken as at least this when the reference is set, so that
