@@ -147,13 +147,13 @@ attn_status_t attn_kv_read(const attn_kv_cache_t *cache, void *k_out, void *v_ou
  * Arithmetic: fp32 accumulation and softmax statistics.  bf16 cache: for the
  * second product a probability is the sum of two bf16 numbers (off by 2^-16 of it)
  * where (H_q / H_kv) * S_q <= 8, and one (2^-8) with more rows; values up to
- * 3.3e38 (2^-8 below bf16's largest number) give a finite O while scores stay below
- * 2^26 (beyond, an fp32 exponent no longer holds the margin that keeps sums in
- * range).  4-bit cache: the codes are exact in the products, the queries are exact down to 2^-17 of their
- * row's largest element (smaller elements are off by 2^-25 of it at most), and the
- * probabilities times the values' scales are rounded to fp16 (an error of 2^-11
- * of a key's share in O, or of 2^-30 of the largest value that the query sees, or
- * 2^-90, where that is more).
+ * 3.3e38 (a rounding by 2^-8 may lift larger ones out of bf16's range) give a
+ * finite O while scores stay below 2^26 (beyond, an fp32 exponent no longer holds the
+ * margin that keeps sums in range).  4-bit cache: the codes are exact in the
+ * products, the queries are exact down to 2^-17 of their row's largest element
+ * (smaller elements are off by 2^-25 of it at most), and the probabilities times the
+ * values' scales are rounded to fp16 (an error of 2^-11 of a key's share in O, or of
+ * 2^-30 of the largest value that the query sees, or 2^-90, where that is more).
  */
 attn_status_t attn_fwd_paged(const attn_kv_cache_t *cache, const attn_bhsd_t *q, void *o,
                              float *lse, const int *lens, const int *q_lens, void *workspace,
