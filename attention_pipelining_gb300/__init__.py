@@ -21,7 +21,8 @@ from ._build import LIB as _LIB_PATH, build as _build_lib
 __all__ = ["attn_fwd", "attn_fwd_out", "attn_fwd_host", "attn_fwd_trace", "attn_fwd_splitkv",
            "splitkv_default_splits", "attn_bwd", "attn_bwd_host", "bwd_workspace_bytes",
            "chunk_scan", "chunk_scan_host", "kv_cache_empty", "kv_append", "kv_read",
-           "attn_fwd_paged", "paged_workspace_bytes", "selftest_qk", "selftest_pv", "device_status", "status_string",
+           "attn_fwd_paged", "paged_workspace_bytes", "rope_packed", "attn_fwd_packed",
+           "attn_bwd_packed", "packed_workspace_bytes", "packed_bwd_workspace_bytes", "selftest_qk", "selftest_pv", "device_status", "status_string",
            "lib_path", "build", "AttnError", "STATUS"]
 
 STATUS = {
@@ -44,7 +45,8 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_status_string", "attn_device_statu
            "attn_bwd_workspace_bytes", "attn_bwd_timeout_test",
            "attn_bwd_host", "chunk_scan_fwd", "chunk_scan_fwd_host",
            "attn_kv_append", "attn_kv_read", "attn_fwd_paged", "attn_paged_workspace_bytes",
-           "attn_fwd_paged_timeout_test"]
+           "attn_fwd_paged_timeout_test", "attn_rope_packed", "attn_fwd_packed", "attn_bwd_packed",
+           "attn_packed_workspace_bytes", "attn_packed_bwd_workspace_bytes"]
 
 
 class AttnError(RuntimeError):
@@ -132,6 +134,16 @@ def _load():
     lib.attn_fwd_paged_timeout_test.restype = ci
     lib.attn_paged_workspace_bytes.argtypes = [ci] * 6
     lib.attn_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_rope_packed.argtypes = [vp] * 6 + [ci] + [vp] * 2 + [ci] * 8 + [vp]
+    lib.attn_rope_packed.restype = ci
+    lib.attn_fwd_packed.argtypes = [vp] * 9 + [ctypes.c_size_t, vp]
+    lib.attn_fwd_packed.restype = ci
+    lib.attn_bwd_packed.argtypes = [vp] * 13 + [ctypes.c_size_t, ci, vp]
+    lib.attn_bwd_packed.restype = ci
+    lib.attn_packed_workspace_bytes.argtypes = [vp]
+    lib.attn_packed_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_packed_bwd_workspace_bytes.argtypes = [vp, ci]
+    lib.attn_packed_bwd_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -437,8 +449,8 @@ def selftest_pv(p, v):
 
 
 def device_status(reset: bool = True) -> int:
-    """The device-side status word (0, 5 = a kernel wait timed out, or 6 = a paged-cache kernel met
-    an index out of range)."""
+    """The device-side status word (0, 5 = a kernel wait timed out, or 6 = a kernel of the paged
+    cache or of packed sequences met an index out of range)."""
     st = ctypes.c_int(0)
     _check(_load().attn_device_status(ctypes.byref(st), int(bool(reset))), "attn_device_status")
     return st.value
@@ -446,3 +458,5 @@ def device_status(reset: bool = True) -> int:
 
 from .paged import (attn_fwd_paged, kv_append, kv_cache_empty, kv_read,  # noqa: E402
                     paged_workspace_bytes)
+from .packed import (attn_bwd_packed, attn_fwd_packed, packed_bwd_workspace_bytes,  # noqa: E402
+                     packed_workspace_bytes, rope_packed)

@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libattn_gb300.so")
 
 SOURCES = ["attn_fwd_sm103.cu", "attn_api.cu", "selftest.cu", "attn_combine.cu",
            "attn_noalloc.cu", "attn_bwd_sm103.cu", "chunk_scan_sm103.cu",
-           "attn_paged_sm103.cu", "kv_cache_sm103.cu", "attn_paged_api.cu"]
+           "attn_paged_sm103.cu", "kv_cache_sm103.cu", "attn_paged_api.cu",
+           "packed_sm103.cu", "attn_packed_api.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -58,18 +58,30 @@ attn_status_t check_device() {
   return ATTN_OK;
 }
 
-bool encode_bf16_map_3d(CUtensorMap* map, const void* base, uint64_t D, uint64_t rows,
-                        uint64_t outer, uint32_t box_rows) {
+// {D, d1, d2} with the strides (bytes) of the last two, box {64, box1, box2}.
+static bool encode_map(CUtensorMap* map, const void* base, uint64_t D, uint64_t d1, uint64_t d2,
+                       uint64_t stride1, uint64_t stride2, uint32_t box1, uint32_t box2) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {D, rows, outer};
-  cuuint64_t strides[2] = {D * 2, rows * D * 2};  // bytes, for dims 1 and 2
-  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint64_t dims[3] = {D, d1, d2};
+  cuuint64_t strides[2] = {stride1, stride2};
+  cuuint32_t box[3] = {64, box1, box2};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool encode_bf16_map_3d(CUtensorMap* map, const void* base, uint64_t D, uint64_t rows,
+                        uint64_t outer, uint32_t box_rows) {
+  return encode_map(map, base, D, rows, outer, D * 2, rows * D * 2, box_rows, 1);
+}
+
+bool encode_bf16_map_thd(CUtensorMap* map, const void* base, uint64_t D, uint64_t heads,
+                         uint64_t tokens, uint64_t stride_h, uint64_t stride_t,
+                         uint32_t box_heads, uint32_t box_tokens) {
+  return encode_map(map, base, D, heads, tokens, stride_h * 2, stride_t * 2, box_heads, box_tokens);
 }
 
 // Pure argument checks (no CUDA calls), shared by the entry points.
@@ -109,7 +121,7 @@ namespace attnpipe {
 // runs as the smallest normal float of the same sign: then every scaled
 // score of magnitude below 2^100 is under 2^-26, and its probability rounds
 // to exactly 1, as with a zero scale.
-static float scale_log2_of(float scale) {
+float scale_log2_of(float scale) {
   const float v = (float)((double)scale * 1.4426950408889634);
   if (v == 0.f) return std::signbit(scale) ? -FLT_MIN : FLT_MIN;
   return v;
@@ -910,17 +922,19 @@ attn_status_t attn_device_status(int* status_out, int reset) {
   attn_status_t st = check_device();
   if (st != ATTN_OK) return st;
   int main_status = 0, selftest_status = 0, bwd_status = 0, cs_status = 0;
-  int kv_status = 0, paged_status = 0;
+  int kv_status = 0, paged_status = 0, packed_status = 0;
   if (read_device_status(&main_status, reset != 0) != cudaSuccess ||
       read_selftest_status(&selftest_status, reset != 0) != cudaSuccess ||
       read_bwd_status(&bwd_status, reset != 0) != cudaSuccess ||
       read_chunk_scan_status(&cs_status, reset != 0) != cudaSuccess ||
       read_kv_status(&kv_status, reset != 0) != cudaSuccess ||
-      read_paged_status(&paged_status, reset != 0) != cudaSuccess)
+      read_paged_status(&paged_status, reset != 0) != cudaSuccess ||
+      read_packed_status(&packed_status, reset != 0) != cudaSuccess)
     return ATTN_ERR_CUDA;
   // A timeout says more than an index out of range: outputs are then unspecified.
   *status_out = ATTN_OK;
-  for (int s : {main_status, bwd_status, cs_status, kv_status, paged_status, selftest_status})
+  for (int s : {main_status, bwd_status, cs_status, kv_status, paged_status, packed_status,
+                selftest_status})
     if (s == ATTN_ERR_TIMEOUT || *status_out == ATTN_OK) *status_out = s;
   return ATTN_OK;
 }

@@ -36,6 +36,15 @@
 // elected lane issues), warps 10-11 idle, warps 12-15 the dQ read-out.
 // Every wait is bounded; a timeout raises a CTA-wide abort flag and the
 // device status word records ATTN_ERR_TIMEOUT.
+//
+// Packed sequences (the kPacked instantiations, include/attn_packed.h): both paths
+// over lists of key blocks and query tiles of all sequences that a plan kernel made.
+// A query tile's 128 rows are whole groups of query heads of consecutive tokens
+// (row = token * R + head); the row vectors and the accumulator follow that order,
+// [K/V head][token * R + head], so a tile's rows of them are contiguous.  Behind a
+// sequence's end the copies bring other sequences' rows: where these would meet a
+// zero of P or dS in a sum over rows or keys (0 times an infinity is a NaN) the
+// issuer warp clears them in shared memory first.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -43,6 +52,7 @@
 
 #include "attn_internal.h"
 #include "attn_tiles.cuh"
+#include "kv_cache.cuh"
 #include "ptx.cuh"
 
 namespace attnpipe {
@@ -273,6 +283,9 @@ __device__ __forceinline__ void banded_rank(int idx, int n_ranks, int groups, in
   }
 }
 
+template <bool kPacked>
+using BwdParamsOf = std::conditional_t<kPacked, PackedBwdParams, BwdParams>;
+
 }  // namespace
 
 // ---------------------------------------------------------------- prep
@@ -348,6 +361,99 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const BwdParams p,
   }
 }
 
+// The same for packed sequences: rows are (token, head) in the order of O, and
+// the vectors' place of a token's follows from its sequence, found by bisection.
+template <int D>
+__global__ void __launch_bounds__(256)
+    packed_bwd_prep_kernel(const __grid_constant__ PackedBwdParams p, const uint16_t* o,
+                           const uint16_t* dout, const float* lse) {
+  constexpr int kLanesPerRow = D * 2 / 16;
+  constexpr int kRowsPerLoad = 32 / kLanesPerRow;
+  constexpr int kLoads = kPrepRowsPerWarp / kRowsPerLoad;
+  const long long row0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kPrepRowsPerWarp;
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / kLanesPerRow, piece = lane % kLanesPerRow;
+  allow_later();
+  wait_for_earlier();
+  const int q_first = p.sh.head->q_first, q_end = p.sh.head->q_end;
+  uint4 a[kLoads], b[kLoads];
+  int tok[kLoads], head[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const long long row = row0 + i * kRowsPerLoad + sub;
+    const long long t = row / p.H_q;
+    head[i] = (int)(row - t * p.H_q);
+    tok[i] = t >= q_first && t < q_end ? (int)t : -1;
+    a[i] = make_uint4(0u, 0u, 0u, 0u);
+    b[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tok[i] >= 0) {
+      a[i] = *reinterpret_cast<const uint4*>(o + t * p.o_st + head[i] * p.o_sh + piece * 8);
+      b[i] = *reinterpret_cast<const uint4*>(dout + t * p.do_st + head[i] * p.do_sh + piece * 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const uint32_t av[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+    const uint32_t bv[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+    float acc = 0.f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      acc += __uint_as_float(av[t] << 16) * __uint_as_float(bv[t] << 16);
+      acc += __uint_as_float(av[t] & 0xffff0000u) * __uint_as_float(bv[t] & 0xffff0000u);
+    }
+#pragma unroll
+    for (int off = kLanesPerRow / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(kAll, acc, off);
+    if (tok[i] < 0) continue;
+    const int group = p.sh.group, g = head[i] / group, r = head[i] - g * group;
+    if (p.dq_acc != nullptr) {
+      float4* z = reinterpret_cast<float4*>(
+          p.dq_acc + (((long long)g * p.sh.T_q + tok[i]) * group + r) * D + piece * 8);
+      z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+      z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (piece == 0) {
+      int b0 = 0, b1 = p.B;   // seq_q[b0] <= tok < seq_q[b1]
+      while (b1 - b0 > 1) {
+        const int mid = (b0 + b1) >> 1;
+        if (p.seq_q[mid] <= tok[i]) b0 = mid;
+        else b1 = mid;
+      }
+      const int q0 = p.seq_q[b0];
+      const long long at =
+          g * p.vec_stride + (long long)(packed_vec0(q0, b0) + tok[i] - q0) * group + r;
+      p.ndelta[at] = -acc;
+      p.nlse2[at] = -(lse[(long long)head[i] * p.sh.T_q + tok[i]] * 1.4426950408889634f);
+    }
+  }
+}
+
+// dq = bf16(scale * dq_acc) over the tokens of the packed sequences; one thread per 8
+// elements.
+template <int D>
+__global__ void __launch_bounds__(256)
+    packed_bwd_dq_convert_kernel(const __grid_constant__ PackedBwdParams p) {
+  constexpr int kPieces = D / 8;
+  wait_for_earlier();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long row = i / kPieces;   // (K/V head, token, head in the group)
+  const int piece = (int)(i - row * kPieces);
+  const long long gt = row / p.sh.group;
+  const int r = (int)(row - gt * p.sh.group);
+  const int g = (int)(gt / p.sh.T_q);
+  const long long t = gt - (long long)g * p.sh.T_q;
+  if (g >= p.H_kv || t < p.sh.head->q_first || t >= p.sh.head->q_end) return;
+  const float4* src = reinterpret_cast<const float4*>(p.dq_acc + row * D + piece * 8);
+  const float4 a = src[0], b = src[1];
+  const float sc = p.scale;
+  uint4 out;
+  out.x = pack_bf16x2(a.x * sc, a.y * sc);
+  out.y = pack_bf16x2(a.z * sc, a.w * sc);
+  out.z = pack_bf16x2(b.x * sc, b.y * sc);
+  out.w = pack_bf16x2(b.z * sc, b.w * sc);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dq) + t * p.dq_st +
+                            (g * p.sh.group + r) * p.dq_sh + piece * 8) = out;
+}
+
 // dq = bf16(scale * dq_acc) over the rows of every group (padding rows
 // skipped); one thread per 8 elements.
 template <int D>
@@ -378,9 +484,9 @@ __global__ void __launch_bounds__(256) attn_bwd_dq_convert_kernel(const BwdParam
 // into the half's dP^T columns, and warps 12-15 read it out and add it into
 // the fp32 accumulator p.dq_acc in L2 (red.global.add); dS^T for dK then
 // sits in tensor memory next to P^T.  512 threads.
-template <int D, bool kFuse>
+template <int D, bool kFuse, bool kPacked = false>
 __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
-    attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
+    attn_bwd_dkdv_kernel(const __grid_constant__ BwdParamsOf<kPacked> p) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw_b[];
   uint8_t* smem = align_smem_1024(smem_raw_b);
@@ -407,21 +513,40 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // blocks carry the most query blocks, so they go first (in bands, see
   // banded_rank); without it the blocks of one group are adjacent (they
   // share their Q and dO tiles in L2)
-  const int n_kvb = (p.S_kv + kRows - 1) / kRows;
+  //
+  // (packed: an entry of the list and a K/V head, in bands of entries as well)
+  const int n_kvb = kPacked ? 0 : (p.S_kv + kRows - 1) / kRows;
   int kvb, zkv;
-  if (p.causal) {
+  int n_keys = 0, tok_k = 0;   // packed: keys of the block, its first token
+  int tok_q = 0, q_len = 0, vec0 = 0, shift = 0, first_tile = 0, n_tiles = 0;   // and PackedKeys' others
+  if constexpr (kPacked) {
+    wait_for_earlier();
+    const int entries = p.sh.head->key_blocks;
+    if ((long long)blockIdx.x >= (long long)entries * p.H_kv) return;
+    banded_rank((int)blockIdx.x, entries, p.H_kv, kvb, zkv);
+    const int4* src = reinterpret_cast<const int4*>(p.sh.keys + kvb);
+    const int4 a = src[0], b = src[1];   // in PackedKeys' order
+    tok_k = a.x;
+    n_keys = a.y;
+    tok_q = a.z;
+    q_len = a.w;
+    vec0 = b.x;
+    shift = b.y;
+    first_tile = b.z;
+    n_tiles = b.w;
+  } else if (p.causal) {
     banded_rank((int)blockIdx.x, n_kvb, p.groups, kvb, zkv);
   } else {
     zkv = blockIdx.x / n_kvb;
     kvb = blockIdx.x - zkv * n_kvb;
   }
   const int kv0 = kvb * kRows;              // first key of the block
-  const int n_qb = (p.R + kRows - 1) / kRows;
+  const int n_qb = kPacked ? n_tiles : (p.R + kRows - 1) / kRows;
   // the order every role walks the query blocks in: with kFuse and no mask
   // rotated by the key block, so the CTAs running at once add into
   // different dQ rows (with the causal mask each key block starts at its own
   // diagonal anyway)
-  const int rot = (kFuse && !p.causal) ? kvb % n_qb : 0;
+  const int rot = kPacked ? first_tile : (kFuse && !p.causal) ? kvb % n_qb : 0;
   auto qb_at = [&](int i) { return i + rot < n_qb ? i + rot : i + rot - n_qb; };
   // The query blocks with work (items n = 0 .. n_work - 1), walked by every
   // role in the same order.  With the causal mask and S_q a multiple of 128
@@ -430,11 +555,11 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // those blocks of each head in turn, found without a scan (a scan's
   // division per skipped block cost a short CTA tens of microseconds).
   // Otherwise (a ragged S_q) the blocks are scanned with qblock_sees.
-  const bool by_head = p.causal && (p.S_q % kRows == 0);
+  const bool by_head = !kPacked && p.causal && (p.S_q % kRows == 0);
   const int nqh = by_head ? p.S_q / kRows : 1;             // position blocks per head
   const int per_head = by_head ? (nqh > kvb ? nqh - kvb : 0) : 0;
   int n_work = 0;
-  if (!p.causal) {
+  if (kPacked || !p.causal) {
     n_work = n_qb;
   } else if (by_head) {
     n_work = (p.R / p.S_q) * per_head;
@@ -444,6 +569,9 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // first row of item n's query block; `cursor` is the caller's scan
   // position (the ragged causal case only; items are asked for in order)
   auto item_r0 = [&](int n, int& cursor) -> int {
+    // (packed: the tile's first query position)
+    if constexpr (kPacked)
+      return (p.causal ? first_tile + n : qb_at(n)) * p.sh.positions;
     if (!p.causal) return qb_at(n) * kRows;
     if (by_head) {
       const int h = n / per_head;
@@ -474,6 +602,13 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     *sAbort = 0;
     fence_mbar_init();
   }
+  if constexpr (kPacked) {
+    // the spare rows of the Q and dO tiles, which no copy writes
+    const int spare = p.sh.group * p.sh.positions;
+    if (spare < kRows && warp < 2 * C::kQStages)
+      clear_rows<D>(smem + C::kOffQRing + (warp >> 1) * C::kQStageBytes + (warp & 1) * C::kTileBytes,
+                    spare);
+  }
   if (warp == 8) {
     tmem_alloc(sTmemBase, C::kTmemCols);
     tmem_relinquish();
@@ -500,7 +635,8 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;          // key row within the block
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const int key = kv0 + r;
+    const int key = kPacked ? r : kv0 + r;         // (packed: within the block)
+    const int key_end = kPacked ? n_keys : p.S_kv;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     bool ok = true;
@@ -523,9 +659,19 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       const int s = n % C::kQStages;
       // masking: rows past R, keys past S_kv, and (causal) keys after a row's
       // position; a block needs none when every row sees every key
-      bool masked = (r0 + kRows > p.R) || (kv0 + kRows > p.S_kv);
+      bool masked;
       int base_pos = 0;
-      if (p.causal) {
+      int row_lo = 0, row_hi = kRows;   // packed: the tile's rows that see this thread's key
+      if constexpr (kPacked) {
+        const int group = p.sh.group;
+        row_hi = min(q_len - r0, p.sh.positions) * group;
+        masked = row_hi < kRows || n_keys < kRows || (p.causal && r0 < shift + kRows - 1);
+        if (p.causal) row_lo = min(max(key + shift - r0, 0), kRows) * group;
+        if (key >= n_keys) row_hi = 0;
+      } else {
+        masked = (r0 + kRows > p.R) || (kv0 + kRows > p.S_kv);
+      }
+      if (!kPacked && p.causal) {
         base_pos = r0 % p.S_q;
         const bool one_head = (base_pos + kRows <= p.S_q);
         masked = masked || !(one_head && base_pos >= kv0 + kRows - 1);
@@ -570,7 +716,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float pv = ex2_approx(x[e]);
-              if constexpr (kMasked) {
+              if constexpr (kMasked && kPacked) {
+                const int row = col0 + c + e;
+                pv = row >= row_lo && row < row_hi ? pv : 0.f;
+              } else if constexpr (kMasked) {
                 const int rho = r0 + col0 + c + e;
                 bool vis = (rho < p.R) && (key < p.S_kv);
                 if (p.causal) {
@@ -597,6 +746,14 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
             float d0, d1, d2, d3;
             f2_unpack(ds01, d0, d1);
             f2_unpack(ds23, d2, d3);
+            if constexpr (kMasked && kPacked) {
+              // (what a masked dP or D holds may be another sequence's infinity)
+              const int row = col0 + c;
+              d0 = row >= row_lo && row < row_hi ? d0 : 0.f;
+              d1 = row + 1 >= row_lo && row + 1 < row_hi ? d1 : 0.f;
+              d2 = row + 2 >= row_lo && row + 2 < row_hi ? d2 : 0.f;
+              d3 = row + 3 >= row_lo && row + 3 < row_hi ? d3 : 0.f;
+            }
             pk[2 * i4] = pack_bf16x2(pr[0], pr[1]);
             pk[2 * i4 + 1] = pack_bf16x2(pr[2], pr[3]);
             dk[2 * i4] = pack_bf16x2(d0, d1);
@@ -644,9 +801,16 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       if (!warp_wait_b(acc_done, 0, sAbort, budget)) { ok = false; have_acc = false; }
       tc_fence_after_sync();
     }
-    const bool row_ok = key < p.S_kv;
-    uint16_t* dk_row = static_cast<uint16_t*>(p.dk) + ((size_t)zkv * p.S_kv + key) * D;
-    uint16_t* dv_row = static_cast<uint16_t*>(p.dv) + ((size_t)zkv * p.S_kv + key) * D;
+    const bool row_ok = key < key_end;
+    uint16_t* dk_row = static_cast<uint16_t*>(p.dk);
+    uint16_t* dv_row = static_cast<uint16_t*>(p.dv);
+    if constexpr (kPacked) {
+      dk_row += (long long)(tok_k + key) * p.dk_st + zkv * p.dk_sh;
+      dv_row += (long long)(tok_k + key) * p.dv_st + zkv * p.dv_sh;
+    } else {
+      dk_row += ((size_t)zkv * p.S_kv + key) * D;
+      dv_row += ((size_t)zkv * p.S_kv + key) * D;
+    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {  // 0: dV, 1: dK
       uint16_t* dst = which ? dk_row : dv_row;
@@ -687,6 +851,22 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const uint32_t tdV = tmem + C::kTmAcc0, tdK = tmem + C::kTmAcc1;
     bool ok = n_work > 0 &&
               warp_wait_b(C::kKVinTmem ? kt_ready : kv_full, 0, sAbort, budget);
+    // packed: what the copies brought from behind the sequence's end, cleared (K for
+    // dQ^T = K^T dS^T; a query tile for dV += P^T dO and dK += dS^T Q)
+    if constexpr (kPacked && kFuse) {
+      if (ok && n_keys < kRows) clear_rows<D>(sK, n_keys);
+    }
+    auto clear_tile = [&](int n) {
+      if constexpr (kPacked) {
+        int cursor = 0;
+        const int rows = (q_len - item_r0(n, cursor)) * p.sh.group;
+        const int s = n % C::kQStages;
+        if (rows < p.sh.group * p.sh.positions) {
+          clear_rows<D>(stage_q(s), rows);
+          clear_rows<D>(stage_do(s), rows);
+        }
+      }
+    };
     // S^T and dP^T of half h of work item n (its Q / dO stage is loaded);
     // at D = 64 K and V are read from tensor memory
     auto issue_sp = [&](int n, int h) {
@@ -704,6 +884,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     };
     if (ok && warp_wait_b(&q_full[0], 0, sAbort, budget)) {
       tc_fence_after_sync();
+      clear_tile(0);
       issue_sp(0, 0);
       issue_sp(0, 1);
     } else {
@@ -743,6 +924,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
               break;
             }
             tc_fence_after_sync();
+            clear_tile(n + 1);
           }
           if constexpr (kFuse) {
             // ... and over this half's dQ^T once it has been read out
@@ -768,8 +950,13 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     bool ok = n_work > 0;
     if (ok && leader) {
       mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
-      tma_load_tile<D>(sK, &p.tm_k, kv_full, kv0, zkv, pol_kv);
-      tma_load_tile<D>(sV, &p.tm_v, kv_full, kv0, zkv, pol_kv);
+      if constexpr (kPacked) {
+        tma_load_tile<D>(sK, &p.tm_k, kv_full, zkv, tok_k, pol_kv);
+        tma_load_tile<D>(sV, &p.tm_v, kv_full, zkv, tok_k, pol_kv);
+      } else {
+        tma_load_tile<D>(sK, &p.tm_k, kv_full, kv0, zkv, pol_kv);
+        tma_load_tile<D>(sV, &p.tm_v, kv_full, kv0, zkv, pol_kv);
+      }
     }
     int cursor = 0;
     for (int n = 0; n < n_work && ok; ++n) {
@@ -781,10 +968,20 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         break;
       }
       if (leader) {
-        mbar_arrive_expect_tx(&q_full[s], 2 * C::kTileBytes + 2 * C::kVecBytes);
-        tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], r0, zkv, pol_q);
-        tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], r0, zkv, pol_q);
-        const size_t vo = (size_t)zkv * p.Rp + r0;
+        size_t vo;
+        if constexpr (kPacked) {
+          const int group = p.sh.group;
+          mbar_arrive_expect_tx(&q_full[s],
+                                (uint32_t)(2 * group * p.sh.positions * D * 2) + 2 * C::kVecBytes);
+          tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], zkv * group, tok_q + r0, pol_q);
+          tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], zkv * group, tok_q + r0, pol_q);
+          vo = (size_t)(zkv * p.vec_stride + (long long)(vec0 + r0) * group);
+        } else {
+          mbar_arrive_expect_tx(&q_full[s], 2 * C::kTileBytes + 2 * C::kVecBytes);
+          tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], r0, zkv, pol_q);
+          tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], r0, zkv, pol_q);
+          vo = (size_t)zkv * p.Rp + r0;
+        }
         bulk_load(stage_lse(s), p.nlse2 + vo, C::kVecBytes, &q_full[s]);
         bulk_load(stage_delta(s), p.ndelta + vo, C::kVecBytes, &q_full[s]);
       }
@@ -841,10 +1038,21 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         reg_after_wait(v1);
         tc_fence_before_sync();
         mbar_arrive(&dq_free[h]);            // the columns may be overwritten
-        const int q0 = r0 + 64 * h;
+        // rows of the half that exist (those past R, or a packed tile's past its
+        // sequence's end, are skipped), and their accumulators
+        int rows;
+        float* acc;
+        if constexpr (kPacked) {
+          const int group = p.sh.group;
+          rows = min(q_len - r0, p.sh.positions) * group - 64 * h;
+          acc = p.dq_acc +
+                (((long long)zkv * p.sh.T_q + tok_q + r0) * group + 64 * h) * D;
+        } else {
+          rows = p.R - (r0 + 64 * h);
+          acc = p.dq_acc + ((size_t)zkv * p.Rp + r0 + 64 * h) * D;
+        }
         if constexpr (D == 128) {
-          const int rows = p.R - q0;           // rows past R are padding: skipped
-          float* dst = p.dq_acc + ((size_t)zkv * p.Rp + q0) * D + d;
+          float* dst = acc + d;
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (j < rows) red_add_f32(dst + (size_t)j * D, u2f_b(v0[j]));
@@ -862,10 +1070,8 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
           fence_proxy_async_smem();            // the bulk copy reads through the async proxy
           named_barrier_sync(1, 128);
           if (threadIdx.x == 12 * 32) {
-            const int rows = min(64, p.R - q0);  // rows past R are padding: skipped
             if (rows > 0)
-              bulk_reduce_add_f32(p.dq_acc + ((size_t)zkv * p.Rp + q0) * D, smem_u32(stg),
-                                  (uint32_t)rows * D * 4);
+              bulk_reduce_add_f32(acc, smem_u32(stg), (uint32_t)min(rows, 64) * D * 4);
             tma_store_commit();                // one group per half, possibly empty
           }
           ++nh;
@@ -885,8 +1091,9 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 
 // ---------------------------------------------------------------- dQ
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
+template <int D, bool kPacked = false>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    attn_bwd_dq_kernel(const __grid_constant__ BwdParamsOf<kPacked> p) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw_b[];
   uint8_t* smem = align_smem_1024(smem_raw_b);
@@ -909,29 +1116,64 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
   // longest first (with S_q a multiple of 128 a rank is one position block
   // of one head of the group, so the group's heads interleave), in bands
   // (see banded_rank); without it group-major, query blocks last to first
-  const int n_qb = (p.R + kRows - 1) / kRows;
-  int qb, zkv;
-  if (p.causal) {
-    int rank;
-    banded_rank((int)blockIdx.x, n_qb, p.groups, rank, zkv);
-    const int hr = p.R / p.S_q;  // heads per group
-    if (p.S_q % kRows == 0) {
-      const int nh = p.S_q / kRows;
-      qb = (rank % hr) * nh + (nh - 1 - rank / hr);
-    } else {
-      qb = n_qb - 1 - rank;
+  //
+  // (packed: a half of a tile of the list, and a K/V head, in bands of tiles)
+  int zkv, r0 = 0, n_kb;
+  int n_rows = kRows;                                   // packed: the tile's rows that exist
+  int tok_q = 0, tok_k = 0, k_len = 0, n_keys = 0, diag = 0, vec0 = 0;   // and PackedTile's others
+  if constexpr (kPacked) {
+    wait_for_earlier();
+    const int entries = p.sh.head->tiles, positions = p.sh.positions;
+    const int half = (int)(blockIdx.x & 1);
+    if ((long long)(blockIdx.x >> 1) >= (long long)entries * p.H_kv) return;
+    int entry;
+    banded_rank((int)(blockIdx.x >> 1), entries, p.H_kv, entry, zkv);
+    const int4* src = reinterpret_cast<const int4*>(p.sh.tiles + entry);
+    const int4 a = src[0], b = src[1];   // in PackedTile's order
+    const int rows = a.y - half * positions;
+    if (rows <= 0) return;
+    n_rows = min(rows, positions) * p.sh.group;
+    tok_q = a.x + half * positions;
+    tok_k = a.z;
+    k_len = a.w;
+    diag = b.y + half * positions;
+    n_keys = p.causal ? min(max(diag + min(rows, positions) - 1, 0), k_len) : k_len;
+    vec0 = b.z + half * positions;
+    n_kb = (n_keys + kRows - 1) / kRows;
+    if (n_kb == 0) {   // no row sees a key: dQ = 0
+      for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreadsB) {
+        const int row = i / (D / 8), at = (row * p.sh.inv_group) >> 16;
+        uint16_t* dst = static_cast<uint16_t*>(p.dq) + (long long)(tok_q + at) * p.dq_st +
+                        (zkv * p.sh.group + row - at * p.sh.group) * p.dq_sh + i % (D / 8) * 8;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      return;
     }
   } else {
-    zkv = blockIdx.x / n_qb;
-    qb = n_qb - 1 - (blockIdx.x - zkv * n_qb);
+    const int n_qb = (p.R + kRows - 1) / kRows;
+    int qb;
+    if (p.causal) {
+      int rank;
+      banded_rank((int)blockIdx.x, n_qb, p.groups, rank, zkv);
+      const int hr = p.R / p.S_q;  // heads per group
+      if (p.S_q % kRows == 0) {
+        const int nh = p.S_q / kRows;
+        qb = (rank % hr) * nh + (nh - 1 - rank / hr);
+      } else {
+        qb = n_qb - 1 - rank;
+      }
+    } else {
+      zkv = blockIdx.x / n_qb;
+      qb = n_qb - 1 - (blockIdx.x - zkv * n_qb);
+    }
+    r0 = qb * kRows;
+    int kv_end = p.S_kv;
+    if (p.causal) {
+      const int last = min(r0 + kRows, p.R) - 1;
+      kv_end = min(p.S_kv, (r0 / p.S_q == last / p.S_q) ? last % p.S_q + 1 : p.S_q);
+    }
+    n_kb = (kv_end + kRows - 1) / kRows;   // >= 1: every row sees key 0
   }
-  const int r0 = qb * kRows;
-  int kv_end = p.S_kv;
-  if (p.causal) {
-    const int last = min(r0 + kRows, p.R) - 1;
-    kv_end = min(p.S_kv, (r0 / p.S_q == last / p.S_q) ? last % p.S_q + 1 : p.S_q);
-  }
-  const int n_kb = (kv_end + kRows - 1) / kRows;   // >= 1: every row sees key 0
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -968,12 +1210,23 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
     const int r = (warp & 3) * 32 + lane;          // query row within the block
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int rho = r0 + r;
-    const bool row_ok = rho < p.R;
-    const size_t vo = (size_t)zkv * p.Rp + rho;    // in the padded layout (rho < Rp)
+    const bool row_ok = kPacked ? r < n_rows : rho < p.R;
+    // in the padded layout (rho < Rp; packed: the vectors go on behind the last tile)
+    size_t vo;
+    if constexpr (kPacked)
+      vo = (size_t)(zkv * p.vec_stride + (long long)vec0 * p.sh.group + r);
+    else
+      vo = (size_t)zkv * p.Rp + rho;
     const uint64_t nlse2x2 = f2_pack(p.nlse2[vo], p.nlse2[vo]);  // -LSE * log2(e), twice
     const uint64_t ndl2 = f2_pack(p.ndelta[vo], p.ndelta[vo]);    // -D_i, twice
-    const int pos = rho % p.S_q;
-    const int key_limit = p.causal ? min(p.S_kv, pos + 1) : p.S_kv;
+    int key_limit, at = 0;
+    if constexpr (kPacked) {
+      at = (r * p.sh.inv_group) >> 16;             // the row's query token
+      key_limit = p.causal ? min(n_keys, diag + at) : n_keys;
+    } else {
+      const int pos = rho % p.S_q;
+      key_limit = p.causal ? min(p.S_kv, pos + 1) : p.S_kv;
+    }
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     // Q (warpgroup 0) and dO (warpgroup 1) into tensor memory, the A
@@ -1018,6 +1271,11 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
             float d0, d1;
             f2_unpack(f2_mul(f2_pack(p0, p1),
                              f2_add(f2_pack(u2f_b(dp[c]), u2f_b(dp[c + 1])), ndl2)), d0, d1);
+            if constexpr (kMasked && kPacked) {
+              // (what a masked dP holds may be another sequence's infinity)
+              d0 = (row_ok && kb0 + col0 + c < key_limit) ? d0 : 0.f;
+              d1 = (row_ok && kb0 + col0 + c + 1 < key_limit) ? d1 : 0.f;
+            }
             dk[i] = pack_bf16x2(d0, d1);
           }
         };
@@ -1036,7 +1294,12 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
     // ---------------------------------------------------------- epilogue
     if (ok && warp_wait_b(acc_done, 0, sAbort, budget)) {
       tc_fence_after_sync();
-      uint16_t* dst = static_cast<uint16_t*>(p.dq) + ((size_t)zkv * p.R + rho) * D + (D / 2) * w;
+      uint16_t* dst = static_cast<uint16_t*>(p.dq) + (D / 2) * w;
+      if constexpr (kPacked)
+        dst += (long long)(tok_q + at) * p.dq_st +
+               (zkv * p.sh.group + r - at * p.sh.group) * p.dq_sh;
+      else
+        dst += ((size_t)zkv * p.R + rho) * D;
       const uint32_t acc = tmem + lane_base + C::kTmAcc0 + (D / 2) * w;
 #pragma unroll
       for (int ch = 0; ch < D / 64; ++ch) {
@@ -1079,8 +1342,15 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
         tc_commit(&sp_full[h]);
       }
     };
+    // packed: rows of K behind the sequence's end, for dQ += dS K
+    auto clear_keys = [&](int j) {
+      if constexpr (kPacked) {
+        if (k_len - j * kRows < kRows) clear_rows<D>(stage_k(j % C::kKVStages), k_len - j * kRows);
+      }
+    };
     if (ok && warp_wait_b(&kv_full[0], 0, sAbort, budget)) {
       tc_fence_after_sync();
+      clear_keys(0);
       issue_sp(0, 0);
       issue_sp(0, 1);
     } else {
@@ -1107,6 +1377,7 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
               break;
             }
             tc_fence_after_sync();
+            clear_keys(j + 1);
           }
           issue_sp(j + 1, h);
         }
@@ -1124,9 +1395,16 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
     const uint64_t pol_q = l2_policy_evict_first();
     const uint64_t pol_kv = l2_policy_evict_last();
     if (leader) {
-      mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
-      tma_load_tile<D>(sQ, &p.tm_q, q_full, r0, zkv, pol_q);
-      tma_load_tile<D>(sDO, &p.tm_do, q_full, r0, zkv, pol_q);
+      if constexpr (kPacked) {
+        const int group = p.sh.group;
+        mbar_arrive_expect_tx(q_full, (uint32_t)(2 * group * p.sh.positions * D * 2));
+        tma_load_tile<D>(sQ, &p.tm_q, q_full, zkv * group, tok_q, pol_q);
+        tma_load_tile<D>(sDO, &p.tm_do, q_full, zkv * group, tok_q, pol_q);
+      } else {
+        mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
+        tma_load_tile<D>(sQ, &p.tm_q, q_full, r0, zkv, pol_q);
+        tma_load_tile<D>(sDO, &p.tm_do, q_full, r0, zkv, pol_q);
+      }
     }
     int issued = 0;
     for (int j = 0; j < n_kb; ++j) {
@@ -1135,8 +1413,13 @@ __global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_
       if (round > 0 && !warp_wait_b(&kv_empty[s], (round - 1) & 1, sAbort, budget)) break;
       if (leader) {
         mbar_arrive_expect_tx(&kv_full[s], 2 * C::kTileBytes);
-        tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], j * kRows, zkv, pol_kv);
-        tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], j * kRows, zkv, pol_kv);
+        if constexpr (kPacked) {
+          tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], zkv, tok_k + j * kRows, pol_kv);
+          tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], zkv, tok_k + j * kRows, pol_kv);
+        } else {
+          tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], j * kRows, zkv, pol_kv);
+          tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], j * kRows, zkv, pol_kv);
+        }
       }
       ++issued;
     }
@@ -1212,7 +1495,67 @@ cudaError_t launch_bwd_d(const BwdParams& p, const void* o, const void* dout, co
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const void* dout,
+                                const float* lse, int tile_room, int key_room,
+                                cudaStream_t stream) {
+  using C = BwdCfg<D>;
+  static bool attr_set[64] = {};   // (of this head dimension, by device)
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lk(g_bwd_mu);
+    if (!attr_set[dev]) {
+      constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+      if ((err = cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, false, true>, kAttr, C::kSmemKV)) !=
+              cudaSuccess ||
+          (err = cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, true, true>, kAttr, C::kSmemKV)) !=
+              cudaSuccess ||
+          (err = cudaFuncSetAttribute(attn_bwd_dq_kernel<D, true>, kAttr, C::kSmemQ)) != cudaSuccess)
+        return err;
+      attr_set[dev] = true;
+    }
+  }
+  const long long rows = (long long)p.sh.T_q * p.H_q, rows_per_block = 8 * kPrepRowsPerWarp;
+  const dim3 prep((unsigned)((rows + rows_per_block - 1) / rows_per_block));
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = prep;
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, packed_bwd_prep_kernel<D>, p, static_cast<const uint16_t*>(o),
+                           static_cast<const uint16_t*>(dout), lse);
+  if (err != cudaSuccess) return err;
+  const dim3 grid_kv((unsigned)key_room * (unsigned)p.H_kv);
+  if (p.dq_acc != nullptr) {
+    err = launch_ahead(attn_bwd_dkdv_kernel<D, true, true>, grid_kv, kThreadsFused, C::kSmemKV,
+                       stream, p);
+    if (err != cudaSuccess) return err;
+    return launch_ahead(packed_bwd_dq_convert_kernel<D>, dim3((unsigned)((rows * (D / 8) + 255) / 256)),
+                        256, 0, stream, p);
+  }
+  err = launch_ahead(attn_bwd_dkdv_kernel<D, false, true>, grid_kv, kThreadsB, C::kSmemKV, stream, p);
+  if (err != cudaSuccess) return err;
+  return launch_ahead(attn_bwd_dq_kernel<D, true>,
+                      dim3((unsigned)tile_room * 2u * (unsigned)p.H_kv), kThreadsB, C::kSmemQ, stream,
+                      p);
+}
+
 }  // namespace
+
+cudaError_t launch_attn_bwd_packed(const PackedBwdParams& p, int D, const void* o,
+                                   const void* dout, const float* lse, int tile_room,
+                                   int key_room, cudaStream_t stream) {
+  if (D == 128) return launch_packed_bwd_d<128>(p, o, dout, lse, tile_room, key_room, stream);
+  if (D == 64) return launch_packed_bwd_d<64>(p, o, dout, lse, tile_room, key_room, stream);
+  return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_attn_bwd(const BwdParams& p, int D, const void* o, const void* dout,
                             const float* lse, cudaStream_t stream) {

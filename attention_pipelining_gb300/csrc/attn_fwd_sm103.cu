@@ -57,6 +57,15 @@
 // Cluster barriers at start (barriers initialised) and exit (no CTA leaves
 // while its partner may still touch its shared memory) bracket the kernel.
 //
+// Packed sequences (the kPacked instantiation, include/attn_packed.h): the
+// tiles come from a list in the workspace that a plan kernel made.  A
+// sub-tile's rows are whole groups of query heads of consecutive tokens
+// (row = token * R + head), so the copies are boxes of [64, R, tokens]; behind
+// a sequence's end they bring other sequences' rows.  Those are harmless as
+// queries (rows that are not written) and as keys (masked), but not as values:
+// a masked probability is 0, and 0 times an infinity a NaN, so the issuer warp
+// clears them in shared memory before the product that reads them.
+//
 // Every wait is bounded (see ptx.cuh); a timeout raises a CTA-wide abort
 // flag, every role unwinds to the teardown, and the device status word
 // records ATTN_ERR_TIMEOUT.  No trap, no assert.
@@ -67,6 +76,7 @@
 
 #include "attn_internal.h"
 #include "attn_tiles.cuh"
+#include "kv_cache.cuh"
 #include "ptx.cuh"
 
 namespace attnpipe {
@@ -197,6 +207,8 @@ struct Tile {
   bool has_sub1;  // rows m0 + 128 .. m0 + 255 exist in the row group
   int pair;       // -1: a whole tile; 0 / 1: the first / second KV half of a
                   // split tail tile, run by cluster ranks 0 / 1
+  // packed sequences only (zkv is then the K/V head): see PackedTile
+  int tok0, rows, k0, k_len, n_keys, diag;
 };
 
 // Index of the k-th tile of this CTA, or -1 when it has no k-th tile: round
@@ -276,12 +288,42 @@ __device__ __forceinline__ Tile decode_tile(const AttnParams& p, int ti, int pai
   return t;
 }
 
+// The k-th tile of this CTA in the list of a packed call, `n_tiles` long with its K/V
+// heads, in the same order of rounds; false when there is none.
+__device__ __forceinline__ bool packed_tile(const PackedFwdParams& p, int n_tiles, int k, Tile& t) {
+  const long long G = gridDim.x, c = blockIdx.x;
+  const long long idx = (long long)k * G + ((k & 1) ? (G - 1 - c) : c);
+  if (idx >= n_tiles) return false;
+  const int item = (int)idx / p.H_kv;
+  t.zkv = (int)idx - item * p.H_kv;
+  const int4* src = reinterpret_cast<const int4*>(p.sh.tiles + item);
+  const int4 a = src[0], b = src[1];   // in PackedTile's order
+  t.tok0 = a.x;
+  t.rows = a.y;
+  t.k0 = a.z;
+  t.k_len = a.w;
+  t.n_keys = b.x;
+  t.diag = b.y;
+  t.jb = 0;
+  t.n_blocks = (t.n_keys + kBlockN - 1) / kBlockN;
+  t.has_sub1 = t.rows > p.sh.positions;
+  t.m0 = 0;
+  t.split = 0;
+  t.pair = -1;
+  return true;
+}
+
+template <bool kPacked>
+using FwdParamsOf = std::conditional_t<kPacked, PackedFwdParams, AttnParams>;
+
 }  // namespace
 
 // kTail: the instantiation with the split tail (launched only when the tail
 // is split; the other one carries none of its code)
-template <int D, bool kTrace, bool kTail>
-__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ AttnParams p) {
+template <int D, bool kTrace, bool kTail, bool kPacked = false>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_fwd_kernel(const __grid_constant__ FwdParamsOf<kPacked> p) {
+  static_assert(!kPacked || (!kTrace && !kTail), "packed sequences: the plain instantiation only");
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -371,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     tma_prefetch_map(&p.tm_q);
     tma_prefetch_map(&p.tm_k);
     tma_prefetch_map(&p.tm_v);
-    if (!kTrace) tma_prefetch_map(&p.tm_o);
+    if (!kTrace && !kPacked) tma_prefetch_map(&p.tm_o);
   }
   if (warp == 12) {
     tmem_alloc(sTmemBase, C::kTmemCols);
@@ -385,6 +427,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   const uint32_t tmem = *sTmemBase;
   const int wg = warp >> 2;
   const int R = p.rows_per_group;
+  int n_tiles = 0;   // of a packed call
+  if constexpr (kPacked) {
+    wait_for_earlier();
+    n_tiles = p.sh.head->tiles * p.H_kv;
+  }
+  // the k-th tile of this CTA; false when there is none
+  auto tile_at = [&](int k, Tile& tl) -> bool {
+    if constexpr (kPacked) {
+      return packed_tile(p, n_tiles, k, tl);
+    } else {
+      int pr = -1;
+      const int ti = tile_of<kTail>(p, k, pr);
+      if (ti < 0) return false;
+      tl = decode_tile(p, ti, pr);
+      return true;
+    }
+  };
+  // packed: the query token and the head in the group of a sub-tile's row r
+  auto token_of = [&](int r) {
+    if constexpr (kPacked) return (r * p.sh.inv_group) >> 16;
+    return 0;
+  };
 
   if (wg < 2) {
     // ------------------------------------------------------------ softmax
@@ -398,20 +462,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     uint32_t ntl = 0;   // tiles with sub-tile t so far: row-stat buffer, fin phase
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      int pr = -1;
-      const int ti = tile_of<kTail>(p, k, pr);
-      if (ti < 0) break;
-      const Tile tl = decode_tile(p, ti, pr);
+      Tile tl;
+      if (!tile_at(k, tl)) break;
       // (warpgroup 1 has nothing to do when the tile has no sub-tile 1)
       if (tl.n_blocks <= 0 || (t == 1 && !tl.has_sub1)) continue;
       const bool tr = trace_cta && k == 0 && lane == 0 && (warp & 3) == 0;
-      const int rho = tl.m0 + t * kBlockM + r;               // row in the row group
-      const int pos = rho % p.S_q;                           // its query position
-      // smallest query position in this sub-tile (0 if it spans two heads)
-      const int sub_first = tl.m0 + t * kBlockM;
-      const int min_pos =
-          (sub_first / p.S_q == (sub_first + kBlockM - 1) / p.S_q) ? sub_first % p.S_q : 0;
-      const int key_limit = p.causal ? min(p.S_kv, pos + 1) : p.S_kv;
+      // keys below key_limit are visible to this row, keys below full_limit to
+      // every row of the sub-tile
+      int key_limit, full_limit;
+      if constexpr (kPacked) {
+        const int first = t * p.sh.positions;                // the sub-tile's first token
+        key_limit = p.causal ? min(tl.n_keys, tl.diag + first + token_of(r)) : tl.n_keys;
+        full_limit = p.causal ? min(tl.n_keys, tl.diag + first) : tl.n_keys;
+      } else {
+        const int rho = tl.m0 + t * kBlockM + r;             // row in the row group
+        const int pos = rho % p.S_q;                         // its query position
+        // smallest query position in this sub-tile (0 if it spans two heads)
+        const int sub_first = tl.m0 + t * kBlockM;
+        const int min_pos =
+            (sub_first / p.S_q == (sub_first + kBlockM - 1) / p.S_q) ? sub_first % p.S_q : 0;
+        key_limit = p.causal ? min(p.S_kv, pos + 1) : p.S_kv;
+        full_limit = p.causal ? min(p.S_kv, min_pos + 1) : p.S_kv;
+      }
       // Two row sums: l_run of the fp32 probabilities (for the LSE), and
       // lp_run of the bf16-rounded probabilities that the PV GEMM actually
       // consumes, so O is normalised by the same weights it was accumulated
@@ -443,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
         stamp(tr, t ? kEvSm1Loaded : kEvSm0Loaded, j);
         const int kv0 = (tl.jb + j) * kBlockN;
-        const bool masked = (kv0 + kBlockN > p.S_kv) || (p.causal && kv0 + kBlockN - 1 > min_pos);
+        const bool masked = kv0 + kBlockN > full_limit;
         const int lim = key_limit - kv0;  // columns c < lim are visible to this row
         float m_use = m_run;
         float alpha = 1.f;
@@ -551,11 +623,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // returned: even with no KV block it owes its partner a partial result.
     auto next_work = [&](int& k, Tile& tl) -> bool {
       for (;; ++k) {
-        int pr = -1;
-        const int ti = tile_of<kTail>(p, k, pr);
-        if (ti < 0) return false;
-        tl = decode_tile(p, ti, pr);
+        if (!tile_at(k, tl)) return false;
         if (tl.n_blocks > 0 || tl.pair >= 0) return true;
+        if constexpr (kPacked) {
+          // queries that see no key: O = 0, LSE = -inf
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int i = token_of(r), at = h * p.sh.positions + i;
+            if (i >= p.sh.positions || at >= tl.rows) continue;
+            const int head = tl.zkv * p.sh.group + (r - i * p.sh.group);
+            const long long tok = tl.tok0 + at;
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + tok * p.o_st +
+                                                  head * p.o_sh);
+            for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+            p.lse[(long long)head * p.sh.T_q + tok] = -INFINITY;
+          }
+          continue;
+        }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int rho = tl.m0 + h * kBlockM + r;
@@ -759,7 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           stamp(tr, kEvEpilogue, t);
           // a row with no visible key (possible only within one KV split)
           // has l = 0: its partial result is O = 0, LSE = -inf
-          const bool empty = !(lp > 0.f);
+          // (packed sequences: a sum that is a NaN stays one)
+          const bool empty = kPacked ? lp == 0.f : !(lp > 0.f);
           const float inv_l = empty ? 0.f : 1.f / lp;
           const float lse_row = empty ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
           const uint32_t tO = tmem + lane_base + (t ? C::kTmO1 : C::kTmO0);
@@ -789,7 +874,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
               lse_out = (mx + log2f(e0 + e1)) * 0.69314718055994530942f;
             }
           }
-          if (p.o_part != nullptr) {
+          if constexpr (kPacked) {
+            // bf16 O through shared memory: per 64-column slab, each warp
+            // writes its 32 rows into its own staging slab (16-byte piece c of row
+            // r at piece c ^ (r % 8)) and takes them out again four rows at a
+            // time, whole 128-byte lines; rows behind the sequence's end and spare rows
+            // are left out.
+            const uint32_t stage = smem_u32(smem + C::kOffStage + q4 * 4096);
+            const uint32_t srow = stage + (uint32_t)lane * 128u;
+            const int group = p.sh.group, first = t * p.sh.positions;
+#pragma unroll 1
+            for (int h = 0; h < D / 64; ++h) {
+#pragma unroll 1
+              for (int q16 = 0; q16 < 4; ++q16) {
+                uint32_t o[16];
+                tmem_ld_x16(tO + h * 64 + q16 * 16, o);
+                tmem_ld_wait();
+                reg_after_wait(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = f2u(u2f(o[i]) * inv_l);
+#pragma unroll
+                for (int qd = 0; qd < 2; ++qd) {
+                  const int c = q16 * 2 + qd;
+                  st_shared_v4(srow + 16u * (uint32_t)(c ^ (lane & 7)),
+                               pack_bf16x2(u2f(o[qd * 8 + 0]), u2f(o[qd * 8 + 1])),
+                               pack_bf16x2(u2f(o[qd * 8 + 2]), u2f(o[qd * 8 + 3])),
+                               pack_bf16x2(u2f(o[qd * 8 + 4]), u2f(o[qd * 8 + 5])),
+                               pack_bf16x2(u2f(o[qd * 8 + 6]), u2f(o[qd * 8 + 7])));
+                }
+              }
+              __syncwarp();
+#pragma unroll
+              for (int it = 0; it < 8; ++it) {
+                const int rr = it * 4 + (lane >> 3), c = lane & 7;   // row of the slab, piece
+                const int row = q4 * 32 + rr, i = token_of(row);
+                if (i < p.sh.positions && first + i < cur.rows) {
+                  const float4 x = ld_shared_v4f(stage + (uint32_t)rr * 128u +
+                                                 16u * (uint32_t)(c ^ (rr & 7)));
+                  const int head = cur.zkv * group + (row - i * group);
+                  uint16_t* dst = static_cast<uint16_t*>(p.o) +
+                                  (long long)(cur.tok0 + first + i) * p.o_st + head * p.o_sh +
+                                  h * 64 + c * 8;
+                  *reinterpret_cast<float4*>(dst) = x;
+                }
+              }
+              __syncwarp();   // the slab may be written again
+            }
+            const int i = token_of(r);
+            if (i < p.sh.positions && first + i < cur.rows)
+              p.lse[(long long)(cur.zkv * group + (r - i * group)) * p.sh.T_q + cur.tok0 + first + i] =
+                  lse_row;
+          } else if (p.o_part != nullptr) {
             // split-KV partial: fp32 O normalised within the split, and its LSE
             const size_t row = (size_t)cur.split * p.total_rows + (size_t)cur.zkv * R + rho;
             float4* dst = reinterpret_cast<float4*>(p.o_part + row * D);
@@ -930,10 +1065,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t nb[2] = {0, 0};   // blocks so far per sub-tile: the phase of p_full[t]
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        int pr = -1;
-        const int ti = tile_of<kTail>(p, k, pr);
-        if (ti < 0) break;
-        const Tile tl = decode_tile(p, ti, pr);
+        Tile tl;
+        if (!tile_at(k, tl)) break;
         const int n = tl.n_blocks;
         if (n <= 0) continue;
         const bool tr = trace_cta && k == 0;
@@ -973,6 +1106,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           }
           ++e_next;
           const uint32_t vslot = (2 * st + C::kSlots - 1) % C::kSlots;
+          if constexpr (kPacked) {
+            // rows of V behind the sequence's end
+            if (!more && tl.k_len < n * kBlockN)
+              clear_rows<D>(sKV + vslot * C::kTileBytes, tl.k_len - j * kBlockN);
+          }
           uint64_t dv = dv0 + (uint64_t)vslot * kSlotDesc;
           if constexpr (C::kSumCol) {
             // [V | ones]: the ones atom sits at a fixed place above the ring,
@@ -1030,6 +1168,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       const uint64_t pol_kv = l2_policy_evict_last();
       uint32_t e = 0;            // ring entries issued so far
       uint32_t nq[2] = {0, 0};   // Q_t loads issued so far
+      // (packed sequences: rows are tokens of the tensor, row groups its heads,
+      // and the coordinates the other way round)
+      auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int z,
+                           uint64_t pol) {
+        if constexpr (kPacked)
+          tma_load_tile<D>(dst, map, bar, z, row, pol);
+        else
+          tma_load_tile<D>(dst, map, bar, row, z, pol);
+      };
       // V tile owed to the next entry: row group (-1: none), first key, and
       // for the trace its block index and whether its tile is traced
       int v_zkv = -1, v_row = 0, v_j = 0;
@@ -1045,27 +1192,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
               (v_zkv >= 0 ? C::kTileBytes : 0) + (k_zkv >= 0 ? C::kTileBytes : 0);
           mbar_arrive_expect_tx(&kv_full[st], bytes);
           if (v_zkv >= 0) {
-            tma_load_tile<D>(sKV + ((2 * st + C::kSlots - 1) % C::kSlots) * C::kTileBytes,
-                             &p.tm_v, &kv_full[st], v_row, v_zkv, pol_kv);
+            load_tile(sKV + ((2 * st + C::kSlots - 1) % C::kSlots) * C::kTileBytes, &p.tm_v,
+                      &kv_full[st], v_row, v_zkv, pol_kv);
             stamp(v_tr, kEvLoadV, v_j);
           }
           if (k_zkv >= 0)
-            tma_load_tile<D>(sKV + 2 * st * C::kTileBytes, &p.tm_k, &kv_full[st], k_row, k_zkv,
-                             pol_kv);
+            load_tile(sKV + 2 * st * C::kTileBytes, &p.tm_k, &kv_full[st], k_row, k_zkv, pol_kv);
         }
         ++e;
         return true;
       };
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        int pr = -1;
-        const int ti = tile_of<kTail>(p, k, pr);
-        if (ti < 0) break;
-        const Tile tl = decode_tile(p, ti, pr);
+        Tile tl;
+        if (!tile_at(k, tl)) break;
         if (tl.n_blocks <= 0) continue;
         const bool tr = trace_cta && k == 0;
         for (int j = 0; j < tl.n_blocks; ++j) {
-          const int row = (tl.jb + j) * kBlockN;
+          const int row = (tl.jb + j) * kBlockN + (kPacked ? tl.k0 : 0);
           if (!issue_entry(tl.zkv, row)) { ok = false; break; }
           stamp(tr && leader, kEvLoadK, j);
           v_zkv = tl.zkv;
@@ -1084,9 +1228,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 break;
               }
               if (leader) {
-                mbar_arrive_expect_tx(&q_full[t], C::kTileBytes);
-                tma_load_tile<D>(sQ + t * C::kTileBytes, &p.tm_q, &q_full[t],
-                                 tl.m0 + t * kBlockM, tl.zkv, pol_q);
+                if constexpr (kPacked) {
+                  // `positions` tokens of the group's heads; a spare row keeps
+                  // whatever it held
+                  const int group = p.sh.group, positions = p.sh.positions;
+                  mbar_arrive_expect_tx(&q_full[t], (uint32_t)(group * positions * D * 2));
+                  load_tile(sQ + t * C::kTileBytes, &p.tm_q, &q_full[t],
+                            tl.tok0 + t * positions, tl.zkv * group, pol_q);
+                } else {
+                  mbar_arrive_expect_tx(&q_full[t], C::kTileBytes);
+                  load_tile(sQ + t * C::kTileBytes, &p.tm_q, &q_full[t], tl.m0 + t * kBlockM,
+                            tl.zkv, pol_q);
+                }
               }
               ++nq[t];
             }
@@ -1256,6 +1409,30 @@ cudaError_t launch_d(const AttnParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+bool g_packed_attr_set[2][64] = {};  // [D == 128][device]
+
+template <int D>
+cudaError_t launch_packed_d(const PackedFwdParams& p, cudaStream_t stream) {
+  int sms = 0, dev = 0;
+  cudaError_t err = prepare<D, false, false>(&sms);
+  if (err != cudaSuccess) return err;
+  if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+  {
+    std::lock_guard<std::mutex> lk(g_launch_mu);
+    bool& attr_set = g_packed_attr_set[D == 128][dev];
+    if (!attr_set) {
+      err = cudaFuncSetAttribute(attn_fwd_kernel<D, false, false, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
+      if (err != cudaSuccess) return err;
+      attr_set = true;
+    }
+  }
+  if (p.num_tiles <= 0 || sms <= 0) return cudaErrorInvalidValue;
+  return launch_ahead(attn_fwd_kernel<D, false, false, true>,
+                      dim3((unsigned)(p.num_tiles < sms ? p.num_tiles : sms)), kThreads,
+                      Cfg<D>::kSmemBytes, stream, p);
+}
+
 }  // namespace
 
 int fwd_tail_pairs(const AttnParams& p, int D) {
@@ -1281,6 +1458,12 @@ cudaError_t launch_attn_fwd(const AttnParams& p, int D, cudaStream_t stream) {
   }
   if (D == 128) return launch_d<128, false>(p, stream);
   if (D == 64) return launch_d<64, false>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_fwd_packed(const PackedFwdParams& p, int D, cudaStream_t stream) {
+  if (D == 128) return launch_packed_d<128>(p, stream);
+  if (D == 64) return launch_packed_d<64>(p, stream);
   return cudaErrorInvalidValue;
 }
 

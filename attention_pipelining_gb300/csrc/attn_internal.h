@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "attn.h"
+#include "attn_packed.h"
 #include "attn_paged.h"
 
 namespace attnpipe {
@@ -219,6 +220,119 @@ cudaError_t launch_attn_paged(const PagedParams& p, int D, bool int4, int rows,
 cudaError_t read_kv_status(int* status, bool reset);
 cudaError_t read_paged_status(int* status, bool reset);
 
+// ---- packed sequences (include/attn_packed.h)
+//
+// A tile's 128 rows are `positions` consecutive tokens of one sequence times the
+// group's R = H_q / H_kv query heads (row = token * R + head, so that a tile needs
+// only one K/V head and few keys past its diagonal); rows behind positions * R are
+// spare.  A plan kernel lists the work of all sequences, the costliest first.
+
+// A forward tile: up to 2 x `positions` tokens of a sequence.
+struct __align__(16) PackedTile {
+  int tok0;    // first query token
+  int rows;    // tokens of the tile, 1 .. 2 positions
+  int k0;      // the sequence's first key token
+  int k_len;   // the sequence's keys
+  int n_keys;  // keys that the tile's last token sees
+  int diag;    // causal: keys that the tile's first token sees (may be <= 0)
+  int vec0;    // where the tile's tokens lie in the backward's row vectors
+  int unused;
+};
+
+// A block of up to 128 keys of a sequence, with the query tiles that see it.
+struct __align__(16) PackedKeys {
+  int k0;      // first key token
+  int keys;    // 1 .. 128
+  int q0;      // the sequence's first query token
+  int q_len;
+  int vec0;    // where the sequence's queries lie in the row vectors
+  int shift;   // causal: key r of the block is seen by queries at r + shift and behind
+  int first;   // the tile (of `positions` queries) that the block begins with: causal, the first
+               // that sees a key of it
+  int n_work;  // tiles from there on (not causal: all, the last followed by the first)
+};
+
+struct PackedHeader {
+  int tiles, key_blocks;              // entries of the two lists
+  int q_first, q_end;                 // tokens that belong to a sequence
+  int unused[60];
+};
+
+struct PackedPlan {
+  const int* cu_q;
+  const int* cu_k;     // == cu_q where they are the same
+  int B, T_q, T_k;
+  int positions;       // query tokens of a 128-row tile
+  int causal;
+  PackedHeader* head;  // workspace, from here on
+  int* seq_q;          // [B + 1], cu_q in order
+  int* seq_k;          // [B + 1] (== seq_q where they are the same)
+  PackedTile* tiles;   // room for tile_room(...) of them
+  PackedKeys* keys;    // nullptr: not listed
+};
+
+// Entries of the lists, at most.
+inline long long packed_tile_room(int T_q, int B, int positions) {
+  return (long long)T_q / (2 * positions) + B;
+}
+inline long long packed_key_room(int T_k, int B) { return (long long)T_k / 128 + B; }
+
+// First token of sequence b in the row vectors: a multiple of 4 (so that a tile's
+// part is 16-byte aligned), with room for every sequence before it.
+__host__ __device__ inline int packed_vec0(int q0, int b) {
+  return (int)(((long long)q0 + 4ll * b) & ~3ll);
+}
+
+// What the attention kernels take beside the fields they share with attn_fwd and
+// attn_bwd (of which S_q, S_kv and the tile counts are unused).
+struct PackedShape {
+  const PackedHeader* head;
+  const PackedTile* tiles;
+  const PackedKeys* keys;
+  int group;           // R
+  int positions;       // query tokens of a 128-row tile
+  int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
+  int T_q;
+};
+
+struct PackedFwdParams : AttnParams {
+  PackedShape sh;
+  long long o_st, o_sh;  // strides of O (elements)
+};
+
+struct PackedBwdParams : BwdParams {
+  PackedShape sh;
+  const int* seq_q;
+  long long vec_stride;  // row vectors of one K/V head
+  long long o_st, o_sh, do_st, do_sh, dq_st, dq_sh, dk_st, dk_sh, dv_st, dv_sh;
+};
+
+struct RopePackedParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  long long q_st, q_sh, k_st, k_sh, qo_st, qo_sh, ko_st, ko_sh;
+  const int* positions;  // [axes, T]
+  const float* cos;
+  const float* sin;
+  int rope_rows, rot_dim, inverse;
+  int axes, ends[4];     // pairs up to the end of each section
+  int T, H_q, H_kv;
+  int rows;              // heads of a token that one thread block takes (set at launch)
+};
+
+cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream);
+cudaError_t launch_attn_fwd_packed(const PackedFwdParams& p, int D, cudaStream_t stream);
+// With p.dq_acc set, dQ is added up there; otherwise a kernel of its own computes it.
+cudaError_t launch_attn_bwd_packed(const PackedBwdParams& p, int D, const void* o,
+                                   const void* dout, const float* lse, int tile_room,
+                                   int key_room, cudaStream_t stream);
+cudaError_t launch_rope_packed(const RopePackedParams& p, int D, bool interleaved,
+                               cudaStream_t stream);
+// Reads (and optionally clears) the plan's and the rotation's status word.
+cudaError_t read_packed_status(int* status, bool reset);
+
 // Events stamped by the trace instantiation, one slot per KV block j.
 enum TraceEvent : int {
   kEvSm0Wake = 0,   // softmax 0: S_0(j) ready (wait returned)
@@ -250,6 +364,12 @@ constexpr int kMaxTraceBlocks = 128;  // KV blocks a trace records per event, at
 bool encode_bf16_map_3d(CUtensorMap* map, const void* base, uint64_t D, uint64_t rows,
                         uint64_t outer, uint32_t box_rows);
 
+// The same over a [tokens, heads, D] tensor with any strides (elements, multiples of 8),
+// box {64, box_heads, box_tokens}.
+bool encode_bf16_map_thd(CUtensorMap* map, const void* base, uint64_t D, uint64_t heads,
+                         uint64_t tokens, uint64_t stride_h, uint64_t stride_t,
+                         uint32_t box_heads, uint32_t box_tokens);
+
 // Queues the fused kernel (D = 64 or 128) on min(p.num_tiles, SM count) CTAs.
 // With p.trace set or p.fault_drop_block >= 0, the diagnostic instantiation
 // (timeline stamps, timeout test) runs instead.
@@ -276,6 +396,8 @@ cudaError_t launch_selftest_pv(const uint16_t* p, const CUtensorMap& tv, float* 
                                cudaStream_t stream);
 
 // Host-side pieces of the C ABI (attn_api.cu) used by more than one file.
+// scale * log2(e), never zero (the kernels' softmax runs in base 2).
+float scale_log2_of(float scale);
 // ATTN_OK when the current device is an sm_103 part (cached per device).
 attn_status_t check_device();
 attn_status_t validate(const void* q, const void* k, const void* v, const void* o, const void* lse,

@@ -38,6 +38,19 @@ __device__ __forceinline__ void tma_load_tile(uint8_t* dst, const CUtensorMap* m
     tma_load_3d(dst + s * kSlabBytes, map, bar, s * 64, row0, z, hint);
 }
 
+// Clears rows [from, 128) of a tile in shared memory that a copy has filled, for
+// the tensor core's next read of it (through the async proxy).  Whole warp.
+template <int D>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
+  const uint32_t base = smem_u32(tile);
+#pragma unroll 1
+  for (int s = 0; s < TileShape<D>::kSlabs; ++s)
+    for (int at = from * 128 + (int)(threadIdx.x & 31) * 16; at < kSlabBytes; at += 512)
+      st_shared_v4(base + (uint32_t)(s * kSlabBytes + at), 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Shared-memory descriptor of the start of a tile, for either operand use.
 // The GEMM helpers below add constant offsets to its start-address field
 // (bits 0-13, address >> 4), which never carries: shared addresses stay

@@ -11,6 +11,7 @@
 #include "attn_internal.h"
 #include "kv_cache.cuh"
 #include "ptx.cuh"
+#include "rotate.cuh"
 
 namespace attnpipe {
 
@@ -40,108 +41,6 @@ __device__ __forceinline__ void copy_async_commit() {
 template <int N>
 __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// ---------------------------------------------------------------- rotation
-
-// x a - y b rounded once to bf16 (returned as a float).  x and y are bf16
-// values and a and b fp32, so the exact value may have more bits than a float:
-// the products' and the sum's rounding errors are recovered (fma, two-sum) and
-// added back, and the fp32 result, when it falls on a tie of the bf16 rounding
-// that the remainder breaks, is moved one step to the remainder's side.  Non-finite
-// values take the plain formula's result.
-__device__ __forceinline__ float rotate_bf16(float x, float a, float y, float b) {
-  const float h = __fmul_rn(x, a), h2 = __fmul_rn(-y, b);
-  const float e = __fmaf_rn(x, a, -h), e2 = __fmaf_rn(-y, b, -h2);
-  const float s = __fadd_rn(h, h2);
-  const float t = __fsub_rn(s, h);
-  const float es = __fadd_rn(__fsub_rn(h, __fsub_rn(s, t)), __fsub_rn(h2, t));
-  const float lo = __fadd_rn(es, __fadd_rn(e, e2));
-  const float r = __fadd_rn(s, lo);
-  if (!(fabsf(r) <= 3.4028235e38f)) return s;   // an infinity or a NaN
-  const float rem = __fsub_rn(lo, __fsub_rn(r, s));
-  uint32_t u = __float_as_uint(r);
-  if ((u & 0xffffu) == 0x8000u && rem != 0.f) u += ((rem > 0.f) == (r > 0.f)) ? 1u : 0xffffffffu;
-  return __uint_as_float(u);
-}
-
-// Four pairs, v = {x, y, c, s}: r = {x c - y s, y c + x s}.
-__device__ __noinline__ void rotate4_exactly(const float (&v)[4][4], float (&r)[2][4]) {
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    r[0][i] = rotate_bf16(v[0][i], v[2][i], v[1][i], v[3][i]);
-    r[1][i] = rotate_bf16(v[1][i], v[2][i], -v[0][i], v[3][i]);
-  }
-}
-
-// The same, two pairs at a time: first with five operations a result,
-// fma(x, c, h) + e with h + e = -y s exactly, which is off by at most two units of
-// fp32's last place (half a unit in each of the two sums, of which the first may
-// be twice as large as the second's; the sum of products that cancel is exact);
-// only where that leaves the bf16 rounding open (two units around a tie: one
-// element in 13000) or a value is not finite, by rotate_bf16.
-// Rounding the plain fp32 formula instead would round about one element in 2^15
-// the other way than the exact value, and in a 4-bit cache change its code.
-__device__ __forceinline__ void rotate4(const uint64_t (&x)[2], const uint64_t (&y)[2],
-                                        const uint64_t (&c)[2], const uint64_t (&s)[2],
-                                        float (&r1)[4], float (&r2)[4]) {
-  const uint64_t minus = f2_pack(-1.f, -1.f), zero = f2_pack(0.f, 0.f);
-  uint32_t nearest = 0xffffffffu;   // of the first of each two, of the second
-  uint64_t finite = zero;
-  const auto one = [&](uint64_t u, uint64_t w, uint64_t cs, uint64_t sn, uint64_t minus_sn,
-                       float& f0, float& f1) {   // u cs + w sn
-    const uint64_t e = f2_fma(w, sn, f2_mul(w, minus_sn));
-    const uint64_t r = f2_add(f2_fma(u, cs, f2_mul(w, sn)), e);
-    finite = f2_fma(r, zero, finite);
-    f2_unpack(r, f0, f1);
-    nearest = __viaddmin_u16x2(
-        __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x5410u), 0x80028002u, nearest);
-  };
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t ms = f2_mul(s[i], minus);
-    one(x[i], y[i], c[i], ms, s[i], r1[2 * i], r1[2 * i + 1]);
-    one(y[i], x[i], c[i], s[i], ms, r2[2 * i], r2[2 * i + 1]);
-  }
-  float f0, f1;
-  f2_unpack(finite, f0, f1);
-  if ((nearest & 0xffffu) <= 4u || (nearest >> 16) <= 4u || f0 + f1 != 0.f) {
-    float v[4][4], r[2][4];   // copies: the arrays themselves stay in registers
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f2_unpack(x[i], v[0][2 * i], v[0][2 * i + 1]);
-      f2_unpack(y[i], v[1][2 * i], v[1][2 * i + 1]);
-      f2_unpack(c[i], v[2][2 * i], v[2][2 * i + 1]);
-      f2_unpack(s[i], v[3][2 * i], v[3][2 * i + 1]);
-    }
-    rotate4_exactly(v, r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r1[i] = r[0][i], r2[i] = r[1][i];
-  }
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// The rotation of a lane's eight elements, w.x, w.y and w.z, w.w: four first
-// and four second elements of its pairs, or (interleaved) four adjacent pairs.
-template <bool kInterleaved>
-__device__ __forceinline__ void rotate_lane(uint4& w, const uint64_t (&cs)[2],
-                                            const uint64_t (&sn)[2]) {
-  uint64_t x[2], y[2];
-  float r1[4], r2[4];
-  if constexpr (kInterleaved) {
-    x[0] = f2_pack(bf16_lo(w.x), bf16_lo(w.y)), x[1] = f2_pack(bf16_lo(w.z), bf16_lo(w.w));
-    y[0] = f2_pack(bf16_hi(w.x), bf16_hi(w.y)), y[1] = f2_pack(bf16_hi(w.z), bf16_hi(w.w));
-  } else {
-    x[0] = f2_pack(bf16_lo(w.x), bf16_hi(w.x)), x[1] = f2_pack(bf16_lo(w.y), bf16_hi(w.y));
-    y[0] = f2_pack(bf16_lo(w.z), bf16_hi(w.z)), y[1] = f2_pack(bf16_lo(w.w), bf16_hi(w.w));
-  }
-  rotate4(x, y, cs, sn, r1, r2);
-  w = kInterleaved ? make_uint4(pack_bf16x2(r1[0], r2[0]), pack_bf16x2(r1[1], r2[1]),
-                                pack_bf16x2(r1[2], r2[2]), pack_bf16x2(r1[3], r2[3]))
-                   : make_uint4(pack_bf16x2(r1[0], r1[1]), pack_bf16x2(r1[2], r1[3]),
-                                pack_bf16x2(r2[0], r2[1]), pack_bf16x2(r2[2], r2[3]));
 }
 
 // ---------------------------------------------------------------- 4 bits

@@ -1,0 +1,302 @@
+// packed_sm103.cu -- packed sequences: the plan of their attention's work, and
+// the rotation of queries and keys by positions with several axes
+// (include/attn_packed.h).
+#include <climits>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "kv_cache.cuh"
+#include "ptx.cuh"
+#include "rotate.cuh"
+
+namespace attnpipe {
+
+__device__ int g_packed_status = 0;
+
+namespace {
+
+// ---------------------------------------------------------------- plan
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 1024;   // of costs
+
+// Sum (or maximum) over the warp's lanes up to this one.
+template <typename Op>
+__device__ __forceinline__ int warp_scan(int x, Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x = op(x, y);
+  }
+  return x;
+}
+
+// The scan over the block's threads before this one (`none` for the first); `warps`: 32
+// ints of shared memory.
+template <typename Op>
+__device__ __forceinline__ int block_scan_before(int x, int none, int* warps, Op op) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int upto = warp_scan(x, op);
+  __syncthreads();   // (warps may still be read from the scan before)
+  if (lane == 31) warps[warp] = upto;
+  __syncthreads();
+  if (warp == 0) warps[lane] = warp_scan(warps[lane], op);
+  __syncthreads();
+  int before = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (lane == 0) before = none;
+  return warp > 0 ? op(warps[warp - 1], before) : before;
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// cu in order, within [0, T]: each entry the largest up to there.  True if it was not.
+__device__ bool put_in_order(const int* cu, int n, int T, int* out, int* warps) {
+  const auto larger = [](int a, int b) { return max(a, b); };
+  const int per = ceil_div(n, kPlanThreads);
+  const int first = min((int)threadIdx.x * per, n), end = min(first + per, n);
+  int most = 0;
+  for (int i = first; i < end; ++i) most = max(most, min(cu[i], T));
+  int run = block_scan_before(most, 0, warps, larger);
+  bool bad = false;
+  for (int i = first; i < end; ++i) {
+    const int x = cu[i];
+    run = max(run, min(x, T));
+    bad |= x != run;
+    out[i] = run;
+  }
+  return bad;
+}
+
+// One thread block lists the tiles (and the key blocks) of all sequences, by a
+// counting sort over their costs in blocks (of 128 keys, or of query tiles), so that
+// the costliest run first and the last to end are short.  The order among equal costs
+// differs from run to run; no result depends on it.
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
+  __shared__ int at[2][kBuckets];   // entries of a cost, then where the next of them goes
+  __shared__ int warps[32], most[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  at[0][threadIdx.x] = at[1][threadIdx.x] = 0;
+  if (threadIdx.x < 2) most[threadIdx.x] = 0;
+  allow_later();
+  wait_for_earlier();
+  bool bad = put_in_order(p.cu_q, p.B + 1, p.T_q, p.seq_q, warps);
+  if (p.seq_k != p.seq_q) bad |= put_in_order(p.cu_k, p.B + 1, p.T_k, p.seq_k, warps);
+  if (bad) g_packed_status = ATTN_ERR_BAD_INDEX;
+  __syncthreads();
+  const int P = p.positions;
+  for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
+    const int n = p.seq_q[b + 1] - p.seq_q[b], m = p.seq_k[b + 1] - p.seq_k[b];
+    if (n > 0) atomicMax(&most[0], ceil_div(m, 128));
+    if (m > 0) atomicMax(&most[1], ceil_div(n, P));
+  }
+  __syncthreads();
+  int shift[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    shift[i] = 0;
+    while ((most[i] >> shift[i]) >= kBuckets) ++shift[i];
+  }
+  // every tile (list 0) and key block (list 1), each with its cost
+  const auto each = [&](auto&& put) {
+    for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+      const int q0 = p.seq_q[b], n = p.seq_q[b + 1] - q0;
+      const int k0 = p.seq_k[b], m = p.seq_k[b + 1] - k0;
+      const int vec0 = packed_vec0(q0, b);
+      for (int t = lane; t < ceil_div(n, 2 * P); t += 32) {
+        PackedTile x;
+        const int pos = t * 2 * P;
+        x.tok0 = q0 + pos;
+        x.rows = min(n - pos, 2 * P);
+        x.k0 = k0;
+        x.k_len = m;
+        x.diag = m - n + pos + 1;
+        x.n_keys = p.causal ? min(max(x.diag + x.rows - 1, 0), m) : m;
+        x.vec0 = vec0 + pos;
+        x.unused = 0;
+        put(0, ceil_div(x.n_keys, 128), &x, (PackedKeys*)nullptr);
+      }
+      if (p.keys == nullptr) continue;
+      const int tiles = ceil_div(n, P);
+      for (int t = lane; t < ceil_div(m, 128); t += 32) {
+        PackedKeys x;
+        x.k0 = k0 + t * 128;
+        x.keys = min(m - t * 128, 128);
+        x.q0 = q0;
+        x.q_len = n;
+        x.vec0 = vec0;
+        x.shift = t * 128 - (m - n);
+        // (without a mask each block begins elsewhere, so that those that run at once
+        // add to different rows of dQ)
+        x.first = p.causal ? min(max(x.shift, 0) / P, tiles) : tiles > 0 ? t % tiles : 0;
+        x.n_work = p.causal ? tiles - x.first : tiles;
+        put(1, x.n_work, (PackedTile*)nullptr, &x);
+      }
+    }
+  };
+  each([&](int list, int cost, const PackedTile*, const PackedKeys*) {
+    atomicAdd(&at[list][kBuckets - 1 - min(cost >> shift[list], kBuckets - 1)], 1);
+  });
+  __syncthreads();
+  const auto sum = [](int a, int b) { return a + b; };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int mine = at[i][threadIdx.x];
+    const int before = block_scan_before(mine, 0, warps, sum);
+    at[i][threadIdx.x] = before;
+    if (threadIdx.x == kBuckets - 1) {
+      if (i == 0) p.head->tiles = before + mine;
+      if (i == 1) p.head->key_blocks = before + mine;
+    }
+  }
+  if (threadIdx.x == 0) {
+    p.head->q_first = p.seq_q[0];
+    p.head->q_end = p.seq_q[p.B];
+  }
+  __syncthreads();
+  each([&](int list, int cost, const PackedTile* tile, const PackedKeys* keys) {
+    const int i = atomicAdd(&at[list][kBuckets - 1 - min(cost >> shift[list], kBuckets - 1)], 1);
+    if (list == 0) p.tiles[i] = *tile;
+    if (list == 1) p.keys[i] = *keys;
+  });
+}
+static_assert(kBuckets == kPlanThreads, "one thread to a bucket");
+
+// ---------------------------------------------------------------- rotation
+
+constexpr int kRopeThreads = 128;
+constexpr int kRopeAhead = 4;        // rows of a thread under way
+constexpr int kRopeBlocks = 4864;    // 32 blocks on each of 152 SMs, at least, where there is work for them
+
+// A token's vector of one head is a row that D / 16 neighbouring lanes hold, 16
+// elements each: eight first and eight second elements of their pairs, or (adjacent
+// pairs, or not rotated) 16 side by side.  A thread block takes kSlots consecutive
+// tokens and goes with all of them through p.rows of their H_q + H_kv heads: the
+// rotation is read once for all of them.
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_packed_kernel(const __grid_constant__ RopePackedParams p) {
+  constexpr int kLanes = D / 16;
+  constexpr int kSlots = kRopeThreads / kLanes;
+  const int c = threadIdx.x % kLanes;
+  allow_later();
+  wait_for_earlier();
+  const long long t = (long long)blockIdx.x * kSlots + threadIdx.x / kLanes;
+  if (t >= p.T) return;
+  const int pairs = p.rot_dim / 2;
+  const bool rotates = c < p.rot_dim / 16;
+  const bool apart = !kInterleaved && rotates;
+  // the lane's elements lo .. lo + 7 and hi .. hi + 7
+  const int lo = apart ? 8 * c : 16 * c, hi = apart ? pairs + 8 * c : 16 * c + 8;
+  int row[4];
+  bool good = true;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    row[a] = a < p.axes ? p.positions[(long long)a * p.T + t] : 0;
+    good = good && (unsigned)row[a] < (unsigned)p.rope_rows;
+  }
+  if (!good) {
+    g_packed_status = ATTN_ERR_BAD_INDEX;
+    return;
+  }
+  uint64_t cs[4] = {}, sn[4] = {};   // cosines and sines of the lane's eight pairs
+  if (rotates) {
+    const auto row_of = [&](int d) {   // the row that pair d takes
+      return d < p.ends[0] ? row[0] : d < p.ends[1] ? row[1] : d < p.ends[2] ? row[2] : row[3];
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = 8 * c + 2 * i;
+      const long long x = (long long)row_of(d) * pairs + d;
+      const long long y = (long long)row_of(d + 1) * pairs + d + 1;
+      cs[i] = f2_pack(p.cos[x], p.cos[y]);
+      const float s0 = p.sin[x], s1 = p.sin[y];
+      sn[i] = p.inverse ? f2_pack(-s0, -s1) : f2_pack(s0, s1);
+    }
+  }
+  // heads [r0, r1) of the queries and the keys behind them
+  const int r0 = blockIdx.y * p.rows, r1 = min(r0 + p.rows, p.H_q + p.H_kv);
+  const uint16_t* const q = p.q + t * p.q_st;
+  const uint16_t* const k = p.k + t * p.k_st - p.H_q * p.k_sh;
+  uint16_t* const qo = p.q_out + t * p.qo_st;
+  uint16_t* const ko = p.k_out + t * p.ko_st - p.H_q * p.ko_sh;
+#pragma unroll 1
+  for (int h0 = r0; h0 < r1; h0 += kRopeAhead) {
+    uint4 w[kRopeAhead][2];
+#pragma unroll
+    for (int i = 0; i < kRopeAhead; ++i) {
+      const int h = h0 + i;
+      if (h >= r1) break;
+      const uint16_t* const src = h < p.H_q ? q + h * p.q_sh : k + h * p.k_sh;
+      w[i][0] = *reinterpret_cast<const uint4*>(src + lo);
+      w[i][1] = *reinterpret_cast<const uint4*>(src + hi);
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeAhead; ++i) {
+      const int h = h0 + i;
+      if (h >= r1) break;
+      if (rotates) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          // four pairs: {first, second} halves of w[0], w[1], or four adjacent pairs of w[n]
+          const uint64_t c2[2] = {cs[2 * n], cs[2 * n + 1]}, s2[2] = {sn[2 * n], sn[2 * n + 1]};
+          if constexpr (kInterleaved) {
+            rotate_lane<true>(w[i][n], c2, s2);
+          } else {
+            uint4 x = n == 0 ? make_uint4(w[i][0].x, w[i][0].y, w[i][1].x, w[i][1].y)
+                             : make_uint4(w[i][0].z, w[i][0].w, w[i][1].z, w[i][1].w);
+            rotate_lane<false>(x, c2, s2);
+            if (n == 0)
+              w[i][0].x = x.x, w[i][0].y = x.y, w[i][1].x = x.z, w[i][1].y = x.w;
+            else
+              w[i][0].z = x.x, w[i][0].w = x.y, w[i][1].z = x.z, w[i][1].w = x.w;
+          }
+        }
+      }
+      uint16_t* const dst = h < p.H_q ? qo + h * p.qo_sh : ko + h * p.ko_sh;
+      *reinterpret_cast<uint4*>(dst + lo) = w[i][0];
+      *reinterpret_cast<uint4*>(dst + hi) = w[i][1];
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_rope_d(const RopePackedParams& in, bool interleaved, cudaStream_t stream) {
+  RopePackedParams p = in;
+  const int slots = kRopeThreads / (D / 16);
+  const int heads = p.H_q + p.H_kv;
+  const long long groups = ((long long)p.T + slots - 1) / slots;
+  // all heads of a token to one thread block where the tokens fill the GPU
+  long long parts = (kRopeBlocks + groups - 1) / groups;
+  if (parts > heads) parts = heads;
+  p.rows = (int)((heads + parts - 1) / parts);
+  const dim3 grid((unsigned)groups, (unsigned)((heads + p.rows - 1) / p.rows));
+  return interleaved ? launch_ahead(rope_packed_kernel<D, true>, grid, kRopeThreads, 0, stream, p)
+                     : launch_ahead(rope_packed_kernel<D, false>, grid, kRopeThreads, 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream) {
+  return launch_ahead(packed_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
+}
+
+cudaError_t launch_rope_packed(const RopePackedParams& p, int D, bool interleaved,
+                               cudaStream_t stream) {
+  if (D == 128) return launch_rope_d<128>(p, interleaved, stream);
+  if (D == 64) return launch_rope_d<64>(p, interleaved, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t read_packed_status(int* status, bool reset) {
+  cudaError_t err = cudaMemcpyFromSymbol(status, g_packed_status, sizeof(int));
+  if (err != cudaSuccess) return err;
+  if (reset) {
+    const int zero = 0;
+    err = cudaMemcpyToSymbol(g_packed_status, &zero, sizeof(int));
+  }
+  return err;
+}
+
+}  // namespace attnpipe

@@ -1,0 +1,234 @@
+"""Packed sequences: rotation with several axes, attention and its gradients (include/attn_packed.h).
+
+    q, k = rope_packed(q, k, positions, cos, sin, sections)
+    o, lse = attn_fwd_packed(q, k, v, cu, True, scale)
+    dq, dk, dv = attn_bwd_packed(q, k, v, o, lse, dout, cu, True, scale)
+    dq, dk = rope_packed(dq, dk, positions, cos, sin, sections, inverse=True, out=(dq, dk))
+
+Argument marshalling only, as in the package's other entry points.  The tokens of all sequences lie
+one after the other: q [T, H_q, D], k and v [T, H_kv, D] bf16, and ``cu`` int32 [B + 1] says where
+they begin and end (sequence b is tokens cu[b] .. cu[b + 1] - 1; any may be empty).  With ``cu_k`` the
+keys have lengths, and a number of tokens, of their own.  Tensors may have any positive strides that
+are multiples of 8 elements with the last dimension contiguous (views of one projection's output).
+Calls run on ``stream``, or else on the current stream of the tensors' device, whichever device is
+current; what they allocate belongs to that stream.
+"""
+from __future__ import annotations
+
+import functools
+import struct
+
+from . import AttnError, _check, _load, paged
+
+# attn_packed_t: B, T_q, T_k, H_q, H_kv, D, causal, scale
+_SIZES = struct.Struct("@iiiiiiif")
+# attn_thd_t: data and the strides of the tokens and the heads
+_THD = struct.Struct("@Pqq")
+_INT_MAX = 2 ** 31 - 1   # the C entries' sizes are ints
+
+torch = None   # imported with the first call, as in the package's other functions
+
+
+def _import():
+    global torch, _Tensor, _bf16, _u8, _i32, _f32, _alloc, _free
+    if paged.torch is None:
+        paged._import()
+    _Tensor, _bf16, _u8, _i32, _f32 = paged._Tensor, paged._bf16, paged._u8, paged._i32, paged._f32
+    _alloc, _free = paged._alloc, paged._free
+    torch = paged.torch
+
+
+def _first(name, t):
+    """(device index, tokens, heads, D) of a call's first tensor"""
+    if torch is None:
+        _import()
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _bf16 or t.dim() != 3:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor [tokens, heads, D]")
+    T, H, D = t.shape
+    if T > _INT_MAX or H > _INT_MAX or D > _INT_MAX:   # (a view may claim any number of them)
+        raise ValueError(f"{name}: sizes must be below 2^31")
+    return t.get_device(), T, H, D
+
+
+def _thd(name, t, shape, dev):
+    """attn_thd_t of a bf16 tensor of that shape"""
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not _bf16:
+        raise TypeError(f"{name} must be a bfloat16 tensor on the same device as the others")
+    st, sh, sd = t.stride() if t.shape == shape else (0, 0, 0)
+    if sd != 1:
+        raise ValueError(f"{name} must be {list(shape)} with a contiguous last dimension, not "
+                         f"{list(t.shape)} with strides {t.stride()}")
+    return _THD.pack(t.data_ptr(), st, sh)
+
+
+def _flat(name, t, shape, dtype, dev):
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not dtype \
+            or t.shape != shape or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the same device as "
+                        "the others")
+    return t.data_ptr()
+
+
+def _bounds(cu_q, cu_k, dev):
+    """(sequences, cu_q's pointer, cu_k's pointer or None)"""
+    if not isinstance(cu_q, _Tensor) or cu_q.dim() != 1 or not 1 < cu_q.shape[0] <= _INT_MAX:
+        raise TypeError("cu_q must be an int32 [sequences + 1] tensor")
+    shape = cu_q.shape
+    return (shape[0] - 1, _flat("cu_q", cu_q, shape, _i32, dev),
+            None if cu_k is None else _flat("cu_k", cu_k, shape, _i32, dev))
+
+
+def _sizes(q, k, v, cu_q, cu_k, causal, scale):
+    """What both attention calls begin with: device, shapes, attn_packed_t, tensors and bounds."""
+    dev, T_q, H_q, D = _first("q", q)
+    _, T_k, H_kv, _ = _first("k", k)
+    if cu_k is None and T_k != T_q:
+        raise ValueError("without cu_k, k and v must have as many tokens as q")
+    B, cq, ck = _bounds(cu_q, cu_k, dev)
+    q_shape, k_shape = (T_q, H_q, D), (T_k, H_kv, D)
+    return (dev, q_shape, k_shape,
+            _SIZES.pack(B, T_q, T_k, H_q, H_kv, D, 1 if causal else 0, scale),
+            _thd("q", q, q_shape, dev), _thd("k", k, k_shape, dev), _thd("v", v, k_shape, dev),
+            cq, ck)
+
+
+@functools.lru_cache(maxsize=1024)
+def _fwd_bytes(sizes) -> int:
+    return int(_load().attn_packed_workspace_bytes(sizes))
+
+
+@functools.lru_cache(maxsize=1024)
+def _bwd_bytes(sizes, deterministic) -> int:
+    return int(_load().attn_packed_bwd_workspace_bytes(sizes, deterministic))
+
+
+def packed_workspace_bytes(B: int, T_q: int, T_k: int, H_q: int, H_kv: int, D: int) -> int:
+    """Workspace bytes of attn_fwd_packed (0 if the sizes are invalid)."""
+    return _fwd_bytes(_SIZES.pack(B, T_q, T_k, H_q, H_kv, D, 0, 1.0))
+
+
+def packed_bwd_workspace_bytes(B: int, T_q: int, T_k: int, H_q: int, H_kv: int, D: int,
+                               deterministic: bool = False) -> int:
+    """Workspace bytes of attn_bwd_packed (0 if the sizes are invalid)."""
+    return _bwd_bytes(_SIZES.pack(B, T_q, T_k, H_q, H_kv, D, 0, 1.0), 1 if deterministic else 0)
+
+
+def _with_workspace(workspace, nbytes, dev, handle, where, call):
+    """call(pointer, bytes) with the caller's workspace, or one that lives until what is queued is done."""
+    if nbytes == 0:
+        raise AttnError(1, where)
+    if workspace is not None:
+        if not isinstance(workspace, _Tensor) or workspace.get_device() != dev \
+                or workspace.dtype is not _u8 or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous uint8 tensor on the same device as the others")
+        call(workspace.data_ptr(), workspace.numel())
+        return
+    mine = _alloc(nbytes, handle)
+    try:
+        call(mine, nbytes)
+    finally:   # (used again only by what follows on the stream)
+        _free(mine)
+
+
+def attn_fwd_packed(q, k, v, cu_q, causal: bool, scale: float, cu_k=None, workspace=None, out=None,
+                    stream=None):
+    """Attention of every sequence over its own keys; returns (o [T_q, H_q, D] bf16, lse [H_q, T_q]
+    float32).  With ``causal`` the queries are the newest of the sequence's tokens: of n queries and m
+    keys query i sees keys j <= i + m - n.  ``workspace``: optional uint8 tensor of at least
+    packed_workspace_bytes(...) bytes, not shared with calls that may run at the same time (allocated
+    if None); ``out``: optional (o, lse) to write into (rows of tokens that belong to no sequence keep
+    what it held, zeros where it is allocated here)."""
+    # (the tensors keep their names: a caller may hold no other reference to one, and what is free
+    # the workspace may get)
+    dev, q_shape, k_shape, sizes, qs, ks, vs, cq, ck = _sizes(q, k, v, cu_q, cu_k, causal, scale)
+    lse_shape = (q_shape[1], q_shape[0])
+
+    def call(handle):
+        o, lse = out if out is not None else (
+            torch.zeros(q_shape, dtype=_bf16, device=q.device),
+            torch.zeros(lse_shape, dtype=_f32, device=q.device))
+        os, lse_p = _thd("out[0]", o, q_shape, dev), _flat("out[1]", lse, lse_shape, _f32, dev)
+        _with_workspace(workspace, _fwd_bytes(sizes), dev, handle, "attn_packed_workspace_bytes",
+                        lambda ws, n: _check(_load().attn_fwd_packed(
+                            sizes, qs, ks, vs, os, lse_p, cq, ck, ws, n, handle), "attn_fwd_packed"))
+        return o, lse
+
+    return paged._on(dev, stream, call)
+
+
+def attn_bwd_packed(q, k, v, o, lse, dout, cu_q, causal: bool, scale: float, cu_k=None, workspace=None,
+                    out=None, deterministic: bool = False, stream=None):
+    """Gradients (dq, dk, dv) of attn_fwd_packed's q, k and v for the gradient ``dout`` of its o, given
+    its o and lse.  ``workspace``: optional uint8 tensor of at least packed_bwd_workspace_bytes(...)
+    bytes, not shared with calls that may run at the same time (allocated if None); ``out``: optional
+    (dq, dk, dv) to write into (rows of tokens that belong to no sequence keep what it held, zeros
+    where it is allocated here).  ``deterministic``: dq reproducible bit for bit (dk and dv always
+    are)."""
+    dev, q_shape, k_shape, sizes, qs, ks, vs, cq, ck = _sizes(q, k, v, cu_q, cu_k, causal, scale)
+    os, dos = _thd("o", o, q_shape, dev), _thd("dout", dout, q_shape, dev)
+    lse_p = _flat("lse", lse, (q_shape[1], q_shape[0]), _f32, dev)
+    det = 1 if deterministic else 0
+
+    def call(handle):
+        grads = tuple(out) if out is not None else tuple(
+            torch.zeros(s, dtype=_bf16, device=q.device) for s in (q_shape, k_shape, k_shape))
+        gs = [_thd(f"out[{i}]", g, s, dev) for i, (g, s) in enumerate(zip(grads, (q_shape, k_shape, k_shape)))]
+        if len(gs) != 3:
+            raise ValueError("out must be (dq, dk, dv)")
+        _with_workspace(workspace, _bwd_bytes(sizes, det), dev, handle, "attn_packed_bwd_workspace_bytes",
+                        lambda ws, n: _check(_load().attn_bwd_packed(
+                            sizes, qs, ks, vs, os, lse_p, dos, *gs, cq, ck, ws, n, det, handle),
+                            "attn_bwd_packed"))
+        return grads
+
+    return paged._on(dev, stream, call)
+
+
+@functools.lru_cache(maxsize=256)
+def _ints(values):
+    return struct.pack(f"@{len(values)}i", *values)
+
+
+def rope_packed(q, k, positions, cos, sin, sections=None, interleaved: bool = False,
+                inverse: bool = False, out=None, stream=None):
+    """Rotates queries q [T, H_q, D] and keys k [T, H_kv, D] (either may be None) by positions with one
+    to four axes and returns both.  ``positions`` int32 [axes, T]; ``cos`` and ``sin`` float32 [rows,
+    rot_dim / 2], one row a position; the pairs of elements fall into ``sections`` (pairs of each axis,
+    their sum rot_dim / 2; None with one axis: all of them).  ``inverse``: the other way round, which is
+    the gradient's.  ``out``: optional (q, k) to write into, which may be q and k themselves.  A token with
+    a position outside the tables is skipped (its output rows keep what ``out`` held, and are unspecified
+    where it is allocated here) and recorded in the status word."""
+    x = q if q is not None else k
+    dev, T, H, D = _first("q" if q is not None else "k", x)
+    H_q = H if q is not None else 0
+    H_kv = 0 if k is None else _first("k", k)[2]
+    if not isinstance(positions, _Tensor) or positions.dim() != 2:
+        raise TypeError("positions must be an int32 [axes, T] tensor")
+    axes = positions.shape[0]
+    pos_p = _flat("positions", positions, (axes, T), _i32, dev)
+    if not isinstance(cos, _Tensor) or cos.dim() != 2 or cos.shape[0] > _INT_MAX:
+        raise TypeError("cos must be a float32 [rows, rot_dim / 2] tensor")
+    rows, pairs = cos.shape
+    cos_p, sin_p = _flat("cos", cos, (rows, pairs), _f32, dev), _flat("sin", sin, (rows, pairs), _f32, dev)
+    if sections is None:
+        sections = (pairs,)
+    if len(sections) != axes or sum(sections) != pairs or min(sections) <= 0:
+        raise ValueError(f"sections must be {axes} positive numbers of pairs whose sum is {pairs}")
+    sizes = _ints(tuple(int(s) for s in sections))
+    qs = None if q is None else _thd("q", q, (T, H_q, D), dev)
+    ks = None if k is None else _thd("k", k, (T, H_kv, D), dev)
+
+    def call(handle):
+        qo, ko = out if out is not None else (
+            None if q is None else torch.empty((T, H_q, D), dtype=_bf16, device=x.device),
+            None if k is None else torch.empty((T, H_kv, D), dtype=_bf16, device=x.device))
+        if (qo is None) != (q is None) or (ko is None) != (k is None):
+            raise ValueError("out must have a tensor for each of q and k that there is")
+        _check(_load().attn_rope_packed(
+            qs, None if q is None else _thd("out[0]", qo, (T, H_q, D), dev),
+            ks, None if k is None else _thd("out[1]", ko, (T, H_kv, D), dev),
+            pos_p, sizes, axes, cos_p, sin_p, rows, 2 * pairs, 1 if interleaved else 0,
+            1 if inverse else 0, T, H_q, H_kv, D, handle), "attn_rope_packed")
+        return qo, ko
+
+    return paged._on(dev, stream, call)

@@ -53,7 +53,7 @@ typedef enum {
   ATTN_ERR_CUDA = 4,        /* a CUDA runtime or driver call failed */
   ATTN_ERR_TIMEOUT = 5,     /* a kernel wait ran out of time (see attn_device_status) */
   ATTN_ERR_BAD_INDEX = 6    /* a kernel met a page number, length or position out of range
-                               (attn_paged.h; see attn_device_status) */
+                               (attn_paged.h, attn_packed.h; see attn_device_status) */
 } attn_status_t;
 
 /*

@@ -1,0 +1,230 @@
+"""The entry points of packed sequences refuse bad arguments on the host, before any CUDA call
+(CPU only; fake, never-dereferenced device addresses), and the reference of the GPU tests holds
+against torch's own arithmetic and against differences."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import attention_pipelining_gb300 as ap
+from attention_pipelining_gb300 import packed
+from tests import packed_ref as ref
+
+A = 0x10000
+BIG = 1 << 62
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ap.build()
+    return ap._load()
+
+
+def sizes(**kw):
+    d = dict(B=2, T_q=100, T_k=100, H_q=8, H_kv=2, D=128, causal=1, scale=0.1)
+    d.update(kw)
+    return packed._SIZES.pack(*[d[n] for n in ("B", "T_q", "T_k", "H_q", "H_kv", "D", "causal", "scale")])
+
+
+def thd(data=A, st=12 * 128, sh=128):
+    return packed._THD.pack(data or 0, st, sh)
+
+
+def fwd(lib, s=None, q=None, k=None, v=None, o=None, lse=A, cu_q=A, cu_k=A, ws=A, nbytes=BIG):
+    return lib.attn_fwd_packed(sizes() if s is None else s, q or thd(), k or thd(), v or thd(), o or thd(),
+                               lse, cu_q, cu_k, ws, nbytes, None)
+
+
+def bwd(lib, s=None, lse=A, cu_q=A, cu_k=A, ws=A, nbytes=BIG, det=0, **kw):
+    t = [kw.get(n) or thd() for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
+    return lib.attn_bwd_packed(sizes() if s is None else s, *t[:4], lse, *t[4:], cu_q, cu_k, ws, nbytes, det,
+                               None)
+
+
+def rope(lib, q=True, qo=True, k=True, ko=True, positions=A, sections=(16, 24, 24), axes=None, cos=A, sin=A,
+         rows=512, rot=128, inter=0, inverse=0, T=10, H_q=8, H_kv=2, D=128):
+    t = [thd() if x is True else x for x in (q, qo, k, ko)]
+    sec = None if sections is None else packed._ints(tuple(sections))
+    return lib.attn_rope_packed(*t, positions, sec, len(sections or ()) if axes is None else axes, cos, sin,
+                                rows, rot, inter, inverse, T, H_q, H_kv, D, None)
+
+
+BAD_SIZES = [(dict(B=0), 1), (dict(T_q=0), 1), (dict(T_k=-1), 1), (dict(H_q=0), 1), (dict(H_kv=0), 1),
+             (dict(H_q=9), 1), (dict(D=0), 1), (dict(causal=2), 1), (dict(scale=math.nan), 1),
+             (dict(scale=math.inf), 1), (dict(D=96), 2), (dict(B=70000), 2), (dict(H_q=33, H_kv=1), 2),
+             (dict(H_q=132, H_kv=1), 2), (dict(H_q=127, H_kv=1), 2), (dict(T_q=1 << 30), 2),
+             (dict(T_k=1 << 30), 2), (dict(T_k=(1 << 30) - 1, H_q=60000, H_kv=60000), 2),
+             (dict(T_q=(1 << 30) - 1, H_q=128, H_kv=128), 2)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_SIZES, ids=[str(k) for k, _ in BAD_SIZES])
+def test_sizes_are_checked(lib, kw, code):
+    s = sizes(**kw)
+    assert fwd(lib, s) == code
+    assert bwd(lib, s) == code
+    assert lib.attn_packed_workspace_bytes(s) == 0
+    assert lib.attn_packed_bwd_workspace_bytes(s, 0) == 0
+
+
+def test_no_sizes(lib):
+    assert lib.attn_fwd_packed(None, thd(), thd(), thd(), thd(), A, A, A, A, BIG, None) == 1
+    assert lib.attn_packed_workspace_bytes(None) == 0
+
+
+BAD_TENSOR = [(dict(data=None), 1), (dict(data=A + 8), 3), (dict(st=12 * 128 + 4), 3), (dict(sh=12), 3),
+              (dict(st=0), 2), (dict(st=-1536), 2), (dict(sh=-128), 2), (dict(sh=0), 2), (dict(st=1 << 40), 2)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_TENSOR, ids=[str(k) for k, _ in BAD_TENSOR])
+def test_tensors_are_checked(lib, kw, code):
+    for n in ("q", "k", "v", "o"):
+        assert fwd(lib, **{n: thd(**kw)}) == code, n
+    for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv"):
+        assert bwd(lib, **{n: thd(**kw)}) == code, n
+    for n in ("q", "qo", "k", "ko"):
+        assert rope(lib, **{n: thd(**kw)}) == code, n
+
+
+def test_strides_of_single_dimensions_are_not_looked_at(lib):
+    odd = thd(sh=3, st=-5)
+    s = sizes(T_q=1, T_k=1, H_q=1, H_kv=1)
+    assert fwd(lib, s, q=odd, k=odd, v=odd, o=odd, lse=A + 2) == 3      # stops at lse's address
+    assert bwd(lib, s, q=odd, k=odd, v=odd, o=odd, dout=odd, dq=odd, dk=odd, dv=odd, lse=None) == 1
+    assert rope(lib, q=odd, qo=odd, k=odd, ko=odd, T=1, H_q=1, H_kv=1, cos=A + 8) == 3
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(lse=None), 1), (dict(lse=A + 2), 3), (dict(cu_q=None), 1), (dict(cu_q=A + 1), 3),
+    (dict(cu_k=A + 2), 3), (dict(ws=None), 1), (dict(ws=A + 16), 3), (dict(nbytes=100), 1)])
+def test_attention_refuses(lib, kw, code):
+    assert fwd(lib, **kw) == code
+    assert bwd(lib, **kw) == code
+
+
+def test_more_refusals(lib):
+    assert bwd(lib, det=2) == 1
+    assert fwd(lib, sizes(T_k=200), cu_k=None) == 1        # other keys, without their bounds
+    assert bwd(lib, sizes(T_k=200), cu_k=None) == 1
+    need = lib.attn_packed_workspace_bytes(sizes())
+    assert fwd(lib, nbytes=need - 1) == 1
+    assert fwd(lib, nbytes=need, cu_q=A + 2) == 3          # stops at another rule
+    for det in (0, 1):
+        need = lib.attn_packed_bwd_workspace_bytes(sizes(), det)
+        assert bwd(lib, nbytes=need - 1, det=det) == 1
+        assert bwd(lib, nbytes=need, det=det, cu_q=A + 2) == 3
+    assert lib.attn_packed_bwd_workspace_bytes(sizes(), 2) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=0), 1), (dict(H_q=-1), 1), (dict(H_q=0), 1), (dict(q=None), 1), (dict(qo=None), 1),
+    (dict(ko=None), 1), (dict(H_kv=0), 1), (dict(H_q=0, H_kv=0, q=None, qo=None, k=None, ko=None), 1),
+    (dict(positions=None), 1), (dict(sections=None), 1), (dict(sections=(64, 0)), 1),
+    (dict(sections=(64, -1, 1)), 1), (dict(sections=(63,)), 1), (dict(sections=(13,) * 4 + (12,), axes=5), 1),
+    (dict(sections=(2 ** 31 - 1, 2 ** 31 - 1, 66, 64)), 1), (dict(axes=0), 1), (dict(rot=144), 1),
+    (dict(rot=120, sections=(60,)), 1), (dict(rot=0), 1), (dict(rows=0), 1), (dict(inter=2), 1),
+    (dict(inverse=-1), 1), (dict(cos=None), 1), (dict(sin=None), 1), (dict(D=96, rot=96, sections=(48,)), 2),
+    (dict(D=256), 2), (dict(T=1 << 30), 2), (dict(H_q=40000), 2), (dict(positions=A + 2), 3), (dict(cos=A + 8), 3),
+    (dict(sin=A + 4), 3)])
+def test_rotation_refuses(lib, kw, code):
+    assert rope(lib, **kw) == code
+
+
+def test_workspace_holds_the_lists(lib):
+    """A header, the bounds, 32 bytes for each tile and key block that there may be, and (backward)
+    two row vectors and the accumulator."""
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    for H_q, H_kv, positions in ((8, 8, 128), (8, 2, 32), (6, 2, 40), (5, 1, 24), (7, 1, 16), (32, 1, 4),
+                                 (31, 1, 4), (128, 1, 1), (40, 1, 3)):
+        R = H_q // H_kv
+        for B, T in ((1, 1), (3, 1000), (500, 77)):
+            s = sizes(B=B, T_q=T, T_k=T + 3, H_q=H_q, H_kv=H_kv, D=64)
+            lists = 256 + 2 * up(4 * (B + 1)) + up(32 * (T // (2 * positions) + B))
+            assert lib.attn_packed_workspace_bytes(s) == lists
+            vec = (T + 4 * B + 4) * R + 128
+            vec += -vec % 4
+            lists += up(32 * ((T + 3) // 128 + B)) + 2 * up(4 * H_kv * vec)
+            assert lib.attn_packed_bwd_workspace_bytes(s, 1) == lists
+            assert lib.attn_packed_bwd_workspace_bytes(s, 0) == lists + up(4 * T * H_q * 64)
+
+
+def test_binding_refuses_on_the_host():
+    t = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    f = torch.zeros(8, 32)
+    for call in (lambda: ap.attn_fwd_packed(t, t, t, cu, True, 0.1),
+                 lambda: ap.attn_bwd_packed(t, t, t, t, f, t, cu, True, 0.1),
+                 lambda: ap.rope_packed(t, t, cu[None], f, f),
+                 lambda: ap.rope_packed(None, None, cu[None], f, f)):
+        with pytest.raises(TypeError):   # not on a GPU, or no tensor at all
+            call()
+
+
+# ---------------------------------------------------------------- the reference itself
+
+CASES = [([5, 0, 3], [5, 0, 3], True), ([4, 2], [6, 1], True), ([3, 0, 2], [4, 3, 0], False)]
+
+
+def data(lens_q, lens_k, H_q=4, H_kv=2, D=8, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    cu_q, cu_k = ref.bounds(lens_q), ref.bounds(lens_k)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    return (r(cu_q[-1], H_q, D), r(cu_k[-1], H_kv, D), r(cu_k[-1], H_kv, D), r(cu_q[-1], H_q, D), cu_q, cu_k)
+
+
+@pytest.mark.parametrize("lens_q,lens_k,causal", CASES)
+def test_reference_forward(lens_q, lens_k, causal):
+    """Row by row with softmax and logsumexp of torch."""
+    q, k, v, _, cu_q, cu_k = data(lens_q, lens_k)
+    o, lse, to, tl = ref.forward(q, k, v, cu_q, cu_k, causal, 0.3)
+    for b, (n, m) in enumerate(zip(lens_q, lens_k)):
+        for i in range(n):
+            see = max(0, min(m, i + m - n + 1)) if causal else m
+            for h in range(4):
+                t = cu_q[b] + i
+                kk, vv = (x[cu_k[b]:cu_k[b] + see, h // 2] for x in (k, v))
+                if see == 0:
+                    assert (o[t, h] == 0).all() and lse[h, t] == -math.inf
+                    continue
+                s = 0.3 * kk @ q[t, h]
+                assert torch.allclose(torch.softmax(s, 0) @ vv, o[t, h], atol=1e-12)
+                assert torch.allclose(torch.logsumexp(s, 0), lse[h, t], atol=1e-12)
+    assert (to[torch.isfinite(o)] >= 0).all() and (tl[torch.isfinite(lse)] >= 0).all()
+
+
+@pytest.mark.parametrize("lens_q,lens_k,causal", CASES)
+def test_reference_backward_against_differences(lens_q, lens_k, causal):
+    q, k, v, do, cu_q, cu_k = data(lens_q, lens_k)
+    o, lse, _, _ = ref.forward(q, k, v, cu_q, cu_k, causal, 0.3)
+    got = ref.backward(q, k, v, o, lse, do, cu_q, cu_k, causal, 0.3)
+    for name, x in (("dq", q), ("dk", k), ("dv", v)):
+        flat = x.view(-1)
+        for i in range(0, flat.numel(), 3):
+            was, h, ends = flat[i].item(), 1e-5, []
+            for d in (h, -h):
+                flat[i] = was + d
+                ends.append((ref.forward(q, k, v, cu_q, cu_k, causal, 0.3)[0] * do).sum().item())
+            flat[i] = was
+            d = (ends[0] - ends[1]) / (2 * h)
+            # central differences: h^2 times the third derivative, and 2^-52 / h of the sum's rounding
+            assert abs(d - got[name][0].view(-1)[i].item()) <= 1e-7 * (1 + abs(d)), (name, i)
+
+
+def test_reference_rotation():
+    """One axis against complex numbers; several axes section by section; the inverse undoes it to
+    within the two roundings."""
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(6, 3, 32, generator=g).bfloat16().double()
+    pos = torch.randint(0, 50, (3, 6), generator=g)
+    ang = torch.arange(50)[:, None] * 0.3 ** torch.arange(16)
+    cos, sin = torch.cos(ang).float(), torch.sin(ang).float()
+    y = ref.rope(x, pos[:1], cos, sin, [16], True, False)
+    z = torch.view_as_complex(x.view(6, 3, 16, 2).contiguous()) * torch.complex(cos, sin)[pos[0]][:, None].to(torch.complex128)
+    assert torch.equal(y, ref.round_bf16(torch.view_as_real(z).flatten(2)))
+    y = ref.rope(x, pos, cos, sin, [3, 8, 5], False, False)
+    for a, lo, hi in ((0, 0, 3), (1, 3, 11), (2, 11, 16)):
+        one = ref.rope(x, pos[a:a + 1], cos, sin, [16], False, False)
+        assert torch.equal(y[..., lo:hi], one[..., lo:hi]) and torch.equal(y[..., 16 + lo:16 + hi], one[..., 16 + lo:16 + hi])
+    back = ref.rope(y, pos, cos, sin, [3, 8, 5], False, True)
+    r = (x[..., :16] ** 2 + x[..., 16:] ** 2).sqrt().repeat(1, 1, 2)
+    assert ((back - x).abs() <= 3 * 2.0 ** -8 * r).all()
