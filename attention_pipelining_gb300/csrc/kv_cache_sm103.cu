@@ -25,24 +25,6 @@ constexpr int kAhead = 3;               // rows of a thread under way in the app
 constexpr int kFewTokens = 8;           // of a sequence, in a decoding step
 constexpr int kAppendBlocks = 4864;     // 32 blocks on each of 152 SMs, in four rounds
 
-// 16 and 8 bytes to shared memory, asynchronously, in the thread's open group.
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy_async8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// Waits until at most the newest N groups of the thread are under way.
-template <int N>
-__device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // ---------------------------------------------------------------- 4 bits
 
 // The codes (one word, element n in nibble n) and the scale of this lane's 8

@@ -167,28 +167,64 @@ static_assert(kBuckets == kPlanThreads, "one thread to a bucket");
 
 constexpr int kRopeThreads = 128;
 constexpr int kRopeAhead = 4;        // rows of a thread under way
-constexpr int kRopeBlocks = 4864;    // 32 blocks on each of 152 SMs, at least, where there is work for them
+constexpr int kRopeResident = 6;     // thread blocks on an SM
+constexpr int kRopeWave = kRopeResident * 152;
 
 // A token's vector of one head is a row that D / 16 neighbouring lanes hold, 16
 // elements each: eight first and eight second elements of their pairs, or (adjacent
-// pairs, or not rotated) 16 side by side.  A thread block takes kSlots consecutive
+// pairs, or not rotated) eight of either half of the row.  A thread block takes kSlots consecutive
 // tokens and goes with all of them through p.rows of their H_q + H_kv heads: the
-// rotation is read once for all of them.
+// rotation is read once for all of them, and the next rows are on their way while one is
+// worked on.
+//
+// Bound by HBM: 336 MB (16384 tokens of 40 heads of 128) in 57 us are 5.9 TB/s, 89 % of the
+// measured copy rate.  With what rounds exactly left out it took 55 us; with the doubtful
+// roundings in a function of their own, through local memory, 63; with the rows
+// loaded into registers four at a time 69.  Where a row's 16-byte pieces are paired so that one
+// load takes half of each 32-byte sector (adjacent pairs, heads of 64) 24 us became 20.
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kRopeResident)
     rope_packed_kernel(const __grid_constant__ RopePackedParams p) {
   constexpr int kLanes = D / 16;
   constexpr int kSlots = kRopeThreads / kLanes;
+  __shared__ uint4 ring[kRopeAhead][2][kRopeThreads];
   const int c = threadIdx.x % kLanes;
   allow_later();
   wait_for_earlier();
   const long long t = (long long)blockIdx.x * kSlots + threadIdx.x / kLanes;
   if (t >= p.T) return;
-  const int pairs = p.rot_dim / 2;
-  const bool rotates = c < p.rot_dim / 16;
-  const bool apart = !kInterleaved && rotates;
-  // the lane's elements lo .. lo + 7 and hi .. hi + 7
-  const int lo = apart ? 8 * c : 16 * c, hi = apart ? pairs + 8 * c : 16 * c + 8;
+  const int pairs = p.rot_dim / 2, turning = p.rot_dim / 16;
+  // the lane's elements lo .. lo + 7 and hi .. hi + 7, such that neighbouring lanes' lie
+  // side by side; whether each eight hold pairs that are rotated, and the first pair of
+  // the lane's first and second four
+  int lo = 8 * c, hi = D / 2 + 8 * c, d[2] = {4 * c, D / 4 + 4 * c};
+  bool rotates[2] = {lo < p.rot_dim, hi < p.rot_dim};
+  if constexpr (!kInterleaved) {
+    rotates[0] = rotates[1] = c < turning;
+    d[0] = 8 * c, d[1] = 8 * c + 4;
+    hi = pairs + 8 * c;
+    if (c >= turning) {
+      lo = p.rot_dim + 8 * (c - turning);
+      hi = lo + (D - p.rot_dim) / 2;
+    }
+  }
+  // heads [r0, r1) of the queries and the keys behind them; a lane takes what it
+  // requested itself
+  const int r0 = blockIdx.y * p.rows, r1 = min(r0 + p.rows, p.H_q + p.H_kv);
+  int next = r0, put_in = 0;
+  const auto request = [&]() {
+    if (next < r1) {
+      const uint16_t* const src = next < p.H_q ? p.q + t * p.q_st + next * p.q_sh
+                                               : p.k + t * p.k_st + (next - p.H_q) * p.k_sh;
+      copy_async16(&ring[put_in][0][threadIdx.x], src + lo);
+      copy_async16(&ring[put_in][1][threadIdx.x], src + hi);
+      ++next;
+      put_in = put_in + 1 == kRopeAhead ? 0 : put_in + 1;
+    }
+    copy_async_commit();
+  };
+#pragma unroll 1
+  for (int n = 0; n < kRopeAhead; ++n) request();   // (needs no position)
   int row[4];
   bool good = true;
 #pragma unroll
@@ -198,66 +234,53 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
   if (!good) {
     g_packed_status = ATTN_ERR_BAD_INDEX;
+    copy_async_wait<0>();
     return;
   }
   uint64_t cs[4] = {}, sn[4] = {};   // cosines and sines of the lane's eight pairs
-  if (rotates) {
-    const auto row_of = [&](int d) {   // the row that pair d takes
-      return d < p.ends[0] ? row[0] : d < p.ends[1] ? row[1] : d < p.ends[2] ? row[2] : row[3];
+  const auto row_of = [&](int n) {   // the row that pair n takes
+    return n < p.ends[0] ? row[0] : n < p.ends[1] ? row[1] : n < p.ends[2] ? row[2] : row[3];
+  };
+  const float sign = p.inverse ? -1.f : 1.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {   // four pairs, of one row as a rule
+    if (!rotates[i]) continue;
+    int at[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) at[n] = row_of(d[i] + n);
+    const auto table = [&](const float* x) {
+      const float* const y = x + d[i];
+      if (at[0] == at[1] && at[0] == at[2] && at[0] == at[3])
+        return *reinterpret_cast<const float4*>(y + (long long)at[0] * pairs);
+      return make_float4(y[(long long)at[0] * pairs], y[(long long)at[1] * pairs + 1],
+                         y[(long long)at[2] * pairs + 2], y[(long long)at[3] * pairs + 3]);
     };
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = 8 * c + 2 * i;
-      const long long x = (long long)row_of(d) * pairs + d;
-      const long long y = (long long)row_of(d + 1) * pairs + d + 1;
-      cs[i] = f2_pack(p.cos[x], p.cos[y]);
-      const float s0 = p.sin[x], s1 = p.sin[y];
-      sn[i] = p.inverse ? f2_pack(-s0, -s1) : f2_pack(s0, s1);
-    }
+    const float4 a = table(p.cos), b = table(p.sin);
+    cs[2 * i] = f2_pack(a.x, a.y), cs[2 * i + 1] = f2_pack(a.z, a.w);
+    sn[2 * i] = f2_pack(sign * b.x, sign * b.y), sn[2 * i + 1] = f2_pack(sign * b.z, sign * b.w);
   }
-  // heads [r0, r1) of the queries and the keys behind them
-  const int r0 = blockIdx.y * p.rows, r1 = min(r0 + p.rows, p.H_q + p.H_kv);
-  const uint16_t* const q = p.q + t * p.q_st;
-  const uint16_t* const k = p.k + t * p.k_st - p.H_q * p.k_sh;
-  uint16_t* const qo = p.q_out + t * p.qo_st;
-  uint16_t* const ko = p.k_out + t * p.ko_st - p.H_q * p.ko_sh;
+  int take_from = 0;
 #pragma unroll 1
-  for (int h0 = r0; h0 < r1; h0 += kRopeAhead) {
-    uint4 w[kRopeAhead][2];
-#pragma unroll
-    for (int i = 0; i < kRopeAhead; ++i) {
-      const int h = h0 + i;
-      if (h >= r1) break;
-      const uint16_t* const src = h < p.H_q ? q + h * p.q_sh : k + h * p.k_sh;
-      w[i][0] = *reinterpret_cast<const uint4*>(src + lo);
-      w[i][1] = *reinterpret_cast<const uint4*>(src + hi);
+  for (int h = r0; h < r1; ++h) {
+    copy_async_wait<kRopeAhead - 1>();
+    uint4 w[2] = {ring[take_from][0][threadIdx.x], ring[take_from][1][threadIdx.x]};
+    take_from = take_from + 1 == kRopeAhead ? 0 : take_from + 1;
+    request();
+    if constexpr (kInterleaved) {
+      if (rotates[0]) rotate_lane<true>(w[0], {cs[0], cs[1]}, {sn[0], sn[1]});
+      if (rotates[1]) rotate_lane<true>(w[1], {cs[2], cs[3]}, {sn[2], sn[3]});
+    } else if (rotates[0]) {
+      uint4 x = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+      uint4 y = make_uint4(w[0].z, w[0].w, w[1].z, w[1].w);
+      rotate_lane<false>(x, {cs[0], cs[1]}, {sn[0], sn[1]});
+      rotate_lane<false>(y, {cs[2], cs[3]}, {sn[2], sn[3]});
+      w[0] = make_uint4(x.x, x.y, y.x, y.y);
+      w[1] = make_uint4(x.z, x.w, y.z, y.w);
     }
-#pragma unroll
-    for (int i = 0; i < kRopeAhead; ++i) {
-      const int h = h0 + i;
-      if (h >= r1) break;
-      if (rotates) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          // four pairs: {first, second} halves of w[0], w[1], or four adjacent pairs of w[n]
-          const uint64_t c2[2] = {cs[2 * n], cs[2 * n + 1]}, s2[2] = {sn[2 * n], sn[2 * n + 1]};
-          if constexpr (kInterleaved) {
-            rotate_lane<true>(w[i][n], c2, s2);
-          } else {
-            uint4 x = n == 0 ? make_uint4(w[i][0].x, w[i][0].y, w[i][1].x, w[i][1].y)
-                             : make_uint4(w[i][0].z, w[i][0].w, w[i][1].z, w[i][1].w);
-            rotate_lane<false>(x, c2, s2);
-            if (n == 0)
-              w[i][0].x = x.x, w[i][0].y = x.y, w[i][1].x = x.z, w[i][1].y = x.w;
-            else
-              w[i][0].z = x.x, w[i][0].w = x.y, w[i][1].z = x.z, w[i][1].w = x.w;
-          }
-        }
-      }
-      uint16_t* const dst = h < p.H_q ? qo + h * p.qo_sh : ko + h * p.ko_sh;
-      *reinterpret_cast<uint4*>(dst + lo) = w[i][0];
-      *reinterpret_cast<uint4*>(dst + hi) = w[i][1];
-    }
+    uint16_t* const dst = h < p.H_q ? p.q_out + t * p.qo_st + h * p.qo_sh
+                                    : p.k_out + t * p.ko_st + (h - p.H_q) * p.ko_sh;
+    *reinterpret_cast<uint4*>(dst + lo) = w[0];
+    *reinterpret_cast<uint4*>(dst + hi) = w[1];
   }
 }
 
@@ -267,8 +290,10 @@ cudaError_t launch_rope_d(const RopePackedParams& in, bool interleaved, cudaStre
   const int slots = kRopeThreads / (D / 16);
   const int heads = p.H_q + p.H_kv;
   const long long groups = ((long long)p.T + slots - 1) / slots;
-  // all heads of a token to one thread block where the tokens fill the GPU
-  long long parts = (kRopeBlocks + groups - 1) / groups;
+  // A token's heads are shared out so that all thread blocks run at once where they can,
+  // and otherwise come in two waves at least (16384 tokens of 40 heads of 128: 57 us,
+  // in 1.1 waves 63-65; 9001 tokens of 32 heads of 64 in one wave 15.4 us, in two 17-18).
+  long long parts = groups <= kRopeWave ? kRopeWave / groups : (2 * kRopeWave + groups - 1) / groups;
   if (parts > heads) parts = heads;
   p.rows = (int)((heads + parts - 1) / parts);
   const dim3 grid((unsigned)groups, (unsigned)((heads + p.rows - 1) / p.rows));

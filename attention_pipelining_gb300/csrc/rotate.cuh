@@ -8,42 +8,42 @@
 
 namespace attnpipe {
 
-// x a - y b rounded once to bf16 (returned as a float).  x and y are bf16
+// u a + w b of two pairs, rounded once to bf16 (returned as floats).  u and w are bf16
 // values and a and b fp32, so the exact value may have more bits than a float:
 // the products' and the sum's rounding errors are recovered (fma, two-sum) and
 // added back, and the fp32 result, when it falls on a tie of the bf16 rounding
 // that the remainder breaks, is moved one step to the remainder's side.  Non-finite
 // values take the plain formula's result.
-__device__ __forceinline__ float rotate_bf16(float x, float a, float y, float b) {
-  const float h = __fmul_rn(x, a), h2 = __fmul_rn(-y, b);
-  const float e = __fmaf_rn(x, a, -h), e2 = __fmaf_rn(-y, b, -h2);
-  const float s = __fadd_rn(h, h2);
-  const float t = __fsub_rn(s, h);
-  const float es = __fadd_rn(__fsub_rn(h, __fsub_rn(s, t)), __fsub_rn(h2, t));
-  const float lo = __fadd_rn(es, __fadd_rn(e, e2));
-  const float r = __fadd_rn(s, lo);
-  if (!(fabsf(r) <= 3.4028235e38f)) return s;   // an infinity or a NaN
-  const float rem = __fsub_rn(lo, __fsub_rn(r, s));
-  uint32_t u = __float_as_uint(r);
-  if ((u & 0xffffu) == 0x8000u && rem != 0.f) u += ((rem > 0.f) == (r > 0.f)) ? 1u : 0xffffffffu;
-  return __uint_as_float(u);
-}
-
-// Four pairs, v = {x, y, c, s}: r = {x c - y s, y c + x s}.
-static __device__ __noinline__ void rotate4_exactly(const float (&v)[4][4], float (&r)[2][4]) {
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    r[0][i] = rotate_bf16(v[0][i], v[2][i], v[1][i], v[3][i]);
-    r[1][i] = rotate_bf16(v[1][i], v[2][i], -v[0][i], v[3][i]);
+__device__ __forceinline__ void rotate2_exactly(uint64_t u, uint64_t a, uint64_t w, uint64_t b,
+                                                float& r0, float& r1) {
+  const uint64_t minus = f2_pack(-1.f, -1.f);
+  const auto sub = [&](uint64_t x, uint64_t y) { return f2_fma(y, minus, x); };
+  const uint64_t h = f2_mul(u, a), h2 = f2_mul(w, b);
+  const uint64_t e = f2_fma(u, a, f2_mul(h, minus)), e2 = f2_fma(w, b, f2_mul(h2, minus));
+  const uint64_t s = f2_add(h, h2), t = sub(s, h);
+  const uint64_t es = f2_add(sub(h, sub(s, t)), sub(h2, t));
+  const uint64_t lo = f2_add(es, f2_add(e, e2)), r = f2_add(s, lo), rem = sub(lo, sub(r, s));
+  float rr[2], ss[2], mm[2];
+  f2_unpack(r, rr[0], rr[1]);
+  f2_unpack(s, ss[0], ss[1]);
+  f2_unpack(rem, mm[0], mm[1]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t x = __float_as_uint(rr[i]);
+    if ((x & 0xffffu) == 0x8000u && mm[i] != 0.f)
+      x += ((mm[i] > 0.f) == (rr[i] > 0.f)) ? 1u : 0xffffffffu;
+    // an infinity or a NaN: the plain formula's
+    rr[i] = fabsf(rr[i]) <= 3.4028235e38f ? __uint_as_float(x) : ss[i];
   }
+  r0 = rr[0], r1 = rr[1];
 }
 
-// The same, two pairs at a time: first with five operations a result,
+// Four pairs: (x c - y s, y c + x s), first with five operations a result,
 // fma(x, c, h) + e with h + e = -y s exactly, which is off by at most two units of
 // fp32's last place (half a unit in each of the two sums, of which the first may
 // be twice as large as the second's; the sum of products that cancel is exact);
 // only where that leaves the bf16 rounding open (two units around a tie: one
-// element in 13000) or a value is not finite, by rotate_bf16.
+// element in 13000) or a value is not finite, by rotate2_exactly.
 // Rounding the plain fp32 formula instead would round about one element in 2^15
 // the other way than the exact value, and in a 4-bit cache change its code.
 __device__ __forceinline__ void rotate4(const uint64_t (&x)[2], const uint64_t (&y)[2],
@@ -70,17 +70,12 @@ __device__ __forceinline__ void rotate4(const uint64_t (&x)[2], const uint64_t (
   float f0, f1;
   f2_unpack(finite, f0, f1);
   if ((nearest & 0xffffu) <= 4u || (nearest >> 16) <= 4u || f0 + f1 != 0.f) {
-    float v[4][4], r[2][4];   // copies: the arrays themselves stay in registers
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f2_unpack(x[i], v[0][2 * i], v[0][2 * i + 1]);
-      f2_unpack(y[i], v[1][2 * i], v[1][2 * i + 1]);
-      f2_unpack(c[i], v[2][2 * i], v[2][2 * i + 1]);
-      f2_unpack(s[i], v[3][2 * i], v[3][2 * i + 1]);
+      const uint64_t ms = f2_mul(s[i], minus);
+      rotate2_exactly(x[i], c[i], y[i], ms, r1[2 * i], r1[2 * i + 1]);
+      rotate2_exactly(y[i], c[i], x[i], s[i], r2[2 * i], r2[2 * i + 1]);
     }
-    rotate4_exactly(v, r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r1[i] = r[0][i], r2[i] = r[1][i];
   }
 }
 
