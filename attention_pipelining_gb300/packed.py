@@ -38,58 +38,71 @@ def _import():
     torch = paged.torch
 
 
-def _first(name, t):
-    """(device index, tokens, heads, D) of a call's first tensor"""
+# A call looks at each tensor once, and what is wrong is worked out only when something is: a small
+# call's kernels take less time than torch's accessors.
+
+
+def _device(name, t):
+    """The device index of a call's first tensor"""
     if torch is None:
         _import()
-    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype is not _bf16 or t.dim() != 3:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor [tokens, heads, D]")
-    T, H, D = t.shape
-    if T > _INT_MAX or H > _INT_MAX or D > _INT_MAX:   # (a view may claim any number of them)
-        raise ValueError(f"{name}: sizes must be below 2^31")
-    return t.get_device(), T, H, D
+    return t.get_device()
 
 
-def _thd(name, t, shape, dev):
+def _thd(name, t, dev):
+    """(attn_thd_t, shape) of a bf16 tensor [tokens, heads, D]"""
+    try:
+        st, sh, sd = t.stride()
+        if sd == 1 and t.dtype is _bf16 and t.get_device() == dev:
+            return _THD.pack(t.data_ptr(), st, sh), t.shape
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not _bf16 or t.dim() != 3:
+        raise TypeError(f"{name} must be a bfloat16 tensor [tokens, heads, D] on the same device as the others")
+    raise ValueError(f"{name}'s last dimension must be contiguous, not with strides {t.stride()}")
+
+
+def _like(name, t, shape, dev):
     """attn_thd_t of a bf16 tensor of that shape"""
-    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not _bf16:
-        raise TypeError(f"{name} must be a bfloat16 tensor on the same device as the others")
-    st, sh, sd = t.stride() if t.shape == shape else (0, 0, 0)
-    if sd != 1:
-        raise ValueError(f"{name} must be {list(shape)} with a contiguous last dimension, not "
-                         f"{list(t.shape)} with strides {t.stride()}")
-    return _THD.pack(t.data_ptr(), st, sh)
+    x, got = _thd(name, t, dev)
+    if got != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(got)}")
+    return x
 
 
 def _flat(name, t, shape, dtype, dev):
-    if not isinstance(t, _Tensor) or t.get_device() != dev or t.dtype is not dtype \
-            or t.shape != shape or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the same device as "
-                        "the others")
-    return t.data_ptr()
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        pass
+    raise TypeError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the same device as the others")
 
 
-def _bounds(cu_q, cu_k, dev):
-    """(sequences, cu_q's pointer, cu_k's pointer or None)"""
-    if not isinstance(cu_q, _Tensor) or cu_q.dim() != 1 or not 1 < cu_q.shape[0] <= _INT_MAX:
-        raise TypeError("cu_q must be an int32 [sequences + 1] tensor")
-    shape = cu_q.shape
-    return (shape[0] - 1, _flat("cu_q", cu_q, shape, _i32, dev),
-            None if cu_k is None else _flat("cu_k", cu_k, shape, _i32, dev))
+def _small(*sizes):
+    if max(sizes) > _INT_MAX:   # (a view may claim any number of tokens)
+        raise ValueError("sizes must be below 2^31")
 
 
 def _sizes(q, k, v, cu_q, cu_k, causal, scale):
     """What both attention calls begin with: device, shapes, attn_packed_t, tensors and bounds."""
-    dev, T_q, H_q, D = _first("q", q)
-    _, T_k, H_kv, _ = _first("k", k)
-    if cu_k is None and T_k != T_q:
-        raise ValueError("without cu_k, k and v must have as many tokens as q")
-    B, cq, ck = _bounds(cu_q, cu_k, dev)
-    q_shape, k_shape = (T_q, H_q, D), (T_k, H_kv, D)
-    return (dev, q_shape, k_shape,
-            _SIZES.pack(B, T_q, T_k, H_q, H_kv, D, 1 if causal else 0, scale),
-            _thd("q", q, q_shape, dev), _thd("k", k, k_shape, dev), _thd("v", v, k_shape, dev),
-            cq, ck)
+    dev = _device("q", q)
+    (qs, q_shape), (ks, k_shape), (vs, v_shape) = _thd("q", q, dev), _thd("k", k, dev), _thd("v", v, dev)
+    T_q, H_q, D = q_shape
+    T_k, H_kv, Dk = k_shape
+    if k_shape != v_shape or D != Dk or (cu_k is None and T_k != T_q):
+        raise ValueError(f"q {list(q_shape)}, k {list(k_shape)} and v {list(v_shape)} do not go together"
+                         + ("" if cu_k is not None else " (without cu_k they have the same tokens)"))
+    if not isinstance(cu_q, _Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise TypeError("cu_q must be an int32 [sequences + 1] tensor")
+    bounds = cu_q.shape
+    B = bounds[0] - 1
+    _small(T_q, T_k, H_q, D, B)
+    return (dev, q_shape, k_shape, _SIZES.pack(B, T_q, T_k, H_q, H_kv, D, 1 if causal else 0, scale), qs, ks, vs,
+            _flat("cu_q", cu_q, bounds, _i32, dev),
+            None if cu_k is None else _flat("cu_k", cu_k, bounds, _i32, dev))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -113,21 +126,12 @@ def packed_bwd_workspace_bytes(B: int, T_q: int, T_k: int, H_q: int, H_kv: int, 
     return _bwd_bytes(_SIZES.pack(B, T_q, T_k, H_q, H_kv, D, 0, 1.0), 1 if deterministic else 0)
 
 
-def _with_workspace(workspace, nbytes, dev, handle, where, call):
-    """call(pointer, bytes) with the caller's workspace, or one that lives until what is queued is done."""
-    if nbytes == 0:
-        raise AttnError(1, where)
-    if workspace is not None:
-        if not isinstance(workspace, _Tensor) or workspace.get_device() != dev \
-                or workspace.dtype is not _u8 or not workspace.is_contiguous():
-            raise TypeError("workspace must be a contiguous uint8 tensor on the same device as the others")
-        call(workspace.data_ptr(), workspace.numel())
-        return
-    mine = _alloc(nbytes, handle)
-    try:
-        call(mine, nbytes)
-    finally:   # (used again only by what follows on the stream)
-        _free(mine)
+def _given(workspace, dev):
+    """(pointer, bytes) of a caller's workspace"""
+    if not isinstance(workspace, _Tensor) or workspace.get_device() != dev \
+            or workspace.dtype is not _u8 or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor on the same device as the others")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def attn_fwd_packed(q, k, v, cu_q, causal: bool, scale: float, cu_k=None, workspace=None, out=None,
@@ -142,15 +146,22 @@ def attn_fwd_packed(q, k, v, cu_q, causal: bool, scale: float, cu_k=None, worksp
     # the workspace may get)
     dev, q_shape, k_shape, sizes, qs, ks, vs, cq, ck = _sizes(q, k, v, cu_q, cu_k, causal, scale)
     lse_shape = (q_shape[1], q_shape[0])
+    nbytes = _fwd_bytes(sizes)
+    if nbytes == 0:
+        raise AttnError(1, "attn_packed_workspace_bytes")
 
     def call(handle):
         o, lse = out if out is not None else (
             torch.zeros(q_shape, dtype=_bf16, device=q.device),
             torch.zeros(lse_shape, dtype=_f32, device=q.device))
-        os, lse_p = _thd("out[0]", o, q_shape, dev), _flat("out[1]", lse, lse_shape, _f32, dev)
-        _with_workspace(workspace, _fwd_bytes(sizes), dev, handle, "attn_packed_workspace_bytes",
-                        lambda ws, n: _check(_load().attn_fwd_packed(
-                            sizes, qs, ks, vs, os, lse_p, cq, ck, ws, n, handle), "attn_fwd_packed"))
+        os, lse_p = _like("out[0]", o, q_shape, dev), _flat("out[1]", lse, lse_shape, _f32, dev)
+        ws, n = _given(workspace, dev) if workspace is not None else (_alloc(nbytes, handle), nbytes)
+        try:
+            _check(_load().attn_fwd_packed(sizes, qs, ks, vs, os, lse_p, cq, ck, ws, n, handle),
+                   "attn_fwd_packed")
+        finally:   # (used again only by what follows on the stream)
+            if workspace is None:
+                _free(ws)
         return o, lse
 
     return paged._on(dev, stream, call)
@@ -165,28 +176,38 @@ def attn_bwd_packed(q, k, v, o, lse, dout, cu_q, causal: bool, scale: float, cu_
     where it is allocated here).  ``deterministic``: dq reproducible bit for bit (dk and dv always
     are)."""
     dev, q_shape, k_shape, sizes, qs, ks, vs, cq, ck = _sizes(q, k, v, cu_q, cu_k, causal, scale)
-    os, dos = _thd("o", o, q_shape, dev), _thd("dout", dout, q_shape, dev)
+    os, dos = _like("o", o, q_shape, dev), _like("dout", dout, q_shape, dev)
     lse_p = _flat("lse", lse, (q_shape[1], q_shape[0]), _f32, dev)
     det = 1 if deterministic else 0
+    nbytes = _bwd_bytes(sizes, det)
+    if nbytes == 0:
+        raise AttnError(1, "attn_packed_bwd_workspace_bytes")
 
     def call(handle):
-        grads = tuple(out) if out is not None else tuple(
+        dq, dk, dv = out if out is not None else (
             torch.zeros(s, dtype=_bf16, device=q.device) for s in (q_shape, k_shape, k_shape))
-        gs = [_thd(f"out[{i}]", g, s, dev) for i, (g, s) in enumerate(zip(grads, (q_shape, k_shape, k_shape)))]
-        if len(gs) != 3:
-            raise ValueError("out must be (dq, dk, dv)")
-        _with_workspace(workspace, _bwd_bytes(sizes, det), dev, handle, "attn_packed_bwd_workspace_bytes",
-                        lambda ws, n: _check(_load().attn_bwd_packed(
-                            sizes, qs, ks, vs, os, lse_p, dos, *gs, cq, ck, ws, n, det, handle),
-                            "attn_bwd_packed"))
-        return grads
+        dqs, dks = _like("out[0]", dq, q_shape, dev), _like("out[1]", dk, k_shape, dev)
+        dvs = _like("out[2]", dv, k_shape, dev)
+        ws, n = _given(workspace, dev) if workspace is not None else (_alloc(nbytes, handle), nbytes)
+        try:
+            _check(_load().attn_bwd_packed(sizes, qs, ks, vs, os, lse_p, dos, dqs, dks, dvs, cq, ck, ws, n, det,
+                                           handle), "attn_bwd_packed")
+        finally:
+            if workspace is None:
+                _free(ws)
+        return dq, dk, dv
 
     return paged._on(dev, stream, call)
 
 
 @functools.lru_cache(maxsize=256)
-def _ints(values):
-    return struct.pack(f"@{len(values)}i", *values)
+def _sections(sections, axes, pairs):
+    """The sections as the C entry takes them"""
+    if sections is None:
+        sections = (pairs,)
+    if len(sections) != axes or sum(sections) != pairs or min(sections) <= 0:
+        raise ValueError(f"sections must be {axes} positive numbers of pairs whose sum is {pairs}")
+    return struct.pack(f"@{axes}i", *sections)
 
 
 def rope_packed(q, k, positions, cos, sin, sections=None, interleaved: bool = False,
@@ -199,35 +220,37 @@ def rope_packed(q, k, positions, cos, sin, sections=None, interleaved: bool = Fa
     a position outside the tables is skipped (its output rows keep what ``out`` held, and are unspecified
     where it is allocated here) and recorded in the status word."""
     x = q if q is not None else k
-    dev, T, H, D = _first("q" if q is not None else "k", x)
-    H_q = H if q is not None else 0
-    H_kv = 0 if k is None else _first("k", k)[2]
-    if not isinstance(positions, _Tensor) or positions.dim() != 2:
-        raise TypeError("positions must be an int32 [axes, T] tensor")
-    axes = positions.shape[0]
+    dev = _device("q" if q is not None else "k", x)
+    qs = ks = q_shape = k_shape = None
+    H_q = H_kv = 0
+    if k is not None:
+        ks, k_shape = _thd("k", k, dev)
+        T, H_kv, D = k_shape
+    if q is not None:
+        qs, q_shape = _thd("q", q, dev)
+        T, H_q, D = q_shape
+        if k is not None and (T, D) != (k_shape[0], k_shape[2]):
+            raise ValueError(f"q {list(q_shape)} and k {list(k_shape)} do not go together")
+    if not isinstance(positions, _Tensor) or positions.dim() != 2 or not isinstance(cos, _Tensor) \
+            or cos.dim() != 2:
+        raise TypeError("positions must be an int32 [axes, T] tensor and cos a float32 [rows, rot_dim / 2] one")
+    axes, table = positions.shape[0], cos.shape
+    rows, pairs = table
+    _small(T, H_q, H_kv, D, rows, 2 * pairs, axes)
     pos_p = _flat("positions", positions, (axes, T), _i32, dev)
-    if not isinstance(cos, _Tensor) or cos.dim() != 2 or cos.shape[0] > _INT_MAX:
-        raise TypeError("cos must be a float32 [rows, rot_dim / 2] tensor")
-    rows, pairs = cos.shape
-    cos_p, sin_p = _flat("cos", cos, (rows, pairs), _f32, dev), _flat("sin", sin, (rows, pairs), _f32, dev)
-    if sections is None:
-        sections = (pairs,)
-    if len(sections) != axes or sum(sections) != pairs or min(sections) <= 0:
-        raise ValueError(f"sections must be {axes} positive numbers of pairs whose sum is {pairs}")
-    sizes = _ints(tuple(int(s) for s in sections))
-    qs = None if q is None else _thd("q", q, (T, H_q, D), dev)
-    ks = None if k is None else _thd("k", k, (T, H_kv, D), dev)
+    cos_p, sin_p = _flat("cos", cos, table, _f32, dev), _flat("sin", sin, table, _f32, dev)
+    sections = _sections(None if sections is None else tuple(sections), axes, pairs)
 
     def call(handle):
         qo, ko = out if out is not None else (
-            None if q is None else torch.empty((T, H_q, D), dtype=_bf16, device=x.device),
-            None if k is None else torch.empty((T, H_kv, D), dtype=_bf16, device=x.device))
+            None if q is None else torch.empty(q_shape, dtype=_bf16, device=x.device),
+            None if k is None else torch.empty(k_shape, dtype=_bf16, device=x.device))
         if (qo is None) != (q is None) or (ko is None) != (k is None):
             raise ValueError("out must have a tensor for each of q and k that there is")
         _check(_load().attn_rope_packed(
-            qs, None if q is None else _thd("out[0]", qo, (T, H_q, D), dev),
-            ks, None if k is None else _thd("out[1]", ko, (T, H_kv, D), dev),
-            pos_p, sizes, axes, cos_p, sin_p, rows, 2 * pairs, 1 if interleaved else 0,
+            qs, None if q is None else _like("out[0]", qo, q_shape, dev),
+            ks, None if k is None else _like("out[1]", ko, k_shape, dev),
+            pos_p, sections, axes, cos_p, sin_p, rows, 2 * pairs, 1 if interleaved else 0,
             1 if inverse else 0, T, H_q, H_kv, D, handle), "attn_rope_packed")
         return qo, ko
 

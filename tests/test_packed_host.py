@@ -3,6 +3,7 @@
 against torch's own arithmetic and against differences."""
 import ctypes
 import math
+import struct
 
 import pytest
 import torch
@@ -45,7 +46,7 @@ def bwd(lib, s=None, lse=A, cu_q=A, cu_k=A, ws=A, nbytes=BIG, det=0, **kw):
 def rope(lib, q=True, qo=True, k=True, ko=True, positions=A, sections=(16, 24, 24), axes=None, cos=A, sin=A,
          rows=512, rot=128, inter=0, inverse=0, T=10, H_q=8, H_kv=2, D=128):
     t = [thd() if x is True else x for x in (q, qo, k, ko)]
-    sec = None if sections is None else packed._ints(tuple(sections))
+    sec = None if sections is None else struct.pack(f"@{len(sections)}i", *sections)
     return lib.attn_rope_packed(*t, positions, sec, len(sections or ()) if axes is None else axes, cos, sin,
                                 rows, rot, inter, inverse, T, H_q, H_kv, D, None)
 
