@@ -519,6 +519,12 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   int kvb, zkv;
   int n_keys = 0, tok_k = 0;   // packed: keys of the block, its first token
   int tok_q = 0, q_len = 0, vec0 = 0, shift = 0, first_tile = 0, n_tiles = 0;   // and PackedKeys' others
+  int all_tiles = 0;
+  // {sequence's tiles, parts, part, slot}: read where it is needed, to save registers
+  auto of_parts = [&]() -> int4 {
+    if constexpr (kPacked) return reinterpret_cast<const int4*>(p.sh.keys + kvb)[2];
+    return make_int4(0, 1, 0, 0);
+  };
   if constexpr (kPacked) {
     wait_for_earlier();
     const int entries = p.sh.head->key_blocks;
@@ -534,6 +540,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     shift = b.y;
     first_tile = b.z;
     n_tiles = b.w;
+    all_tiles = src[2].x;
   } else if (p.causal) {
     banded_rank((int)blockIdx.x, n_kvb, p.groups, kvb, zkv);
   } else {
@@ -546,7 +553,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // rotated by the key block, so the CTAs running at once add into
   // different dQ rows (with the causal mask each key block starts at its own
   // diagonal anyway)
-  const int rot = kPacked ? first_tile : (kFuse && !p.causal) ? kvb % n_qb : 0;
+  const int rot = (!kPacked && kFuse && !p.causal) ? kvb % n_qb : 0;
   auto qb_at = [&](int i) { return i + rot < n_qb ? i + rot : i + rot - n_qb; };
   // The query blocks with work (items n = 0 .. n_work - 1), walked by every
   // role in the same order.  With the causal mask and S_q a multiple of 128
@@ -570,8 +577,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // position (the ragged causal case only; items are asked for in order)
   auto item_r0 = [&](int n, int& cursor) -> int {
     // (packed: the tile's first query position)
-    if constexpr (kPacked)
-      return (p.causal ? first_tile + n : qb_at(n)) * p.sh.positions;
+    if constexpr (kPacked) {
+      const int t = first_tile + n;
+      return (t < all_tiles ? t : t - all_tiles) * p.sh.positions;
+    }
     if (!p.causal) return qb_at(n) * kRows;
     if (by_head) {
       const int h = n / per_head;
@@ -802,6 +811,8 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       tc_fence_after_sync();
     }
     const bool row_ok = key < key_end;
+    const int4 of = of_parts();
+    const int parts = of.y, part = of.z, slot = of.w;
     uint16_t* dk_row = static_cast<uint16_t*>(p.dk);
     uint16_t* dv_row = static_cast<uint16_t*>(p.dv);
     if constexpr (kPacked) {
@@ -814,7 +825,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 #pragma unroll
     for (int which = 0; which < 2; ++which) {  // 0: dV, 1: dK
       uint16_t* dst = which ? dk_row : dv_row;
-      const float mult = which ? p.scale : 1.f;
+      const float mult = (kPacked && parts > 1) ? 1.f : which ? p.scale : 1.f;
       const uint32_t acc = tmem + lane_base + (which ? C::kTmAcc1 : C::kTmAcc0) + (D / 2) * w;
 #pragma unroll
       for (int ch = 0; ch < D / 64; ++ch) {
@@ -827,7 +838,18 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;  // no query sees these keys
         }
-        if (row_ok && ok) {
+        if (kPacked && parts > 1) {
+          if constexpr (kPacked) {
+            float4* f4 = reinterpret_cast<float4*>(
+                p.sh.key_parts +
+                ((((size_t)(slot + part) * p.H_kv + zkv) * 2 + which) * kRows + r) * D +
+                (D / 2) * w + ch * 32);
+#pragma unroll
+            for (int qd = 0; qd < 8; ++qd)
+              f4[qd] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
+                                   u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
+          }
+        } else if (row_ok && ok) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + (D / 2) * w + ch * 32);
 #pragma unroll
           for (int qd = 0; qd < 4; ++qd) {
@@ -841,6 +863,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         }
       }
     }
+    if (kPacked && parts > 1) __threadfence();
   } else if (warp == 8) {
     // -------------------------------------------------------- tensor-core issuer
     const bool leader = elect_one();
@@ -1087,9 +1110,48 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   tc_fence_after_sync();
   if (warp == 8) tmem_dealloc(tmem, C::kTmemCols);
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
+  if constexpr (kPacked) {
+    // the last of the block's parts adds them up, eight elements a thread
+    const int4 of = of_parts();
+    const int parts = of.y, slot = of.w;
+    if (parts > 1 && !*sAbort &&
+        last_of_parts(p.sh.key_counters + (size_t)slot * p.H_kv + zkv, parts,
+                      reinterpret_cast<volatile int*>(smem + C::kOffMiscKV + 8))) {
+      const size_t step = (size_t)p.H_kv * 2 * kRows * D;
+      for (int i = threadIdx.x; i < 2 * n_keys * (D / 8); i += blockDim.x) {
+        const int which = i / (n_keys * (D / 8)), n = i - which * n_keys * (D / 8);
+        const int r = n / (D / 8), c = n % (D / 8);
+        float x[8];
+        sum_parts(x, p.sh.key_parts + ((((size_t)slot * p.H_kv + zkv) * 2 + which) * kRows + r) * D + c * 8,
+                  step, parts, [](int) { return 1.f; });
+        const long long tok = tok_k + r;
+        uint16_t* dst = which ? static_cast<uint16_t*>(p.dk) + tok * p.dk_st + zkv * p.dk_sh
+                              : static_cast<uint16_t*>(p.dv) + tok * p.dv_st + zkv * p.dv_sh;
+        store_bf16x8(dst + c * 8, x, which ? p.scale : 1.f);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- dQ
+
+// The last of the parts of a packed tile's half adds up their dQ, eight elements a thread;
+// `first`: the rows in the first part.  Whole block.
+template <int D>
+__device__ __forceinline__ void join_dq(const PackedBwdParams& p, size_t slot, int half, int parts,
+                                        int n_rows, int tok_q, int zkv, const float* first,
+                                        volatile int* flag) {
+  if (!last_of_parts(p.sh.tile_counters + slot * 2 + half, parts, flag)) return;
+  for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreadsB) {
+    const int r = i / (D / 8), c = i % (D / 8), at = (r * p.sh.inv_group) >> 16;
+    float x[8];
+    sum_parts(x, first + (size_t)r * D + c * 8, (size_t)p.H_kv * 256 * D, parts,
+              [](int) { return 1.f; });
+    store_bf16x8(static_cast<uint16_t*>(p.dq) + (long long)(tok_q + at) * p.dq_st +
+                     (zkv * p.sh.group + r - at * p.sh.group) * p.dq_sh + c * 8,
+                 x, p.scale);
+  }
+}
 
 template <int D, bool kPacked = false>
 __global__ void __launch_bounds__(kThreadsB, 1)
@@ -1121,15 +1183,24 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   int zkv, r0 = 0, n_kb;
   int n_rows = kRows;                                   // packed: the tile's rows that exist
   int tok_q = 0, tok_k = 0, k_len = 0, n_keys = 0, diag = 0, vec0 = 0;   // and PackedTile's others
+  int jb = 0, parts = 1, half = 0;
+  size_t slot = 0;   // of the tile's first part and this K/V head
+  // the rows' dQ in a part (of a tile's halves 128 rows each)
+  auto part_row = [&](int part, int row) -> float* {
+    if constexpr (kPacked)
+      return p.sh.tile_parts + ((slot + (size_t)part * p.H_kv) * 256 + half * kRows + row) * D;
+    return nullptr;
+  };
+  int part = 0;
   if constexpr (kPacked) {
     wait_for_earlier();
     const int entries = p.sh.head->tiles, positions = p.sh.positions;
-    const int half = (int)(blockIdx.x & 1);
+    half = (int)(blockIdx.x & 1);
     if ((long long)(blockIdx.x >> 1) >= (long long)entries * p.H_kv) return;
     int entry;
     banded_rank((int)(blockIdx.x >> 1), entries, p.H_kv, entry, zkv);
     const int4* src = reinterpret_cast<const int4*>(p.sh.tiles + entry);
-    const int4 a = src[0], b = src[1];   // in PackedTile's order
+    const int4 a = src[0], b = src[1], c4 = src[2];   // in PackedTile's order
     const int rows = a.y - half * positions;
     if (rows <= 0) return;
     n_rows = min(rows, positions) * p.sh.group;
@@ -1139,8 +1210,21 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     diag = b.y + half * positions;
     n_keys = p.causal ? min(max(diag + min(rows, positions) - 1, 0), k_len) : k_len;
     vec0 = b.z + half * positions;
-    n_kb = (n_keys + kRows - 1) / kRows;
-    if (n_kb == 0) {   // no row sees a key: dQ = 0
+    jb = b.w;
+    parts = c4.y;
+    part = c4.z;
+    slot = (size_t)c4.w * p.H_kv + zkv;
+    // (a half may see fewer keys than the tile)
+    n_kb = min((n_keys + kRows - 1) / kRows, jb + c4.x) - jb;
+    if (n_kb <= 0) {   // no row sees a key of these: dQ = 0
+      if (parts > 1) {
+        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreadsB)
+          reinterpret_cast<float4*>(part_row(part, 0))[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        __threadfence();
+        join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, part_row(0, 0),
+                   reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 8));
+        return;
+      }
       for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreadsB) {
         const int row = i / (D / 8), at = (row * p.sh.inv_group) >> 16;
         uint16_t* dst = static_cast<uint16_t*>(p.dq) + (long long)(tok_q + at) * p.dq_st +
@@ -1239,7 +1323,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       mbar_arrive(qt_ready);
     }
     for (int j = 0; j < n_kb && ok; ++j) {
-      const int kb0 = j * kRows;
+      const int kb0 = (jb + j) * kRows;
       const bool masked = !row_ok || (kb0 + kRows > key_limit);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -1307,7 +1391,13 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld_x32(acc + ch * 32, v);
         tmem_ld_wait();
         reg_after_wait(v);
-        if (row_ok) {
+        if (kPacked && parts > 1) {
+          float4* f4 = reinterpret_cast<float4*>(part_row(part, r) + (D / 2) * w + ch * 32);
+#pragma unroll
+          for (int qd = 0; qd < 8; ++qd)
+            f4[qd] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
+                                 u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
+        } else if (row_ok) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
           const float mult = p.scale;
 #pragma unroll
@@ -1321,6 +1411,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           }
         }
       }
+      if (kPacked && parts > 1) __threadfence();
     }
   } else if (warp == 8) {
     // -------------------------------------------------------- tensor-core issuer
@@ -1345,7 +1436,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // packed: rows of K behind the sequence's end, for dQ += dS K
     auto clear_keys = [&](int j) {
       if constexpr (kPacked) {
-        if (k_len - j * kRows < kRows) clear_rows<D>(stage_k(j % C::kKVStages), k_len - j * kRows);
+        const int left = k_len - (jb + j) * kRows;
+        if (left < kRows) clear_rows<D>(stage_k(j % C::kKVStages), left);
       }
     };
     if (ok && warp_wait_b(&kv_full[0], 0, sAbort, budget)) {
@@ -1414,8 +1506,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (leader) {
         mbar_arrive_expect_tx(&kv_full[s], 2 * C::kTileBytes);
         if constexpr (kPacked) {
-          tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], zkv, tok_k + j * kRows, pol_kv);
-          tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], zkv, tok_k + j * kRows, pol_kv);
+          const int tok = tok_k + (jb + j) * kRows;
+          tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], zkv, tok, pol_kv);
+          tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], zkv, tok, pol_kv);
         } else {
           tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], j * kRows, zkv, pol_kv);
           tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], j * kRows, zkv, pol_kv);
@@ -1437,6 +1530,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   tc_fence_after_sync();
   if (warp == 8) tmem_dealloc(tmem, C::kTmemCols);
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
+  if constexpr (kPacked) {
+    if (parts > 1 && !*sAbort)
+      join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, part_row(0, 0),
+                 reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 8));
+  }
 }
 
 namespace {

@@ -208,7 +208,7 @@ struct Tile {
   int pair;       // -1: a whole tile; 0 / 1: the first / second KV half of a
                   // split tail tile, run by cluster ranks 0 / 1
   // packed sequences only (zkv is then the K/V head): see PackedTile
-  int tok0, rows, k0, k_len, n_keys, diag;
+  int tok0, rows, k0, k_len, n_keys, diag, parts, part, slot;
 };
 
 // Index of the k-th tile of this CTA, or -1 when it has no k-th tile: round
@@ -297,20 +297,58 @@ __device__ __forceinline__ bool packed_tile(const PackedFwdParams& p, int n_tile
   const int item = (int)idx / p.H_kv;
   t.zkv = (int)idx - item * p.H_kv;
   const int4* src = reinterpret_cast<const int4*>(p.sh.tiles + item);
-  const int4 a = src[0], b = src[1];   // in PackedTile's order
+  const int4 a = src[0], b = src[1], c4 = src[2];   // in PackedTile's order
   t.tok0 = a.x;
   t.rows = a.y;
   t.k0 = a.z;
   t.k_len = a.w;
   t.n_keys = b.x;
   t.diag = b.y;
-  t.jb = 0;
-  t.n_blocks = (t.n_keys + kBlockN - 1) / kBlockN;
+  t.jb = b.w;
+  t.n_blocks = c4.x;
+  t.parts = c4.y;
+  t.part = c4.z;
+  t.slot = c4.w;
   t.has_sub1 = t.rows > p.sh.positions;
   t.m0 = 0;
   t.split = 0;
   t.pair = -1;
   return true;
+}
+
+// A packed tile's rows from its parts (fp32 O, normalised, and base-2 log-sum-exps): O =
+// sum_i w_i O_i, w_i = 2^(L_i - L).  The whole block: eight elements of a row a thread.
+template <int D>
+__device__ __forceinline__ void join_parts(const PackedFwdParams& p, const Tile& tl) {
+  const int group = p.sh.group;
+  const int rows0 = min(tl.rows, p.sh.positions) * group;   // of sub-tile 0
+  const int rows = tl.rows * group;                         // of both
+  const size_t step = (size_t)p.H_kv * 256;                 // rows from part to part
+#pragma unroll 1
+  for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
+    const int n = i / (D / 8), c = i % (D / 8);
+    const int r = n < rows0 ? n : n - rows0;                // row of the sub-tile
+    const int at = (r * p.sh.inv_group) >> 16;
+    const int head = tl.zkv * group + (r - at * group);
+    const long long tok = tl.tok0 + (n < rows0 ? 0 : p.sh.positions) + at;
+    const size_t row =
+        ((size_t)tl.slot * p.H_kv + tl.zkv) * 256 + (n < rows0 ? 0 : kBlockM) + r;
+    const float* lse = p.sh.tile_lse + row;
+    float most = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < tl.parts; ++k) most = fmaxf(most, __ldcg(lse + k * step));
+    const float sub = most == -INFINITY ? 0.f : most;       // (no key in any part: weights 0)
+    float o[8];
+    sum_parts(o, p.sh.tile_parts + row * D + c * 8, step * D, tl.parts, [&](int k) {
+      const float w = ex2_approx(__ldcg(lse + k * step) - sub);
+      sum += w;
+      return w;
+    });
+    store_bf16x8(static_cast<uint16_t*>(p.o) + tok * p.o_st + head * p.o_sh + c * 8, o,
+                 sum == 0.f ? 0.f : 1.f / sum);
+    if (c == 0)
+      p.lse[(long long)head * p.sh.T_q + tok] = (most + log2f(sum)) * 0.69314718055994530942f;
+  }
 }
 
 template <bool kPacked>
@@ -706,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k_next = k + 1;
       Tile nxt;
       const bool have_next = next_work(k_next, nxt);
+      const bool next_sub1 = have_next && nxt.has_sub1;
       // Split tail tile (the CTA's last): the two KV halves exchange
       // partial results.  With two sub-tiles each CTA writes one (the first
       // CTA sub-tile 0, the second sub-tile 1) and sends the other one's
@@ -874,7 +913,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               lse_out = (mx + log2f(e0 + e1)) * 0.69314718055994530942f;
             }
           }
-          if constexpr (kPacked) {
+          if (kPacked && cur.parts > 1) {
+            // a part of the tile's keys: normalised fp32 O and base-2 log-sum-exp
+            if constexpr (kPacked) {
+              const size_t row =
+                  ((size_t)(cur.slot + cur.part) * p.H_kv + cur.zkv) * 256 + t * kBlockM + r;
+              float4* dst = reinterpret_cast<float4*>(p.sh.tile_parts + row * D);
+              p.sh.tile_lse[row] = empty ? -INFINITY : m + log2f(l);
+#pragma unroll 1
+              for (int ch = 0; ch < D / 16; ++ch) {
+                uint32_t o[16];
+                tmem_ld_x16(tO + ch * 16, o);
+                tmem_ld_wait();
+                reg_after_wait(o);
+#pragma unroll
+                for (int qd = 0; qd < 4; ++qd)
+                  dst[ch * 4 + qd] =
+                      make_float4(u2f(o[qd * 4 + 0]) * inv_l, u2f(o[qd * 4 + 1]) * inv_l,
+                                  u2f(o[qd * 4 + 2]) * inv_l, u2f(o[qd * 4 + 3]) * inv_l);
+              }
+              __threadfence();
+            }
+          } else if constexpr (kPacked) {
             // bf16 O through shared memory: per 64-column slab, each warp
             // writes its 32 rows into its own staging slab (16-byte piece c of row
             // r at piece c ^ (r % 8)) and takes them out again four rows at a
@@ -1028,13 +1088,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // O_t has been read out and the row statistics are consumed: block 0
         // of the next tile may start on sub-tile t
-        if (have_next && (t == 0 || nxt.has_sub1)) mbar_arrive(&p_full[t]);
+        if (have_next && (t == 0 || next_sub1)) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
       stamp(tr, kEvEnd, 0);
       k = k_next;
-      cur = nxt;
       have = have_next;
+      // (packed: read again, which takes fewer registers than keeping it)
+      if constexpr (kPacked)
+        have = have && tile_at(k, cur);
+      else
+        cur = nxt;
     }
   } else {
     // ------------------------------------------------------------ warpgroup 3
@@ -1108,8 +1172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vslot = (2 * st + C::kSlots - 1) % C::kSlots;
           if constexpr (kPacked) {
             // rows of V behind the sequence's end
-            if (!more && tl.k_len < n * kBlockN)
-              clear_rows<D>(sKV + vslot * C::kTileBytes, tl.k_len - j * kBlockN);
+            const int left = tl.k_len - (tl.jb + j) * kBlockN;
+            if (!more && left < kBlockN) clear_rows<D>(sKV + vslot * C::kTileBytes, left);
           }
           uint64_t dv = dv0 + (uint64_t)vslot * kSlotDesc;
           if constexpr (C::kSumCol) {
@@ -1273,6 +1337,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   // memory (every role of both reaches this point, all waits being bounded)
   if (kTail) cluster_sync_all();
   if (warp == 12) tmem_dealloc(tmem, C::kTmemCols);
+  if constexpr (kPacked) {
+    // The last of a tile's parts joins them, the whole block at once (with the registers
+    // that it was launched with), when it has done all its tiles.
+    if (p.sh.head->cut && !*sAbort) {
+      if (wg < 2)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(65536 / kThreads) : "memory");
+      else
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(65536 / kThreads) : "memory");
+      Tile tl;
+      for (int k = 0; tile_at(k, tl); ++k) {
+        if (tl.parts > 1 &&
+            last_of_parts(p.sh.tile_counters + (size_t)tl.slot * p.H_kv + tl.zkv, tl.parts,
+                          reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8)))
+          join_parts<D>(p, tl);
+      }
+    }
+  }
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_attn_status, 0, (int)ATTN_ERR_TIMEOUT);
   if constexpr (kTrace) {
     if (trace_cta) {

@@ -225,9 +225,12 @@ cudaError_t read_paged_status(int* status, bool reset);
 // A tile's 128 rows are `positions` consecutive tokens of one sequence times the
 // group's R = H_q / H_kv query heads (row = token * R + head, so that a tile needs
 // only one K/V head and few keys past its diagonal); rows behind positions * R are
-// spare.  A plan kernel lists the work of all sequences, the costliest first.
+// spare.  A plan kernel lists the work of all sequences, the costliest first, and
+// cuts what takes far longer than its share of the GPU into parts, which are joined by
+// whichever comes last.
 
-// A forward tile: up to 2 x `positions` tokens of a sequence.
+// A tile: up to 2 x `positions` tokens of a sequence, against all keys that they see or
+// a part of them.
 struct __align__(16) PackedTile {
   int tok0;    // first query token
   int rows;    // tokens of the tile, 1 .. 2 positions
@@ -236,10 +239,15 @@ struct __align__(16) PackedTile {
   int n_keys;  // keys that the tile's last token sees
   int diag;    // causal: keys that the tile's first token sees (may be <= 0)
   int vec0;    // where the tile's tokens lie in the backward's row vectors
-  int unused;
+  int jb;      // first of the part's blocks of 128 keys
+  int n_blocks;
+  int parts;   // of the tile (1: not cut), this one's number, and the first one's slot
+  int part;
+  int slot;
 };
 
-// A block of up to 128 keys of a sequence, with the query tiles that see it.
+// A block of up to 128 keys of a sequence, with the query tiles that see it or a part
+// of them.
 struct __align__(16) PackedKeys {
   int k0;      // first key token
   int keys;    // 1 .. 128
@@ -247,15 +255,19 @@ struct __align__(16) PackedKeys {
   int q_len;
   int vec0;    // where the sequence's queries lie in the row vectors
   int shift;   // causal: key r of the block is seen by queries at r + shift and behind
-  int first;   // the tile (of `positions` queries) that the block begins with: causal, the first
-               // that sees a key of it
-  int n_work;  // tiles from there on (not causal: all, the last followed by the first)
+  int first;   // the tile (of `positions` queries) that the part begins with
+  int n_work;  // tiles from there on (the sequence's last is followed by its first)
+  int tiles;   // of the sequence
+  int parts;   // as in PackedTile
+  int part;
+  int slot;
 };
 
 struct PackedHeader {
   int tiles, key_blocks;              // entries of the two lists
   int q_first, q_end;                 // tokens that belong to a sequence
-  int unused[60];
+  int cut;                            // whether any tile was cut
+  int unused[59];
 };
 
 struct PackedPlan {
@@ -263,19 +275,32 @@ struct PackedPlan {
   const int* cu_k;     // == cu_q where they are the same
   int B, T_q, T_k;
   int positions;       // query tokens of a 128-row tile
-  int causal;
+  int causal, H_kv;
   PackedHeader* head;  // workspace, from here on
   int* seq_q;          // [B + 1], cu_q in order
   int* seq_k;          // [B + 1] (== seq_q where they are the same)
-  PackedTile* tiles;   // room for tile_room(...) of them
+  PackedTile* tiles;   // nullptr: not listed
   PackedKeys* keys;    // nullptr: not listed
+  int* counters[2];    // of the tiles' and the key blocks' parts, to be cleared
+  int n_counters;      // of each
 };
 
+// Parts: an entry of n blocks (of keys, or of query tiles) is cut where n is one and a
+// half times `cap` or more, into round(n / cap) parts, with cap the blocks of all entries
+// and K/V heads divided by kPackedCtas, or kPackedLeastPart where that is more.  So there
+// are at most n / cap + 1/2 <= 4/3 n / cap parts of an entry, and 4/3 kPackedCtas of all.
+constexpr int kPackedCtas = 152;
+constexpr int kPackedLeastPart = 6;
+inline int packed_slots(int H_kv) { return 4 * kPackedCtas / (3 * H_kv); }
+constexpr int kPackedCounters = 2;    // of an entry's parts and a K/V head: one a half of a tile
+
 // Entries of the lists, at most.
-inline long long packed_tile_room(int T_q, int B, int positions) {
-  return (long long)T_q / (2 * positions) + B;
+inline long long packed_tile_room(int T_q, int B, int positions, int H_kv) {
+  return (long long)T_q / (2 * positions) + B + packed_slots(H_kv);
 }
-inline long long packed_key_room(int T_k, int B) { return (long long)T_k / 128 + B; }
+inline long long packed_key_room(int T_k, int B, int H_kv) {
+  return (long long)T_k / 128 + B + packed_slots(H_kv);
+}
 
 // First token of sequence b in the row vectors: a multiple of 4 (so that a tile's
 // part is 16-byte aligned), with room for every sequence before it.
@@ -293,6 +318,13 @@ struct PackedShape {
   int positions;       // query tokens of a 128-row tile
   int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
   int T_q;
+  // parts' results, by slot and K/V head: of tiles [256 rows, D] and, in the forward,
+  // their base-2 log-sum-exps [256]; of key blocks dV and dK, [2, 128 rows, D]
+  float* tile_parts;
+  float* tile_lse;
+  float* key_parts;
+  int* tile_counters;  // [slot, K/V head] (in the backward, of each half) parts that are done
+  int* key_counters;
 };
 
 struct PackedFwdParams : AttnParams {

@@ -52,8 +52,8 @@ attn_status_t check_sizes(const attn_packed_t* s) {
   if (positions == 0 || s->B > 65535) return ATTN_ERR_UNSUPPORTED;
   // tokens and what is counted of them stay within ints
   if (s->T_q >= (1 << 30) || s->T_k >= (1 << 30)) return ATTN_ERR_UNSUPPORTED;
-  if (packed_tile_room(s->T_q, s->B, positions) * 2 * s->H_kv >= INT_MAX ||
-      packed_key_room(s->T_k, s->B) * s->H_kv >= INT_MAX)
+  if (packed_tile_room(s->T_q, s->B, positions, s->H_kv) * 2 * s->H_kv >= INT_MAX ||
+      packed_key_room(s->T_k, s->B, s->H_kv) * s->H_kv >= INT_MAX)
     return ATTN_ERR_UNSUPPORTED;
   // thread blocks of the backward's row kernels (16 rows each, at least)
   if ((int64_t)s->T_q * s->H_q / 16 >= INT_MAX) return ATTN_ERR_UNSUPPORTED;
@@ -62,8 +62,10 @@ attn_status_t check_sizes(const attn_packed_t* s) {
 
 // Where the parts of the workspace begin.
 struct Layout {
-  size_t seq_q, seq_k, tiles, keys, nlse, ndelta, dq_acc, end;
+  size_t seq_q, seq_k, tiles, keys, tile_parts, tile_lse, key_parts, tile_counters, key_counters;
+  size_t nlse, ndelta, dq_acc, end;
   int64_t vec_stride;
+  int slots;   // of a K/V head's parts, of each list
 };
 
 Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
@@ -77,9 +79,24 @@ Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
   };
   l.seq_q = part((size_t)(s.B + 1) * sizeof(int));
   l.seq_k = part((size_t)(s.B + 1) * sizeof(int));
-  l.tiles = part((size_t)packed_tile_room(s.T_q, s.B, positions) * sizeof(PackedTile));
+  // Slots for parts, if any entry can be cut: one of kPackedLeastPart blocks and a half.
+  const auto cut = [](int64_t blocks) { return 2 * blocks >= 3 * kPackedLeastPart; };
+  const int64_t key_blocks = ((int64_t)s.T_k + 127) / 128;
+  const int64_t query_tiles = ((int64_t)s.T_q + positions - 1) / positions;
+  l.slots = packed_slots(s.H_kv);
+  const size_t heads = (size_t)l.slots * s.H_kv, counters = heads * kPackedCounters * sizeof(int);
+  if (!backward || deterministic) {
+    l.tiles = part((size_t)packed_tile_room(s.T_q, s.B, positions, s.H_kv) * sizeof(PackedTile));
+    l.tile_counters = part(counters);
+    if (cut(key_blocks)) {
+      l.tile_parts = part(heads * 256 * s.D * sizeof(float));
+      if (!backward) l.tile_lse = part(heads * 256 * sizeof(float));
+    }
+  }
   if (backward) {
-    l.keys = part((size_t)packed_key_room(s.T_k, s.B) * sizeof(PackedKeys));
+    l.keys = part((size_t)packed_key_room(s.T_k, s.B, s.H_kv) * sizeof(PackedKeys));
+    l.key_counters = part(counters);
+    if (cut(query_tiles)) l.key_parts = part(heads * 2 * 128 * s.D * sizeof(float));
     // every sequence's rows from packed_vec0 on, and what a copy of 128 reads past them
     l.vec_stride = (((int64_t)s.T_q + 4ll * s.B + 4) * group + 128 + 3) & ~3ll;
     l.nlse = part((size_t)s.H_kv * l.vec_stride * sizeof(float));
@@ -92,8 +109,7 @@ Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
 
 // The sequences' bounds and the workspace, and the plan over them.
 attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k, void* workspace,
-                        size_t bytes, const Layout& l, bool backward, PackedPlan* plan,
-                        PackedShape* shape) {
+                        size_t bytes, const Layout& l, PackedPlan* plan, PackedShape* shape) {
   if (!cu_q || !workspace || bytes < l.end) return ATTN_ERR_INVALID_ARG;
   if (!cu_k && s.T_k != s.T_q) return ATTN_ERR_INVALID_ARG;
   if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(workspace, 256))
@@ -110,8 +126,19 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   plan->head = reinterpret_cast<PackedHeader*>(ws);
   plan->seq_q = reinterpret_cast<int*>(ws + l.seq_q);
   plan->seq_k = cu_k ? reinterpret_cast<int*>(ws + l.seq_k) : plan->seq_q;
-  plan->tiles = reinterpret_cast<PackedTile*>(ws + l.tiles);
-  plan->keys = backward ? reinterpret_cast<PackedKeys*>(ws + l.keys) : nullptr;
+  plan->H_kv = s.H_kv;
+  // (a part that the layout does not have begins at 0, where the header is)
+  const auto at = [&](size_t offset) { return offset ? ws + offset : nullptr; };
+  plan->tiles = reinterpret_cast<PackedTile*>(at(l.tiles));
+  plan->keys = reinterpret_cast<PackedKeys*>(at(l.keys));
+  plan->counters[0] = reinterpret_cast<int*>(at(l.tile_counters));
+  plan->counters[1] = reinterpret_cast<int*>(at(l.key_counters));
+  plan->n_counters = l.slots * s.H_kv * kPackedCounters;
+  shape->tile_parts = reinterpret_cast<float*>(at(l.tile_parts));
+  shape->tile_lse = reinterpret_cast<float*>(at(l.tile_lse));
+  shape->key_parts = reinterpret_cast<float*>(at(l.key_parts));
+  shape->tile_counters = plan->counters[0];
+  shape->key_counters = plan->counters[1];
   shape->head = plan->head;
   shape->tiles = plan->tiles;
   shape->keys = plan->keys;
@@ -165,7 +192,7 @@ attn_status_t attn_fwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
   PackedFwdParams p;
   std::memset(static_cast<void*>(&p), 0, sizeof(p));
   const Layout l = layout_of(*s, false, false);
-  if ((st = take_plan(*s, cu_q, cu_k, workspace, workspace_bytes, l, false, &plan, &p.sh)) != ATTN_OK)
+  if ((st = take_plan(*s, cu_q, cu_k, workspace, workspace_bytes, l, &plan, &p.sh)) != ATTN_OK)
     return st;
   if ((st = check_device()) != ATTN_OK) return st;
   if (!map_rows(&p.tm_q, tq, *s, p.sh) || !map_keys(&p.tm_k, tk, *s) || !map_keys(&p.tm_v, tv, *s))
@@ -183,7 +210,7 @@ attn_status_t attn_fwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
   p.scale_log2 = scale_log2_of(std::fabs(s->scale));
   p.timeout_ns = kDefaultTimeoutNs;
   p.fault_drop_block = -1;
-  p.num_tiles = (int)(packed_tile_room(s->T_q, s->B, p.sh.positions) * s->H_kv);
+  p.num_tiles = (int)(packed_tile_room(s->T_q, s->B, p.sh.positions, s->H_kv) * s->H_kv);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_packed_plan(plan, cs);
   return done(e != cudaSuccess ? e : launch_attn_fwd_packed(p, s->D, cs));
@@ -214,7 +241,7 @@ attn_status_t attn_bwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
   PackedBwdParams p;
   std::memset(static_cast<void*>(&p), 0, sizeof(p));
   const Layout l = layout_of(*s, true, deterministic != 0);
-  if ((st = take_plan(*s, cu_q, cu_k, workspace, workspace_bytes, l, true, &plan, &p.sh)) != ATTN_OK)
+  if ((st = take_plan(*s, cu_q, cu_k, workspace, workspace_bytes, l, &plan, &p.sh)) != ATTN_OK)
     return st;
   if ((st = check_device()) != ATTN_OK) return st;
   if (!map_rows(&p.tm_q, tq, *s, p.sh) || !map_rows(&p.tm_do, tdo, *s, p.sh) ||
@@ -247,8 +274,8 @@ attn_status_t attn_bwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
   return done(e != cudaSuccess
                   ? e
                   : launch_attn_bwd_packed(p, s->D, to.data, tdo.data, lse,
-                                           (int)packed_tile_room(s->T_q, s->B, p.sh.positions),
-                                           (int)packed_key_room(s->T_k, s->B), cs));
+                                           (int)packed_tile_room(s->T_q, s->B, p.sh.positions, s->H_kv),
+                                           (int)packed_key_room(s->T_k, s->B, s->H_kv), cs));
 }
 
 attn_status_t attn_rope_packed(const attn_thd_t* q, const attn_thd_t* q_out, const attn_thd_t* k,

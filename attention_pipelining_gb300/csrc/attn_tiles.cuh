@@ -51,6 +51,56 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
   __syncwarp();
 }
 
+// Parts of one piece of work, done by different thread blocks, each of which has written its
+// share to global memory, every thread's writes followed by a __threadfence(): true in the
+// block that came last, for which all of them are visible (by loads that do not go
+// through L1).  Whole block; `flag` is in shared memory.
+__device__ __forceinline__ bool last_of_parts(int* counter, int parts, volatile int* flag) {
+  __syncthreads();   // (the writes are done, and the flag's last use)
+  if (threadIdx.x == 0) {
+    __threadfence();
+    *flag = atomicAdd(counter, 1) == parts - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  return *flag != 0;
+}
+
+// sum[0 .. 8) = the sum over the parts of weight(i) * 8 floats at `src` + i * `step`, always
+// in the same order.
+template <typename Weight>
+__device__ __forceinline__ void sum_parts(float (&sum)[8], const float* src, size_t step, int parts,
+                                          Weight&& weight) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < parts; i0 += 4) {
+    float4 x[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // (past the last part: the last again, not added)
+      const float4* s4 = reinterpret_cast<const float4*>(src + (size_t)min(i0 + i, parts - 1) * step);
+      x[i][0] = __ldcg(s4);
+      x[i][1] = __ldcg(s4 + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= parts) break;
+      const float w = weight(i0 + i);
+      sum[0] = fmaf(w, x[i][0].x, sum[0]), sum[1] = fmaf(w, x[i][0].y, sum[1]);
+      sum[2] = fmaf(w, x[i][0].z, sum[2]), sum[3] = fmaf(w, x[i][0].w, sum[3]);
+      sum[4] = fmaf(w, x[i][1].x, sum[4]), sum[5] = fmaf(w, x[i][1].y, sum[5]);
+      sum[6] = fmaf(w, x[i][1].z, sum[6]), sum[7] = fmaf(w, x[i][1].w, sum[7]);
+    }
+  }
+}
+
+// Eight floats times `mult` as bf16, 16 bytes.
+__device__ __forceinline__ void store_bf16x8(uint16_t* dst, const float (&x)[8], float mult) {
+  *reinterpret_cast<uint4*>(dst) =
+      make_uint4(pack_bf16x2(x[0] * mult, x[1] * mult), pack_bf16x2(x[2] * mult, x[3] * mult),
+                 pack_bf16x2(x[4] * mult, x[5] * mult), pack_bf16x2(x[6] * mult, x[7] * mult));
+}
+
 // Shared-memory descriptor of the start of a tile, for either operand use.
 // The GEMM helpers below add constant offsets to its start-address field
 // (bits 0-13, address >> 4), which never carries: shared addresses stay

@@ -69,16 +69,22 @@ __device__ bool put_in_order(const int* cu, int n, int T, int* out, int* warps) 
   return bad;
 }
 
-// One thread block lists the tiles (and the key blocks) of all sequences, by a
+// Into how many parts an entry of n blocks is cut (see kPackedCtas).
+__device__ __forceinline__ int parts_of(int n, int cap) {
+  return 2 * n >= 3 * cap ? (n + cap / 2) / cap : 1;
+}
+
+// One thread block lists the tiles and the key blocks of all sequences, by a
 // counting sort over their costs in blocks (of 128 keys, or of query tiles), so that
 // the costliest run first and the last to end are short.  The order among equal costs
-// differs from run to run; no result depends on it.
+// and the parts' slots differ from run to run; no result depends on them.
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
   __shared__ int at[2][kBuckets];   // entries of a cost, then where the next of them goes
-  __shared__ int warps[32], most[2];
+  __shared__ int warps[32], most[2], slots[2];
+  __shared__ unsigned long long total[2];   // blocks of all entries
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   at[0][threadIdx.x] = at[1][threadIdx.x] = 0;
-  if (threadIdx.x < 2) most[threadIdx.x] = 0;
+  if (threadIdx.x < 2) most[threadIdx.x] = slots[threadIdx.x] = 0, total[threadIdx.x] = 0;
   allow_later();
   wait_for_earlier();
   bool bad = put_in_order(p.cu_q, p.B + 1, p.T_q, p.seq_q, warps);
@@ -92,19 +98,17 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     if (m > 0) atomicMax(&most[1], ceil_div(n, P));
   }
   __syncthreads();
-  int shift[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    shift[i] = 0;
-    while ((most[i] >> shift[i]) >= kBuckets) ++shift[i];
-  }
-  // every tile (list 0) and key block (list 1), each with its cost
+  for (int i = 0; i < 2; ++i)
+    for (int c = threadIdx.x; c < p.n_counters; c += kPlanThreads)
+      if (p.counters[i] != nullptr) p.counters[i][c] = 0;
+  // every tile (list 0) and key block (list 1), whole, each with its cost
   const auto each = [&](auto&& put) {
     for (int b = warp; b < p.B; b += kPlanThreads / 32) {
       const int q0 = p.seq_q[b], n = p.seq_q[b + 1] - q0;
       const int k0 = p.seq_k[b], m = p.seq_k[b + 1] - k0;
       const int vec0 = packed_vec0(q0, b);
-      for (int t = lane; t < ceil_div(n, 2 * P); t += 32) {
+      for (int t = lane; p.tiles != nullptr && t < ceil_div(n, 2 * P); t += 32) {
         PackedTile x;
         const int pos = t * 2 * P;
         x.tok0 = q0 + pos;
@@ -114,7 +118,6 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
         x.diag = m - n + pos + 1;
         x.n_keys = p.causal ? min(max(x.diag + x.rows - 1, 0), m) : m;
         x.vec0 = vec0 + pos;
-        x.unused = 0;
         put(0, ceil_div(x.n_keys, 128), &x, (PackedKeys*)nullptr);
       }
       if (p.keys == nullptr) continue;
@@ -131,12 +134,45 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
         // add to different rows of dQ)
         x.first = p.causal ? min(max(x.shift, 0) / P, tiles) : tiles > 0 ? t % tiles : 0;
         x.n_work = p.causal ? tiles - x.first : tiles;
+        x.tiles = tiles;
         put(1, x.n_work, (PackedTile*)nullptr, &x);
       }
     }
   };
-  each([&](int list, int cost, const PackedTile*, const PackedKeys*) {
-    atomicAdd(&at[list][kBuckets - 1 - min(cost >> shift[list], kBuckets - 1)], 1);
+  int shift[2], cap[2];
+  const bool may_cut = 2 * max(most[0], most[1]) >= 3 * kPackedLeastPart;
+  if (may_cut) {
+    unsigned long long mine[2] = {0, 0};
+    each([&](int list, int cost, PackedTile*, PackedKeys*) { mine[list] += cost; });
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mine[i] += __shfl_xor_sync(0xffffffffu, mine[i], off);
+      if (lane == 0 && mine[i] > 0) atomicAdd(&total[i], mine[i]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const unsigned long long share = (total[i] * p.H_kv + kPackedCtas - 1) / kPackedCtas;
+    cap[i] = may_cut ? (int)min(max(share, (unsigned long long)kPackedLeastPart), 1ull << 29) : 1 << 29;
+    shift[i] = 0;
+    while ((most[i] >> shift[i]) >= kBuckets) ++shift[i];
+  }
+  const auto bucket = [&](int list, int cost) {
+    return &at[list][kBuckets - 1 - min(cost >> shift[list], kBuckets - 1)];
+  };
+  // an entry of n blocks has `parts` parts of `size` blocks, but for the last
+  const auto cut = [&](int list, int n, int& parts, int& size) {
+    parts = parts_of(n, cap[list]);
+    size = ceil_div(n, parts);
+    parts = n > 0 ? ceil_div(n, size) : 1;
+  };
+  each([&](int list, int cost, PackedTile*, PackedKeys*) {
+    int parts, size;
+    cut(list, cost, parts, size);
+    if (parts > 1) atomicAdd(bucket(list, size), parts - 1);
+    atomicAdd(bucket(list, cost - (parts - 1) * size), 1);
   });
   __syncthreads();
   const auto sum = [](int a, int b) { return a + b; };
@@ -153,12 +189,28 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   if (threadIdx.x == 0) {
     p.head->q_first = p.seq_q[0];
     p.head->q_end = p.seq_q[p.B];
+    p.head->cut = 2 * most[0] >= 3 * cap[0];
   }
   __syncthreads();
-  each([&](int list, int cost, const PackedTile* tile, const PackedKeys* keys) {
-    const int i = atomicAdd(&at[list][kBuckets - 1 - min(cost >> shift[list], kBuckets - 1)], 1);
-    if (list == 0) p.tiles[i] = *tile;
-    if (list == 1) p.keys[i] = *keys;
+  each([&](int list, int cost, PackedTile* tile, PackedKeys* keys) {
+    int parts, size;
+    cut(list, cost, parts, size);
+    const int slot = parts > 1 ? atomicAdd(&slots[list], parts) : 0;
+    const int first = list == 1 ? keys->first : 0;
+    for (int part = 0; part < parts; ++part) {
+      const int n = part + 1 < parts ? size : cost - part * size;
+      const int i = atomicAdd(bucket(list, n), 1);
+      if (list == 0) {
+        tile->jb = part * size, tile->n_blocks = n;
+        tile->parts = parts, tile->part = part, tile->slot = slot;
+        p.tiles[i] = *tile;
+      } else {
+        const int t = first + part * size;
+        keys->first = t < keys->tiles ? t : t - keys->tiles, keys->n_work = n;
+        keys->parts = parts, keys->part = part, keys->slot = slot;
+        p.keys[i] = *keys;
+      }
+    }
   });
 }
 static_assert(kBuckets == kPlanThreads, "one thread to a bucket");
