@@ -841,12 +841,12 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         if (kPacked && parts > 1) {
           if constexpr (kPacked) {
             float4* f4 = reinterpret_cast<float4*>(
-                p.sh.key_parts +
-                ((((size_t)(slot + part) * p.H_kv + zkv) * 2 + which) * kRows + r) * D +
-                (D / 2) * w + ch * 32);
+                             p.sh.key_parts +
+                             (((size_t)(slot + part) * p.H_kv + zkv) * 2 + which) * kRows * D) +
+                         ((D / 8) * w + ch * 8) * kRows + r;
 #pragma unroll
             for (int qd = 0; qd < 8; ++qd)
-              f4[qd] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
+              f4[qd * kRows] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
                                    u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
           }
         } else if (row_ok && ok) {
@@ -863,7 +863,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         }
       }
     }
-    if (kPacked && parts > 1) __threadfence();
   } else if (warp == 8) {
     // -------------------------------------------------------- tensor-core issuer
     const bool leader = elect_one();
@@ -1111,23 +1110,29 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   if (warp == 8) tmem_dealloc(tmem, C::kTmemCols);
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
   if constexpr (kPacked) {
-    // the last of the block's parts adds them up, eight elements a thread
+    // the last of the block's parts adds them up
     const int4 of = of_parts();
     const int parts = of.y, slot = of.w;
     if (parts > 1 && !*sAbort &&
         last_of_parts(p.sh.key_counters + (size_t)slot * p.H_kv + zkv, parts,
                       reinterpret_cast<volatile int*>(smem + C::kOffMiscKV + 8))) {
-      const size_t step = (size_t)p.H_kv * 2 * kRows * D;
-      for (int i = threadIdx.x; i < 2 * n_keys * (D / 8); i += blockDim.x) {
-        const int which = i / (n_keys * (D / 8)), n = i - which * n_keys * (D / 8);
-        const int r = n / (D / 8), c = n % (D / 8);
-        float x[8];
-        sum_parts(x, p.sh.key_parts + ((((size_t)slot * p.H_kv + zkv) * 2 + which) * kRows + r) * D + c * 8,
-                  step, parts, [](int) { return 1.f; });
-        const long long tok = tok_k + r;
-        uint16_t* dst = which ? static_cast<uint16_t*>(p.dk) + tok * p.dk_st + zkv * p.dk_sh
-                              : static_cast<uint16_t*>(p.dv) + tok * p.dv_st + zkv * p.dv_sh;
-        store_bf16x8(dst + c * 8, x, which ? p.scale : 1.f);
+      const size_t step = (size_t)p.H_kv * 2 * kRows * (D / 4);
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {
+        const float4* first = reinterpret_cast<const float4*>(
+            p.sh.key_parts + (((size_t)slot * p.H_kv + zkv) * 2 + which) * kRows * D);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < ((n_keys + 7) & ~7) * (D / 8); i += blockDim.x) {
+          int r, c;
+          join_item<D>(i, r, c);
+          if (r >= n_keys) continue;
+          float x[8];
+          sum_parts(x, first + 2 * c * kRows + r, kRows, step, parts, [](int) { return 1.f; });
+          const long long tok = tok_k + r;
+          uint16_t* dst = which ? static_cast<uint16_t*>(p.dk) + tok * p.dk_st + zkv * p.dk_sh
+                                : static_cast<uint16_t*>(p.dv) + tok * p.dv_st + zkv * p.dv_sh;
+          store_bf16x8(dst + c * 8, x, which ? p.scale : 1.f);
+        }
       }
     }
   }
@@ -1135,17 +1140,22 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 
 // ---------------------------------------------------------------- dQ
 
-// The last of the parts of a packed tile's half adds up their dQ, eight elements a thread;
-// `first`: the rows in the first part.  Whole block.
+// The last of the parts of a packed tile's half adds up their dQ; `first`: the rows in the
+// first part.  Whole block.
 template <int D>
 __device__ __forceinline__ void join_dq(const PackedBwdParams& p, size_t slot, int half, int parts,
                                         int n_rows, int tok_q, int zkv, const float* first,
                                         volatile int* flag) {
   if (!last_of_parts(p.sh.tile_counters + slot * 2 + half, parts, flag)) return;
-  for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreadsB) {
-    const int r = i / (D / 8), c = i % (D / 8), at = (r * p.sh.inv_group) >> 16;
+  const float4* f4 = reinterpret_cast<const float4*>(first);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < ((n_rows + 7) & ~7) * (D / 8); i += kThreadsB) {
+    int r, c;
+    join_item<D>(i, r, c);
+    if (r >= n_rows) continue;
+    const int at = (r * p.sh.inv_group) >> 16;
     float x[8];
-    sum_parts(x, first + (size_t)r * D + c * 8, (size_t)p.H_kv * 256 * D, parts,
+    sum_parts(x, f4 + 2 * c * kRows + r, kRows, (size_t)p.H_kv * 256 * (D / 4), parts,
               [](int) { return 1.f; });
     store_bf16x8(static_cast<uint16_t*>(p.dq) + (long long)(tok_q + at) * p.dq_st +
                      (zkv * p.sh.group + r - at * p.sh.group) * p.dq_sh + c * 8,
@@ -1185,10 +1195,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   int tok_q = 0, tok_k = 0, k_len = 0, n_keys = 0, diag = 0, vec0 = 0;   // and PackedTile's others
   int jb = 0, parts = 1, half = 0;
   size_t slot = 0;   // of the tile's first part and this K/V head
-  // the rows' dQ in a part (of a tile's halves 128 rows each)
-  auto part_row = [&](int part, int row) -> float* {
+  // a part's dQ (of a tile's halves 128 rows each)
+  auto dq_of = [&](int part) -> float* {
     if constexpr (kPacked)
-      return p.sh.tile_parts + ((slot + (size_t)part * p.H_kv) * 256 + half * kRows + row) * D;
+      return p.sh.tile_parts + ((slot + (size_t)part * p.H_kv) * 256 + half * kRows) * D;
     return nullptr;
   };
   int part = 0;
@@ -1219,9 +1229,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     if (n_kb <= 0) {   // no row sees a key of these: dQ = 0
       if (parts > 1) {
         for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreadsB)
-          reinterpret_cast<float4*>(part_row(part, 0))[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        __threadfence();
-        join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, part_row(0, 0),
+          reinterpret_cast<float4*>(dq_of(part))[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, dq_of(0),
                    reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 8));
         return;
       }
@@ -1392,10 +1401,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld_wait();
         reg_after_wait(v);
         if (kPacked && parts > 1) {
-          float4* f4 = reinterpret_cast<float4*>(part_row(part, r) + (D / 2) * w + ch * 32);
+          float4* f4 =
+              reinterpret_cast<float4*>(dq_of(part)) + ((D / 8) * w + ch * 8) * kRows + r;
 #pragma unroll
           for (int qd = 0; qd < 8; ++qd)
-            f4[qd] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
+            f4[qd * kRows] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
                                  u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
         } else if (row_ok) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
@@ -1411,8 +1421,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           }
         }
       }
-      if (kPacked && parts > 1) __threadfence();
-    }
+      }
   } else if (warp == 8) {
     // -------------------------------------------------------- tensor-core issuer
     const bool leader = elect_one();
@@ -1532,7 +1541,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
   if constexpr (kPacked) {
     if (parts > 1 && !*sAbort)
-      join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, part_row(0, 0),
+      join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, dq_of(0),
                  reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 8));
   }
 }

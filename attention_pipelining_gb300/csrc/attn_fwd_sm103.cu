@@ -152,6 +152,8 @@ struct Cfg {
   static constexpr uint32_t kSplitIn = (uint32_t)kBlockM * D * 4;
   static_assert(2 * kSplitIn <= (uint32_t)(kSlots * kTileBytes), "split-tail partials in the ring");
   static_assert(2 * kBlockM * 4 <= 2 * kTileBytes, "split-tail log-sum-exps in the Q buffer");
+  // packed sequences: the weights of a tile's parts in the idle ring
+  static_assert(kPackedMostParts * 256 * 4 <= kSlots * kTileBytes, "weights in the ring");
   // Row sums on the tensor core (D = 64, where tensor memory has room): the
   // PV GEMM runs with N = D + 16 against [V | ones], so columns D .. D + 15
   // of O_t accumulate the sum of the bf16 probabilities the GEMM consumed,
@@ -317,37 +319,52 @@ __device__ __forceinline__ bool packed_tile(const PackedFwdParams& p, int n_tile
 }
 
 // A packed tile's rows from its parts (fp32 O, normalised, and base-2 log-sum-exps): O =
-// sum_i w_i O_i, w_i = 2^(L_i - L).  The whole block: eight elements of a row a thread.
+// sum_i w_i O_i, w_i = 2^(L_i - L).  Whole block; `weights`: shared memory, [parts, 256].
 template <int D>
-__device__ __forceinline__ void join_parts(const PackedFwdParams& p, const Tile& tl) {
-  const int group = p.sh.group;
-  const int rows0 = min(tl.rows, p.sh.positions) * group;   // of sub-tile 0
-  const int rows = tl.rows * group;                         // of both
+__device__ __forceinline__ void join_parts(const PackedFwdParams& p, const Tile& tl,
+                                           float* weights) {
+  const int group = p.sh.group, positions = p.sh.positions;
+  const size_t first = (size_t)tl.slot * p.H_kv + tl.zkv;   // of the parts and heads
   const size_t step = (size_t)p.H_kv * 256;                 // rows from part to part
-#pragma unroll 1
-  for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
-    const int n = i / (D / 8), c = i % (D / 8);
-    const int r = n < rows0 ? n : n - rows0;                // row of the sub-tile
-    const int at = (r * p.sh.inv_group) >> 16;
-    const int head = tl.zkv * group + (r - at * group);
-    const long long tok = tl.tok0 + (n < rows0 ? 0 : p.sh.positions) + at;
-    const size_t row =
-        ((size_t)tl.slot * p.H_kv + tl.zkv) * 256 + (n < rows0 ? 0 : kBlockM) + r;
-    const float* lse = p.sh.tile_lse + row;
+  for (int n = threadIdx.x; n < 256; n += kThreads) {
+    const int t = n >> 7, r = n & 127, at = (r * p.sh.inv_group) >> 16;
+    if (at >= positions || t * positions + at >= tl.rows) continue;
+    const float* lse = p.sh.tile_lse + first * 256 + n;
     float most = -INFINITY, sum = 0.f;
 #pragma unroll 4
-    for (int k = 0; k < tl.parts; ++k) most = fmaxf(most, __ldcg(lse + k * step));
+    for (int k = 0; k < tl.parts; ++k) {
+      const float x = __ldcg(lse + k * step);
+      weights[k * 256 + n] = x;
+      most = fmaxf(most, x);
+    }
     const float sub = most == -INFINITY ? 0.f : most;       // (no key in any part: weights 0)
-    float o[8];
-    sum_parts(o, p.sh.tile_parts + row * D + c * 8, step * D, tl.parts, [&](int k) {
-      const float w = ex2_approx(__ldcg(lse + k * step) - sub);
-      sum += w;
-      return w;
-    });
-    store_bf16x8(static_cast<uint16_t*>(p.o) + tok * p.o_st + head * p.o_sh + c * 8, o,
-                 sum == 0.f ? 0.f : 1.f / sum);
-    if (c == 0)
-      p.lse[(long long)head * p.sh.T_q + tok] = (most + log2f(sum)) * 0.69314718055994530942f;
+    for (int k = 0; k < tl.parts; ++k) sum += ex2_approx(weights[k * 256 + n] - sub);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int k = 0; k < tl.parts; ++k)
+      weights[k * 256 + n] = ex2_approx(weights[k * 256 + n] - sub) * inv;
+    p.lse[(long long)(tl.zkv * group + r - at * group) * p.sh.T_q + tl.tok0 + t * positions + at] =
+        (most + log2f(sum)) * 0.69314718055994530942f;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int t = 0; t < 2; ++t) {
+    const int rows = min(tl.rows - t * positions, positions) * group;
+    const float4* src =
+        reinterpret_cast<const float4*>(p.sh.tile_parts + first * 256 * D) + t * kBlockM;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < ((rows + 7) & ~7) * (D / 8); i += kThreads) {
+      int r, c;
+      join_item<D>(i, r, c);
+      if (r >= rows) continue;
+      const int at = (r * p.sh.inv_group) >> 16;
+      float o[8];
+      sum_parts(o, src + 2 * c * 256 + r, 256, step * (D / 4), tl.parts,
+                [&](int k) { return weights[k * 256 + t * kBlockM + r]; });
+      store_bf16x8(static_cast<uint16_t*>(p.o) +
+                       (long long)(tl.tok0 + t * positions + at) * p.o_st +
+                       (tl.zkv * group + r - at * group) * p.o_sh + c * 8,
+                   o, 1.f);
+    }
   }
 }
 
@@ -916,10 +933,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kPacked && cur.parts > 1) {
             // a part of the tile's keys: normalised fp32 O and base-2 log-sum-exp
             if constexpr (kPacked) {
-              const size_t row =
-                  ((size_t)(cur.slot + cur.part) * p.H_kv + cur.zkv) * 256 + t * kBlockM + r;
-              float4* dst = reinterpret_cast<float4*>(p.sh.tile_parts + row * D);
-              p.sh.tile_lse[row] = empty ? -INFINITY : m + log2f(l);
+              const size_t first = ((size_t)(cur.slot + cur.part) * p.H_kv + cur.zkv) * 256;
+              float4* dst =
+                  reinterpret_cast<float4*>(p.sh.tile_parts + first * D) + t * kBlockM + r;
+              p.sh.tile_lse[first + t * kBlockM + r] = empty ? -INFINITY : m + log2f(l);
 #pragma unroll 1
               for (int ch = 0; ch < D / 16; ++ch) {
                 uint32_t o[16];
@@ -928,11 +945,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 reg_after_wait(o);
 #pragma unroll
                 for (int qd = 0; qd < 4; ++qd)
-                  dst[ch * 4 + qd] =
+                  dst[(ch * 4 + qd) * 256] =
                       make_float4(u2f(o[qd * 4 + 0]) * inv_l, u2f(o[qd * 4 + 1]) * inv_l,
                                   u2f(o[qd * 4 + 2]) * inv_l, u2f(o[qd * 4 + 3]) * inv_l);
               }
-              __threadfence();
             }
           } else if constexpr (kPacked) {
             // bf16 O through shared memory: per 64-column slab, each warp
@@ -1350,7 +1366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tl.parts > 1 &&
             last_of_parts(p.sh.tile_counters + (size_t)tl.slot * p.H_kv + tl.zkv, tl.parts,
                           reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8)))
-          join_parts<D>(p, tl);
+          join_parts<D>(p, tl, reinterpret_cast<float*>(sKV));
       }
     }
   }

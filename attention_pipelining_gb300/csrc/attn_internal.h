@@ -275,10 +275,12 @@ struct PackedPlan {
   const int* cu_k;     // == cu_q where they are the same
   int B, T_q, T_k;
   int positions;       // query tokens of a 128-row tile
+  unsigned long long over_positions, over_tile;   // ceil(2^40 / positions), of 2 positions
   int causal, H_kv;
   PackedHeader* head;  // workspace, from here on
   int* seq_q;          // [B + 1], cu_q in order
   int* seq_k;          // [B + 1] (== seq_q where they are the same)
+  int* first[2];       // [B + 1] each, the sequences' first entries of the lists
   PackedTile* tiles;   // nullptr: not listed
   PackedKeys* keys;    // nullptr: not listed
   int* counters[2];    // of the tiles' and the key blocks' parts, to be cleared
@@ -286,11 +288,15 @@ struct PackedPlan {
 };
 
 // Parts: an entry of n blocks (of keys, or of query tiles) is cut where n is one and a
-// half times `cap` or more, into round(n / cap) parts, with cap the blocks of all entries
-// and K/V heads divided by kPackedCtas, or kPackedLeastPart where that is more.  So there
+// half times `cap` or more, into round(n / cap) parts (kPackedMostParts at most), with cap the blocks of all entries
+// and K/V heads divided by kPackedCtas, or kPackedLeast... where that is more.  So there
 // are at most n / cap + 1/2 <= 4/3 n / cap parts of an entry, and 4/3 kPackedCtas of all.
 constexpr int kPackedCtas = 152;
-constexpr int kPackedLeastPart = 6;
+constexpr int kPackedMostParts = 64;
+// blocks of a part, at least, of tiles and of key blocks.  Measured: one prompt of 2048 tokens, 8
+// heads over 2 of 128: 30 us with 8 (33 uncut), 700 tokens of 8 over 1 with 4 24 us (19 uncut); the
+// gradients of four texts of 30 to 300 tokens, 8 over 2 of 64: 28 us with 4 (33 uncut).
+constexpr int kPackedLeastTile = 8, kPackedLeastKeys = 4;
 inline int packed_slots(int H_kv) { return 4 * kPackedCtas / (3 * H_kv); }
 constexpr int kPackedCounters = 2;    // of an entry's parts and a K/V head: one a half of a tile
 

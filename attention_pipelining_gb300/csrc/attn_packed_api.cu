@@ -62,7 +62,7 @@ attn_status_t check_sizes(const attn_packed_t* s) {
 
 // Where the parts of the workspace begin.
 struct Layout {
-  size_t seq_q, seq_k, tiles, keys, tile_parts, tile_lse, key_parts, tile_counters, key_counters;
+  size_t seq_q, seq_k, first, tiles, keys, tile_parts, tile_lse, key_parts, tile_counters, key_counters;
   size_t nlse, ndelta, dq_acc, end;
   int64_t vec_stride;
   int slots;   // of a K/V head's parts, of each list
@@ -79,8 +79,9 @@ Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
   };
   l.seq_q = part((size_t)(s.B + 1) * sizeof(int));
   l.seq_k = part((size_t)(s.B + 1) * sizeof(int));
-  // Slots for parts, if any entry can be cut: one of kPackedLeastPart blocks and a half.
-  const auto cut = [](int64_t blocks) { return 2 * blocks >= 3 * kPackedLeastPart; };
+  l.first = part((size_t)(s.B + 1) * 2 * sizeof(int));
+  // Slots for parts, if any entry can be cut.
+  const auto cut = [](int64_t blocks, int least) { return 2 * blocks >= 3 * least; };
   const int64_t key_blocks = ((int64_t)s.T_k + 127) / 128;
   const int64_t query_tiles = ((int64_t)s.T_q + positions - 1) / positions;
   l.slots = packed_slots(s.H_kv);
@@ -88,7 +89,7 @@ Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
   if (!backward || deterministic) {
     l.tiles = part((size_t)packed_tile_room(s.T_q, s.B, positions, s.H_kv) * sizeof(PackedTile));
     l.tile_counters = part(counters);
-    if (cut(key_blocks)) {
+    if (cut(key_blocks, kPackedLeastTile)) {
       l.tile_parts = part(heads * 256 * s.D * sizeof(float));
       if (!backward) l.tile_lse = part(heads * 256 * sizeof(float));
     }
@@ -96,7 +97,7 @@ Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
   if (backward) {
     l.keys = part((size_t)packed_key_room(s.T_k, s.B, s.H_kv) * sizeof(PackedKeys));
     l.key_counters = part(counters);
-    if (cut(query_tiles)) l.key_parts = part(heads * 2 * 128 * s.D * sizeof(float));
+    if (cut(query_tiles, kPackedLeastKeys)) l.key_parts = part(heads * 2 * 128 * s.D * sizeof(float));
     // every sequence's rows from packed_vec0 on, and what a copy of 128 reads past them
     l.vec_stride = (((int64_t)s.T_q + 4ll * s.B + 4) * group + 128 + 3) & ~3ll;
     l.nlse = part((size_t)s.H_kv * l.vec_stride * sizeof(float));
@@ -122,6 +123,8 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   plan->T_q = s.T_q;
   plan->T_k = s.T_k;
   plan->positions = tile_positions(group);
+  plan->over_positions = ((1ull << 40) + plan->positions - 1) / plan->positions;
+  plan->over_tile = ((1ull << 40) + 2 * plan->positions - 1) / (2 * plan->positions);
   plan->causal = s.causal;
   plan->head = reinterpret_cast<PackedHeader*>(ws);
   plan->seq_q = reinterpret_cast<int*>(ws + l.seq_q);
@@ -129,6 +132,8 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   plan->H_kv = s.H_kv;
   // (a part that the layout does not have begins at 0, where the header is)
   const auto at = [&](size_t offset) { return offset ? ws + offset : nullptr; };
+  plan->first[0] = reinterpret_cast<int*>(ws + l.first);
+  plan->first[1] = plan->first[0] + s.B + 1;
   plan->tiles = reinterpret_cast<PackedTile*>(at(l.tiles));
   plan->keys = reinterpret_cast<PackedKeys*>(at(l.keys));
   plan->counters[0] = reinterpret_cast<int*>(at(l.tile_counters));

@@ -52,9 +52,9 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from) {
 }
 
 // Parts of one piece of work, done by different thread blocks, each of which has written its
-// share to global memory, every thread's writes followed by a __threadfence(): true in the
-// block that came last, for which all of them are visible (by loads that do not go
-// through L1).  Whole block; `flag` is in shared memory.
+// share to global memory: true in the block that came last, for which all of them are
+// visible (by loads that do not go through L1).  Whole block; `flag` is in shared memory.
+// (The fence before the count orders what the block's threads wrote before the barrier.)
 __device__ __forceinline__ bool last_of_parts(int* counter, int parts, volatile int* flag) {
   __syncthreads();   // (the writes are done, and the flag's last use)
   if (threadIdx.x == 0) {
@@ -66,22 +66,36 @@ __device__ __forceinline__ bool last_of_parts(int* counter, int parts, volatile 
   return *flag != 0;
 }
 
-// sum[0 .. 8) = the sum over the parts of weight(i) * 8 floats at `src` + i * `step`, always
-// in the same order.
+// A part's result of `rows` rows of D floats, as the threads of a warp (a row each) write
+// it and the joining threads read it in whole lines: float4 c of row r is float4 c * rows + r.
+//
+// The joining threads' order, eight floats (c: of float4s 2 c, 2 c + 1) a thread: a warp
+// takes eight rows and four pairs of float4s, so that it reads and writes 64 bytes in a
+// row at least.  Item i of (rows rounded up to 8) * D / 8.
+template <int D>
+__device__ __forceinline__ void join_item(int i, int& row, int& c) {
+  constexpr int kAcross = D / 32;   // warps' steps across a row
+  const int block = i >> 5, in = i & 31;
+  row = block / kAcross * 8 + (in & 7);
+  c = block % kAcross * 4 + (in >> 3);
+}
+
+// sum[0 .. 8) = the sum over the parts of weight(i) * the eight floats at `src` and `src` +
+// `rows`, `step` float4s from part to part, always in the same order.
 template <typename Weight>
-__device__ __forceinline__ void sum_parts(float (&sum)[8], const float* src, size_t step, int parts,
-                                          Weight&& weight) {
+__device__ __forceinline__ void sum_parts(float (&sum)[8], const float4* src, int rows, size_t step,
+                                          int parts, Weight&& weight) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll 1
   for (int i0 = 0; i0 < parts; i0 += 4) {
     float4 x[4][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {   // (past the last part: the last again, not added)
-      const float4* s4 = reinterpret_cast<const float4*>(src + (size_t)min(i0 + i, parts - 1) * step);
-      x[i][0] = __ldcg(s4);
-      x[i][1] = __ldcg(s4 + 1);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (i0 + i < parts) {
+        x[i][0] = __ldcg(src + (size_t)(i0 + i) * step);
+        x[i][1] = __ldcg(src + (size_t)(i0 + i) * step + rows);
+      }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i0 + i >= parts) break;

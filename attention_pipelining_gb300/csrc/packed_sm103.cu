@@ -1,7 +1,6 @@
 // packed_sm103.cu -- packed sequences: the plan of their attention's work, and
 // the rotation of queries and keys by positions with several axes
 // (include/attn_packed.h).
-#include <climits>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -19,128 +18,217 @@ namespace {
 // ---------------------------------------------------------------- plan
 
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 1024;   // of costs
-
-// Sum (or maximum) over the warp's lanes up to this one.
-template <typename Op>
-__device__ __forceinline__ int warp_scan(int x, Op op) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int off = 1; off < 32; off *= 2) {
-    const int y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x = op(x, y);
-  }
-  return x;
-}
-
-// The scan over the block's threads before this one (`none` for the first); `warps`: 32
-// ints of shared memory.
-template <typename Op>
-__device__ __forceinline__ int block_scan_before(int x, int none, int* warps, Op op) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int upto = warp_scan(x, op);
-  __syncthreads();   // (warps may still be read from the scan before)
-  if (lane == 31) warps[warp] = upto;
-  __syncthreads();
-  if (warp == 0) warps[lane] = warp_scan(warps[lane], op);
-  __syncthreads();
-  int before = __shfl_up_sync(0xffffffffu, upto, 1);
-  if (lane == 0) before = none;
-  return warp > 0 ? op(warps[warp - 1], before) : before;
-}
+constexpr int kBuckets = kPlanThreads;   // of costs: a thread to each
+constexpr int kPlanShared = 2048;  // sequences (and one) whose bounds fit shared memory
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// cu in order, within [0, T]: each entry the largest up to there.  True if it was not.
-__device__ bool put_in_order(const int* cu, int n, int T, int* out, int* warps) {
-  const auto larger = [](int a, int b) { return max(a, b); };
-  const int per = ceil_div(n, kPlanThreads);
-  const int first = min((int)threadIdx.x * per, n), end = min(first + per, n);
-  int most = 0;
-  for (int i = first; i < end; ++i) most = max(most, min(cu[i], T));
-  int run = block_scan_before(most, 0, warps, larger);
-  bool bad = false;
-  for (int i = first; i < end; ++i) {
-    const int x = cu[i];
-    run = max(run, min(x, T));
-    bad |= x != run;
-    out[i] = run;
+// x / d for x < 2^31 and d <= 256, with `inverse` = ceil(2^40 / d): off by less than 2^-9.
+__device__ __forceinline__ int over(int x, unsigned long long inverse) {
+  return (int)(((unsigned long long)(unsigned)x * inverse) >> 40);
+}
+
+// Scans of two values at once over the warp's lanes up to this one.
+template <typename Op>
+__device__ __forceinline__ int2 scan_warp(int2 v, Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int a = __shfl_up_sync(0xffffffffu, v.x, off), b = __shfl_up_sync(0xffffffffu, v.y, off);
+    if (lane >= off) v.x = op(v.x, a), v.y = op(v.y, b);
   }
-  return bad;
+  return v;
+}
+
+// Scans of two values at once over the block's threads before this one (0 for the first);
+// `warps`: 32 of shared memory.
+template <typename Op>
+__device__ __forceinline__ int2 scan_before(int2 x, int2* warps, Op op) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int2 upto = scan_warp(x, op);
+  if (lane == 31) warps[warp] = upto;
+  __syncthreads();
+  if (warp == 0) warps[lane] = scan_warp(warps[lane], op);
+  __syncthreads();
+  int2 before;
+  before.x = __shfl_up_sync(0xffffffffu, upto.x, 1);
+  before.y = __shfl_up_sync(0xffffffffu, upto.y, 1);
+  if (lane == 0) before = make_int2(0, 0);
+  if (warp > 0) before.x = op(warps[warp - 1].x, before.x), before.y = op(warps[warp - 1].y, before.y);
+  return before;
 }
 
 // Into how many parts an entry of n blocks is cut (see kPackedCtas).
 __device__ __forceinline__ int parts_of(int n, int cap) {
-  return 2 * n >= 3 * cap ? (n + cap / 2) / cap : 1;
+  return 2 * n >= 3 * cap ? min((n + cap / 2) / cap, kPackedMostParts) : 1;
 }
 
-// One thread block lists the tiles and the key blocks of all sequences, by a
-// counting sort over their costs in blocks (of 128 keys, or of query tiles), so that
-// the costliest run first and the last to end are short.  The order among equal costs
-// and the parts' slots differ from run to run; no result depends on them.
+// One thread block lists the tiles (list 0) and the key blocks (list 1) of all
+// sequences, by a counting sort over their costs in blocks (of 128 keys, or of query tiles),
+// so that the costliest run first and the last to end are short.  The order among
+// equal costs and the parts' slots differ from run to run; no result depends on them.
+//
+// It stands before every call, so what counts is its latency: a thread takes an entry
+// (found by bisection over the sequences' first entries), and the bounds stay in
+// shared memory.  A warp to a sequence, with the bounds read back from global memory,
+// took 5 to 9 us, this 3 to 4.
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
   __shared__ int at[2][kBuckets];   // entries of a cost, then where the next of them goes
-  __shared__ int warps[32], most[2], slots[2];
+  __shared__ int2 warps[2][32];
+  __shared__ int most[2], slots[2], bounds[4][kPlanShared];
   __shared__ unsigned long long total[2];   // blocks of all entries
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = p.positions, B = p.B, n = B + 1;
+  const bool same = p.seq_k == p.seq_q;
   at[0][threadIdx.x] = at[1][threadIdx.x] = 0;
   if (threadIdx.x < 2) most[threadIdx.x] = slots[threadIdx.x] = 0, total[threadIdx.x] = 0;
+  // the sequences' first queries and keys, and their first entries in both lists
+  const bool fits = n <= kPlanShared;
+  int* const q = fits ? bounds[0] : p.seq_q;
+  int* const k = same ? q : fits ? bounds[1] : p.seq_k;
+  int* const first[2] = {fits ? bounds[2] : p.first[0], fits ? bounds[3] : p.first[1]};
   allow_later();
   wait_for_earlier();
-  bool bad = put_in_order(p.cu_q, p.B + 1, p.T_q, p.seq_q, warps);
-  if (p.seq_k != p.seq_q) bad |= put_in_order(p.cu_k, p.B + 1, p.T_k, p.seq_k, warps);
-  if (bad) g_packed_status = ATTN_ERR_BAD_INDEX;
-  __syncthreads();
-  const int P = p.positions;
-  for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
-    const int n = p.seq_q[b + 1] - p.seq_q[b], m = p.seq_k[b + 1] - p.seq_k[b];
-    if (n > 0) atomicMax(&most[0], ceil_div(m, 128));
-    if (m > 0) atomicMax(&most[1], ceil_div(n, P));
-  }
-  __syncthreads();
+
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     for (int c = threadIdx.x; c < p.n_counters; c += kPlanThreads)
       if (p.counters[i] != nullptr) p.counters[i][c] = 0;
-  // every tile (list 0) and key block (list 1), whole, each with its cost
+
+  // The bounds in order, within [0, T]: each the largest up to there.  Then the sequences'
+  // first entries, and the most blocks that an entry may have.
+  const auto larger = [](int a, int b) { return max(a, b); };
+  const auto sum = [](int a, int b) { return a + b; };
+  const auto positions = [&](int x) { return over(x, p.over_positions); };
+  const auto entries = [&](int queries, int keys) {
+    return make_int2(p.tiles != nullptr ? over(queries + 2 * P - 1, p.over_tile) : 0,
+                     p.keys != nullptr ? (keys + 127) >> 7 : 0);
+  };
+  if (n <= 32) {   // (one warp, without the block's barriers: 1 us less)
+    if (warp == 0) {
+      const int a = lane < n ? p.cu_q[lane] : 0, b = lane < n && !same ? p.cu_k[lane] : 0;
+      int2 run = scan_warp(make_int2(max(min(a, p.T_q), 0), max(min(b, p.T_k), 0)), larger);
+      if (lane < n && (a != run.x || (!same && b != run.y))) g_packed_status = ATTN_ERR_BAD_INDEX;
+      if (same) run.y = run.x;
+      int queries = __shfl_down_sync(0xffffffffu, run.x, 1) - run.x;
+      int keys = __shfl_down_sync(0xffffffffu, run.y, 1) - run.y;
+      if (lane >= B) queries = keys = 0;
+      const int2 e = queries > 0 || keys > 0 ? entries(queries, keys) : make_int2(0, 0);
+      const int2 upto = scan_warp(e, sum);
+      const int high0 = __reduce_max_sync(0xffffffffu, e.x > 0 ? (keys + 127) >> 7 : 0);
+      const int high1 = __reduce_max_sync(0xffffffffu, e.y > 0 ? positions(queries + P - 1) : 0);
+      if (lane < n) {
+        q[lane] = run.x;
+        p.seq_q[lane] = run.x;
+        if (!same) k[lane] = run.y;
+        first[0][lane] = upto.x - e.x, first[1][lane] = upto.y - e.y;
+      }
+      if (lane == 0) most[0] = high0, most[1] = high1;
+    }
+  } else {
+    const int per = ceil_div(n, kPlanThreads);
+    const int begin = min((int)threadIdx.x * per, n), end = min(begin + per, n);
+    int2 run = make_int2(0, 0);
+    for (int i = begin; i < end; ++i) {
+      run.x = max(run.x, min(p.cu_q[i], p.T_q));
+      if (!same) run.y = max(run.y, min(p.cu_k[i], p.T_k));
+    }
+    run = scan_before(run, warps[0], larger);
+    bool bad = false;
+    for (int i = begin; i < end; ++i) {
+      const int a = p.cu_q[i], b = same ? 0 : p.cu_k[i];
+      run.x = max(run.x, min(a, p.T_q));
+      run.y = max(run.y, min(b, p.T_k));
+      bad |= a != run.x || b != run.y;
+      q[i] = run.x;
+      p.seq_q[i] = run.x;
+      if (!same) k[i] = run.y;
+    }
+    if (bad) g_packed_status = ATTN_ERR_BAD_INDEX;
+    __syncthreads();
+    int2 count = make_int2(0, 0), high = make_int2(0, 0);
+    for (int b = begin; b < min(end, B); ++b) {
+      const int queries = q[b + 1] - q[b], keys = k[b + 1] - k[b];
+      const int2 e = entries(queries, keys);
+      count.x += e.x, count.y += e.y;
+      if (e.x > 0) high.x = max(high.x, (keys + 127) >> 7);
+      if (e.y > 0) high.y = max(high.y, positions(queries + P - 1));
+    }
+    high.x = __reduce_max_sync(0xffffffffu, high.x);
+    high.y = __reduce_max_sync(0xffffffffu, high.y);
+    if (lane == 0 && high.x > 0) atomicMax(&most[0], high.x);
+    if (lane == 0 && high.y > 0) atomicMax(&most[1], high.y);
+    run = scan_before(count, warps[1], sum);
+    for (int b = begin; b < end; ++b) {
+      first[0][b] = run.x, first[1][b] = run.y;
+      if (b == B) break;
+      const int2 e = entries(q[b + 1] - q[b], k[b + 1] - k[b]);
+      run.x += e.x, run.y += e.y;
+    }
+  }
+  __syncthreads();
+
+  // Entry e of either list, whole: its sequence is the last that begins at or before it.
+  const auto sequence = [&](int list, int e) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[list][mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  const auto tile_of = [&](int e, PackedTile& x) {
+    const int b = sequence(0, e), len = q[b + 1] - q[b], m = k[b + 1] - k[b];
+    const int pos = (e - first[0][b]) * 2 * P;
+    x.tok0 = q[b] + pos;
+    x.rows = min(len - pos, 2 * P);
+    x.k0 = k[b];
+    x.k_len = m;
+    x.diag = m - len + pos + 1;
+    x.n_keys = p.causal ? min(max(x.diag + x.rows - 1, 0), m) : m;
+    x.vec0 = packed_vec0(q[b], b) + pos;
+    return (x.n_keys + 127) >> 7;
+  };
+  const auto keys_of = [&](int e, PackedKeys& x) {
+    const int b = sequence(1, e), len = q[b + 1] - q[b], m = k[b + 1] - k[b];
+    const int t = e - first[1][b];
+    x.k0 = k[b] + t * 128;
+    x.keys = min(m - t * 128, 128);
+    x.q0 = q[b];
+    x.q_len = len;
+    x.vec0 = packed_vec0(q[b], b);
+    x.shift = t * 128 - (m - len);
+    x.tiles = positions(len + P - 1);
+    // (without a mask each block begins elsewhere, so that those that run at once
+    // add to different rows of dQ)
+    x.first = p.causal ? min(positions(max(x.shift, 0)), x.tiles) : x.tiles > 0 ? t % x.tiles : 0;
+    return p.causal ? x.tiles - x.first : x.tiles;
+  };
+  // (a thread's first entries stay in registers: there are seldom more)
+  PackedTile tile0;
+  PackedKeys keys0;
+  const int tiles = first[0][B], key_blocks = first[1][B];
+  const int tile_cost = (int)threadIdx.x < tiles ? tile_of(threadIdx.x, tile0) : -1;
+  const int keys_cost = (int)threadIdx.x < key_blocks ? keys_of(threadIdx.x, keys0) : -1;
   const auto each = [&](auto&& put) {
-    for (int b = warp; b < p.B; b += kPlanThreads / 32) {
-      const int q0 = p.seq_q[b], n = p.seq_q[b + 1] - q0;
-      const int k0 = p.seq_k[b], m = p.seq_k[b + 1] - k0;
-      const int vec0 = packed_vec0(q0, b);
-      for (int t = lane; p.tiles != nullptr && t < ceil_div(n, 2 * P); t += 32) {
-        PackedTile x;
-        const int pos = t * 2 * P;
-        x.tok0 = q0 + pos;
-        x.rows = min(n - pos, 2 * P);
-        x.k0 = k0;
-        x.k_len = m;
-        x.diag = m - n + pos + 1;
-        x.n_keys = p.causal ? min(max(x.diag + x.rows - 1, 0), m) : m;
-        x.vec0 = vec0 + pos;
-        put(0, ceil_div(x.n_keys, 128), &x, (PackedKeys*)nullptr);
-      }
-      if (p.keys == nullptr) continue;
-      const int tiles = ceil_div(n, P);
-      for (int t = lane; t < ceil_div(m, 128); t += 32) {
-        PackedKeys x;
-        x.k0 = k0 + t * 128;
-        x.keys = min(m - t * 128, 128);
-        x.q0 = q0;
-        x.q_len = n;
-        x.vec0 = vec0;
-        x.shift = t * 128 - (m - n);
-        // (without a mask each block begins elsewhere, so that those that run at once
-        // add to different rows of dQ)
-        x.first = p.causal ? min(max(x.shift, 0) / P, tiles) : tiles > 0 ? t % tiles : 0;
-        x.n_work = p.causal ? tiles - x.first : tiles;
-        x.tiles = tiles;
-        put(1, x.n_work, (PackedTile*)nullptr, &x);
-      }
+    if (tile_cost >= 0) put(0, tile_cost, &tile0, (PackedKeys*)nullptr);
+    if (keys_cost >= 0) put(1, keys_cost, (PackedTile*)nullptr, &keys0);
+    for (int e = threadIdx.x + kPlanThreads; e < tiles; e += kPlanThreads) {
+      PackedTile x;
+      const int cost = tile_of(e, x);
+      put(0, cost, &x, (PackedKeys*)nullptr);
+    }
+    for (int e = threadIdx.x + kPlanThreads; e < key_blocks; e += kPlanThreads) {
+      PackedKeys x;
+      const int cost = keys_of(e, x);
+      put(1, cost, (PackedTile*)nullptr, &x);
     }
   };
+
   int shift[2], cap[2];
-  const bool may_cut = 2 * max(most[0], most[1]) >= 3 * kPackedLeastPart;
+  const bool may_cut =
+      2 * most[0] >= 3 * kPackedLeastTile || 2 * most[1] >= 3 * kPackedLeastKeys;
   if (may_cut) {
     unsigned long long mine[2] = {0, 0};
     each([&](int list, int cost, PackedTile*, PackedKeys*) { mine[list] += cost; });
@@ -155,65 +243,65 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const unsigned long long share = (total[i] * p.H_kv + kPackedCtas - 1) / kPackedCtas;
-    cap[i] = may_cut ? (int)min(max(share, (unsigned long long)kPackedLeastPart), 1ull << 29) : 1 << 29;
+    const unsigned long long least = i == 0 ? kPackedLeastTile : kPackedLeastKeys;
+    cap[i] = may_cut ? (int)min(max(share, least), 1ull << 29) : 1 << 29;
     shift[i] = 0;
     while ((most[i] >> shift[i]) >= kBuckets) ++shift[i];
   }
+  // (where all entries run at once, their order does not matter: one bucket for all)
+  const bool sorted = (long long)max(tiles, key_blocks) * p.H_kv > kPackedCtas ||
+                      2 * most[0] >= 3 * cap[0] || 2 * most[1] >= 3 * cap[1];
   const auto bucket = [&](int list, int cost) {
-    return &at[list][kBuckets - 1 - min(cost >> shift[list], kBuckets - 1)];
+    return &at[list][sorted ? kBuckets - 1 - min(cost >> shift[list], kBuckets - 1) : 0];
   };
   // an entry of n blocks has `parts` parts of `size` blocks, but for the last
-  const auto cut = [&](int list, int n, int& parts, int& size) {
-    parts = parts_of(n, cap[list]);
-    size = ceil_div(n, parts);
-    parts = n > 0 ? ceil_div(n, size) : 1;
+  const auto cut = [&](int list, int blocks, int& parts, int& size) {
+    parts = parts_of(blocks, cap[list]);
+    size = ceil_div(blocks, parts);
+    parts = blocks > 0 ? ceil_div(blocks, size) : 1;
   };
-  each([&](int list, int cost, PackedTile*, PackedKeys*) {
-    int parts, size;
-    cut(list, cost, parts, size);
-    if (parts > 1) atomicAdd(bucket(list, size), parts - 1);
-    atomicAdd(bucket(list, cost - (parts - 1) * size), 1);
-  });
-  __syncthreads();
-  const auto sum = [](int a, int b) { return a + b; };
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int mine = at[i][threadIdx.x];
-    const int before = block_scan_before(mine, 0, warps, sum);
-    at[i][threadIdx.x] = before;
-    if (threadIdx.x == kBuckets - 1) {
-      if (i == 0) p.head->tiles = before + mine;
-      if (i == 1) p.head->key_blocks = before + mine;
-    }
+  if (sorted) {
+    each([&](int list, int cost, PackedTile*, PackedKeys*) {
+      int parts, size;
+      cut(list, cost, parts, size);
+      if (parts > 1) atomicAdd(bucket(list, size), parts - 1);
+      atomicAdd(bucket(list, cost - (parts - 1) * size), 1);
+    });
+    __syncthreads();
+    // where each cost's entries begin
+    const int2 before = scan_before(make_int2(at[0][threadIdx.x], at[1][threadIdx.x]), warps[0], sum);
+    at[0][threadIdx.x] = before.x, at[1][threadIdx.x] = before.y;
+    __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    p.head->q_first = p.seq_q[0];
-    p.head->q_end = p.seq_q[p.B];
-    p.head->cut = 2 * most[0] >= 3 * cap[0];
-  }
-  __syncthreads();
   each([&](int list, int cost, PackedTile* tile, PackedKeys* keys) {
     int parts, size;
     cut(list, cost, parts, size);
     const int slot = parts > 1 ? atomicAdd(&slots[list], parts) : 0;
-    const int first = list == 1 ? keys->first : 0;
+    const int begins = list == 1 ? keys->first : 0;
     for (int part = 0; part < parts; ++part) {
-      const int n = part + 1 < parts ? size : cost - part * size;
-      const int i = atomicAdd(bucket(list, n), 1);
+      const int blocks = part + 1 < parts ? size : cost - part * size;
+      const int i = atomicAdd(bucket(list, blocks), 1);
       if (list == 0) {
-        tile->jb = part * size, tile->n_blocks = n;
+        tile->jb = part * size, tile->n_blocks = blocks;
         tile->parts = parts, tile->part = part, tile->slot = slot;
         p.tiles[i] = *tile;
       } else {
-        const int t = first + part * size;
-        keys->first = t < keys->tiles ? t : t - keys->tiles, keys->n_work = n;
+        const int t = begins + part * size;
+        keys->first = t < keys->tiles ? t : t - keys->tiles, keys->n_work = blocks;
         keys->parts = parts, keys->part = part, keys->slot = slot;
         p.keys[i] = *keys;
       }
     }
   });
+  __syncthreads();
+  // (behind the last entry of the last bucket, the lists end)
+  if (threadIdx.x == 0) {
+    const int last = sorted ? kBuckets - 1 : 0;
+    p.head->tiles = at[0][last], p.head->key_blocks = at[1][last];
+    p.head->q_first = q[0], p.head->q_end = q[B];
+    p.head->cut = 2 * most[0] >= 3 * cap[0];
+  }
 }
-static_assert(kBuckets == kPlanThreads, "one thread to a bucket");
 
 // ---------------------------------------------------------------- rotation
 

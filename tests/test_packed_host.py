@@ -133,19 +133,19 @@ def test_rotation_refuses(lib, kw, code):
 
 def test_workspace_holds_the_lists(lib):
     """A header, the bounds, 48 bytes for each tile and key block that there may be, with up to 4/3 of 152
-    parts, a part's results where any entry can be cut (six blocks), two counters a part, and (backward)
+    parts, a part's results where any entry can be cut (12 and 6 blocks), two counters a part, and (backward)
     two row vectors and the accumulator."""
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     for H_q, H_kv, positions in ((8, 8, 128), (8, 2, 32), (6, 2, 40), (5, 1, 24), (7, 1, 16), (32, 1, 4),
                                  (31, 1, 4), (128, 1, 1), (40, 1, 3), (512, 256, 64)):
         R = H_q // H_kv
-        for B, T in ((1, 1), (3, 1000), (500, 77)):
+        for B, T in ((1, 1), (3, 1000), (3, 1500), (500, 77)):
             s = sizes(B=B, T_q=T, T_k=T + 3, H_q=H_q, H_kv=H_kv, D=64)
             slots = 4 * 152 // (3 * H_kv)
             counters = up(slots * H_kv * 2 * 4)
-            begin = 256 + 2 * up(4 * (B + 1))
+            begin = 256 + 2 * up(4 * (B + 1)) + up(8 * (B + 1))
             tiles = up(48 * (T // (2 * positions) + B + slots)) + counters
-            if -(-(T + 3) // 128) >= 6:
+            if -(-(T + 3) // 128) >= 12:
                 tiles += up(slots * H_kv * 256 * 64 * 4)
                 lse = up(slots * H_kv * 256 * 4)
             else:
