@@ -142,6 +142,8 @@ struct Cfg {
   static constexpr int kOffTrace = (kOffMisc + 16 + 1023) / 1024 * 1024;
   static constexpr int kOffStage = kOffTrace;
   static constexpr int kStageBytes = 4 * 32 * 128;
+  // packed sequences: this CTA's tiles, after the staging
+  static constexpr int kOffTiles = kOffStage + kStageBytes;
   static constexpr int kTraceBytes = kNumTraceEvents * kMaxTraceBlocks * 8;
   static constexpr int kSmemEnd0 =
       (kOffTrace + (kTraceBytes > kStageBytes ? kTraceBytes : kStageBytes) + 1023) / 1024 * 1024;
@@ -154,6 +156,8 @@ struct Cfg {
   static_assert(2 * kBlockM * 4 <= 2 * kTileBytes, "split-tail log-sum-exps in the Q buffer");
   // packed sequences: the weights of a tile's parts in the idle ring
   static_assert(kPackedMostParts * 256 * 4 <= kSlots * kTileBytes, "weights in the ring");
+  static constexpr int kCachedTiles = (kTraceBytes - kStageBytes) / 64;
+  static_assert(kCachedTiles >= 64, "room for the tiles of a CTA");
   // Row sums on the tensor core (D = 64, where tensor memory has room): the
   // PV GEMM runs with N = D + 16 against [V | ones], so columns D .. D + 15
   // of O_t accumulate the sum of the bf16 probabilities the GEMM consumed,
@@ -311,11 +315,21 @@ __device__ __forceinline__ bool packed_tile(const PackedFwdParams& p, int n_tile
   t.parts = c4.y;
   t.part = c4.z;
   t.slot = c4.w;
-  t.has_sub1 = t.rows > p.sh.positions;
-  t.m0 = 0;
-  t.split = 0;
-  t.pair = -1;
   return true;
+}
+
+// The same from shared memory, where they are kept: read from global memory by every role,
+// a tile cost 0.7 us.
+__device__ __forceinline__ void keep_tile(int4* at, const Tile& t) {
+  at[0] = make_int4(t.n_blocks, t.rows, t.jb, t.k_len);
+  at[1] = make_int4(t.tok0, t.k0, t.n_keys, t.diag);
+  at[2] = make_int4(t.zkv, t.parts, t.part, t.slot);
+}
+__device__ __forceinline__ void kept_tile(const int4* at, Tile& t) {
+  const int4 a = at[0], b = at[1], c = at[2];
+  t.n_blocks = a.x, t.rows = a.y, t.jb = a.z, t.k_len = a.w;
+  t.tok0 = b.x, t.k0 = b.y, t.n_keys = b.z, t.diag = b.w;
+  t.zkv = c.x, t.parts = c.y, t.part = c.z, t.slot = c.w;
 }
 
 // A packed tile's rows from its parts (fp32 O, normalised, and base-2 log-sum-exps): O =
@@ -468,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&p.tm_q);
     tma_prefetch_map(&p.tm_k);
     tma_prefetch_map(&p.tm_v);
-    if (!kTrace && !kPacked) tma_prefetch_map(&p.tm_o);
+    if (!kTrace) tma_prefetch_map(&p.tm_o);
   }
   if (warp == 12) {
     tmem_alloc(sTmemBase, C::kTmemCols);
@@ -482,15 +496,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *sTmemBase;
   const int wg = warp >> 2;
   const int R = p.rows_per_group;
-  int n_tiles = 0;   // of a packed call
+  int my_tiles = 0;  // of a packed call, this CTA's
+  const int4* kept = reinterpret_cast<const int4*>(smem + C::kOffTiles);
   if constexpr (kPacked) {
     wait_for_earlier();
-    n_tiles = p.sh.head->tiles * p.H_kv;
+    // one tile a round, if any in the last (the launch sees to it that there is room)
+    const int n_tiles = p.sh.head->tiles * p.H_kv;
+    const int G = (int)gridDim.x, rounds = n_tiles / G, left = n_tiles - rounds * G;
+    my_tiles = min(rounds + (((rounds & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x) < left),
+                   C::kCachedTiles);
+    Tile tl;
+    if ((int)threadIdx.x < my_tiles && packed_tile(p, n_tiles, threadIdx.x, tl))
+      keep_tile(reinterpret_cast<int4*>(smem + C::kOffTiles) + threadIdx.x * 4, tl);
+    __syncthreads();
   }
   // the k-th tile of this CTA; false when there is none
   auto tile_at = [&](int k, Tile& tl) -> bool {
     if constexpr (kPacked) {
-      return packed_tile(p, n_tiles, k, tl);
+      if (k >= my_tiles) return false;
+      kept_tile(kept + k * 4, tl);
+      tl.has_sub1 = tl.rows > p.sh.positions;
+      tl.m0 = 0;
+      tl.split = 0;
+      tl.pair = -1;
+      return true;
     } else {
       int pr = -1;
       const int ti = tile_of<kTail>(p, k, pr);
@@ -580,7 +609,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // common (unmasked) one carries no per-element predication.
         auto body = [&](auto masked_tag) {
           constexpr bool kMasked = decltype(masked_tag)::value;
-          if constexpr (kMasked) {
+          int lim_most = 128;   // columns that some row of the warp sees
+          if constexpr (kMasked && kPacked) {
+            // A warp's rows are a few neighbouring tokens, so their limits lie close
+            // together: only the columns in between are compared one by one.
+            const int lim_least = __reduce_min_sync(kFull, lim);
+            lim_most = __reduce_max_sync(kFull, lim);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              if (16 * q + 16 <= lim_least) continue;
+#pragma unroll
+              for (int c = 16 * q; c < 16 * q + 16; ++c)
+                if (c >= lim) s[c] = f2u(-INFINITY);
+            }
+          } else if constexpr (kMasked) {
             // keys this row may not see drop out of the max
 #pragma unroll
             for (int c = 0; c < 128; ++c)
@@ -618,6 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ch = 0; ch < 8; ++ch) {
             uint32_t pk[8];
+            if (kMasked && kPacked && ch * 16 >= lim_most) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) pk[i] = 0u;
+              tmem_st_x8(tS + ch * 8, pk);
+              continue;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int c = ch * 16 + 2 * i;
@@ -930,10 +978,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               lse_out = (mx + log2f(e0 + e1)) * 0.69314718055994530942f;
             }
           }
-          if (kPacked && cur.parts > 1) {
+          if (kPacked && kept[k * 4 + 2].y > 1) {
             // a part of the tile's keys: normalised fp32 O and base-2 log-sum-exp
             if constexpr (kPacked) {
-              const size_t first = ((size_t)(cur.slot + cur.part) * p.H_kv + cur.zkv) * 256;
+              const int4 of = kept[k * 4 + 2];   // {K/V head, parts, part, slot}
+              const size_t first = ((size_t)(of.w + of.z) * p.H_kv + of.x) * 256;
               float4* dst =
                   reinterpret_cast<float4*>(p.sh.tile_parts + first * D) + t * kBlockM + r;
               p.sh.tile_lse[first + t * kBlockM + r] = empty ? -INFINITY : m + log2f(l);
@@ -951,16 +1000,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           } else if constexpr (kPacked) {
-            // bf16 O through shared memory: per 64-column slab, each warp
-            // writes its 32 rows into its own staging slab (16-byte piece c of row
-            // r at piece c ^ (r % 8)) and takes them out again four rows at a
-            // time, whole 128-byte lines; rows behind the sequence's end and spare rows
-            // are left out.
+            // bf16 O through shared memory, as below: where the warp's 32 rows are a
+            // box of the tensor (whole groups of heads, or 32 heads of one, of
+            // tokens that all exist) by one TMA copy; otherwise they are taken out
+            // again four rows at a time, whole 128-byte lines, without rows behind the
+            // sequence's end and spare rows.  (That way alone took 226 us instead of
+            // 193 for 16 x 1024 tokens: the correction warps are then late for
+            // the next tile.)
             const uint32_t stage = smem_u32(smem + C::kOffStage + q4 * 4096);
             const uint32_t srow = stage + (uint32_t)lane * 128u;
             const int group = p.sh.group, first = t * p.sh.positions;
+            const int rows = kept[k * 4].y, tok0 = kept[k * 4 + 1].x + first;
+            const int head0 = kept[k * 4 + 2].x * group;
+            {
+              const int i = token_of(r);
+              if (i < p.sh.positions && first + i < rows)
+                p.lse[(long long)(head0 + r - i * group) * p.sh.T_q + tok0 + i] = lse_row;
+            }
+            const bool whole = p.sh.o_box != 0 && first + token_of(q4 * 32 + 31) < rows;
 #pragma unroll 1
             for (int h = 0; h < D / 64; ++h) {
+              if (lane == 0) tma_store_wait_read<0>();
+              __syncwarp();
 #pragma unroll 1
               for (int q16 = 0; q16 < 4; ++q16) {
                 uint32_t o[16];
@@ -979,27 +1040,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                                pack_bf16x2(u2f(o[qd * 8 + 6]), u2f(o[qd * 8 + 7])));
                 }
               }
-              __syncwarp();
-#pragma unroll
-              for (int it = 0; it < 8; ++it) {
-                const int rr = it * 4 + (lane >> 3), c = lane & 7;   // row of the slab, piece
-                const int row = q4 * 32 + rr, i = token_of(row);
-                if (i < p.sh.positions && first + i < cur.rows) {
-                  const float4 x = ld_shared_v4f(stage + (uint32_t)rr * 128u +
-                                                 16u * (uint32_t)(c ^ (rr & 7)));
-                  const int head = cur.zkv * group + (row - i * group);
-                  uint16_t* dst = static_cast<uint16_t*>(p.o) +
-                                  (long long)(cur.tok0 + first + i) * p.o_st + head * p.o_sh +
-                                  h * 64 + c * 8;
-                  *reinterpret_cast<float4*>(dst) = x;
+              if (whole) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  const int at0 = token_of(q4 * 32);
+                  tma_store_3d(&p.tm_o, smem + C::kOffStage + q4 * 4096, h * 64,
+                               head0 + q4 * 32 - at0 * group, tok0 + at0);
+                  tma_store_commit();
                 }
+              } else {
+                __syncwarp();
+#pragma unroll 1
+                for (int rr = lane >> 3; rr < 32; rr += 4) {   // row of the slab
+                  const int c = lane & 7, i = token_of(q4 * 32 + rr);
+                  if (i < p.sh.positions && first + i < rows) {
+                    const float4 x = ld_shared_v4f(stage + (uint32_t)rr * 128u +
+                                                   16u * (uint32_t)(c ^ (rr & 7)));
+                    uint16_t* dst = static_cast<uint16_t*>(p.o) + (long long)(tok0 + i) * p.o_st +
+                                    (head0 + q4 * 32 + rr - i * group) * p.o_sh + h * 64 + c * 8;
+                    *reinterpret_cast<float4*>(dst) = x;
+                  }
+                }
+                __syncwarp();   // the slab may be written again
               }
-              __syncwarp();   // the slab may be written again
             }
-            const int i = token_of(r);
-            if (i < p.sh.positions && first + i < cur.rows)
-              p.lse[(long long)(cur.zkv * group + (r - i * group)) * p.sh.T_q + cur.tok0 + first + i] =
-                  lse_row;
           } else if (p.o_part != nullptr) {
             // split-KV partial: fp32 O normalised within the split, and its LSE
             const size_t row = (size_t)cur.split * p.total_rows + (size_t)cur.zkv * R + rho;
@@ -1525,8 +1590,12 @@ cudaError_t launch_packed_d(const PackedFwdParams& p, cudaStream_t stream) {
     }
   }
   if (p.num_tiles <= 0 || sms <= 0) return cudaErrorInvalidValue;
-  return launch_ahead(attn_fwd_kernel<D, false, false, true>,
-                      dim3((unsigned)(p.num_tiles < sms ? p.num_tiles : sms)), kThreads,
+  // persistent, as launch_d's, and as many times over as it takes for every CTA to keep its
+  // tiles in shared memory
+  const long long kept = (long long)sms * Cfg<D>::kCachedTiles;
+  const long long grid =
+      p.num_tiles < sms ? p.num_tiles : (p.num_tiles + kept - 1) / kept * sms;
+  return launch_ahead(attn_fwd_kernel<D, false, false, true>, dim3((unsigned)grid), kThreads,
                       Cfg<D>::kSmemBytes, stream, p);
 }
 

@@ -324,6 +324,7 @@ struct PackedShape {
   int positions;       // query tokens of a 128-row tile
   int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
   int T_q;
+  int o_box;           // whether 32 rows of a tile are a box of O (attn_fwd_packed)
   // parts' results, by slot and K/V head: of tiles [256 rows, D] and, in the forward,
   // their base-2 log-sum-exps [256]; of key blocks dV and dK, [2, 128 rows, D]
   float* tile_parts;

@@ -202,6 +202,12 @@ attn_status_t attn_fwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
   if ((st = check_device()) != ATTN_OK) return st;
   if (!map_rows(&p.tm_q, tq, *s, p.sh) || !map_keys(&p.tm_k, tk, *s) || !map_keys(&p.tm_v, tv, *s))
     return ATTN_ERR_CUDA;
+  // 32 rows of a tile: whole groups of heads of one token or more, or 32 heads of one
+  const int group = p.sh.group, box_heads = group < 32 ? group : 32;
+  p.sh.o_box = 32 % box_heads == 0 && group % box_heads == 0;
+  if (p.sh.o_box && !encode_bf16_map_thd(&p.tm_o, to.data, s->D, s->H_q, s->T_q, to.sh, to.st,
+                                         box_heads, 32 / box_heads))
+    return ATTN_ERR_CUDA;
   p.o = to.data;
   p.o_st = to.st;
   p.o_sh = to.sh;
