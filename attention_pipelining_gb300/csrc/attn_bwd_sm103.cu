@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // banded_rank); without it the blocks of one group are adjacent (they
   // share their Q and dO tiles in L2)
   //
-  // (packed: an entry of the list and a K/V head, in bands of entries as well)
+  // (packed: an entry of the list and a K/V head, in the plan's order)
   const int n_kvb = kPacked ? 0 : (p.S_kv + kRows - 1) / kRows;
   int kvb, zkv;
   int n_keys = 0, tok_k = 0;   // packed: keys of the block, its first token
@@ -527,9 +527,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   };
   if constexpr (kPacked) {
     wait_for_earlier();
-    const int entries = p.sh.head->key_blocks;
+    const int entries = p.sh.head->key_blocks, of = p.sh.key_order[blockIdx.x];
     if ((long long)blockIdx.x >= (long long)entries * p.H_kv) return;
-    banded_rank((int)blockIdx.x, entries, p.H_kv, kvb, zkv);
+    kvb = of / p.H_kv;
+    zkv = of - kvb * p.H_kv;
     const int4* src = reinterpret_cast<const int4*>(p.sh.keys + kvb);
     const int4 a = src[0], b = src[1];   // in PackedKeys' order
     tok_k = a.x;

@@ -283,6 +283,8 @@ struct PackedPlan {
   int* first[2];       // [B + 1] each, the sequences' first entries of the lists
   PackedTile* tiles;   // nullptr: not listed
   PackedKeys* keys;    // nullptr: not listed
+  int* key_order;      // [entries * H_kv] entry * H_kv + K/V head, in the order they run in
+  int* group_at;       // [entries] scratch
   int* counters[2];    // of the tiles' and the key blocks' parts, to be cleared
   int n_counters;      // of each
 };
@@ -293,6 +295,7 @@ struct PackedPlan {
 // are at most n / cap + 1/2 <= 4/3 n / cap parts of an entry, and 4/3 kPackedCtas of all.
 constexpr int kPackedCtas = 152;
 constexpr int kPackedMostParts = 64;
+constexpr int kPackedBand = 4;       // key blocks of a group
 // blocks of a part, at least, of tiles and of key blocks.  Measured: one prompt of 2048 tokens, 8
 // heads over 2 of 128: 30 us with 8 (33 uncut), 700 tokens of 8 over 1 with 4 24 us (19 uncut); the
 // gradients of four texts of 30 to 300 tokens, 8 over 2 of 64: 28 us with 4 (33 uncut).
@@ -320,6 +323,7 @@ struct PackedShape {
   const PackedHeader* head;
   const PackedTile* tiles;
   const PackedKeys* keys;
+  const int* key_order;
   int group;           // R
   int positions;       // query tokens of a 128-row tile
   int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
