@@ -222,7 +222,8 @@ struct BwdCfg {
   // columns each after the two accumulators; at D = 128 there is no room)
   static constexpr bool kKVinTmem = (D == 64);
   static constexpr int kOffMiscKV = kOffBarKV + kNumBarsKV * 8;
-  static constexpr int kSmemKV = kOffMiscKV + 16 + 1024;
+  static constexpr int kOffBlockKV = kOffMiscKV + 16;   // packed sequences: int [16], the CTA's block
+  static constexpr int kSmemKV = kOffBlockKV + 64 + 1024;
   // dQ kernel: Q, dO, then a ring of (K, V) stages
   static constexpr int kKVStages = (D == 128) ? 2 : 4;
   static constexpr int kOffQ = 0;
@@ -514,34 +515,50 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // banded_rank); without it the blocks of one group are adjacent (they
   // share their Q and dO tiles in L2)
   //
-  // (packed: an entry of the list and a K/V head, in the plan's order)
+  // (packed: in the plan's order)
   const int n_kvb = kPacked ? 0 : (p.S_kv + kRows - 1) / kRows;
   int kvb, zkv;
-  int n_keys = 0, tok_k = 0;   // packed: keys of the block, its first token
-  int tok_q = 0, q_len = 0, vec0 = 0, shift = 0, first_tile = 0, n_tiles = 0;   // and PackedKeys' others
-  int all_tiles = 0;
-  // {sequence's tiles, parts, part, slot}: read where it is needed, to save registers
-  auto of_parts = [&]() -> int4 {
-    if constexpr (kPacked) return reinterpret_cast<const int4*>(p.sh.keys + kvb)[2];
-    return make_int4(0, 1, 0, 0);
-  };
+  // Packed: what the block is, worked out by one thread and read from shared memory where
+  // it is needed, which saves registers.
+  enum { kTokK, kNKeys, kTokQ, kVec0, kHead, kPart, kSlot, kParts };
+  volatile int* const sBlock = reinterpret_cast<volatile int*>(smem + C::kOffBlockKV);
+  int n_tiles = 0, first_tile = 0, all_tiles = 0, q_len = 0, shift = 0;   // (in the loops)
   if constexpr (kPacked) {
+    // The blocks of a group come one K/V head after the other; any entry of the group
+    // says what the group is, so one load is enough.
     wait_for_earlier();
-    const int entries = p.sh.head->key_blocks, of = p.sh.key_order[blockIdx.x];
-    if ((long long)blockIdx.x >= (long long)entries * p.H_kv) return;
-    kvb = of / p.H_kv;
-    zkv = of - kvb * p.H_kv;
+    kvb = (int)blockIdx.x / p.H_kv;
     const int4* src = reinterpret_cast<const int4*>(p.sh.keys + kvb);
-    const int4 a = src[0], b = src[1];   // in PackedKeys' order
-    tok_k = a.x;
-    n_keys = a.y;
-    tok_q = a.z;
+    const int entries = p.sh.head->key_blocks;
+    const int4 a = src[0], b = src[1], c = src[2], d = src[3];   // in PackedKeys' order
+    if (kvb >= entries) return;
+    const int size = b.z;
+    all_tiles = c.x;
     q_len = a.w;
-    vec0 = b.x;
-    shift = b.y;
-    first_tile = b.z;
-    n_tiles = b.w;
-    all_tiles = src[2].x;
+    const int in_group = (int)blockIdx.x - (kvb - b.w) * p.H_kv;   // (head, block)
+    zkv = in_group / size;
+    const int t = in_group - zkv * size;
+    shift = b.y + t * kRows;
+    if (c.w > 1) {
+      first_tile = d.x;
+      n_tiles = d.y;
+    } else if (p.causal) {
+      first_tile = min(packed_over(max(shift, 0), p.sh.over_positions), all_tiles);
+      n_tiles = all_tiles - first_tile;
+    } else {
+      first_tile = all_tiles > 0 ? (d.x + t) % all_tiles : 0;
+      n_tiles = all_tiles;
+    }
+    if (threadIdx.x == 0) {
+      sBlock[kTokK] = a.x + t * kRows;
+      sBlock[kNKeys] = min(a.y - t * kRows, kRows);
+      sBlock[kTokQ] = a.z;
+      sBlock[kVec0] = b.x;
+      sBlock[kHead] = zkv;
+      sBlock[kPart] = c.y;
+      sBlock[kSlot] = c.z;
+      sBlock[kParts] = c.w;
+    }
   } else if (p.causal) {
     banded_rank((int)blockIdx.x, n_kvb, p.groups, kvb, zkv);
   } else {
@@ -646,7 +663,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const int r = (warp & 3) * 32 + lane;          // key row within the block
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int key = kPacked ? r : kv0 + r;         // (packed: within the block)
-    const int key_end = kPacked ? n_keys : p.S_kv;
+    const int key_end = kPacked ? sBlock[kNKeys] : p.S_kv;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     bool ok = true;
@@ -675,9 +692,9 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       if constexpr (kPacked) {
         const int group = p.sh.group;
         row_hi = min(q_len - r0, p.sh.positions) * group;
-        masked = row_hi < kRows || n_keys < kRows || (p.causal && r0 < shift + kRows - 1);
+        masked = row_hi < kRows || key_end < kRows || (p.causal && r0 < shift + kRows - 1);
         if (p.causal) row_lo = min(max(key + shift - r0, 0), kRows) * group;
-        if (key >= n_keys) row_hi = 0;
+        if (key >= key_end) row_hi = 0;
       } else {
         masked = (r0 + kRows > p.R) || (kv0 + kRows > p.S_kv);
       }
@@ -812,13 +829,14 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       tc_fence_after_sync();
     }
     const bool row_ok = key < key_end;
-    const int4 of = of_parts();
-    const int parts = of.y, part = of.z, slot = of.w;
+    const int parts = kPacked ? sBlock[kParts] : 1;
     uint16_t* dk_row = static_cast<uint16_t*>(p.dk);
     uint16_t* dv_row = static_cast<uint16_t*>(p.dv);
     if constexpr (kPacked) {
-      dk_row += (long long)(tok_k + key) * p.dk_st + zkv * p.dk_sh;
-      dv_row += (long long)(tok_k + key) * p.dv_st + zkv * p.dv_sh;
+      const int head = sBlock[kHead];
+      const long long tok = sBlock[kTokK] + key;
+      dk_row += tok * p.dk_st + head * p.dk_sh;
+      dv_row += tok * p.dv_st + head * p.dv_sh;
     } else {
       dk_row += ((size_t)zkv * p.S_kv + key) * D;
       dv_row += ((size_t)zkv * p.S_kv + key) * D;
@@ -843,7 +861,8 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
           if constexpr (kPacked) {
             float4* f4 = reinterpret_cast<float4*>(
                              p.sh.key_parts +
-                             (((size_t)(slot + part) * p.H_kv + zkv) * 2 + which) * kRows * D) +
+                             (((size_t)(sBlock[kSlot] + sBlock[kPart]) * p.H_kv +
+                               sBlock[kHead]) * 2 + which) * kRows * D) +
                          ((D / 8) * w + ch * 8) * kRows + r;
 #pragma unroll
             for (int qd = 0; qd < 8; ++qd)
@@ -877,7 +896,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     // packed: what the copies brought from behind the sequence's end, cleared (K for
     // dQ^T = K^T dS^T; a query tile for dV += P^T dO and dK += dS^T Q)
     if constexpr (kPacked && kFuse) {
-      if (ok && n_keys < kRows) clear_rows<D>(sK, n_keys);
+      if (ok && sBlock[kNKeys] < kRows) clear_rows<D>(sK, sBlock[kNKeys]);
     }
     auto clear_tile = [&](int n) {
       if constexpr (kPacked) {
@@ -971,11 +990,12 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const uint64_t pol_q = l2_policy_evict_last();
     int issued = 0;
     bool ok = n_work > 0;
+    const int tok_q = kPacked ? sBlock[kTokQ] : 0, vec0 = kPacked ? sBlock[kVec0] : 0;
     if (ok && leader) {
       mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
       if constexpr (kPacked) {
-        tma_load_tile<D>(sK, &p.tm_k, kv_full, zkv, tok_k, pol_kv);
-        tma_load_tile<D>(sV, &p.tm_v, kv_full, zkv, tok_k, pol_kv);
+        tma_load_tile<D>(sK, &p.tm_k, kv_full, zkv, sBlock[kTokK], pol_kv);
+        tma_load_tile<D>(sV, &p.tm_v, kv_full, zkv, sBlock[kTokK], pol_kv);
       } else {
         tma_load_tile<D>(sK, &p.tm_k, kv_full, kv0, zkv, pol_kv);
         tma_load_tile<D>(sV, &p.tm_v, kv_full, kv0, zkv, pol_kv);
@@ -996,8 +1016,9 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
           const int group = p.sh.group;
           mbar_arrive_expect_tx(&q_full[s],
                                 (uint32_t)(2 * group * p.sh.positions * D * 2) + 2 * C::kVecBytes);
-          tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], zkv * group, tok_q + r0, pol_q);
-          tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], zkv * group, tok_q + r0, pol_q);
+          const int tok = tok_q + r0;
+          tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], zkv * group, tok, pol_q);
+          tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], zkv * group, tok, pol_q);
           vo = (size_t)(zkv * p.vec_stride + (long long)(vec0 + r0) * group);
         } else {
           mbar_arrive_expect_tx(&q_full[s], 2 * C::kTileBytes + 2 * C::kVecBytes);
@@ -1031,6 +1052,9 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     // values go to a staging buffer and one thread adds all 16 KB with a
     // bulk reduction (one bulk group per half block; two buffers)
     float* sStage = reinterpret_cast<float*>(smem + C::kOffDqStage);
+    float* first_row = nullptr;   // packed: the sequence's first in the accumulator
+    if constexpr (kPacked)
+      first_row = p.dq_acc + ((long long)zkv * p.sh.T_q + sBlock[kTokQ]) * p.sh.group * D;
     int nh = 0;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     bool ok = true;
@@ -1068,8 +1092,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         if constexpr (kPacked) {
           const int group = p.sh.group;
           rows = min(q_len - r0, p.sh.positions) * group - 64 * h;
-          acc = p.dq_acc +
-                (((long long)zkv * p.sh.T_q + tok_q + r0) * group + 64 * h) * D;
+          acc = first_row + ((long long)r0 * group + 64 * h) * D;
         } else {
           rows = p.R - (r0 + 64 * h);
           acc = p.dq_acc + ((size_t)zkv * p.Rp + r0 + 64 * h) * D;
@@ -1112,8 +1135,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
   if constexpr (kPacked) {
     // the last of the block's parts adds them up
-    const int4 of = of_parts();
-    const int parts = of.y, slot = of.w;
+    const int parts = sBlock[kParts], slot = sBlock[kSlot], n_keys = sBlock[kNKeys];
     if (parts > 1 && !*sAbort &&
         last_of_parts(p.sh.key_counters + (size_t)slot * p.H_kv + zkv, parts,
                       reinterpret_cast<volatile int*>(smem + C::kOffMiscKV + 8))) {
@@ -1129,7 +1151,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
           if (r >= n_keys) continue;
           float x[8];
           sum_parts(x, first + 2 * c * kRows + r, kRows, step, parts, [](int) { return 1.f; });
-          const long long tok = tok_k + r;
+          const long long tok = sBlock[kTokK] + r;
           uint16_t* dst = which ? static_cast<uint16_t*>(p.dk) + tok * p.dk_st + zkv * p.dk_sh
                                 : static_cast<uint16_t*>(p.dv) + tok * p.dv_st + zkv * p.dv_sh;
           store_bf16x8(dst + c * 8, x, which ? p.scale : 1.f);

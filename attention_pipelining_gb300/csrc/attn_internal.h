@@ -246,21 +246,25 @@ struct __align__(16) PackedTile {
   int slot;
 };
 
-// A block of up to 128 keys of a sequence, with the query tiles that see it or a part
-// of them.
+// A group of up to kPackedBand blocks of 128 keys of a sequence that follow one another,
+// with the query tiles that see them; it stands in the list once for each block.  Or
+// one block with a part of its tiles.
 struct __align__(16) PackedKeys {
-  int k0;      // first key token
-  int keys;    // 1 .. 128
+  int k0;      // the group's first key token
+  int left;    // keys of the sequence from there on
   int q0;      // the sequence's first query token
   int q_len;
   int vec0;    // where the sequence's queries lie in the row vectors
-  int shift;   // causal: key r of the block is seen by queries at r + shift and behind
-  int first;   // the tile (of `positions` queries) that the part begins with
-  int n_work;  // tiles from there on (the sequence's last is followed by its first)
-  int tiles;   // of the sequence
-  int parts;   // as in PackedTile
-  int part;
+  int shift;   // causal: key r of the group is seen by queries at r + shift and behind
+  int size;    // blocks of the group
+  int before;  // this entry's place among them
+  int tiles;   // of the sequence (of `positions` queries)
+  int part;    // as in PackedTile, where parts > 1
   int slot;
+  int parts;
+  int first;   // of a part: the tile that it begins with, and how many tiles; otherwise the
+  int n_work;  // group's first block's place in the sequence, and 0
+  int unused[2];
 };
 
 struct PackedHeader {
@@ -283,7 +287,6 @@ struct PackedPlan {
   int* first[2];       // [B + 1] each, the sequences' first entries of the lists
   PackedTile* tiles;   // nullptr: not listed
   PackedKeys* keys;    // nullptr: not listed
-  int* key_order;      // [entries * H_kv] entry * H_kv + K/V head, in the order they run in
   int* group_at;       // [entries] scratch
   int* counters[2];    // of the tiles' and the key blocks' parts, to be cleared
   int n_counters;      // of each
@@ -302,6 +305,11 @@ constexpr int kPackedBand = 4;       // key blocks of a group
 constexpr int kPackedLeastTile = 8, kPackedLeastKeys = 4;
 inline int packed_slots(int H_kv) { return 4 * kPackedCtas / (3 * H_kv); }
 constexpr int kPackedCounters = 2;    // of an entry's parts and a K/V head: one a half of a tile
+
+// x / d for x < 2^31 and d <= 256, with `inverse` = ceil(2^40 / d): off by less than 2^-9.
+__host__ __device__ inline int packed_over(int x, unsigned long long inverse) {
+  return (int)(((unsigned long long)(unsigned)x * inverse) >> 40);
+}
 
 // Entries of the lists, at most.
 inline long long packed_tile_room(int T_q, int B, int positions, int H_kv) {
@@ -323,9 +331,9 @@ struct PackedShape {
   const PackedHeader* head;
   const PackedTile* tiles;
   const PackedKeys* keys;
-  const int* key_order;
   int group;           // R
   int positions;       // query tokens of a 128-row tile
+  unsigned long long over_positions;   // as in PackedPlan
   int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
   int T_q;
   int o_box;           // whether 32 rows of a tile are a box of O (attn_fwd_packed)

@@ -63,7 +63,7 @@ attn_status_t check_sizes(const attn_packed_t* s) {
 // Where the parts of the workspace begin.
 struct Layout {
   size_t seq_q, seq_k, first, tiles, keys, tile_parts, tile_lse, key_parts, tile_counters, key_counters;
-  size_t key_order, group_at;
+  size_t group_at;
   size_t nlse, ndelta, dq_acc, end;
   int64_t vec_stride;
   int slots;   // of a K/V head's parts, of each list
@@ -97,7 +97,6 @@ Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
   }
   if (backward) {
     l.keys = part((size_t)packed_key_room(s.T_k, s.B, s.H_kv) * sizeof(PackedKeys));
-    l.key_order = part((size_t)packed_key_room(s.T_k, s.B, s.H_kv) * s.H_kv * sizeof(int));
     l.group_at = part((size_t)packed_key_room(s.T_k, s.B, s.H_kv) * sizeof(int));
     l.key_counters = part(counters);
     if (cut(query_tiles, kPackedLeastKeys)) l.key_parts = part(heads * 2 * 128 * s.D * sizeof(float));
@@ -139,9 +138,8 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   plan->first[1] = plan->first[0] + s.B + 1;
   plan->tiles = reinterpret_cast<PackedTile*>(at(l.tiles));
   plan->keys = reinterpret_cast<PackedKeys*>(at(l.keys));
-  plan->key_order = reinterpret_cast<int*>(at(l.key_order));
   plan->group_at = reinterpret_cast<int*>(at(l.group_at));
-  shape->key_order = plan->key_order;
+  shape->over_positions = plan->over_positions;
   plan->counters[0] = reinterpret_cast<int*>(at(l.tile_counters));
   plan->counters[1] = reinterpret_cast<int*>(at(l.key_counters));
   plan->n_counters = l.slots * s.H_kv * kPackedCounters;

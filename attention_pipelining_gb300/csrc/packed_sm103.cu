@@ -23,11 +23,6 @@ constexpr int kPlanShared = 2048;  // sequences (and one) whose bounds fit share
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// x / d for x < 2^31 and d <= 256, with `inverse` = ceil(2^40 / d): off by less than 2^-9.
-__device__ __forceinline__ int over(int x, unsigned long long inverse) {
-  return (int)(((unsigned long long)(unsigned)x * inverse) >> 40);
-}
-
 // Scans of two values at once over the warp's lanes up to this one.
 template <typename Op>
 __device__ __forceinline__ int2 scan_warp(int2 v, Op op) {
@@ -99,9 +94,9 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   // first entries, and the most blocks that an entry may have.
   const auto larger = [](int a, int b) { return max(a, b); };
   const auto sum = [](int a, int b) { return a + b; };
-  const auto positions = [&](int x) { return over(x, p.over_positions); };
+  const auto positions = [&](int x) { return packed_over(x, p.over_positions); };
   const auto entries = [&](int queries, int keys) {
-    return make_int2(p.tiles != nullptr ? over(queries + 2 * P - 1, p.over_tile) : 0,
+    return make_int2(p.tiles != nullptr ? packed_over(queries + 2 * P - 1, p.over_tile) : 0,
                      p.keys != nullptr ? (keys + 127) >> 7 : 0);
   };
   if (n <= 32) {   // (one warp, without the block's barriers: 1 us less)
@@ -190,24 +185,26 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     x.vec0 = packed_vec0(q[b], b) + pos;
     return (x.n_keys + 127) >> 7;
   };
-  // query tiles that see a key of block t of a sequence of len queries and m keys
-  const auto tiles_from = [&](int t, int len, int m) {
+  // the first query tile that sees a key of block t of a sequence of len queries and m keys
+  const auto first_tile = [&](int t, int len, int m) {
     return p.causal ? min(positions(max(t * 128 - (m - len), 0)), positions(len + P - 1)) : 0;
   };
+  // (as the first of the group that it is in; the cost is its own)
   const auto keys_of = [&](int e, PackedKeys& x) {
     const int b = sequence(1, e), len = q[b + 1] - q[b], m = k[b + 1] - k[b];
-    const int t = e - first[1][b];
-    x.k0 = k[b] + t * 128;
-    x.keys = min(m - t * 128, 128);
+    const int t = e - first[1][b], t0 = t - t % kPackedBand;
+    x.k0 = k[b] + t0 * 128;
+    x.left = m - t0 * 128;
     x.q0 = q[b];
     x.q_len = len;
     x.vec0 = packed_vec0(q[b], b);
-    x.shift = t * 128 - (m - len);
+    x.shift = t0 * 128 - (m - len);
+    x.size = min((x.left + 127) >> 7, kPackedBand);
+    x.before = t - t0;
     x.tiles = positions(len + P - 1);
-    // (without a mask each block begins elsewhere, so that those that run at once
-    // add to different rows of dQ)
-    x.first = p.causal ? tiles_from(t, len, m) : x.tiles > 0 ? t % x.tiles : 0;
-    return p.causal ? x.tiles - x.first : x.tiles;
+    x.parts = 1, x.part = 0, x.slot = 0;
+    x.first = t0, x.n_work = 0;
+    return x.tiles - first_tile(t, len, m);
   };
   // (a thread's first entries stay in registers: there are seldom more)
   PackedTile tile0;
@@ -261,14 +258,11 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   // Key blocks, where none is cut, come in groups of up to kPackedBand neighbours, at the
   // first one's cost: the blocks of a group run side by side, one K/V head after the
   // other, and share that head's queries in L2.  (In the order of their own costs, with
-  // the heads innermost, 16 x 1024 tokens took 633 us instead of 590.)
+  // the heads innermost, 16 x 1024 tokens took 633 us instead of 570, in groups of 16 589;
+  // 4 x 4096 1421, 1417 and 1450.)
   const bool grouped = 2 * most[1] < 3 * cap[1];
-  const auto group_of = [&](int e, int& before, int& size) {
-    const int b = sequence(1, e), t = e - first[1][b];
-    const int len = q[b + 1] - q[b], m = k[b + 1] - k[b];
-    before = t % kPackedBand;
-    size = min((m + 127) >> 7, t - before + kPackedBand) - (t - before);
-    return positions(len + P - 1) - tiles_from(t - before, len, m);
+  const auto group_cost = [&](const PackedKeys& x) {   // its first block's
+    return x.tiles - (p.causal ? min(positions(max(x.shift, 0)), x.tiles) : 0);
   };
   // an entry of n blocks has `parts` parts of `size` blocks, but for the last
   const auto cut = [&](int list, int blocks, int& parts, int& size) {
@@ -277,11 +271,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     parts = blocks > 0 ? ceil_div(blocks, size) : 1;
   };
   if (sorted) {
-    each([&](int list, int e, int cost, PackedTile*, PackedKeys*) {
+    each([&](int list, int, int cost, PackedTile*, PackedKeys* keys) {
       int parts, size;
       if (list == 1 && grouped) {
-        const int of_group = group_of(e, parts, size);
-        if (parts == 0) atomicAdd(bucket(1, of_group), size);
+        if (keys->before == 0) atomicAdd(bucket(1, cost), keys->size);
         return;
       }
       cut(list, cost, parts, size);
@@ -296,29 +289,29 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   }
   if (grouped && p.keys != nullptr) {
     // the groups' places, by their first blocks
-    each([&](int list, int e, int, PackedTile*, PackedKeys*) {
-      int before, size;
-      if (list == 0) return;
-      const int cost = group_of(e, before, size);
-      if (before == 0) p.group_at[e] = atomicAdd(bucket(1, cost), size);
+    each([&](int list, int e, int cost, PackedTile*, PackedKeys* keys) {
+      if (list == 1 && keys->before == 0)
+        p.group_at[e] = atomicAdd(bucket(1, cost), keys->size);
     });
     __syncthreads();
   }
   each([&](int list, int e, int cost, PackedTile* tile, PackedKeys* keys) {
     int parts, size;
     if (list == 1 && grouped) {
-      int before;
-      group_of(e, before, size);
-      const int at0 = p.group_at[e - before];
-      keys->n_work = cost, keys->parts = 1, keys->part = 0, keys->slot = 0;
-      p.keys[at0 + before] = *keys;
-      for (int h = 0; h < p.H_kv; ++h)
-        p.key_order[at0 * p.H_kv + h * size + before] = (at0 + before) * p.H_kv + h;
+      p.keys[p.group_at[e - keys->before] + keys->before] = *keys;
       return;
     }
     cut(list, cost, parts, size);
     const int slot = parts > 1 ? atomicAdd(&slots[list], parts) : 0;
-    const int begins = list == 1 ? keys->first : 0;
+    int begins = 0;
+    if (list == 1) {   // a group of its own; without a mask each block begins with another
+      const int t = keys->before;   // tile, so that those that run at once add to different
+      const int block = keys->first + t;   // rows of dQ
+      keys->k0 += t * 128, keys->left -= t * 128, keys->shift += t * 128;
+      keys->size = 1, keys->before = 0;
+      begins = p.causal ? keys->tiles - cost : keys->tiles > 0 ? block % keys->tiles : 0;
+      keys->first = block;
+    }
     for (int part = 0; part < parts; ++part) {
       const int blocks = part + 1 < parts ? size : cost - part * size;
       const int i = atomicAdd(bucket(list, blocks), 1);
@@ -327,11 +320,12 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
         tile->parts = parts, tile->part = part, tile->slot = slot;
         p.tiles[i] = *tile;
       } else {
-        const int t = begins + part * size;
-        keys->first = t < keys->tiles ? t : t - keys->tiles, keys->n_work = blocks;
-        keys->parts = parts, keys->part = part, keys->slot = slot;
+        if (parts > 1) {
+          const int t = begins + part * size;
+          keys->first = t < keys->tiles ? t : t - keys->tiles, keys->n_work = blocks;
+          keys->parts = parts, keys->part = part, keys->slot = slot;
+        }
         p.keys[i] = *keys;
-        for (int h = 0; h < p.H_kv; ++h) p.key_order[i * p.H_kv + h] = i * p.H_kv + h;
       }
     }
   });
