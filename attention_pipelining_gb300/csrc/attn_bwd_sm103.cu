@@ -217,13 +217,16 @@ struct BwdCfg {
   // kv_full, q_full[S], q_empty[S], sp_full[2], ps_ready[2], acc_done, drain,
   // kt_ready (K and V copied into tensor memory; D = 64), then with kFuse
   // dq_full[2], dq_free[2], ds_free
-  static constexpr int kNumBarsKV = 2 * kQStages + 8 + 5;
+  // (and in the packed kernel kv_free, acc_free, work_full[2], work_empty[2])
+  static constexpr int kNumBarsKV = 2 * kQStages + 8 + 5 + 6;
   // dK/dV kernel at D = 64: K and V as tensor-memory A operands too (D / 2
   // columns each after the two accumulators; at D = 128 there is no room)
   static constexpr bool kKVinTmem = (D == 64);
   static constexpr int kOffMiscKV = kOffBarKV + kNumBarsKV * 8;
-  static constexpr int kOffBlockKV = kOffMiscKV + 16;   // packed sequences: int [16], the CTA's block
-  static constexpr int kSmemKV = kOffBlockKV + 64 + 1024;
+  // packed sequences: two slots of 64 bytes for works, and a list of parts
+  static constexpr int kOffWorkKV = kOffMiscKV + 16;
+  static constexpr int kPartsKV = 4 * kPackedCtas / 3;   // of all CTAs
+  static constexpr int kSmemKV = kOffWorkKV + 2 * 64 + kPartsKV * 4 + 1024;
   // dQ kernel: Q, dO, then a ring of (K, V) stages
   static constexpr int kKVStages = (D == 128) ? 2 : 4;
   static constexpr int kOffQ = 0;
@@ -379,11 +382,14 @@ __global__ void __launch_bounds__(256)
   const int q_first = p.sh.head->q_first, q_end = p.sh.head->q_end;
   uint4 a[kLoads], b[kLoads];
   int tok[kLoads], head[kLoads];
+  float delta[kLoads];
+  const long long t0 = row0 / p.H_q;
+  const int h0 = (int)(row0 - t0 * p.H_q);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const long long row = row0 + i * kRowsPerLoad + sub;
-    const long long t = row / p.H_q;
-    head[i] = (int)(row - t * p.H_q);
+    long long t = t0;
+    head[i] = h0 + i * kRowsPerLoad + sub;
+    while (head[i] >= p.H_q) head[i] -= p.H_q, ++t;
     tok[i] = t >= q_first && t < q_end ? (int)t : -1;
     a[i] = make_uint4(0u, 0u, 0u, 0u);
     b[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -404,28 +410,41 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int off = kLanesPerRow / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(kAll, acc, off);
+    delta[i] = acc;
     if (tok[i] < 0) continue;
-    const int group = p.sh.group, g = head[i] / group, r = head[i] - g * group;
+    const int group = p.sh.group, g = packed_over(head[i], p.sh.over_group), r = head[i] - g * group;
     if (p.dq_acc != nullptr) {
       float4* z = reinterpret_cast<float4*>(
           p.dq_acc + (((long long)g * p.sh.T_q + tok[i]) * group + r) * D + piece * 8);
       z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
       z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (piece == 0) {
-      int b0 = 0, b1 = p.B;   // seq_q[b0] <= tok < seq_q[b1]
-      while (b1 - b0 > 1) {
-        const int mid = (b0 + b1) >> 1;
-        if (p.seq_q[mid] <= tok[i]) b0 = mid;
-        else b1 = mid;
-      }
-      const int q0 = p.seq_q[b0];
-      const long long at =
-          g * p.vec_stride + (long long)(packed_vec0(q0, b0) + tok[i] - q0) * group + r;
-      p.ndelta[at] = -acc;
-      p.nlse2[at] = -(lse[(long long)head[i] * p.sh.T_q + tok[i]] * 1.4426950408889634f);
-    }
   }
+  // lane n < 8 has the warp's row n: its place in the vectors
+  float mine = 0.f;
+  int my_tok = -1, my_head = 0;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+    for (int n = 0; n < kRowsPerLoad; ++n) {
+      const float x = __shfl_sync(kAll, delta[i], n * kLanesPerRow);
+      const int t = __shfl_sync(kAll, tok[i], n * kLanesPerRow);
+      const int h = __shfl_sync(kAll, head[i], n * kLanesPerRow);
+      if (lane == i * kRowsPerLoad + n) mine = x, my_tok = t, my_head = h;
+    }
+  if (my_tok < 0) return;
+  int b0 = 0, b1 = p.B;   // seq_q[b0] <= my_tok < seq_q[b1]
+  while (b1 - b0 > 1) {
+    const int mid = (b0 + b1) >> 1;
+    if (p.seq_q[mid] <= my_tok) b0 = mid;
+    else b1 = mid;
+  }
+  const int group = p.sh.group, g = packed_over(my_head, p.sh.over_group), r = my_head - g * group;
+  const int q0 = p.seq_q[b0];
+  const long long at =
+      g * p.vec_stride + (long long)(packed_vec0(q0, b0) + my_tok - q0) * group + r;
+  p.ndelta[at] = -mine;
+  p.nlse2[at] = -(lse[(long long)my_head * p.sh.T_q + my_tok] * 1.4426950408889634f);
 }
 
 // dq = bf16(scale * dq_acc) over the tokens of the packed sequences; one thread per 8
@@ -435,14 +454,15 @@ __global__ void __launch_bounds__(256)
     packed_bwd_dq_convert_kernel(const __grid_constant__ PackedBwdParams p) {
   constexpr int kPieces = D / 8;
   wait_for_earlier();
+  // blockIdx.y: K/V head; in it (token, head in the group, piece)
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long row = i / kPieces;   // (K/V head, token, head in the group)
-  const int piece = (int)(i - row * kPieces);
-  const long long gt = row / p.sh.group;
-  const int r = (int)(row - gt * p.sh.group);
-  const int g = (int)(gt / p.sh.T_q);
-  const long long t = gt - (long long)g * p.sh.T_q;
-  if (g >= p.H_kv || t < p.sh.head->q_first || t >= p.sh.head->q_end) return;
+  const long long gr = i / kPieces;
+  const int piece = (int)(i % kPieces), g = (int)blockIdx.y;
+  const long long t =
+      p.sh.group == 1 ? gr : (long long)__umul64hi((unsigned long long)gr, p.sh.over_group64);
+  const int r = (int)(gr - t * p.sh.group);
+  if (t < p.sh.head->q_first || t >= p.sh.head->q_end) return;
+  const long long row = (long long)g * p.sh.T_q * p.sh.group + gr;
   const float4* src = reinterpret_cast<const float4*>(p.dq_acc + row * D + piece * 8);
   const float4 a = src[0], b = src[1];
   const float sc = p.scale;
@@ -485,9 +505,9 @@ __global__ void __launch_bounds__(256) attn_bwd_dq_convert_kernel(const BwdParam
 // into the half's dP^T columns, and warps 12-15 read it out and add it into
 // the fp32 accumulator p.dq_acc in L2 (red.global.add); dS^T for dK then
 // sits in tensor memory next to P^T.  512 threads.
-template <int D, bool kFuse, bool kPacked = false>
+template <int D, bool kFuse>
 __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
-    attn_bwd_dkdv_kernel(const __grid_constant__ BwdParamsOf<kPacked> p) {
+    attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw_b[];
   uint8_t* smem = align_smem_1024(smem_raw_b);
@@ -514,64 +534,21 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // blocks carry the most query blocks, so they go first (in bands, see
   // banded_rank); without it the blocks of one group are adjacent (they
   // share their Q and dO tiles in L2)
-  //
-  // (packed: in the plan's order)
-  const int n_kvb = kPacked ? 0 : (p.S_kv + kRows - 1) / kRows;
+  const int n_kvb = (p.S_kv + kRows - 1) / kRows;
   int kvb, zkv;
-  // Packed: what the block is, worked out by one thread and read from shared memory where
-  // it is needed, which saves registers.
-  enum { kTokK, kNKeys, kTokQ, kVec0, kHead, kPart, kSlot, kParts };
-  volatile int* const sBlock = reinterpret_cast<volatile int*>(smem + C::kOffBlockKV);
-  int n_tiles = 0, first_tile = 0, all_tiles = 0, q_len = 0, shift = 0;   // (in the loops)
-  if constexpr (kPacked) {
-    // The blocks of a group come one K/V head after the other; any entry of the group
-    // says what the group is, so one load is enough.
-    wait_for_earlier();
-    kvb = (int)blockIdx.x / p.H_kv;
-    const int4* src = reinterpret_cast<const int4*>(p.sh.keys + kvb);
-    const int entries = p.sh.head->key_blocks;
-    const int4 a = src[0], b = src[1], c = src[2], d = src[3];   // in PackedKeys' order
-    if (kvb >= entries) return;
-    const int size = b.z;
-    all_tiles = c.x;
-    q_len = a.w;
-    const int in_group = (int)blockIdx.x - (kvb - b.w) * p.H_kv;   // (head, block)
-    zkv = in_group / size;
-    const int t = in_group - zkv * size;
-    shift = b.y + t * kRows;
-    if (c.w > 1) {
-      first_tile = d.x;
-      n_tiles = d.y;
-    } else if (p.causal) {
-      first_tile = min(packed_over(max(shift, 0), p.sh.over_positions), all_tiles);
-      n_tiles = all_tiles - first_tile;
-    } else {
-      first_tile = all_tiles > 0 ? (d.x + t) % all_tiles : 0;
-      n_tiles = all_tiles;
-    }
-    if (threadIdx.x == 0) {
-      sBlock[kTokK] = a.x + t * kRows;
-      sBlock[kNKeys] = min(a.y - t * kRows, kRows);
-      sBlock[kTokQ] = a.z;
-      sBlock[kVec0] = b.x;
-      sBlock[kHead] = zkv;
-      sBlock[kPart] = c.y;
-      sBlock[kSlot] = c.z;
-      sBlock[kParts] = c.w;
-    }
-  } else if (p.causal) {
+  if (p.causal) {
     banded_rank((int)blockIdx.x, n_kvb, p.groups, kvb, zkv);
   } else {
     zkv = blockIdx.x / n_kvb;
     kvb = blockIdx.x - zkv * n_kvb;
   }
   const int kv0 = kvb * kRows;              // first key of the block
-  const int n_qb = kPacked ? n_tiles : (p.R + kRows - 1) / kRows;
+  const int n_qb = (p.R + kRows - 1) / kRows;
   // the order every role walks the query blocks in: with kFuse and no mask
   // rotated by the key block, so the CTAs running at once add into
   // different dQ rows (with the causal mask each key block starts at its own
   // diagonal anyway)
-  const int rot = (!kPacked && kFuse && !p.causal) ? kvb % n_qb : 0;
+  const int rot = (kFuse && !p.causal) ? kvb % n_qb : 0;
   auto qb_at = [&](int i) { return i + rot < n_qb ? i + rot : i + rot - n_qb; };
   // The query blocks with work (items n = 0 .. n_work - 1), walked by every
   // role in the same order.  With the causal mask and S_q a multiple of 128
@@ -580,11 +557,11 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // those blocks of each head in turn, found without a scan (a scan's
   // division per skipped block cost a short CTA tens of microseconds).
   // Otherwise (a ragged S_q) the blocks are scanned with qblock_sees.
-  const bool by_head = !kPacked && p.causal && (p.S_q % kRows == 0);
+  const bool by_head = p.causal && (p.S_q % kRows == 0);
   const int nqh = by_head ? p.S_q / kRows : 1;             // position blocks per head
   const int per_head = by_head ? (nqh > kvb ? nqh - kvb : 0) : 0;
   int n_work = 0;
-  if (kPacked || !p.causal) {
+  if (!p.causal) {
     n_work = n_qb;
   } else if (by_head) {
     n_work = (p.R / p.S_q) * per_head;
@@ -594,11 +571,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   // first row of item n's query block; `cursor` is the caller's scan
   // position (the ragged causal case only; items are asked for in order)
   auto item_r0 = [&](int n, int& cursor) -> int {
-    // (packed: the tile's first query position)
-    if constexpr (kPacked) {
-      const int t = first_tile + n;
-      return (t < all_tiles ? t : t - all_tiles) * p.sh.positions;
-    }
     if (!p.causal) return qb_at(n) * kRows;
     if (by_head) {
       const int h = n / per_head;
@@ -629,13 +601,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     *sAbort = 0;
     fence_mbar_init();
   }
-  if constexpr (kPacked) {
-    // the spare rows of the Q and dO tiles, which no copy writes
-    const int spare = p.sh.group * p.sh.positions;
-    if (spare < kRows && warp < 2 * C::kQStages)
-      clear_rows<D>(smem + C::kOffQRing + (warp >> 1) * C::kQStageBytes + (warp & 1) * C::kTileBytes,
-                    spare);
-  }
   if (warp == 8) {
     tmem_alloc(sTmemBase, C::kTmemCols);
     tmem_relinquish();
@@ -662,8 +627,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;          // key row within the block
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const int key = kPacked ? r : kv0 + r;         // (packed: within the block)
-    const int key_end = kPacked ? sBlock[kNKeys] : p.S_kv;
+    const int key = kv0 + r;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     bool ok = true;
@@ -686,19 +650,9 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       const int s = n % C::kQStages;
       // masking: rows past R, keys past S_kv, and (causal) keys after a row's
       // position; a block needs none when every row sees every key
-      bool masked;
+      bool masked = (r0 + kRows > p.R) || (kv0 + kRows > p.S_kv);
       int base_pos = 0;
-      int row_lo = 0, row_hi = kRows;   // packed: the tile's rows that see this thread's key
-      if constexpr (kPacked) {
-        const int group = p.sh.group;
-        row_hi = min(q_len - r0, p.sh.positions) * group;
-        masked = row_hi < kRows || key_end < kRows || (p.causal && r0 < shift + kRows - 1);
-        if (p.causal) row_lo = min(max(key + shift - r0, 0), kRows) * group;
-        if (key >= key_end) row_hi = 0;
-      } else {
-        masked = (r0 + kRows > p.R) || (kv0 + kRows > p.S_kv);
-      }
-      if (!kPacked && p.causal) {
+      if (p.causal) {
         base_pos = r0 % p.S_q;
         const bool one_head = (base_pos + kRows <= p.S_q);
         masked = masked || !(one_head && base_pos >= kv0 + kRows - 1);
@@ -743,10 +697,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float pv = ex2_approx(x[e]);
-              if constexpr (kMasked && kPacked) {
-                const int row = col0 + c + e;
-                pv = row >= row_lo && row < row_hi ? pv : 0.f;
-              } else if constexpr (kMasked) {
+              if constexpr (kMasked) {
                 const int rho = r0 + col0 + c + e;
                 bool vis = (rho < p.R) && (key < p.S_kv);
                 if (p.causal) {
@@ -773,14 +724,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
             float d0, d1, d2, d3;
             f2_unpack(ds01, d0, d1);
             f2_unpack(ds23, d2, d3);
-            if constexpr (kMasked && kPacked) {
-              // (what a masked dP or D holds may be another sequence's infinity)
-              const int row = col0 + c;
-              d0 = row >= row_lo && row < row_hi ? d0 : 0.f;
-              d1 = row + 1 >= row_lo && row + 1 < row_hi ? d1 : 0.f;
-              d2 = row + 2 >= row_lo && row + 2 < row_hi ? d2 : 0.f;
-              d3 = row + 3 >= row_lo && row + 3 < row_hi ? d3 : 0.f;
-            }
             pk[2 * i4] = pack_bf16x2(pr[0], pr[1]);
             pk[2 * i4 + 1] = pack_bf16x2(pr[2], pr[3]);
             dk[2 * i4] = pack_bf16x2(d0, d1);
@@ -828,23 +771,13 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       if (!warp_wait_b(acc_done, 0, sAbort, budget)) { ok = false; have_acc = false; }
       tc_fence_after_sync();
     }
-    const bool row_ok = key < key_end;
-    const int parts = kPacked ? sBlock[kParts] : 1;
-    uint16_t* dk_row = static_cast<uint16_t*>(p.dk);
-    uint16_t* dv_row = static_cast<uint16_t*>(p.dv);
-    if constexpr (kPacked) {
-      const int head = sBlock[kHead];
-      const long long tok = sBlock[kTokK] + key;
-      dk_row += tok * p.dk_st + head * p.dk_sh;
-      dv_row += tok * p.dv_st + head * p.dv_sh;
-    } else {
-      dk_row += ((size_t)zkv * p.S_kv + key) * D;
-      dv_row += ((size_t)zkv * p.S_kv + key) * D;
-    }
+    const bool row_ok = key < p.S_kv;
+    uint16_t* dk_row = static_cast<uint16_t*>(p.dk) + ((size_t)zkv * p.S_kv + key) * D;
+    uint16_t* dv_row = static_cast<uint16_t*>(p.dv) + ((size_t)zkv * p.S_kv + key) * D;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {  // 0: dV, 1: dK
       uint16_t* dst = which ? dk_row : dv_row;
-      const float mult = (kPacked && parts > 1) ? 1.f : which ? p.scale : 1.f;
+      const float mult = which ? p.scale : 1.f;
       const uint32_t acc = tmem + lane_base + (which ? C::kTmAcc1 : C::kTmAcc0) + (D / 2) * w;
 #pragma unroll
       for (int ch = 0; ch < D / 64; ++ch) {
@@ -857,19 +790,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0u;  // no query sees these keys
         }
-        if (kPacked && parts > 1) {
-          if constexpr (kPacked) {
-            float4* f4 = reinterpret_cast<float4*>(
-                             p.sh.key_parts +
-                             (((size_t)(sBlock[kSlot] + sBlock[kPart]) * p.H_kv +
-                               sBlock[kHead]) * 2 + which) * kRows * D) +
-                         ((D / 8) * w + ch * 8) * kRows + r;
-#pragma unroll
-            for (int qd = 0; qd < 8; ++qd)
-              f4[qd * kRows] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
-                                   u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
-          }
-        } else if (row_ok && ok) {
+        if (row_ok && ok) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + (D / 2) * w + ch * 32);
 #pragma unroll
           for (int qd = 0; qd < 4; ++qd) {
@@ -893,22 +814,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const uint32_t tdV = tmem + C::kTmAcc0, tdK = tmem + C::kTmAcc1;
     bool ok = n_work > 0 &&
               warp_wait_b(C::kKVinTmem ? kt_ready : kv_full, 0, sAbort, budget);
-    // packed: what the copies brought from behind the sequence's end, cleared (K for
-    // dQ^T = K^T dS^T; a query tile for dV += P^T dO and dK += dS^T Q)
-    if constexpr (kPacked && kFuse) {
-      if (ok && sBlock[kNKeys] < kRows) clear_rows<D>(sK, sBlock[kNKeys]);
-    }
-    auto clear_tile = [&](int n) {
-      if constexpr (kPacked) {
-        int cursor = 0;
-        const int rows = (q_len - item_r0(n, cursor)) * p.sh.group;
-        const int s = n % C::kQStages;
-        if (rows < p.sh.group * p.sh.positions) {
-          clear_rows<D>(stage_q(s), rows);
-          clear_rows<D>(stage_do(s), rows);
-        }
-      }
-    };
     // S^T and dP^T of half h of work item n (its Q / dO stage is loaded);
     // at D = 64 K and V are read from tensor memory
     auto issue_sp = [&](int n, int h) {
@@ -926,7 +831,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     };
     if (ok && warp_wait_b(&q_full[0], 0, sAbort, budget)) {
       tc_fence_after_sync();
-      clear_tile(0);
       issue_sp(0, 0);
       issue_sp(0, 1);
     } else {
@@ -966,7 +870,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
               break;
             }
             tc_fence_after_sync();
-            clear_tile(n + 1);
           }
           if constexpr (kFuse) {
             // ... and over this half's dQ^T once it has been read out
@@ -990,16 +893,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const uint64_t pol_q = l2_policy_evict_last();
     int issued = 0;
     bool ok = n_work > 0;
-    const int tok_q = kPacked ? sBlock[kTokQ] : 0, vec0 = kPacked ? sBlock[kVec0] : 0;
     if (ok && leader) {
       mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
-      if constexpr (kPacked) {
-        tma_load_tile<D>(sK, &p.tm_k, kv_full, zkv, sBlock[kTokK], pol_kv);
-        tma_load_tile<D>(sV, &p.tm_v, kv_full, zkv, sBlock[kTokK], pol_kv);
-      } else {
-        tma_load_tile<D>(sK, &p.tm_k, kv_full, kv0, zkv, pol_kv);
-        tma_load_tile<D>(sV, &p.tm_v, kv_full, kv0, zkv, pol_kv);
-      }
+      tma_load_tile<D>(sK, &p.tm_k, kv_full, kv0, zkv, pol_kv);
+      tma_load_tile<D>(sV, &p.tm_v, kv_full, kv0, zkv, pol_kv);
     }
     int cursor = 0;
     for (int n = 0; n < n_work && ok; ++n) {
@@ -1011,21 +908,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         break;
       }
       if (leader) {
-        size_t vo;
-        if constexpr (kPacked) {
-          const int group = p.sh.group;
-          mbar_arrive_expect_tx(&q_full[s],
-                                (uint32_t)(2 * group * p.sh.positions * D * 2) + 2 * C::kVecBytes);
-          const int tok = tok_q + r0;
-          tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], zkv * group, tok, pol_q);
-          tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], zkv * group, tok, pol_q);
-          vo = (size_t)(zkv * p.vec_stride + (long long)(vec0 + r0) * group);
-        } else {
-          mbar_arrive_expect_tx(&q_full[s], 2 * C::kTileBytes + 2 * C::kVecBytes);
-          tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], r0, zkv, pol_q);
-          tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], r0, zkv, pol_q);
-          vo = (size_t)zkv * p.Rp + r0;
-        }
+        mbar_arrive_expect_tx(&q_full[s], 2 * C::kTileBytes + 2 * C::kVecBytes);
+        tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], r0, zkv, pol_q);
+        tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], r0, zkv, pol_q);
+        const size_t vo = (size_t)zkv * p.Rp + r0;
         bulk_load(stage_lse(s), p.nlse2 + vo, C::kVecBytes, &q_full[s]);
         bulk_load(stage_delta(s), p.ndelta + vo, C::kVecBytes, &q_full[s]);
       }
@@ -1052,9 +938,6 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     // values go to a staging buffer and one thread adds all 16 KB with a
     // bulk reduction (one bulk group per half block; two buffers)
     float* sStage = reinterpret_cast<float*>(smem + C::kOffDqStage);
-    float* first_row = nullptr;   // packed: the sequence's first in the accumulator
-    if constexpr (kPacked)
-      first_row = p.dq_acc + ((long long)zkv * p.sh.T_q + sBlock[kTokQ]) * p.sh.group * D;
     int nh = 0;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     bool ok = true;
@@ -1085,20 +968,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
         reg_after_wait(v1);
         tc_fence_before_sync();
         mbar_arrive(&dq_free[h]);            // the columns may be overwritten
-        // rows of the half that exist (those past R, or a packed tile's past its
-        // sequence's end, are skipped), and their accumulators
-        int rows;
-        float* acc;
-        if constexpr (kPacked) {
-          const int group = p.sh.group;
-          rows = min(q_len - r0, p.sh.positions) * group - 64 * h;
-          acc = first_row + ((long long)r0 * group + 64 * h) * D;
-        } else {
-          rows = p.R - (r0 + 64 * h);
-          acc = p.dq_acc + ((size_t)zkv * p.Rp + r0 + 64 * h) * D;
-        }
+        const int q0 = r0 + 64 * h;
         if constexpr (D == 128) {
-          float* dst = acc + d;
+          const int rows = p.R - q0;           // rows past R are padding: skipped
+          float* dst = p.dq_acc + ((size_t)zkv * p.Rp + q0) * D + d;
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (j < rows) red_add_f32(dst + (size_t)j * D, u2f_b(v0[j]));
@@ -1116,8 +989,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
           fence_proxy_async_smem();            // the bulk copy reads through the async proxy
           named_barrier_sync(1, 128);
           if (threadIdx.x == 12 * 32) {
+            const int rows = min(64, p.R - q0);  // rows past R are padding: skipped
             if (rows > 0)
-              bulk_reduce_add_f32(acc, smem_u32(stg), (uint32_t)min(rows, 64) * D * 4);
+              bulk_reduce_add_f32(p.dq_acc + ((size_t)zkv * p.Rp + q0) * D, smem_u32(stg),
+                                  (uint32_t)rows * D * 4);
             tma_store_commit();                // one group per half, possibly empty
           }
           ++nh;
@@ -1133,29 +1008,610 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
   tc_fence_after_sync();
   if (warp == 8) tmem_dealloc(tmem, C::kTmemCols);
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
-  if constexpr (kPacked) {
-    // the last of the block's parts adds them up
-    const int parts = sBlock[kParts], slot = sBlock[kSlot], n_keys = sBlock[kNKeys];
-    if (parts > 1 && !*sAbort &&
-        last_of_parts(p.sh.key_counters + (size_t)slot * p.H_kv + zkv, parts,
-                      reinterpret_cast<volatile int*>(smem + C::kOffMiscKV + 8))) {
-      const size_t step = (size_t)p.H_kv * 2 * kRows * (D / 4);
-#pragma unroll 1
-      for (int which = 0; which < 2; ++which) {
-        const float4* first = reinterpret_cast<const float4*>(
-            p.sh.key_parts + (((size_t)slot * p.H_kv + zkv) * 2 + which) * kRows * D);
-#pragma unroll 1
-        for (int i = threadIdx.x; i < ((n_keys + 7) & ~7) * (D / 8); i += blockDim.x) {
-          int r, c;
-          join_item<D>(i, r, c);
-          if (r >= n_keys) continue;
-          float x[8];
-          sum_parts(x, first + 2 * c * kRows + r, kRows, step, parts, [](int) { return 1.f; });
-          const long long tok = sBlock[kTokK] + r;
-          uint16_t* dst = which ? static_cast<uint16_t*>(p.dk) + tok * p.dk_st + zkv * p.dk_sh
-                                : static_cast<uint16_t*>(p.dv) + tok * p.dv_st + zkv * p.dv_sh;
-          store_bf16x8(dst + c * 8, x, which ? p.scale : 1.f);
+}
+
+// ---------------------------------------------------------------- dK, dV, packed
+
+// One work item of the kernel below: a block of keys and a K/V head.
+struct PackedWork {
+  int valid;
+  int n_keys, head, tok_k;               // keys of the block, K/V head, first key token
+  int tok_q, q_len, vec0, shift;         // as in PackedKeys, of the block
+  int first, n_work, tiles;              // its query tiles
+  int part, slot, parts;
+  int unused[2];
+};
+
+// The blocks of a group come one K/V head after the other; any entry of the group says
+// what the group is, so one load is enough.
+__device__ __forceinline__ PackedWork packed_work(const PackedBwdParams& p, int entries, int idx) {
+  PackedWork x;
+  const int at = idx / p.H_kv;
+  x.valid = at < entries;
+  if (!x.valid) return x;
+  const int4* src = reinterpret_cast<const int4*>(p.sh.keys + at);
+  const int4 a = src[0], b = src[1], c = src[2], d = src[3];   // in PackedKeys' order
+  const int size = b.z;
+  const int in_group = idx - (at - b.w) * p.H_kv;              // (head, block)
+  x.head = in_group / size;
+  const int t = in_group - x.head * size;
+  x.tok_k = a.x + t * kRows;
+  x.n_keys = min(a.y - t * kRows, kRows);
+  x.tok_q = a.z;
+  x.q_len = a.w;
+  x.vec0 = b.x;
+  x.shift = b.y + t * kRows;
+  x.tiles = c.x;
+  x.part = c.y;
+  x.slot = c.z;
+  x.parts = c.w;
+  if (c.w > 1) {
+    x.first = d.x;
+    x.n_work = d.y;
+  } else if (p.causal) {
+    x.first = min(packed_over(max(x.shift, 0), p.sh.over_positions), x.tiles);
+    x.n_work = x.tiles - x.first;
+  } else {   // each block begins elsewhere, so that those that run at once add to different rows
+    x.first = x.tiles > 0 ? (d.x + t) % x.tiles : 0;
+    x.n_work = x.tiles;
+  }
+  return x;
+}
+
+// attn_bwd_dkdv_kernel over packed sequences, persistent: with short sequences a block of
+// keys has a few query tiles only, and a thread block of its own for each spent most of
+// its time starting and ending (16 x 16 heads of 64, queries of 20 to 1000 tokens over
+// keys of 64 to 2304: 77 us).  The producer warp takes the next work from a counter
+// (the costliest come first), tells the other roles what it is in one of two slots of
+// shared memory, and loads ahead as far as the ring and the K and V buffers allow, while
+// the work before is finished and its dK and dV are written.  The roles, the products and
+// their hand-offs are attn_bwd_dkdv_kernel's, their phases counted on from work to work;
+// beside them
+//   kv_free    the work's products have read K and V (shared memory)
+//   acc_free   dV and dK have been read out of tensor memory
+//   work_full, work_empty [slot]
+// Which thread block does which work differs from run to run; no result depends on it.
+template <int D, bool kFuse>
+__global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
+    packed_bwd_dkdv_kernel(const __grid_constant__ PackedBwdParams p) {
+  using C = BwdCfg<D>;
+  extern __shared__ uint8_t smem_raw_b[];
+  uint8_t* smem = align_smem_1024(smem_raw_b);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBarKV);
+  uint64_t* kv_full = bars;
+  uint64_t* q_full = bars + 1;
+  uint64_t* q_empty = q_full + C::kQStages;
+  uint64_t* sp_full = q_empty + C::kQStages;
+  uint64_t* ps_ready = sp_full + 2;
+  uint64_t* acc_done = sp_full + 4;
+  uint64_t* drain = sp_full + 5;
+  uint64_t* kt_ready = sp_full + 6;
+  uint64_t* dq_full = sp_full + 7;
+  uint64_t* dq_free = sp_full + 9;
+  uint64_t* ds_free = sp_full + 11;
+  uint64_t* kv_free = sp_full + 12;
+  uint64_t* acc_free = sp_full + 13;
+  uint64_t* work_full = sp_full + 14;
+  uint64_t* work_empty = sp_full + 16;
+  uint8_t* sDsT = smem + C::kOffDsT;
+  uint32_t* sTmemBase = reinterpret_cast<uint32_t*>(smem + C::kOffMiscKV);
+  volatile int* sAbort = reinterpret_cast<volatile int*>(smem + C::kOffMiscKV + 4);
+  volatile int* sFlag = reinterpret_cast<volatile int*>(smem + C::kOffMiscKV + 8);
+  volatile int* sNumParts = reinterpret_cast<volatile int*>(smem + C::kOffMiscKV + 12);
+  PackedWork* sWork = reinterpret_cast<PackedWork*>(smem + C::kOffWorkKV);
+  int* sParts = reinterpret_cast<int*>(smem + C::kOffWorkKV + 2 * sizeof(PackedWork));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint64_t budget = p.timeout_ns;
+  const int group = p.sh.group, positions = p.sh.positions;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < C::kQStages; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sp_full[h], 1);
+      mbar_init(&ps_ready[h], 2 * 128);
+      mbar_init(&dq_full[h], 1);
+      mbar_init(&dq_free[h], 128);
+      mbar_init(&work_full[h], 1);
+      mbar_init(&work_empty[h], 9 + (kFuse ? 4 : 0));   // warps 0-8, 12-15
+    }
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    mbar_init(kt_ready, 2 * 128);
+    mbar_init(ds_free, 1);
+    mbar_init(kv_free, 1);
+    mbar_init(acc_free, 2 * 128);
+    *sAbort = 0;
+    *sNumParts = 0;
+    fence_mbar_init();
+  }
+  // the spare rows of the Q and dO tiles, which no copy writes
+  if (group * positions < kRows && warp < 2 * C::kQStages)
+    clear_rows<D>(smem + C::kOffQRing + (warp >> 1) * C::kQStageBytes + (warp & 1) * C::kTileBytes,
+                  group * positions);
+  if (warp == 8) {
+    tmem_alloc(sTmemBase, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *sTmemBase;
+  wait_for_earlier();
+  uint8_t* sK = smem + C::kOffK;
+  uint8_t* sV = smem + C::kOffV;
+  auto stage_q = [&](int s) { return smem + C::kOffQRing + s * C::kQStageBytes; };
+  auto stage_do = [&](int s) { return stage_q(s) + C::kTileBytes; };
+  auto stage_lse = [&](int s) {
+    return reinterpret_cast<float*>(stage_q(s) + 2 * C::kTileBytes);
+  };
+  auto stage_delta = [&](int s) {
+    return reinterpret_cast<float*>(stage_q(s) + 2 * C::kTileBytes + C::kVecBytes);
+  };
+  // the w-th work of this CTA, once it is known; nullptr behind the last (or when a wait
+  // ran out)
+  auto work_at = [&](int w) -> const PackedWork* {
+    if (!warp_wait_b(&work_full[w & 1], (w >> 1) & 1, sAbort, budget)) return nullptr;
+    const PackedWork* x = sWork + (w & 1);
+    return x->valid ? x : nullptr;
+  };
+  auto work_done = [&](int w) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&work_empty[w & 1]);
+  };
+  // first query position of the n-th tile of a work
+  auto tile_r0 = [&](int first, int tiles, int n) {
+    const int t = first + n;
+    return (t < tiles ? t : t - tiles) * positions;
+  };
+
+  if (warp < 8) {
+    // -------------------------------------------------------- elementwise
+    const int wg = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;          // key row within the block
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    int item = 0;                                  // query tiles so far
+    uint32_t wk = 0;                               // works with any so far
+    bool ok = true;
+    for (int w = 0; ok; ++w) {
+      const PackedWork* x = work_at(w);
+      if (!x) break;
+      const int n_work = x->n_work, n_keys = x->n_keys;
+      if constexpr (C::kKVinTmem) {
+        // K (warpgroup 0) and V (warpgroup 1) into tensor memory; the products of the work
+        // before, which read them there, are done (acc_done below)
+        if (n_work > 0) {
+          ok = warp_wait_b(kv_full, wk & 1, sAbort, budget);
+          if (!ok) break;
+          copy_tile_to_tmem<D>(wg == 0 ? sK : sV,
+                               tmem + lane_base + (wg == 0 ? C::kTmKt : C::kTmVt), r);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          mbar_arrive(kt_ready);
         }
+      }
+      const int first = x->first, tiles = x->tiles, q_len = x->q_len, shift = x->shift;
+      for (int n = 0; n < n_work && ok; ++n, ++item) {
+        const int r0 = tile_r0(first, tiles, n);
+        const int s = item % C::kQStages;
+        // the tile's rows that see this thread's key; no masking where every row sees
+        // every key
+        int row_lo = 0, row_hi = min(q_len - r0, positions) * group;
+        const bool masked =
+            row_hi < kRows || n_keys < kRows || (p.causal && r0 < shift + kRows - 1);
+        if (p.causal) row_lo = min(max(r + shift - r0, 0), kRows) * group;
+        if (r >= n_keys) row_hi = 0;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!warp_wait_b(&sp_full[h], item & 1, sAbort, budget)) { ok = false; break; }
+          if (h == 0 && !warp_wait_b(&q_full[s], (item / C::kQStages) & 1, sAbort, budget)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const int col0 = 64 * h + 32 * wg;
+          const uint32_t cS = 128 * h + 32 * wg;
+          uint32_t sv[32], dp[32];
+          tmem_ld_x32(tmem + lane_base + cS, sv);
+          tmem_ld_x32(tmem + lane_base + cS + 64, dp);
+          const float4* lse4 = reinterpret_cast<const float4*>(stage_lse(s) + col0);
+          const float4* dl4 = reinterpret_cast<const float4*>(stage_delta(s) + col0);
+          tmem_ld_wait();
+          reg_after_wait(sv);
+          reg_after_wait(dp);
+          uint32_t pk[16], dk[16];
+          auto body = [&](auto masked_tag) {
+            constexpr bool kMasked = decltype(masked_tag)::value;
+#pragma unroll
+            for (int i4 = 0; i4 < 8; ++i4) {
+              const float4 l4 = lse4[i4];              // -LSE * log2(e) of 4 queries
+              const float4 d4 = dl4[i4];               // -D of the same queries
+              const int c = 4 * i4;
+              float e[4];
+              f2_unpack(f2_fma(f2_pack(u2f_b(sv[c]), u2f_b(sv[c + 1])), sl2x2,
+                               f2_pack(l4.x, l4.y)), e[0], e[1]);
+              f2_unpack(f2_fma(f2_pack(u2f_b(sv[c + 2]), u2f_b(sv[c + 3])), sl2x2,
+                               f2_pack(l4.z, l4.w)), e[2], e[3]);
+              bool sees[4];
+              float pr[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                sees[i] = !kMasked || (col0 + c + i >= row_lo && col0 + c + i < row_hi);
+                pr[i] = sees[i] ? ex2_approx(e[i]) : 0.f;
+              }
+              // dS = P (dP - D)
+              float ds[4];
+              f2_unpack(f2_mul(f2_pack(pr[0], pr[1]),
+                               f2_add(f2_pack(u2f_b(dp[c]), u2f_b(dp[c + 1])),
+                                      f2_pack(d4.x, d4.y))), ds[0], ds[1]);
+              f2_unpack(f2_mul(f2_pack(pr[2], pr[3]),
+                               f2_add(f2_pack(u2f_b(dp[c + 2]), u2f_b(dp[c + 3])),
+                                      f2_pack(d4.z, d4.w))), ds[2], ds[3]);
+              // (what a masked dP or D holds may be another sequence's infinity)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) ds[i] = sees[i] ? ds[i] : 0.f;
+              pk[2 * i4] = pack_bf16x2(pr[0], pr[1]);
+              pk[2 * i4 + 1] = pack_bf16x2(pr[2], pr[3]);
+              dk[2 * i4] = pack_bf16x2(ds[0], ds[1]);
+              dk[2 * i4 + 1] = pack_bf16x2(ds[2], ds[3]);
+            }
+          };
+          if (masked)
+            body(std::true_type{});
+          else
+            body(std::false_type{});
+          // P^T over its S^T columns; dS^T into the shared buffer (kFuse) and next to P^T, or
+          // over the dP^T columns
+          tmem_st_x16(tmem + lane_base + cS, pk);
+          if constexpr (kFuse) {
+            const int nh = 2 * item + h;
+            if (nh > 0 && !warp_wait_b(ds_free, (nh - 1) & 1, sAbort, budget)) {
+              ok = false;
+              break;
+            }
+            const uint32_t row = smem_u32(sDsT) + (uint32_t)r * 128u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              st_shared_v4(row + 16u * (uint32_t)((4 * wg + j) ^ (r & 7)), dk[4 * j], dk[4 * j + 1],
+                           dk[4 * j + 2], dk[4 * j + 3]);
+            fence_proxy_async_smem();
+            tmem_st_x16(tmem + lane_base + cS + 16, dk);
+          } else {
+            tmem_st_x16(tmem + lane_base + cS + 64, dk);
+          }
+          tmem_st_wait();
+          tc_fence_before_sync();
+          mbar_arrive(&ps_ready[h]);
+        }
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- dV and dK
+      // warpgroup wg writes columns [D/2 wg, D/2 (wg + 1)) of dV and dK
+      if (n_work > 0) {
+        if (!warp_wait_b(acc_done, wk & 1, sAbort, budget)) break;
+        tc_fence_after_sync();
+      }
+      const int parts = x->parts, head = x->head;
+      const long long tok = x->tok_k + r;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {  // 0: dV, 1: dK
+        const uint32_t acc = tmem + lane_base + (which ? C::kTmAcc1 : C::kTmAcc0) + (D / 2) * wg;
+        uint16_t* dst = which ? static_cast<uint16_t*>(p.dk) + tok * p.dk_st + head * p.dk_sh
+                              : static_cast<uint16_t*>(p.dv) + tok * p.dv_st + head * p.dv_sh;
+        float4* f4 = reinterpret_cast<float4*>(
+                         p.sh.key_parts +
+                         (((size_t)(x->slot + x->part) * p.H_kv + head) * 2 + which) * kRows * D) +
+                     (D / 8) * wg * kRows + r;
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t v[32];
+          if (n_work > 0) {
+            tmem_ld_x32(acc + ch * 32, v);
+            tmem_ld_wait();
+            reg_after_wait(v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;  // no query sees these keys
+          }
+          if (which == 1 && ch == D / 64 - 1 && n_work > 0) {
+            tc_fence_before_sync();
+            mbar_arrive(acc_free);
+          }
+          if (parts > 1) {
+#pragma unroll
+            for (int qd = 0; qd < 8; ++qd)
+              f4[(ch * 8 + qd) * kRows] =
+                  make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
+                              u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
+          } else if (r < n_keys) {
+            const float mult = which ? p.scale : 1.f;
+            uint4* d4 = reinterpret_cast<uint4*>(dst + (D / 2) * wg + ch * 32);
+#pragma unroll
+            for (int qd = 0; qd < 4; ++qd) {
+              uint4 val;
+              val.x = pack_bf16x2(u2f_b(v[qd * 8 + 0]) * mult, u2f_b(v[qd * 8 + 1]) * mult);
+              val.y = pack_bf16x2(u2f_b(v[qd * 8 + 2]) * mult, u2f_b(v[qd * 8 + 3]) * mult);
+              val.z = pack_bf16x2(u2f_b(v[qd * 8 + 4]) * mult, u2f_b(v[qd * 8 + 5]) * mult);
+              val.w = pack_bf16x2(u2f_b(v[qd * 8 + 6]) * mult, u2f_b(v[qd * 8 + 7]) * mult);
+              d4[qd] = val;
+            }
+          }
+        }
+      }
+      if (threadIdx.x == 0 && parts > 1) {   // for the end, when the CTA's threads join them
+        sParts[*sNumParts] = x->unused[0];
+        *sNumParts = *sNumParts + 1;
+      }
+      if (n_work > 0) ++wk;
+      work_done(w);
+    }
+  } else if (warp == 8) {
+    // -------------------------------------------------------- tensor-core issuer
+    const bool leader = elect_one();
+    const uint64_t dK = kmajor_tile_desc(smem_u32(sK));
+    const uint64_t dV = kmajor_tile_desc(smem_u32(sV));
+    const uint32_t tS = tmem, tDP = tmem + 64;
+    const uint32_t tdV = tmem + C::kTmAcc0, tdK = tmem + C::kTmAcc1;
+    int item = 0;
+    uint32_t wk = 0;
+    bool ok = true;
+    for (int w = 0; ok; ++w) {
+      const PackedWork* x = work_at(w);
+      if (!x) break;
+      const int n_work = x->n_work, n_keys = x->n_keys;
+      const int first = x->first, tiles = x->tiles, q_len = x->q_len;
+      work_done(w);
+      if (n_work == 0) continue;
+      ok = warp_wait_b(C::kKVinTmem ? kt_ready : kv_full, wk & 1, sAbort, budget);
+      if (!ok) break;
+      tc_fence_after_sync();
+      // What the copies brought from behind the sequence's end, cleared (K for dQ^T = K^T
+      // dS^T; a query tile for dV += P^T dO and dK += dS^T Q)
+      if (kFuse && n_keys < kRows) clear_rows<D>(sK, n_keys);
+      // Q and dO of the work's n-th tile, once they are there
+      auto take_tile = [&](int n) {
+        const int s = (item + n) % C::kQStages;
+        if (!warp_wait_b(&q_full[s], ((item + n) / C::kQStages) & 1, sAbort, budget)) return false;
+        tc_fence_after_sync();
+        const int rows = (q_len - tile_r0(first, tiles, n)) * group;
+        if (rows < group * positions) {
+          clear_rows<D>(stage_q(s), rows);
+          clear_rows<D>(stage_do(s), rows);
+        }
+        return true;
+      };
+      // S^T and dP^T of half h of it, over that half's dQ^T of the tile before once it has been
+      // read out
+      auto issue_sp = [&](int n, int h) {
+        const int i = item + n, s = i % C::kQStages;
+        if constexpr (kFuse) {
+          if (i > 0 && !warp_wait_b(&dq_free[h], (i - 1) & 1, sAbort, budget)) return false;
+          tc_fence_after_sync();
+        }
+        if (leader) {
+          if constexpr (C::kKVinTmem) {
+            issue_qk_half_ts<D>(tS + 128 * h, tmem + C::kTmKt, kmajor_tile_desc(smem_u32(stage_q(s))), h);
+            issue_qk_half_ts<D>(tDP + 128 * h, tmem + C::kTmVt, kmajor_tile_desc(smem_u32(stage_do(s))), h);
+          } else {
+            issue_qk_half<D>(tS + 128 * h, dK, kmajor_tile_desc(smem_u32(stage_q(s))), h);
+            issue_qk_half<D>(tDP + 128 * h, dV, kmajor_tile_desc(smem_u32(stage_do(s))), h);
+          }
+          tc_commit(&sp_full[h]);
+        }
+        return true;
+      };
+      ok = take_tile(0) && issue_sp(0, 0) && issue_sp(0, 1);
+      for (int n = 0; n < n_work && ok; ++n) {
+        const int i = item + n, s = i % C::kQStages;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!warp_wait_b(&ps_ready[h], i & 1, sAbort, budget)) { ok = false; break; }
+          // the first products overwrite the dV and dK of the work before
+          if (n == 0 && h == 0 && wk > 0 && !warp_wait_b(acc_free, (wk - 1) & 1, sAbort, budget)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          if (leader) {
+            if constexpr (kFuse) {
+              issue_dqt_half<D>(tDP + 128 * h, mnmajor_tile_desc<D>(smem_u32(sK)),
+                                mnmajor_tile_desc<64>(smem_u32(sDsT)));
+              tc_commit(&dq_full[h]);
+              tc_commit(ds_free);
+            }
+            issue_pv_half<D>(tdV, tS + 128 * h, mnmajor_tile_desc<D>(smem_u32(stage_do(s))), h,
+                             n > 0 || h > 0);
+            issue_pv_half<D>(tdK, kFuse ? tS + 128 * h + 16 : tDP + 128 * h,
+                             mnmajor_tile_desc<D>(smem_u32(stage_q(s))), h, n > 0 || h > 0);
+            if (h == 1) tc_commit(&q_empty[s]);
+          }
+          if (n + 1 < n_work && ((h == 0 && !take_tile(n + 1)) || !issue_sp(n + 1, h))) {
+            ok = false;
+            break;
+          }
+        }
+      }
+      if (!ok) break;
+      if (leader) {
+        tc_commit(acc_done);
+        tc_commit(kv_free);
+      }
+      item += n_work;
+      ++wk;
+    }
+    if (leader) {
+      tc_commit(drain);
+      drain_wait_b(drain, 0, budget);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // -------------------------------------------------------- producer
+    const bool leader = elect_one();
+    const uint64_t pol_kv = l2_policy_evict_first();
+    const uint64_t pol_q = l2_policy_evict_last();
+    const int entries = p.sh.head->key_blocks;
+    int issued = 0;
+    uint32_t wk = 0;
+    int idx = (int)blockIdx.x;
+    bool ok = true;
+    for (int w = 0; ok; ++w) {
+      PackedWork x = packed_work(p, entries, idx);
+      if (w >= 2 && !warp_wait_b(&work_empty[w & 1], ((w >> 1) - 1) & 1, sAbort, budget)) break;
+      x.unused[0] = idx;
+      if (lane == 0) {
+        sWork[w & 1] = x;
+        mbar_arrive(&work_full[w & 1]);
+      }
+      __syncwarp();
+      if (!x.valid) break;
+      if (x.n_work > 0) {
+        if (wk > 0 && !warp_wait_b(kv_free, (wk - 1) & 1, sAbort, budget)) break;
+        if (leader) {
+          mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
+          tma_load_tile<D>(sK, &p.tm_k, kv_full, x.head, x.tok_k, pol_kv);
+          tma_load_tile<D>(sV, &p.tm_v, kv_full, x.head, x.tok_k, pol_kv);
+        }
+        ++wk;
+        for (int n = 0; n < x.n_work; ++n) {
+          const int s = issued % C::kQStages, round = issued / C::kQStages;
+          if (round > 0 && !warp_wait_b(&q_empty[s], (round - 1) & 1, sAbort, budget)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const int r0 = tile_r0(x.first, x.tiles, n), tok = x.tok_q + r0;
+            mbar_arrive_expect_tx(&q_full[s],
+                                  (uint32_t)(2 * group * positions * D * 2) + 2 * C::kVecBytes);
+            tma_load_tile<D>(stage_q(s), &p.tm_q, &q_full[s], x.head * group, tok, pol_q);
+            tma_load_tile<D>(stage_do(s), &p.tm_do, &q_full[s], x.head * group, tok, pol_q);
+            const size_t vo =
+                (size_t)(x.head * p.vec_stride + (long long)(x.vec0 + r0) * group);
+            bulk_load(stage_lse(s), p.nlse2 + vo, C::kVecBytes, &q_full[s]);
+            bulk_load(stage_delta(s), p.ndelta + vo, C::kVecBytes, &q_full[s]);
+          }
+          ++issued;
+        }
+      }
+      // (asked for late, when this work's last tiles are under way: works taken sooner would
+      // be bound to a CTA that is long busy)
+      if (lane == 0) idx = (int)gridDim.x + atomicAdd(p.sh.next, 1);
+      idx = __shfl_sync(kAll, idx, 0);
+    }
+    if (leader) {
+      if (wk > 0) drain_wait_b(kv_full, (wk - 1) & 1, budget);
+      const int from = issued > C::kQStages ? issued - C::kQStages : 0;
+      for (int t = from; t < issued; ++t)
+        drain_wait_b(&q_full[t % C::kQStages], (t / C::kQStages) & 1, budget);
+    }
+    __syncwarp();
+  } else if (kFuse && warp >= 12) {
+    // -------------------------------------------------------- dQ read-out
+    const bool has_d = (D == 128) || lane < 16;
+    const int d = (D == 128) ? (warp & 3) * 32 + lane : (warp & 3) * 16 + (lane & 15);
+    float* sStage = reinterpret_cast<float*>(smem + C::kOffDqStage);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    int item = 0, nh = 0;
+    bool ok = true;
+    for (int w = 0; ok; ++w) {
+      const PackedWork* x = work_at(w);
+      if constexpr (D == 64) {   // (the four warps meet at barriers below: they leave together)
+        if (barrier_or(1, 128, !x)) break;
+      } else {
+        if (!x) break;
+      }
+      const int n_work = x->n_work, first = x->first, tiles = x->tiles, q_len = x->q_len;
+      // the sequence's first row in the accumulator
+      float* rows0 = p.dq_acc + ((long long)x->head * p.sh.T_q + x->tok_q) * group * D;
+      work_done(w);
+      for (int n = 0; n < n_work && ok; ++n, ++item) {
+        const int r0 = tile_r0(first, tiles, n);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (D == 64) {
+            if (threadIdx.x == 12 * 32) tma_store_wait_read<1>();
+          }
+          const bool got = warp_wait_b(&dq_full[h], item & 1, sAbort, budget);
+          if constexpr (D == 64) {
+            if (barrier_or(1, 128, !got)) { ok = false; break; }
+          } else {
+            if (!got) { ok = false; break; }
+          }
+          tc_fence_after_sync();
+          uint32_t v0[32], v1[32];
+          tmem_ld_x32(tmem + lane_base + 128 * h + 64, v0);
+          tmem_ld_x32(tmem + lane_base + 128 * h + 96, v1);
+          tmem_ld_wait();
+          reg_after_wait(v0);
+          reg_after_wait(v1);
+          tc_fence_before_sync();
+          mbar_arrive(&dq_free[h]);
+          // rows of the half that exist, and their accumulators
+          const int rows = min(q_len - r0, positions) * group - 64 * h;
+          float* acc = rows0 + ((long long)r0 * group + 64 * h) * D;
+          if constexpr (D == 128) {
+            float* dst = acc + d;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < rows) red_add_f32(dst + (size_t)j * D, u2f_b(v0[j]));
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 + j < rows) red_add_f32(dst + (size_t)(32 + j) * D, u2f_b(v1[j]));
+          } else {
+            float* stg = sStage + (nh & 1) * 64 * D;
+            if (has_d) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) stg[j * D + d] = u2f_b(v0[j]);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) stg[(32 + j) * D + d] = u2f_b(v1[j]);
+            }
+            fence_proxy_async_smem();
+            named_barrier_sync(1, 128);
+            if (threadIdx.x == 12 * 32) {
+              if (rows > 0)
+                bulk_reduce_add_f32(acc, smem_u32(stg), (uint32_t)min(rows, 64) * D * 4);
+              tma_store_commit();
+            }
+            ++nh;
+          }
+        }
+      }
+    }
+    if (D == 64 && threadIdx.x == 12 * 32) tma_store_wait_all();
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 8) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
+  if (*sAbort) return;
+  // the last of a block's parts adds them up
+  for (int i = 0, n = *sNumParts, entries = p.sh.head->key_blocks; i < n; ++i) {
+    const PackedWork x = packed_work(p, entries, sParts[i]);
+    if (!last_of_parts(p.sh.key_counters + (size_t)x.slot * p.H_kv + x.head, x.parts, sFlag))
+      continue;
+    const size_t step = (size_t)p.H_kv * 2 * kRows * (D / 4);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const float4* from = reinterpret_cast<const float4*>(
+          p.sh.key_parts + (((size_t)x.slot * p.H_kv + x.head) * 2 + which) * kRows * D);
+#pragma unroll 1
+      for (int j = threadIdx.x; j < ((x.n_keys + 7) & ~7) * (D / 8); j += blockDim.x) {
+        int r, c;
+        join_item<D>(j, r, c);
+        if (r >= x.n_keys) continue;
+        float sum[8];
+        sum_parts(sum, from + 2 * c * kRows + r, kRows, step, x.parts, [](int) { return 1.f; });
+        const long long tok = x.tok_k + r;
+        uint16_t* dst = which ? static_cast<uint16_t*>(p.dk) + tok * p.dk_st + x.head * p.dk_sh
+                              : static_cast<uint16_t*>(p.dv) + tok * p.dv_st + x.head * p.dv_sh;
+        store_bf16x8(dst + c * 8, sum, which ? p.scale : 1.f);
       }
     }
   }
@@ -1639,9 +2095,9 @@ cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const v
     std::lock_guard<std::mutex> lk(g_bwd_mu);
     if (!attr_set[dev]) {
       constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-      if ((err = cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, false, true>, kAttr, C::kSmemKV)) !=
+      if ((err = cudaFuncSetAttribute(packed_bwd_dkdv_kernel<D, false>, kAttr, C::kSmemKV)) !=
               cudaSuccess ||
-          (err = cudaFuncSetAttribute(attn_bwd_dkdv_kernel<D, true, true>, kAttr, C::kSmemKV)) !=
+          (err = cudaFuncSetAttribute(packed_bwd_dkdv_kernel<D, true>, kAttr, C::kSmemKV)) !=
               cudaSuccess ||
           (err = cudaFuncSetAttribute(attn_bwd_dq_kernel<D, true>, kAttr, C::kSmemQ)) != cudaSuccess)
         return err;
@@ -1662,15 +2118,21 @@ cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const v
   err = cudaLaunchKernelEx(&cfg, packed_bwd_prep_kernel<D>, p, static_cast<const uint16_t*>(o),
                            static_cast<const uint16_t*>(dout), lse);
   if (err != cudaSuccess) return err;
-  const dim3 grid_kv((unsigned)key_room * (unsigned)p.H_kv);
+  // persistent: one CTA per SM
+  int sms = 0;
+  if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return err;
+  const long long works = (long long)key_room * p.H_kv;
+  const dim3 grid_kv((unsigned)(works < sms ? works : sms));
   if (p.dq_acc != nullptr) {
-    err = launch_ahead(attn_bwd_dkdv_kernel<D, true, true>, grid_kv, kThreadsFused, C::kSmemKV,
+    err = launch_ahead(packed_bwd_dkdv_kernel<D, true>, grid_kv, kThreadsFused, C::kSmemKV,
                        stream, p);
     if (err != cudaSuccess) return err;
-    return launch_ahead(packed_bwd_dq_convert_kernel<D>, dim3((unsigned)((rows * (D / 8) + 255) / 256)),
-                        256, 0, stream, p);
+    const long long per_head = (long long)p.sh.T_q * p.sh.group * (D / 8);
+    return launch_ahead(packed_bwd_dq_convert_kernel<D>,
+                        dim3((unsigned)((per_head + 255) / 256), (unsigned)p.H_kv), 256, 0, stream, p);
   }
-  err = launch_ahead(attn_bwd_dkdv_kernel<D, false, true>, grid_kv, kThreadsB, C::kSmemKV, stream, p);
+  err = launch_ahead(packed_bwd_dkdv_kernel<D, false>, grid_kv, kThreadsB, C::kSmemKV, stream, p);
   if (err != cudaSuccess) return err;
   return launch_ahead(attn_bwd_dq_kernel<D, true>,
                       dim3((unsigned)tile_room * 2u * (unsigned)p.H_kv), kThreadsB, C::kSmemQ, stream,

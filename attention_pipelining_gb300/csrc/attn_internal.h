@@ -271,7 +271,8 @@ struct PackedHeader {
   int tiles, key_blocks;              // entries of the two lists
   int q_first, q_end;                 // tokens that belong to a sequence
   int cut;                            // whether any tile was cut
-  int unused[59];
+  int next;                           // next of the backward's key blocks and K/V heads
+  int unused[58];
 };
 
 struct PackedPlan {
@@ -334,6 +335,7 @@ struct PackedShape {
   int group;           // R
   int positions;       // query tokens of a 128-row tile
   unsigned long long over_positions;   // as in PackedPlan
+  unsigned long long over_group, over_group64;   // ceil(2^40 / R) and ceil(2^64 / R), R > 1
   int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
   int T_q;
   int o_box;           // whether 32 rows of a tile are a box of O (attn_fwd_packed)
@@ -342,6 +344,7 @@ struct PackedShape {
   float* tile_parts;
   float* tile_lse;
   float* key_parts;
+  int* next;           // the header's
   int* tile_counters;  // [slot, K/V head] (in the backward, of each half) parts that are done
   int* key_counters;
 };

@@ -49,7 +49,7 @@ attn_status_t check_sizes(const attn_packed_t* s) {
   if ((s->causal != 0 && s->causal != 1) || !std::isfinite(s->scale)) return ATTN_ERR_INVALID_ARG;
   if (s->D != 64 && s->D != 128) return ATTN_ERR_UNSUPPORTED;
   const int positions = tile_positions(s->H_q / s->H_kv);
-  if (positions == 0 || s->B > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (positions == 0 || s->B > 65535 || s->H_kv > 65535) return ATTN_ERR_UNSUPPORTED;
   // tokens and what is counted of them stay within ints
   if (s->T_q >= (1 << 30) || s->T_k >= (1 << 30)) return ATTN_ERR_UNSUPPORTED;
   if (packed_tile_room(s->T_q, s->B, positions, s->H_kv) * 2 * s->H_kv >= INT_MAX ||
@@ -140,6 +140,8 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   plan->keys = reinterpret_cast<PackedKeys*>(at(l.keys));
   plan->group_at = reinterpret_cast<int*>(at(l.group_at));
   shape->over_positions = plan->over_positions;
+  shape->over_group = ((1ull << 40) + group - 1) / group;
+  shape->over_group64 = ~0ull / (unsigned)group + 1;
   plan->counters[0] = reinterpret_cast<int*>(at(l.tile_counters));
   plan->counters[1] = reinterpret_cast<int*>(at(l.key_counters));
   plan->n_counters = l.slots * s.H_kv * kPackedCounters;
@@ -149,6 +151,7 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   shape->tile_counters = plan->counters[0];
   shape->key_counters = plan->counters[1];
   shape->head = plan->head;
+  shape->next = &plan->head->next;
   shape->tiles = plan->tiles;
   shape->keys = plan->keys;
   shape->group = group;

@@ -42,7 +42,7 @@ typedef struct {
 } attn_thd_t;
 
 /* The sizes of a packed attention.  H_q a multiple of H_kv; H_q / H_kv at most
- * 32, or a multiple of 4 up to 128; D 64 or 128; B at most 65535. */
+ * 32, or a multiple of 4 up to 128; D 64 or 128; B and H_kv at most 65535. */
 typedef struct {
   int B, T_q, T_k;  /* sequences, tokens of the tensors */
   int H_q, H_kv, D;

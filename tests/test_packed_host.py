@@ -53,7 +53,7 @@ def rope(lib, q=True, qo=True, k=True, ko=True, positions=A, sections=(16, 24, 2
 
 BAD_SIZES = [(dict(B=0), 1), (dict(T_q=0), 1), (dict(T_k=-1), 1), (dict(H_q=0), 1), (dict(H_kv=0), 1),
              (dict(H_q=9), 1), (dict(D=0), 1), (dict(causal=2), 1), (dict(scale=math.nan), 1),
-             (dict(scale=math.inf), 1), (dict(D=96), 2), (dict(B=70000), 2), (dict(H_q=33, H_kv=1), 2),
+             (dict(scale=math.inf), 1), (dict(D=96), 2), (dict(B=70000), 2), (dict(H_q=70000, H_kv=70000), 2), (dict(H_q=33, H_kv=1), 2),
              (dict(H_q=132, H_kv=1), 2), (dict(H_q=127, H_kv=1), 2), (dict(T_q=1 << 30), 2),
              (dict(T_k=1 << 30), 2), (dict(T_k=(1 << 30) - 1, H_q=60000, H_kv=60000), 2),
              (dict(T_q=(1 << 30) - 1, H_q=128, H_kv=128), 2)]
