@@ -46,7 +46,8 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_status_string", "attn_device_statu
            "attn_bwd_host", "chunk_scan_fwd", "chunk_scan_fwd_host",
            "attn_kv_append", "attn_kv_read", "attn_fwd_paged", "attn_paged_workspace_bytes",
            "attn_fwd_paged_timeout_test", "attn_rope_packed", "attn_fwd_packed", "attn_bwd_packed",
-           "attn_packed_workspace_bytes", "attn_packed_bwd_workspace_bytes"]
+           "attn_packed_workspace_bytes", "attn_packed_bwd_workspace_bytes",
+           "attn_fwd_packed_timeout_test", "attn_bwd_packed_timeout_test"]
 
 
 class AttnError(RuntimeError):
@@ -140,6 +141,11 @@ def _load():
     lib.attn_fwd_packed.restype = ci
     lib.attn_bwd_packed.argtypes = [vp] * 13 + [ctypes.c_size_t, ci, vp]
     lib.attn_bwd_packed.restype = ci
+    lib.attn_fwd_packed_timeout_test.argtypes = [vp] * 9 + [ctypes.c_size_t, ci, ctypes.c_ulonglong, vp]
+    lib.attn_fwd_packed_timeout_test.restype = ci
+    lib.attn_bwd_packed_timeout_test.argtypes = [vp] * 13 + [ctypes.c_size_t, ci, ci, ctypes.c_ulonglong,
+                                                           vp]
+    lib.attn_bwd_packed_timeout_test.restype = ci
     lib.attn_packed_workspace_bytes.argtypes = [vp]
     lib.attn_packed_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_packed_bwd_workspace_bytes.argtypes = [vp, ci]

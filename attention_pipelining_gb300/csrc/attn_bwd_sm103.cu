@@ -1287,7 +1287,7 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
           }
           tmem_st_wait();
           tc_fence_before_sync();
-          mbar_arrive(&ps_ready[h]);
+          if (!(wg == 0 && h == 0 && item == p.fault_drop_item)) mbar_arrive(&ps_ready[h]);
         }
       }
       if (!ok) break;

@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         stamp(tr, t ? kEvSm1Done : kEvSm0Done, j);
         bool signal = true;
-        if constexpr (kTrace) signal = !(t == 0 && j == p.fault_drop_block);
+        if constexpr (kTrace || kPacked) signal = !(t == 0 && j == p.fault_drop_block);
         if (signal) mbar_arrive(&p_full[t]);
         m_run = m_use;
       }

@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "attn_internal.h"
+#include "attn_testing.h"
 
 namespace attnpipe {
 namespace {
@@ -170,26 +171,11 @@ bool map_keys(CUtensorMap* map, const Thd& t, const attn_packed_t& s) {
 
 attn_status_t done(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
-}  // namespace
-}  // namespace attnpipe
-
-using namespace attnpipe;
-
-extern "C" {
-
-size_t attn_packed_workspace_bytes(const attn_packed_t* s) {
-  return check_sizes(s) == ATTN_OK ? layout_of(*s, false, false).end : 0;
-}
-
-size_t attn_packed_bwd_workspace_bytes(const attn_packed_t* s, int deterministic) {
-  if (check_sizes(s) != ATTN_OK || (deterministic != 0 && deterministic != 1)) return 0;
-  return layout_of(*s, true, deterministic != 0).end;
-}
-
-attn_status_t attn_fwd_packed(const attn_packed_t* s, const attn_thd_t* q, const attn_thd_t* k,
-                              const attn_thd_t* v, const attn_thd_t* o, float* lse,
-                              const int* cu_q, const int* cu_k, void* workspace,
-                              size_t workspace_bytes, attn_stream_t stream) {
+attn_status_t fwd_impl(const attn_packed_t* s, const attn_thd_t* q, const attn_thd_t* k,
+                       const attn_thd_t* v, const attn_thd_t* o, float* lse,
+                       const int* cu_q, const int* cu_k, void* workspace,
+                       size_t workspace_bytes, attn_stream_t stream, int drop_block = -1,
+                       unsigned long long timeout_ns = kDefaultTimeoutNs) {
   attn_status_t st = check_sizes(s);
   if (st != ATTN_OK) return st;
   Thd tq, tk, tv, to;
@@ -226,20 +212,21 @@ attn_status_t attn_fwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
   // (a negative scale runs as -Q K^T times |scale|, as in attn_fwd)
   p.neg_scores = std::signbit(s->scale) ? 1 : 0;
   p.scale_log2 = scale_log2_of(std::fabs(s->scale));
-  p.timeout_ns = kDefaultTimeoutNs;
-  p.fault_drop_block = -1;
+  p.timeout_ns = timeout_ns;
+  p.fault_drop_block = drop_block;
   p.num_tiles = (int)(packed_tile_room(s->T_q, s->B, p.sh.positions, s->H_kv) * s->H_kv);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_packed_plan(plan, cs);
   return done(e != cudaSuccess ? e : launch_attn_fwd_packed(p, s->D, cs));
 }
 
-attn_status_t attn_bwd_packed(const attn_packed_t* s, const attn_thd_t* q, const attn_thd_t* k,
-                              const attn_thd_t* v, const attn_thd_t* o, const float* lse,
-                              const attn_thd_t* dout, const attn_thd_t* dq, const attn_thd_t* dk,
-                              const attn_thd_t* dv, const int* cu_q, const int* cu_k,
-                              void* workspace, size_t workspace_bytes, int deterministic,
-                              attn_stream_t stream) {
+attn_status_t bwd_impl(const attn_packed_t* s, const attn_thd_t* q, const attn_thd_t* k,
+                       const attn_thd_t* v, const attn_thd_t* o, const float* lse,
+                       const attn_thd_t* dout, const attn_thd_t* dq, const attn_thd_t* dk,
+                       const attn_thd_t* dv, const int* cu_q, const int* cu_k,
+                       void* workspace, size_t workspace_bytes, int deterministic,
+                       attn_stream_t stream, int drop_item = -1,
+                       unsigned long long timeout_ns = kDefaultTimeoutNs) {
   attn_status_t st = check_sizes(s);
   if (st != ATTN_OK) return st;
   if (deterministic != 0 && deterministic != 1) return ATTN_ERR_INVALID_ARG;
@@ -285,8 +272,8 @@ attn_status_t attn_bwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
   p.causal = s->causal;
   p.scale = s->scale;
   p.scale_log2 = scale_log2_of(s->scale);
-  p.timeout_ns = kDefaultTimeoutNs;
-  p.fault_drop_item = -1;
+  p.timeout_ns = timeout_ns;
+  p.fault_drop_item = drop_item;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_packed_plan(plan, cs);
   return done(e != cudaSuccess
@@ -294,6 +281,64 @@ attn_status_t attn_bwd_packed(const attn_packed_t* s, const attn_thd_t* q, const
                   : launch_attn_bwd_packed(p, s->D, to.data, tdo.data, lse,
                                            (int)packed_tile_room(s->T_q, s->B, p.sh.positions, s->H_kv),
                                            (int)packed_key_room(s->T_k, s->B, s->H_kv), cs));
+}
+
+}  // namespace
+}  // namespace attnpipe
+
+using namespace attnpipe;
+
+extern "C" {
+
+size_t attn_packed_workspace_bytes(const attn_packed_t* s) {
+  return check_sizes(s) == ATTN_OK ? layout_of(*s, false, false).end : 0;
+}
+
+size_t attn_packed_bwd_workspace_bytes(const attn_packed_t* s, int deterministic) {
+  if (check_sizes(s) != ATTN_OK || (deterministic != 0 && deterministic != 1)) return 0;
+  return layout_of(*s, true, deterministic != 0).end;
+}
+
+attn_status_t attn_fwd_packed(const attn_packed_t* s, const attn_thd_t* q, const attn_thd_t* k,
+                              const attn_thd_t* v, const attn_thd_t* o, float* lse,
+                              const int* cu_q, const int* cu_k, void* workspace,
+                              size_t workspace_bytes, attn_stream_t stream) {
+  return fwd_impl(s, q, k, v, o, lse, cu_q, cu_k, workspace, workspace_bytes, stream);
+}
+
+attn_status_t attn_bwd_packed(const attn_packed_t* s, const attn_thd_t* q, const attn_thd_t* k,
+                              const attn_thd_t* v, const attn_thd_t* o, const float* lse,
+                              const attn_thd_t* dout, const attn_thd_t* dq, const attn_thd_t* dk,
+                              const attn_thd_t* dv, const int* cu_q, const int* cu_k,
+                              void* workspace, size_t workspace_bytes, int deterministic,
+                              attn_stream_t stream) {
+  return bwd_impl(s, q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, workspace, workspace_bytes,
+                  deterministic, stream);
+}
+
+attn_status_t attn_fwd_packed_timeout_test(const attn_packed_t* s, const attn_thd_t* q,
+                                           const attn_thd_t* k, const attn_thd_t* v,
+                                           const attn_thd_t* o, float* lse, const int* cu_q,
+                                           const int* cu_k, void* workspace,
+                                           size_t workspace_bytes, int drop_block,
+                                           unsigned long long wait_budget_ns,
+                                           attn_stream_t stream) {
+  if (drop_block < 0 || wait_budget_ns < 1000000ull || wait_budget_ns > kDefaultTimeoutNs)
+    return ATTN_ERR_INVALID_ARG;
+  return fwd_impl(s, q, k, v, o, lse, cu_q, cu_k, workspace, workspace_bytes, stream, drop_block,
+                  wait_budget_ns);
+}
+
+attn_status_t attn_bwd_packed_timeout_test(
+    const attn_packed_t* s, const attn_thd_t* q, const attn_thd_t* k, const attn_thd_t* v,
+    const attn_thd_t* o, const float* lse, const attn_thd_t* dout, const attn_thd_t* dq,
+    const attn_thd_t* dk, const attn_thd_t* dv, const int* cu_q, const int* cu_k, void* workspace,
+    size_t workspace_bytes, int deterministic, int drop_item, unsigned long long wait_budget_ns,
+    attn_stream_t stream) {
+  if (drop_item < 0 || wait_budget_ns < 1000000ull || wait_budget_ns > kDefaultTimeoutNs)
+    return ATTN_ERR_INVALID_ARG;
+  return bwd_impl(s, q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, workspace, workspace_bytes,
+                  deterministic, stream, drop_item, wait_budget_ns);
 }
 
 attn_status_t attn_rope_packed(const attn_thd_t* q, const attn_thd_t* q_out, const attn_thd_t* k,

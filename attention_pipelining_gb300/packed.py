@@ -135,7 +135,7 @@ def _given(workspace, dev):
 
 
 def attn_fwd_packed(q, k, v, cu_q, causal: bool, scale: float, cu_k=None, workspace=None, out=None,
-                    stream=None):
+                    stream=None, _fault=None):
     """Attention of every sequence over its own keys; returns (o [T_q, H_q, D] bf16, lse [H_q, T_q]
     float32).  With ``causal`` the queries are the newest of the sequence's tokens: of n queries and m
     keys query i sees keys j <= i + m - n.  ``workspace``: optional uint8 tensor of at least
@@ -157,8 +157,12 @@ def attn_fwd_packed(q, k, v, cu_q, causal: bool, scale: float, cu_k=None, worksp
         os, lse_p = _like("out[0]", o, q_shape, dev), _flat("out[1]", lse, lse_shape, _f32, dev)
         ws, n = _given(workspace, dev) if workspace is not None else (_alloc(nbytes, handle), nbytes)
         try:
-            _check(_load().attn_fwd_packed(sizes, qs, ks, vs, os, lse_p, cq, ck, ws, n, handle),
-                   "attn_fwd_packed")
+            args = (sizes, qs, ks, vs, os, lse_p, cq, ck, ws, n)
+            if _fault is None:
+                _check(_load().attn_fwd_packed(*args, handle), "attn_fwd_packed")
+            else:
+                _check(_load().attn_fwd_packed_timeout_test(*args, *_fault, handle),
+                       "attn_fwd_packed_timeout_test")
         finally:   # (used again only by what follows on the stream)
             if workspace is None:
                 _free(ws)
@@ -168,7 +172,7 @@ def attn_fwd_packed(q, k, v, cu_q, causal: bool, scale: float, cu_k=None, worksp
 
 
 def attn_bwd_packed(q, k, v, o, lse, dout, cu_q, causal: bool, scale: float, cu_k=None, workspace=None,
-                    out=None, deterministic: bool = False, stream=None):
+                    out=None, deterministic: bool = False, stream=None, _fault=None):
     """Gradients (dq, dk, dv) of attn_fwd_packed's q, k and v for the gradient ``dout`` of its o, given
     its o and lse.  ``workspace``: optional uint8 tensor of at least packed_bwd_workspace_bytes(...)
     bytes, not shared with calls that may run at the same time (allocated if None); ``out``: optional
@@ -190,14 +194,29 @@ def attn_bwd_packed(q, k, v, o, lse, dout, cu_q, causal: bool, scale: float, cu_
         dvs = _like("out[2]", dv, k_shape, dev)
         ws, n = _given(workspace, dev) if workspace is not None else (_alloc(nbytes, handle), nbytes)
         try:
-            _check(_load().attn_bwd_packed(sizes, qs, ks, vs, os, lse_p, dos, dqs, dks, dvs, cq, ck, ws, n, det,
-                                           handle), "attn_bwd_packed")
+            args = (sizes, qs, ks, vs, os, lse_p, dos, dqs, dks, dvs, cq, ck, ws, n, det)
+            if _fault is None:
+                _check(_load().attn_bwd_packed(*args, handle), "attn_bwd_packed")
+            else:
+                _check(_load().attn_bwd_packed_timeout_test(*args, *_fault, handle),
+                       "attn_bwd_packed_timeout_test")
         finally:
             if workspace is None:
                 _free(ws)
         return dq, dk, dv
 
     return paged._on(dev, stream, call)
+
+
+def fwd_packed_timeout_test(*args, drop_block: int, wait_budget_ns: int = 20_000_000, **kw):
+    """Test hook: attn_fwd_packed with one "P stored" signal withheld, so that the kernel's bounded
+    wait for it runs out (see attn_testing.h).  The device status word then reads ATTN_ERR_TIMEOUT."""
+    return attn_fwd_packed(*args, _fault=(int(drop_block), int(wait_budget_ns)), **kw)
+
+
+def bwd_packed_timeout_test(*args, drop_item: int, wait_budget_ns: int = 20_000_000, **kw):
+    """Test hook: attn_bwd_packed likewise, in its dK/dV kernel."""
+    return attn_bwd_packed(*args, _fault=(int(drop_item), int(wait_budget_ns)), **kw)
 
 
 @functools.lru_cache(maxsize=256)

@@ -47,6 +47,16 @@
  * are in.  Outputs are unspecified.  `drop_stage` must be >= 0 and `wait_budget_ns` in
  * [1 ms, 2 s] (else ATTN_ERR_INVALID_ARG).  For tests only.
  *
+ * attn_fwd_packed_timeout_test and attn_bwd_packed_timeout_test run attn_fwd_packed and
+ * attn_bwd_packed (attn_packed.h; same arguments and buffers) with one signal
+ * withheld: the forward's first softmax warpgroup does not report its probabilities of
+ * block `drop_block` of each of its tiles that has one, and the dK/dV kernel's first
+ * elementwise warpgroup not those of half 0 of the `drop_item`-th query tile that
+ * each thread block gets to (both counted from 0), so that the issuer's wait for them runs
+ * out after `wait_budget_ns`, and all roles unwind.  Outputs are unspecified.  Limits of
+ * `wait_budget_ns` as above; the other number must be >= 0 (else ATTN_ERR_INVALID_ARG).
+ * For tests only.
+ *
  * attn_fwd_tail_pairs returns how many tiles attn_fwd splits across CTA
  * pairs for these sizes on the current device (0 when the tail is not
  * split), or -1 for invalid sizes or a device that cannot be queried.
@@ -56,6 +66,7 @@
 #define ATTN_GB300_TESTING_H
 
 #include "attn.h"
+#include "attn_packed.h"
 #include "attn_paged.h"
 
 #ifdef __cplusplus
@@ -86,6 +97,21 @@ attn_status_t attn_fwd_paged_timeout_test(const attn_kv_cache_t *cache, const at
                                           float scale, int drop_stage,
                                           unsigned long long wait_budget_ns,
                                           attn_stream_t stream);
+
+attn_status_t attn_fwd_packed_timeout_test(const attn_packed_t *sizes, const attn_thd_t *q,
+                                           const attn_thd_t *k, const attn_thd_t *v,
+                                           const attn_thd_t *o, float *lse, const int *cu_q,
+                                           const int *cu_k, void *workspace,
+                                           size_t workspace_bytes, int drop_block,
+                                           unsigned long long wait_budget_ns,
+                                           attn_stream_t stream);
+
+attn_status_t attn_bwd_packed_timeout_test(
+    const attn_packed_t *sizes, const attn_thd_t *q, const attn_thd_t *k, const attn_thd_t *v,
+    const attn_thd_t *o, const float *lse, const attn_thd_t *dout, const attn_thd_t *dq,
+    const attn_thd_t *dk, const attn_thd_t *dv, const int *cu_q, const int *cu_k, void *workspace,
+    size_t workspace_bytes, int deterministic, int drop_item, unsigned long long wait_budget_ns,
+    attn_stream_t stream);
 
 int attn_fwd_tail_pairs(int B, int H_q, int H_kv, int S_q, int S_kv, int D, int causal);
 

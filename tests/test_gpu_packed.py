@@ -415,6 +415,101 @@ def test_tokens_beyond_32_bit_offsets():
     assert torch.equal(a[at:], c) and torch.equal(b[at:], d)
 
 
+CUT = [
+    # H_q, H_kv, D, lens_q, lens_k, causal: tiles of long sequences, and the key blocks that few
+    # tiles see, are cut into parts (of 8 and of 4 blocks at least) where there are few
+    (8, 2, 128, [3, 1], [5000, 40], True),
+    (4, 4, 64, [1, 130, 0], [9000, 2100, 3000], True),
+    (8, 1, 128, [1500], None, True),
+    (5, 1, 64, [700, 20], None, True),
+    (2, 1, 128, [260], [1700], False),
+    (4, 2, 64, [1100, 1], [1300, 700], False),
+    (16, 1, 64, [40], [8200], True),
+    (1, 1, 128, [2], [70000], False),      # as many parts as there may be
+    (1, 1, 64, [70000], [2], False),
+]
+
+
+@pytest.mark.parametrize("case", CUT, ids=[f"{c[0]}_{c[1]}_{c[2]}_{c[3][0]}" for c in CUT])
+def test_work_cut_into_parts(case):
+    """Against the reference, and bit for bit the same each time, whichever part comes last."""
+    H_q, H_kv, D, lens_q, lens_k, causal = case
+    q, k, v, do, cu_q, cu_k = make(H_q, H_kv, D, lens_q, lens_k, lead=1, pad=70, seed=11)
+    scale = D ** -0.5
+    o, lse = forward(q, k, v, cu_q, cu_k, causal, scale)
+    check_forward(q, k, v, cu_q, cu_k, causal, scale, (o, lse))
+    first = None
+    for det in (True, False, True):
+        got = backward(q, k, v, o, lse, do, cu_q, cu_k, causal, scale, deterministic=det)
+        check_backward(q, k, v, o, lse, do, cu_q, cu_k, causal, scale, got, det)
+        first = first or [t.clone() for t in got]
+        for x, y in zip(first if det else first[1:], got if det else got[1:]):
+            assert torch.equal(x, y)
+    for _ in range(3):
+        for x, y in zip(forward(q, k, v, cu_q, cu_k, causal, scale), (o, lse)):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("B", [31, 32, 1023, 1024, 2047, 2048, 5000])
+def test_any_number_of_sequences(B):
+    """Around the numbers at which the plan changes its way of going through them."""
+    lens_q = [(3 * i) % 5 for i in range(B)]
+    lens_k = [(7 * i) % 4 + (i % 97 == 0) * 50 for i in range(B)]
+    for lk in (None, lens_k):
+        q, k, v, do, cu_q, cu_k = make(1, 1, 64, lens_q, lk, pad=3)
+        o, lse = forward(q, k, v, cu_q, cu_k, False, 0.125)
+        check_forward(q, k, v, cu_q, cu_k, False, 0.125, (o, lse))
+        got = backward(q, k, v, o, lse, do, cu_q, cu_k, False, 0.125)
+        check_backward(q, k, v, o, lse, do, cu_q, cu_k, False, 0.125, got)
+
+
+def test_more_tiles_than_thread_blocks_keep():
+    """The forward's thread blocks keep 64 tiles each: with more, there are more of them.  The same
+    heads in two calls are the reference."""
+    H, D, lens = 128, 64, [5 + i % 3 for i in range(100)]
+    q, k, v, do, cu, _ = make(H, H, D, lens)
+    o, lse = forward(q, k, v, cu, cu, True, 0.125)
+    g = backward(q, k, v, o, lse, do, cu, cu, True, 0.125)
+    for h in (slice(0, 64), slice(64, 128)):
+        a = forward(q[:, h], k[:, h], v[:, h], cu, cu, True, 0.125)
+        assert torch.equal(o[:, h], a[0]) and torch.equal(lse[h], a[1])
+        b = backward(q[:, h], k[:, h], v[:, h], o[:, h], lse[h].contiguous(), do[:, h], cu, cu, True, 0.125)
+        for x, y in zip(g[1:], b[1:]):
+            assert torch.equal(x[:, h], y)
+
+
+def test_tensors_that_only_the_call_holds():
+    """Bounds and positions made in the call's own argument list live as long as the call needs them,
+    whatever memory it allocates itself."""
+    q, k, v, do, cu, _ = make(2, 1, 64, [(5 * i) % 9 for i in range(600)])
+    o, lse = forward(q, k, v, cu, cu, True, 0.125)
+    for _ in range(20):
+        a, b = ap.attn_fwd_packed(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), True, 0.125,
+                                  cu_k=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
+@pytest.mark.parametrize("D,H_q,H_kv", [(128, 4, 1), (64, 2, 2)])
+@pytest.mark.parametrize("what", ["forward", "backward", "deterministic"])
+def test_a_wait_that_runs_out(D, H_q, H_kv, what):
+    """A signal withheld: every role unwinds, the status word says so, and the next call works."""
+    from attention_pipelining_gb300 import packed
+    q, k, v, do, cu, _ = make(H_q, H_kv, D, [300, 700, 40])
+    o, lse = forward(q, k, v, cu, cu, True, 0.1)
+    c = ints(cu)
+    if what == "forward":
+        packed.fwd_packed_timeout_test(q, k, v, c, True, 0.1, drop_block=1)
+    else:
+        packed.bwd_packed_timeout_test(q, k, v, o, lse, do, c, True, 0.1, drop_item=2,
+                                       deterministic=what == "deterministic")
+    torch.cuda.synchronize()
+    assert ap.device_status(reset=True) == 5
+    a = forward(q, k, v, cu, cu, True, 0.1)
+    assert torch.equal(a[0], o) and torch.equal(a[1], lse)
+    got = backward(q, k, v, o, lse, do, cu, cu, True, 0.1)
+    check_backward(q, k, v, o, lse, do, cu, cu, True, 0.1, got)
+
+
 # ---------------------------------------------------------------- rotation
 
 ROPE = [

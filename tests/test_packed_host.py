@@ -103,6 +103,13 @@ def test_attention_refuses(lib, kw, code):
     assert bwd(lib, **kw) == code
 
 
+@pytest.mark.parametrize("drop,budget", [(-1, 10**7), (0, 999_999), (0, 2**63)])
+def test_timeout_hooks_refuse(lib, drop, budget):
+    t = [thd() for _ in range(8)]
+    assert lib.attn_fwd_packed_timeout_test(sizes(), *t[:4], A, A, A, A, BIG, drop, budget, None) == 1
+    assert lib.attn_bwd_packed_timeout_test(sizes(), *t[:4], A, *t[4:], A, A, A, BIG, 0, drop, budget, None) == 1
+
+
 def test_more_refusals(lib):
     assert bwd(lib, det=2) == 1
     assert fwd(lib, sizes(T_k=200), cu_k=None) == 1        # other keys, without their bounds
