@@ -37,14 +37,15 @@
 // Every wait is bounded; a timeout raises a CTA-wide abort flag and the
 // device status word records ATTN_ERR_TIMEOUT.
 //
-// Packed sequences (the kPacked instantiations, include/attn_packed.h): both paths
-// over lists of key blocks and query tiles of all sequences that a plan kernel made.
-// A query tile's 128 rows are whole groups of query heads of consecutive tokens
-// (row = token * R + head); the row vectors and the accumulator follow that order,
-// [K/V head][token * R + head], so a tile's rows of them are contiguous.  Behind a
-// sequence's end the copies bring other sequences' rows: where these would meet a
-// zero of P or dS in a sum over rows or keys (0 times an infinity is a NaN) the
-// issuer warp clears them in shared memory first.
+// Packed sequences (include/attn_packed.h): both paths over lists of key blocks and query
+// tiles of all sequences that a plan kernel made: packed_bwd_prep_kernel, the persistent
+// packed_bwd_dkdv_kernel, and packed_bwd_dq_convert_kernel or attn_bwd_dq_kernel's kPacked
+// instantiation.  A query tile's 128 rows are whole groups of query heads of
+// consecutive tokens (row = token * R + head); the row vectors and the accumulator follow
+// that order, [K/V head][token * R + head], so a tile's rows of them are contiguous.
+// Behind a sequence's end the copies bring other sequences' rows: where these would meet
+// a zero of P or dS in a sum over rows or keys (0 times an infinity is a NaN) the issuer
+// warp clears them in shared memory first.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>

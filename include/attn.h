@@ -278,10 +278,10 @@ const char *attn_status_string(attn_status_t status);
 
 /*
  * Reads the device-side status words of the current device (forward,
- * backward, self-test and paged-cache kernels): ATTN_OK, ATTN_ERR_TIMEOUT if a
+ * backward, self-test, paged-cache and packed-sequence kernels): ATTN_OK, ATTN_ERR_TIMEOUT if a
  * launch since the last reset gave up on a wait (that launch's outputs are then
- * unspecified), or ATTN_ERR_BAD_INDEX if a paged-cache kernel met an index out
- * of range (attn_paged.h says what it did with it) and none gave up.  Synchronises
+ * unspecified), or ATTN_ERR_BAD_INDEX if a kernel of the paged cache or of packed sequences met an
+ * index out of range (attn_paged.h and attn_packed.h say what it did with it) and none gave up.  Synchronises
  * the device.  With reset != 0 the words are cleared afterwards.
  */
 attn_status_t attn_device_status(int *status_out, int reset);

@@ -41,7 +41,7 @@ typedef struct {
   int64_t stride_t, stride_h;
 } attn_thd_t;
 
-/* The sizes of a packed attention.  H_q a multiple of H_kv; H_q / H_kv at most
+/* The sizes of a packed attention, each at least 1.  H_q a multiple of H_kv; H_q / H_kv at most
  * 32, or a multiple of 4 up to 128; D 64 or 128; B and H_kv at most 65535. */
 typedef struct {
   int B, T_q, T_k;  /* sequences, tokens of the tensors */
@@ -75,14 +75,15 @@ typedef struct {
  *
  * A first kernel lists the tiles of all sequences, the longest first; the
  * attention kernel (attn_fwd's, over tiles of 256 rows that hold whole groups of
- * query heads) takes them on a persistent grid of one thread block per SM.  The
- * results are deterministic.  Many queries keep the GPU busy; a few queries over
- * long contexts are attn_fwd_paged's and attn_fwd_splitkv's work, which split
- * the keys.
+ * query heads) takes them on a persistent grid of one thread block per SM.  Where
+ * there are few of them, the keys of long ones are cut into parts, which the thread
+ * block that ends last joins.  The results are deterministic.
  *
  * Arithmetic as attn_fwd's: fp32 accumulation and softmax statistics, the
  * probabilities rounded to bf16 (2^-8) before the second product, whose
- * rounded values are also what O is divided by.  An infinity or a NaN in a
+ * rounded values are also what O is divided by.  A row's exponentials are taken
+ * against a maximum that may lag by 2^8, so sums stay finite while |v| times the
+ * sequence's keys stays below 2^119.  An infinity or a NaN in a
  * sequence may reach any row of that sequence, masked places included, but of
  * no other sequence.
  */
@@ -96,7 +97,7 @@ attn_status_t attn_fwd_packed(const attn_packed_t *sizes, const attn_thd_t *q,
 size_t attn_packed_workspace_bytes(const attn_packed_t *sizes);
 
 /*
- * Gradients of attn_fwd_packed: given its inputs, its o and lse, and the
+ * Gradients of attn_fwd_packed (its sizes, bounds and workspace rules): given its inputs, its o and lse, and the
  * gradient dout of o,
  *
  *     P_ij = exp(s_ij - lse_i),  dS_ij = P_ij (dout_i . v_j - dout_i . o_i)
@@ -105,12 +106,14 @@ size_t attn_packed_workspace_bytes(const attn_packed_t *sizes);
  *
  *   q, k, v, o, lse, dout   read
  *   dq         [T_q, H_q, D], written; dk, dv [T_k, H_kv, D], written; queries
- *              that see no key and keys that no query sees get zeros
+ *              that see no key and keys that no query sees get zeros; they must not
+ *              overlap an input or one another
  *   deterministic  0: dq is added up in fp32 in the workspace by atomic
  *              additions, whose order (and so dq's last bit) may differ from run
  *              to run; 1: by a kernel of its own, reproducible bit for bit
  *
- * Rounded to bf16: P and dS before their products, and the results.
+ * dk and dv are reproducible in any case.  Rounded to bf16: P and dS before their
+ * products, and the results.
  */
 attn_status_t attn_bwd_packed(const attn_packed_t *sizes, const attn_thd_t *q,
                               const attn_thd_t *k, const attn_thd_t *v, const attn_thd_t *o,
