@@ -77,11 +77,13 @@
 #include "attn_internal.h"
 #include "attn_tiles.cuh"
 #include "kv_cache.cuh"
+#include "packed_plan.cuh"
 #include "ptx.cuh"
 
 namespace attnpipe {
 
 __device__ int g_attn_status = 0;
+__device__ int g_attn_index_status = 0;   // packed sequences: bounds that were not in order
 
 namespace {
 
@@ -500,15 +502,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int4* kept = reinterpret_cast<const int4*>(smem + C::kOffTiles);
   if constexpr (kPacked) {
     wait_for_earlier();
-    // one tile a round, if any in the last (the launch sees to it that there is room)
-    const int n_tiles = p.sh.head->tiles * p.H_kv;
-    const int G = (int)gridDim.x, rounds = n_tiles / G, left = n_tiles - rounds * G;
-    my_tiles = min(rounds + (((rounds & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x) < left),
-                   C::kCachedTiles);
-    Tile tl;
-    if ((int)threadIdx.x < my_tiles && packed_tile(p, n_tiles, threadIdx.x, tl))
-      keep_tile(reinterpret_cast<int4*>(smem + C::kOffTiles) + threadIdx.x * 4, tl);
-    __syncthreads();
+    if (p.sh.head == nullptr) {
+      // Few tiles, each with a CTA of its own, and none to cut: no plan, the first warp finds
+      // the CTA's tile (a prompt of 100 tokens, 32 heads over 8 of 128: 8.6 us; with a plan
+      // before it 11.9).
+      if (warp == 0) {
+        int2 first;
+        if (warp_bounds(p.cu_q, p.cu_k, p.B, p.sh.T_q, p.sh.T_k, first))
+          g_attn_index_status = ATTN_ERR_BAD_INDEX;
+        int queries = __shfl_down_sync(kFull, first.x, 1) - first.x;
+        int keys = __shfl_down_sync(kFull, first.y, 1) - first.y;
+        if (lane >= p.B) queries = keys = 0;
+        const int tiles = (queries + 2 * p.sh.positions - 1) / (2 * p.sh.positions);
+        const int end =
+            scan_warp(make_int2(tiles, 0), [](int a, int b) { return a + b; }).x;
+        const int item = (int)blockIdx.x / p.H_kv;
+        if (item >= end - tiles && item < end) {   // (one lane, or none)
+          const PackedTile x =
+              packed_tile_at(lane, first.x, queries, first.y, keys,
+                             (item - (end - tiles)) * 2 * p.sh.positions, p.sh.positions, p.causal);
+          Tile tl;
+          tl.tok0 = x.tok0, tl.rows = x.rows, tl.k0 = x.k0, tl.k_len = x.k_len;
+          tl.n_keys = x.n_keys, tl.diag = x.diag, tl.jb = 0, tl.n_blocks = x.n_blocks;
+          tl.parts = 1, tl.part = 0, tl.slot = 0;
+          tl.zkv = (int)blockIdx.x - item * p.H_kv;
+          keep_tile(reinterpret_cast<int4*>(smem + C::kOffTiles), tl);
+        }
+        const int all = __shfl_sync(kFull, end, 31);
+        if (lane == 0) *reinterpret_cast<int*>(smem + C::kOffMisc + 8) = item < all ? 1 : 0;
+      }
+      __syncthreads();
+      my_tiles = *reinterpret_cast<int*>(smem + C::kOffMisc + 8);
+    } else {
+      // one tile a round, if any in the last (the launch sees to it that there is room)
+      const int n_tiles = p.sh.head->tiles * p.H_kv;
+      const int G = (int)gridDim.x, rounds = n_tiles / G, left = n_tiles - rounds * G;
+      my_tiles = min(rounds + (((rounds & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x) < left),
+                     C::kCachedTiles);
+      Tile tl;
+      if ((int)threadIdx.x < my_tiles && packed_tile(p, n_tiles, threadIdx.x, tl))
+        keep_tile(reinterpret_cast<int4*>(smem + C::kOffTiles) + threadIdx.x * 4, tl);
+      __syncthreads();
+    }
   }
   // the k-th tile of this CTA; false when there is none
   auto tile_at = [&](int k, Tile& tl) -> bool {
@@ -1421,7 +1456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPacked) {
     // The last of a tile's parts joins them, the whole block at once (with the registers
     // that it was launched with), when it has done all its tiles.
-    if (p.sh.head->cut && !*sAbort) {
+    if (p.sh.head != nullptr && p.sh.head->cut && !*sAbort) {
       if (wg < 2)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(65536 / kThreads) : "memory");
       else
@@ -1591,10 +1626,11 @@ cudaError_t launch_packed_d(const PackedFwdParams& p, cudaStream_t stream) {
   }
   if (p.num_tiles <= 0 || sms <= 0) return cudaErrorInvalidValue;
   // persistent, as launch_d's, and as many times over as it takes for every CTA to keep its
-  // tiles in shared memory
+  // tiles in shared memory; a CTA to a tile where there is no plan
   const long long kept = (long long)sms * Cfg<D>::kCachedTiles;
-  const long long grid =
-      p.num_tiles < sms ? p.num_tiles : (p.num_tiles + kept - 1) / kept * sms;
+  const long long grid = p.sh.head == nullptr || p.num_tiles < sms
+                             ? p.num_tiles
+                             : (p.num_tiles + kept - 1) / kept * sms;
   return launch_ahead(attn_fwd_kernel<D, false, false, true>, dim3((unsigned)grid), kThreads,
                       Cfg<D>::kSmemBytes, stream, p);
 }
@@ -1634,11 +1670,15 @@ cudaError_t launch_attn_fwd_packed(const PackedFwdParams& p, int D, cudaStream_t
 }
 
 cudaError_t read_device_status(int* status, bool reset) {
+  int index = 0;
   cudaError_t err = cudaMemcpyFromSymbol(status, g_attn_status, sizeof(int));
+  if (err == cudaSuccess) err = cudaMemcpyFromSymbol(&index, g_attn_index_status, sizeof(int));
   if (err != cudaSuccess) return err;
+  if (*status == ATTN_OK) *status = index;   // (a timeout says more)
   if (reset) {
     const int zero = 0;
     err = cudaMemcpyToSymbol(g_attn_status, &zero, sizeof(int));
+    if (err == cudaSuccess) err = cudaMemcpyToSymbol(g_attn_index_status, &zero, sizeof(int));
   }
   return err;
 }

@@ -329,7 +329,7 @@ __host__ __device__ inline int packed_vec0(int q0, int b) {
 // What the attention kernels take beside the fields they share with attn_fwd and
 // attn_bwd (of which S_q, S_kv and the tile counts are unused).
 struct PackedShape {
-  const PackedHeader* head;
+  const PackedHeader* head;   // nullptr: no plan (see packed_without_plan)
   const PackedTile* tiles;
   const PackedKeys* keys;
   int group;           // R
@@ -337,7 +337,7 @@ struct PackedShape {
   unsigned long long over_positions;   // as in PackedPlan
   unsigned long long over_group, over_group64;   // ceil(2^40 / R) and ceil(2^64 / R), R > 1
   int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
-  int T_q;
+  int T_q, T_k;
   int o_box;           // whether 32 rows of a tile are a box of O (attn_fwd_packed)
   // parts' results, by slot and K/V head: of tiles [256 rows, D] and, in the forward,
   // their base-2 log-sum-exps [256]; of key blocks dV and dK, [2, 128 rows, D]
@@ -349,8 +349,17 @@ struct PackedShape {
   int* key_counters;
 };
 
+// Whether a forward needs no plan: its tiles run at once whatever the bounds are, none is
+// long enough to be cut, and one warp can go through the bounds.
+inline bool packed_without_plan(int B, int T_q, int T_k, int H_kv, int positions) {
+  return B < 32 && ((long long)T_q / (2 * positions) + B) * H_kv <= kPackedCtas &&
+         2 * (((long long)T_k + 127) / 128) < 3 * kPackedLeastTile;
+}
+
 struct PackedFwdParams : AttnParams {
   PackedShape sh;
+  const int* cu_q;       // (without a plan)
+  const int* cu_k;
   long long o_st, o_sh;  // strides of O (elements)
 };
 

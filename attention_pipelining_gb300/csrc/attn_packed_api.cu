@@ -159,6 +159,7 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   shape->positions = plan->positions;
   shape->inv_group = (65536 + group - 1) / group;
   shape->T_q = s.T_q;
+  shape->T_k = s.T_k;
   return ATTN_OK;
 }
 
@@ -216,6 +217,13 @@ attn_status_t fwd_impl(const attn_packed_t* s, const attn_thd_t* q, const attn_t
   p.fault_drop_block = drop_block;
   p.num_tiles = (int)(packed_tile_room(s->T_q, s->B, p.sh.positions, s->H_kv) * s->H_kv);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (packed_without_plan(s->B, s->T_q, s->T_k, s->H_kv, p.sh.positions)) {
+    p.sh.head = nullptr;
+    p.cu_q = plan.cu_q;
+    p.cu_k = plan.cu_k;
+    p.num_tiles = (int)((s->T_q / (2 * p.sh.positions) + s->B) * s->H_kv);
+    return done(launch_attn_fwd_packed(p, s->D, cs));
+  }
   const cudaError_t e = launch_packed_plan(plan, cs);
   return done(e != cudaSuccess ? e : launch_attn_fwd_packed(p, s->D, cs));
 }

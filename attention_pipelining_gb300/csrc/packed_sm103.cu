@@ -6,6 +6,7 @@
 
 #include "attn_internal.h"
 #include "kv_cache.cuh"
+#include "packed_plan.cuh"
 #include "ptx.cuh"
 #include "rotate.cuh"
 
@@ -22,18 +23,6 @@ constexpr int kBuckets = kPlanThreads;   // of costs: a thread to each
 constexpr int kPlanShared = 2048;  // sequences (and one) whose bounds fit shared memory
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// Scans of two values at once over the warp's lanes up to this one.
-template <typename Op>
-__device__ __forceinline__ int2 scan_warp(int2 v, Op op) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int off = 1; off < 32; off *= 2) {
-    const int a = __shfl_up_sync(0xffffffffu, v.x, off), b = __shfl_up_sync(0xffffffffu, v.y, off);
-    if (lane >= off) v.x = op(v.x, a), v.y = op(v.y, b);
-  }
-  return v;
-}
 
 // Scans of two values at once over the block's threads before this one (0 for the first);
 // `warps`: 32 of shared memory.
@@ -101,10 +90,8 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   };
   if (n <= 32) {   // (one warp, without the block's barriers: 1 us less)
     if (warp == 0) {
-      const int a = lane < n ? p.cu_q[lane] : 0, b = lane < n && !same ? p.cu_k[lane] : 0;
-      int2 run = scan_warp(make_int2(max(min(a, p.T_q), 0), max(min(b, p.T_k), 0)), larger);
-      if (lane < n && (a != run.x || (!same && b != run.y))) g_packed_status = ATTN_ERR_BAD_INDEX;
-      if (same) run.y = run.x;
+      int2 run;
+      if (warp_bounds(p.cu_q, p.cu_k, B, p.T_q, p.T_k, run)) g_packed_status = ATTN_ERR_BAD_INDEX;
       int queries = __shfl_down_sync(0xffffffffu, run.x, 1) - run.x;
       int keys = __shfl_down_sync(0xffffffffu, run.y, 1) - run.y;
       if (lane >= B) queries = keys = 0;
@@ -175,15 +162,8 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   };
   const auto tile_of = [&](int e, PackedTile& x) {
     const int b = sequence(0, e), len = q[b + 1] - q[b], m = k[b + 1] - k[b];
-    const int pos = (e - first[0][b]) * 2 * P;
-    x.tok0 = q[b] + pos;
-    x.rows = min(len - pos, 2 * P);
-    x.k0 = k[b];
-    x.k_len = m;
-    x.diag = m - len + pos + 1;
-    x.n_keys = p.causal ? min(max(x.diag + x.rows - 1, 0), m) : m;
-    x.vec0 = packed_vec0(q[b], b) + pos;
-    return (x.n_keys + 127) >> 7;
+    x = packed_tile_at(b, q[b], len, k[b], m, (e - first[0][b]) * 2 * P, P, p.causal);
+    return x.n_blocks;
   };
   // the first query tile that sees a key of block t of a sequence of len queries and m keys
   const auto first_tile = [&](int t, int len, int m) {

@@ -145,6 +145,29 @@ def test_forward(case):
         check_forward(q, k, v, cu_q, cu_k, causal, scale, got, (lead, pad))
 
 
+@pytest.mark.parametrize("case", [c for c in CASES if len(c[3]) < 32],
+                         ids=[i for i, c in zip(IDS, CASES) if len(c[3]) < 32])
+def test_forward_among_many_tokens(case):
+    """Few tokens take one kernel, more of them a plan before it: the same results to the bit, also for bounds
+    that are not in order."""
+    H_q, H_kv, D, lens_q, lens_k, causal, scale, kscale = case
+    pad = 256 * 152   # (a tile holds 256 positions at most, a device has 152 multiprocessors)
+    q, k, v, _, cu_q, cu_k = make(H_q, H_kv, D, lens_q, lens_k, kscale=kscale)
+    more = [torch.cat([x, x.new_full((pad, *x.shape[1:]), math.nan)]) for x in (q, k, v)]
+    few = forward(q, k, v, cu_q, cu_k, causal, scale)
+    many = forward(*more, cu_q, cu_k, causal, scale)
+    n = q.shape[0]
+    assert torch.equal(many[0][:n], few[0]) and torch.equal(many[1][:, :n], few[1])
+    if len(cu_q) > 2:
+        swapped = cu_q[:-2] + [cu_q[-1], cu_q[-2]]
+        ends = [0] + [cu_k[-1]] * (len(cu_k) - 1)
+        few = forward(q, k, v, swapped, ends, causal, scale)
+        many = forward(*more, swapped, ends, causal, scale)
+        assert torch.equal(many[0][:n], few[0]) and torch.equal(many[1][:, :n], few[1])
+        torch.cuda.synchronize()
+        assert ap.device_status(reset=True) == (BAD_INDEX if cu_q[-1] > cu_q[-2] else 0)
+
+
 @pytest.mark.parametrize("det", [False, True], ids=["atomic", "deterministic"])
 @pytest.mark.parametrize("case", CASES, ids=IDS)
 def test_backward(case, det):
