@@ -294,9 +294,11 @@ struct PackedPlan {
 };
 
 // Parts: an entry of n blocks (of keys, or of query tiles) is cut where n is one and a
-// half times `cap` or more, into round(n / cap) parts (kPackedMostParts at most), with cap the blocks of all entries
-// and K/V heads divided by kPackedCtas, or kPackedLeast... where that is more.  So there
-// are at most n / cap + 1/2 <= 4/3 n / cap parts of an entry, and 4/3 kPackedCtas of all.
+// half times `cap` or more, into round(n / cap) parts (kPackedMostParts at most), with
+// cap the blocks of all entries and K/V heads divided by kPackedCtas, or
+// kPackedLeastTile (of keys) or kPackedLeastKeys (of query tiles) where that is more.  So
+// there are at most n / cap + 1/2 <= 4/3 n / cap parts of an entry, and 4/3 kPackedCtas
+// of all.
 constexpr int kPackedCtas = 152;
 constexpr int kPackedMostParts = 64;
 constexpr int kPackedBand = 4;       // key blocks of a group

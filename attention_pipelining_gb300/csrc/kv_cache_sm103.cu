@@ -365,7 +365,7 @@ cudaError_t launch_kv_append(const KvAppendParams& p0, int D, bool int4, cudaStr
   const int rows = p.H_q + 2 * p.cache.H_kv;
   const long long blocks = ((long long)p.cache.B * p.S + slots - 1) / slots;
   // Where there are few tokens, their rows are spread over several blocks (1024
-  // blocks of tokens, 48 rows: cut in five 39 us, in three 41, in ten 45)
+  // blocks of tokens, 48 rows: cut in five 39 us, in three 41, in ten 45; an earlier build)
   const long long spread = (kAppendBlocks + blocks - 1) / blocks;
   p.rows = spread >= rows ? 1 : (int)((rows + spread - 1) / spread);
   const dim3 grid((unsigned)blocks, (unsigned)((rows + p.rows - 1) / p.rows));

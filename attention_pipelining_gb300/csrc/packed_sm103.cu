@@ -52,10 +52,11 @@ __device__ __forceinline__ int parts_of(int n, int cap) {
 // so that the costliest run first and the last to end are short.  The order among
 // equal costs and the parts' slots differ from run to run; no result depends on them.
 //
-// It stands before every call, so what counts is its latency: a thread takes an entry
-// (found by bisection over the sequences' first entries), and the bounds stay in
-// shared memory.  A warp to a sequence, with the bounds read back from global memory,
-// took 5 to 9 us, this 3 to 4.
+// It stands before every call but the shortest forwards (packed_without_plan), so what
+// counts is its latency, a chain of scans with the block's barriers between them: a
+// thread takes an entry (found by bisection over the sequences' first entries), and the
+// bounds stay in shared memory.  A warp to a sequence, with the bounds read back from
+// global memory, took 5 to 9 us, this 3 to 4.
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
   __shared__ int at[2][kBuckets];   // entries of a cost, then where the next of them goes
   __shared__ int2 warps[2][32];
@@ -237,9 +238,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   };
   // Key blocks, where none is cut, come in groups of up to kPackedBand neighbours, at the
   // first one's cost: the blocks of a group run side by side, one K/V head after the
-  // other, and share that head's queries in L2.  (In the order of their own costs, with
-  // the heads innermost, 16 x 1024 tokens took 633 us instead of 570, in groups of 16 589;
-  // 4 x 4096 1421, 1417 and 1450.)
+  // other, and share that head's queries in L2.  (The gradients of 32 heads over 8 of 128,
+  // causal, in an earlier build: 16 x 1024 tokens 570 us, in the order of the blocks' own
+  // costs, with the heads innermost, 633, in groups of 16 589; 4 x 4096 1417, 1421 and
+  // 1450.  Now 524 and 1372.)
   const bool grouped = 2 * most[1] < 3 * cap[1];
   const auto group_cost = [&](const PackedKeys& x) {   // its first block's
     return x.tiles - (p.causal ? min(positions(max(x.shift, 0)), x.tiles) : 0);
@@ -335,7 +337,8 @@ constexpr int kRopeWave = kRopeResident * 152;
 // worked on.
 //
 // Bound by HBM: 336 MB (16384 tokens of 40 heads of 128) in 57 us are 5.9 TB/s, 89 % of the
-// measured copy rate.  With what rounds exactly left out it took 55 us; with the doubtful
+// measured copy rate (9001 tokens of 32 heads of 64, adjacent pairs: 74 MB, 15.6 us, 71 %; 32
+// tokens 2.5 us, a chain of loads).  With what rounds exactly left out it took 55 us; with the doubtful
 // roundings in a function of their own, through local memory, 63; with the rows
 // loaded into registers four at a time 69.  Where a row's 16-byte pieces are paired so that one
 // load takes half of each 32-byte sector (adjacent pairs, heads of 64) 24 us became 20.
