@@ -39,8 +39,8 @@
 //
 // Packed sequences (include/attn_packed.h): both paths over lists of key blocks and query
 // tiles of all sequences that a plan kernel made: packed_bwd_prep_kernel, the persistent
-// packed_bwd_dkdv_kernel, and packed_bwd_dq_convert_kernel or attn_bwd_dq_kernel's kPacked
-// instantiation.  A query tile's 128 rows are whole groups of query heads of
+// packed_bwd_dkdv_kernel, and packed_bwd_dq_convert_kernel or the persistent
+// packed_bwd_dq_kernel.  A query tile's 128 rows are whole groups of query heads of
 // consecutive tokens (row = token * R + head); the row vectors and the accumulator follow
 // that order, [K/V head][token * R + head], so a tile's rows of them are contiguous.
 // Behind a sequence's end the copies bring other sequences' rows: where these would meet
@@ -236,9 +236,12 @@ struct BwdCfg {
   static constexpr int kOffBarQ = kOffKVRing + kKVStages * 2 * kTileBytes;
   // q_full, kv_full[S], kv_empty[S], sp_full[2], ds_ready[2], acc_done, drain,
   // qt_ready (Q and dO copied into tensor memory)
-  static constexpr int kNumBarsQ = 2 * kKVStages + 8;
+  // (and in the packed kernel work_full[2], work_empty[2])
+  static constexpr int kNumBarsQ = 2 * kKVStages + 8 + 4;
   static constexpr int kOffMiscQ = kOffBarQ + kNumBarsQ * 8;
-  static constexpr int kSmemQ = kOffMiscQ + 16 + 1024;
+  // packed sequences: two slots of 64 bytes for works, and a list of parts (of both halves)
+  static constexpr int kOffWorkQ = kOffMiscQ + 16;
+  static constexpr int kSmemQ = kOffWorkQ + 2 * 64 + 2 * kPartsKV * 4 + 1024;
   // tensor memory: S (or S^T) [0,128), dP [128,256), accumulators after;
   // the dQ kernel keeps Q and dO as A operands (D / 2 columns each) after its
   // one accumulator.  The dK/dV kernel places the two halves as slots of
@@ -287,9 +290,6 @@ __device__ __forceinline__ void banded_rank(int idx, int n_ranks, int groups, in
     rank = full * kRankBand + (rem - zkv * tail);
   }
 }
-
-template <bool kPacked>
-using BwdParamsOf = std::conditional_t<kPacked, PackedBwdParams, BwdParams>;
 
 }  // namespace
 
@@ -1632,32 +1632,8 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
 
 // ---------------------------------------------------------------- dQ
 
-// The last of the parts of a packed tile's half adds up their dQ; `first`: the rows in the
-// first part.  Whole block.
 template <int D>
-__device__ __forceinline__ void join_dq(const PackedBwdParams& p, size_t slot, int half, int parts,
-                                        int n_rows, int tok_q, int zkv, const float* first,
-                                        volatile int* flag) {
-  if (!last_of_parts(p.sh.tile_counters + slot * 2 + half, parts, flag)) return;
-  const float4* f4 = reinterpret_cast<const float4*>(first);
-#pragma unroll 1
-  for (int i = threadIdx.x; i < ((n_rows + 7) & ~7) * (D / 8); i += kThreadsB) {
-    int r, c;
-    join_item<D>(i, r, c);
-    if (r >= n_rows) continue;
-    const int at = (r * p.sh.inv_group) >> 16;
-    float x[8];
-    sum_parts(x, f4 + 2 * c * kRows + r, kRows, (size_t)p.H_kv * 256 * (D / 4), parts,
-              [](int) { return 1.f; });
-    store_bf16x8(static_cast<uint16_t*>(p.dq) + (long long)(tok_q + at) * p.dq_st +
-                     (zkv * p.sh.group + r - at * p.sh.group) * p.dq_sh + c * 8,
-                 x, p.scale);
-  }
-}
-
-template <int D, bool kPacked = false>
-__global__ void __launch_bounds__(kThreadsB, 1)
-    attn_bwd_dq_kernel(const __grid_constant__ BwdParamsOf<kPacked> p) {
+__global__ void __launch_bounds__(kThreadsB, 1) attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D>;
   extern __shared__ uint8_t smem_raw_b[];
   uint8_t* smem = align_smem_1024(smem_raw_b);
@@ -1680,85 +1656,29 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   // longest first (with S_q a multiple of 128 a rank is one position block
   // of one head of the group, so the group's heads interleave), in bands
   // (see banded_rank); without it group-major, query blocks last to first
-  //
-  // (packed: a half of a tile of the list, and a K/V head, in bands of tiles)
-  int zkv, r0 = 0, n_kb;
-  int n_rows = kRows;                                   // packed: the tile's rows that exist
-  int tok_q = 0, tok_k = 0, k_len = 0, n_keys = 0, diag = 0, vec0 = 0;   // and PackedTile's others
-  int jb = 0, parts = 1, half = 0;
-  size_t slot = 0;   // of the tile's first part and this K/V head
-  // a part's dQ (of a tile's halves 128 rows each)
-  auto dq_of = [&](int part) -> float* {
-    if constexpr (kPacked)
-      return p.sh.tile_parts + ((slot + (size_t)part * p.H_kv) * 256 + half * kRows) * D;
-    return nullptr;
-  };
-  int part = 0;
-  if constexpr (kPacked) {
-    wait_for_earlier();
-    const int entries = p.sh.head->tiles, positions = p.sh.positions;
-    half = (int)(blockIdx.x & 1);
-    if ((long long)(blockIdx.x >> 1) >= (long long)entries * p.H_kv) return;
-    int entry;
-    banded_rank((int)(blockIdx.x >> 1), entries, p.H_kv, entry, zkv);
-    const int4* src = reinterpret_cast<const int4*>(p.sh.tiles + entry);
-    const int4 a = src[0], b = src[1], c4 = src[2];   // in PackedTile's order
-    const int rows = a.y - half * positions;
-    if (rows <= 0) return;
-    n_rows = min(rows, positions) * p.sh.group;
-    tok_q = a.x + half * positions;
-    tok_k = a.z;
-    k_len = a.w;
-    diag = b.y + half * positions;
-    n_keys = p.causal ? min(max(diag + min(rows, positions) - 1, 0), k_len) : k_len;
-    vec0 = b.z + half * positions;
-    jb = b.w;
-    parts = c4.y;
-    part = c4.z;
-    slot = (size_t)c4.w * p.H_kv + zkv;
-    // (a half may see fewer keys than the tile)
-    n_kb = min((n_keys + kRows - 1) / kRows, jb + c4.x) - jb;
-    if (n_kb <= 0) {   // no row sees a key of these: dQ = 0
-      if (parts > 1) {
-        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreadsB)
-          reinterpret_cast<float4*>(dq_of(part))[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, dq_of(0),
-                   reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 8));
-        return;
-      }
-      for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreadsB) {
-        const int row = i / (D / 8), at = (row * p.sh.inv_group) >> 16;
-        uint16_t* dst = static_cast<uint16_t*>(p.dq) + (long long)(tok_q + at) * p.dq_st +
-                        (zkv * p.sh.group + row - at * p.sh.group) * p.dq_sh + i % (D / 8) * 8;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      return;
+  const int n_qb = (p.R + kRows - 1) / kRows;
+  int qb, zkv;
+  if (p.causal) {
+    int rank;
+    banded_rank((int)blockIdx.x, n_qb, p.groups, rank, zkv);
+    const int hr = p.R / p.S_q;  // heads per group
+    if (p.S_q % kRows == 0) {
+      const int nh = p.S_q / kRows;
+      qb = (rank % hr) * nh + (nh - 1 - rank / hr);
+    } else {
+      qb = n_qb - 1 - rank;
     }
   } else {
-    const int n_qb = (p.R + kRows - 1) / kRows;
-    int qb;
-    if (p.causal) {
-      int rank;
-      banded_rank((int)blockIdx.x, n_qb, p.groups, rank, zkv);
-      const int hr = p.R / p.S_q;  // heads per group
-      if (p.S_q % kRows == 0) {
-        const int nh = p.S_q / kRows;
-        qb = (rank % hr) * nh + (nh - 1 - rank / hr);
-      } else {
-        qb = n_qb - 1 - rank;
-      }
-    } else {
-      zkv = blockIdx.x / n_qb;
-      qb = n_qb - 1 - (blockIdx.x - zkv * n_qb);
-    }
-    r0 = qb * kRows;
-    int kv_end = p.S_kv;
-    if (p.causal) {
-      const int last = min(r0 + kRows, p.R) - 1;
-      kv_end = min(p.S_kv, (r0 / p.S_q == last / p.S_q) ? last % p.S_q + 1 : p.S_q);
-    }
-    n_kb = (kv_end + kRows - 1) / kRows;   // >= 1: every row sees key 0
+    zkv = blockIdx.x / n_qb;
+    qb = n_qb - 1 - (blockIdx.x - zkv * n_qb);
   }
+  const int r0 = qb * kRows;
+  int kv_end = p.S_kv;
+  if (p.causal) {
+    const int last = min(r0 + kRows, p.R) - 1;
+    kv_end = min(p.S_kv, (r0 / p.S_q == last / p.S_q) ? last % p.S_q + 1 : p.S_q);
+  }
+  const int n_kb = (kv_end + kRows - 1) / kRows;   // >= 1: every row sees key 0
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -1795,23 +1715,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int r = (warp & 3) * 32 + lane;          // query row within the block
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int rho = r0 + r;
-    const bool row_ok = kPacked ? r < n_rows : rho < p.R;
-    // in the padded layout (rho < Rp; packed: the vectors go on behind the last tile)
-    size_t vo;
-    if constexpr (kPacked)
-      vo = (size_t)(zkv * p.vec_stride + (long long)vec0 * p.sh.group + r);
-    else
-      vo = (size_t)zkv * p.Rp + rho;
+    const bool row_ok = rho < p.R;
+    const size_t vo = (size_t)zkv * p.Rp + rho;    // in the padded layout (rho < Rp)
     const uint64_t nlse2x2 = f2_pack(p.nlse2[vo], p.nlse2[vo]);  // -LSE * log2(e), twice
     const uint64_t ndl2 = f2_pack(p.ndelta[vo], p.ndelta[vo]);    // -D_i, twice
-    int key_limit, at = 0;
-    if constexpr (kPacked) {
-      at = (r * p.sh.inv_group) >> 16;             // the row's query token
-      key_limit = p.causal ? min(n_keys, diag + at) : n_keys;
-    } else {
-      const int pos = rho % p.S_q;
-      key_limit = p.causal ? min(p.S_kv, pos + 1) : p.S_kv;
-    }
+    const int pos = rho % p.S_q;
+    const int key_limit = p.causal ? min(p.S_kv, pos + 1) : p.S_kv;
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     // Q (warpgroup 0) and dO (warpgroup 1) into tensor memory, the A
@@ -1824,7 +1733,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       mbar_arrive(qt_ready);
     }
     for (int j = 0; j < n_kb && ok; ++j) {
-      const int kb0 = (jb + j) * kRows;
+      const int kb0 = j * kRows;
       const bool masked = !row_ok || (kb0 + kRows > key_limit);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -1856,11 +1765,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             float d0, d1;
             f2_unpack(f2_mul(f2_pack(p0, p1),
                              f2_add(f2_pack(u2f_b(dp[c]), u2f_b(dp[c + 1])), ndl2)), d0, d1);
-            if constexpr (kMasked && kPacked) {
-              // (what a masked dP holds may be another sequence's infinity)
-              d0 = (row_ok && kb0 + col0 + c < key_limit) ? d0 : 0.f;
-              d1 = (row_ok && kb0 + col0 + c + 1 < key_limit) ? d1 : 0.f;
-            }
             dk[i] = pack_bf16x2(d0, d1);
           }
         };
@@ -1879,12 +1783,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // ---------------------------------------------------------- epilogue
     if (ok && warp_wait_b(acc_done, 0, sAbort, budget)) {
       tc_fence_after_sync();
-      uint16_t* dst = static_cast<uint16_t*>(p.dq) + (D / 2) * w;
-      if constexpr (kPacked)
-        dst += (long long)(tok_q + at) * p.dq_st +
-               (zkv * p.sh.group + r - at * p.sh.group) * p.dq_sh;
-      else
-        dst += ((size_t)zkv * p.R + rho) * D;
+      uint16_t* dst = static_cast<uint16_t*>(p.dq) + ((size_t)zkv * p.R + rho) * D + (D / 2) * w;
       const uint32_t acc = tmem + lane_base + C::kTmAcc0 + (D / 2) * w;
 #pragma unroll
       for (int ch = 0; ch < D / 64; ++ch) {
@@ -1892,14 +1791,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld_x32(acc + ch * 32, v);
         tmem_ld_wait();
         reg_after_wait(v);
-        if (kPacked && parts > 1) {
-          float4* f4 =
-              reinterpret_cast<float4*>(dq_of(part)) + ((D / 8) * w + ch * 8) * kRows + r;
-#pragma unroll
-          for (int qd = 0; qd < 8; ++qd)
-            f4[qd * kRows] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
-                                 u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
-        } else if (row_ok) {
+        if (row_ok) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
           const float mult = p.scale;
 #pragma unroll
@@ -1913,7 +1805,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
           }
         }
       }
-      }
+    }
   } else if (warp == 8) {
     // -------------------------------------------------------- tensor-core issuer
     const bool leader = elect_one();
@@ -1934,16 +1826,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tc_commit(&sp_full[h]);
       }
     };
-    // packed: rows of K behind the sequence's end, for dQ += dS K
-    auto clear_keys = [&](int j) {
-      if constexpr (kPacked) {
-        const int left = k_len - (jb + j) * kRows;
-        if (left < kRows) clear_rows<D>(stage_k(j % C::kKVStages), left);
-      }
-    };
     if (ok && warp_wait_b(&kv_full[0], 0, sAbort, budget)) {
       tc_fence_after_sync();
-      clear_keys(0);
       issue_sp(0, 0);
       issue_sp(0, 1);
     } else {
@@ -1970,7 +1854,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
               break;
             }
             tc_fence_after_sync();
-            clear_keys(j + 1);
           }
           issue_sp(j + 1, h);
         }
@@ -1988,16 +1871,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const uint64_t pol_q = l2_policy_evict_first();
     const uint64_t pol_kv = l2_policy_evict_last();
     if (leader) {
-      if constexpr (kPacked) {
-        const int group = p.sh.group;
-        mbar_arrive_expect_tx(q_full, (uint32_t)(2 * group * p.sh.positions * D * 2));
-        tma_load_tile<D>(sQ, &p.tm_q, q_full, zkv * group, tok_q, pol_q);
-        tma_load_tile<D>(sDO, &p.tm_do, q_full, zkv * group, tok_q, pol_q);
-      } else {
-        mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
-        tma_load_tile<D>(sQ, &p.tm_q, q_full, r0, zkv, pol_q);
-        tma_load_tile<D>(sDO, &p.tm_do, q_full, r0, zkv, pol_q);
-      }
+      mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
+      tma_load_tile<D>(sQ, &p.tm_q, q_full, r0, zkv, pol_q);
+      tma_load_tile<D>(sDO, &p.tm_do, q_full, r0, zkv, pol_q);
     }
     int issued = 0;
     for (int j = 0; j < n_kb; ++j) {
@@ -2006,14 +1882,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (round > 0 && !warp_wait_b(&kv_empty[s], (round - 1) & 1, sAbort, budget)) break;
       if (leader) {
         mbar_arrive_expect_tx(&kv_full[s], 2 * C::kTileBytes);
-        if constexpr (kPacked) {
-          const int tok = tok_k + (jb + j) * kRows;
-          tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], zkv, tok, pol_kv);
-          tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], zkv, tok, pol_kv);
-        } else {
-          tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], j * kRows, zkv, pol_kv);
-          tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], j * kRows, zkv, pol_kv);
-        }
+        tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], j * kRows, zkv, pol_kv);
+        tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], j * kRows, zkv, pol_kv);
       }
       ++issued;
     }
@@ -2031,10 +1901,418 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   tc_fence_after_sync();
   if (warp == 8) tmem_dealloc(tmem, C::kTmemCols);
   if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
-  if constexpr (kPacked) {
-    if (parts > 1 && !*sAbort)
-      join_dq<D>(p, slot, half, parts, n_rows, tok_q, zkv, dq_of(0),
-                 reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 8));
+}
+
+// ---------------------------------------------------------------- dQ, packed
+
+// One work item of the kernel below: 128 rows (half a tile of the list) of a K/V head, or a
+// part of their keys.
+struct PackedDqWork {
+  int valid;
+  int rows, tok_q, vec0;                 // rows that exist (0: an empty half), their first token
+  int tok_k, k_len, n_keys, diag;        // as in PackedTile, of the half
+  int jb, n_blocks;                      // its key blocks
+  int part, parts, slot;                 // slot: of the tile's first part and the head
+  int head, half;
+  int idx;
+};
+static_assert(sizeof(PackedDqWork) == 64 && sizeof(PackedWork) == 64, "slots of shared memory");
+
+__device__ __forceinline__ PackedDqWork packed_dq_work(const PackedBwdParams& p, int entries,
+                                                       int idx) {
+  PackedDqWork x;
+  x.idx = idx;
+  x.half = idx & 1;
+  x.valid = (long long)(idx >> 1) < (long long)entries * p.H_kv;
+  if (!x.valid) return x;
+  int entry;
+  banded_rank(idx >> 1, entries, p.H_kv, entry, x.head);
+  const int positions = p.sh.positions, at = x.half * positions;
+  const int4* src = reinterpret_cast<const int4*>(p.sh.tiles + entry);
+  const int4 a = src[0], b = src[1], c = src[2];   // in PackedTile's order
+  const int tokens = max(min(a.y - at, positions), 0);
+  x.rows = tokens * p.sh.group;
+  x.tok_q = a.x + at;
+  x.tok_k = a.z;
+  x.k_len = a.w;
+  x.diag = b.y + at;
+  x.vec0 = b.z + at;
+  x.jb = b.w;
+  x.parts = c.y;
+  x.part = c.z;
+  x.slot = c.w * p.H_kv + x.head;
+  // (a half may see fewer keys than the tile)
+  x.n_keys = p.causal ? min(max(x.diag + tokens - 1, 0), x.k_len) : x.k_len;
+  x.n_blocks = max(min((x.n_keys + kRows - 1) / kRows, x.jb + c.x) - x.jb, 0);
+  return x;
+}
+
+// attn_bwd_dq_kernel over packed sequences, persistent as packed_bwd_dkdv_kernel is and with
+// the same counter and slots: while the dQ of one work is written, the producer has the
+// next one's Q and dO in shared memory (free as soon as they have been copied into tensor
+// memory) and its first keys in the ring.  Beside attn_bwd_dq_kernel's barriers
+//   qt_ready   also tells the issuer that the dQ before has been read out
+//   work_full, work_empty [slot]
+// The order of a row's sums does not depend on which thread block does a work.
+//
+// Bound by the chain of hand-offs, as packed_bwd_dkdv_kernel.  Deterministic gradients of
+// 16 x 1024 tokens, 32 heads over 8 of 128, causal: 546 us in all, 613 with a thread block
+// to each half of a tile; 64 x 256 tokens 300 and 367; 16 x 16 heads of 64, queries of
+// 20 to 1000 tokens over keys of 64 to 2304, 110 and 121.
+template <int D>
+__global__ void __launch_bounds__(kThreadsB, 1)
+    packed_bwd_dq_kernel(const __grid_constant__ PackedBwdParams p) {
+  using C = BwdCfg<D>;
+  extern __shared__ uint8_t smem_raw_b[];
+  uint8_t* smem = align_smem_1024(smem_raw_b);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBarQ);
+  uint64_t* q_full = bars;
+  uint64_t* kv_full = bars + 1;
+  uint64_t* kv_empty = kv_full + C::kKVStages;
+  uint64_t* sp_full = kv_empty + C::kKVStages;
+  uint64_t* ds_ready = sp_full + 2;
+  uint64_t* acc_done = sp_full + 4;
+  uint64_t* drain = sp_full + 5;
+  uint64_t* qt_ready = sp_full + 6;
+  uint64_t* work_full = sp_full + 7;
+  uint64_t* work_empty = sp_full + 9;
+  uint32_t* sTmemBase = reinterpret_cast<uint32_t*>(smem + C::kOffMiscQ);
+  volatile int* sAbort = reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 4);
+  volatile int* sFlag = reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 8);
+  volatile int* sNumParts = reinterpret_cast<volatile int*>(smem + C::kOffMiscQ + 12);
+  PackedDqWork* sWork = reinterpret_cast<PackedDqWork*>(smem + C::kOffWorkQ);
+  int* sParts = reinterpret_cast<int*>(smem + C::kOffWorkQ + 2 * sizeof(PackedDqWork));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint64_t budget = p.timeout_ns;
+  const int group = p.sh.group, positions = p.sh.positions;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::kKVStages; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sp_full[h], 1);
+      mbar_init(&ds_ready[h], 2 * 128);
+      mbar_init(&work_full[h], 1);
+      mbar_init(&work_empty[h], 9);   // warps 0-8
+    }
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    mbar_init(qt_ready, 2 * 128);
+    *sAbort = 0;
+    *sNumParts = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(sTmemBase, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *sTmemBase;
+  wait_for_earlier();
+  uint8_t* sQ = smem + C::kOffQ;
+  uint8_t* sDO = smem + C::kOffDO;
+  auto stage_k = [&](int s) { return smem + C::kOffKVRing + s * 2 * C::kTileBytes; };
+  auto stage_v = [&](int s) { return stage_k(s) + C::kTileBytes; };
+  // the w-th work of this CTA, once it is known; nullptr behind the last (or when a wait
+  // ran out)
+  auto work_at = [&](int w) -> const PackedDqWork* {
+    if (!warp_wait_b(&work_full[w & 1], (w >> 1) & 1, sAbort, budget)) return nullptr;
+    const PackedDqWork* x = sWork + (w & 1);
+    return x->valid ? x : nullptr;
+  };
+  auto work_done = [&](int w) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&work_empty[w & 1]);
+  };
+  // the float4s of a part's dQ
+  auto part_of = [&](const PackedDqWork& x, int part) {
+    return reinterpret_cast<float4*>(
+        p.sh.tile_parts + ((x.slot + (size_t)part * p.H_kv) * 256 + x.half * kRows) * D);
+  };
+
+  if (warp < 8) {
+    // -------------------------------------------------------- elementwise
+    const int wg = warp >> 2;                      // key columns 32 wg .. 32 wg + 31 of a half
+    const int r = (warp & 3) * 32 + lane;          // query row within the tile
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int at = (r * p.sh.inv_group) >> 16;     // its query token
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    int item = 0;                                  // key blocks so far
+    uint32_t wk = 0;                               // works with any so far
+    bool ok = true;
+    for (int w = 0; ok; ++w) {
+      const PackedDqWork* x = work_at(w);
+      if (!x) break;
+      const int n_blocks = x->n_blocks;
+      const bool row_ok = r < x->rows;
+      if (n_blocks > 0) {
+        // (the vectors go on behind the last tile)
+        const size_t vo = (size_t)(x->head * p.vec_stride + (long long)x->vec0 * group + r);
+        const float nlse2 = p.nlse2[vo], ndl = p.ndelta[vo];   // -LSE * log2(e), -D_i
+        const uint64_t nlse2x2 = f2_pack(nlse2, nlse2), ndl2 = f2_pack(ndl, ndl);
+        const int key_limit =
+            !row_ok ? 0 : p.causal ? min(x->n_keys, x->diag + at) : x->n_keys;
+        // Q (warpgroup 0) and dO (warpgroup 1) into tensor memory; the products of the work
+        // before, which read them there, are done (acc_done below)
+        ok = warp_wait_b(q_full, wk & 1, sAbort, budget);
+        if (!ok) break;
+        copy_tile_to_tmem<D>(wg == 0 ? sQ : sDO,
+                             tmem + lane_base + (wg == 0 ? C::kTmQt : C::kTmDOt), r);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(qt_ready);
+        const int key0 = x->jb * kRows;
+        for (int j = 0; j < n_blocks && ok; ++j, ++item) {
+          const int kb0 = key0 + j * kRows;
+          const bool masked = kb0 + kRows > key_limit;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (!warp_wait_b(&sp_full[h], item & 1, sAbort, budget)) { ok = false; break; }
+            tc_fence_after_sync();
+            const int col0 = 64 * h + 32 * wg;
+            uint32_t sv[32], dp[32];
+            tmem_ld_x32(tmem + lane_base + C::kTmS + col0, sv);
+            tmem_ld_x32(tmem + lane_base + C::kTmDP + col0, dp);
+            tmem_ld_wait();
+            reg_after_wait(sv);
+            reg_after_wait(dp);
+            uint32_t dk[16];
+            auto body = [&](auto masked_tag) {
+              constexpr bool kMasked = decltype(masked_tag)::value;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int c = 2 * i;
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(u2f_b(sv[c]), u2f_b(sv[c + 1])), sl2x2, nlse2x2), x0, x1);
+                float d0, d1;
+                f2_unpack(f2_mul(f2_pack(ex2_approx(x0), ex2_approx(x1)),
+                                 f2_add(f2_pack(u2f_b(dp[c]), u2f_b(dp[c + 1])), ndl2)), d0, d1);
+                if constexpr (kMasked) {
+                  // (what a masked S or dP holds may be another sequence's infinity)
+                  d0 = kb0 + col0 + c < key_limit ? d0 : 0.f;
+                  d1 = kb0 + col0 + c + 1 < key_limit ? d1 : 0.f;
+                }
+                dk[i] = pack_bf16x2(d0, d1);
+              }
+            };
+            if (masked)
+              body(std::true_type{});
+            else
+              body(std::false_type{});
+            // dS over the slice's own columns of S, which have been read
+            tmem_st_x16(tmem + lane_base + C::kTmS + col0, dk);
+            tmem_st_wait();
+            tc_fence_before_sync();
+            if (!(wg == 0 && h == 0 && item == p.fault_drop_item)) mbar_arrive(&ds_ready[h]);
+          }
+        }
+        if (!ok) break;
+        if (!warp_wait_b(acc_done, wk & 1, sAbort, budget)) break;
+        tc_fence_after_sync();
+        ++wk;
+      }
+      // ---------------------------------------------------------- dQ
+      // warpgroup wg writes columns [D/2 wg, D/2 (wg + 1))
+      const uint32_t acc = tmem + lane_base + C::kTmAcc0 + (D / 2) * wg;
+      const int parts = x->parts;
+      float4* f4 = part_of(*x, x->part) + (D / 8) * wg * kRows + r;
+      uint16_t* dst = static_cast<uint16_t*>(p.dq) + (long long)(x->tok_q + at) * p.dq_st +
+                      (x->head * group + r - at * group) * p.dq_sh + (D / 2) * wg;
+#pragma unroll
+      for (int ch = 0; ch < D / 64; ++ch) {
+        uint32_t v[32];
+        if (n_blocks > 0) {
+          tmem_ld_x32(acc + ch * 32, v);
+          tmem_ld_wait();
+          reg_after_wait(v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;   // no row sees a key of these
+        }
+        if (parts > 1) {
+#pragma unroll
+          for (int qd = 0; qd < 8; ++qd)
+            f4[(ch * 8 + qd) * kRows] = make_float4(u2f_b(v[qd * 4 + 0]), u2f_b(v[qd * 4 + 1]),
+                                                    u2f_b(v[qd * 4 + 2]), u2f_b(v[qd * 4 + 3]));
+        } else if (row_ok) {
+          uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
+          const float mult = p.scale;
+#pragma unroll
+          for (int qd = 0; qd < 4; ++qd) {
+            uint4 val;
+            val.x = pack_bf16x2(u2f_b(v[qd * 8 + 0]) * mult, u2f_b(v[qd * 8 + 1]) * mult);
+            val.y = pack_bf16x2(u2f_b(v[qd * 8 + 2]) * mult, u2f_b(v[qd * 8 + 3]) * mult);
+            val.z = pack_bf16x2(u2f_b(v[qd * 8 + 4]) * mult, u2f_b(v[qd * 8 + 5]) * mult);
+            val.w = pack_bf16x2(u2f_b(v[qd * 8 + 6]) * mult, u2f_b(v[qd * 8 + 7]) * mult);
+            d4[qd] = val;
+          }
+        }
+      }
+      tc_fence_before_sync();   // (dQ is read out before qt_ready of the next work)
+      if (threadIdx.x == 0 && parts > 1) {   // for the end, when the CTA's threads join them
+        sParts[*sNumParts] = x->idx;
+        *sNumParts = *sNumParts + 1;
+      }
+      work_done(w);
+    }
+  } else if (warp == 8) {
+    // -------------------------------------------------------- tensor-core issuer
+    const bool leader = elect_one();
+    const uint32_t tS = tmem + C::kTmS, tDP = tmem + C::kTmDP, tdQ = tmem + C::kTmAcc0;
+    const uint32_t tQt = tmem + C::kTmQt, tDOt = tmem + C::kTmDOt;
+    int item = 0;
+    uint32_t wk = 0;
+    bool ok = true;
+    for (int w = 0; ok; ++w) {
+      const PackedDqWork* x = work_at(w);
+      if (!x) break;
+      const int n_blocks = x->n_blocks, left = x->k_len - x->jb * kRows;
+      work_done(w);
+      if (n_blocks == 0) continue;
+      ok = warp_wait_b(qt_ready, wk & 1, sAbort, budget);
+      if (!ok) break;
+      tc_fence_after_sync();
+      // K and V of the work's j-th block, once they are there; rows of K behind the sequence's
+      // end cleared, for dQ += dS K
+      auto take_keys = [&](int j) {
+        const int s = (item + j) % C::kKVStages;
+        if (!warp_wait_b(&kv_full[s], ((item + j) / C::kKVStages) & 1, sAbort, budget)) return false;
+        tc_fence_after_sync();
+        if (left - j * kRows < kRows) clear_rows<D>(stage_k(s), left - j * kRows);
+        return true;
+      };
+      // S and dP of half h of it, with Q and dO read from tensor memory
+      auto issue_sp = [&](int j, int h) {
+        const int s = (item + j) % C::kKVStages;
+        if (leader) {
+          issue_qk_half_ts<D>(tS + 64 * h, tQt, kmajor_tile_desc(smem_u32(stage_k(s))), h);
+          issue_qk_half_ts<D>(tDP + 64 * h, tDOt, kmajor_tile_desc(smem_u32(stage_v(s))), h);
+          tc_commit(&sp_full[h]);
+        }
+      };
+      ok = take_keys(0);
+      if (!ok) break;
+      issue_sp(0, 0);
+      issue_sp(0, 1);
+      for (int j = 0; j < n_blocks && ok; ++j) {
+        const int i = item + j, s = i % C::kKVStages;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!warp_wait_b(&ds_ready[h], i & 1, sAbort, budget)) { ok = false; break; }
+          tc_fence_after_sync();
+          if (leader) {
+            issue_pv_half<D>(tdQ, tS + 64 * h, mnmajor_tile_desc<D>(smem_u32(stage_k(s))), h,
+                             j > 0 || h > 0);
+            if (h == 1) tc_commit(&kv_empty[s]);
+          }
+          if (j + 1 < n_blocks) {
+            if (h == 0 && !take_keys(j + 1)) { ok = false; break; }
+            issue_sp(j + 1, h);
+          }
+        }
+      }
+      if (!ok) break;
+      if (leader) tc_commit(acc_done);
+      item += n_blocks;
+      ++wk;
+    }
+    if (leader) {
+      tc_commit(drain);
+      drain_wait_b(drain, 0, budget);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // -------------------------------------------------------- producer
+    const bool leader = elect_one();
+    const uint64_t pol_q = l2_policy_evict_first();
+    const uint64_t pol_kv = l2_policy_evict_last();
+    const int entries = p.sh.head->tiles;
+    int issued = 0;
+    uint32_t wk = 0;
+    int idx = (int)blockIdx.x;
+    auto claim = [&]() {
+      if (lane == 0) idx = (int)gridDim.x + atomicAdd(p.sh.next + 1, 1);
+      idx = __shfl_sync(kAll, idx, 0);
+    };
+    bool ok = true;
+    for (int w = 0; ok; ++w) {
+      PackedDqWork x = packed_dq_work(p, entries, idx);
+      while (x.valid && x.rows == 0) {   // an empty half
+        claim();
+        x = packed_dq_work(p, entries, idx);
+      }
+      if (w >= 2 && !warp_wait_b(&work_empty[w & 1], ((w >> 1) - 1) & 1, sAbort, budget)) break;
+      if (lane == 0) {
+        sWork[w & 1] = x;
+        mbar_arrive(&work_full[w & 1]);
+      }
+      __syncwarp();
+      if (!x.valid) break;
+      if (x.n_blocks > 0) {
+        if (wk > 0 && !warp_wait_b(qt_ready, (wk - 1) & 1, sAbort, budget)) break;
+        if (leader) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)(2 * group * positions * D * 2));
+          tma_load_tile<D>(sQ, &p.tm_q, q_full, x.head * group, x.tok_q, pol_q);
+          tma_load_tile<D>(sDO, &p.tm_do, q_full, x.head * group, x.tok_q, pol_q);
+        }
+        ++wk;
+        for (int j = 0; j < x.n_blocks; ++j) {
+          const int s = issued % C::kKVStages, round = issued / C::kKVStages;
+          if (round > 0 && !warp_wait_b(&kv_empty[s], (round - 1) & 1, sAbort, budget)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const int tok = x.tok_k + (x.jb + j) * kRows;
+            mbar_arrive_expect_tx(&kv_full[s], 2 * C::kTileBytes);
+            tma_load_tile<D>(stage_k(s), &p.tm_k, &kv_full[s], x.head, tok, pol_kv);
+            tma_load_tile<D>(stage_v(s), &p.tm_v, &kv_full[s], x.head, tok, pol_kv);
+          }
+          ++issued;
+        }
+      }
+      claim();   // (late, as in packed_bwd_dkdv_kernel)
+    }
+    if (leader) {
+      if (wk > 0) drain_wait_b(q_full, (wk - 1) & 1, budget);
+      const int from = issued > C::kKVStages ? issued - C::kKVStages : 0;
+      for (int t = from; t < issued; ++t)
+        drain_wait_b(&kv_full[t % C::kKVStages], (t / C::kKVStages) & 1, budget);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 8) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && *sAbort) atomicCAS(&g_bwd_status, 0, (int)ATTN_ERR_TIMEOUT);
+  if (*sAbort) return;
+  // the last of a tile's parts adds them up
+  for (int i = 0, n = *sNumParts, entries = p.sh.head->tiles; i < n; ++i) {
+    const PackedDqWork x = packed_dq_work(p, entries, sParts[i]);
+    if (!last_of_parts(p.sh.tile_counters + (size_t)x.slot * 2 + x.half, x.parts, sFlag)) continue;
+    const float4* from = part_of(x, 0);
+#pragma unroll 1
+    for (int j = threadIdx.x; j < ((x.rows + 7) & ~7) * (D / 8); j += kThreadsB) {
+      int r, c;
+      join_item<D>(j, r, c);
+      if (r >= x.rows) continue;
+      const int at = (r * p.sh.inv_group) >> 16;
+      float sum[8];
+      sum_parts(sum, from + 2 * c * kRows + r, kRows, (size_t)p.H_kv * 256 * (D / 4), x.parts,
+                [](int) { return 1.f; });
+      store_bf16x8(static_cast<uint16_t*>(p.dq) + (long long)(x.tok_q + at) * p.dq_st +
+                       (x.head * group + r - at * group) * p.dq_sh + c * 8,
+                   sum, p.scale);
+    }
   }
 }
 
@@ -2112,7 +2390,7 @@ cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const v
               cudaSuccess ||
           (err = cudaFuncSetAttribute(packed_bwd_dkdv_kernel<D, true>, kAttr, C::kSmemKV)) !=
               cudaSuccess ||
-          (err = cudaFuncSetAttribute(attn_bwd_dq_kernel<D, true>, kAttr, C::kSmemQ)) != cudaSuccess)
+          (err = cudaFuncSetAttribute(packed_bwd_dq_kernel<D>, kAttr, C::kSmemQ)) != cudaSuccess)
         return err;
       attr_set[dev] = true;
     }
@@ -2147,9 +2425,9 @@ cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const v
   }
   err = launch_ahead(packed_bwd_dkdv_kernel<D, false>, grid_kv, kThreadsB, C::kSmemKV, stream, p);
   if (err != cudaSuccess) return err;
-  return launch_ahead(attn_bwd_dq_kernel<D, true>,
-                      dim3((unsigned)tile_room * 2u * (unsigned)p.H_kv), kThreadsB, C::kSmemQ, stream,
-                      p);
+  const long long halves = (long long)tile_room * p.H_kv * 2;
+  return launch_ahead(packed_bwd_dq_kernel<D>, dim3((unsigned)(halves < sms ? halves : sms)),
+                      kThreadsB, C::kSmemQ, stream, p);
 }
 
 }  // namespace

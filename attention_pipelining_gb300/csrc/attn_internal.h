@@ -271,8 +271,8 @@ struct PackedHeader {
   int tiles, key_blocks;              // entries of the two lists
   int q_first, q_end;                 // tokens that belong to a sequence
   int cut;                            // whether any tile was cut
-  int next;                           // next of the backward's key blocks and K/V heads
-  int unused[58];
+  int next[2];                        // next of the backward's works (dK and dV, dQ)
+  int unused[57];
 };
 
 struct PackedPlan {

@@ -152,7 +152,7 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   shape->tile_counters = plan->counters[0];
   shape->key_counters = plan->counters[1];
   shape->head = plan->head;
-  shape->next = &plan->head->next;
+  shape->next = plan->head->next;
   shape->tiles = plan->tiles;
   shape->keys = plan->keys;
   shape->group = group;

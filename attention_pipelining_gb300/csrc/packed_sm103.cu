@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     const int last = sorted ? kBuckets - 1 : 0;
     p.head->tiles = at[0][last], p.head->key_blocks = at[1][last];
     p.head->q_first = q[0], p.head->q_end = q[B];
-    p.head->next = 0;
+    p.head->next[0] = p.head->next[1] = 0;
     p.head->cut = 2 * most[0] >= 3 * cap[0];
   }
 }
