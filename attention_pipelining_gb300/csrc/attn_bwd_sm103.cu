@@ -1484,7 +1484,10 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       __syncwarp();
       if (!x.valid) break;
       if (x.n_work > 0) {
-        if (wk > 0 && !warp_wait_b(kv_free, (wk - 1) & 1, sAbort, budget)) break;
+        // (kept in tensor memory, K and V leave their buffers when they have been copied,
+        // unless dQ reads K there)
+        uint64_t* const free = C::kKVinTmem && !kFuse ? kt_ready : kv_free;
+        if (wk > 0 && !warp_wait_b(free, (wk - 1) & 1, sAbort, budget)) break;
         if (leader) {
           mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
           tma_load_tile<D>(sK, &p.tm_k, kv_full, x.head, x.tok_k, pol_kv);
