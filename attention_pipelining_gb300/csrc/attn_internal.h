@@ -282,6 +282,7 @@ struct PackedPlan {
   int positions;       // query tokens of a 128-row tile
   unsigned long long over_positions, over_tile;   // ceil(2^40 / positions), of 2 positions
   int causal, H_kv;
+  int least_keys;      // packed_least_keys
   PackedHeader* head;  // workspace, from here on
   int* seq_q;          // [B + 1], cu_q in order
   int* seq_k;          // [B + 1] (== seq_q where they are the same)
@@ -296,16 +297,20 @@ struct PackedPlan {
 // Parts: an entry of n blocks (of keys, or of query tiles) is cut where n is one and a
 // half times `cap` or more, into round(n / cap) parts (kPackedMostParts at most), with
 // cap the blocks of all entries and K/V heads divided by kPackedCtas, or
-// kPackedLeastTile (of keys) or kPackedLeastKeys (of query tiles) where that is more.  So
+// kPackedLeastTile (of keys) or packed_least_keys (of query tiles) where that is more.  So
 // there are at most n / cap + 1/2 <= 4/3 n / cap parts of an entry, and 4/3 kPackedCtas
 // of all.
 constexpr int kPackedCtas = 152;
 constexpr int kPackedMostParts = 64;
 constexpr int kPackedBand = 4;       // key blocks of a group
 // blocks of a part, at least, of tiles and of key blocks.  Measured: one prompt of 2048 tokens, 8
-// heads over 2 of 128: 30 us with 8 (33 uncut), 700 tokens of 8 over 1 with 4 24 us (19 uncut); the
-// gradients of four texts of 30 to 300 tokens, 8 over 2 of 64: 28 us with 4 (33 uncut).
-constexpr int kPackedLeastTile = 8, kPackedLeastKeys = 4;
+// heads over 2 of 128: 30 us with 8 (33 uncut), 700 tokens of 8 over 1 with 4 24 us (19 uncut).
+// Gradients, with 2, 3, 4 and 6: four texts of 30 to 300 tokens, 8 heads over 2 of 64, 25.2,
+// 28.1, 28.2, 29.6 us; 1500 tokens of 4 heads of 64 26.5, 26.5, 27.7, 29.2; 700 tokens, 8
+// heads over 2 of 128, where a part's dK and dV are twice the bytes, 43.4, 39.6, 40.2,
+// 41.4; three texts of 200 to 500 tokens, 8 heads of 128, 30.9, 27.9, 27.9, 28.0.
+constexpr int kPackedLeastTile = 8;
+__host__ __device__ constexpr int packed_least_keys(int D) { return D == 64 ? 2 : 3; }
 inline int packed_slots(int H_kv) { return 4 * kPackedCtas / (3 * H_kv); }
 constexpr int kPackedCounters = 2;    // of an entry's parts and a K/V head: one a half of a tile
 

@@ -100,7 +100,7 @@ Layout layout_of(const attn_packed_t& s, bool backward, bool deterministic) {
     l.keys = part((size_t)packed_key_room(s.T_k, s.B, s.H_kv) * sizeof(PackedKeys));
     l.group_at = part((size_t)packed_key_room(s.T_k, s.B, s.H_kv) * sizeof(int));
     l.key_counters = part(counters);
-    if (cut(query_tiles, kPackedLeastKeys)) l.key_parts = part(heads * 2 * 128 * s.D * sizeof(float));
+    if (cut(query_tiles, packed_least_keys(s.D))) l.key_parts = part(heads * 2 * 128 * s.D * sizeof(float));
     // every sequence's rows from packed_vec0 on, and what a copy of 128 reads past them
     l.vec_stride = (((int64_t)s.T_q + 4ll * s.B + 4) * group + 128 + 3) & ~3ll;
     l.nlse = part((size_t)s.H_kv * l.vec_stride * sizeof(float));
@@ -133,6 +133,7 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   plan->seq_q = reinterpret_cast<int*>(ws + l.seq_q);
   plan->seq_k = cu_k ? reinterpret_cast<int*>(ws + l.seq_k) : plan->seq_q;
   plan->H_kv = s.H_kv;
+  plan->least_keys = packed_least_keys(s.D);
   // (a part that the layout does not have begins at 0, where the header is)
   const auto at = [&](size_t offset) { return offset ? ws + offset : nullptr; };
   plan->first[0] = reinterpret_cast<int*>(ws + l.first);

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 
   int shift[2], cap[2];
   const bool may_cut =
-      2 * most[0] >= 3 * kPackedLeastTile || 2 * most[1] >= 3 * kPackedLeastKeys;
+      2 * most[0] >= 3 * kPackedLeastTile || 2 * most[1] >= 3 * p.least_keys;
   if (may_cut) {
     unsigned long long mine[2] = {0, 0};
     each([&](int list, int, int cost, PackedTile*, PackedKeys*) { mine[list] += cost; });
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const unsigned long long share = (total[i] * p.H_kv + kPackedCtas - 1) / kPackedCtas;
-    const unsigned long long least = i == 0 ? kPackedLeastTile : kPackedLeastKeys;
+    const unsigned long long least = i == 0 ? kPackedLeastTile : p.least_keys;
     cap[i] = may_cut ? (int)min(max(share, least), 1ull << 29) : 1 << 29;
     shift[i] = 0;
     while ((most[i] >> shift[i]) >= kBuckets) ++shift[i];

@@ -50,10 +50,11 @@
  * attn_fwd_packed_timeout_test and attn_bwd_packed_timeout_test run attn_fwd_packed and
  * attn_bwd_packed (attn_packed.h; same arguments and buffers) with one signal
  * withheld: the forward's first softmax warpgroup does not report its probabilities of
- * block `drop_block` of each of its tiles that has one, and the dK/dV kernel's first
- * elementwise warpgroup not those of half 0 of the `drop_item`-th query tile that
- * each thread block gets to (both counted from 0), so that the issuer's wait for them runs
- * out after `wait_budget_ns`, and all roles unwind.  Outputs are unspecified.  Limits of
+ * block `drop_block` of each of its tiles that has one, and the first elementwise
+ * warpgroup of the dK/dV kernel (and, where deterministic, of the dQ kernel) not those of half
+ * 0 of the `drop_item`-th query tile (key block) that each thread block gets to (both
+ * counted from 0), so that the issuer's wait for them runs out after `wait_budget_ns`, and
+ * all roles unwind.  Outputs are unspecified.  Limits of
  * `wait_budget_ns` as above; the other number must be >= 0 (else ATTN_ERR_INVALID_ARG).
  * For tests only.
  *

@@ -523,7 +523,7 @@ def test_a_wait_that_runs_out(D, H_q, H_kv, what):
     if what == "forward":
         packed.fwd_packed_timeout_test(q, k, v, c, True, 0.1, drop_block=1)
     else:
-        packed.bwd_packed_timeout_test(q, k, v, o, lse, do, c, True, 0.1, drop_item=2,
+        packed.bwd_packed_timeout_test(q, k, v, o, lse, do, c, True, 0.1, drop_item=1,
                                        deterministic=what == "deterministic")
     torch.cuda.synchronize()
     assert ap.device_status(reset=True) == 5

@@ -140,7 +140,7 @@ def test_rotation_refuses(lib, kw, code):
 
 def test_workspace_holds_the_lists(lib):
     """A header, the bounds, 48 and 64 bytes for each tile and key block that there may be, with up to 4/3
-    of 152 parts, a part's results where any entry can be cut (12 and 6 blocks), two counters a part, and (backward)
+    of 152 parts, a part's results where any entry can be cut (12 blocks of keys, 3 tiles), two counters a part, and (backward)
     two row vectors and the accumulator."""
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     for H_q, H_kv, positions in ((8, 8, 128), (8, 2, 32), (6, 2, 40), (5, 1, 24), (7, 1, 16), (32, 1, 4),
@@ -160,7 +160,7 @@ def test_workspace_holds_the_lists(lib):
             assert lib.attn_packed_workspace_bytes(s) == begin + tiles + lse
             blocks = (T + 3) // 128 + B + slots
             keys = up(64 * blocks) + up(4 * blocks) + counters
-            if -(-T // positions) >= 6:
+            if -(-T // positions) >= 3:
                 keys += up(slots * H_kv * 256 * 64 * 4)
             vec = (T + 4 * B + 4) * R + 128
             vec += -vec % 4
