@@ -113,11 +113,12 @@ __device__ __forceinline__ void store4(uint8_t* block, int r, int c, bool value,
 // worked on.
 //
 // Measured, 8192 tokens of 32 + 8 heads of 128 (device time): 4 bits, 181 MB,
-// 39 us, 4.6 TB/s (68 % of the measured HBM copy rate; 36 us with adjacent pairs),
-// bf16, 206 MB, 37.8 us, 5.4 TB/s (80 %; 35.3 us with adjacent pairs).  Bound by
+// 38 us, 4.8 TB/s (70 % of the measured HBM copy rate; 35 us with adjacent pairs),
+// bf16, 206 MB, 35.5 us, 5.8 TB/s (86 %; 34.7 us with adjacent pairs).  Bound by
 // the instructions of rotation and quantisation together with the rows' latencies.
-// It took 54 us with one token to a block or two rows ahead in registers, 44 with
-// eight neighbouring elements a lane throughout.
+// In earlier builds it took 54 us with one token to a block or two rows ahead in
+// registers, 44 with eight neighbouring elements a lane throughout, and 39 (bf16 38) with
+// the exact roundings in a function of their own (rotate.cuh).
 template <int D, bool kInt4, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, 8)
     kv_append_kernel(const __grid_constant__ KvAppendParams p) {

@@ -77,7 +77,8 @@ typedef struct {
  * attention kernel (attn_fwd's, over tiles of 256 rows that hold whole groups of
  * query heads) takes them on a persistent grid of one thread block per SM.  Where
  * there are few of them, the keys of long ones are cut into parts, which the thread
- * block that ends last joins.  The results are deterministic.
+ * block that ends last joins; up to 31 short sequences take one kernel only.  The
+ * results are deterministic.
  *
  * Arithmetic as attn_fwd's: fp32 accumulation and softmax statistics, the
  * probabilities rounded to bf16 (2^-8) before the second product, whose
@@ -97,8 +98,8 @@ attn_status_t attn_fwd_packed(const attn_packed_t *sizes, const attn_thd_t *q,
 size_t attn_packed_workspace_bytes(const attn_packed_t *sizes);
 
 /*
- * Gradients of attn_fwd_packed (its sizes, bounds and workspace rules): given its inputs, its o and lse, and the
- * gradient dout of o,
+ * Gradients of attn_fwd_packed (its sizes, bounds and workspace rules): given its
+ * inputs, its o and lse, and the gradient dout of o,
  *
  *     P_ij = exp(s_ij - lse_i),  dS_ij = P_ij (dout_i . v_j - dout_i . o_i)
  *     dv_j = sum P_ij dout_i,  dk_j = scale sum dS_ij q_i  (over the group's heads too)
