@@ -274,20 +274,21 @@ __device__ __forceinline__ bool qblock_sees(const BwdParams& p, int r0, int kv0)
 // sweep, twice the L2).
 constexpr int kRankBand = 16;
 
+template <int kBand = kRankBand>
 __device__ __forceinline__ void banded_rank(int idx, int n_ranks, int groups, int& rank,
                                             int& zkv) {
-  const int full = n_ranks / kRankBand;  // whole bands
-  const int per_band = groups * kRankBand;
+  const int full = n_ranks / kBand;  // whole bands
+  const int per_band = groups * kBand;
   if (idx < full * per_band) {
     const int band = idx / per_band;
     const int rem = idx - band * per_band;
-    zkv = rem / kRankBand;
-    rank = band * kRankBand + (rem - zkv * kRankBand);
+    zkv = rem / kBand;
+    rank = band * kBand + (rem - zkv * kBand);
   } else {
-    const int tail = n_ranks - full * kRankBand;  // ranks of the last, partial band
+    const int tail = n_ranks - full * kBand;  // ranks of the last, partial band
     const int rem = idx - full * per_band;
     zkv = rem / tail;
-    rank = full * kRankBand + (rem - zkv * tail);
+    rank = full * kBand + (rem - zkv * tail);
   }
 }
 
@@ -1929,7 +1930,7 @@ __device__ __forceinline__ PackedDqWork packed_dq_work(const PackedBwdParams& p,
   x.valid = (long long)(idx >> 1) < (long long)entries * p.H_kv;
   if (!x.valid) return x;
   int entry;
-  banded_rank(idx >> 1, entries, p.H_kv, entry, x.head);
+  banded_rank<kPackedBand>(idx >> 1, entries, p.H_kv, entry, x.head);
   const int positions = p.sh.positions, at = x.half * positions;
   const int4* src = reinterpret_cast<const int4*>(p.sh.tiles + entry);
   const int4 a = src[0], b = src[1], c = src[2];   // in PackedTile's order
@@ -1956,12 +1957,15 @@ __device__ __forceinline__ PackedDqWork packed_dq_work(const PackedBwdParams& p,
 // memory) and its first keys in the ring.  Beside attn_bwd_dq_kernel's barriers
 //   qt_ready   also tells the issuer that the dQ before has been read out
 //   work_full, work_empty [slot]
-// The order of a row's sums does not depend on which thread block does a work.
+// The order of a row's sums does not depend on which thread block does a work.  In bands of
+// four tiles the costliest run first where there are few, and a head's keys are still
+// shared in L2 (bands of 16, 4 and 1: the cross attention below 109.5, 99.6, 99.2 us; one
+// sequence of 16384 tokens 5295, 5176, 5226).
 //
 // Bound by the chain of hand-offs, as packed_bwd_dkdv_kernel.  Deterministic gradients of
 // 16 x 1024 tokens, 32 heads over 8 of 128, causal: 546 us in all, 613 with a thread block
 // to each half of a tile; 64 x 256 tokens 300 and 367; 16 x 16 heads of 64, queries of
-// 20 to 1000 tokens over keys of 64 to 2304, 110 and 121.
+// 20 to 1000 tokens over keys of 64 to 2304, 100 and 121.
 template <int D>
 __global__ void __launch_bounds__(kThreadsB, 1)
     packed_bwd_dq_kernel(const __grid_constant__ PackedBwdParams p) {

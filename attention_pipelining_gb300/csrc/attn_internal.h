@@ -302,7 +302,7 @@ struct PackedPlan {
 // of all.
 constexpr int kPackedCtas = 152;
 constexpr int kPackedMostParts = 64;
-constexpr int kPackedBand = 4;       // key blocks of a group
+constexpr int kPackedBand = 4;       // key blocks of a group, and tiles of a band (dQ)
 // blocks of a part, at least, of tiles and of key blocks.  Measured: one prompt of 2048 tokens, 8
 // heads over 2 of 128: 30 us with 8 (33 uncut), 700 tokens of 8 over 1 with 4 24 us (19 uncut).
 // Gradients, with 2, 3, 4 and 6: four texts of 30 to 300 tokens, 8 heads over 2 of 64, 25.2,

@@ -215,7 +215,7 @@ def fwd_packed_timeout_test(*args, drop_block: int, wait_budget_ns: int = 20_000
 
 
 def bwd_packed_timeout_test(*args, drop_item: int, wait_budget_ns: int = 20_000_000, **kw):
-    """Test hook: attn_bwd_packed likewise, in its dK/dV kernel."""
+    """Test hook: attn_bwd_packed likewise, in its dK/dV kernel (and its dQ kernel, if deterministic)."""
     return attn_bwd_packed(*args, _fault=(int(drop_item), int(wait_budget_ns)), **kw)
 
 

@@ -533,6 +533,32 @@ def test_a_wait_that_runs_out(D, H_q, H_kv, what):
     check_backward(q, k, v, o, lse, do, cu, cu, True, 0.1, got)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_wait_that_runs_out_in_cut_work(D):
+    """The same where a plan cuts tiles into parts: what they counted does not reach the next call in
+    the same workspace."""
+    from attention_pipelining_gb300 import packed
+    q, k, v, do, cu, _ = make(4, 2, D, [2500, 700])
+    ws = torch.full((max(ap.packed_workspace_bytes(2, 3200, 3200, 4, 2, D),
+                         ap.packed_bwd_workspace_bytes(2, 3200, 3200, 4, 2, D, True)),), 255,
+                    dtype=torch.uint8, device="cuda")
+    o, lse = forward(q, k, v, cu, cu, True, 0.1, workspace=ws)
+    check_forward(q, k, v, cu, cu, True, 0.1, (o, lse))
+    want = backward(q, k, v, o, lse, do, cu, cu, True, 0.1, workspace=ws, deterministic=True)
+    for _ in range(2):
+        packed.fwd_packed_timeout_test(q, k, v, ints(cu), True, 0.1, drop_block=5, workspace=ws)
+        torch.cuda.synchronize()
+        assert ap.device_status(reset=True) == 5
+        a = forward(q, k, v, cu, cu, True, 0.1, workspace=ws)
+        assert torch.equal(a[0], o) and torch.equal(a[1], lse)
+        packed.bwd_packed_timeout_test(q, k, v, o, lse, do, ints(cu), True, 0.1, drop_item=1, workspace=ws,
+                                       deterministic=True)
+        torch.cuda.synchronize()
+        assert ap.device_status(reset=True) == 5
+        got = backward(q, k, v, o, lse, do, cu, cu, True, 0.1, workspace=ws, deterministic=True)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 # ---------------------------------------------------------------- rotation
 
 ROPE = [
