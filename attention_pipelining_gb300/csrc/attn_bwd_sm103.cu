@@ -1067,7 +1067,7 @@ __device__ __forceinline__ PackedWork packed_work(const PackedBwdParams& p, int 
 // attn_bwd_dkdv_kernel over packed sequences, persistent: with short sequences a block of
 // keys has a few query tiles only, and a thread block of its own for each spent most of
 // its time starting and ending (16 x 16 heads of 64, queries of 20 to 1000 tokens over
-// keys of 64 to 2304: 77 us, so 59).  The producer warp takes the next work from a counter
+// keys of 64 to 2304: 77 us, so 56).  The producer warp takes the next work from a counter
 // (the costliest come first), tells the other roles what it is in one of two slots of
 // shared memory, and loads ahead as far as the ring and the K and V buffers allow, while
 // the work before is finished and its dK and dV are written.  The roles, the products and
@@ -1192,23 +1192,25 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
     int item = 0;                                  // query tiles so far
     uint32_t wk = 0;                               // works with any so far
-    bool ok = true;
+    bool ok = true, copied = false;
+    // K (warpgroup 0) and V (warpgroup 1) of the n-th work with any into tensor memory; the
+    // products of the work before, which read them there, are done (acc_done below)
+    auto copy_keys = [&](uint32_t n) {
+      if (!warp_wait_b(kv_full, n & 1, sAbort, budget)) return false;
+      copy_tile_to_tmem<D>(wg == 0 ? sK : sV,
+                           tmem + lane_base + (wg == 0 ? C::kTmKt : C::kTmVt), r);
+      tmem_st_wait();
+      tc_fence_before_sync();
+      mbar_arrive(kt_ready);
+      return true;
+    };
     for (int w = 0; ok; ++w) {
       const PackedWork* x = work_at(w);
       if (!x) break;
       const int n_work = x->n_work, n_keys = x->n_keys;
       if constexpr (C::kKVinTmem) {
-        // K (warpgroup 0) and V (warpgroup 1) into tensor memory; the products of the work
-        // before, which read them there, are done (acc_done below)
-        if (n_work > 0) {
-          ok = warp_wait_b(kv_full, wk & 1, sAbort, budget);
-          if (!ok) break;
-          copy_tile_to_tmem<D>(wg == 0 ? sK : sV,
-                               tmem + lane_base + (wg == 0 ? C::kTmKt : C::kTmVt), r);
-          tmem_st_wait();
-          tc_fence_before_sync();
-          mbar_arrive(kt_ready);
-        }
+        if (n_work > 0 && !copied && !copy_keys(wk)) break;
+        copied = false;
       }
       const int first = x->first, tiles = x->tiles, q_len = x->q_len, shift = x->shift;
       for (int n = 0; n < n_work && ok; ++n, ++item) {
@@ -1310,6 +1312,16 @@ __global__ void __launch_bounds__(kFuse ? kThreadsFused : kThreadsB, 1)
       if (n_work > 0) {
         if (!warp_wait_b(acc_done, wk & 1, sAbort, budget)) break;
         tc_fence_after_sync();
+        if constexpr (C::kKVinTmem && !kFuse) {
+          // the next work's first products may run while this one's dV and dK are written
+          // (16 x 16 heads of 64 as above: 56 us, without 60; the same in the dQ kernel, with
+          // a barrier more, lost 1 % at heads of 128)
+          const PackedWork* y = work_at(w + 1);
+          if (y && y->n_work > 0) {
+            if (!copy_keys(wk + 1)) break;
+            copied = true;
+          }
+        }
       }
       const int parts = x->parts, head = x->head;
       const long long tok = x->tok_k + r;
@@ -1965,7 +1977,7 @@ __device__ __forceinline__ PackedDqWork packed_dq_work(const PackedBwdParams& p,
 // Bound by the chain of hand-offs, as packed_bwd_dkdv_kernel.  Deterministic gradients of
 // 16 x 1024 tokens, 32 heads over 8 of 128, causal: 546 us in all, 613 with a thread block
 // to each half of a tile; 64 x 256 tokens 300 and 367; 16 x 16 heads of 64, queries of
-// 20 to 1000 tokens over keys of 64 to 2304, 100 and 121.
+// 20 to 1000 tokens over keys of 64 to 2304, 100 and 121 (96 now).
 template <int D>
 __global__ void __launch_bounds__(kThreadsB, 1)
     packed_bwd_dq_kernel(const __grid_constant__ PackedBwdParams p) {

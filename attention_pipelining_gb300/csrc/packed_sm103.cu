@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   // other, and share that head's queries in L2.  (The gradients of 32 heads over 8 of 128,
   // causal, in an earlier build: 16 x 1024 tokens 570 us, in the order of the blocks' own
   // costs, with the heads innermost, 633, in groups of 16 589; 4 x 4096 1417, 1421 and
-  // 1450.  Now 524 and 1372.)
+  // 1450.  Now 522 and 1370.)
   const bool grouped = 2 * most[1] < 3 * cap[1];
   const auto group_cost = [&](const PackedKeys& x) {   // its first block's
     return x.tiles - (p.causal ? min(positions(max(x.shift, 0)), x.tiles) : 0);
