@@ -54,6 +54,7 @@
 #include "attn_internal.h"
 #include "attn_tiles.cuh"
 #include "kv_cache.cuh"
+#include "packed_plan.cuh"
 #include "ptx.cuh"
 
 namespace attnpipe {
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const BwdParams p,
 // the vectors' place of a token's follows from its sequence, found by bisection.
 // Bound by HBM (13 thousand tokens of 32 heads of 128, with the zeros of the accumulator:
 // 385 MB of HBM traffic in 63 us, 6.1 TB/s); where there is no accumulator, by its chain of loads
-// (2588 tokens of 16 heads of 64: 6.4 us).
+// (2588 tokens of 16 heads of 64: 5.6 us).
 template <int D>
 __global__ void __launch_bounds__(256)
     packed_bwd_prep_kernel(const __grid_constant__ PackedBwdParams p, const uint16_t* o,
@@ -382,9 +383,24 @@ __global__ void __launch_bounds__(256)
   const long long row0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kPrepRowsPerWarp;
   const int lane = threadIdx.x & 31;
   const int sub = lane / kLanesPerRow, piece = lane % kLanesPerRow;
-  allow_later();
-  wait_for_earlier();
-  const int q_first = p.sh.head->q_first, q_end = p.sh.head->q_end;
+  // up to 31 sequences: the bounds by themselves, and the plan at the same time
+  // (PackedPlan::early; four texts of 30 to 300 tokens, 8 heads over 2 of 64: 22.5 us, with the
+  // plan first 24.2; three of 200 to 500, 8 heads of 128: 25.0 and 27.4)
+  const bool first = p.cu_q != nullptr;
+  int2 bounds = make_int2(0, 0);
+  int q_first, q_end;
+  if (first) {
+    wait_for_earlier();
+    allow_later();
+    (void)warp_bounds(p.cu_q, p.cu_q, p.B, p.sh.T_q, p.sh.T_q, bounds);
+    q_first = __shfl_sync(kAll, bounds.x, 0);
+    q_end = __shfl_sync(kAll, bounds.x, p.B);
+  } else {
+    allow_later();
+    wait_for_earlier();
+    q_first = p.sh.head->q_first;
+    q_end = p.sh.head->q_end;
+  }
   uint4 a[kLoads], b[kLoads];
   int tok[kLoads], head[kLoads];
   float delta[kLoads];
@@ -437,15 +453,26 @@ __global__ void __launch_bounds__(256)
       const int h = __shfl_sync(kAll, head[i], n * kLanesPerRow);
       if (lane == i * kRowsPerLoad + n) mine = x, my_tok = t, my_head = h;
     }
+  int b0 = 0, q0 = 0;   // the last sequence that begins at or before my_tok, its first token
+  if (first) {
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1) {
+      const int mid = b0 + step, begins = __shfl_sync(kAll, bounds.x, mid & 31);
+      if (mid < p.B && begins <= my_tok) b0 = mid;
+    }
+    q0 = __shfl_sync(kAll, bounds.x, b0);
+  }
   if (my_tok < 0) return;
-  int b0 = 0, b1 = p.B;   // seq_q[b0] <= my_tok < seq_q[b1]
-  while (b1 - b0 > 1) {
-    const int mid = (b0 + b1) >> 1;
-    if (p.seq_q[mid] <= my_tok) b0 = mid;
-    else b1 = mid;
+  if (!first) {
+    int b1 = p.B;   // seq_q[b0] <= my_tok < seq_q[b1]
+    while (b1 - b0 > 1) {
+      const int mid = (b0 + b1) >> 1;
+      if (p.seq_q[mid] <= my_tok) b0 = mid;
+      else b1 = mid;
+    }
+    q0 = p.seq_q[b0];
   }
   const int group = p.sh.group, g = packed_over(my_head, p.sh.over_group), r = my_head - g * group;
-  const int q0 = p.seq_q[b0];
   const long long at =
       g * p.vec_stride + (long long)(packed_vec0(q0, b0) + my_tok - q0) * group + r;
   p.ndelta[at] = -mine;
@@ -2392,8 +2419,8 @@ cudaError_t launch_bwd_d(const BwdParams& p, const void* o, const void* dout, co
 }
 
 template <int D>
-cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const void* dout,
-                                const float* lse, int tile_room, int key_room,
+cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const PackedPlan& plan, const void* o,
+                                const void* dout, const float* lse, int tile_room, int key_room,
                                 cudaStream_t stream) {
   using C = BwdCfg<D>;
   static bool attr_set[64] = {};   // (of this head dimension, by device)
@@ -2425,9 +2452,11 @@ cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const v
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (!plan.early && (err = launch_packed_plan(plan, stream)) != cudaSuccess) return err;
   err = cudaLaunchKernelEx(&cfg, packed_bwd_prep_kernel<D>, p, static_cast<const uint16_t*>(o),
                            static_cast<const uint16_t*>(dout), lse);
   if (err != cudaSuccess) return err;
+  if (plan.early && (err = launch_packed_plan(plan, stream)) != cudaSuccess) return err;
   // persistent: one CTA per SM
   int sms = 0;
   if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
@@ -2451,11 +2480,11 @@ cudaError_t launch_packed_bwd_d(const PackedBwdParams& p, const void* o, const v
 
 }  // namespace
 
-cudaError_t launch_attn_bwd_packed(const PackedBwdParams& p, int D, const void* o,
-                                   const void* dout, const float* lse, int tile_room,
-                                   int key_room, cudaStream_t stream) {
-  if (D == 128) return launch_packed_bwd_d<128>(p, o, dout, lse, tile_room, key_room, stream);
-  if (D == 64) return launch_packed_bwd_d<64>(p, o, dout, lse, tile_room, key_room, stream);
+cudaError_t launch_attn_bwd_packed(const PackedBwdParams& p, const PackedPlan& plan, int D,
+                                   const void* o, const void* dout, const float* lse,
+                                   int tile_room, int key_room, cudaStream_t stream) {
+  if (D == 128) return launch_packed_bwd_d<128>(p, plan, o, dout, lse, tile_room, key_room, stream);
+  if (D == 64) return launch_packed_bwd_d<64>(p, plan, o, dout, lse, tile_room, key_room, stream);
   return cudaErrorInvalidValue;
 }
 

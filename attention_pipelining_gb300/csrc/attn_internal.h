@@ -283,6 +283,7 @@ struct PackedPlan {
   unsigned long long over_positions, over_tile;   // ceil(2^40 / positions), of 2 positions
   int causal, H_kv;
   int least_keys;      // packed_least_keys
+  int early;           // starts while the kernel before it runs (see packed_plan_kernel)
   PackedHeader* head;  // workspace, from here on
   int* seq_q;          // [B + 1], cu_q in order
   int* seq_k;          // [B + 1] (== seq_q where they are the same)
@@ -373,6 +374,7 @@ struct PackedFwdParams : AttnParams {
 struct PackedBwdParams : BwdParams {
   PackedShape sh;
   const int* seq_q;
+  const int* cu_q;       // for the row vectors, where these come before the plan; or nullptr
   long long vec_stride;  // row vectors of one K/V head
   long long o_st, o_sh, do_st, do_sh, dq_st, dq_sh, dk_st, dk_sh, dv_st, dv_sh;
 };
@@ -394,10 +396,11 @@ struct RopePackedParams {
 
 cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream);
 cudaError_t launch_attn_fwd_packed(const PackedFwdParams& p, int D, cudaStream_t stream);
-// With p.dq_acc set, dQ is added up there; otherwise a kernel of its own computes it.
-cudaError_t launch_attn_bwd_packed(const PackedBwdParams& p, int D, const void* o,
-                                   const void* dout, const float* lse, int tile_room,
-                                   int key_room, cudaStream_t stream);
+// The plan too.  With p.dq_acc set, dQ is added up there; otherwise a kernel of its own
+// computes it.
+cudaError_t launch_attn_bwd_packed(const PackedBwdParams& p, const PackedPlan& plan, int D,
+                                   const void* o, const void* dout, const float* lse,
+                                   int tile_room, int key_room, cudaStream_t stream);
 cudaError_t launch_rope_packed(const RopePackedParams& p, int D, bool interleaved,
                                cudaStream_t stream);
 // Reads (and optionally clears) the plan's and the rotation's status word.

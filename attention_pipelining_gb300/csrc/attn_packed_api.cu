@@ -134,6 +134,7 @@ attn_status_t take_plan(const attn_packed_t& s, const int* cu_q, const int* cu_k
   plan->seq_k = cu_k ? reinterpret_cast<int*>(ws + l.seq_k) : plan->seq_q;
   plan->H_kv = s.H_kv;
   plan->least_keys = packed_least_keys(s.D);
+  plan->early = 0;
   // (a part that the layout does not have begins at 0, where the header is)
   const auto at = [&](size_t offset) { return offset ? ws + offset : nullptr; };
   plan->first[0] = reinterpret_cast<int*>(ws + l.first);
@@ -283,13 +284,13 @@ attn_status_t bwd_impl(const attn_packed_t* s, const attn_thd_t* q, const attn_t
   p.scale_log2 = scale_log2_of(s->scale);
   p.timeout_ns = timeout_ns;
   p.fault_drop_item = drop_item;
-  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_packed_plan(plan, cs);
-  return done(e != cudaSuccess
-                  ? e
-                  : launch_attn_bwd_packed(p, s->D, to.data, tdo.data, lse,
-                                           (int)packed_tile_room(s->T_q, s->B, p.sh.positions, s->H_kv),
-                                           (int)packed_key_room(s->T_k, s->B, s->H_kv), cs));
+  // (the row vectors of up to 31 sequences need no plan, which then runs beside them)
+  plan.early = s->B < 32 ? 1 : 0;
+  p.cu_q = plan.early ? plan.cu_q : nullptr;
+  return done(launch_attn_bwd_packed(p, plan, s->D, to.data, tdo.data, lse,
+                                     (int)packed_tile_room(s->T_q, s->B, p.sh.positions, s->H_kv),
+                                     (int)packed_key_room(s->T_k, s->B, s->H_kv),
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

@@ -73,7 +73,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   int* const k = same ? q : fits ? bounds[1] : p.seq_k;
   int* const first[2] = {fits ? bounds[2] : p.first[0], fits ? bounds[3] : p.first[1]};
   allow_later();
-  wait_for_earlier();
+  // early: behind packed_bwd_prep_kernel, which lets it come when it has itself waited for
+  // what is earlier in the stream; its own work the plan neither reads nor changes, and waits
+  // for at the end, for those that wait for the plan
+  if (!p.early) wait_for_earlier();
 
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -320,6 +323,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     p.head->next[0] = p.head->next[1] = 0;
     p.head->cut = 2 * most[0] >= 3 * cap[0];
   }
+  if (p.early) wait_for_earlier();
 }
 
 // ---------------------------------------------------------------- rotation
