@@ -18,14 +18,12 @@ namespace {
 
 // ---------------------------------------------------------------- plan
 
-constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = kPlanThreads;   // of costs: a thread to each
 constexpr int kPlanShared = 2048;  // sequences (and one) whose bounds fit shared memory
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Scans of two values at once over the block's threads before this one (0 for the first);
-// `warps`: 32 of shared memory.
+// `warps`: 32 of shared memory (those of warps that the block does not have come last).
 template <typename Op>
 __device__ __forceinline__ int2 scan_before(int2 x, int2* warps, Op op) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -56,8 +54,12 @@ __device__ __forceinline__ int parts_of(int n, int cap) {
 // counts is its latency, a chain of scans with the block's barriers between them: a
 // thread takes an entry (found by bisection over the sequences' first entries), and the
 // bounds stay in shared memory.  A warp to a sequence, with the bounds read back from
-// global memory, took 5 to 9 us, this 3 to 4.
+// global memory, took 5 to 9 us, this 3 to 4.  1024 threads, or 512 for up to 31 sequences
+// (8 pieces behind prefixes, by itself: 5.8 us, with 1024 6.6; 500 sequences of 1 to 300
+// tokens, with the forward: 173.3, with 1024 171.4).
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedPlan p) {
+  constexpr int kBuckets = kPlanThreads;   // of costs: a thread to each
   __shared__ int at[2][kBuckets];   // entries of a cost, then where the next of them goes
   __shared__ int2 warps[2][32];
   __shared__ int most[2], slots[2], bounds[4][kPlanShared];
@@ -468,7 +470,8 @@ cudaError_t launch_rope_d(const RopePackedParams& in, bool interleaved, cudaStre
 }  // namespace
 
 cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t stream) {
-  return launch_ahead(packed_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
+  return p.B < 32 ? launch_ahead(packed_plan_kernel<512>, dim3(1), 512, 0, stream, p)
+                  : launch_ahead(packed_plan_kernel<1024>, dim3(1), 1024, 0, stream, p);
 }
 
 cudaError_t launch_rope_packed(const RopePackedParams& p, int D, bool interleaved,
