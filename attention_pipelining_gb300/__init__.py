@@ -47,7 +47,8 @@ EXPORTS = ["attn_fwd", "attn_fwd_host", "attn_status_string", "attn_device_statu
            "attn_kv_append", "attn_kv_read", "attn_fwd_paged", "attn_paged_workspace_bytes",
            "attn_fwd_paged_timeout_test", "attn_rope_packed", "attn_fwd_packed", "attn_bwd_packed",
            "attn_packed_workspace_bytes", "attn_packed_bwd_workspace_bytes",
-           "attn_fwd_packed_timeout_test", "attn_bwd_packed_timeout_test"]
+           "attn_fwd_packed_timeout_test", "attn_bwd_packed_timeout_test",
+           "attn_fwd_packed_o_boxes"]
 
 
 class AttnError(RuntimeError):
@@ -146,6 +147,8 @@ def _load():
     lib.attn_bwd_packed_timeout_test.argtypes = [vp] * 13 + [ctypes.c_size_t, ci, ci, ctypes.c_ulonglong,
                                                            vp]
     lib.attn_bwd_packed_timeout_test.restype = ci
+    lib.attn_fwd_packed_o_boxes.argtypes = [vp]
+    lib.attn_fwd_packed_o_boxes.restype = ci
     lib.attn_packed_workspace_bytes.argtypes = [vp]
     lib.attn_packed_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_packed_bwd_workspace_bytes.argtypes = [vp, ci]

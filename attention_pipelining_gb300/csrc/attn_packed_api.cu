@@ -200,7 +200,7 @@ attn_status_t fwd_impl(const attn_packed_t* s, const attn_thd_t* q, const attn_t
     return ATTN_ERR_CUDA;
   // 32 rows of a tile: whole groups of heads of one token or more, or 32 heads of one
   const int group = p.sh.group, box_heads = group < 32 ? group : 32;
-  p.sh.o_box = 32 % box_heads == 0 && group % box_heads == 0;
+  p.sh.o_box = packed_o_boxes(group, p.sh.positions);
   if (p.sh.o_box && !encode_bf16_map_thd(&p.tm_o, to.data, s->D, s->H_q, s->T_q, to.sh, to.st,
                                          box_heads, 32 / box_heads))
     return ATTN_ERR_CUDA;
@@ -349,6 +349,12 @@ attn_status_t attn_bwd_packed_timeout_test(
     return ATTN_ERR_INVALID_ARG;
   return bwd_impl(s, q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, workspace, workspace_bytes,
                   deterministic, stream, drop_item, wait_budget_ns);
+}
+
+int attn_fwd_packed_o_boxes(const attn_packed_t* s) {
+  if (check_sizes(s) != ATTN_OK) return -1;
+  const int group = s->H_q / s->H_kv;
+  return packed_o_boxes(group, tile_positions(group)) ? 1 : 0;
 }
 
 attn_status_t attn_rope_packed(const attn_thd_t* q, const attn_thd_t* q_out, const attn_thd_t* k,

@@ -58,6 +58,11 @@
  * `wait_budget_ns` as above; the other number must be >= 0 (else ATTN_ERR_INVALID_ARG).
  * For tests only.
  *
+ * attn_fwd_packed_o_boxes returns 1 where attn_fwd_packed of these sizes writes O by TMA boxes
+ * of 32 rows of a tile each (rows are token * R + head, R = H_q / H_kv; the box that begins with
+ * a row has min(R, 32) heads of 32 / min(R, 32) tokens), 0 where it writes row by row, or -1
+ * for invalid sizes.  Reads nothing but the sizes.
+ *
  * attn_fwd_tail_pairs returns how many tiles attn_fwd splits across CTA
  * pairs for these sizes on the current device (0 when the tail is not
  * split), or -1 for invalid sizes or a device that cannot be queried.
@@ -113,6 +118,8 @@ attn_status_t attn_bwd_packed_timeout_test(
     const attn_thd_t *dk, const attn_thd_t *dv, const int *cu_q, const int *cu_k, void *workspace,
     size_t workspace_bytes, int deterministic, int drop_item, unsigned long long wait_budget_ns,
     attn_stream_t stream);
+
+int attn_fwd_packed_o_boxes(const attn_packed_t *sizes);
 
 int attn_fwd_tail_pairs(int B, int H_q, int H_kv, int S_q, int S_kv, int D, int causal);
 

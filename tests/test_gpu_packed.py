@@ -525,6 +525,33 @@ def test_any_number_of_sequences(B):
         check_backward(q, k, v, o, lse, do, cu_q, cu_k, False, 0.125, got)
 
 
+# heads a key head: above 32 with spare rows (one or more tokens a tile), without, and just 32
+LARGE = [(32, 1, [1, 2, 7, 8, 9, 33]), (64, 2, [4, 17]), (36, 1, [5, 6, 7, 50]), (96, 1, [1, 2, 3, 40, 41]),
+         (192, 2, [2, 33]), (100, 1, [1, 2, 31]), (124, 1, [2, 3, 20])]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H_q,H_kv,lens", LARGE, ids=[f"{c[0]}_{c[1]}" for c in LARGE])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_large_groups(H_q, H_kv, lens, D, causal):
+    """Tiles of one to four tokens, odd and even numbers of them: against the reference, and the same bits
+    again and again, also behind many tokens (where a plan comes first)."""
+    q, k, v, do, cu, _ = make(H_q, H_kv, D, lens, lead=1, pad=3, seed=H_q)
+    scale = D ** -0.5
+    o, lse = forward(q, k, v, cu, cu, causal, scale)
+    check_forward(q, k, v, cu, cu, causal, scale, (o, lse))
+    for _ in range(20):
+        a, b = forward(q, k, v, cu, cu, causal, scale)
+        assert torch.equal(a, o) and torch.equal(b, lse)
+    pad = 304 * (128 * H_kv // H_q)   # (more tiles than a device has multiprocessors)
+    more = [torch.cat([x, x.new_full((pad, *x.shape[1:]), math.nan)]) for x in (q, k, v)]
+    a, b = forward(*more, cu, cu, causal, scale)
+    assert torch.equal(a[:-pad], o) and torch.equal(b[:, :-pad], lse)
+    for det in (False, True):
+        got = backward(q, k, v, o, lse, do, cu, cu, causal, scale, deterministic=det)
+        check_backward(q, k, v, o, lse, do, cu, cu, causal, scale, got, det)
+
+
 def test_more_tiles_than_thread_blocks_keep():
     """The forward's thread blocks keep 64 tiles each: with more, there are more of them.  The same
     heads in two calls are the reference."""

@@ -169,6 +169,30 @@ def test_workspace_holds_the_lists(lib):
             assert lib.attn_packed_bwd_workspace_bytes(s, 0) == begin + keys + up(4 * T * H_q * 64)
 
 
+# query heads a key head that the calls take
+GROUPS = [g for g in range(1, 129) if g <= 32 or g % 4 == 0]
+
+
+def test_boxes_of_o_hold_rows_of_their_tile_alone(lib):
+    """Where O leaves by boxes of 32 rows, each box is those rows in their order and none of them is a
+    spare one, which would be a row of the next token."""
+    for R in GROUPS:
+        rows = R * (128 // R if R % 4 == 0 else 32 // R * 4)
+        boxes = lib.attn_fwd_packed_o_boxes(sizes(H_q=3 * R, H_kv=3))
+        assert boxes in (0, 1)
+        if boxes:
+            heads = min(R, 32)
+            for row0 in range(0, 128, 32):
+                t0, h0 = row0 // R, row0 % R
+                box = [(t0 + t) * R + h0 + h for t in range(32 // heads) for h in range(heads)]
+                assert h0 + heads <= R and box == list(range(row0, row0 + 32)), R
+                assert box[-1] < rows, (R, "a box of spare rows")
+        else:
+            assert 128 % R, (R, "could leave by boxes")
+    assert lib.attn_fwd_packed_o_boxes(sizes(H_q=33, H_kv=1)) == -1
+    assert lib.attn_fwd_packed_o_boxes(None) == -1
+
+
 def test_binding_refuses_on_the_host():
     t = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     cu = torch.tensor([0, 4], dtype=torch.int32)
