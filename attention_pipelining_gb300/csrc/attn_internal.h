@@ -315,9 +315,13 @@ __host__ __device__ constexpr int packed_least_keys(int D) { return D == 64 ? 2 
 inline int packed_slots(int H_kv) { return 4 * kPackedCtas / (3 * H_kv); }
 constexpr int kPackedCounters = 2;    // of an entry's parts and a K/V head: one a half of a tile
 
-// x / d for x < 2^31 and d <= 256, with `inverse` = ceil(2^40 / d): off by less than 2^-9.
+// x / d for 0 <= x < 2^31 and d <= 256, with `inverse` = ceil(2^40 / d): x * inverse / 2^40 is
+// above x / d by less than 2^-9.  The product has up to 71 bits, so it is made of the inverse's
+// upper and lower 20 (and the lower product's fraction, which is below one, dropped first).
 __host__ __device__ inline int packed_over(int x, unsigned long long inverse) {
-  return (int)(((unsigned long long)(unsigned)x * inverse) >> 40);
+  const unsigned high = (unsigned)(inverse >> 20), low = (unsigned)inverse & 0xfffffu;
+  return (int)(((unsigned long long)(unsigned)x * high +
+                (((unsigned long long)(unsigned)x * low) >> 20)) >> 20);
 }
 
 // Entries of the lists, at most.

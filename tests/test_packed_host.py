@@ -4,12 +4,13 @@ against torch's own arithmetic and against differences."""
 import ctypes
 import math
 import struct
+import subprocess
 
 import pytest
 import torch
 
 import attention_pipelining_gb300 as ap
-from attention_pipelining_gb300 import packed
+from attention_pipelining_gb300 import _build, packed
 from tests import packed_ref as ref
 
 A = 0x10000
@@ -191,6 +192,37 @@ def test_boxes_of_o_hold_rows_of_their_tile_alone(lib):
             assert 128 % R, (R, "could leave by boxes")
     assert lib.attn_fwd_packed_o_boxes(sizes(H_q=33, H_kv=1)) == -1
     assert lib.attn_fwd_packed_o_boxes(None) == -1
+
+
+DIVISIONS = r"""
+#include <cstdio>
+#include "attn_internal.h"
+int main() {
+  for (long long d = 1; d <= 256; ++d) {
+    const unsigned long long inverse = ((1ull << 40) + d - 1) / d;
+    const long long most = (1ll << 31) - 1;
+    for (int bit = 0; bit <= 31; ++bit)
+      for (long long around : {1ll << bit, (1ll << bit) * d, (most >> bit) / d * d})
+        for (long long x = around - 2; x <= around + 2; ++x)
+          if (x >= 0 && x <= most && attnpipe::packed_over((int)x, inverse) != x / d) {
+            std::printf("%lld / %lld gave %d\n", x, d, attnpipe::packed_over((int)x, inverse));
+            return 1;
+          }
+  }
+  return 0;
+}
+"""
+
+
+def test_divisions_by_an_inverse(tmp_path):
+    """packed_over over the whole range that the sizes admit: around powers of two, alone and times the
+    divisor, and around the largest multiples."""
+    src, exe = tmp_path / "over.cpp", tmp_path / "over"
+    src.write_text(DIVISIONS)
+    subprocess.run([_build.nvcc(), "-std=c++17", "-O1", "-I", _build.INCLUDE, "-I", _build.CSRC, str(src), "-o",
+                    str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
 
 
 def test_binding_refuses_on_the_host():
