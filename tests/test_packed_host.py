@@ -237,6 +237,28 @@ def test_binding_refuses_on_the_host():
             call()
 
 
+@pytest.fixture
+def on_the_host(lib, monkeypatch):
+    """The binding's checks, with tensors on the host in place of a GPU's (they stop before any launch)."""
+    packed._import()
+    monkeypatch.setattr(packed, "_device", lambda name, t: t.get_device())
+
+
+@pytest.mark.parametrize("H_q,H_kv,D,scale,code", [
+    (33, 1, 64, 0.1, 2), (132, 1, 64, 0.1, 2), (2, 2, 96, 0.1, 2), (2, 2, 32, 0.1, 2), (3, 2, 64, 0.1, 1),
+    (2, 2, 64, math.nan, 1), (2, 2, 64, -math.inf, 1)])
+def test_binding_says_why_it_refuses_sizes(on_the_host, H_q, H_kv, D, scale, code):
+    """The status is the C entry's: what is not supported is no invalid argument."""
+    q, k = (torch.zeros(4, h, D, dtype=torch.bfloat16) for h in (H_q, H_kv))
+    cu, lse = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(H_q, 4)
+    for call in (lambda: ap.attn_fwd_packed(q, k, k, cu, True, scale),
+                 lambda: ap.attn_bwd_packed(q, k, k, q, lse, q, cu, True, scale),
+                 lambda: ap.attn_bwd_packed(q, k, k, q, lse, q, cu, True, scale, deterministic=True)):
+        with pytest.raises(ap.AttnError) as e:
+            call()
+        assert e.value.code == code, e.value
+
+
 # ---------------------------------------------------------------- the reference itself
 
 CASES = [([5, 0, 3], [5, 0, 3], True), ([4, 2], [6, 1], True), ([3, 0, 2], [4, 3, 0], False)]
