@@ -99,7 +99,7 @@ def _sizes(q, k, v, cu_q, cu_k, causal, scale):
         raise TypeError("cu_q must be an int32 [sequences + 1] tensor")
     bounds = cu_q.shape
     B = bounds[0] - 1
-    _small(T_q, T_k, H_q, D, B)
+    _small(T_q, T_k, H_q, H_kv, D, B)
     return (dev, q_shape, k_shape, _SIZES.pack(B, T_q, T_k, H_q, H_kv, D, 1 if causal else 0, scale), qs, ks, vs,
             _flat("cu_q", cu_q, bounds, _i32, dev),
             None if cu_k is None else _flat("cu_k", cu_k, bounds, _i32, dev))

@@ -259,6 +259,24 @@ def test_binding_says_why_it_refuses_sizes(on_the_host, H_q, H_kv, D, scale, cod
         assert e.value.code == code, e.value
 
 
+@pytest.mark.parametrize("which", ["q", "k", "T_q"])
+def test_binding_refuses_sizes_beyond_its_ints(on_the_host, which):
+    """Views that claim 2^31 heads or tokens."""
+    n = 2 ** 31
+    q, k = torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16)
+    if which == "q":
+        q = q.expand(4, n, 64)
+    elif which == "k":
+        k = k.expand(4, n, 64)
+    else:
+        q = q[:1].expand(n, 1, 64)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        ap.attn_fwd_packed(q, k, k, cu, True, 0.1, cu_k=cu)
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        ap.attn_bwd_packed(q, k, k, q, torch.zeros(1, 4), q, cu, True, 0.1, cu_k=cu)
+
+
 # ---------------------------------------------------------------- the reference itself
 
 CASES = [([5, 0, 3], [5, 0, 3], True), ([4, 2], [6, 1], True), ([3, 0, 2], [4, 3, 0], False)]
