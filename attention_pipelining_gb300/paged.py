@@ -131,7 +131,7 @@ def _on(dev, stream, call):
     stream, to which what it allocates belongs."""
     if stream is not None:
         if stream.device.index != dev:
-            raise ValueError("stream belongs to another device than the cache")
+            raise ValueError("stream belongs to another device than the tensors")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
     if _current_device() == dev:

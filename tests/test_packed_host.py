@@ -277,6 +277,20 @@ def test_binding_refuses_sizes_beyond_its_ints(on_the_host, which):
         ap.attn_bwd_packed(q, k, k, q, torch.zeros(1, 4), q, cu, True, 0.1, cu_k=cu)
 
 
+def test_a_stream_of_another_device_is_refused(on_the_host):
+    """With a text that names what the call has: tensors, no cache."""
+    class Stream:
+        device = torch.device("cuda", 5)
+
+    q = torch.zeros(4, 1, 64, dtype=torch.bfloat16)
+    cu, table = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(8, 32)
+    for call in (lambda: ap.attn_fwd_packed(q, q, q, cu, True, 0.1, stream=Stream),
+                 lambda: ap.attn_bwd_packed(q, q, q, q, torch.zeros(1, 4), q, cu, True, 0.1, stream=Stream),
+                 lambda: ap.rope_packed(q, q, cu[None, :1].expand(1, 4).contiguous(), table, table, stream=Stream)):
+        with pytest.raises(ValueError, match="stream belongs to another device than the tensors"):
+            call()
+
+
 # ---------------------------------------------------------------- the reference itself
 
 CASES = [([5, 0, 3], [5, 0, 3], True), ([4, 2], [6, 1], True), ([3, 0, 2], [4, 3, 0], False)]
