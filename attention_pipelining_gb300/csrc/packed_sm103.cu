@@ -248,9 +248,6 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   // costs, with the heads innermost, 633, in groups of 16 589; 4 x 4096 1417, 1421 and
   // 1450.  Now 522 and 1370.)
   const bool grouped = 2 * most[1] < 3 * cap[1];
-  const auto group_cost = [&](const PackedKeys& x) {   // its first block's
-    return x.tiles - (p.causal ? min(positions(max(x.shift, 0)), x.tiles) : 0);
-  };
   // an entry of n blocks has `parts` parts of `size` blocks, but for the last
   const auto cut = [&](int list, int blocks, int& parts, int& size) {
     parts = parts_of(blocks, cap[list]);
