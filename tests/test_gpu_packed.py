@@ -8,6 +8,7 @@ import torch
 
 import attention_pipelining_gb300 as ap
 from tests import packed_ref as ref
+from tests.test_packed_host import CUT_KEYS, CUT_TILES
 
 pytestmark = pytest.mark.gpu
 
@@ -479,7 +480,8 @@ def test_tokens_beyond_32_bit_offsets():
 
 CUT = [
     # H_q, H_kv, D, lens_q, lens_k, causal: tiles of long sequences, and the key blocks that few
-    # tiles see, are cut into parts (of 8 and of 4 blocks at least) where there are few
+    # tiles see, are cut into parts where there are few (from CUT_KEYS blocks of keys, and CUT_TILES
+    # query tiles, on)
     (8, 2, 128, [3, 1], [5000, 40], True),
     (4, 4, 64, [1, 130, 0], [9000, 2100, 3000], True),
     (8, 1, 128, [1500], None, True),
@@ -510,6 +512,29 @@ def test_work_cut_into_parts(case):
     for _ in range(3):
         for x, y in zip(forward(q, k, v, cu_q, cu_k, causal, scale), (o, lse)):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("off", [-1, 0, 1])
+def test_around_the_least_parts(D, off):
+    """Works of one block less than is cut, of as many, and of one more; the last block of one key or
+    query, or full."""
+    scale = D ** -0.5
+    for last in (1, 128):
+        m, n = ((blocks + off - 1) * 128 + last for blocks in (CUT_KEYS, CUT_TILES[D]))
+        for lens_q, lens_k, causal in (([5, 0, 2], [m, 30, 9], True), ([n], [40], False), ([n, 3], [n, 3], True)):
+            q, k, v, do, cu_q, cu_k = make(2, 1, D, lens_q, lens_k, pad=1, seed=m)
+            if lens_q[0] == n:   # (a tile of one head's 128 tokens)
+                q, do = q[:, :1], do[:, :1]
+            o, lse = forward(q, k, v, cu_q, cu_k, causal, scale)
+            check_forward(q, k, v, cu_q, cu_k, causal, scale, (o, lse))
+            first = None
+            for det in (True, False, True):
+                got = backward(q, k, v, o, lse, do, cu_q, cu_k, causal, scale, deterministic=det)
+                check_backward(q, k, v, o, lse, do, cu_q, cu_k, causal, scale, got, det)
+                first = first or [t.clone() for t in got]
+                for x, y in zip(first if det else first[1:], got if det else got[1:]):
+                    assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("B", [31, 32, 1023, 1024, 2047, 2048, 5000])

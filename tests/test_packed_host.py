@@ -170,6 +170,35 @@ def test_workspace_holds_the_lists(lib):
             assert lib.attn_packed_bwd_workspace_bytes(s, 0) == begin + keys + up(4 * T * H_q * 64)
 
 
+# the least blocks of keys (forward, dq) or query tiles (dk, dv) that are cut into parts: one and a half
+# times a part's least
+CUT_KEYS = 12
+CUT_TILES = {64: 3, 128: 5}
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_where_work_may_be_cut(lib, D):
+    """The workspace has room for parts' results from these numbers on (test_around_the_least_parts has
+    works of just that many blocks)."""
+    def grows(nbytes, field, blocks, step):
+        """What the last token that makes it so many blocks adds, beside what each token takes"""
+        at = (blocks - 1) * step
+        a, b, c = (nbytes(sizes(B=1, H_q=1, H_kv=1, D=D, **{**dict(T_q=5, T_k=5), field: at + n})) for n in (-1, 0, 1))
+        return c - b - (b - a)
+
+    slots = 4 * 152 // 3
+    tile, keys = slots * 256 * D * 4, slots * 2 * 128 * D * 4
+    fwd = lib.attn_packed_workspace_bytes
+    assert grows(fwd, "T_k", CUT_KEYS - 1, 128) < 1000
+    assert grows(fwd, "T_k", CUT_KEYS, 128) >= tile
+    for det in (0, 1):
+        bwd = lambda s: lib.attn_packed_bwd_workspace_bytes(s, det)  # noqa: E731
+        assert grows(bwd, "T_q", CUT_TILES[D] - 1, 128) < 2000
+        assert grows(bwd, "T_q", CUT_TILES[D], 128) >= keys - 2000
+        assert grows(bwd, "T_k", CUT_KEYS - 1, 128) < 2000
+        assert (grows(bwd, "T_k", CUT_KEYS, 128) >= tile) == bool(det)
+
+
 # query heads a key head that the calls take
 GROUPS = [g for g in range(1, 129) if g <= 32 or g % 4 == 0]
 
