@@ -13,7 +13,9 @@ namespace attnpipe {
 // the products' and the sum's rounding errors are recovered (fma, two-sum) and
 // added back, and the fp32 result, when it falls on a tie of the bf16 rounding
 // that the remainder breaks, is moved one step to the remainder's side.  Non-finite
-// values take the plain formula's result.
+// values take the plain formula's result.  (A product's error has its 32 bits' last, 2^-30 of
+// the product's factors' powers of two, and is a float where the product is 2^-117 or more; below
+// that the errors are rounded to 2^-149, by 2^-150 each.)
 __device__ __forceinline__ void rotate2_exactly(uint64_t u, uint64_t a, uint64_t w, uint64_t b,
                                                 float& r0, float& r1) {
   const uint64_t minus = f2_pack(-1.f, -1.f);

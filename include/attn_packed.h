@@ -135,8 +135,9 @@ size_t attn_packed_bwd_workspace_bytes(const attn_packed_t *sizes, int determini
  *     (u cos[x,d] - w sin[x,d], w cos[x,d] + u sin[x,d])        inverse = 0
  *     (u cos[x,d] + w sin[x,d], w cos[x,d] - u sin[x,d])        inverse = 1
  *
- * rounded once to bf16 from the exact value.  The second is the gradient of the
- * first.  One axis is the usual rotation.
+ * rounded once to bf16 from the exact value (where a product is not 0 but below 2^-117, whose last
+ * bits fp32 does not reach, from a value that may be off by 2^-148).  The second is the
+ * gradient of the first.  One axis is the usual rotation.
  *
  *   q, q_out   [T, H_q, D], read and written (may be the same tensor); both NULL
  *              with H_q = 0

@@ -94,7 +94,8 @@ typedef struct {
  *              1: element 2 d pairs with 2 d + 1
  *
  * A pair (a, b) at position x becomes (a cos - b sin, b cos + a sin), rounded
- * once to bf16 from the exact value, and a 4-bit cache quantises that rounded
+ * once to bf16 from the exact value (as attn_rope_packed's, attn_packed.h, also where products
+ * are below 2^-117), and a 4-bit cache quantises that rounded
  * key: the result depends on nothing but the inputs' values.  Slots must be distinct: two tokens of one call in the same
  * slot (two sequences appending to a shared page) leave either, or a mixture.
  */

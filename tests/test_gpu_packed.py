@@ -730,6 +730,27 @@ def test_rotation_of_values_that_are_not_finite():
     assert torch.equal(got[same], clean[same]) and not torch.isfinite(got[~same]).any()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotation_of_tiny_values(interleaved):
+    """Where the products' last bits lie below fp32's smallest step, 2^-149: each product's error, and
+    each sum's, is rounded to that, by 2^-150 at most; four of them, beside the one rounding to
+    bf16 (2^-8 of the value, or half of its smallest step, 2^-134)."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q = torch.randn(400, 2, 64, generator=g, device="cuda") * 2.0 ** torch.randint(
+        -134, -100, (400, 1, 64), generator=g, device="cuda")
+    q = q.bfloat16()
+    assert (q.abs() < 2.0 ** -126).any() and (q != 0).any()
+    pos = torch.randint(0, 50, (1, 400), generator=g, device="cuda", dtype=torch.int32)
+    cos, sin = tables(50, 32)
+    got, _ = ap.rope_packed(q, None, pos, cos, sin, interleaved=interleaved)
+    x, c, s = q.double(), cos.double()[pos[0].long()][:, None], sin.double()[pos[0].long()][:, None]
+    u, w = (x[..., 0::2], x[..., 1::2]) if interleaved else (x[..., :32], x[..., 32:])
+    first, second = u * c - w * s, w * c + u * s     # (doubles are exact to 2^-53 of the products)
+    want = torch.stack([first, second], -1).flatten(2) if interleaved else torch.cat([first, second], -1)
+    off = (got.double() - want).abs()
+    assert (off <= torch.maximum(want.abs() * 2.0 ** -8, torch.full_like(want, 2.0 ** -134)) + 2.0 ** -148).all()
+
+
 def test_rotation_s_gradient_against_differences():
     """sum(w rope(x)) changes by the inverse rotation of w (whole numbers, so that only the two
     roundings differ)."""
