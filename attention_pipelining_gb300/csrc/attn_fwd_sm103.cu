@@ -1041,11 +1041,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else if constexpr (kPacked) {
             // bf16 O through shared memory, as below: where the warp's 32 rows are a
-            // box of the tensor (packed_o_boxes, of tokens that all exist) by one TMA copy; otherwise they are taken out
-            // again four rows at a time, whole 128-byte lines, without rows behind the
-            // sequence's end and spare rows.  (That way alone took 226 us instead of
-            // 193 for 16 x 1024 tokens without a mask, in an earlier build; now 204: the
-            // correction warps are then late for the next tile.)
+            // box of the tensor (packed_o_boxes, of tokens that all exist) by one TMA
+            // copy; otherwise they are taken out again four rows at a time, whole 128-byte
+            // lines, without rows behind the sequence's end and spare rows.  (That way
+            // alone took 226 us instead of 193 for 16 x 1024 tokens without a mask, in an
+            // earlier build; now 204: the correction warps are then late for the next
+            // tile.)
             const uint32_t stage = smem_u32(smem + C::kOffStage + q4 * 4096);
             const uint32_t srow = stage + (uint32_t)lane * 128u;
             const int group = p.sh.group, first = t * p.sh.positions;
@@ -1056,8 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (i < p.sh.positions && first + i < rows)
                 p.lse[(long long)(head0 + r - i * group) * p.sh.T_q + tok0 + i] = lse_row;
             }
-            // (no spare rows where there are boxes, so these are the sub-tile's own)
-            const bool whole = p.sh.o_box != 0 && first + token_of(q4 * 32 + 31) < rows;
+            const bool whole = q4 < p.sh.o_boxes && first + token_of(q4 * 32 + 31) < rows;
 #pragma unroll 1
             for (int h = 0; h < D / 64; ++h) {
               if (lane == 0) tma_store_wait_read<0>();

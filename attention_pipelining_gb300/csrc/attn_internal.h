@@ -350,7 +350,7 @@ struct PackedShape {
   unsigned long long over_group, over_group64;   // ceil(2^40 / R) and ceil(2^64 / R), R > 1
   int inv_group;       // ceil(2^16 / R): row / R = row * inv_group >> 16 for row < 128
   int T_q, T_k;
-  int o_box;           // packed_o_boxes
+  int o_boxes;         // packed_o_boxes
   // parts' results, by slot and K/V head: of tiles [256 rows, D] and, in the forward,
   // their base-2 log-sum-exps [256]; of key blocks dV and dK, [2, 128 rows, D]
   float* tile_parts;
@@ -361,12 +361,13 @@ struct PackedShape {
   int* key_counters;
 };
 
-// Whether the forward writes O by boxes of a tensor map, 32 rows of a tile at a time: whole groups of
-// heads of one token or more, or 32 heads of one.  Only where a tile has no spare rows: 96
-// heads of one token would leave 32, whose box is heads of the next token, which another warp writes.
-inline bool packed_o_boxes(int group, int positions) {
+// How many of a tile's four times 32 rows, the first ones, the forward may write as boxes of O's
+// tensor map: whole groups of heads of one token or more, or 32 heads of one (0: such rows are
+// no box).  Spare rows are not among them: 96 heads of one token leave the last 32, whose box
+// would be heads of the next token, which another warp writes.
+inline int packed_o_boxes(int group, int positions) {
   const int box_heads = group < 32 ? group : 32;
-  return 32 % box_heads == 0 && group % box_heads == 0 && group * positions == 128;
+  return 32 % box_heads == 0 && group % box_heads == 0 ? group * positions / 32 : 0;
 }
 
 // Whether a forward needs no plan: its tiles run at once whatever the bounds are, none is

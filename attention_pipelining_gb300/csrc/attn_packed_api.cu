@@ -200,8 +200,8 @@ attn_status_t fwd_impl(const attn_packed_t* s, const attn_thd_t* q, const attn_t
     return ATTN_ERR_CUDA;
   // 32 rows of a tile: whole groups of heads of one token or more, or 32 heads of one
   const int group = p.sh.group, box_heads = group < 32 ? group : 32;
-  p.sh.o_box = packed_o_boxes(group, p.sh.positions);
-  if (p.sh.o_box && !encode_bf16_map_thd(&p.tm_o, to.data, s->D, s->H_q, s->T_q, to.sh, to.st,
+  p.sh.o_boxes = packed_o_boxes(group, p.sh.positions);
+  if (p.sh.o_boxes > 0 && !encode_bf16_map_thd(&p.tm_o, to.data, s->D, s->H_q, s->T_q, to.sh, to.st,
                                          box_heads, 32 / box_heads))
     return ATTN_ERR_CUDA;
   p.o = to.data;
@@ -354,7 +354,7 @@ attn_status_t attn_bwd_packed_timeout_test(
 int attn_fwd_packed_o_boxes(const attn_packed_t* s) {
   if (check_sizes(s) != ATTN_OK) return -1;
   const int group = s->H_q / s->H_kv;
-  return packed_o_boxes(group, tile_positions(group)) ? 1 : 0;
+  return packed_o_boxes(group, tile_positions(group));
 }
 
 attn_status_t attn_rope_packed(const attn_thd_t* q, const attn_thd_t* q_out, const attn_thd_t* k,

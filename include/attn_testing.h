@@ -58,10 +58,10 @@
  * `wait_budget_ns` as above; the other number must be >= 0 (else ATTN_ERR_INVALID_ARG).
  * For tests only.
  *
- * attn_fwd_packed_o_boxes returns 1 where attn_fwd_packed of these sizes writes O by TMA boxes
- * of 32 rows of a tile each (rows are token * R + head, R = H_q / H_kv; the box that begins with
- * a row has min(R, 32) heads of 32 / min(R, 32) tokens), 0 where it writes row by row, or -1
- * for invalid sizes.  Reads nothing but the sizes.
+ * attn_fwd_packed_o_boxes returns how many TMA boxes of 32 rows attn_fwd_packed of these sizes
+ * may write a tile's O as, from its first row on (rows are token * R + head, R = H_q / H_kv; the
+ * box that begins with a row has min(R, 32) heads of 32 / min(R, 32) tokens), 0 where it
+ * writes row by row, or -1 for invalid sizes.  Reads nothing but the sizes.
  *
  * attn_fwd_tail_pairs returns how many tiles attn_fwd splits across CTA
  * pairs for these sizes on the current device (0 when the tail is not

@@ -205,20 +205,19 @@ GROUPS = [g for g in range(1, 129) if g <= 32 or g % 4 == 0]
 
 def test_boxes_of_o_hold_rows_of_their_tile_alone(lib):
     """Where O leaves by boxes of 32 rows, each box is those rows in their order and none of them is a
-    spare one, which would be a row of the next token."""
+    spare one, which would be a row of the next token; and all rows that could leave so do."""
     for R in GROUPS:
         rows = R * (128 // R if R % 4 == 0 else 32 // R * 4)
         boxes = lib.attn_fwd_packed_o_boxes(sizes(H_q=3 * R, H_kv=3))
-        assert boxes in (0, 1)
-        if boxes:
-            heads = min(R, 32)
-            for row0 in range(0, 128, 32):
-                t0, h0 = row0 // R, row0 % R
-                box = [(t0 + t) * R + h0 + h for t in range(32 // heads) for h in range(heads)]
-                assert h0 + heads <= R and box == list(range(row0, row0 + 32)), R
-                assert box[-1] < rows, (R, "a box of spare rows")
-        else:
-            assert 128 % R, (R, "could leave by boxes")
+        heads, could = min(R, 32), 0
+        for i in range(4):
+            t0, h0 = 32 * i // R, 32 * i % R
+            box = [(t0 + t) * R + h0 + h for t in range(32 // heads) for h in range(heads)]
+            if h0 + heads <= R and box == list(range(32 * i, 32 * i + 32)) and box[-1] < rows and could == i:
+                could += 1
+        if R % 32 and 32 % R:
+            could = 0   # (a box's shape would change from row to row)
+        assert boxes == could, (R, boxes, could)
     assert lib.attn_fwd_packed_o_boxes(sizes(H_q=33, H_kv=1)) == -1
     assert lib.attn_fwd_packed_o_boxes(None) == -1
 
