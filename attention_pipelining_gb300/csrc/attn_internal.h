@@ -301,6 +301,8 @@ struct PackedPlan {
 // kPackedLeastTile (of keys) or packed_least_keys (of query tiles) where that is more.  So
 // there are at most n / cap + 1/2 <= 4/3 n / cap parts of an entry, and 4/3 kPackedCtas
 // of all.
+// (the SMs of a whole GB300; where fewer are visible the cuts are finer than they need be, and
+// the results the same)
 constexpr int kPackedCtas = 152;
 constexpr int kPackedMostParts = 64;
 constexpr int kPackedBand = 4;       // key blocks of a group, and tiles of a band (dQ)

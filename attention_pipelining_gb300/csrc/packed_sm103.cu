@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 constexpr int kRopeThreads = 128;
 constexpr int kRopeAhead = 4;        // rows of a thread under way
 constexpr int kRopeResident = 6;     // thread blocks on an SM
-constexpr int kRopeWave = kRopeResident * 152;
+constexpr int kRopeWave = kRopeResident * 152;   // of a whole GB300
 
 // A token's vector of one head is a row that D / 16 neighbouring lanes hold, 16
 // elements each: eight first and eight second elements of their pairs, or (adjacent
